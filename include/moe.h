@@ -450,6 +450,123 @@ int moe_attn_append(const uint16_t *k_new_dev, const uint16_t *v_new_dev, int M,
                     uint16_t *vt_cache_dev, int T_cap, moe_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * 8-bit key/value cache for a batch of sequences: appending rows, the decode
+ * attention over it, eviction by accumulated attention weight, and reading
+ * values back.  Half the bytes of the bf16 cache above, any of the head
+ * layouts below, and every length on the device, so that a captured graph
+ * replays with the lengths of the moment.
+ *
+ * A cached value is code * 2^e.  Codes, 8 bits each, lie as
+ * [batch][kv_heads][T_cap][head_dim] (keys and values alike); each block of
+ * `block` positions of a head has one step 2^e, stored as the fp32 number, in
+ * [batch][kv_heads][T_cap / block].  Powers of two, because codes are rounded
+ * again when a growing block or an eviction gives them a larger step: then a
+ * value stays within one step of what was appended however often that
+ * happens.  All four buffers are the caller's, 16-byte aligned; they need no
+ * initialisation.
+ *
+ * Common to the calls: pos_dev, counts_dev, lens_dev are int32 [batch] on
+ * the device.  Sequence b has positions 0 .. pos[b] - 1 before the call and
+ * the call's row m is position pos[b] + m, for m < counts[b] (NULL: all M).
+ * pos[b] < 0 marks an idle sequence: nothing of it is read or written and its
+ * outputs are zero.  Rows past counts[b] are padding: never read, their
+ * outputs zero.  err_dev (int, the caller clears it) collects
+ * MOE_KV8_ERR_RANGE (positions or counts outside the cache; those rows are
+ * left out) and MOE_KV8_ERR_NONFINITE.  The current device is the buffers'
+ * device.  Calls that write the same cache, or share a workspace, must not
+ * overlap on the GPU; two captured graphs that can run at once need a
+ * workspace each.  Every call only enqueues. */
+#define MOE_KV8_ERR_RANGE 1
+#define MOE_KV8_ERR_NONFINITE 2
+#define MOE_KV8_MAX_ROWS 8            /* rows of an attention call */
+#define MOE_KV8_MAX_GROUP 64          /* query heads per key/value head */
+#define MOE_KV8_MAX_BATCH 1024
+#define MOE_KV8_MAX_HEADS 1024        /* key/value heads */
+#define MOE_KV8_MAX_POSITIONS (1 << 22)
+enum { MOE_KV8_INT8 = 0, MOE_KV8_E4M3 = 1 };            /* code formats: -127 .. 127; fp8 e4m3 (largest 448) */
+enum { MOE_BF16 = 0, MOE_F16 = 1, MOE_F32 = 2 };        /* element types */
+
+typedef struct moe_kv8 {
+    int batch, q_heads, kv_heads;  /* q_heads a multiple of kv_heads */
+    int head_dim;                  /* 64, 128 or 256 */
+    int T_cap;                     /* positions per sequence, a multiple of block */
+    int block;                     /* positions per step: 16, 32, 64 or 128 */
+    int format;                    /* MOE_KV8_INT8 or MOE_KV8_E4M3 */
+    void *k_dev, *v_dev;
+    float *k_scale_dev, *v_scale_dev;
+} moe_kv8;
+
+/* Rows [batch][M][heads][head_dim] as they lie: strides in elements, the last
+ * dimension contiguous (a slice of a wider projection is a view like this). */
+typedef struct moe_rows {
+    const void *data_dev;
+    int type;                      /* MOE_BF16, MOE_F16, MOE_F32 */
+    long long seq, row, head;
+} moe_rows;
+
+/* Quantises M rows per sequence (bf16, fp16 or fp32) into the cache.  Per
+ * block, head and tensor: the step is the smallest power of two (2^-126 at
+ * least) in which the largest magnitude among the new rows is at most 127.5
+ * (int8) or 448 (e4m3) steps; where the block holds earlier positions
+ * (< pos[b]), no smaller than its present one, and if it grows their codes
+ * are rounded again.  Codes are rounded to nearest, ties to even.
+ * Infinities count as the type's largest value and NaN as zero, and set
+ * MOE_KV8_ERR_NONFINITE.  Appending the same rows again changes nothing;
+ * appending at an earlier position overwrites (a rejected draft), keeping the
+ * step that the block had.  M from 1 (a token) to T_cap (a prompt).  One
+ * launch.  Errors: INVALID_ARG, UNSUPPORTED (head layout, block, format), CUDA. */
+int moe_kv8_append(const moe_kv8 *cache, const moe_rows *k_new, const moe_rows *v_new, int M, const int32_t *pos_dev,
+                   const int32_t *counts_dev, int *err_dev, moe_stream_t stream);
+
+/* Values of positions start[b] .. start[b] + n - 1 (start NULL: 0) as bf16,
+ * k_out_dev and v_out_dev [batch][n][kv_heads][head_dim], for attention over a
+ * prompt's earlier part, or moving a sequence.  Exact (a code has at most 7
+ * bits; magnitudes below 2^-133 round).  Zero at positions outside the
+ * cache, or from lens[b] on (lens NULL: T_cap).  One launch. */
+int moe_kv8_read(const moe_kv8 *cache, const int32_t *start_dev, int n, const int32_t *lens_dev, uint16_t *k_out_dev,
+                 uint16_t *v_out_dev, moe_stream_t stream);
+
+/* Scratch of moe_kv8_attn for up to M rows (with acc_dev: weights != 0), no
+ * initialisation.  Errors: INVALID_ARG, UNSUPPORTED. */
+int moe_kv8_attn_workspace_size(const moe_kv8 *cache, int M, int weights, size_t *bytes);
+
+/* Attention of M rows (1 .. 8) of q [batch][M][q_heads][head_dim] (bf16 or
+ * fp16) over the cache, whose positions up to the rows' own are valid:
+ *   s_t = scale q . k_t,  t <= pos[b] + m;  o = sum_t softmax(s)_t v_t,
+ * query head h reading key/value head h / (q_heads / kv_heads).  o_dev
+ * [batch][M][q_heads][head_dim] of o_type.  The keys are split into chunks whose
+ * size depends on the cache's shape alone and joined in order, so a row's result
+ * is bitwise the same for any M and whatever the other sequences are.
+ *
+ * acc_dev (or NULL), fp32 [batch][kv_heads][T_cap], receives the weight of each
+ * position t < pos[b] + counts[b]:
+ *   acc[t] = decay acc_in[t] (t < pos[b]; none from there on) + the sum of
+ *            softmax(s)_t over the rows and the group's query heads;
+ * other entries, and sequences without rows, are left as they were.  acc_in_dev: the earlier weights, may
+ * be acc_dev itself or NULL (none).  Errors: INVALID_ARG, UNSUPPORTED,
+ * BUFFER_TOO_SMALL, CUDA. */
+int moe_kv8_attn(const moe_kv8 *cache, const moe_rows *q, int M, const int32_t *pos_dev, const int32_t *counts_dev,
+                 float scale, void *o_dev, int o_type, const float *acc_in_dev, float *acc_dev, float decay,
+                 void *ws_dev, size_t ws_bytes, int *err_dev, moe_stream_t stream);
+
+/* Keeps at most `budget` of each sequence's lens[b] positions, per key/value
+ * head, and writes them in order to the start of dst (same batch, kv_heads,
+ * head_dim, block and format; budget <= its T_cap; its buffers apart from
+ * src's).  lens[b] <= budget: all of them.  Otherwise the first `sinks`, the
+ * last `recent` (sinks + recent <= budget) and, of the others, those with the
+ * largest acc_dev (fp32 [batch][kv_heads][T_cap]; ties to the lower position,
+ * NaN last).  A dst block's step is the smallest that holds its values; codes
+ * that had a smaller one are rounded to it, the others move exactly.
+ * idx_dev int32 [batch][kv_heads][budget]: the kept positions, -1 past the
+ * last; lens_out_dev int32 [batch] = min(lens[b], budget); dst_acc_dev (or
+ * NULL) fp32 [batch][kv_heads][dst T_cap]: the kept positions' weights.  What
+ * lies past the kept positions in dst and dst_acc is left as it was.  Outputs
+ * must not overlap inputs.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+int moe_kv8_evict(const moe_kv8 *src, const moe_kv8 *dst, const int32_t *lens_dev, const float *acc_dev, int budget,
+                  int sinks, int recent, float *dst_acc_dev, int32_t *idx_dev, int32_t *lens_out_dev, int *err_dev,
+                  moe_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * Streamed layers: the routed experts of a layer live in host memory (the
  * Grace side of a GB300, over NVLink-C2C) and only the experts the router
  * selects are copied into an HBM cache of n_slots expert slots, least

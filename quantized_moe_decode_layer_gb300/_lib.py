@@ -26,6 +26,7 @@ SYMBOLS = ["moe_pack_size", "moe_pack_weights", "moe_layer_destroy", "moe_export
            "moe_decode_layer_noalloc", "moe_noalloc_status",
            "moe_qkv_pack_size", "moe_qkv_pack", "moe_qkv_forward", "moe_qkv_destroy",
            "moe_attn_workspace_size", "moe_attn_decode", "moe_attn_append",
+           "moe_kv8_append", "moe_kv8_read", "moe_kv8_attn_workspace_size", "moe_kv8_attn", "moe_kv8_evict",
            "moe_streamed_size", "moe_streamed_create", "moe_streamed_layer", "moe_streamed_prepare",
            "moe_streamed_stats", "moe_streamed_destroy", "moe_streamed_forward",
            "moe_stream_status", "moe_build_flags", "moe_debug_inject", "moe_debug_set", "moe_debug_trace", "moe_set_grouped", "moe_set_grouped_products", "moe_gate_up_tc", "moe_down_tc", "moe_status_str",
@@ -52,6 +53,17 @@ class SrcMatrix(C.Structure):
 
 class QkvDesc(C.Structure):
     _fields_ = [("H", C.c_int), ("n_q", C.c_int), ("n_k", C.c_int), ("n_v", C.c_int), ("bits", C.c_int)]
+
+
+class Kv8(C.Structure):
+    _fields_ = [("batch", C.c_int), ("q_heads", C.c_int), ("kv_heads", C.c_int), ("head_dim", C.c_int),
+                ("T_cap", C.c_int), ("block", C.c_int), ("format", C.c_int), ("k_dev", C.c_void_p),
+                ("v_dev", C.c_void_p), ("k_scale_dev", C.c_void_p), ("v_scale_dev", C.c_void_p)]
+
+
+class Rows(C.Structure):
+    _fields_ = [("data_dev", C.c_void_p), ("type", C.c_int), ("seq", C.c_longlong), ("row", C.c_longlong),
+                ("head", C.c_longlong)]
 
 
 class SrcLayer(C.Structure):
@@ -95,6 +107,12 @@ def lib():
             "moe_attn_workspace_size": (i, [i, C.POINTER(sz)]),
             "moe_attn_decode": (i, [vp, vp, vp, i, i, i, vp, vp, sz, vp, vp]),
             "moe_attn_append": (i, [vp, vp, i, i, vp, vp, i, vp]),
+            "moe_kv8_append": (i, [C.POINTER(Kv8), C.POINTER(Rows), C.POINTER(Rows), i, vp, vp, vp, vp]),
+            "moe_kv8_read": (i, [C.POINTER(Kv8), vp, i, vp, vp, vp, vp]),
+            "moe_kv8_attn_workspace_size": (i, [C.POINTER(Kv8), i, i, C.POINTER(sz)]),
+            "moe_kv8_attn": (i, [C.POINTER(Kv8), C.POINTER(Rows), i, vp, vp, C.c_float, vp, i, vp, vp, C.c_float, vp,
+                                 sz, vp, vp]),
+            "moe_kv8_evict": (i, [C.POINTER(Kv8), C.POINTER(Kv8), vp, vp, i, i, i, vp, vp, vp, vp, vp]),
             "moe_streamed_size": (i, [C.POINTER(LayerDesc), i, C.POINTER(sz)]),
             "moe_streamed_create": (i, [vp, vp, sz, vp, sz, i, C.POINTER(vp), vp]),
             "moe_streamed_layer": (vp, [vp]),

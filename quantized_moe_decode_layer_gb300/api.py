@@ -7,7 +7,7 @@ import ctypes as C
 import torch
 
 from . import _lib
-from ._lib import LayerDesc, QkvDesc, SrcLayer, SrcMatrix, check, lib
+from ._lib import Kv8, LayerDesc, QkvDesc, Rows, SrcLayer, SrcMatrix, check, lib
 
 
 def _ptr(t) -> int | None:
@@ -479,6 +479,176 @@ class AttnCache:
                                                        pos0, M, _ptr(out), _ptr(self.ws), self.ws.numel(),
                                                        _ptr(err), _stream(stream)))
         return out, err
+
+
+_KV8_FMT = {"int8": (0, torch.int8), "e4m3": (1, torch.float8_e4m3fn)}
+_ROW_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+class KV8Cache:
+    """An 8-bit key/value cache of `batch` sequences (moe_kv8_*): codes k, v
+    [batch, kv_heads, T_cap, head_dim] (int8 or e4m3) and steps k_scale,
+    v_scale, fp32 powers of two, [batch, kv_heads, T_cap / block]; with the
+    scratch that attention of up to max_rows rows needs (weights: also for its
+    position weights) and the calls' error word err (int32 [1]: 1 = a position,
+    count or length outside the cache, 2 = an infinity or NaN was appended).
+
+    pos, counts, lens are int32 [batch] CUDA tensors, read on the device.
+    buffers: (k, v, k_scale, v_scale) to use instead of new ones.  Calls run
+    on the current stream of the cache's device; calls that can overlap on the
+    GPU need caches of their own (or, to read one cache twice at a time,
+    caches over the same buffers)."""
+
+    ERR_RANGE, ERR_NONFINITE = 1, 2
+
+    def __init__(self, T_cap: int, batch: int = 1, q_heads: int = 16, kv_heads: int = 2, head_dim: int = 256,
+                 block: int = 64, fmt: str = "int8", max_rows: int = 8, weights: bool = False, device="cuda",
+                 buffers=None):
+        if fmt not in _KV8_FMT:
+            raise ValueError(f"fmt must be one of {sorted(_KV8_FMT)}")
+        code, self.dtype = _KV8_FMT[fmt]
+        self.T_cap, self.batch, self.q_heads, self.kv_heads = T_cap, batch, q_heads, kv_heads
+        self.head_dim, self.block, self.fmt, self.max_rows, self.weights = head_dim, block, fmt, max_rows, weights
+        self._c = Kv8(batch, q_heads, kv_heads, head_dim, T_cap, block, code)
+        n = C.c_size_t()
+        check("moe_kv8_attn_workspace_size",
+              lib().moe_kv8_attn_workspace_size(C.byref(self._c), max_rows, 1 if weights else 0, C.byref(n)))
+        rows, steps = (batch, kv_heads, T_cap, head_dim), (batch, kv_heads, T_cap // block)
+        if buffers is None:
+            buffers = (torch.zeros(rows, dtype=self.dtype, device=device), torch.zeros(rows, dtype=self.dtype, device=device),
+                       torch.zeros(steps, device=device), torch.zeros(steps, device=device))
+        self.k, self.v, self.k_scale, self.v_scale = buffers
+        for name, t, dt, shape in (("k", self.k, self.dtype, rows), ("v", self.v, self.dtype, rows),
+                                   ("k_scale", self.k_scale, torch.float32, steps),
+                                   ("v_scale", self.v_scale, torch.float32, steps)):
+            _need(t, name, dt, shape)
+        self.device = self.k.device
+        if any(t.device != self.device for t in buffers):
+            raise ValueError("the cache's buffers must be on one device")
+        self.ws = torch.empty(n.value, dtype=torch.uint8, device=self.device)
+        self.err = torch.zeros(1, dtype=torch.int32, device=self.device)
+        c = self._c
+        c.k_dev, c.v_dev, c.k_scale_dev, c.v_scale_dev = (t.data_ptr() for t in buffers)
+        self._ref = C.byref(c)
+
+    def _vec(self, t, name: str, optional: bool = True):
+        if t is None and optional:
+            return None
+        if not (isinstance(t, torch.Tensor) and t.dtype == torch.int32 and t.shape == (self.batch,) and t.is_contiguous()
+                and t.device == self.device):
+            raise ValueError(f"{name} must be a contiguous int32 tensor of shape [{self.batch}] on {self.device}")
+        return t.data_ptr()
+
+    def _view(self, t, name: str, heads: int, types) -> Rows:
+        """A [batch, M, heads, head_dim] tensor, strided but for its last dimension."""
+        if not (isinstance(t, torch.Tensor) and t.dim() == 4 and t.dtype in types and t.device == self.device):
+            raise ValueError(f"{name} must be a tensor of shape [{self.batch}, M, {heads}, {self.head_dim}], one of {types}, "
+                             f"on {self.device}")
+        b, _, h, d = t.shape
+        s = t.stride()
+        if b != self.batch or h != heads or d != self.head_dim or s[3] != 1:
+            raise ValueError(f"{name} must have shape [{self.batch}, M, {heads}, {self.head_dim}] with a contiguous last "
+                             f"dimension; got {tuple(t.shape)}, strides {s}")
+        return Rows(t.data_ptr(), _ROW_TYPES[t.dtype], s[0], s[1], s[2])
+
+    def _like(self, t, name: str, dtype, shape):
+        _need(t, name, dtype, shape)
+        if t.device != self.device:
+            raise ValueError(f"{name} must be on {self.device}")
+        return t.data_ptr()
+
+    def _run(self, fn: str, stream, *args):
+        """The call on `stream` (default: the device's current one) with the cache's device current."""
+        if stream is None:
+            stream = torch.cuda.current_stream(self.device)
+        elif stream.device != self.device:
+            raise ValueError(f"the stream must be on {self.device}")
+        if torch.cuda.current_device() == self.device.index:
+            check(fn, getattr(lib(), fn)(*args, stream.cuda_stream))
+        else:
+            with torch.cuda.device(self.device):
+                check(fn, getattr(lib(), fn)(*args, stream.cuda_stream))
+
+    def append(self, k_new: torch.Tensor, v_new: torch.Tensor, pos: torch.Tensor, counts=None, err=None, stream=None):
+        """Quantise rows [batch, M, kv_heads, head_dim] (bf16, fp16 or fp32; strided
+        views with a contiguous last dimension) into positions pos[b] ..
+        pos[b] + M - 1, or + counts[b] - 1 (moe_kv8_append)."""
+        k = self._view(k_new, "k_new", self.kv_heads, tuple(_ROW_TYPES))
+        v = self._view(v_new, "v_new", self.kv_heads, tuple(_ROW_TYPES))
+        if k_new.dtype != v_new.dtype or k_new.shape != v_new.shape:
+            raise ValueError("k_new and v_new must have one shape and type")
+        e = self.err.data_ptr() if err is None else self._like(err, "err", torch.int32, (1,))
+        self._run("moe_kv8_append", stream, self._ref, C.byref(k), C.byref(v), k_new.shape[1], self._vec(pos, "pos", False),
+                  self._vec(counts, "counts"), e)
+
+    def read(self, start, n: int, lens=None, stream=None):
+        """(k, v) bf16 [batch, n, kv_heads, head_dim]: the values of positions
+        start[b] .. start[b] + n - 1 (start None: 0); zero outside the cache and
+        from lens[b] on (moe_kv8_read)."""
+        out = torch.empty((2, self.batch, n, self.kv_heads, self.head_dim), dtype=torch.bfloat16, device=self.device)
+        k, v = out.unbind(0)
+        self._run("moe_kv8_read", stream, self._ref, self._vec(start, "start"), n, self._vec(lens, "lens"), k.data_ptr(),
+                  v.data_ptr())
+        return k, v
+
+    def attend(self, q: torch.Tensor, pos: torch.Tensor, counts=None, scale=None, acc=None, acc_in=None, decay: float = 1.0,
+               out=None, out_dtype=torch.float32, err=None, stream=None):
+        """Attention of q [batch, M, q_heads, head_dim] (bf16 or fp16, M <= max_rows)
+        at positions pos[b] .. pos[b] + M - 1 (moe_kv8_attn); returns (o, err) with o
+        [batch, M, q_heads, head_dim] of out_dtype (fp32, bf16 or fp16).  scale:
+        1 / sqrt(head_dim) by default.  acc (fp32 [batch, kv_heads, T_cap], the
+        cache built with weights=True) receives decay * acc_in + the weight each
+        position got; acc_in defaults to acc."""
+        r = self._view(q, "q", self.q_heads, (torch.bfloat16, torch.float16))
+        M = q.shape[1]
+        if out is None:
+            out = torch.empty((self.batch, M, self.q_heads, self.head_dim), dtype=out_dtype, device=self.device)
+        elif out.dtype not in _ROW_TYPES:
+            raise ValueError("out must be fp32, bf16 or fp16")
+        else:
+            self._like(out, "out", out.dtype, (self.batch, M, self.q_heads, self.head_dim))
+        if out.dtype not in _ROW_TYPES:
+            raise ValueError("out_dtype must be fp32, bf16 or fp16")
+        if M > self.max_rows:
+            raise ValueError(f"q has {M} rows; the cache was built for max_rows={self.max_rows}")
+        a = a_in = None
+        if acc is not None:
+            if not self.weights:
+                raise ValueError("acc needs a cache built with weights=True")
+            shape = (self.batch, self.kv_heads, self.T_cap)
+            a = self._like(acc, "acc", torch.float32, shape)
+            a_in = a if acc_in is None else self._like(acc_in, "acc_in", torch.float32, shape)
+        elif acc_in is not None:
+            raise ValueError("acc_in needs acc")
+        if err is None:
+            err = self.err
+            e = err.data_ptr()
+        else:
+            e = self._like(err, "err", torch.int32, (1,))
+        self._run("moe_kv8_attn", stream, self._ref, C.byref(r), M, self._vec(pos, "pos", False), self._vec(counts, "counts"),
+                  self.head_dim ** -0.5 if scale is None else scale, out.data_ptr(), _ROW_TYPES[out.dtype], a_in, a, decay,
+                  self.ws.data_ptr(), self.ws.numel(), e)
+        return out, err
+
+    def evict_into(self, dst: "KV8Cache", lens: torch.Tensor, acc: torch.Tensor, budget: int, sinks: int = 4,
+                   recent: int = 0, dst_acc=None, err=None, stream=None):
+        """Keep at most `budget` of each sequence's lens[b] positions per head (the
+        first `sinks`, the last `recent`, then the largest acc) in order at the start of
+        dst (moe_kv8_evict); returns (idx int32 [batch, kv_heads, budget], lens of
+        dst int32 [batch])."""
+        if not isinstance(dst, KV8Cache) or dst.device != self.device:
+            raise ValueError(f"dst must be a KV8Cache on {self.device}")
+        if budget < 1:
+            raise ValueError("budget must be at least 1")
+        a = self._like(acc, "acc", torch.float32, (self.batch, self.kv_heads, self.T_cap))
+        da = None if dst_acc is None else self._like(dst_acc, "dst_acc", torch.float32,
+                                                     (self.batch, self.kv_heads, dst.T_cap))
+        e = self.err.data_ptr() if err is None else self._like(err, "err", torch.int32, (1,))
+        idx = torch.empty((self.batch, self.kv_heads, budget), dtype=torch.int32, device=self.device)
+        n = torch.empty(self.batch, dtype=torch.int32, device=self.device)
+        self._run("moe_kv8_evict", stream, self._ref, dst._ref, self._vec(lens, "lens", False), a, budget, sinks, recent, da,
+                  idx.data_ptr(), n.data_ptr(), e)
+        return idx, n
 
 
 def debug_set(skip_row: int = -1, timeout_ns: int = 0) -> None:

@@ -790,6 +790,116 @@ int moe_attn_append(const uint16_t *k_new_dev, const uint16_t *v_new_dev, int M,
                               reinterpret_cast<cudaStream_t>(stream));
 }
 
+// Shape of an 8-bit cache; the buffers too when `buffers`.
+static int kv8_check(const moe_kv8 *c, bool buffers)
+{
+    if (!c) return MOE_ERR_INVALID_ARG;
+    if (c->batch < 1 || c->kv_heads < 1 || c->q_heads < 1 || c->T_cap < 1) return MOE_ERR_INVALID_ARG;
+    if (c->format != MOE_KV8_INT8 && c->format != MOE_KV8_E4M3) return MOE_ERR_UNSUPPORTED;
+    if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return MOE_ERR_UNSUPPORTED;
+    if (c->block != 16 && c->block != 32 && c->block != 64 && c->block != 128) return MOE_ERR_UNSUPPORTED;
+    if (c->batch > MOE_KV8_MAX_BATCH || c->kv_heads > MOE_KV8_MAX_HEADS || c->T_cap > MOE_KV8_MAX_POSITIONS)
+        return MOE_ERR_UNSUPPORTED;
+    if (c->q_heads % c->kv_heads != 0 || c->q_heads / c->kv_heads > MOE_KV8_MAX_GROUP) return MOE_ERR_UNSUPPORTED;
+    if (c->T_cap % c->block != 0) return MOE_ERR_INVALID_ARG;
+    if (!buffers) return MOE_OK;
+    if (!c->k_dev || !c->v_dev || !c->k_scale_dev || !c->v_scale_dev) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(c->k_dev) || !aligned16(c->v_dev) || !aligned16(c->k_scale_dev) || !aligned16(c->v_scale_dev))
+        return MOE_ERR_INVALID_ARG;
+    return MOE_OK;
+}
+
+static bool kv8_rows_ok(const moe_rows *r, int last_type)
+{
+    return r && r->data_dev && r->type >= MOE_BF16 && r->type <= last_type && r->seq >= 0 && r->row >= 0 && r->head >= 0 &&
+           reinterpret_cast<uintptr_t>(r->data_dev) % (r->type == MOE_F32 ? 4 : 2) == 0;
+}
+
+static bool overlap(const void *a, size_t na, const void *b, size_t nb)
+{
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a && b && x < y + nb && y < x + na;
+}
+
+int moe_kv8_append(const moe_kv8 *cache, const moe_rows *k_new, const moe_rows *v_new, int M, const int32_t *pos_dev,
+                   const int32_t *counts_dev, int *err_dev, moe_stream_t stream)
+{
+    const int rc = kv8_check(cache, true);
+    if (rc) return rc;
+    if (!kv8_rows_ok(k_new, MOE_F32) || !kv8_rows_ok(v_new, MOE_F32) || k_new->type != v_new->type)
+        return MOE_ERR_INVALID_ARG;
+    if (!pos_dev || !err_dev || M < 1 || M > cache->T_cap) return MOE_ERR_INVALID_ARG;
+    return launch_kv8_append(*cache, *k_new, *v_new, M, pos_dev, counts_dev, err_dev,
+                             reinterpret_cast<cudaStream_t>(stream));
+}
+
+int moe_kv8_read(const moe_kv8 *cache, const int32_t *start_dev, int n, const int32_t *lens_dev, uint16_t *k_out_dev,
+                 uint16_t *v_out_dev, moe_stream_t stream)
+{
+    const int rc = kv8_check(cache, true);
+    if (rc) return rc;
+    if (!k_out_dev || !v_out_dev || !aligned16(k_out_dev) || !aligned16(v_out_dev) || n < 1 || n > cache->T_cap)
+        return MOE_ERR_INVALID_ARG;
+    return launch_kv8_read(*cache, start_dev, n, lens_dev, k_out_dev, v_out_dev, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int moe_kv8_attn_workspace_size(const moe_kv8 *cache, int M, int weights, size_t *bytes)
+{
+    const int rc = kv8_check(cache, false);
+    if (rc) return rc;
+    if (!bytes || M < 1 || M > MOE_KV8_MAX_ROWS) return MOE_ERR_INVALID_ARG;
+    *bytes = kv8_attn_workspace_bytes(*cache, M, weights != 0);
+    return MOE_OK;
+}
+
+int moe_kv8_attn(const moe_kv8 *cache, const moe_rows *q, int M, const int32_t *pos_dev, const int32_t *counts_dev,
+                 float scale, void *o_dev, int o_type, const float *acc_in_dev, float *acc_dev, float decay,
+                 void *ws_dev, size_t ws_bytes, int *err_dev, moe_stream_t stream)
+{
+    const int rc = kv8_check(cache, true);
+    if (rc) return rc;
+    if (!kv8_rows_ok(q, MOE_F16) || !pos_dev || !o_dev || !ws_dev || !err_dev || o_type < MOE_BF16 || o_type > MOE_F32)
+        return MOE_ERR_INVALID_ARG;
+    if (M < 1 || M > MOE_KV8_MAX_ROWS || M > cache->T_cap || !aligned16(ws_dev) || !aligned16(o_dev))
+        return MOE_ERR_INVALID_ARG;
+    if (!acc_dev && acc_in_dev) return MOE_ERR_INVALID_ARG;
+    const size_t acc_bytes = (size_t)cache->batch * cache->kv_heads * cache->T_cap * sizeof(float);
+    if (acc_dev != acc_in_dev && overlap(acc_dev, acc_bytes, acc_in_dev, acc_bytes)) return MOE_ERR_INVALID_ARG;
+    if (ws_bytes < kv8_attn_workspace_bytes(*cache, M, acc_dev != nullptr)) return MOE_ERR_BUFFER_TOO_SMALL;
+    return launch_kv8_attn(*cache, *q, M, pos_dev, counts_dev, scale, o_dev, o_type, acc_in_dev, acc_dev, decay, ws_dev,
+                           err_dev, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int moe_kv8_evict(const moe_kv8 *src, const moe_kv8 *dst, const int32_t *lens_dev, const float *acc_dev, int budget,
+                  int sinks, int recent, float *dst_acc_dev, int32_t *idx_dev, int32_t *lens_out_dev, int *err_dev,
+                  moe_stream_t stream)
+{
+    int rc = kv8_check(src, true);
+    if (rc == MOE_OK) rc = kv8_check(dst, true);
+    if (rc) return rc;
+    if (src->batch != dst->batch || src->kv_heads != dst->kv_heads || src->head_dim != dst->head_dim ||
+        src->block != dst->block || src->format != dst->format)
+        return MOE_ERR_INVALID_ARG;
+    if (!lens_dev || !acc_dev || !idx_dev || !lens_out_dev || !err_dev) return MOE_ERR_INVALID_ARG;
+    if (budget < 1 || budget > dst->T_cap || sinks < 0 || recent < 0 || sinks > budget || recent > budget - sinks)
+        return MOE_ERR_INVALID_ARG;
+    const size_t heads = (size_t)src->batch * src->kv_heads, sn = heads * src->T_cap, dn = heads * dst->T_cap;
+    const size_t in_n[] = {sn * src->head_dim, sn * src->head_dim, sn / src->block * 4, sn / src->block * 4, sn * 4,
+                           (size_t)src->batch * 4};
+    const void *in[] = {src->k_dev, src->v_dev, src->k_scale_dev, src->v_scale_dev, acc_dev, lens_dev};
+    const size_t out_n[] = {dn * src->head_dim, dn * src->head_dim, dn / src->block * 4, dn / src->block * 4, dn * 4,
+                            heads * budget * 4, (size_t)src->batch * 4};
+    const void *out[] = {dst->k_dev, dst->v_dev, dst->k_scale_dev, dst->v_scale_dev, dst_acc_dev, idx_dev, lens_out_dev};
+    for (int o = 0; o < 7; ++o) {
+        for (int i = 0; i < 6; ++i)
+            if (overlap(out[o], out_n[o], in[i], in_n[i])) return MOE_ERR_INVALID_ARG;
+        for (int i = 0; i < o; ++i)
+            if (overlap(out[o], out_n[o], out[i], out_n[i])) return MOE_ERR_INVALID_ARG;
+    }
+    return launch_kv8_evict(*src, *dst, lens_dev, acc_dev, budget, sinks, recent, dst_acc_dev, idx_dev, lens_out_dev,
+                            err_dev, reinterpret_cast<cudaStream_t>(stream));
+}
+
 const char *moe_status_str(int status)
 {
     switch (status) {
