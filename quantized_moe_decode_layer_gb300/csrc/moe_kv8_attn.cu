@@ -12,6 +12,10 @@
 // on the other sequences.  A chunk yields, per query column (row and head of
 // a key/value head's group), the maximum, the sum of exp(s - max) and the
 // unnormalised output; the merge kernel joins a row's chunks in order.
+#include <algorithm>
+#include <climits>
+#include <mutex>
+
 #include "moe_kv8.cuh"
 
 namespace moe {
@@ -29,93 +33,571 @@ struct AttnP {
     float *acc;
     float decay, scale_log2;        // scale * log2(e)
     int *err;
-    int B, Hq, Hkv, G, M, C, T_cap, chunk, nchunk, blk_log, nblk, f16, o_type;
+    int B, Hq, Hkv, G, M, C, T_cap, chunk, nchunk, blk_log, nblk, f16, qvec, o_type;
 };
 
-constexpr int kPlainThreads = 128, kPlainCols = 8;
+// ------------------------------------------------------------------ chunks
+// Persistent CTAs of 8 warps take (sequence, chunk, key/value head, column
+// pass) items in turn.  Within a chunk a warp works alone on tiles of 16 R
+// positions (R = 256 / D: 4 KB of keys and 4 KB of values), every eighth
+// one, through a ring of three tiles of its own that cp.async fills ahead,
+// across items, so that loads never stop for the end of a chunk.
+//
+// Per 16 positions and 8 query columns, on m16n8k16 fp16 MMAs:
+//     S^T [16 positions x 8] = K Q^T,   O^T [D x 8] += V^T P^T.
+// Codes are exact in fp16; queries are, after a power of two per row.  The
+// contraction index may be any order of the dimensions as long as both
+// operands share it, so a lane's 16 loaded bytes of a key row are its elements
+// of four MMAs as they come.  Values need pairs of positions in one register:
+// byte permutes of two rows' words.  P^T's transpose is movmatrix.  The
+// weights go in as two fp16 halves (22 bits): sums of many small weights
+// keep fp32's precision, and an fp32 output means something.
+constexpr int kWarps = 8, kThreads = 32 * kWarps, kStages = 3;
+constexpr int kTileBytes = 4096;                       // keys (or values) of a warp's tile
+constexpr int kStageBytes = 2 * kTileBytes + 64;       // and the steps of its up to 4 groups of 16 positions
+constexpr float kWeightUnit = 32768.f;                 // weights are held in units of 2^-15: fp16's small end reaches 2^-39
 
-// The simplest form, in fp32: a CTA takes one chunk of one key/value head for
-// up to 8 query columns; a thread scores one position at a time, then
-// gathers one value dimension.
-template <int FMT, int D>
-__global__ void __launch_bounds__(kPlainThreads) kv8_attn_plain_kernel(const AttnP p)
+template <int D, int NT>
+struct Lay {
+    static constexpr int round = NT == 1 ? 4 : 2;      // m-tiles of the output joined at once
+    static constexpr int ring = 0, red = kWarps * kStages * kStageBytes, q = red + kWarps * round * 512, qrow = 2 * D + 16,
+                         qf = q + 2 * 8 * NT * qrow, ml = qf + 2 * 8 * NT * 4, first = ml + 2 * kWarps * 8 * NT * 4,
+                         total = first;                // + (batch + 1) ints
+};
+
+__device__ __forceinline__ uint32_t smem_u32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool in)
 {
-    __shared__ float q[kPlainCols][D], sc[kPlainCols][kPlainThreads], red[33];
-    const int chunk = blockIdx.x, g = blockIdx.y % p.Hkv, c0 = blockIdx.y / p.Hkv * kPlainCols, b = blockIdx.z, tid = threadIdx.x;
-    int p0;
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp4(uint32_t dst, const void *src, bool in)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t movtrans(uint32_t a)
+{
+    uint32_t d;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    return d;
+}
+
+// Codes to fp16 pairs.  pairs(w): (byte 0, byte 2) and (byte 1, byte 3) for
+// int8 -- fp16 0x6400 | u is 1024 + u, so flipping a code's top bit gives
+// 1024 + 128 + code, and one subtraction is exact --, (0, 1) and (2, 3) for
+// e4m3.  Dimension order does not matter as long as queries follow it.
+template <int FMT>
+__device__ __forceinline__ void pairs(uint32_t w, uint32_t &x, uint32_t &y)
+{
+    if (FMT == MOE_KV8_INT8) {
+        const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
+        const uint32_t a = (w & 0x00FF00FFu) ^ 0x64806480u, b = ((w >> 8) & 0x00FF00FFu) ^ 0x64806480u;
+        const __half2 ha = __hsub2(*reinterpret_cast<const __half2 *>(&a), off), hb = __hsub2(*reinterpret_cast<const __half2 *>(&b), off);
+        x = *reinterpret_cast<const uint32_t *>(&ha);
+        y = *reinterpret_cast<const uint32_t *>(&hb);
+    } else {
+        asm("{ .reg .b16 l, h; mov.b32 {l, h}, %2; cvt.rn.f16x2.e4m3x2 %0, l; cvt.rn.f16x2.e4m3x2 %1, h; }"
+            : "=r"(x), "=r"(y) : "r"(w));
+    }
+}
+// Two rows' words: fp16 pairs (row 0, row 1) of dimensions 0 .. 3.
+template <int FMT>
+__device__ __forceinline__ void cross(uint32_t r0, uint32_t r1, uint32_t (&d)[4])
+{
+    if (FMT == MOE_KV8_INT8) {
+        pairs<FMT>(__byte_perm(r0, r1, 0x5410), d[0], d[1]);
+        pairs<FMT>(__byte_perm(r0, r1, 0x7632), d[2], d[3]);
+    } else {
+        pairs<FMT>(__byte_perm(r0, r1, 0x5140), d[0], d[1]);
+        pairs<FMT>(__byte_perm(r0, r1, 0x7362), d[2], d[3]);
+    }
+}
+
+// One (sequence, chunk, head, column pass).
+struct Item {
+    int b, g, cp, k0, k1, p0, rows;    // positions k0 .. k1 - 1
+};
+
+template <int D, int NT>
+__device__ __forceinline__ Item decode_item(const AttnP &p, const int *first, int item, int passes)
+{
+    Item it;
+    it.cp = item % passes;
+    item /= passes;
+    it.g = item % p.Hkv;
+    item /= p.Hkv;
+    int lo = 0, hi = p.B;              // first[lo] <= item < first[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (first[mid] <= item) lo = mid;
+        else hi = mid;
+    }
+    it.b = lo;
     bool bad;
-    const int rows = kv8_rows(p.pos, p.counts, b, p.M, p.T_cap, p0, bad);
-    if (bad && chunk == 0 && blockIdx.y == 0 && tid == 0) atomicOr(p.err, kKv8ErrRange);
-    const int n = rows > 0 ? p0 + rows : 0, k0 = chunk * p.chunk, k1 = min(k0 + p.chunk, n), nc = min(kPlainCols, p.C - c0);
-    if (k0 >= k1) return;
-    for (int i = tid; i < nc * D; i += kPlainThreads) {
-        const int c = c0 + i / D, m = c / p.G, h = g * p.G + c % p.G;
-        const long long at = b * p.qb + m * p.qm + h * p.qh + i % D;
-        q[i / D][i % D] = p.f16 ? __half2float(static_cast<const __half *>(p.q)[at])
-                                : __bfloat162float(static_cast<const __nv_bfloat16 *>(p.q)[at]);
+    it.rows = kv8_rows(p.pos, p.counts, lo, p.M, p.T_cap, it.p0, bad);
+    it.k0 = (item - first[lo]) * p.chunk;
+    it.k1 = min(it.k0 + p.chunk, it.p0 + it.rows);
+    return it;
+}
+
+// Query columns of an item, one group of D / 8 lanes each: raw values ahead
+// of time, then scaled by a power of two (exactly; 2^12 <= the row's largest
+// < 2^13, elements 2^26 times smaller lose bits) into shared memory.
+template <int D, int NT>
+struct QLoad {
+    static constexpr int kLanes = D / 8, kPer = 8 * NT * kLanes / kThreads > 0 ? 8 * NT * kLanes / kThreads : 1;
+    uint16_t h[kPer][8];
+
+    __device__ __forceinline__ void fetch(const AttnP &p, const Item &it)
+    {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int id = threadIdx.x + i * kThreads, col = id / kLanes, c = it.cp * 8 * NT + col, m = c / p.G;
+            const bool in = col < 8 * NT && c < p.C && m < it.rows;
+            const uint16_t *src = static_cast<const uint16_t *>(p.q) + it.b * p.qb + m * p.qm + (it.g * p.G + c % p.G) * p.qh +
+                                  id % kLanes * 8;
+            if (p.qvec && in) *reinterpret_cast<uint4 *>(h[i]) = __ldg(reinterpret_cast<const uint4 *>(src));
+            else
+#pragma unroll
+                for (int j = 0; j < 8; ++j) h[i][j] = in ? __ldg(src + j) : (uint16_t)0;
+        }
     }
-    const size_t head = (size_t)b * p.Hkv + g;
-    const uint8_t *K = p.k + head * p.T_cap * D, *V = p.v + head * p.T_cap * D;
-    const float *ks = p.ks + head * p.nblk, *vs = p.vs + head * p.nblk;
-    float mx[kPlainCols], l[kPlainCols], o[kPlainCols][(D + kPlainThreads - 1) / kPlainThreads];
-    for (int c = 0; c < kPlainCols; ++c) {
-        mx[c] = -INFINITY;
-        l[c] = 0.f;
-        for (float &x : o[c]) x = 0.f;
-    }
-    for (int t0 = k0; t0 < k1; t0 += kPlainThreads) {
-        const int t = t0 + tid;
-        float s[kPlainCols];
-        for (float &x : s) x = 0.f;
-        __syncthreads();
-        if (t < k1) {
-            const float f = ks[t >> p.blk_log] * p.scale_log2;
-            for (int d = 0; d < D; d += 4) {
-                float x[4];
-                decode4<FMT>(__ldg(reinterpret_cast<const uint32_t *>(K + (size_t)t * D + d)), x);
-                for (int c = 0; c < kPlainCols; ++c)
-                    if (c < nc)
-                        for (int i = 0; i < 4; ++i) s[c] = fmaf(q[c][d + i], x[i], s[c]);
+    __device__ __forceinline__ void store(const AttnP &p, uint8_t *q, float *qf)
+    {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int id = threadIdx.x + i * kThreads, col = id / kLanes;
+            float v[8], a = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                v[j] = p.f16 ? __half2float(__ushort_as_half(h[i][j])) : __uint_as_float((uint32_t)h[i][j] << 16);
+                a = fmaxf(a, fabsf(v[j]));
             }
-            for (int c = 0; c < kPlainCols; ++c)
-                if (c < nc) {
-                    s[c] *= f;
-                    if (p.sc) p.sc[(head * p.T_cap + t) * p.C + c0 + c] = s[c];
-                }
-        }
-        for (int c = 0; c < nc; ++c) {
-            const bool see = t < k1 && t <= p0 + (c0 + c) / p.G && (c0 + c) / p.G < rows;
-            const float tm = cta_max(see ? s[c] : -INFINITY, red);
-            const float nm = fmaxf(mx[c], tm), base = nm == -INFINITY ? 0.f : nm;
-            const float w = see ? exp2f(s[c] - base) : 0.f, al = exp2f(mx[c] - base);
-            sc[c][tid] = w;
-            mx[c] = nm;
-            l[c] *= al;
-            for (float &x : o[c]) x *= al;
-        }
-        __syncthreads();
-        for (int i = 0; i < min(kPlainThreads, k1 - t0); ++i) {
-            const float f = vs[(t0 + i) >> p.blk_log];
-            for (int c = 0; c < nc; ++c) l[c] += sc[c][i];
-            for (int j = 0; j < (D + kPlainThreads - 1) / kPlainThreads; ++j) {
-                const int d = tid + j * kPlainThreads;
-                if (d < D) {
-                    float x[4];
-                    decode4<FMT>(V[(size_t)(t0 + i) * D + d], x);
-                    for (int c = 0; c < nc; ++c) o[c][j] = fmaf(sc[c][i], x[0] * f, o[c][j]);
-                }
+#pragma unroll
+            for (int o = kLanes / 2; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
+            const int e = (int)(__float_as_uint(a) >> 23) - 127;
+            const bool odd = a == 0.f || e == 128;               // zero or infinite: as it is
+            const int up = odd ? 0 : max(-126, min(126, 12 - e));
+            const float f = pow2f(up);
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const __half2 t = __floats2half2_rn(v[2 * j] * f, v[2 * j + 1] * f);
+                w[j] = *reinterpret_cast<const uint32_t *>(&t);
+            }
+            if (col < 8 * NT) {
+                *reinterpret_cast<uint4 *>(q + col * Lay<D, NT>::qrow + id % kLanes * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+                if (id % kLanes == 0) qf[col] = p.scale_log2 * pow2f(-up);
             }
         }
     }
-    const size_t slot = ((size_t)b * p.nchunk + chunk) * p.Hkv + g;
-    for (int c = 0; c < nc; ++c) {
-        if (tid == 0) {
-            p.part_ml[(slot * p.C + c0 + c) * 2] = mx[c];
-            p.part_ml[(slot * p.C + c0 + c) * 2 + 1] = l[c];
-        }
-        for (int j = 0; j < (D + kPlainThreads - 1) / kPlainThreads; ++j)
-            if (tid + j * kPlainThreads < D) p.part_o[(slot * p.C + c0 + c) * D + tid + j * kPlainThreads] = o[c][j];
+};
+
+template <int FMT, int D, int NT>
+__global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const AttnP p)
+{
+    using L = Lay<D, NT>;
+    constexpr int R = 256 / D, TK = 16 * R, KS = D / 16, NC = 8 * NT;   // KS: k-steps of S, m-tiles of O
+    extern __shared__ __align__(128) uint8_t sm[];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, tq = lane & 3;
+    int *first = reinterpret_cast<int *>(sm + L::first);
+    float *red_m = reinterpret_cast<float *>(sm + L::ml), *red_l = red_m + kWarps * NC;
+    const int passes = (p.C + NC - 1) / NC;
+
+    // chunks before each sequence's
+    for (int b = tid; b < p.B; b += kThreads) {
+        int p0;
+        bool bad;
+        const int rows = kv8_rows(p.pos, p.counts, b, p.M, p.T_cap, p0, bad);
+        if (bad && blockIdx.x == 0) atomicOr(p.err, kKv8ErrRange);
+        first[b + 1] = rows > 0 ? (p0 + rows + p.chunk - 1) / p.chunk : 0;
     }
+    __syncthreads();
+    if (warp == 0) {
+        int before = 0;
+        for (int b0 = 0; b0 < p.B; b0 += 32) {
+            int v = b0 + lane < p.B ? first[b0 + lane + 1] : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u = __shfl_up_sync(0xFFFFFFFFu, v, o);
+                if (lane >= o) v += u;
+            }
+            if (b0 + lane < p.B) first[b0 + lane + 1] = before + v;
+            before += __shfl_sync(0xFFFFFFFFu, v, 31);
+        }
+        if (lane == 0) first[0] = 0;
+    }
+    __syncthreads();
+    const int total = first[p.B] * p.Hkv * passes;
+    if ((int)blockIdx.x >= total) return;
+
+    uint8_t *ring = sm + L::ring + warp * kStages * kStageBytes;
+    const uint32_t ring_u = smem_u32(ring);
+
+    // The load cursor runs kStages tiles ahead of the compute cursor; an
+    // empty commit keeps the group count when it has run out.
+    int ld_item = blockIdx.x, ld_j = warp, ld_stage = 0;
+    Item ld = decode_item<D, NT>(p, first, ld_item, passes);
+    auto load_tile = [&]() {
+        while (ld_item < total && ld.k0 + ld_j * TK >= ld.k1) {
+            ld_item += gridDim.x;
+            ld_j = warp;
+            if (ld_item < total) ld = decode_item<D, NT>(p, first, ld_item, passes);
+        }
+        if (ld_item < total) {
+            const int t0 = ld.k0 + ld_j * TK;
+            const size_t head = (size_t)ld.b * p.Hkv + ld.g;
+            const uint8_t *K = p.k + (head * p.T_cap + t0) * D, *V = p.v + (head * p.T_cap + t0) * D;
+            const uint32_t dst = ring_u + ld_stage * kStageBytes;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int id = lane + 32 * i, row = id / (D / 16), c = id % (D / 16);
+                const bool in = t0 + row < ld.k1;
+                const int ck = D == 64 ? c : c ^ ((row & 1) << 2), cv = D == 64 ? c ^ (row & 2) : c ^ (row & 6);
+                cp16(dst + row * D + ck * 16, in ? K + id * 16 : p.k, in);
+                cp16(dst + kTileBytes + row * D + cv * 16, in ? V + id * 16 : p.v, in);
+            }
+            if (lane < 2 * R) {
+                const int t = t0 + 16 * (lane >> 1);
+                const bool in = t < ld.k1;
+                const float *s = (lane & 1 ? p.vs : p.ks) + head * p.nblk;
+                cp4(dst + 2 * kTileBytes + lane * 4, in ? s + (t >> p.blk_log) : s, in);
+            }
+            ld_j += kWarps;
+        }
+        cp_commit();
+        ld_stage = ld_stage + 1 == kStages ? 0 : ld_stage + 1;
+    };
+#pragma unroll
+    for (int i = 0; i < kStages; ++i) load_tile();
+
+    QLoad<D, NT> ql;
+    Item it = decode_item<D, NT>(p, first, blockIdx.x, passes);
+    ql.fetch(p, it);
+    ql.store(p, sm + L::q, reinterpret_cast<float *>(sm + L::qf));
+    __syncthreads();
+
+    int stage = 0, par = 0;
+#pragma unroll 1
+    for (int item = blockIdx.x; item < total; item += gridDim.x, par ^= 1) {
+        Item next;
+        const bool more = item + (int)gridDim.x < total;
+        if (more) {
+            next = decode_item<D, NT>(p, first, item + gridDim.x, passes);
+            ql.fetch(p, next);
+        }
+        const uint8_t *qs = sm + L::q + par * NC * L::qrow;
+        const float *qf = reinterpret_cast<const float *>(sm + L::qf) + par * NC;
+        float f[NT][2], m[NT][2], l[NT][2], o[NT][KS][4], vref = 0.f, inv_vref = 0.f;
+        uint32_t qr[NT == 1 ? KS : 1][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                f[n][c] = qf[8 * n + 2 * tq + c];
+                m[n][c] = -INFINITY;
+                l[n][c] = 0.f;
+            }
+#pragma unroll
+            for (int k = 0; k < KS; ++k)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) o[n][k][c] = 0.f;
+        }
+        // Element order of k-step 4 i + j: the lane's bytes 4 j .. 4 j + 3 of
+        // 16 at 64 i + 16 t, pairs as pairs() gives them.
+        auto q_frag = [&](int n, int i, uint32_t (&b)[8]) {
+            const uint4 *src = reinterpret_cast<const uint4 *>(qs + (8 * n + gq) * L::qrow + (64 * i + 16 * tq) * 2);
+            const uint4 x = src[0], y = src[1];
+            const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                b[2 * j] = FMT == MOE_KV8_INT8 ? __byte_perm(w[2 * j], w[2 * j + 1], 0x5410) : w[2 * j];
+                b[2 * j + 1] = FMT == MOE_KV8_INT8 ? __byte_perm(w[2 * j], w[2 * j + 1], 0x7632) : w[2 * j + 1];
+            }
+        };
+        if (NT == 1) {
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) {
+                uint32_t b[8];
+                q_frag(0, i, b);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    qr[NT == 1 ? 4 * i + j : 0][0] = b[2 * j];
+                    qr[NT == 1 ? 4 * i + j : 0][1] = b[2 * j + 1];
+                }
+            }
+        }
+
+#pragma unroll 1
+        for (int t0 = it.k0 + warp * TK; t0 < it.k1; t0 += kWarps * TK) {
+            cp_wait<kStages - 1>();
+            __syncwarp();
+            const uint8_t *kt = ring + stage * kStageBytes, *vt = kt + kTileBytes;
+            const float *steps = reinterpret_cast<const float *>(vt + kTileBytes);
+            // ---- scores
+            float s[R][NT][4];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                float acc[NT][2][4];
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) acc[n][0][c] = acc[n][1][c] = 0.f;
+#pragma unroll
+                for (int i = 0; i < D / 64; ++i) {
+                    const int row = 16 * r + gq, ck = D == 64 ? 4 * i + tq : (4 * i + tq) ^ ((gq & 1) << 2);
+                    const uint4 u = *reinterpret_cast<const uint4 *>(kt + row * D + ck * 16);
+                    const uint4 w = *reinterpret_cast<const uint4 *>(kt + (row + 8) * D + ck * 16);
+                    const uint32_t uw[4] = {u.x, u.y, u.z, u.w}, ww[4] = {w.x, w.y, w.z, w.w};
+                    uint32_t b[NT][8];
+                    if (NT > 1) {
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) q_frag(n, i, b[n]);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t a0, a1, a2, a3;
+                        pairs<FMT>(uw[j], a0, a2);
+                        pairs<FMT>(ww[j], a1, a3);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+                            if (NT == 1) mma(acc[n][j & 1], a0, a1, a2, a3, qr[NT == 1 ? 4 * i + j : 0][0], qr[NT == 1 ? 4 * i + j : 0][1]);
+                            else mma(acc[n][j & 1], a0, a1, a2, a3, b[n][2 * j], b[n][2 * j + 1]);
+                    }
+                }
+                const float ks = steps[2 * r];
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        s[r][n][c] = __fmul_rn(__fadd_rn(acc[n][0][c], acc[n][1][c]), __fmul_rn(ks, f[n][c & 1]));
+            }
+            if (p.sc) {
+                float *sc = p.sc + (((size_t)it.b * p.Hkv + it.g) * p.T_cap + t0) * p.C + it.cp * NC;
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const int row = 16 * r + gq + 8 * (c >> 1), col = 8 * n + 2 * tq + (c & 1);
+                            if (t0 + row < it.k1 && it.cp * NC + col < p.C) sc[(size_t)row * p.C + col] = s[r][n][c];
+                        }
+            }
+            // ---- positions that a row does not see (the call's own rows, and the end)
+            if (t0 + TK > it.p0 + 1) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const int see = min(it.p0 + 1 + (it.cp * NC + 8 * n + 2 * tq + c) / p.G, it.k1);
+#pragma unroll
+                        for (int r = 0; r < R; ++r) {
+                            if (t0 + 16 * r + gq >= see) s[r][n][c] = -INFINITY;
+                            if (t0 + 16 * r + gq + 8 >= see) s[r][n][c + 2] = -INFINITY;
+                        }
+                    }
+            }
+            // ---- running maxima; the values' largest step so far is the unit of the output
+            float mn[NT][2];
+            bool grew = false;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float x = fmaxf(s[0][n][c], s[0][n][c + 2]);
+#pragma unroll
+                    for (int r = 1; r < R; ++r) x = fmaxf(x, fmaxf(s[r][n][c], s[r][n][c + 2]));
+                    x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 4));
+                    x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
+                    x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
+                    mn[n][c] = fmaxf(m[n][c], x);
+                    grew |= mn[n][c] > m[n][c];
+                }
+            float vmax = steps[1];
+#pragma unroll
+            for (int r = 1; r < R; ++r) vmax = fmaxf(vmax, steps[2 * r + 1]);
+            if (__any_sync(0xFFFFFFFFu, grew) || vmax > vref) {
+                float down = 1.f;
+                if (vmax > vref) {
+                    inv_vref = 1.f / vmax;
+                    down = __fmul_rn(vref, inv_vref);
+                    vref = vmax;
+                }
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const float al = mn[n][c] == -INFINITY ? 1.f : ex2(__fsub_rn(m[n][c], mn[n][c]));
+                        l[n][c] = __fmul_rn(l[n][c], al);
+                        const float ao = __fmul_rn(al, down);
+#pragma unroll
+                        for (int k = 0; k < KS; ++k) {
+                            o[n][k][c] = __fmul_rn(o[n][k][c], ao);
+                            o[n][k][c + 2] = __fmul_rn(o[n][k][c + 2], ao);
+                        }
+                        m[n][c] = mn[n][c];
+                    }
+            }
+            // ---- weights, their sums, and the output
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                uint32_t ph[NT][2], pl[NT][2];
+                const float unit = __fmul_rn(__fmul_rn(steps[2 * r + 1], inv_vref), kWeightUnit);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    float w[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const float base = m[n][c & 1] == -INFINITY ? 0.f : m[n][c & 1];
+                        const float x = ex2(__fsub_rn(s[r][n][c], base));
+                        l[n][c & 1] = __fadd_rn(l[n][c & 1], x);
+                        w[c] = __fmul_rn(x, unit);
+                    }
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const __half2 hi = __floats2half2_rn(w[2 * h], w[2 * h + 1]);
+                        const float2 back = __half22float2(hi);
+                        const __half2 lo = __floats2half2_rn(__fsub_rn(w[2 * h], back.x), __fsub_rn(w[2 * h + 1], back.y));
+                        ph[n][h] = movtrans(*reinterpret_cast<const uint32_t *>(&hi));
+                        pl[n][h] = movtrans(*reinterpret_cast<const uint32_t *>(&lo));
+                    }
+                }
+                constexpr int VW = D >= 128 ? 4 : 2;             // words of a row per load
+#pragma unroll
+                for (int h = 0; h < (D + 127) / 128; ++h) {
+                    uint32_t v[4][VW];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const int row = 16 * r + 2 * tq + (x & 1) + 8 * (x >> 1);
+                        if (D >= 128) {
+                            const int c = (gq + 8 * h) ^ (row & 6);
+                            const uint4 u = *reinterpret_cast<const uint4 *>(vt + row * D + c * 16);
+                            v[x][0] = u.x;
+                            v[x][1] = u.y;
+                            v[x][VW - 2] = u.z;
+                            v[x][VW - 1] = u.w;
+                        } else {
+                            const int c = (gq >> 1) ^ (row & 2);
+                            const uint2 u = *reinterpret_cast<const uint2 *>(vt + row * D + c * 16 + (gq & 1) * 8);
+                            v[x][0] = u.x;
+                            v[x][1] = u.y;
+                        }
+                    }
+#pragma unroll
+                    for (int w = 0; w < VW; ++w) {
+                        uint32_t a[4], b[4];
+                        cross<FMT>(v[0][w], v[1][w], a);
+                        cross<FMT>(v[2][w], v[3][w], b);
+                        const int k = (VW * h + w) * 2;
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            mma(o[n][k], a[0], a[1], b[0], b[1], ph[n][0], ph[n][1]);
+                            mma(o[n][k + 1], a[2], a[3], b[2], b[3], ph[n][0], ph[n][1]);
+                            mma(o[n][k], a[0], a[1], b[0], b[1], pl[n][0], pl[n][1]);
+                            mma(o[n][k + 1], a[2], a[3], b[2], b[3], pl[n][0], pl[n][1]);
+                        }
+                    }
+                }
+            }
+            __syncwarp();                                          // the tile is read before its slot is filled again
+            load_tile();
+            stage = stage + 1 == kStages ? 0 : stage + 1;
+        }
+
+        // ---- the chunk's result from the warps'
+        if (more) ql.store(p, sm + L::q + (par ^ 1) * NC * L::qrow, reinterpret_cast<float *>(sm + L::qf) + (par ^ 1) * NC);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                float x = l[n][c];
+                x = __fadd_rn(x, __shfl_xor_sync(0xFFFFFFFFu, x, 4));
+                x = __fadd_rn(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
+                x = __fadd_rn(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
+                if (gq == 0) {
+                    red_m[warp * NC + 8 * n + 2 * tq + c] = m[n][c];
+                    red_l[warp * NC + 8 * n + 2 * tq + c] = x;
+                }
+            }
+        __syncthreads();
+        const size_t slot = ((size_t)it.b * p.nchunk + it.k0 / p.chunk) * p.Hkv + it.g, col0 = slot * p.C + it.cp * NC;
+        const int cols = min(NC, p.C - it.cp * NC);
+        if (tid < cols) {
+            float mx = -INFINITY, sum = 0.f;
+            for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, red_m[w * NC + tid]);
+            for (int w = 0; w < kWarps; ++w) {
+                const float x = red_m[w * NC + tid];
+                sum = fmaf(mx == -INFINITY ? 1.f : ex2(__fsub_rn(x, mx)), red_l[w * NC + tid], sum);
+            }
+            p.part_ml[(col0 + tid) * 2] = mx;
+            p.part_ml[(col0 + tid) * 2 + 1] = sum;
+        }
+        float co[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                float mx = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, red_m[w * NC + 8 * n + 2 * tq + c]);
+                co[n][c] = mx == -INFINITY ? 1.f : ex2(__fsub_rn(m[n][c], mx));
+            }
+        const float back = __fmul_rn(vref, 1.f / kWeightUnit);
+        // a few m-tiles at a time: every warp's fragments side by side, then one
+        // warp per m-tile adds them up
+        float4 *red = reinterpret_cast<float4 *>(sm + L::red);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int k0 = 0; k0 < KS; k0 += L::round) {
+                __syncthreads();
+#pragma unroll
+                for (int k = 0; k < L::round; ++k) {
+                    const float *x = o[n][k0 + k];
+                    red[(warp * L::round + k) * 32 + lane] = make_float4(__fmul_rn(__fmul_rn(x[0], co[n][0]), back), __fmul_rn(__fmul_rn(x[1], co[n][1]), back),
+                                                                  __fmul_rn(__fmul_rn(x[2], co[n][0]), back), __fmul_rn(__fmul_rn(x[3], co[n][1]), back));
+                }
+                __syncthreads();
+                if (tid < 32 * L::round) {
+                    const int k = k0 + (tid >> 5);
+                    float4 a = red[tid];
+#pragma unroll
+                    for (int w = 1; w < kWarps; ++w) {
+                        const float4 x = red[w * 32 * L::round + tid];
+                        a.x = __fadd_rn(a.x, x.x);
+                        a.y = __fadd_rn(a.y, x.y);
+                        a.z = __fadd_rn(a.z, x.z);
+                        a.w = __fadd_rn(a.w, x.w);
+                    }
+                    // m-tile k: dimensions d (rows g) and d + 1 (rows g + 8)
+                    constexpr int VW = D >= 128 ? 4 : 2;
+                    const int h = k / (2 * VW), w = k / 2 % VW, d = 4 * VW * (gq + 8 * h) + 4 * w + 2 * (k & 1);
+                    const int c = 8 * n + 2 * tq;
+                    if (c < cols) *reinterpret_cast<float2 *>(p.part_o + (col0 + c) * D + d) = make_float2(a.x, a.z);
+                    if (c + 1 < cols) *reinterpret_cast<float2 *>(p.part_o + (col0 + c + 1) * D + d) = make_float2(a.y, a.w);
+                }
+            }
+        if (more) it = next;
+    }
+    cp_wait<0>();
 }
 
 __device__ __forceinline__ void store_out(void *o, int type, size_t i, float v)
@@ -125,34 +607,57 @@ __device__ __forceinline__ void store_out(void *o, int type, size_t i, float v)
     else static_cast<float *>(o)[i] = v;
 }
 
-// Joins a row's chunks in order: one CTA per (row and query head, sequence), a thread per value dimension.
-__global__ void kv8_merge_kernel(const AttnP p)
+// Joins a row's chunks: one CTA per (row, query head, 64 value dimensions;
+// sequence).  16 groups of 16 lanes (four dimensions each) take every 16th
+// chunk and are added in order, so the order depends on the number of chunks
+// alone.
+constexpr int kMergeThreads = 256;
+
+__global__ void __launch_bounds__(kMergeThreads) kv8_merge_kernel(const AttnP p, int D)
 {
-    const int D = blockDim.x, m = blockIdx.x / p.Hq, h = blockIdx.x % p.Hq, b = blockIdx.y, d = threadIdx.x;
+    __shared__ float red[33], so[16][16][4], sl[16];
+    const int slices = D / 64, tid = threadIdx.x, x = blockIdx.x / slices, b = blockIdx.y;
+    const int m = x / p.Hq, h = x % p.Hq, lane = tid & 15, grp = tid >> 4, d = blockIdx.x % slices * 64 + lane * 4;
     const int g = h / p.G, c = m * p.G + h % p.G;
     int p0;
     bool bad;
     const int rows = kv8_rows(p.pos, p.counts, b, p.M, p.T_cap, p0, bad);
     const int n = m < rows ? p0 + m + 1 : 0, nch = (n + p.chunk - 1) / p.chunk;
-    const size_t out = ((size_t)(b * p.M + m) * p.Hq + h) * D + d;
+    const size_t out = ((size_t)(b * p.M + m) * p.Hq + h) * D;
     if (nch == 0) {
-        store_out(p.o, p.o_type, out, 0.f);
+        if (tid < 64) store_out(p.o, p.o_type, out + blockIdx.x % slices * 64 + tid, 0.f);
         return;
     }
-    const size_t slot0 = (size_t)b * p.nchunk * p.Hkv + g;
+    const size_t c0 = ((size_t)b * p.nchunk * p.Hkv + g) * p.C + c, step = (size_t)p.Hkv * p.C;
     float mx = -INFINITY;
-    for (int j = 0; j < nch; ++j) {
-        const float v = __ldg(p.part_ml + ((slot0 + (size_t)j * p.Hkv) * p.C + c) * 2);
-        mx = v > mx || v != v ? v : mx;   // a NaN stays
+    for (int j = tid; j < nch; j += kMergeThreads) mx = fmaxf(mx, __ldg(p.part_ml + (c0 + j * step) * 2));
+    mx = cta_max(mx, red);
+    float o[4] = {0.f, 0.f, 0.f, 0.f}, l = 0.f;
+#pragma unroll 4
+    for (int j = grp; j < nch; j += 16) {
+        const size_t i = c0 + j * step;
+        const float2 ml = __ldg(reinterpret_cast<const float2 *>(p.part_ml) + i);
+        const float4 v = __ldg(reinterpret_cast<const float4 *>(p.part_o + i * D + d));
+        const float w = exp2f(ml.x - mx);
+        l = fmaf(w, ml.y, l);
+        o[0] = fmaf(w, v.x, o[0]);
+        o[1] = fmaf(w, v.y, o[1]);
+        o[2] = fmaf(w, v.z, o[2]);
+        o[3] = fmaf(w, v.w, o[3]);
     }
-    float o = 0.f, l = 0.f;
-    for (int j = 0; j < nch; ++j) {
-        const size_t i = (slot0 + (size_t)j * p.Hkv) * p.C + c;
-        const float w = exp2f(__ldg(p.part_ml + i * 2) - mx);
-        l = fmaf(w, __ldg(p.part_ml + i * 2 + 1), l);
-        o = fmaf(w, __ldg(p.part_o + i * D + d), o);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) so[grp][lane][i] = o[i];
+    if (lane == 0) sl[grp] = l;
+    __syncthreads();
+    if (tid < 64) {
+        float a = 0.f, s = 0.f;
+        const int ng = min(nch, 16);
+        for (int i = 0; i < ng; ++i) {
+            a += so[i][tid >> 2][tid & 3];
+            s += sl[i];
+        }
+        store_out(p.o, p.o_type, out + blockIdx.x % slices * 64 + tid, a / s);
     }
-    store_out(p.o, p.o_type, out, o / l);
 }
 
 // Weight received by each position: every CTA joins the columns' maxima and
@@ -194,8 +699,14 @@ __global__ void __launch_bounds__(kAccThreads) kv8_weights_kernel(const AttnP p)
     p.acc[head * p.T_cap + t] = a;
 }
 
-// Positions per chunk.
-int kv8_chunk(const moe_kv8 &c) { return c.T_cap <= 8192 ? 256 : 512; }
+// Positions per chunk: a multiple of what the 8 warps take at once (64 KB of keys and values).
+int kv8_chunk(const moe_kv8 &c) { return (c.T_cap <= 8192 ? 1 : 4) * 32768 / c.head_dim; }
+
+// Once per kernel and device.
+struct Once {
+    std::once_flag flag[64];
+    int sms[64] = {};
+};
 
 struct Kv8Ws {
     size_t ml, o, sc, total;
@@ -256,26 +767,52 @@ int launch_kv8_attn(const moe_kv8 &c, const moe_rows &q, int M, const int32_t *p
     p.nblk = c.T_cap / c.block;
     p.f16 = q.type == MOE_F16;
     p.o_type = o_type;
-    const dim3 grid(p.nchunk, c.kv_heads * ((p.C + kPlainCols - 1) / kPlainCols), c.batch);
-    auto go = [&](auto kernel) { kernel<<<grid, kPlainThreads, 0, stream>>>(p); };
+    p.qvec = reinterpret_cast<uintptr_t>(q.data_dev) % 16 == 0 && q.seq % 8 == 0 && q.row % 8 == 0 && q.head % 8 == 0;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || dev < 0 || dev >= 64) { note_cuda_error((int)e); return MOE_ERR_CUDA; }
+    const int nt = p.C <= 8 ? 1 : 2;
+    const long long items = (long long)p.nchunk * p.B * p.Hkv * ((p.C + 8 * nt - 1) / (8 * nt));
+    if (items > INT_MAX) return MOE_ERR_UNSUPPORTED;
+    auto go = [&](auto kernel, int smem, Once &once) {
+        std::call_once(once.flag[dev], [&] {
+            e = cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+            if (e == cudaSuccess) e = cudaDeviceGetAttribute(&once.sms[dev], cudaDevAttrMultiProcessorCount, dev);
+        });
+        if (e != cudaSuccess || once.sms[dev] < 1) return;
+        kernel<<<(int)std::min<long long>(items, once.sms[dev]), kThreads, smem + (p.B + 1) * (int)sizeof(int), stream>>>(p);
+    };
+#define KV8_GO(F, D, N)                                                                     \
+    do {                                                                                    \
+        static Once once;                                                                   \
+        static_assert(Lay<D, N>::total + (MOE_KV8_MAX_BATCH + 1) * 4 <= kSmemMax, "shared memory"); \
+        go(kv8_chunk_kernel<F, D, N>, Lay<D, N>::total, once);                              \
+    } while (0)
+#define KV8_GO_D(F, N)                                \
+    do {                                              \
+        if (c.head_dim == 64) KV8_GO(F, 64, N);       \
+        else if (c.head_dim == 128) KV8_GO(F, 128, N); \
+        else KV8_GO(F, 256, N);                       \
+    } while (0)
     if (c.format == MOE_KV8_INT8) {
-        if (c.head_dim == 64) go(kv8_attn_plain_kernel<MOE_KV8_INT8, 64>);
-        else if (c.head_dim == 128) go(kv8_attn_plain_kernel<MOE_KV8_INT8, 128>);
-        else go(kv8_attn_plain_kernel<MOE_KV8_INT8, 256>);
+        if (nt == 1) KV8_GO_D(MOE_KV8_INT8, 1);
+        else KV8_GO_D(MOE_KV8_INT8, 2);
     } else {
-        if (c.head_dim == 64) go(kv8_attn_plain_kernel<MOE_KV8_E4M3, 64>);
-        else if (c.head_dim == 128) go(kv8_attn_plain_kernel<MOE_KV8_E4M3, 128>);
-        else go(kv8_attn_plain_kernel<MOE_KV8_E4M3, 256>);
+        if (nt == 1) KV8_GO_D(MOE_KV8_E4M3, 1);
+        else KV8_GO_D(MOE_KV8_E4M3, 2);
     }
+#undef KV8_GO_D
+#undef KV8_GO
+    if (e != cudaSuccess) { note_cuda_error((int)e); return MOE_ERR_CUDA; }
     note_launch();
-    kv8_merge_kernel<<<dim3(M * c.q_heads, c.batch), c.head_dim, 0, stream>>>(p);
+    kv8_merge_kernel<<<dim3(M * c.q_heads * (c.head_dim / 64), c.batch), kMergeThreads, 0, stream>>>(p, c.head_dim);
     note_launch();
     if (acc) {
         kv8_weights_kernel<<<dim3((c.T_cap + kAccThreads - 1) / kAccThreads, c.kv_heads, c.batch), kAccThreads,
                              p.C * 2 * sizeof(float), stream>>>(p);
         note_launch();
     }
-    const cudaError_t e = cudaGetLastError();
+    e = cudaGetLastError();
     if (e != cudaSuccess) { note_cuda_error((int)e); return MOE_ERR_CUDA; }
     return MOE_OK;
 }

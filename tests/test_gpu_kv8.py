@@ -10,7 +10,7 @@ more factors: |e| <= (D + 4) 2^-23 smax with smax the largest scale * sum |q_d
 k_d|; the exponential adds a few 2^-23 of itself and of |s| <= smax.  A relative
 error e of every weight moves the weighted mean by at most 2 e sum_t w_t |v_t|
 (oabs).  The sums over positions add at most one 2^-23 per addition in a row;
-a chunk has at most 1024 positions, and a row's chunks are joined one by one:
+a chunk has at most 1024 additions in a row, and a row's chunks are joined one by one:
 (1024 + chunks) 2^-23 oabs, for numerator and denominator.  A weight may
 be split into two halves of 11 bits: 2^-22.  An output in bf16 (fp16) is off
 by 2^-8 (2^-11) of itself more; fp16's smallest step is 2^-24."""
