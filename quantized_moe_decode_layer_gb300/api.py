@@ -483,6 +483,7 @@ class AttnCache:
 
 _KV8_FMT = {"int8": (0, torch.int8), "e4m3": (1, torch.float8_e4m3fn)}
 _ROW_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_Q_TYPES = (torch.bfloat16, torch.float16)
 
 
 class KV8Cache:
@@ -529,66 +530,81 @@ class KV8Cache:
         self.err = torch.zeros(1, dtype=torch.int32, device=self.device)
         c = self._c
         c.k_dev, c.v_dev, c.k_scale_dev, c.v_scale_dev = (t.data_ptr() for t in buffers)
+        # What every call needs, once: a decode step is a few microseconds of
+        # device time, so the binding's own time is most of a small call's.
+        self._index = self.device.index
         self._ref = C.byref(c)
+        self._ws, self._err, self._ws_bytes = self.ws.data_ptr(), self.err.data_ptr(), n.value
+        self._vec_shape, self._acc_shape = (batch,), (batch, kv_heads, T_cap)
+        L = lib()
+        self._f_append, self._f_read, self._f_attn, self._f_evict = (L.moe_kv8_append, L.moe_kv8_read, L.moe_kv8_attn,
+                                                                     L.moe_kv8_evict)
 
-    def _vec(self, t, name: str, optional: bool = True):
-        if t is None and optional:
-            return None
-        if not (isinstance(t, torch.Tensor) and t.dtype == torch.int32 and t.shape == (self.batch,) and t.is_contiguous()
-                and t.device == self.device):
-            raise ValueError(f"{name} must be a contiguous int32 tensor of shape [{self.batch}] on {self.device}")
-        return t.data_ptr()
+    def _vec(self, t, name: str):
+        if (isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.shape == self._vec_shape and t.is_contiguous()
+                and t.get_device() == self._index):
+            return t.data_ptr()
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape [{self.batch}] on {self.device}")
 
     def _view(self, t, name: str, heads: int, types) -> Rows:
         """A [batch, M, heads, head_dim] tensor, strided but for its last dimension."""
-        if not (isinstance(t, torch.Tensor) and t.dim() == 4 and t.dtype in types and t.device == self.device):
-            raise ValueError(f"{name} must be a tensor of shape [{self.batch}, M, {heads}, {self.head_dim}], one of {types}, "
-                             f"on {self.device}")
-        b, _, h, d = t.shape
-        s = t.stride()
-        if b != self.batch or h != heads or d != self.head_dim or s[3] != 1:
-            raise ValueError(f"{name} must have shape [{self.batch}, M, {heads}, {self.head_dim}] with a contiguous last "
-                             f"dimension; got {tuple(t.shape)}, strides {s}")
-        return Rows(t.data_ptr(), _ROW_TYPES[t.dtype], s[0], s[1], s[2])
+        if isinstance(t, torch.Tensor) and t.dim() == 4 and t.dtype in types and t.get_device() == self._index:
+            b, _, h, d = t.shape
+            s0, s1, s2, s3 = t.stride()
+            if b == self.batch and h == heads and d == self.head_dim and s3 == 1:
+                return Rows(t.data_ptr(), _ROW_TYPES[t.dtype], s0, s1, s2)
+        got = f"{tuple(t.shape)} {t.dtype} on {t.device}, strides {t.stride()}" if isinstance(t, torch.Tensor) else type(t).__name__
+        raise ValueError(f"{name} must be [{self.batch}, M, {heads}, {self.head_dim}] with a contiguous last dimension, one of "
+                         f"{', '.join(map(str, types))}, on {self.device}; got {got}")
 
-    def _like(self, t, name: str, dtype, shape):
-        _need(t, name, dtype, shape)
-        if t.device != self.device:
-            raise ValueError(f"{name} must be on {self.device}")
-        return t.data_ptr()
+    def _like(self, t, name: str, dtype, shape) -> int:
+        if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous()
+                and t.get_device() == self._index):
+            return t.data_ptr()
+        got = (f"{tuple(t.shape)} {t.dtype} on {t.device}, contiguous={t.is_contiguous()}" if isinstance(t, torch.Tensor)
+               else type(t).__name__)
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)} on {self.device}; got {got}")
 
-    def _run(self, fn: str, stream, *args):
-        """The call on `stream` (default: the device's current one) with the cache's device current."""
+    def _on(self, stream) -> int:
+        """The stream's handle (default: the current one of the cache's device)."""
         if stream is None:
-            stream = torch.cuda.current_stream(self.device)
-        elif stream.device != self.device:
+            return torch._C._cuda_getCurrentRawStream(self._index)
+        if stream.device != self.device:
             raise ValueError(f"the stream must be on {self.device}")
-        if torch.cuda.current_device() == self.device.index:
-            check(fn, getattr(lib(), fn)(*args, stream.cuda_stream))
+        return stream.cuda_stream
+
+    def _run(self, name: str, f, *args) -> None:
+        """A call of the library with the cache's device current."""
+        if torch._C._cuda_getDevice() == self._index:
+            rc = f(*args)
         else:
-            with torch.cuda.device(self.device):
-                check(fn, getattr(lib(), fn)(*args, stream.cuda_stream))
+            with torch.cuda.device(self._index):
+                rc = f(*args)
+        if rc:
+            check(name, rc)
 
     def append(self, k_new: torch.Tensor, v_new: torch.Tensor, pos: torch.Tensor, counts=None, err=None, stream=None):
         """Quantise rows [batch, M, kv_heads, head_dim] (bf16, fp16 or fp32; strided
         views with a contiguous last dimension) into positions pos[b] ..
         pos[b] + M - 1, or + counts[b] - 1 (moe_kv8_append)."""
-        k = self._view(k_new, "k_new", self.kv_heads, tuple(_ROW_TYPES))
-        v = self._view(v_new, "v_new", self.kv_heads, tuple(_ROW_TYPES))
-        if k_new.dtype != v_new.dtype or k_new.shape != v_new.shape:
+        k = self._view(k_new, "k_new", self.kv_heads, _ROW_TYPES)
+        v = self._view(v_new, "v_new", self.kv_heads, _ROW_TYPES)
+        M = k_new.size(1)
+        if k.type != v.type or M != v_new.size(1):
             raise ValueError("k_new and v_new must have one shape and type")
-        e = self.err.data_ptr() if err is None else self._like(err, "err", torch.int32, (1,))
-        self._run("moe_kv8_append", stream, self._ref, C.byref(k), C.byref(v), k_new.shape[1], self._vec(pos, "pos", False),
-                  self._vec(counts, "counts"), e)
+        self._run("moe_kv8_append", self._f_append, self._ref, k, v, M, self._vec(pos, "pos"),
+                  None if counts is None else self._vec(counts, "counts"),
+                  self._err if err is None else self._like(err, "err", torch.int32, (1,)), self._on(stream))
 
     def read(self, start, n: int, lens=None, stream=None):
         """(k, v) bf16 [batch, n, kv_heads, head_dim]: the values of positions
         start[b] .. start[b] + n - 1 (start None: 0); zero outside the cache and
         from lens[b] on (moe_kv8_read)."""
-        out = torch.empty((2, self.batch, n, self.kv_heads, self.head_dim), dtype=torch.bfloat16, device=self.device)
-        k, v = out.unbind(0)
-        self._run("moe_kv8_read", stream, self._ref, self._vec(start, "start"), n, self._vec(lens, "lens"), k.data_ptr(),
-                  v.data_ptr())
+        shape = (self.batch, n, self.kv_heads, self.head_dim)
+        k = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
+        v = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
+        self._run("moe_kv8_read", self._f_read, self._ref, None if start is None else self._vec(start, "start"), n,
+                  None if lens is None else self._vec(lens, "lens"), k.data_ptr(), v.data_ptr(), self._on(stream))
         return k, v
 
     def attend(self, q: torch.Tensor, pos: torch.Tensor, counts=None, scale=None, acc=None, acc_in=None, decay: float = 1.0,
@@ -599,36 +615,33 @@ class KV8Cache:
         1 / sqrt(head_dim) by default.  acc (fp32 [batch, kv_heads, T_cap], the
         cache built with weights=True) receives decay * acc_in + the weight each
         position got; acc_in defaults to acc."""
-        r = self._view(q, "q", self.q_heads, (torch.bfloat16, torch.float16))
-        M = q.shape[1]
-        if out is None:
-            out = torch.empty((self.batch, M, self.q_heads, self.head_dim), dtype=out_dtype, device=self.device)
-        elif out.dtype not in _ROW_TYPES:
-            raise ValueError("out must be fp32, bf16 or fp16")
-        else:
-            self._like(out, "out", out.dtype, (self.batch, M, self.q_heads, self.head_dim))
-        if out.dtype not in _ROW_TYPES:
-            raise ValueError("out_dtype must be fp32, bf16 or fp16")
+        r = self._view(q, "q", self.q_heads, _Q_TYPES)
+        M = q.size(1)
         if M > self.max_rows:
             raise ValueError(f"q has {M} rows; the cache was built for max_rows={self.max_rows}")
+        if out is None:
+            if out_dtype not in _ROW_TYPES:
+                raise ValueError("out_dtype must be fp32, bf16 or fp16")
+            out = torch.empty((self.batch, M, self.q_heads, self.head_dim), dtype=out_dtype, device=self.device)
+            o = out.data_ptr()
+        else:
+            out_dtype = getattr(out, "dtype", None)
+            if out_dtype not in _ROW_TYPES:
+                raise ValueError("out must be an fp32, bf16 or fp16 tensor")
+            o = self._like(out, "out", out_dtype, (self.batch, M, self.q_heads, self.head_dim))
         a = a_in = None
         if acc is not None:
             if not self.weights:
                 raise ValueError("acc needs a cache built with weights=True")
-            shape = (self.batch, self.kv_heads, self.T_cap)
-            a = self._like(acc, "acc", torch.float32, shape)
-            a_in = a if acc_in is None else self._like(acc_in, "acc_in", torch.float32, shape)
+            a = self._like(acc, "acc", torch.float32, self._acc_shape)
+            a_in = a if acc_in is None else self._like(acc_in, "acc_in", torch.float32, self._acc_shape)
         elif acc_in is not None:
             raise ValueError("acc_in needs acc")
-        if err is None:
-            err = self.err
-            e = err.data_ptr()
-        else:
-            e = self._like(err, "err", torch.int32, (1,))
-        self._run("moe_kv8_attn", stream, self._ref, C.byref(r), M, self._vec(pos, "pos", False), self._vec(counts, "counts"),
-                  self.head_dim ** -0.5 if scale is None else scale, out.data_ptr(), _ROW_TYPES[out.dtype], a_in, a, decay,
-                  self.ws.data_ptr(), self.ws.numel(), e)
-        return out, err
+        e = self._err if err is None else self._like(err, "err", torch.int32, (1,))
+        self._run("moe_kv8_attn", self._f_attn, self._ref, r, M, self._vec(pos, "pos"),
+                  None if counts is None else self._vec(counts, "counts"), self.head_dim ** -0.5 if scale is None else scale, o,
+                  _ROW_TYPES[out_dtype], a_in, a, decay, self._ws, self._ws_bytes, e, self._on(stream))
+        return out, self.err if err is None else err
 
     def evict_into(self, dst: "KV8Cache", lens: torch.Tensor, acc: torch.Tensor, budget: int, sinks: int = 4,
                    recent: int = 0, dst_acc=None, err=None, stream=None):
@@ -636,18 +649,17 @@ class KV8Cache:
         first `sinks`, the last `recent`, then the largest acc) in order at the start of
         dst (moe_kv8_evict); returns (idx int32 [batch, kv_heads, budget], lens of
         dst int32 [batch])."""
-        if not isinstance(dst, KV8Cache) or dst.device != self.device:
+        if not isinstance(dst, KV8Cache) or dst._index != self._index:
             raise ValueError(f"dst must be a KV8Cache on {self.device}")
         if budget < 1:
             raise ValueError("budget must be at least 1")
-        a = self._like(acc, "acc", torch.float32, (self.batch, self.kv_heads, self.T_cap))
-        da = None if dst_acc is None else self._like(dst_acc, "dst_acc", torch.float32,
-                                                     (self.batch, self.kv_heads, dst.T_cap))
-        e = self.err.data_ptr() if err is None else self._like(err, "err", torch.int32, (1,))
+        a = self._like(acc, "acc", torch.float32, self._acc_shape)
+        da = None if dst_acc is None else self._like(dst_acc, "dst_acc", torch.float32, (self.batch, self.kv_heads, dst.T_cap))
+        e = self._err if err is None else self._like(err, "err", torch.int32, (1,))
         idx = torch.empty((self.batch, self.kv_heads, budget), dtype=torch.int32, device=self.device)
         n = torch.empty(self.batch, dtype=torch.int32, device=self.device)
-        self._run("moe_kv8_evict", stream, self._ref, dst._ref, self._vec(lens, "lens", False), a, budget, sinks, recent, da,
-                  idx.data_ptr(), n.data_ptr(), e)
+        self._run("moe_kv8_evict", self._f_evict, self._ref, dst._ref, self._vec(lens, "lens"), a, budget, sinks, recent, da,
+                  idx.data_ptr(), n.data_ptr(), e, self._on(stream))
         return idx, n
 
 
