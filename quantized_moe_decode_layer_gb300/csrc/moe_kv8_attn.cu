@@ -37,11 +37,12 @@ struct AttnP {
 };
 
 // ------------------------------------------------------------------ chunks
-// Persistent CTAs of 8 warps take (sequence, chunk, key/value head, column
-// pass) items in turn.  Within a chunk a warp works alone on tiles of 16 R
-// positions (R = 256 / D: 4 KB of keys and 4 KB of values), every eighth
-// one, through a ring of three tiles of its own that cp.async fills ahead,
-// across items, so that loads never stop for the end of a chunk.
+// Persistent CTAs of 4 warps, three on an SM, take (sequence, chunk,
+// key/value head, column pass) items in turn.  Within a chunk a warp works
+// alone on tiles of 16 R positions (R = 256 / D: 4 KB of keys and 4 KB of
+// values), every fourth one, through a ring of two tiles of its own that
+// cp.async fills ahead, across items, so that loads never stop for the end of
+// a chunk; what a CTA waits for there, the other two work through.
 //
 // Per 16 positions and 8 query columns, on m16n8k16 fp16 MMAs:
 //     S^T [16 positions x 8] = K Q^T,   O^T [D x 8] += V^T P^T.
@@ -52,26 +53,39 @@ struct AttnP {
 // byte permutes of two rows' words.  P^T's transpose is movmatrix.  The
 // weights go in as two fp16 halves (22 bits): sums of many small weights
 // keep fp32's precision, and an fp32 output means something.
-constexpr int kWarps = 8, kThreads = 32 * kWarps, kStages = 3;
+//
+// The warps of a chunk and their order are the same for every number of
+// columns, which keeps a row's bits independent of the call's other rows.
+// 12 warps on an SM leave 168 registers a thread: the output of 8 columns of
+// 256 dimensions (64) with its queries (32), or 16 of 128 or 64.
+#ifndef KV8_WARPS
+#define KV8_WARPS 4
+#define KV8_CTAS 3
+#endif
+constexpr int kWarps = KV8_WARPS, kCtas = KV8_CTAS, kThreads = 32 * kWarps, kStages = 2;
 constexpr int kTileBytes = 4096;                       // keys (or values) of a warp's tile
 constexpr int kStageBytes = 2 * kTileBytes + 64;       // and the steps of its up to 4 groups of 16 positions
 constexpr float kWeightUnit = 32768.f;                 // weights are held in units of 2^-15: fp16's small end reaches 2^-39
 
 template <int D, int NT>
 struct Lay {
-    static constexpr int round = NT == 1 ? 4 : 2;      // m-tiles of the output joined at once
+    static constexpr int round = 2;                    // m-tiles of the output joined at once
     static constexpr int ring = 0, red = kWarps * kStages * kStageBytes, q = red + kWarps * round * 512, qrow = 2 * D + 16,
-                         qf = q + 2 * 8 * NT * qrow, ml = qf + 2 * 8 * NT * 4, first = ml + 2 * kWarps * 8 * NT * 4,
-                         total = first;                // + (batch + 1) ints
+                         qf = q + 8 * NT * qrow, ml = qf + 8 * NT * 4, first = ml + 2 * kWarps * 8 * NT * 4;
+    static constexpr int total(int B) { return first + (3 * B + 1) * 4; }   // first[B + 1], then position and rows of each sequence
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool in)
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src)
 {
-    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void cp4(uint32_t dst, const void *src, bool in)
+__device__ __forceinline__ void cp16z(uint32_t dst, const void *src, bool in)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp4z(uint32_t dst, const void *src, bool in)
 {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0) : "memory");
 }
@@ -88,7 +102,7 @@ __device__ __forceinline__ float ex2(float x)
 
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
 {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -135,7 +149,6 @@ struct Item {
     int b, g, cp, k0, k1, p0, rows;    // positions k0 .. k1 - 1
 };
 
-template <int D, int NT>
 __device__ __forceinline__ Item decode_item(const AttnP &p, const int *first, int item, int passes)
 {
     Item it;
@@ -150,68 +163,63 @@ __device__ __forceinline__ Item decode_item(const AttnP &p, const int *first, in
         else hi = mid;
     }
     it.b = lo;
-    bool bad;
-    it.rows = kv8_rows(p.pos, p.counts, lo, p.M, p.T_cap, it.p0, bad);
+    it.p0 = first[p.B + 1 + lo];
+    it.rows = first[2 * p.B + 1 + lo];
     it.k0 = (item - first[lo]) * p.chunk;
     it.k1 = min(it.k0 + p.chunk, it.p0 + it.rows);
     return it;
 }
 
-// Query columns of an item, one group of D / 8 lanes each: raw values ahead
-// of time, then scaled by a power of two (exactly; 2^12 <= the row's largest
-// < 2^13, elements 2^26 times smaller lose bits) into shared memory.
-template <int D, int NT>
-struct QLoad {
-    static constexpr int kLanes = D / 8, kPer = 8 * NT * kLanes / kThreads > 0 ? 8 * NT * kLanes / kThreads : 1;
+// Query columns of an item into shared memory, D / 8 lanes each: scaled by a
+// power of two (exactly; the row's largest to 2^12 .. 2^13, so that only
+// elements 2^26 times smaller lose bits), in the order of pairs().
+template <int FMT, int D, int NT>
+__device__ __forceinline__ void load_q(const AttnP &p, const Item &it, uint8_t *q, float *qf)
+{
+    constexpr int kLanes = D / 8, kPer = (8 * NT * kLanes + kThreads - 1) / kThreads;
     uint16_t h[kPer][8];
-
-    __device__ __forceinline__ void fetch(const AttnP &p, const Item &it)
-    {
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int id = threadIdx.x + i * kThreads, col = id / kLanes, c = it.cp * 8 * NT + col, m = c / p.G;
-            const bool in = col < 8 * NT && c < p.C && m < it.rows;
-            const uint16_t *src = static_cast<const uint16_t *>(p.q) + it.b * p.qb + m * p.qm + (it.g * p.G + c % p.G) * p.qh +
-                                  id % kLanes * 8;
-            if (p.qvec && in) *reinterpret_cast<uint4 *>(h[i]) = __ldg(reinterpret_cast<const uint4 *>(src));
-            else
+    for (int i = 0; i < kPer; ++i) {
+        const int id = threadIdx.x + i * kThreads, col = id / kLanes, c = it.cp * 8 * NT + col, m = c / p.G;
+        const bool in = col < 8 * NT && c < p.C && m < it.rows;
+        const uint16_t *src = static_cast<const uint16_t *>(p.q) + it.b * p.qb + m * p.qm + (it.g * p.G + c % p.G) * p.qh +
+                              id % kLanes * 8;
+        if (p.qvec && in) *reinterpret_cast<uint4 *>(h[i]) = __ldg(reinterpret_cast<const uint4 *>(src));
+        else
 #pragma unroll
-                for (int j = 0; j < 8; ++j) h[i][j] = in ? __ldg(src + j) : (uint16_t)0;
+            for (int j = 0; j < 8; ++j) h[i][j] = in ? __ldg(src + j) : (uint16_t)0;
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int id = threadIdx.x + i * kThreads, col = id / kLanes;
+        float v[8], a = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            v[j] = p.f16 ? __half2float(__ushort_as_half(h[i][j])) : __uint_as_float((uint32_t)h[i][j] << 16);
+            a = fmaxf(a, fabsf(v[j]));
+        }
+#pragma unroll
+        for (int o = kLanes / 2; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
+        const int e = (int)(__float_as_uint(a) >> 23) - 127;
+        const bool odd = a == 0.f || e == 128;                   // zero or infinite: as it is
+        const int up = odd ? 0 : max(-126, min(126, 12 - e));
+        const float f = pow2f(up);
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int x = FMT == MOE_KV8_INT8 ? 4 * (j >> 1) + (j & 1) : 2 * j, y = FMT == MOE_KV8_INT8 ? x + 2 : x + 1;
+            const __half2 t = __floats2half2_rn(v[x] * f, v[y] * f);
+            w[j] = *reinterpret_cast<const uint32_t *>(&t);
+        }
+        if (col < 8 * NT) {
+            *reinterpret_cast<uint4 *>(q + col * Lay<D, NT>::qrow + id % kLanes * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+            if (id % kLanes == 0) qf[col] = p.scale_log2 * pow2f(-up);
         }
     }
-    __device__ __forceinline__ void store(const AttnP &p, uint8_t *q, float *qf)
-    {
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int id = threadIdx.x + i * kThreads, col = id / kLanes;
-            float v[8], a = 0.f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                v[j] = p.f16 ? __half2float(__ushort_as_half(h[i][j])) : __uint_as_float((uint32_t)h[i][j] << 16);
-                a = fmaxf(a, fabsf(v[j]));
-            }
-#pragma unroll
-            for (int o = kLanes / 2; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
-            const int e = (int)(__float_as_uint(a) >> 23) - 127;
-            const bool odd = a == 0.f || e == 128;               // zero or infinite: as it is
-            const int up = odd ? 0 : max(-126, min(126, 12 - e));
-            const float f = pow2f(up);
-            uint32_t w[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const __half2 t = __floats2half2_rn(v[2 * j] * f, v[2 * j + 1] * f);
-                w[j] = *reinterpret_cast<const uint32_t *>(&t);
-            }
-            if (col < 8 * NT) {
-                *reinterpret_cast<uint4 *>(q + col * Lay<D, NT>::qrow + id % kLanes * 16) = make_uint4(w[0], w[1], w[2], w[3]);
-                if (id % kLanes == 0) qf[col] = p.scale_log2 * pow2f(-up);
-            }
-        }
-    }
-};
+}
 
 template <int FMT, int D, int NT>
-__global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const AttnP p)
+__global__ void __launch_bounds__(kThreads, kCtas) kv8_chunk_kernel(const AttnP p)
 {
     using L = Lay<D, NT>;
     constexpr int R = 256 / D, TK = 16 * R, KS = D / 16, NC = 8 * NT;   // KS: k-steps of S, m-tiles of O
@@ -228,6 +236,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const AttnP p)
         const int rows = kv8_rows(p.pos, p.counts, b, p.M, p.T_cap, p0, bad);
         if (bad && blockIdx.x == 0) atomicOr(p.err, kKv8ErrRange);
         first[b + 1] = rows > 0 ? (p0 + rows + p.chunk - 1) / p.chunk : 0;
+        first[p.B + 1 + b] = p0;
+        first[2 * p.B + 1 + b] = rows;
     }
     __syncthreads();
     if (warp == 0) {
@@ -252,60 +262,76 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const AttnP p)
     const uint32_t ring_u = smem_u32(ring);
 
     // The load cursor runs kStages tiles ahead of the compute cursor; an
-    // empty commit keeps the group count when it has run out.
-    int ld_item = blockIdx.x, ld_j = warp, ld_stage = 0;
-    Item ld = decode_item<D, NT>(p, first, ld_item, passes);
+    // empty commit keeps the group count when it has run out.  A lane's i-th
+    // 16 bytes of a tile are row lr + i 512 / D, chunk lc; chunks are swapped
+    // within a row so that the reads below hit every bank once.
+    const int lr = lane / (D / 16), lc = lane % (D / 16);
+    const uint32_t k_lane = lr * D + (D == 64 ? lc : lc ^ ((lr & 1) << 2)) * 16;
+    constexpr int VX = D == 256 ? 4 : D == 128 ? 2 : 1;   // the values' swap depends on i mod VX
+    uint32_t v_lane[VX];
+#pragma unroll
+    for (int i = 0; i < VX; ++i) v_lane[i] = lr * D + (lc ^ ((lr + i * (512 / D)) & (D == 64 ? 2 : 6))) * 16;
+    int ld_item = blockIdx.x, ld_t = 0, ld_k1 = 0, ld_stage = 0;
+    const uint8_t *ld_k = nullptr, *ld_v = nullptr;
+    const float *ld_s = nullptr;
+    auto open_item = [&]() {
+        const Item x = decode_item(p, first, ld_item, passes);
+        const size_t head = (size_t)x.b * p.Hkv + x.g;
+        ld_t = x.k0 + warp * TK;
+        ld_k1 = x.k1;
+        ld_k = p.k + (head * p.T_cap + ld_t) * D + lane * 16;
+        ld_v = p.v + (head * p.T_cap + ld_t) * D + lane * 16;
+        ld_s = (lane & 1 ? p.vs : p.ks) + head * p.nblk;
+    };
+    open_item();
     auto load_tile = [&]() {
-        while (ld_item < total && ld.k0 + ld_j * TK >= ld.k1) {
+        while (ld_t >= ld_k1 && ld_item < total) {
             ld_item += gridDim.x;
-            ld_j = warp;
-            if (ld_item < total) ld = decode_item<D, NT>(p, first, ld_item, passes);
+            if (ld_item < total) open_item();
         }
         if (ld_item < total) {
-            const int t0 = ld.k0 + ld_j * TK;
-            const size_t head = (size_t)ld.b * p.Hkv + ld.g;
-            const uint8_t *K = p.k + (head * p.T_cap + t0) * D, *V = p.v + (head * p.T_cap + t0) * D;
             const uint32_t dst = ring_u + ld_stage * kStageBytes;
+            if (ld_t + TK <= ld_k1) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int id = lane + 32 * i, row = id / (D / 16), c = id % (D / 16);
-                const bool in = t0 + row < ld.k1;
-                const int ck = D == 64 ? c : c ^ ((row & 1) << 2), cv = D == 64 ? c ^ (row & 2) : c ^ (row & 6);
-                cp16(dst + row * D + ck * 16, in ? K + id * 16 : p.k, in);
-                cp16(dst + kTileBytes + row * D + cv * 16, in ? V + id * 16 : p.v, in);
+                for (int i = 0; i < 8; ++i) {
+                    cp16(dst + k_lane + i * 512, ld_k + i * 512);
+                    cp16(dst + kTileBytes + v_lane[i % VX] + i * 512, ld_v + i * 512);
+                }
+            } else {
+                // rows past the end are zeros, not what lies there
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const bool in = ld_t + lr + i * (512 / D) < ld_k1;
+                    cp16z(dst + k_lane + i * 512, in ? ld_k + i * 512 : p.k, in);
+                    cp16z(dst + kTileBytes + v_lane[i % VX] + i * 512, in ? ld_v + i * 512 : p.v, in);
+                }
             }
             if (lane < 2 * R) {
-                const int t = t0 + 16 * (lane >> 1);
-                const bool in = t < ld.k1;
-                const float *s = (lane & 1 ? p.vs : p.ks) + head * p.nblk;
-                cp4(dst + 2 * kTileBytes + lane * 4, in ? s + (t >> p.blk_log) : s, in);
+                const int t = ld_t + 16 * (lane >> 1);
+                const bool in = t < ld_k1;
+                cp4z(dst + 2 * kTileBytes + lane * 4, in ? ld_s + (t >> p.blk_log) : ld_s, in);
             }
-            ld_j += kWarps;
+            ld_t += kWarps * TK;
+            ld_k += kWarps * kTileBytes;
+            ld_v += kWarps * kTileBytes;
         }
         cp_commit();
-        ld_stage = ld_stage + 1 == kStages ? 0 : ld_stage + 1;
+        ld_stage ^= 1;
     };
+    static_assert(kStages == 2, "stages alternate");
 #pragma unroll
     for (int i = 0; i < kStages; ++i) load_tile();
 
-    QLoad<D, NT> ql;
-    Item it = decode_item<D, NT>(p, first, blockIdx.x, passes);
-    ql.fetch(p, it);
-    ql.store(p, sm + L::q, reinterpret_cast<float *>(sm + L::qf));
-    __syncthreads();
-
-    int stage = 0, par = 0;
+    int stage = 0;
 #pragma unroll 1
-    for (int item = blockIdx.x; item < total; item += gridDim.x, par ^= 1) {
-        Item next;
-        const bool more = item + (int)gridDim.x < total;
-        if (more) {
-            next = decode_item<D, NT>(p, first, item + gridDim.x, passes);
-            ql.fetch(p, next);
-        }
-        const uint8_t *qs = sm + L::q + par * NC * L::qrow;
-        const float *qf = reinterpret_cast<const float *>(sm + L::qf) + par * NC;
+    for (int item = blockIdx.x; item < total; item += gridDim.x) {
+        const Item it = decode_item(p, first, item, passes);
+        const uint8_t *qs = sm + L::q;
+        float *qf = reinterpret_cast<float *>(sm + L::qf);
+        load_q<FMT, D, NT>(p, it, sm + L::q, qf);   // every warp has passed the last item's barriers, and with them its reads
+        __syncthreads();
         float f[NT][2], m[NT][2], l[NT][2], o[NT][KS][4], vref = 0.f, inv_vref = 0.f;
+        bool fresh = true;             // no tile yet: m = -inf, everything else 0
         uint32_t qr[NT == 1 ? KS : 1][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -320,17 +346,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const AttnP p)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) o[n][k][c] = 0.f;
         }
-        // Element order of k-step 4 i + j: the lane's bytes 4 j .. 4 j + 3 of
-        // 16 at 64 i + 16 t, pairs as pairs() gives them.
+        // k-step 4 i + j: the dimensions of the lane's bytes 4 j .. 4 j + 3 of 16 at 64 i + 16 t
         auto q_frag = [&](int n, int i, uint32_t (&b)[8]) {
             const uint4 *src = reinterpret_cast<const uint4 *>(qs + (8 * n + gq) * L::qrow + (64 * i + 16 * tq) * 2);
             const uint4 x = src[0], y = src[1];
             const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                b[2 * j] = FMT == MOE_KV8_INT8 ? __byte_perm(w[2 * j], w[2 * j + 1], 0x5410) : w[2 * j];
-                b[2 * j + 1] = FMT == MOE_KV8_INT8 ? __byte_perm(w[2 * j], w[2 * j + 1], 0x7632) : w[2 * j + 1];
-            }
+            for (int j = 0; j < 8; ++j) b[j] = w[j];
         };
         if (NT == 1) {
 #pragma unroll
@@ -434,7 +456,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const AttnP p)
             float vmax = steps[1];
 #pragma unroll
             for (int r = 1; r < R; ++r) vmax = fmaxf(vmax, steps[2 * r + 1]);
-            if (__any_sync(0xFFFFFFFFu, grew) || vmax > vref) {
+            if (fresh) {
+                fresh = false;
+                vref = vmax;
+                inv_vref = vmax > 0.f ? 1.f / vmax : 0.f;
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) m[n][c] = mn[n][c];
+            } else if (__any_sync(0xFFFFFFFFu, grew) || vmax > vref) {
                 float down = 1.f;
                 if (vmax > vref) {
                     inv_vref = 1.f / vmax;
@@ -519,11 +549,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const AttnP p)
             }
             __syncwarp();                                          // the tile is read before its slot is filled again
             load_tile();
-            stage = stage + 1 == kStages ? 0 : stage + 1;
+            stage ^= 1;
         }
 
         // ---- the chunk's result from the warps'
-        if (more) ql.store(p, sm + L::q + (par ^ 1) * NC * L::qrow, reinterpret_cast<float *>(sm + L::qf) + (par ^ 1) * NC);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -595,7 +624,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const AttnP p)
                     if (c + 1 < cols) *reinterpret_cast<float2 *>(p.part_o + (col0 + c + 1) * D + d) = make_float2(a.y, a.w);
                 }
             }
-        if (more) it = next;
     }
     cp_wait<0>();
 }
@@ -699,8 +727,20 @@ __global__ void __launch_bounds__(kAccThreads) kv8_weights_kernel(const AttnP p)
     p.acc[head * p.T_cap + t] = a;
 }
 
-// Positions per chunk: a multiple of what the 8 warps take at once (64 KB of keys and values).
-int kv8_chunk(const moe_kv8 &c) { return (c.T_cap <= 8192 ? 1 : 4) * 32768 / c.head_dim; }
+// Positions per chunk: 2 to 32 rounds of a CTA's warps (a round: 32 KB of keys
+// and values), as many as leave every CTA slot of 152 SMs a few chunks of a
+// full cache.
+#ifndef KV8_ITEMS
+#define KV8_ITEMS 4
+#endif
+int kv8_chunk(const moe_kv8 &c)
+{
+    const int round = kWarps * 4096 / c.head_dim;
+    const long long rounds = (long long)c.batch * c.kv_heads * c.T_cap / round;
+    int r = 32;
+    while (r > 2 && rounds < 152LL * kCtas * KV8_ITEMS * r) r /= 2;
+    return r * round;
+}
 
 // Once per kernel and device.
 struct Once {
@@ -771,37 +811,41 @@ int launch_kv8_attn(const moe_kv8 &c, const moe_rows &q, int M, const int32_t *p
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess || dev < 0 || dev >= 64) { note_cuda_error((int)e); return MOE_ERR_CUDA; }
-    const int nt = p.C <= 8 ? 1 : 2;
+    // Column tiles a warp holds: what its registers take, and no more than there are columns.
+    const int nt = p.C <= 8 || c.head_dim == 256 ? 1 : 2;
     const long long items = (long long)p.nchunk * p.B * p.Hkv * ((p.C + 8 * nt - 1) / (8 * nt));
     if (items > INT_MAX) return MOE_ERR_UNSUPPORTED;
     auto go = [&](auto kernel, int smem, Once &once) {
         std::call_once(once.flag[dev], [&] {
             e = cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+            if (e == cudaSuccess)
+                e = cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                         (int)cudaSharedmemCarveoutMaxShared);
             if (e == cudaSuccess) e = cudaDeviceGetAttribute(&once.sms[dev], cudaDevAttrMultiProcessorCount, dev);
         });
         if (e != cudaSuccess || once.sms[dev] < 1) return;
-        kernel<<<(int)std::min<long long>(items, once.sms[dev]), kThreads, smem + (p.B + 1) * (int)sizeof(int), stream>>>(p);
+        kernel<<<(int)std::min<long long>(items, (long long)once.sms[dev] * kCtas), kThreads, smem, stream>>>(p);
     };
 #define KV8_GO(F, D, N)                                                                     \
     do {                                                                                    \
         static Once once;                                                                   \
-        static_assert(Lay<D, N>::total + (MOE_KV8_MAX_BATCH + 1) * 4 <= kSmemMax, "shared memory"); \
-        go(kv8_chunk_kernel<F, D, N>, Lay<D, N>::total, once);                              \
+        static_assert(Lay<D, N>::total(MOE_KV8_MAX_BATCH) <= kSmemMax, "shared memory");    \
+        go(kv8_chunk_kernel<F, D, N>, Lay<D, N>::total(p.B), once);                         \
     } while (0)
-#define KV8_GO_D(F, N)                                \
-    do {                                              \
-        if (c.head_dim == 64) KV8_GO(F, 64, N);       \
-        else if (c.head_dim == 128) KV8_GO(F, 128, N); \
-        else KV8_GO(F, 256, N);                       \
+#define KV8_GO_F(F)                              \
+    do {                                         \
+        if (c.head_dim == 256) KV8_GO(F, 256, 1); \
+        else if (c.head_dim == 128) {            \
+            if (nt == 1) KV8_GO(F, 128, 1);      \
+            else KV8_GO(F, 128, 2);              \
+        } else {                                 \
+            if (nt == 1) KV8_GO(F, 64, 1);       \
+            else KV8_GO(F, 64, 2);               \
+        }                                        \
     } while (0)
-    if (c.format == MOE_KV8_INT8) {
-        if (nt == 1) KV8_GO_D(MOE_KV8_INT8, 1);
-        else KV8_GO_D(MOE_KV8_INT8, 2);
-    } else {
-        if (nt == 1) KV8_GO_D(MOE_KV8_E4M3, 1);
-        else KV8_GO_D(MOE_KV8_E4M3, 2);
-    }
-#undef KV8_GO_D
+    if (c.format == MOE_KV8_INT8) KV8_GO_F(MOE_KV8_INT8);
+    else KV8_GO_F(MOE_KV8_E4M3);
+#undef KV8_GO_F
 #undef KV8_GO
     if (e != cudaSuccess) { note_cuda_error((int)e); return MOE_ERR_CUDA; }
     note_launch();
