@@ -65,7 +65,13 @@ struct AttnP {
 constexpr int kWarps = KV8_WARPS, kCtas = KV8_CTAS, kThreads = 32 * kWarps, kStages = 2;
 constexpr int kTileBytes = 4096;                       // keys (or values) of a warp's tile
 constexpr int kStageBytes = 2 * kTileBytes + 64;       // and the steps of its up to 4 groups of 16 positions
-constexpr float kWeightUnit = 32768.f;                 // weights are held in units of 2^-15: fp16's small end reaches 2^-39
+// A column's exponents are taken from a reference that follows its maximum
+// only when that has grown by more than 2^8 (rescaling the output takes a tenth
+// of a tile's instructions, and with 8 columns every other tile had a new
+// maximum).  Weights are then at most 2^8, held in units of 2^-7; their low
+// halves reach down to 2^-31, and what a warp's share of a chunk (2048
+// positions at most) loses below is under 2^-20 of its largest weight.
+constexpr float kSlack = 8.f, kWeightUnit = 128.f;
 
 template <int D, int NT>
 struct Lay {
@@ -122,7 +128,9 @@ __device__ __forceinline__ void pairs(uint32_t w, uint32_t &x, uint32_t &y)
 {
     if (FMT == MOE_KV8_INT8) {
         const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
-        const uint32_t a = (w & 0x00FF00FFu) ^ 0x64806480u, b = ((w >> 8) & 0x00FF00FFu) ^ 0x64806480u;
+        uint32_t a, b;                                // (w & mask) ^ flip
+        asm("lop3.b32 %0, %1, 0x00FF00FF, %2, 0x6A;" : "=r"(a) : "r"(w), "r"(0x64806480u));
+        asm("lop3.b32 %0, %1, 0x00FF00FF, %2, 0x6A;" : "=r"(b) : "r"(w >> 8), "r"(0x64806480u));
         const __half2 ha = __hsub2(*reinterpret_cast<const __half2 *>(&a), off), hb = __hsub2(*reinterpret_cast<const __half2 *>(&b), off);
         x = *reinterpret_cast<const uint32_t *>(&ha);
         y = *reinterpret_cast<const uint32_t *>(&hb);
@@ -322,6 +330,11 @@ __global__ void __launch_bounds__(kThreads, kCtas) kv8_chunk_kernel(const AttnP 
 #pragma unroll
     for (int i = 0; i < kStages; ++i) load_tile();
 
+    // A lane's reads of a tile: chunk 4 i + t of key rows g and g + 8 (the
+    // swap turns i even into i + 1 and back in odd rows), 16 (8) bytes of
+    // value rows 2 t, 2 t + 1, 2 t + 8, 2 t + 9.
+    const int k_even = gq * D + tq * 16 + (D == 64 ? 0 : (gq & 1) * 64), k_odd = gq * D + tq * 16 - (D == 64 ? 0 : (gq & 1) * 64);
+    const int v_at = 2 * tq * D + (D == 64 ? ((gq >> 1) ^ ((tq & 1) * 2)) * 16 + (gq & 1) * 8 : (gq ^ (2 * tq)) * 16);
     int stage = 0;
 #pragma unroll 1
     for (int item = blockIdx.x; item < total; item += gridDim.x) {
@@ -371,8 +384,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) kv8_chunk_kernel(const AttnP 
         for (int t0 = it.k0 + warp * TK; t0 < it.k1; t0 += kWarps * TK) {
             cp_wait<kStages - 1>();
             __syncwarp();
-            const uint8_t *kt = ring + stage * kStageBytes, *vt = kt + kTileBytes;
-            const float *steps = reinterpret_cast<const float *>(vt + kTileBytes);
+            const uint8_t *kt = ring + stage * kStageBytes;
+            const float *steps = reinterpret_cast<const float *>(kt + 2 * kTileBytes);
             // ---- scores
             float s[R][NT][4];
 #pragma unroll
@@ -384,9 +397,9 @@ __global__ void __launch_bounds__(kThreads, kCtas) kv8_chunk_kernel(const AttnP 
                     for (int c = 0; c < 4; ++c) acc[n][0][c] = acc[n][1][c] = 0.f;
 #pragma unroll
                 for (int i = 0; i < D / 64; ++i) {
-                    const int row = 16 * r + gq, ck = D == 64 ? 4 * i + tq : (4 * i + tq) ^ ((gq & 1) << 2);
-                    const uint4 u = *reinterpret_cast<const uint4 *>(kt + row * D + ck * 16);
-                    const uint4 w = *reinterpret_cast<const uint4 *>(kt + (row + 8) * D + ck * 16);
+                    const uint8_t *src = kt + (i & 1 ? k_odd : k_even) + 16 * r * D + 64 * i;
+                    const uint4 u = *reinterpret_cast<const uint4 *>(src);
+                    const uint4 w = *reinterpret_cast<const uint4 *>(src + 8 * D);
                     const uint32_t uw[4] = {u.x, u.y, u.z, u.w}, ww[4] = {w.x, w.y, w.z, w.w};
                     uint32_t b[NT][8];
                     if (NT > 1) {
@@ -437,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) kv8_chunk_kernel(const AttnP 
                         }
                     }
             }
-            // ---- running maxima; the values' largest step so far is the unit of the output
+            // ---- reference exponents; the values' largest step so far is the unit of the output
             float mn[NT][2];
             bool grew = false;
 #pragma unroll
@@ -450,8 +463,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) kv8_chunk_kernel(const AttnP 
                     x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 4));
                     x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
                     x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
-                    mn[n][c] = fmaxf(m[n][c], x);
-                    grew |= mn[n][c] > m[n][c];
+                    mn[n][c] = x > m[n][c] + kSlack ? x : m[n][c];
+                    grew |= mn[n][c] != m[n][c];
                 }
             float vmax = steps[1];
 #pragma unroll
@@ -463,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) kv8_chunk_kernel(const AttnP 
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) m[n][c] = mn[n][c];
+                    for (int c = 0; c < 2; ++c) m[n][c] = mn[n][c];      // from -inf: the maximum itself
             } else if (__any_sync(0xFFFFFFFFu, grew) || vmax > vref) {
                 float down = 1.f;
                 if (vmax > vref) {
@@ -516,17 +529,15 @@ __global__ void __launch_bounds__(kThreads, kCtas) kv8_chunk_kernel(const AttnP 
                     uint32_t v[4][VW];
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
-                        const int row = 16 * r + 2 * tq + (x & 1) + 8 * (x >> 1);
+                        const uint8_t *src = kt + v_at + kTileBytes + (16 * r + (x & 1) + 8 * (x >> 1)) * D + 128 * h;
                         if (D >= 128) {
-                            const int c = (gq + 8 * h) ^ (row & 6);
-                            const uint4 u = *reinterpret_cast<const uint4 *>(vt + row * D + c * 16);
+                            const uint4 u = *reinterpret_cast<const uint4 *>(src);
                             v[x][0] = u.x;
                             v[x][1] = u.y;
                             v[x][VW - 2] = u.z;
                             v[x][VW - 1] = u.w;
                         } else {
-                            const int c = (gq >> 1) ^ (row & 2);
-                            const uint2 u = *reinterpret_cast<const uint2 *>(vt + row * D + c * 16 + (gq & 1) * 8);
+                            const uint2 u = *reinterpret_cast<const uint2 *>(src);
                             v[x][0] = u.x;
                             v[x][1] = u.y;
                         }
