@@ -27,22 +27,24 @@ struct AttnP {
     const uint8_t *k, *v;
     const float *ks, *vs;
     const int32_t *pos, *counts;
-    float *part_o, *part_ml, *sc;   // sc: scores [B][Hkv][T_cap][C], or NULL
+    float *part_o, *part_ml, *fin, *sc;   // chunks' results; joined (reference, 1 / sum); scores [B][Hkv][T_cap][C] or NULL
     void *o;                        // [B][M][Hq][D]
     const float *acc_in;
     float *acc;
     float decay, scale_log2;        // scale * log2(e)
-    int *err;
+    int *err, *counter;                   // counter: items taken beyond the first of each CTA, or NULL (in turn)
     int B, Hq, Hkv, G, M, C, T_cap, chunk, nchunk, blk_log, nblk, f16, qvec, o_type;
 };
 
 // ------------------------------------------------------------------ chunks
 // Persistent CTAs of 4 warps, three on an SM, take (sequence, chunk,
-// key/value head, column pass) items in turn.  Within a chunk a warp works
-// alone on tiles of 16 R positions (R = 256 / D: 4 KB of keys and 4 KB of
-// values), every fourth one, through a ring of two tiles of its own that
-// cp.async fills ahead, across items, so that loads never stop for the end of
-// a chunk; what a CTA waits for there, the other two work through.
+// key/value head, column pass) items; long runs take them from a counter, as
+// SMs that share a GPC's port with fewer others run a tenth faster.  Within a
+// chunk a warp works alone on tiles of 16 R positions (R = 256 / D: 4 KB of
+// keys and 4 KB of values), every fourth one, through a ring of two tiles of
+// its own that cp.async fills ahead, across items.  At the end of a chunk the
+// warps join their outputs through the ring slots that their last tiles
+// left, while the other slots and the other CTAs keep the loads going.
 //
 // Per 16 positions and 8 query columns, on m16n8k16 fp16 MMAs:
 //     S^T [16 positions x 8] = K Q^T,   O^T [D x 8] += V^T P^T.
@@ -54,15 +56,13 @@ struct AttnP {
 // weights go in as two fp16 halves (22 bits): sums of many small weights
 // keep fp32's precision, and an fp32 output means something.
 //
-// The warps of a chunk and their order are the same for every number of
-// columns, which keeps a row's bits independent of the call's other rows.
 // 12 warps on an SM leave 168 registers a thread: the output of 8 columns of
-// 256 dimensions (64) with its queries (32), or 16 of 128 or 64.
-#ifndef KV8_WARPS
-#define KV8_WARPS 4
-#define KV8_CTAS 3
-#endif
-constexpr int kWarps = KV8_WARPS, kCtas = KV8_CTAS, kThreads = 32 * kWarps, kStages = 2;
+// 256 dimensions (64) with its queries (32), or 16 of 128, or 16 of 64.  More
+// columns run twice as many at a time, two CTAs on an SM with 255 registers,
+// their queries in shared memory: expanding the codes is most of the work,
+// and it is done once per column pass.  A column's arithmetic is the same
+// either way, to the bit.
+constexpr int kWarps = 4, kThreads = 32 * kWarps, kStages = 2;
 constexpr int kTileBytes = 4096;                       // keys (or values) of a warp's tile
 constexpr int kStageBytes = 2 * kTileBytes + 64;       // and the steps of its up to 4 groups of 16 positions
 // A column's exponents are taken from a reference that follows its maximum
@@ -73,11 +73,18 @@ constexpr int kStageBytes = 2 * kTileBytes + 64;       // and the steps of its u
 // positions at most) loses below is under 2^-20 of its largest weight.
 constexpr float kSlack = 8.f, kWeightUnit = 128.f;
 
+// Column tiles of 8 that a warp holds, and with how many CTAs on an SM.
+__host__ __device__ constexpr int kv8_nt(int C, int D)
+{
+    const int most = D == 256 ? 2 : 4;
+    return C <= 8 ? 1 : C <= 16 || most == 2 ? 2 : 4;
+}
 template <int D, int NT>
 struct Lay {
-    static constexpr int round = 2;                    // m-tiles of the output joined at once
-    static constexpr int ring = 0, red = kWarps * kStages * kStageBytes, q = red + kWarps * round * 512, qrow = 2 * D + 16,
-                         qf = q + 8 * NT * qrow, ml = qf + 8 * NT * 4, first = ml + 2 * kWarps * 8 * NT * 4;
+    static constexpr bool wide = NT * D > 256 || NT > 2;
+    static constexpr int ctas = wide ? 2 : 3, NC = 8 * NT;
+    static constexpr int ring = 0, ml = kWarps * kStages * kStageBytes, unit = ml + kWarps * NC * 8, seq = unit + kWarps * 8,
+                         q = seq + 16, qf = q + (wide ? NT * D * 16 : 0), first = qf + (wide ? NC * 4 : 0);
     static constexpr int total(int B) { return first + (3 * B + 1) * 4; }   // first[B + 1], then position and rows of each sequence
 };
 
@@ -178,66 +185,69 @@ __device__ __forceinline__ Item decode_item(const AttnP &p, const int *first, in
     return it;
 }
 
-// Query columns of an item into shared memory, D / 8 lanes each: scaled by a
+// A lane's query fragments: column g, dimensions 64 i + 16 t .. + 15, as the
+// B operands of k-steps 4 i .. 4 i + 3, in the order of pairs(); scaled by a
 // power of two (exactly; the row's largest to 2^12 .. 2^13, so that only
-// elements 2^26 times smaller lose bits), in the order of pairs().
-template <int FMT, int D, int NT>
-__device__ __forceinline__ void load_q(const AttnP &p, const Item &it, uint8_t *q, float *qf)
+// elements 2^26 times smaller lose bits).  Returns its inverse.
+template <int FMT, int D>
+__device__ __forceinline__ float load_q(const AttnP &p, const Item &it, int c, int tq, uint32_t (&b)[D / 16][2])
 {
-    constexpr int kLanes = D / 8, kPer = (8 * NT * kLanes + kThreads - 1) / kThreads;
-    uint16_t h[kPer][8];
+    const int m = c / p.G;
+    const bool in = c < p.C && m < it.rows;
+    const uint16_t *src = static_cast<const uint16_t *>(p.q) + it.b * p.qb + m * p.qm + (it.g * p.G + c % p.G) * p.qh + 16 * tq;
+    uint16_t h[D / 64][16];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int id = threadIdx.x + i * kThreads, col = id / kLanes, c = it.cp * 8 * NT + col, m = c / p.G;
-        const bool in = col < 8 * NT && c < p.C && m < it.rows;
-        const uint16_t *src = static_cast<const uint16_t *>(p.q) + it.b * p.qb + m * p.qm + (it.g * p.G + c % p.G) * p.qh +
-                              id % kLanes * 8;
-        if (p.qvec && in) *reinterpret_cast<uint4 *>(h[i]) = __ldg(reinterpret_cast<const uint4 *>(src));
-        else
+    for (int i = 0; i < D / 64; ++i) {
+        if (p.qvec) {
+            const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+            *reinterpret_cast<uint4 *>(h[i]) = in ? __ldg(reinterpret_cast<const uint4 *>(src + 64 * i)) : zero;
+            *reinterpret_cast<uint4 *>(h[i] + 8) = in ? __ldg(reinterpret_cast<const uint4 *>(src + 64 * i + 8)) : zero;
+        } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) h[i][j] = in ? __ldg(src + j) : (uint16_t)0;
+            for (int j = 0; j < 16; ++j) h[i][j] = in ? __ldg(src + 64 * i + j) : (uint16_t)0;
+        }
     }
+    auto value = [&](int i, int j) {
+        return p.f16 ? __half2float(__ushort_as_half(h[i][j])) : __uint_as_float((uint32_t)h[i][j] << 16);
+    };
+    float a = 0.f;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int id = threadIdx.x + i * kThreads, col = id / kLanes;
-        float v[8], a = 0.f;
+    for (int i = 0; i < D / 64; ++i)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) a = fmaxf(a, fabsf(value(i, j)));
+    a = fmaxf(a, __shfl_xor_sync(0xFFFFFFFFu, a, 1));
+    a = fmaxf(a, __shfl_xor_sync(0xFFFFFFFFu, a, 2));
+    const int e = (int)(__float_as_uint(a) >> 23) - 127;
+    const bool odd = a == 0.f || e == 128;                       // zero or infinite: as it is
+    const int up = odd ? 0 : max(-126, min(126, 12 - e));
+    const float f = pow2f(up);
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i)
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            v[j] = p.f16 ? __half2float(__ushort_as_half(h[i][j])) : __uint_as_float((uint32_t)h[i][j] << 16);
-            a = fmaxf(a, fabsf(v[j]));
-        }
-#pragma unroll
-        for (int o = kLanes / 2; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
-        const int e = (int)(__float_as_uint(a) >> 23) - 127;
-        const bool odd = a == 0.f || e == 128;                   // zero or infinite: as it is
-        const int up = odd ? 0 : max(-126, min(126, 12 - e));
-        const float f = pow2f(up);
-        uint32_t w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
             const int x = FMT == MOE_KV8_INT8 ? 4 * (j >> 1) + (j & 1) : 2 * j, y = FMT == MOE_KV8_INT8 ? x + 2 : x + 1;
-            const __half2 t = __floats2half2_rn(v[x] * f, v[y] * f);
-            w[j] = *reinterpret_cast<const uint32_t *>(&t);
+            const __half2 t = __floats2half2_rn(value(i, x) * f, value(i, y) * f);
+            b[4 * i + (j >> 1)][j & 1] = *reinterpret_cast<const uint32_t *>(&t);
         }
-        if (col < 8 * NT) {
-            *reinterpret_cast<uint4 *>(q + col * Lay<D, NT>::qrow + id % kLanes * 16) = make_uint4(w[0], w[1], w[2], w[3]);
-            if (id % kLanes == 0) qf[col] = p.scale_log2 * pow2f(-up);
-        }
-    }
+    return pow2f(-up);
 }
 
 template <int FMT, int D, int NT>
-__global__ void __launch_bounds__(kThreads, kCtas) kv8_chunk_kernel(const AttnP p)
+__global__ void __launch_bounds__(kThreads, Lay<D, NT>::ctas) kv8_chunk_kernel(const AttnP p)
 {
     using L = Lay<D, NT>;
     constexpr int R = 256 / D, TK = 16 * R, KS = D / 16, NC = 8 * NT;   // KS: k-steps of S, m-tiles of O
     extern __shared__ __align__(128) uint8_t sm[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, tq = lane & 3;
-    int *first = reinterpret_cast<int *>(sm + L::first);
-    float *red_m = reinterpret_cast<float *>(sm + L::ml), *red_l = red_m + kWarps * NC;
+    int *first = reinterpret_cast<int *>(sm + L::first), *seq = reinterpret_cast<int *>(sm + L::seq);
+    float2 *red_ml = reinterpret_cast<float2 *>(sm + L::ml), *red_unit = reinterpret_cast<float2 *>(sm + L::unit);
     const int passes = (p.C + NC - 1) / NC;
 
     // chunks before each sequence's
+    if (tid == 0) {
+        seq[0] = blockIdx.x;
+        seq[1] = gridDim.x + (p.counter ? atomicAdd(p.counter, 1) : (int)blockIdx.x);
+    }
     for (int b = tid; b < p.B; b += kThreads) {
         int p0;
         bool bad;
@@ -269,17 +279,17 @@ __global__ void __launch_bounds__(kThreads, kCtas) kv8_chunk_kernel(const AttnP 
     uint8_t *ring = sm + L::ring + warp * kStages * kStageBytes;
     const uint32_t ring_u = smem_u32(ring);
 
-    // The load cursor runs kStages tiles ahead of the compute cursor; an
-    // empty commit keeps the group count when it has run out.  A lane's i-th
-    // 16 bytes of a tile are row lr + i 512 / D, chunk lc; chunks are swapped
-    // within a row so that the reads below hit every bank once.
+    // The load cursor runs up to two tiles ahead of the compute cursor, and
+    // up to one item.  A lane's i-th 16 bytes of a tile are row lr + i 512 /
+    // D, chunk lc; chunks are swapped within a row so that the reads below hit
+    // every bank once.
     const int lr = lane / (D / 16), lc = lane % (D / 16);
     const uint32_t k_lane = lr * D + (D == 64 ? lc : lc ^ ((lr & 1) << 2)) * 16;
     constexpr int VX = D == 256 ? 4 : D == 128 ? 2 : 1;   // the values' swap depends on i mod VX
     uint32_t v_lane[VX];
 #pragma unroll
     for (int i = 0; i < VX; ++i) v_lane[i] = lr * D + (lc ^ ((lr + i * (512 / D)) & (D == 64 ? 2 : 6))) * 16;
-    int ld_item = blockIdx.x, ld_t = 0, ld_k1 = 0, ld_stage = 0;
+    int nth = 0, ld_nth = 0, ld_item = blockIdx.x, ld_t = 0, ld_k1 = 0, ld_stage = 0, free_slots = kStages;
     const uint8_t *ld_k = nullptr, *ld_v = nullptr;
     const float *ld_s = nullptr;
     auto open_item = [&]() {
@@ -292,12 +302,14 @@ __global__ void __launch_bounds__(kThreads, kCtas) kv8_chunk_kernel(const AttnP 
         ld_s = (lane & 1 ? p.vs : p.ks) + head * p.nblk;
     };
     open_item();
-    auto load_tile = [&]() {
-        while (ld_t >= ld_k1 && ld_item < total) {
-            ld_item += gridDim.x;
-            if (ld_item < total) open_item();
-        }
-        if (ld_item < total) {
+    auto fill = [&]() {
+        while (free_slots > 0) {
+            while (ld_t >= ld_k1) {
+                if (ld_nth > nth || ld_item >= total) return;
+                ld_item = seq[++ld_nth & 3];
+                if (ld_item >= total) return;
+                open_item();
+            }
             const uint32_t dst = ring_u + ld_stage * kStageBytes;
             if (ld_t + TK <= ld_k1) {
 #pragma unroll
@@ -319,16 +331,35 @@ __global__ void __launch_bounds__(kThreads, kCtas) kv8_chunk_kernel(const AttnP 
                 const bool in = t < ld_k1;
                 cp4z(dst + 2 * kTileBytes + lane * 4, in ? ld_s + (t >> p.blk_log) : ld_s, in);
             }
+            cp_commit();
             ld_t += kWarps * TK;
             ld_k += kWarps * kTileBytes;
             ld_v += kWarps * kTileBytes;
+            ld_stage ^= 1;
+            --free_slots;
         }
-        cp_commit();
-        ld_stage ^= 1;
     };
     static_assert(kStages == 2, "stages alternate");
+    fill();
+
+    // Queries of an item into shared memory (wide form): warp n column tile n
+    uint4 *const qs = reinterpret_cast<uint4 *>(sm + L::q);
+    float *const qf = reinterpret_cast<float *>(sm + L::qf);
+    auto stage_q = [&](const Item &x) {
+        if (warp < NT) {
+            uint32_t b[KS][2];
+            const float back = __fmul_rn(p.scale_log2, load_q<FMT, D>(p, x, x.cp * NC + 8 * warp + gq, tq, b));
 #pragma unroll
-    for (int i = 0; i < kStages; ++i) load_tile();
+            for (int k = 0; k < KS; k += 2)
+                qs[(warp * KS + k) * 16 + lane] = make_uint4(b[k][0], b[k][1], b[k + 1][0], b[k + 1][1]);
+            if (tq == 0) qf[8 * warp + gq] = back;
+        }
+    };
+    Item it = decode_item(p, first, blockIdx.x, passes);
+    if (L::wide) {
+        stage_q(it);
+        __syncthreads();
+    }
 
     // A lane's reads of a tile: chunk 4 i + t of key rows g and g + 8 (the
     // swap turns i even into i + 1 and back in odd rows), 16 (8) bytes of
@@ -337,20 +368,20 @@ __global__ void __launch_bounds__(kThreads, kCtas) kv8_chunk_kernel(const AttnP 
     const int v_at = 2 * tq * D + (D == 64 ? ((gq >> 1) ^ ((tq & 1) * 2)) * 16 + (gq & 1) * 8 : (gq ^ (2 * tq)) * 16);
     int stage = 0;
 #pragma unroll 1
-    for (int item = blockIdx.x; item < total; item += gridDim.x) {
-        const Item it = decode_item(p, first, item, passes);
-        const uint8_t *qs = sm + L::q;
-        float *qf = reinterpret_cast<float *>(sm + L::qf);
-        load_q<FMT, D, NT>(p, it, sm + L::q, qf);   // every warp has passed the last item's barriers, and with them its reads
-        __syncthreads();
+    for (;;) {
+        int after = 0;                 // the item after next
+        if (tid == 0) after = p.counter ? gridDim.x + atomicAdd(p.counter, 1) : seq[(nth + 1) & 3] + gridDim.x;
         float f[NT][2], m[NT][2], l[NT][2], o[NT][KS][4], vref = 0.f, inv_vref = 0.f;
         bool fresh = true;             // no tile yet: m = -inf, everything else 0
-        uint32_t qr[NT == 1 ? KS : 1][2];
+        uint32_t qr[L::wide ? 1 : NT][L::wide ? 1 : KS][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
+            float back = 0.f;
+            if constexpr (!L::wide) back = __fmul_rn(p.scale_log2, load_q<FMT, D>(p, it, it.cp * NC + 8 * n + gq, tq, qr[n]));
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                f[n][c] = qf[8 * n + 2 * tq + c];
+                // of the columns that the lane's scores belong to
+                f[n][c] = L::wide ? qf[8 * n + 2 * tq + c] : __shfl_sync(0xFFFFFFFFu, back, 4 * (2 * tq + c));
                 m[n][c] = -INFINITY;
                 l[n][c] = 0.f;
             }
@@ -359,30 +390,11 @@ __global__ void __launch_bounds__(kThreads, kCtas) kv8_chunk_kernel(const AttnP 
 #pragma unroll
                 for (int c = 0; c < 4; ++c) o[n][k][c] = 0.f;
         }
-        // k-step 4 i + j: the dimensions of the lane's bytes 4 j .. 4 j + 3 of 16 at 64 i + 16 t
-        auto q_frag = [&](int n, int i, uint32_t (&b)[8]) {
-            const uint4 *src = reinterpret_cast<const uint4 *>(qs + (8 * n + gq) * L::qrow + (64 * i + 16 * tq) * 2);
-            const uint4 x = src[0], y = src[1];
-            const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-#pragma unroll
-            for (int j = 0; j < 8; ++j) b[j] = w[j];
-        };
-        if (NT == 1) {
-#pragma unroll
-            for (int i = 0; i < D / 64; ++i) {
-                uint32_t b[8];
-                q_frag(0, i, b);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    qr[NT == 1 ? 4 * i + j : 0][0] = b[2 * j];
-                    qr[NT == 1 ? 4 * i + j : 0][1] = b[2 * j + 1];
-                }
-            }
-        }
 
 #pragma unroll 1
         for (int t0 = it.k0 + warp * TK; t0 < it.k1; t0 += kWarps * TK) {
-            cp_wait<kStages - 1>();
+            if (free_slots == 0) cp_wait<1>();
+            else cp_wait<0>();
             __syncwarp();
             const uint8_t *kt = ring + stage * kStageBytes;
             const float *steps = reinterpret_cast<const float *>(kt + 2 * kTileBytes);
@@ -391,6 +403,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) kv8_chunk_kernel(const AttnP 
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 float acc[NT][2][4];
+                uint4 qw[NT];
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -401,20 +414,19 @@ __global__ void __launch_bounds__(kThreads, kCtas) kv8_chunk_kernel(const AttnP 
                     const uint4 u = *reinterpret_cast<const uint4 *>(src);
                     const uint4 w = *reinterpret_cast<const uint4 *>(src + 8 * D);
                     const uint32_t uw[4] = {u.x, u.y, u.z, u.w}, ww[4] = {w.x, w.y, w.z, w.w};
-                    uint32_t b[NT][8];
-                    if (NT > 1) {
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) q_frag(n, i, b[n]);
-                    }
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
+                        if (L::wide && !(j & 1)) {
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) qw[n] = qs[(n * KS + 4 * i + j) * 16 + lane];
+                        }
                         uint32_t a0, a1, a2, a3;
                         pairs<FMT>(uw[j], a0, a2);
                         pairs<FMT>(ww[j], a1, a3);
 #pragma unroll
                         for (int n = 0; n < NT; ++n)
-                            if (NT == 1) mma(acc[n][j & 1], a0, a1, a2, a3, qr[NT == 1 ? 4 * i + j : 0][0], qr[NT == 1 ? 4 * i + j : 0][1]);
-                            else mma(acc[n][j & 1], a0, a1, a2, a3, b[n][2 * j], b[n][2 * j + 1]);
+                            if constexpr (L::wide) mma(acc[n][j & 1], a0, a1, a2, a3, j & 1 ? qw[n].z : qw[n].x, j & 1 ? qw[n].w : qw[n].y);
+                            else mma(acc[n][j & 1], a0, a1, a2, a3, qr[n][4 * i + j][0], qr[n][4 * i + j][1]);
                     }
                 }
                 const float ks = steps[2 * r];
@@ -559,11 +571,14 @@ __global__ void __launch_bounds__(kThreads, kCtas) kv8_chunk_kernel(const AttnP 
                 }
             }
             __syncwarp();                                          // the tile is read before its slot is filled again
-            load_tile();
+            ++free_slots;
             stage ^= 1;
+            if (t0 + kWarps * TK < it.k1) fill();                  // the last tile's slot serves the join first
         }
 
-        // ---- the chunk's result from the warps'
+        // ---- the chunk's result from the warps' that had a tile
+        const int having = min(kWarps, (it.k1 - it.k0 + TK - 1) / TK), cols = min(NC, p.C - it.cp * NC);
+        const size_t slot = (((size_t)it.b * p.nchunk + it.k0 / p.chunk) * p.Hkv + it.g) * passes + it.cp;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -572,69 +587,75 @@ __global__ void __launch_bounds__(kThreads, kCtas) kv8_chunk_kernel(const AttnP 
                 x = __fadd_rn(x, __shfl_xor_sync(0xFFFFFFFFu, x, 4));
                 x = __fadd_rn(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
                 x = __fadd_rn(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
-                if (gq == 0) {
-                    red_m[warp * NC + 8 * n + 2 * tq + c] = m[n][c];
-                    red_l[warp * NC + 8 * n + 2 * tq + c] = x;
+                if (gq == 0) red_ml[warp * NC + 8 * n + 2 * tq + c] = make_float2(m[n][c], x);
+            }
+        if (lane == 0) red_unit[warp] = make_float2(__fmul_rn(vref, 1.f / kWeightUnit), __int_as_float(stage ^ 1));
+        if (tid == 0) seq[(nth + 2) & 3] = after;
+        constexpr int kAll = NT * KS, kRound = kAll < 16 ? kAll : 16;    // m-tiles, and of them a slot's worth
+#pragma unroll
+        for (int h = 0; h < kAll / kRound; ++h) {
+            if (warp < having) {
+                float4 *dst = reinterpret_cast<float4 *>(ring + (stage ^ 1) * kStageBytes) + lane;
+#pragma unroll
+                for (int x = 0; x < kRound; ++x) {
+                    const float *v = o[(h * kRound + x) / KS][(h * kRound + x) % KS];
+                    dst[x * 32] = make_float4(v[0], v[1], v[2], v[3]);
                 }
             }
-        __syncthreads();
-        const size_t slot = ((size_t)it.b * p.nchunk + it.k0 / p.chunk) * p.Hkv + it.g, col0 = slot * p.C + it.cp * NC;
-        const int cols = min(NC, p.C - it.cp * NC);
-        if (tid < cols) {
-            float mx = -INFINITY, sum = 0.f;
-            for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, red_m[w * NC + tid]);
-            for (int w = 0; w < kWarps; ++w) {
-                const float x = red_m[w * NC + tid];
-                sum = fmaf(mx == -INFINITY ? 1.f : ex2(__fsub_rn(x, mx)), red_l[w * NC + tid], sum);
+            __syncthreads();
+            if (L::wide && h == 0) {                               // every warp is done with the queries
+                const int ni = seq[(nth + 1) & 3];
+                if (ni < total) stage_q(decode_item(p, first, ni, passes));
             }
-            p.part_ml[(col0 + tid) * 2] = mx;
-            p.part_ml[(col0 + tid) * 2 + 1] = sum;
-        }
-        float co[NT][2];
+            constexpr int kShare = kRound / kWarps;                // m-tiles a warp adds up, of one column tile
+            const int x0 = h * kRound + warp * kShare, n = x0 / KS;
+            float cf[kWarps][2], mx[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
+            const float4 *src[kWarps];
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+            for (int v = 0; v < kWarps; ++v)
+                if (v < having) {
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                float mx = -INFINITY;
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, red_m[w * NC + 8 * n + 2 * tq + c]);
-                co[n][c] = mx == -INFINITY ? 1.f : ex2(__fsub_rn(m[n][c], mx));
-            }
-        const float back = __fmul_rn(vref, 1.f / kWeightUnit);
-        // a few m-tiles at a time: every warp's fragments side by side, then one
-        // warp per m-tile adds them up
-        float4 *red = reinterpret_cast<float4 *>(sm + L::red);
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int k0 = 0; k0 < KS; k0 += L::round) {
-                __syncthreads();
-#pragma unroll
-                for (int k = 0; k < L::round; ++k) {
-                    const float *x = o[n][k0 + k];
-                    red[(warp * L::round + k) * 32 + lane] = make_float4(__fmul_rn(__fmul_rn(x[0], co[n][0]), back), __fmul_rn(__fmul_rn(x[1], co[n][1]), back),
-                                                                  __fmul_rn(__fmul_rn(x[2], co[n][0]), back), __fmul_rn(__fmul_rn(x[3], co[n][1]), back));
+                    for (int c = 0; c < 2; ++c) mx[c] = fmaxf(mx[c], red_ml[v * NC + 8 * n + 2 * tq + c].x);
                 }
-                __syncthreads();
-                if (tid < 32 * L::round) {
-                    const int k = k0 + (tid >> 5);
-                    float4 a = red[tid];
 #pragma unroll
-                    for (int w = 1; w < kWarps; ++w) {
-                        const float4 x = red[w * 32 * L::round + tid];
-                        a.x = __fadd_rn(a.x, x.x);
-                        a.y = __fadd_rn(a.y, x.y);
-                        a.z = __fadd_rn(a.z, x.z);
-                        a.w = __fadd_rn(a.w, x.w);
+            for (int v = 0; v < kWarps; ++v)
+                if (v < having) {
+                    const float2 u = red_unit[v];
+                    src[v] = reinterpret_cast<const float4 *>(sm + L::ring + (v * kStages + __float_as_int(u.y)) * kStageBytes) +
+                             (x0 - h * kRound) * 32 + lane;
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const float2 x = red_ml[v * NC + 8 * n + 2 * tq + c];
+                        const float w = mx[c] == -INFINITY ? 1.f : ex2(__fsub_rn(x.x, mx[c]));
+                        sum[c] = __fmaf_rn(w, x.y, sum[c]);
+                        cf[v][c] = __fmul_rn(w, u.x);
                     }
-                    // m-tile k: dimensions d (rows g) and d + 1 (rows g + 8)
-                    constexpr int VW = D >= 128 ? 4 : 2;
-                    const int h = k / (2 * VW), w = k / 2 % VW, d = 4 * VW * (gq + 8 * h) + 4 * w + 2 * (k & 1);
-                    const int c = 8 * n + 2 * tq;
-                    if (c < cols) *reinterpret_cast<float2 *>(p.part_o + (col0 + c) * D + d) = make_float2(a.x, a.z);
-                    if (c + 1 < cols) *reinterpret_cast<float2 *>(p.part_o + (col0 + c + 1) * D + d) = make_float2(a.y, a.w);
+                }
+            if (8 * n + 2 * tq < cols) {
+                if (x0 % KS == 0 && gq == 0)
+                    *reinterpret_cast<float4 *>(p.part_ml + (slot * NC + 8 * n + 2 * tq) * 2) = make_float4(mx[0], sum[0], mx[1], sum[1]);
+                float4 *dst = reinterpret_cast<float4 *>(p.part_o) + (slot * kAll + x0) * 32 + lane;
+#pragma unroll
+                for (int x = 0; x < kShare; ++x) {
+                    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int v = 0; v < kWarps; ++v)
+                        if (v < having) {
+                            const float4 y = src[v][x * 32];
+                            a.x = __fmaf_rn(cf[v][0], y.x, a.x);
+                            a.y = __fmaf_rn(cf[v][1], y.y, a.y);
+                            a.z = __fmaf_rn(cf[v][0], y.z, a.z);
+                            a.w = __fmaf_rn(cf[v][1], y.w, a.w);
+                        }
+                    dst[x * 32] = a;
                 }
             }
+            __syncthreads();
+        }
+        const int ni = seq[++nth & 3];
+        if (ni >= total) break;
+        it = decode_item(p, first, ni, passes);
+        fill();
     }
     cp_wait<0>();
 }
@@ -646,91 +667,131 @@ __device__ __forceinline__ void store_out(void *o, int type, size_t i, float v)
     else static_cast<float *>(o)[i] = v;
 }
 
-// Joins a row's chunks: one CTA per (row, query head, 64 value dimensions;
-// sequence).  16 groups of 16 lanes (four dimensions each) take every 16th
-// chunk and are added in order, so the order depends on the number of chunks
-// alone.
-constexpr int kMergeThreads = 256;
+// ------------------------------------------------------------------- merge
+// Joins the chunks of a (sequence, head, column tile): a CTA per two m-tiles
+// (4 dimensions for each group of 4 lanes) and share of the chunks, the shares
+// of a cluster joined through its first CTA's shared memory.  Within a CTA
+// 4 warps per m-tile take every 4th chunk, so the order of additions depends
+// on the number of chunks and the cache's shape alone; chunks that a column does not see
+// (another row's) add exact zeros.
+constexpr int kMergeThreads = 256, kMergeShares = 8;
 
-__global__ void __launch_bounds__(kMergeThreads) kv8_merge_kernel(const AttnP p, int D)
+// (m, l, o) += another, with per-column references; -inf: nothing.
+__device__ __forceinline__ void join(float (&m)[2], float (&l)[2], float4 &o, const float4 &ml, const float4 &x)
 {
-    __shared__ float red[33], so[16][16][4], sl[16];
-    const int slices = D / 64, tid = threadIdx.x, x = blockIdx.x / slices, b = blockIdx.y;
-    const int m = x / p.Hq, h = x % p.Hq, lane = tid & 15, grp = tid >> 4, d = blockIdx.x % slices * 64 + lane * 4;
-    const int g = h / p.G, c = m * p.G + h % p.G;
+    const float bm[2] = {ml.x, ml.z}, bl[2] = {ml.y, ml.w};
+    float fa[2], fb[2];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        const float r = fmaxf(m[c], bm[c]), base = r == -INFINITY ? 0.f : r;
+        fa[c] = exp2f(m[c] - base);
+        fb[c] = exp2f(bm[c] - base);
+        l[c] = l[c] * fa[c] + fb[c] * bl[c];
+        m[c] = r;
+    }
+    o.x = o.x * fa[0] + fb[0] * x.x;
+    o.y = o.y * fa[1] + fb[1] * x.y;
+    o.z = o.z * fa[0] + fb[0] * x.z;
+    o.w = o.w * fa[1] + fb[1] * x.w;
+}
+
+__global__ void __launch_bounds__(kMergeThreads) kv8_merge_kernel(const AttnP p, int D, int shares)
+{
+    __shared__ float4 so[8][32], sml[8][32];
+    __shared__ float4 co[kMergeShares][64], cml[kMergeShares][64];   // the shares' results, in the cluster's first CTA
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, tq = lane & 3;
+    const int KS = D / 16, nt = kv8_nt(p.C, D), NC = 8 * nt, passes = (p.C + NC - 1) / NC;
+    // blockIdx.x: share, then pair of m-tiles, then column tile
+    const int share = blockIdx.x % shares, pair = blockIdx.x / shares % (KS / 2), ct = blockIdx.x / shares / (KS / 2);
+    const int g = blockIdx.y, b = blockIdx.z, k = 2 * pair + (warp & 1);
     int p0;
     bool bad;
     const int rows = kv8_rows(p.pos, p.counts, b, p.M, p.T_cap, p0, bad);
-    const int n = m < rows ? p0 + m + 1 : 0, nch = (n + p.chunk - 1) / p.chunk;
-    const size_t out = ((size_t)(b * p.M + m) * p.Hq + h) * D;
-    if (nch == 0) {
-        if (tid < 64) store_out(p.o, p.o_type, out + blockIdx.x % slices * 64 + tid, 0.f);
-        return;
-    }
-    const size_t c0 = ((size_t)b * p.nchunk * p.Hkv + g) * p.C + c, step = (size_t)p.Hkv * p.C;
-    float mx = -INFINITY;
-    for (int j = tid; j < nch; j += kMergeThreads) mx = fmaxf(mx, __ldg(p.part_ml + (c0 + j * step) * 2));
-    mx = cta_max(mx, red);
-    float o[4] = {0.f, 0.f, 0.f, 0.f}, l = 0.f;
-#pragma unroll 4
-    for (int j = grp; j < nch; j += 16) {
-        const size_t i = c0 + j * step;
-        const float2 ml = __ldg(reinterpret_cast<const float2 *>(p.part_ml) + i);
-        const float4 v = __ldg(reinterpret_cast<const float4 *>(p.part_o + i * D + d));
-        const float w = exp2f(ml.x - mx);
-        l = fmaf(w, ml.y, l);
-        o[0] = fmaf(w, v.x, o[0]);
-        o[1] = fmaf(w, v.y, o[1]);
-        o[2] = fmaf(w, v.z, o[2]);
-        o[3] = fmaf(w, v.w, o[3]);
-    }
+    const int n = rows > 0 ? p0 + rows : 0, nch = (n + p.chunk - 1) / p.chunk;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    const bool on = 8 * ct + 2 * tq < p.C;
+    const int stride = 4 * shares;
+    auto slot = [&](int j) { return (((size_t)b * p.nchunk + j) * p.Hkv + g) * passes + ct / nt; };
+    if (on) {
+        for (int j = share * 4 + (warp >> 1); j < nch; j += 4 * stride) {
+            float4 ml[4], x[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) so[grp][lane][i] = o[i];
-    if (lane == 0) sl[grp] = l;
-    __syncthreads();
-    if (tid < 64) {
-        float a = 0.f, s = 0.f;
-        const int ng = min(nch, 16);
-        for (int i = 0; i < ng; ++i) {
-            a += so[i][tid >> 2][tid & 3];
-            s += sl[i];
+            for (int u = 0; u < 4; ++u) {
+                const int ju = j + u * stride;
+                ml[u] = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+                x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (ju < nch) {
+                    const size_t s = slot(ju);
+                    ml[u] = __ldcg(reinterpret_cast<const float4 *>(p.part_ml + (s * NC + 8 * (ct % nt) + 2 * tq) * 2));
+                    x[u] = __ldcg(reinterpret_cast<const float4 *>(p.part_o) + ((s * nt + ct % nt) * KS + k) * 32 + lane);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) join(m, l, o, ml[u], x[u]);
         }
-        store_out(p.o, p.o_type, out + blockIdx.x % slices * 64 + tid, a / s);
+    }
+    so[warp][lane] = o;
+    sml[warp][lane] = make_float4(m[0], l[0], m[1], l[1]);
+    __syncthreads();
+    if (warp < 2) {
+#pragma unroll
+        for (int w = 1; w < 4; ++w) join(m, l, o, sml[warp + 2 * w][lane], so[warp + 2 * w][lane]);
+    }
+    if (shares > 1) {
+        if (warp < 2) {
+            // to the first CTA of the cluster
+            uint32_t dst;
+            const float4 ml = make_float4(m[0], l[0], m[1], l[1]);
+            asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(dst) : "r"(smem_u32(&co[share][warp * 32 + lane])));
+            asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "f"(o.x), "f"(o.y), "f"(o.z), "f"(o.w) : "memory");
+            asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(dst) : "r"(smem_u32(&cml[share][warp * 32 + lane])));
+            asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "f"(ml.x), "f"(ml.y), "f"(ml.z), "f"(ml.w) : "memory");
+        }
+        asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+        if (share != 0) return;
+        if (warp < 2)
+            for (int s = 1; s < shares; ++s) join(m, l, o, cml[s][warp * 32 + lane], co[s][warp * 32 + lane]);
+    }
+    if (warp >= 2) return;
+    // dimensions of m-tile k: d (rows g) and d + 1 (rows g + 8)
+    const int VW = D >= 128 ? 4 : 2, d = 4 * VW * (gq + 8 * (k / (2 * VW))) + 4 * (k / 2 % VW) + 2 * (k & 1);
+    const float v[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        const int col = 8 * ct + 2 * tq + c;
+        if (col >= p.C) continue;
+        const int row = col / p.G, h = g * p.G + col % p.G;
+        const size_t out = (((size_t)b * p.M + row) * p.Hq + h) * D + d;
+        const bool seen = row < rows;
+        store_out(p.o, p.o_type, out, seen ? v[c] / l[c] : 0.f);
+        store_out(p.o, p.o_type, out + 1, seen ? v[2 + c] / l[c] : 0.f);
+        if (p.sc && k == 0 && gq == 0) {
+            float *fin = p.fin + (((size_t)b * p.Hkv + g) * p.C + col) * 2;
+            fin[0] = m[c];
+            fin[1] = 1.f / l[c];
+        }
     }
 }
 
-// Weight received by each position: every CTA joins the columns' maxima and
-// sums, then adds its positions' normalised weights in column order.
+// Weight received by each position: the stored scores against the columns'
+// joined references and sums, in column order.
 constexpr int kAccThreads = 256;
 
 __global__ void __launch_bounds__(kAccThreads) kv8_weights_kernel(const AttnP p)
 {
-    extern __shared__ float st[];   // [C][2]: maximum, 1 / sum
+    extern __shared__ float st[];   // [C][2]: reference, 1 / sum
     const int g = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
     int p0;
     bool bad;
     const int rows = kv8_rows(p.pos, p.counts, b, p.M, p.T_cap, p0, bad);
     const int n = rows > 0 ? p0 + rows : 0, t0 = blockIdx.x * kAccThreads;
     if (t0 >= n) return;
-    const size_t slot0 = (size_t)b * p.nchunk * p.Hkv + g;
-    for (int c = tid; c < p.C; c += kAccThreads) {
-        const int m = c / p.G, nch = m < rows ? (p0 + m + p.chunk) / p.chunk : 0;
-        float mx = -INFINITY, l = 0.f;
-        for (int j = 0; j < nch; ++j) {
-            const float v = __ldg(p.part_ml + ((slot0 + (size_t)j * p.Hkv) * p.C + c) * 2);
-            mx = v > mx || v != v ? v : mx;
-        }
-        for (int j = 0; j < nch; ++j) {
-            const size_t i = (slot0 + (size_t)j * p.Hkv) * p.C + c;
-            l = fmaf(exp2f(__ldg(p.part_ml + i * 2) - mx), __ldg(p.part_ml + i * 2 + 1), l);
-        }
-        st[2 * c] = mx;
-        st[2 * c + 1] = 1.f / l;
-    }
+    const size_t head = (size_t)b * p.Hkv + g;
+    for (int i = tid; i < 2 * p.C; i += kAccThreads) st[i] = __ldg(p.fin + head * p.C * 2 + i);
     __syncthreads();
     const int t = t0 + tid;
     if (t >= n) return;
-    const size_t head = (size_t)b * p.Hkv + g;
     float a = t < p0 && p.acc_in ? p.decay * p.acc_in[head * p.T_cap + t] : 0.f;
     for (int c = 0; c < p.C; ++c)
         if (c / p.G < rows && t <= p0 + c / p.G)
@@ -738,18 +799,20 @@ __global__ void __launch_bounds__(kAccThreads) kv8_weights_kernel(const AttnP p)
     p.acc[head * p.T_cap + t] = a;
 }
 
-// Positions per chunk: 2 to 32 rounds of a CTA's warps (a round: 32 KB of keys
-// and values), as many as leave every CTA slot of 152 SMs a few chunks of a
-// full cache.
+// Positions per chunk: 1 to 16 tiles a warp, as many as leave every CTA slot
+// of 152 SMs a few chunks of a full cache.
 #ifndef KV8_ITEMS
-#define KV8_ITEMS 4
+#define KV8_ITEMS 2
+#endif
+#ifndef KV8_MAXT
+#define KV8_MAXT 16
 #endif
 int kv8_chunk(const moe_kv8 &c)
 {
-    const int round = kWarps * 4096 / c.head_dim;
+    const int round = kWarps * kTileBytes / c.head_dim;
     const long long rounds = (long long)c.batch * c.kv_heads * c.T_cap / round;
-    int r = 32;
-    while (r > 2 && rounds < 152LL * kCtas * KV8_ITEMS * r) r /= 2;
+    int r = KV8_MAXT;
+    while (r > 1 && rounds < 152LL * 3 * KV8_ITEMS * r) r /= 2;
     return r * round;
 }
 
@@ -760,17 +823,20 @@ struct Once {
 };
 
 struct Kv8Ws {
-    size_t ml, o, sc, total;
+    size_t cnt, ml, o, fin, sc, total;
 };
 Kv8Ws kv8_ws(const moe_kv8 &c, int M, bool weights)
 {
     const size_t slots = (size_t)c.batch * ((c.T_cap + kv8_chunk(c) - 1) / kv8_chunk(c)) * c.kv_heads;
-    const size_t cols = (size_t)(c.q_heads / c.kv_heads) * M;
+    const int C = c.q_heads / c.kv_heads * M, NC = 8 * kv8_nt(C, c.head_dim);
+    const size_t cols = (size_t)(C + NC - 1) / NC * NC;
     Kv8Ws w;
-    w.ml = 0;
-    w.o = align_up(slots * cols * 2 * sizeof(float), 256);
-    w.sc = align_up(w.o + slots * cols * c.head_dim * sizeof(float), 256);
-    w.total = weights ? align_up(w.sc + (size_t)c.batch * c.kv_heads * c.T_cap * cols * sizeof(float), 256) : w.sc;
+    w.cnt = 0;
+    w.ml = 256;
+    w.o = align_up(w.ml + slots * cols * 2 * sizeof(float), 256);
+    w.fin = align_up(w.o + slots * cols * c.head_dim * sizeof(float), 256);
+    w.sc = align_up(w.fin + (size_t)c.batch * c.kv_heads * C * 2 * sizeof(float), 256);
+    w.total = weights ? align_up(w.sc + (size_t)c.batch * c.kv_heads * c.T_cap * C * sizeof(float), 256) : w.sc;
     return w;
 }
 
@@ -797,6 +863,7 @@ int launch_kv8_attn(const moe_kv8 &c, const moe_rows &q, int M, const int32_t *p
     p.counts = counts;
     p.part_ml = reinterpret_cast<float *>(base + w.ml);
     p.part_o = reinterpret_cast<float *>(base + w.o);
+    p.fin = reinterpret_cast<float *>(base + w.fin);
     p.sc = acc ? reinterpret_cast<float *>(base + w.sc) : nullptr;
     p.o = o;
     p.acc_in = acc_in;
@@ -822,11 +889,10 @@ int launch_kv8_attn(const moe_kv8 &c, const moe_rows &q, int M, const int32_t *p
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess || dev < 0 || dev >= 64) { note_cuda_error((int)e); return MOE_ERR_CUDA; }
-    // Column tiles a warp holds: what its registers take, and no more than there are columns.
-    const int nt = p.C <= 8 || c.head_dim == 256 ? 1 : 2;
+    const int nt = kv8_nt(p.C, c.head_dim);
     const long long items = (long long)p.nchunk * p.B * p.Hkv * ((p.C + 8 * nt - 1) / (8 * nt));
-    if (items > INT_MAX) return MOE_ERR_UNSUPPORTED;
-    auto go = [&](auto kernel, int smem, Once &once) {
+    if (items > INT_MAX / 2) return MOE_ERR_UNSUPPORTED;
+    auto go = [&](auto kernel, int smem, int ctas, Once &once) {
         std::call_once(once.flag[dev], [&] {
             e = cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
             if (e == cudaSuccess)
@@ -834,24 +900,36 @@ int launch_kv8_attn(const moe_kv8 &c, const moe_rows &q, int M, const int32_t *p
                                          (int)cudaSharedmemCarveoutMaxShared);
             if (e == cudaSuccess) e = cudaDeviceGetAttribute(&once.sms[dev], cudaDevAttrMultiProcessorCount, dev);
         });
-        if (e != cudaSuccess || once.sms[dev] < 1) return;
-        kernel<<<(int)std::min<long long>(items, (long long)once.sms[dev] * kCtas), kThreads, smem, stream>>>(p);
+        if (e == cudaSuccess && once.sms[dev] < 1) e = cudaErrorInvalidDevice;
+        if (e != cudaSuccess) return;
+        const int grid = (int)std::min<long long>(items, (long long)once.sms[dev] * ctas);
+        p.counter = nullptr;
+        if (items >= 3LL * grid) {
+            p.counter = reinterpret_cast<int *>(base + w.cnt);
+            e = cudaMemsetAsync(p.counter, 0, sizeof(int), stream);
+            if (e != cudaSuccess) return;
+        }
+        kernel<<<grid, kThreads, smem, stream>>>(p);
     };
-#define KV8_GO(F, D, N)                                                                     \
-    do {                                                                                    \
-        static Once once;                                                                   \
-        static_assert(Lay<D, N>::total(MOE_KV8_MAX_BATCH) <= kSmemMax, "shared memory");    \
-        go(kv8_chunk_kernel<F, D, N>, Lay<D, N>::total(p.B), once);                         \
+#define KV8_GO(F, D, N)                                                                      \
+    do {                                                                                     \
+        static Once once;                                                                    \
+        static_assert(Lay<D, N>::total(MOE_KV8_MAX_BATCH) <= kSmemMax, "shared memory");     \
+        go(kv8_chunk_kernel<F, D, N>, Lay<D, N>::total(p.B), Lay<D, N>::ctas, once);         \
     } while (0)
 #define KV8_GO_F(F)                              \
     do {                                         \
-        if (c.head_dim == 256) KV8_GO(F, 256, 1); \
-        else if (c.head_dim == 128) {            \
+        if (c.head_dim == 256) {                 \
+            if (nt == 1) KV8_GO(F, 256, 1);      \
+            else KV8_GO(F, 256, 2);              \
+        } else if (c.head_dim == 128) {          \
             if (nt == 1) KV8_GO(F, 128, 1);      \
-            else KV8_GO(F, 128, 2);              \
+            else if (nt == 2) KV8_GO(F, 128, 2); \
+            else KV8_GO(F, 128, 4);              \
         } else {                                 \
             if (nt == 1) KV8_GO(F, 64, 1);       \
-            else KV8_GO(F, 64, 2);               \
+            else if (nt == 2) KV8_GO(F, 64, 2);  \
+            else KV8_GO(F, 64, 4);               \
         }                                        \
     } while (0)
     if (c.format == MOE_KV8_INT8) KV8_GO_F(MOE_KV8_INT8);
@@ -860,7 +938,22 @@ int launch_kv8_attn(const moe_kv8 &c, const moe_rows &q, int M, const int32_t *p
 #undef KV8_GO
     if (e != cudaSuccess) { note_cuda_error((int)e); return MOE_ERR_CUDA; }
     note_launch();
-    kv8_merge_kernel<<<dim3(M * c.q_heads * (c.head_dim / 64), c.batch), kMergeThreads, 0, stream>>>(p, c.head_dim);
+    {
+        int shares = 1;
+        while (shares < kMergeShares && p.nchunk > 32 * shares) shares *= 2;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(shares * (c.head_dim / 32) * ((p.C + 7) / 8), p.Hkv, p.B);
+        cfg.blockDim = dim3(kMergeThreads);
+        cfg.stream = stream;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = shares;
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        e = cudaLaunchKernelEx(&cfg, kv8_merge_kernel, p, c.head_dim, shares);
+        if (e != cudaSuccess) { note_cuda_error((int)e); return MOE_ERR_CUDA; }
+    }
     note_launch();
     if (acc) {
         kv8_weights_kernel<<<dim3((c.T_cap + kAccThreads - 1) / kAccThreads, c.kv_heads, c.batch), kAccThreads,
