@@ -1,18 +1,51 @@
 // The 8-bit key/value cache (moe_kv8.cuh): appending rows, reading values
 // back, and eviction by accumulated attention weight.  The attention over it
 // is moe_kv8_attn.cu.
+#include <algorithm>
+#include <mutex>
+
 #include "moe_kv8.cuh"
 
 namespace moe {
 namespace {
 
-// ------------------------------------------------------------------ append
-// One CTA per (block of positions that the rows can touch, head and tensor,
-// sequence).  The block's step is the smallest that holds the new rows, and
-// no smaller than that of its earlier rows, whose codes are rounded again
-// when it grew.  A thread holds 8 consecutive values of a row.
-constexpr int kAppThreads = 256;
+// A block of positions of one head and tensor belongs to (block / 8) (D / 8)
+// consecutive threads, 16 to 512 of them: a thread holds 8 consecutive values
+// of 8 rows, so a block is read once, its maximum taken, and written from
+// registers.  CTAs hold as many blocks as 256 threads do.
+struct Place {
+    int j, row, d, threads;        // block within the CTA's blocks, first of the thread's rows, dimension, threads per block
+};
+__device__ __forceinline__ Place place_of(int blk, int D)
+{
+    Place q;
+    q.threads = (blk >> 3) * (D >> 3);
+    const int r = threadIdx.x & (q.threads - 1);
+    q.j = threadIdx.x / q.threads;
+    q.row = r / (D >> 3);
+    q.d = r % (D >> 3) * 8;
+    return q;
+}
 
+// Maximum over a block's threads (a power of two); `red` holds a float per warp.
+__device__ __forceinline__ float place_max(float v, const Place &q, float *red)
+{
+    for (int o = min(q.threads, 32) >> 1; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+    if (q.threads <= 32) return v;
+    const int warp = threadIdx.x >> 5, nw = q.threads >> 5;
+    if ((threadIdx.x & 31) == 0) red[warp] = v;
+    __syncthreads();
+    for (int w = 0; w < nw; ++w) v = fmaxf(v, red[(warp & ~(nw - 1)) + w]);
+    return v;
+}
+int place_threads(int blk, int D) { return std::max(256, blk / 8 * (D / 8)); }
+int place_blocks(int blk, int D) { return place_threads(blk, D) / (blk / 8 * (D / 8)); }
+
+// ------------------------------------------------------------------ append
+// The blocks that a sequence's new rows touch.  A block's step is the
+// smallest that holds the new rows, and no smaller than that of its earlier
+// rows, whose codes are rounded again when it grew.  Bound by the copy: two (four)
+// bytes in and one out per value.
 struct AppendParams {
     const void *src[2];            // new keys, values
     uint8_t *codes[2];
@@ -24,101 +57,135 @@ struct AppendParams {
     int vec;                       // 16-byte loads of 8 (4) consecutive values
 };
 
+// 8 consecutive elements as they lie, and their values.
 template <int TYPE>
-__device__ __forceinline__ void load8(const void *src, long long i, int vec, float (&v)[8])
-{
-    if (TYPE == MOE_F32) {
-        const float *p = static_cast<const float *>(src) + i;
+struct Raw {
+    uint32_t w[TYPE == MOE_F32 ? 8 : 4];
+
+    __device__ __forceinline__ void load(const void *src, long long i, bool vec)
+    {
+        const uint8_t *p = static_cast<const uint8_t *>(src) + i * (TYPE == MOE_F32 ? 4 : 2);
         if (vec) {
-            const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
-            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+#pragma unroll
+            for (int j = 0; j < (TYPE == MOE_F32 ? 2 : 1); ++j)
+                *reinterpret_cast<uint4 *>(w + 4 * j) = __ldg(reinterpret_cast<const uint4 *>(p) + j);
+        } else if (TYPE == MOE_F32) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[TYPE == MOE_F32 ? j : 0] = __ldg(reinterpret_cast<const uint32_t *>(p) + j);
         } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = __ldg(p + j);
+            for (int j = 0; j < 4; ++j)
+                w[j] = (uint32_t)__ldg(reinterpret_cast<const uint16_t *>(p) + 2 * j) |
+                       (uint32_t)__ldg(reinterpret_cast<const uint16_t *>(p) + 2 * j + 1) << 16;
         }
-        return;
     }
-    uint16_t h[8];
-    const uint16_t *p = static_cast<const uint16_t *>(src) + i;
-    if (vec) {
-        *reinterpret_cast<uint4 *>(h) = __ldg(reinterpret_cast<const uint4 *>(p));
-    } else {
+    // Largest of m and the magnitudes' bits, which order as the magnitudes do:
+    // two 16-bit halves, or one word.
+    __device__ __forceinline__ uint32_t amax(uint32_t m) const
+    {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) h[j] = __ldg(p + j);
+        for (int j = 0; j < (TYPE == MOE_F32 ? 8 : 4); ++j)
+            m = TYPE == MOE_F32 ? max(m, w[j] & 0x7FFFFFFFu) : __vmaxu2(m, w[j] & 0x7FFF7FFFu);
+        return m;
     }
+    // Their value; infinite or NaN: not finite.
+    static __device__ __forceinline__ float magnitude(uint32_t m)
+    {
+        if (TYPE == MOE_F32) return __uint_as_float(m);
+        m = max(m & 0xFFFFu, m >> 16);
+        return TYPE == MOE_BF16 ? __uint_as_float(m << 16) : __half2float(__ushort_as_half((uint16_t)m));
+    }
+    // CLEAN: with infinities as the type's largest value and NaN as zero.
+    template <bool CLEAN>
+    __device__ __forceinline__ void values(float (&v)[8]) const
+    {
+        const float big = TYPE == MOE_BF16 ? __uint_as_float(0x7F7F0000u) : TYPE == MOE_F16 ? 65504.f : __uint_as_float(0x7F7FFFFFu);
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-        v[j] = TYPE == MOE_BF16 ? __uint_as_float((uint32_t)h[j] << 16) : __half2float(__ushort_as_half(h[j]));
-}
-
-// Infinities become the type's largest value, NaN zero; says whether there was any.
-template <int TYPE>
-__device__ __forceinline__ bool make_finite(float (&v)[8])
-{
-    const float big = TYPE == MOE_BF16 ? __uint_as_float(0x7F7F0000u) : TYPE == MOE_F16 ? 65504.f : __uint_as_float(0x7F7FFFFFu);
-    bool odd = false;
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        if (!(fabsf(v[j]) <= big)) {
-            odd = true;
-            v[j] = v[j] != v[j] ? 0.f : copysignf(big, v[j]);
+        for (int j = 0; j < 8; ++j) {
+            if (TYPE == MOE_F32) v[j] = __uint_as_float(w[TYPE == MOE_F32 ? j : 0]);
+            else if (TYPE == MOE_BF16) v[j] = __uint_as_float(j & 1 ? w[j / 2] & 0xFFFF0000u : w[j / 2] << 16);
+            else v[j] = __half2float(__ushort_as_half((uint16_t)(w[j / 2] >> (16 * (j & 1)))));
+            if (CLEAN && !(fabsf(v[j]) <= big)) v[j] = v[j] != v[j] ? 0.f : copysignf(big, v[j]);
         }
-    return odd;
-}
+    }
+};
 
 template <int FMT, int TYPE>
-__global__ void __launch_bounds__(kAppThreads) kv8_append_kernel(const AppendParams p)
+__global__ void __launch_bounds__(512) kv8_append_kernel(const AppendParams p)
 {
-    __shared__ float red[33];
+    __shared__ float red[16];
     const int b = blockIdx.z, g = blockIdx.y >> 1, which = blockIdx.y & 1;
     int p0;
     bool bad;
     const int n = kv8_rows(p.pos, p.counts, b, p.M, p.T_cap, p0, bad);
     if (bad && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) atomicOr(p.err, kKv8ErrRange);
     if (n <= 0) return;
-    const int j = p0 / p.blk + blockIdx.x, t0 = j * p.blk;
-    if (t0 >= p0 + n) return;
-    const int first = max(t0, p0), last = min(t0 + p.blk, p0 + n);   // new rows: positions first .. last - 1
-    const int lanes = p.D / 8, r0 = threadIdx.x / lanes, d = threadIdx.x % lanes * 8, dr = kAppThreads / lanes;
-    const long long s0 = b * p.sb[which] + g * p.sh[which] + d, sm = p.sm[which];
-    float amax = 0.f;
-    bool odd = false;
-    for (int t = first + r0; t < last; t += dr) {
-        float v[8];
-        load8<TYPE>(p.src[which], s0 + (t - p0) * sm, p.vec, v);
-        odd |= make_finite<TYPE>(v);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
-    }
-    if (odd) atomicOr(p.err, kKv8ErrNonFinite);
-    amax = cta_max(amax, red);
-    int e = step_exp<FMT>(amax);
+    const Place q = place_of(p.blk, p.D);
+    const int j = p0 / p.blk + blockIdx.x * (blockDim.x / q.threads) + q.j, t0 = j * p.blk;
+    const int first = max(t0, p0), last = min(t0 + p.blk, p0 + n);   // new rows: positions first .. last - 1, none past the call's blocks
     const size_t head = (size_t)b * p.Hkv + g;
+    const long long s0 = b * p.sb[which] + g * p.sh[which] + q.d, sm = p.sm[which];
+    Raw<TYPE> raw[8];
+    uint32_t most = 0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int t = t0 + q.row + i * (p.blk >> 3);
+        if (t >= first && t < last) raw[i].load(p.src[which], s0 + (t - p0) * sm, p.vec);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int t = t0 + q.row + i * (p.blk >> 3);
+        if (t >= first && t < last) most = raw[i].amax(most);
+    }
+    float amax = Raw<TYPE>::magnitude(most);
+    const bool odd = !(amax <= __uint_as_float(0x7F7FFFFFu));        // an infinity or NaN among the thread's values
+    if (odd) {
+        atomicOr(p.err, kKv8ErrNonFinite);
+        amax = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int t = t0 + q.row + i * (p.blk >> 3);
+            if (t >= first && t < last) {
+                float v[8];
+                raw[i].template values<true>(v);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) amax = fmaxf(amax, fabsf(v[c]));
+            }
+        }
+    }
+    const bool mixed = first > t0 && first < last;                   // earlier rows in the block
     float *scale = p.scale[which] + head * p.nblk + j;
-    uint8_t *codes = p.codes[which] + head * p.T_cap * p.D + d;
-    if (first > t0) {
-        const float was = *scale;
+    const float was = mixed ? *scale : 0.f;
+    amax = place_max(amax, q, red);
+    __syncthreads();                                                 // every thread has read the old step
+    if (first >= last) return;
+    int e = step_exp<FMT>(amax);
+    uint8_t *codes = p.codes[which] + head * p.T_cap * p.D + q.d;
+    if (mixed) {
         const int e_old = max((int)(__float_as_uint(was) >> 23) - 127, kKv8MinExp);
         if (e > e_old) {
             // 2^(e_old - e), zero where no code can survive (or the block had no step)
             const float down = was > 0.f && e - e_old <= 126 ? pow2f(e_old - e) : 0.f;
-            for (int t = t0 + r0; t < first; t += dr) {
+            for (int t = t0 + q.row; t < first; t += p.blk >> 3) {
                 uint2 *w = reinterpret_cast<uint2 *>(codes + (size_t)t * p.D);
                 *w = recode8<FMT>(*w, down);
             }
         }
         e = max(e, e_old);
     }
-    __syncthreads();   // every thread has read the old step
-    if (threadIdx.x == 0) *scale = pow2f(e);
+    if (q.row == 0 && q.d == 0) *scale = pow2f(e);
     const float inv = pow2f(-e);
-    for (int t = first + r0; t < last; t += dr) {
-        float v[8];
-        load8<TYPE>(p.src[which], s0 + (t - p0) * sm, p.vec, v);
-        make_finite<TYPE>(v);
-        *reinterpret_cast<uint2 *>(codes + (size_t)t * p.D) =
-            make_uint2(encode4<FMT>(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
-                       encode4<FMT>(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int t = t0 + q.row + i * (p.blk >> 3);
+        if (t >= first && t < last) {
+            float v[8];
+            if (odd) raw[i].template values<true>(v);
+            else raw[i].template values<false>(v);
+            *reinterpret_cast<uint2 *>(codes + (size_t)t * p.D) =
+                make_uint2(encode4<FMT>(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
+                           encode4<FMT>(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
+        }
     }
 }
 
@@ -162,12 +229,16 @@ __global__ void __launch_bounds__(256) kv8_read_kernel(const ReadParams p)
 }
 
 // ------------------------------------------------------------------- evict
-// Selection: one CTA per (sequence, head).  Of n > budget positions the
-// first `sinks` and last `recent` stay, and the rest are ranked by weight
-// (larger first, then the lower position): a radix select over 32-bit keys
-// finds the weight of the last one that stays and how many of its equals do,
-// and a scan in position order writes the kept positions.
-constexpr int kSelThreads = 1024;
+// Selection: a cluster of 1 to 8 CTAs per (sequence, head), a slice of the
+// positions each.  Of n > budget positions the first `sinks` and last `recent`
+// stay, and the rest are ranked by weight (larger first, then the lower
+// position).  A radix select over 32-bit keys (11, 11 and 10 bits, the slices'
+// histograms added up through distributed shared memory) finds the weight of
+// the last one that stays and how many of its equals do; then every warp
+// counts what its part keeps, and writes it behind what the parts before it
+// do.  Bound by latency: three passes over keys in shared memory (in L2 where
+// a slice has more than 16K), a cluster barrier each.
+constexpr int kSelThreads = 1024, kSelKeys = 16384, kSelBins = 2048, kSelCtas = 8;
 
 struct EvictParams {
     const uint8_t *codes[2];
@@ -190,158 +261,224 @@ __device__ __forceinline__ uint32_t weight_key(float v)
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-__device__ __forceinline__ int cta_sum(int v, int *red)
+__device__ __forceinline__ void cluster_sync(int ctas)
 {
-    v = __reduce_add_sync(0xFFFFFFFFu, v);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    __syncthreads();
-    if (lane == 0) red[warp] = v;
-    __syncthreads();
-    int s = 0;
-    for (int w = 0; w < (int)(blockDim.x >> 5); ++w) s += red[w];
-    return s;
+    if (ctas == 1) __syncthreads();
+    else asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Word of another CTA of the cluster at the place that p has in this one.
+__device__ __forceinline__ int peer(const int *p, int rank)
+{
+    uint32_t a;
+    int v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
 }
 
-__global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(const EvictParams p)
+__global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(const EvictParams p, int ctas)
 {
-    __shared__ unsigned hist[256];
-    __shared__ int red[32], sh_digit, sh_need;
-    const int g = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    extern __shared__ uint32_t sel[];
+    int *hist = reinterpret_cast<int *>(sel);                       // [2][bins]: the passes take turns
+    uint32_t *keys = sel + 2 * kSelBins;                            // [kSelKeys]
+    __shared__ int wsum[32], weq[32], total[2], sh_digit, sh_need;
+    const int rank = blockIdx.x % ctas, g = blockIdx.x / ctas, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int len = p.lens[b];
-    if (len > p.T_cap && g == 0 && tid == 0) atomicOr(p.err, kKv8ErrRange);
+    if (len > p.T_cap && blockIdx.x == 0 && tid == 0) atomicOr(p.err, kKv8ErrRange);
     const int n = max(0, min(len, p.T_cap)), kept = min(n, p.budget);
     const size_t head = (size_t)b * p.Hkv + g;
     const float *acc = p.acc + head * p.T_cap;
     int32_t *idx = p.idx + head * p.budget;
-    if (g == 0 && tid == 0) p.lens_out[b] = kept;
-    for (int i = kept + tid; i < p.budget; i += kSelThreads) idx[i] = -1;
+    float *dacc = p.dacc ? p.dacc + head * p.dT_cap : nullptr;
+    if (blockIdx.x == 0 && tid == 0) p.lens_out[b] = kept;
+    for (int i = kept + rank * kSelThreads + tid; i < p.budget; i += ctas * kSelThreads) idx[i] = -1;
     if (n <= p.budget) {
-        for (int i = tid; i < n; i += kSelThreads) {
+        for (int i = rank * kSelThreads + tid; i < n; i += ctas * kSelThreads) {
             idx[i] = i;
-            if (p.dacc) p.dacc[head * p.dT_cap + i] = acc[i];
+            if (dacc) dacc[i] = acc[i];
         }
         return;
     }
-    const int lo = p.sinks, hi = n - p.recent;          // candidates: positions lo .. hi - 1
-    int need = p.budget - p.sinks - p.recent;           // 0 <= need < hi - lo
-    uint32_t prefix = 0u;
-    for (int shift = 24; shift >= 0 && need > 0; shift -= 8) {
-        if (tid < 256) hist[tid] = 0u;
+    const int lo = p.sinks, hi = n - p.recent;                      // candidates: positions lo .. hi - 1
+    int need = p.budget - p.sinks - p.recent;                       // 0 <= need < hi - lo
+    const bool any = need > 0;
+    // this CTA's positions s0 .. s1 - 1, a warp's w0 .. w1 - 1
+    const int slice = ((n + ctas - 1) / ctas + 31) & ~31, s0 = min(rank * slice, n), s1 = min(s0 + slice, n);
+    const int part = ((slice + 31) / 32 + 31) & ~31, w0 = min(s0 + warp * part, s1), w1 = min(w0 + part, s1);
+    const bool local = slice <= kSelKeys;
+    if (local) {
+#pragma unroll 4
+        for (int t = s0 + tid; t < s1; t += kSelThreads) keys[t - s0] = weight_key(acc[t]);
+    }
+    auto key = [&](int t) { return local ? keys[t - s0] : weight_key(acc[t]); };
+    uint32_t prefix = 0u, mask = 0u;
+    const int c0 = max(lo, s0), c1 = min(hi, s1);
+    for (int pass = 0; pass < 3 && any; ++pass) {
+        const int bits = pass < 2 ? 11 : 10, shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+        int *h = hist + (pass & 1) * kSelBins;
+        for (int i = tid; i < kSelBins; i += kSelThreads) h[i] = 0;
         __syncthreads();
-        const uint32_t mask = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
-        for (int t = lo + tid; t < hi; t += kSelThreads) {
-            const uint32_t k = weight_key(acc[t]);
-            if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & 255u], 1u);
+#pragma unroll 4
+        for (int t = c0 + tid; t < c1; t += kSelThreads) {
+            const uint32_t k = key(t);
+            if ((k & mask) == prefix) atomicAdd(&h[(k >> shift) & ((1u << bits) - 1u)], 1);
         }
-        __syncthreads();
-        if (warp == 0) {
-            // digits from the largest down: the one in which the need-th largest lies
-            int before = 0;
-            for (int base = 248; base >= 0; base -= 8) {
-                int c = 0;
-                for (int i = 0; i < 8; ++i) c += (int)hist[base + i];
-                if (before + c >= need) {
-                    int dgt = base + 7;
-                    while (before + (int)hist[dgt] < need) before += (int)hist[dgt--];
-                    if (lane == 0) { sh_digit = dgt; sh_need = need - before; }
-                    break;
+        cluster_sync(ctas);
+        // bins from the largest down, two a thread: the one in which the need-th largest lies
+        int c[2] = {0, 0};
+        const int top = (1 << bits) - 1 - 2 * tid;
+        if (top >= 0) {
+            if (ctas == 1) {
+                c[0] = h[top];
+                c[1] = h[top - 1];
+            } else {
+                int v[kSelCtas][2];                                 // all on their way at once
+#pragma unroll
+                for (int r = 0; r < kSelCtas; ++r) {
+                    v[r][0] = r < ctas ? peer(h + top, r) : 0;
+                    v[r][1] = r < ctas ? peer(h + top - 1, r) : 0;
                 }
-                before += c;
+#pragma unroll
+                for (int r = 0; r < kSelCtas; ++r) {
+                    c[0] += v[r][0];
+                    c[1] += v[r][1];
+                }
             }
+        }
+        int before = c[0] + c[1];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xFFFFFFFFu, before, o);
+            if (lane >= o) before += u;
+        }
+        if (lane == 31) wsum[warp] = before;
+        __syncthreads();
+        {
+            int u = lane < warp ? wsum[lane] : 0;
+            u = __reduce_add_sync(0xFFFFFFFFu, u);
+            before += u - c[0] - c[1];
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (before < need && need <= before + c[i]) {
+                sh_digit = top - i;
+                sh_need = need - before;
+            }
+            before += c[i];
         }
         __syncthreads();
         prefix |= (uint32_t)sh_digit << shift;
+        mask |= ((1u << bits) - 1u) << shift;
         need = sh_need;
-        __syncthreads();
     }
+    if (!any) __syncthreads();
     // kept: sinks, recent, keys above `prefix`, and the first `need` equal to it
-    const bool any = p.budget > p.sinks + p.recent;
-    int done = 0, equals = 0;
-    for (int base = 0; base < n; base += kSelThreads) {
-        const int t = base + tid;
-        bool above = false, equal = false;
-        if (t < n) {
-            if (t < lo || t >= hi) above = true;
-            else if (any) {
-                const uint32_t k = weight_key(acc[t]);
-                above = k > prefix;
-                equal = k == prefix;
-            }
+    auto kind = [&](int t, bool &above, bool &equal) {
+        above = equal = false;
+        if (t >= w1) return;
+        if (t < lo || t >= hi) above = true;
+        else if (any) {
+            const uint32_t k = key(t);
+            above = k > prefix;
+            equal = k == prefix;
         }
-        const unsigned below = (1u << lane) - 1u;
-        const unsigned be = __ballot_sync(0xFFFFFFFFu, equal);
-        __syncthreads();
-        if (lane == 0) red[warp] = __popc(be);
-        __syncthreads();
-        int before = equals, total = 0;
-        for (int w = 0; w < 32; ++w) {
-            before += w < warp ? red[w] : 0;
-            total += red[w];
-        }
-        const bool keep = above || (equal && before + __popc(be & below) < need);
-        equals += total;
-        const unsigned bk = __ballot_sync(0xFFFFFFFFu, keep);
-        __syncthreads();
-        if (lane == 0) red[warp] = __popc(bk);
-        __syncthreads();
-        int at = done;
-        total = 0;
-        for (int w = 0; w < 32; ++w) {
-            at += w < warp ? red[w] : 0;
-            total += red[w];
-        }
-        if (keep) {
-            const int i = at + __popc(bk & below);
-            idx[i] = t;
-            if (p.dacc) p.dacc[head * p.dT_cap + i] = acc[t];
-        }
-        done += total;
+    };
+    int na = 0, ne = 0;
+#pragma unroll 4
+    for (int t = w0 + lane; t - lane < w1; t += 32) {
+        bool above, equal;
+        kind(t, above, equal);
+        na += __popc(__ballot_sync(0xFFFFFFFFu, above));
+        ne += __popc(__ballot_sync(0xFFFFFFFFu, equal));
     }
+    __syncthreads();                                                // wsum is read
+    if (lane == 0) {
+        wsum[warp] = na;
+        weq[warp] = ne;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        const int a = __reduce_add_sync(0xFFFFFFFFu, wsum[lane]), q = __reduce_add_sync(0xFFFFFFFFu, weq[lane]);
+        if (lane == 0) {
+            total[0] = a;
+            total[1] = q;
+        }
+    }
+    cluster_sync(ctas);
+    int a0 = 0, e0 = 0;                                             // above and equal before this warp's part
+    if (lane < rank) {
+        a0 = peer(&total[0], lane);
+        e0 = peer(&total[1], lane);
+    }
+    if (lane < warp) {
+        a0 += wsum[lane];
+        e0 += weq[lane];
+    }
+    a0 = __reduce_add_sync(0xFFFFFFFFu, a0);
+    e0 = __reduce_add_sync(0xFFFFFFFFu, e0);
+    for (int t = w0 + lane; t - lane < w1; t += 32) {
+        bool above, equal;
+        kind(t, above, equal);
+        const unsigned below = (1u << lane) - 1u, be = __ballot_sync(0xFFFFFFFFu, equal), ba = __ballot_sync(0xFFFFFFFFu, above);
+        const int le = e0 + __popc(be & below);
+        if (above || (equal && le < need)) {
+            const int i = a0 + __popc(ba & below) + min(le, need);
+            idx[i] = t;
+            if (dacc) dacc[i] = acc[t];
+        }
+        a0 += __popc(ba);
+        e0 += __popc(be);
+    }
+    cluster_sync(ctas);                                             // nobody leaves while its words are read
 }
 
-// Moving: one CTA per (destination block, head and tensor, sequence).  The
-// block's step is the smallest that holds its values; a code whose own step
-// was smaller is rounded to it, one whose step was larger is exact.
-constexpr int kMoveThreads = 256;
-
+// Moving: a destination block's step is the smallest that holds its values; a
+// code whose own step was smaller is rounded to it, one whose step was larger
+// is exact.
 template <int FMT>
-__global__ void __launch_bounds__(kMoveThreads) kv8_move_kernel(const EvictParams p)
+__global__ void __launch_bounds__(512) kv8_move_kernel(const EvictParams p)
 {
-    __shared__ float red[33];
-    const int j = blockIdx.x, g = blockIdx.y >> 1, which = blockIdx.y & 1, b = blockIdx.z;
-    const int kept = p.lens_out[b], i0 = j * p.blk, i1 = min(i0 + p.blk, kept);
-    if (i0 >= kept) return;
+    __shared__ float red[16];
+    const int g = blockIdx.y >> 1, which = blockIdx.y & 1, b = blockIdx.z;
+    const Place q = place_of(p.blk, p.D);
+    const int kept = p.lens_out[b], j = blockIdx.x * (blockDim.x / q.threads) + q.j, i0 = j * p.blk;
+    if ((int)(blockIdx.x * (blockDim.x / q.threads)) * p.blk >= kept) return;
     const size_t head = (size_t)b * p.Hkv + g;
-    const int lanes = p.D / 8, r0 = threadIdx.x / lanes, d = threadIdx.x % lanes * 8, dr = kMoveThreads / lanes;
-    const uint8_t *src = p.codes[which] + head * p.T_cap * p.D + d;
+    const uint8_t *src = p.codes[which] + head * p.T_cap * p.D + q.d;
     const float *scale = p.scale[which] + head * p.nblk;
     const int32_t *idx = p.idx + head * p.budget;
-    float amax = 0.f;
-    for (int i = i0 + r0; i < i1; i += dr) {
-        const int t = idx[i];
-        amax = fmaxf(amax, amax8<FMT>(__ldg(reinterpret_cast<const uint2 *>(src + (size_t)t * p.D))) * scale[t >> p.blk_log]);
+    uint2 w[8];
+    float s[8], amax = 0.f;
+    int t[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int at = i0 + q.row + i * (p.blk >> 3);
+        t[i] = at < kept ? idx[at] : -1;
     }
-    amax = cta_max(amax, red);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        w[i] = make_uint2(0u, 0u);
+        s[i] = 0.f;
+        if (t[i] >= 0) {
+            w[i] = __ldg(reinterpret_cast<const uint2 *>(src + (size_t)t[i] * p.D));
+            s[i] = __ldg(scale + (t[i] >> p.blk_log));
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, amax8<FMT>(w[i]) * s[i]);
+    amax = place_max(amax, q, red);
+    if (i0 >= kept) return;
     const int e = step_exp<FMT>(amax);
     const float inv = pow2f(-e);
-    if (threadIdx.x == 0) p.dscale[which][head * p.dnblk + j] = pow2f(e);
-    uint8_t *dst = p.dcodes[which] + head * p.dT_cap * p.D + d;
-    for (int i = i0 + r0; i < i1; i += dr) {
-        const int t = idx[i];
-        const float s = scale[t >> p.blk_log];
-        // values, then units of the new step: the product of the two powers
-        // could leave fp32's range, each factor alone cannot
-        float a[4], c[4];
-        const uint2 w = __ldg(reinterpret_cast<const uint2 *>(src + (size_t)t * p.D));
-        decode4<FMT>(w.x, a);
-        decode4<FMT>(w.y, c);
+    if (q.row == 0 && q.d == 0) p.dscale[which][head * p.dnblk + j] = pow2f(e);
+    uint8_t *dst = p.dcodes[which] + head * p.dT_cap * p.D + q.d;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            a[k] = a[k] * s * inv;
-            c[k] = c[k] * s * inv;
-        }
-        *reinterpret_cast<uint2 *>(dst + (size_t)i * p.D) =
-            make_uint2(encode4<FMT>(a[0], a[1], a[2], a[3]), encode4<FMT>(c[0], c[1], c[2], c[3]));
+    for (int i = 0; i < 8; ++i) {
+        if (t[i] < 0) continue;
+        // no more than 2^17, see recode4; a row of zeros may have any step
+        const float ratio = fminf(s[i] * inv, 131072.f);
+        *reinterpret_cast<uint2 *>(dst + (size_t)(i0 + q.row + i * (p.blk >> 3)) * p.D) =
+            ratio == 1.f ? w[i] : recode8<FMT>(w[i], ratio);
     }
 }
 
@@ -388,8 +525,9 @@ int launch_kv8_append(const moe_kv8 &c, const moe_rows &k_new, const moe_rows &v
     p.T_cap = c.T_cap;
     p.blk = c.block;
     p.nblk = c.T_cap / c.block;
-    const dim3 grid(min((M - 1) / c.block + 2, p.nblk), 2 * c.kv_heads, c.batch);
-    auto go = [&](auto kernel) { kernel<<<grid, kAppThreads, 0, stream>>>(p); };
+    const int per = place_blocks(c.block, c.head_dim), threads = place_threads(c.block, c.head_dim);
+    const dim3 grid((min((M - 1) / c.block + 2, p.nblk) + per - 1) / per, 2 * c.kv_heads, c.batch);
+    auto go = [&](auto kernel) { kernel<<<grid, threads, 0, stream>>>(p); };
     if (c.format == MOE_KV8_INT8) {
         if (type == MOE_BF16) go(kv8_append_kernel<MOE_KV8_INT8, MOE_BF16>);
         else if (type == MOE_F16) go(kv8_append_kernel<MOE_KV8_INT8, MOE_F16>);
@@ -458,11 +596,37 @@ int launch_kv8_evict(const moe_kv8 &c, const moe_kv8 &d, const int32_t *lens, co
     p.budget = budget;
     p.sinks = sinks;
     p.recent = recent;
-    kv8_select_kernel<<<dim3(c.kv_heads, c.batch), kSelThreads, 0, stream>>>(p);
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || dev < 0 || dev >= 64) { note_cuda_error((int)e); return MOE_ERR_CUDA; }
+    // CTAs per head: as many as slices of 4K positions of a full cache
+    int ctas = 1;
+    while (ctas < kSelCtas && c.T_cap > 4096 * ctas) ctas *= 2;
+    const int smem = (2 * kSelBins + kSelKeys) * (int)sizeof(uint32_t);
+    static std::once_flag once[64];
+    std::call_once(once[dev], [&] {
+        e = cudaFuncSetAttribute((const void *)kv8_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    });
+    if (e == cudaSuccess) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(ctas * c.kv_heads, c.batch);
+        cfg.blockDim = dim3(kSelThreads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = stream;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = ctas;
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        e = cudaLaunchKernelEx(&cfg, kv8_select_kernel, p, ctas);
+    }
+    if (e != cudaSuccess) { note_cuda_error((int)e); return MOE_ERR_CUDA; }
     note_launch();
-    const dim3 grid((budget + c.block - 1) / c.block, 2 * c.kv_heads, c.batch);
-    if (c.format == MOE_KV8_INT8) kv8_move_kernel<MOE_KV8_INT8><<<grid, kMoveThreads, 0, stream>>>(p);
-    else kv8_move_kernel<MOE_KV8_E4M3><<<grid, kMoveThreads, 0, stream>>>(p);
+    const int per = place_blocks(c.block, c.head_dim), threads = place_threads(c.block, c.head_dim);
+    const dim3 grid(((budget + c.block - 1) / c.block + per - 1) / per, 2 * c.kv_heads, c.batch);
+    if (c.format == MOE_KV8_INT8) kv8_move_kernel<MOE_KV8_INT8><<<grid, threads, 0, stream>>>(p);
+    else kv8_move_kernel<MOE_KV8_E4M3><<<grid, threads, 0, stream>>>(p);
     note_launch();
     return launched();
 }

@@ -55,14 +55,15 @@ __device__ __forceinline__ int step_exp(float a)
     return max(e, kKv8MinExp);
 }
 
-// Four values in units of the step to four codes (bytes 0 .. 3), nearest, ties to even.
+// Four values in units of the step (at most 127.5 or 448 of them) to four
+// codes (bytes 0 .. 3), nearest, ties to even.  int8: adding 1.5 2^23 leaves
+// the rounded value in the low mantissa bits.
 template <int FMT>
 __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d)
 {
     if (FMT == MOE_KV8_INT8) {
-        const int ia = max(-127, min(127, __float2int_rn(a))), ib = max(-127, min(127, __float2int_rn(b)));
-        const int ic = max(-127, min(127, __float2int_rn(c))), id = max(-127, min(127, __float2int_rn(d)));
-        return __byte_perm(__byte_perm((uint32_t)ia, (uint32_t)ib, 0x0040), __byte_perm((uint32_t)ic, (uint32_t)id, 0x0040), 0x5410);
+        auto r = [](float x) { return __float_as_uint(__fadd_rn(fminf(fmaxf(x, -127.f), 127.f), 12582912.f)); };
+        return __byte_perm(__byte_perm(r(a), r(b), 0x0040), __byte_perm(r(c), r(d), 0x0040), 0x5410);
     }
     uint16_t lo, hi;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
@@ -70,44 +71,77 @@ __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d)
     return (uint32_t)lo | ((uint32_t)hi << 16);
 }
 
-// Four codes to four values in units of the step (exact in fp16).
+// Codes to fp16 pairs, exactly.  pairs(w): (byte 0, byte 2) and (byte 1, byte
+// 3) for int8 -- fp16 0x6400 | u is 1024 + u, so flipping a code's top bit
+// gives 1024 + 128 + code, and one subtraction is exact --, (0, 1) and (2, 3)
+// for e4m3.
 template <int FMT>
-__device__ __forceinline__ void decode4(uint32_t w, float (&v)[4])
+__device__ __forceinline__ void pairs(uint32_t w, uint32_t &x, uint32_t &y)
 {
     if (FMT == MOE_KV8_INT8) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = (float)(int8_t)(w >> (8 * i));
+        const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
+        uint32_t a, b;                                // (w & mask) ^ flip
+        asm("lop3.b32 %0, %1, 0x00FF00FF, %2, 0x6A;" : "=r"(a) : "r"(w), "r"(0x64806480u));
+        asm("lop3.b32 %0, %1, 0x00FF00FF, %2, 0x6A;" : "=r"(b) : "r"(w >> 8), "r"(0x64806480u));
+        const __half2 ha = __hsub2(*reinterpret_cast<const __half2 *>(&a), off), hb = __hsub2(*reinterpret_cast<const __half2 *>(&b), off);
+        x = *reinterpret_cast<const uint32_t *>(&ha);
+        y = *reinterpret_cast<const uint32_t *>(&hb);
     } else {
-        uint32_t lo, hi;
         asm("{ .reg .b16 l, h; mov.b32 {l, h}, %2; cvt.rn.f16x2.e4m3x2 %0, l; cvt.rn.f16x2.e4m3x2 %1, h; }"
-            : "=r"(lo), "=r"(hi) : "r"(w));
-        const float2 a = __half22float2(*reinterpret_cast<__half2 *>(&lo)), b = __half22float2(*reinterpret_cast<__half2 *>(&hi));
-        v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
+            : "=r"(x), "=r"(y) : "r"(w));
     }
 }
 
-// 8 codes in units of one step to a larger one: down = 2^(e_old - e_new).
+__device__ __forceinline__ __half2 as_half2(uint32_t w) { return *reinterpret_cast<const __half2 *>(&w); }
+
+// Four codes to four values in units of the step.
 template <int FMT>
-__device__ __forceinline__ uint2 recode8(uint2 w, float down)
+__device__ __forceinline__ void decode4(uint32_t w, float (&v)[4])
 {
-    float a[4], b[4];
-    decode4<FMT>(w.x, a);
-    decode4<FMT>(w.y, b);
-    return make_uint2(encode4<FMT>(a[0] * down, a[1] * down, a[2] * down, a[3] * down),
-                      encode4<FMT>(b[0] * down, b[1] * down, b[2] * down, b[3] * down));
+    uint32_t x, y;
+    pairs<FMT>(w, x, y);
+    const float2 a = __half22float2(as_half2(x)), b = __half22float2(as_half2(y));
+    v[0] = a.x;
+    v[1] = FMT == MOE_KV8_INT8 ? b.x : a.y;
+    v[2] = FMT == MOE_KV8_INT8 ? a.y : b.x;
+    v[3] = b.y;
+}
+
+// 4 codes in units of one step to units of another: times ratio, a power of
+// two of at most 2^17 (that many times, no code of such a block can be
+// larger: the new step holds the block's largest).
+template <int FMT>
+__device__ __forceinline__ uint32_t recode4(uint32_t w, float ratio)
+{
+    if (FMT == MOE_KV8_INT8) {
+        // in fp16: code * ratio + 1536 is rounded once, to the integer in its
+        // low byte; below 2^-14 every code rounds to 0 as it does at 2^-14,
+        // and above 2^7 there are only zeros
+        const __half2 r = __float2half2_rn(fminf(fmaxf(ratio, 6.103515625e-05f), 128.f)), magic = __float2half2_rn(1536.f);
+        uint32_t x, y;
+        pairs<FMT>(w, x, y);
+        const __half2 a = __hfma2(as_half2(x), r, magic), b = __hfma2(as_half2(y), r, magic);
+        return __byte_perm(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b), 0x6240);
+    }
+    float v[4];
+    decode4<FMT>(w, v);
+    return encode4<FMT>(v[0] * ratio, v[1] * ratio, v[2] * ratio, v[3] * ratio);
+}
+template <int FMT>
+__device__ __forceinline__ uint2 recode8(uint2 w, float ratio)
+{
+    return make_uint2(recode4<FMT>(w.x, ratio), recode4<FMT>(w.y, ratio));
 }
 
 // Largest magnitude of 8 codes, in units of their step.
 template <int FMT>
 __device__ __forceinline__ float amax8(uint2 w)
 {
-    float a[4], b[4];
-    decode4<FMT>(w.x, a);
-    decode4<FMT>(w.y, b);
-    float m = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) m = fmaxf(m, fmaxf(fabsf(a[i]), fabsf(b[i])));
-    return m;
+    uint32_t a, b, c, d;
+    pairs<FMT>(w.x, a, b);
+    pairs<FMT>(w.y, c, d);
+    const __half2 m = __hmax2(__hmax2(__habs2(as_half2(a)), __habs2(as_half2(b))), __hmax2(__habs2(as_half2(c)), __habs2(as_half2(d))));
+    return fmaxf(__low2float(m), __high2float(m));
 }
 
 __device__ __forceinline__ float warp_max(float v)

@@ -126,26 +126,6 @@ __device__ __forceinline__ uint32_t movtrans(uint32_t a)
     return d;
 }
 
-// Codes to fp16 pairs.  pairs(w): (byte 0, byte 2) and (byte 1, byte 3) for
-// int8 -- fp16 0x6400 | u is 1024 + u, so flipping a code's top bit gives
-// 1024 + 128 + code, and one subtraction is exact --, (0, 1) and (2, 3) for
-// e4m3.  Dimension order does not matter as long as queries follow it.
-template <int FMT>
-__device__ __forceinline__ void pairs(uint32_t w, uint32_t &x, uint32_t &y)
-{
-    if (FMT == MOE_KV8_INT8) {
-        const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
-        uint32_t a, b;                                // (w & mask) ^ flip
-        asm("lop3.b32 %0, %1, 0x00FF00FF, %2, 0x6A;" : "=r"(a) : "r"(w), "r"(0x64806480u));
-        asm("lop3.b32 %0, %1, 0x00FF00FF, %2, 0x6A;" : "=r"(b) : "r"(w >> 8), "r"(0x64806480u));
-        const __half2 ha = __hsub2(*reinterpret_cast<const __half2 *>(&a), off), hb = __hsub2(*reinterpret_cast<const __half2 *>(&b), off);
-        x = *reinterpret_cast<const uint32_t *>(&ha);
-        y = *reinterpret_cast<const uint32_t *>(&hb);
-    } else {
-        asm("{ .reg .b16 l, h; mov.b32 {l, h}, %2; cvt.rn.f16x2.e4m3x2 %0, l; cvt.rn.f16x2.e4m3x2 %1, h; }"
-            : "=r"(x), "=r"(y) : "r"(w));
-    }
-}
 // Two rows' words: fp16 pairs (row 0, row 1) of dimensions 0 .. 3.
 template <int FMT>
 __device__ __forceinline__ void cross(uint32_t r0, uint32_t r1, uint32_t (&d)[4])

@@ -560,3 +560,25 @@ def test_binding_refusals():
         with pytest.raises(moe.MoeError):
             bad()
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_evict_far_apart_steps_and_zeros(fmt):
+    """Blocks whose steps are as far apart as fp32 allows, rows of zeros under a
+    large step beside small values, the smallest codes alone in a block."""
+    cache, r = filled(1, 2, 2, 64, 256, 16, fmt, [256], 28)
+    k = torch.zeros((1, 256, 2, 64), device=DEV)
+    k[0, :16] = rows(r, 16, 2, 64, dtype=torch.float32) * 2.0 ** 110
+    k[0, 3:16:2] = 0.0
+    k[0, 16:32] = rows(r, 16, 2, 64, dtype=torch.float32) * 2.0 ** -119
+    k[0, 32] = 1.0
+    k[0, 33:48, :, ::7] = 1.0 / 512
+    k[0, 48:64] = rows(r, 16, 2, 64, dtype=torch.float32) * 1e-3
+    k[0, 64:] = rows(r, 192, 2, 64, dtype=torch.float32)
+    cache.append(k, k * 2.0 ** -3, i32([0]))
+    acc = torch.rand((1, 2, 256), generator=r, device=DEV)
+    acc[0, 0, 3:16:2] += 2.0
+    acc[0, 0, 16:32] += 1.0
+    acc[0, 1, 33:64] += 2.0
+    check_evict(cache, [256], acc, 40, 0, 0)
+    check_evict(cache, [256], 3 - acc, 100, 2, 5)
