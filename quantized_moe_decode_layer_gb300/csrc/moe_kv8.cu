@@ -232,13 +232,15 @@ __global__ void __launch_bounds__(256) kv8_read_kernel(const ReadParams p)
 // Selection: a cluster of 1 to 8 CTAs per (sequence, head), a slice of the
 // positions each.  Of n > budget positions the first `sinks` and last `recent`
 // stay, and the rest are ranked by weight (larger first, then the lower
-// position).  A radix select over 32-bit keys (11, 11 and 10 bits, the slices'
-// histograms added up through distributed shared memory) finds the weight of
-// the last one that stays and how many of its equals do; then every warp
-// counts what its part keeps, and writes it behind what the parts before it
-// do.  Bound by latency: three passes over keys in shared memory (in L2 where
-// a slice has more than 16K), a cluster barrier each.
-constexpr int kSelThreads = 1024, kSelKeys = 16384, kSelBins = 2048, kSelCtas = 8;
+// position).  A radix select over 32-bit keys, 8 bits at a time, finds the
+// weight of the last one that stays and how many of its equals do; then every
+// warp counts what its part keeps, and writes it behind what the parts before
+// it do.  Bound by latency: four passes over keys in shared memory (in L2 where
+// a slice has more than 16K), a cluster barrier each, the slices' 256 counts
+// added up through distributed shared memory (2048 counts, in three passes,
+// took 25 us where these take fewer).  Weights share few exponents, so a
+// CTA counts in 8 copies, a lane in its own.
+constexpr int kSelThreads = 1024, kSelKeys = 16384, kSelBins = 256, kSelCopies = 8, kSelCtas = 8, kSelSlice = 4096;
 
 struct EvictParams {
     const uint8_t *codes[2];
@@ -279,9 +281,9 @@ __device__ __forceinline__ int peer(const int *p, int rank)
 __global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(const EvictParams p, int ctas)
 {
     extern __shared__ uint32_t sel[];
-    int *hist = reinterpret_cast<int *>(sel);                       // [2][bins]: the passes take turns
-    uint32_t *keys = sel + 2 * kSelBins;                            // [kSelKeys]
-    __shared__ int wsum[32], weq[32], total[2], sh_digit, sh_need;
+    int *copies = reinterpret_cast<int *>(sel);                     // [bins][copies]
+    float *weights = reinterpret_cast<float *>(sel + kSelBins * kSelCopies);   // [kSelKeys]: this slice's
+    __shared__ int hist[2][kSelBins], wsum[32], weq[32], total[2], sh_digit, sh_need;   // hist: the passes take turns
     const int rank = blockIdx.x % ctas, g = blockIdx.x / ctas, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int len = p.lens[b];
     if (len > p.T_cap && blockIdx.x == 0 && tid == 0) atomicOr(p.err, kKv8ErrRange);
@@ -308,67 +310,60 @@ __global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(const EvictPara
     const bool local = slice <= kSelKeys;
     if (local) {
 #pragma unroll 4
-        for (int t = s0 + tid; t < s1; t += kSelThreads) keys[t - s0] = weight_key(acc[t]);
+        for (int t = s0 + tid; t < s1; t += kSelThreads) weights[t - s0] = acc[t];
     }
-    auto key = [&](int t) { return local ? keys[t - s0] : weight_key(acc[t]); };
+    auto weight = [&](int t) { return local ? weights[t - s0] : acc[t]; };
+    auto key = [&](int t) { return weight_key(weight(t)); };
     uint32_t prefix = 0u, mask = 0u;
     const int c0 = max(lo, s0), c1 = min(hi, s1);
-    for (int pass = 0; pass < 3 && any; ++pass) {
-        const int bits = pass < 2 ? 11 : 10, shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-        int *h = hist + (pass & 1) * kSelBins;
-        for (int i = tid; i < kSelBins; i += kSelThreads) h[i] = 0;
+    for (int pass = 0; pass < 4 && any; ++pass) {
+        const int shift = 24 - 8 * pass;
+        int *h = hist[pass & 1];
+        for (int i = tid; i < kSelBins * kSelCopies; i += kSelThreads) copies[i] = 0;
         __syncthreads();
 #pragma unroll 4
         for (int t = c0 + tid; t < c1; t += kSelThreads) {
             const uint32_t k = key(t);
-            if ((k & mask) == prefix) atomicAdd(&h[(k >> shift) & ((1u << bits) - 1u)], 1);
+            if ((k & mask) == prefix) atomicAdd(&copies[((k >> shift) & 255u) * kSelCopies + (lane & (kSelCopies - 1))], 1);
+        }
+        __syncthreads();
+        const int bin = 255 - tid;                                  // from the largest down
+        if (tid < kSelBins) {
+            const int4 u = reinterpret_cast<const int4 *>(copies)[2 * bin], v = reinterpret_cast<const int4 *>(copies)[2 * bin + 1];
+            h[bin] = u.x + u.y + u.z + u.w + v.x + v.y + v.z + v.w;
         }
         cluster_sync(ctas);
-        // bins from the largest down, two a thread: the one in which the need-th largest lies
-        int c[2] = {0, 0};
-        const int top = (1 << bits) - 1 - 2 * tid;
-        if (top >= 0) {
-            if (ctas == 1) {
-                c[0] = h[top];
-                c[1] = h[top - 1];
-            } else {
-                int v[kSelCtas][2];                                 // all on their way at once
+        // the bin in which the need-th largest lies
+        int c = 0, before = 0;
+        if (tid < kSelBins) {
+            if (ctas == 1) c = h[bin];
+            else {
+                int v[kSelCtas];                                    // all on their way at once
 #pragma unroll
-                for (int r = 0; r < kSelCtas; ++r) {
-                    v[r][0] = r < ctas ? peer(h + top, r) : 0;
-                    v[r][1] = r < ctas ? peer(h + top - 1, r) : 0;
-                }
+                for (int r = 0; r < kSelCtas; ++r) v[r] = r < ctas ? peer(h + bin, r) : 0;
 #pragma unroll
-                for (int r = 0; r < kSelCtas; ++r) {
-                    c[0] += v[r][0];
-                    c[1] += v[r][1];
-                }
+                for (int r = 0; r < kSelCtas; ++r) c += v[r];
             }
-        }
-        int before = c[0] + c[1];
+            before = c;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_up_sync(0xFFFFFFFFu, before, o);
-            if (lane >= o) before += u;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u = __shfl_up_sync(0xFFFFFFFFu, before, o);
+                if (lane >= o) before += u;
+            }
+            if (lane == 31) wsum[warp] = before;
         }
-        if (lane == 31) wsum[warp] = before;
         __syncthreads();
-        {
-            int u = lane < warp ? wsum[lane] : 0;
-            u = __reduce_add_sync(0xFFFFFFFFu, u);
-            before += u - c[0] - c[1];
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            if (before < need && need <= before + c[i]) {
-                sh_digit = top - i;
+        if (tid < kSelBins) {
+            for (int w = 0; w < warp; ++w) before += wsum[w];
+            before -= c;
+            if (before < need && need <= before + c) {
+                sh_digit = bin;
                 sh_need = need - before;
             }
-            before += c[i];
         }
         __syncthreads();
         prefix |= (uint32_t)sh_digit << shift;
-        mask |= ((1u << bits) - 1u) << shift;
+        mask |= 255u << shift;
         need = sh_need;
     }
     if (!any) __syncthreads();
@@ -416,6 +411,7 @@ __global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(const EvictPara
     }
     a0 = __reduce_add_sync(0xFFFFFFFFu, a0);
     e0 = __reduce_add_sync(0xFFFFFFFFu, e0);
+#pragma unroll 4
     for (int t = w0 + lane; t - lane < w1; t += 32) {
         bool above, equal;
         kind(t, above, equal);
@@ -424,7 +420,7 @@ __global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(const EvictPara
         if (above || (equal && le < need)) {
             const int i = a0 + __popc(ba & below) + min(le, need);
             idx[i] = t;
-            if (dacc) dacc[i] = acc[t];
+            if (dacc) dacc[i] = weight(t);
         }
         a0 += __popc(ba);
         e0 += __popc(be);
@@ -599,10 +595,11 @@ int launch_kv8_evict(const moe_kv8 &c, const moe_kv8 &d, const int32_t *lens, co
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess || dev < 0 || dev >= 64) { note_cuda_error((int)e); return MOE_ERR_CUDA; }
-    // CTAs per head: as many as slices of 4K positions of a full cache
+    // CTAs per head: as many as slices of 4K positions of a full cache (8 heads of
+    // 32K: 1, 2, 4, 8 CTAs take 33, 22, 16, 14 us; one of 2K in two slices 10 for 8)
     int ctas = 1;
-    while (ctas < kSelCtas && c.T_cap > 4096 * ctas) ctas *= 2;
-    const int smem = (2 * kSelBins + kSelKeys) * (int)sizeof(uint32_t);
+    while (ctas < kSelCtas && c.T_cap > kSelSlice * ctas) ctas *= 2;
+    const int smem = (kSelBins * kSelCopies + kSelKeys) * (int)sizeof(uint32_t);
     static std::once_flag once[64];
     std::call_once(once[dev], [&] {
         e = cudaFuncSetAttribute((const void *)kv8_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
