@@ -21,6 +21,24 @@
 namespace moe {
 namespace {
 
+// n / d for n < 2^31 by a product: m = 2^32 (2^s - d) / d + 1 rounded down, s = log2 d rounded up.
+struct Div {
+    unsigned d, m, s;
+    __device__ __forceinline__ int by(int &n) const   // n becomes the remainder
+    {
+        const unsigned q = (__umulhi((unsigned)n, m) + (unsigned)n) >> s;
+        n -= (int)(q * d);
+        return (int)q;
+    }
+};
+Div div_of(unsigned d)
+{
+    Div v = {d, 0u, 0u};
+    while ((1ull << v.s) < d) ++v.s;
+    v.m = (unsigned)((((1ull << v.s) - d) << 32) / d + 1);
+    return v;
+}
+
 struct AttnP {
     const void *q;
     long long qb, qm, qh;           // strides in elements: sequence, row, head
@@ -33,6 +51,7 @@ struct AttnP {
     float *acc;
     float decay, scale_log2;        // scale * log2(e)
     int *err, *counter;                   // counter: items taken beyond the first of each CTA, or NULL (in turn)
+    Div by_pass, by_head, by_group;       // column passes, key/value heads, G
     int B, Hq, Hkv, G, M, C, T_cap, chunk, nchunk, blk_log, nblk, f16, qvec, o_type;
 };
 
@@ -144,13 +163,13 @@ struct Item {
     int b, g, cp, k0, k1, p0, rows;    // positions k0 .. k1 - 1
 };
 
-__device__ __forceinline__ Item decode_item(const AttnP &p, const int *first, int item, int passes)
+__device__ __forceinline__ Item decode_item(const AttnP &p, const int *first, int item)
 {
     Item it;
-    it.cp = item % passes;
-    item /= passes;
-    it.g = item % p.Hkv;
-    item /= p.Hkv;
+    it.cp = item;
+    item = p.by_pass.by(it.cp);
+    it.g = item;
+    item = p.by_head.by(it.g);
     int lo = 0, hi = p.B;              // first[lo] <= item < first[hi]
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -172,23 +191,24 @@ __device__ __forceinline__ Item decode_item(const AttnP &p, const int *first, in
 template <int FMT, int D>
 __device__ __forceinline__ float load_q(const AttnP &p, const Item &it, int c, int tq, uint32_t (&b)[D / 16][2])
 {
-    const int m = c / p.G;
+    int h = c;
+    const int m = p.by_group.by(h);
     const bool in = c < p.C && m < it.rows;
-    const uint16_t *src = static_cast<const uint16_t *>(p.q) + it.b * p.qb + m * p.qm + (it.g * p.G + c % p.G) * p.qh + 16 * tq;
-    uint16_t h[D / 64][16];
+    const uint16_t *src = static_cast<const uint16_t *>(p.q) + it.b * p.qb + m * p.qm + (it.g * p.G + h) * p.qh + 16 * tq;
+    uint16_t raw[D / 64][16];
 #pragma unroll
     for (int i = 0; i < D / 64; ++i) {
         if (p.qvec) {
             const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-            *reinterpret_cast<uint4 *>(h[i]) = in ? __ldg(reinterpret_cast<const uint4 *>(src + 64 * i)) : zero;
-            *reinterpret_cast<uint4 *>(h[i] + 8) = in ? __ldg(reinterpret_cast<const uint4 *>(src + 64 * i + 8)) : zero;
+            *reinterpret_cast<uint4 *>(raw[i]) = in ? __ldg(reinterpret_cast<const uint4 *>(src + 64 * i)) : zero;
+            *reinterpret_cast<uint4 *>(raw[i] + 8) = in ? __ldg(reinterpret_cast<const uint4 *>(src + 64 * i + 8)) : zero;
         } else {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) h[i][j] = in ? __ldg(src + 64 * i + j) : (uint16_t)0;
+            for (int j = 0; j < 16; ++j) raw[i][j] = in ? __ldg(src + 64 * i + j) : (uint16_t)0;
         }
     }
     auto value = [&](int i, int j) {
-        return p.f16 ? __half2float(__ushort_as_half(h[i][j])) : __uint_as_float((uint32_t)h[i][j] << 16);
+        return p.f16 ? __half2float(__ushort_as_half(raw[i][j])) : __uint_as_float((uint32_t)raw[i][j] << 16);
     };
     float a = 0.f;
 #pragma unroll
@@ -256,6 +276,7 @@ __global__ void __launch_bounds__(kThreads, Lay<D, NT>::ctas) kv8_chunk_kernel(c
     const int total = first[p.B] * p.Hkv * passes;
     if ((int)blockIdx.x >= total) return;
 
+    asm volatile("griddepcontrol.launch_dependents;");               // the merge may start, and waits for the results
     uint8_t *ring = sm + L::ring + warp * kStages * kStageBytes;
     const uint32_t ring_u = smem_u32(ring);
 
@@ -273,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, Lay<D, NT>::ctas) kv8_chunk_kernel(c
     const uint8_t *ld_k = nullptr, *ld_v = nullptr;
     const float *ld_s = nullptr;
     auto open_item = [&]() {
-        const Item x = decode_item(p, first, ld_item, passes);
+        const Item x = decode_item(p, first, ld_item);
         const size_t head = (size_t)x.b * p.Hkv + x.g;
         ld_t = x.k0 + warp * TK;
         ld_k1 = x.k1;
@@ -335,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, Lay<D, NT>::ctas) kv8_chunk_kernel(c
             if (tq == 0) qf[8 * warp + gq] = back;
         }
     };
-    Item it = decode_item(p, first, blockIdx.x, passes);
+    Item it = decode_item(p, first, blockIdx.x);
     if (L::wide) {
         stage_q(it);
         __syncthreads();
@@ -350,6 +371,18 @@ __global__ void __launch_bounds__(kThreads, Lay<D, NT>::ctas) kv8_chunk_kernel(c
 #pragma unroll 1
     for (;;) {
         int after = 0;                 // the item after next
+        if (!L::wide && warp == kWarps - 1 && seq[(nth + 1) & 3] < total) {
+            // the next item's queries into L1: 128-byte lines of its columns
+            const Item x = decode_item(p, first, seq[(nth + 1) & 3]);
+            for (int i = lane; i < NC * D / 64; i += 32) {
+                int h = x.cp * NC + i / (D / 64);
+                const bool in = h < p.C;
+                const int m = p.by_group.by(h);
+                if (in)
+                    asm volatile("prefetch.global.L1 [%0];" ::"l"(static_cast<const uint16_t *>(p.q) + x.b * p.qb + m * p.qm +
+                                                                  (x.g * p.G + h) * p.qh + i % (D / 64) * 64));
+            }
+        }
         if (tid == 0) after = p.counter ? gridDim.x + atomicAdd(p.counter, 1) : seq[(nth + 1) & 3] + gridDim.x;
         float f[NT][2], m[NT][2], l[NT][2], o[NT][KS][4], vref = 0.f, inv_vref = 0.f;
         bool fresh = true;             // no tile yet: m = -inf, everything else 0
@@ -423,9 +456,15 @@ __global__ void __launch_bounds__(kThreads, Lay<D, NT>::ctas) kv8_chunk_kernel(c
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            const int row = 16 * r + gq + 8 * (c >> 1), col = 8 * n + 2 * tq + (c & 1);
-                            if (t0 + row < it.k1 && it.cp * NC + col < p.C) sc[(size_t)row * p.C + col] = s[r][n][c];
+                        for (int c = 0; c < 4; c += 2) {
+                            const int row = 16 * r + gq + 4 * c, col = 8 * n + 2 * tq;
+                            if (t0 + row >= it.k1 || it.cp * NC + col >= p.C) continue;
+                            float *dst = sc + (size_t)row * p.C + col;
+                            if (!(p.C & 1)) *reinterpret_cast<float2 *>(dst) = make_float2(s[r][n][c], s[r][n][c + 1]);
+                            else {
+                                dst[0] = s[r][n][c];
+                                if (it.cp * NC + col + 1 < p.C) dst[1] = s[r][n][c + 1];
+                            }
                         }
             }
             // ---- positions that a row does not see (the call's own rows, and the end)
@@ -434,7 +473,8 @@ __global__ void __launch_bounds__(kThreads, Lay<D, NT>::ctas) kv8_chunk_kernel(c
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        const int see = min(it.p0 + 1 + (it.cp * NC + 8 * n + 2 * tq + c) / p.G, it.k1);
+                        int col = it.cp * NC + 8 * n + 2 * tq + c;
+                        const int see = min(it.p0 + 1 + p.by_group.by(col), it.k1);
 #pragma unroll
                         for (int r = 0; r < R; ++r) {
                             if (t0 + 16 * r + gq >= see) s[r][n][c] = -INFINITY;
@@ -585,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, Lay<D, NT>::ctas) kv8_chunk_kernel(c
             __syncthreads();
             if (L::wide && h == 0) {                               // every warp is done with the queries
                 const int ni = seq[(nth + 1) & 3];
-                if (ni < total) stage_q(decode_item(p, first, ni, passes));
+                if (ni < total) stage_q(decode_item(p, first, ni));
             }
             constexpr int kShare = kRound / kWarps;                // m-tiles a warp adds up, of one column tile
             const int x0 = h * kRound + warp * kShare, n = x0 / KS;
@@ -634,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, Lay<D, NT>::ctas) kv8_chunk_kernel(c
         }
         const int ni = seq[++nth & 3];
         if (ni >= total) break;
-        it = decode_item(p, first, ni, passes);
+        it = decode_item(p, first, ni);
         fill();
     }
     cp_wait<0>();
@@ -688,6 +728,8 @@ __global__ void __launch_bounds__(kMergeThreads) kv8_merge_kernel(const AttnP p,
     bool bad;
     const int rows = kv8_rows(p.pos, p.counts, b, p.M, p.T_cap, p0, bad);
     const int n = rows > 0 ? p0 + rows : 0, nch = (n + p.chunk - 1) / p.chunk;
+    asm volatile("griddepcontrol.launch_dependents;");
+    asm volatile("griddepcontrol.wait;" ::: "memory");              // the chunks' results
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     const bool on = 8 * ct + 2 * tq < p.C;
@@ -755,7 +797,8 @@ __global__ void __launch_bounds__(kMergeThreads) kv8_merge_kernel(const AttnP p,
 }
 
 // Weight received by each position: the stored scores against the columns'
-// joined references and sums, in column order.
+// joined references and sums, in column order.  Bound by reading the scores
+// (from L2, mostly), four columns a load where a position's scores are aligned.
 constexpr int kAccThreads = 256;
 
 __global__ void __launch_bounds__(kAccThreads) kv8_weights_kernel(const AttnP p)
@@ -765,35 +808,53 @@ __global__ void __launch_bounds__(kAccThreads) kv8_weights_kernel(const AttnP p)
     int p0;
     bool bad;
     const int rows = kv8_rows(p.pos, p.counts, b, p.M, p.T_cap, p0, bad);
-    const int n = rows > 0 ? p0 + rows : 0, t0 = blockIdx.x * kAccThreads;
-    if (t0 >= n) return;
+    const int n = rows > 0 ? p0 + rows : 0, t = blockIdx.x * kAccThreads + tid;
+    if (t - tid >= n) return;
     const size_t head = (size_t)b * p.Hkv + g;
-    for (int i = tid; i < 2 * p.C; i += kAccThreads) st[i] = __ldg(p.fin + head * p.C * 2 + i);
-    __syncthreads();
-    const int t = t0 + tid;
-    if (t >= n) return;
+    // what does not come from the merge is loaded ahead of it
     float a = t < p0 && p.acc_in ? p.decay * p.acc_in[head * p.T_cap + t] : 0.f;
-    for (int c = 0; c < p.C; ++c)
-        if (c / p.G < rows && t <= p0 + c / p.G)
-            a = fmaf(exp2f(__ldg(p.sc + (head * p.T_cap + t) * p.C + c) - st[2 * c]), st[2 * c + 1], a);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    for (int i = tid; i < 2 * p.C; i += kAccThreads) st[i] = __ldcg(p.fin + head * p.C * 2 + i);
+    __syncthreads();
+    if (t >= n) return;
+    const float *sc = p.sc + (head * p.T_cap + t) * p.C;
+    auto add = [&](int c, float s) {
+        int h = c;
+        const int m = p.by_group.by(h);
+        if (m < rows && t <= p0 + m) a = fmaf(exp2f(s - st[2 * c]), st[2 * c + 1], a);
+    };
+    if (p.C % 4 == 0) {
+#pragma unroll 2
+        for (int c = 0; c < p.C; c += 4) {
+            const float4 v = __ldcg(reinterpret_cast<const float4 *>(sc + c));
+            add(c, v.x);
+            add(c + 1, v.y);
+            add(c + 2, v.z);
+            add(c + 3, v.w);
+        }
+    } else
+        for (int c = 0; c < p.C; ++c) add(c, __ldcg(sc + c));
     p.acc[head * p.T_cap + t] = a;
 }
 
-// Positions per chunk: 1 to 16 tiles a warp, as many as leave every CTA slot
-// of 152 SMs a few chunks of a full cache.
-#ifndef KV8_ITEMS
-#define KV8_ITEMS 2
-#endif
-#ifndef KV8_MAXT
-#define KV8_MAXT 16
-#endif
+// Positions per chunk: r tiles a warp.  The chunks of a full cache run in waves
+// over the 456 CTA slots of 152 SMs; the r that makes waves (r + 2) least is
+// taken, a chunk's end costing about two tiles, the larger of equals.  A rule
+// of the cache's shape alone.
 int kv8_chunk(const moe_kv8 &c)
 {
     const int round = kWarps * kTileBytes / c.head_dim;
-    const long long rounds = (long long)c.batch * c.kv_heads * c.T_cap / round;
-    int r = KV8_MAXT;
-    while (r > 1 && rounds < 152LL * 3 * KV8_ITEMS * r) r /= 2;
-    return r * round;
+    int best = 1;
+    long long least = LLONG_MAX;
+    for (const int r : {1, 2, 3, 4, 5, 6, 8, 10, 16}) {
+        const long long chunks = (long long)c.batch * c.kv_heads * ((c.T_cap + r * round - 1) / (r * round));
+        const long long cost = (chunks + 455) / 456 * (r + 2);
+        if (cost <= least) {
+            least = cost;
+            best = r;
+        }
+    }
+    return best * round;
 }
 
 // Once per kernel and device.
@@ -863,6 +924,8 @@ int launch_kv8_attn(const moe_kv8 &c, const moe_rows &q, int M, const int32_t *p
     p.blk_log = 0;
     while ((1 << p.blk_log) < c.block) ++p.blk_log;
     p.nblk = c.T_cap / c.block;
+    p.by_head = div_of(p.Hkv);
+    p.by_group = div_of(p.G);
     p.f16 = q.type == MOE_F16;
     p.o_type = o_type;
     p.qvec = reinterpret_cast<uintptr_t>(q.data_dev) % 16 == 0 && q.seq % 8 == 0 && q.row % 8 == 0 && q.head % 8 == 0;
@@ -870,6 +933,7 @@ int launch_kv8_attn(const moe_kv8 &c, const moe_rows &q, int M, const int32_t *p
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess || dev < 0 || dev >= 64) { note_cuda_error((int)e); return MOE_ERR_CUDA; }
     const int nt = kv8_nt(p.C, c.head_dim);
+    p.by_pass = div_of((p.C + 8 * nt - 1) / (8 * nt));
     const long long items = (long long)p.nchunk * p.B * p.Hkv * ((p.C + 8 * nt - 1) / (8 * nt));
     if (items > INT_MAX / 2) return MOE_ERR_UNSUPPORTED;
     auto go = [&](auto kernel, int smem, int ctas, Once &once) {
@@ -925,19 +989,31 @@ int launch_kv8_attn(const moe_kv8 &c, const moe_rows &q, int M, const int32_t *p
         cfg.gridDim = dim3(shares * (c.head_dim / 32) * ((p.C + 7) / 8), p.Hkv, p.B);
         cfg.blockDim = dim3(kMergeThreads);
         cfg.stream = stream;
-        cudaLaunchAttribute at[1];
-        at[0].id = cudaLaunchAttributeClusterDimension;
-        at[0].val.clusterDim.x = shares;
-        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        cudaLaunchAttribute at[2];
+        at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[0].val.programmaticStreamSerializationAllowed = 1;
+        at[1].id = cudaLaunchAttributeClusterDimension;
+        at[1].val.clusterDim.x = shares;
+        at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
         cfg.attrs = at;
-        cfg.numAttrs = 1;
+        cfg.numAttrs = 2;
         e = cudaLaunchKernelEx(&cfg, kv8_merge_kernel, p, c.head_dim, shares);
         if (e != cudaSuccess) { note_cuda_error((int)e); return MOE_ERR_CUDA; }
     }
     note_launch();
     if (acc) {
-        kv8_weights_kernel<<<dim3((c.T_cap + kAccThreads - 1) / kAccThreads, c.kv_heads, c.batch), kAccThreads,
-                             p.C * 2 * sizeof(float), stream>>>(p);
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((c.T_cap + kAccThreads - 1) / kAccThreads, p.Hkv, p.B);
+        cfg.blockDim = dim3(kAccThreads);
+        cfg.dynamicSmemBytes = p.C * 2 * sizeof(float);
+        cfg.stream = stream;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        e = cudaLaunchKernelEx(&cfg, kv8_weights_kernel, p);
+        if (e != cudaSuccess) { note_cuda_error((int)e); return MOE_ERR_CUDA; }
         note_launch();
     }
     e = cudaGetLastError();
