@@ -52,7 +52,7 @@ struct AttnP {
     float decay, scale_log2;        // scale * log2(e)
     int *err, *counter;                   // counter: items taken beyond the first of each CTA, or NULL (in turn)
     Div by_pass, by_head, by_group;       // column passes, key/value heads, G
-    int B, Hq, Hkv, G, M, C, T_cap, chunk, nchunk, blk_log, nblk, f16, qvec, o_type;
+    int B, Hq, Hkv, G, M, C, T_cap, chunk, nchunk, blk_log, nblk, f16, qvec, o_type, streams;
 };
 
 // ------------------------------------------------------------------ chunks
@@ -109,9 +109,9 @@ struct Lay {
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void *src)
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, uint64_t policy)
 {
-    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "l"(policy) : "memory");
 }
 __device__ __forceinline__ void cp16z(uint32_t dst, const void *src, bool in)
 {
@@ -290,6 +290,10 @@ __global__ void __launch_bounds__(kThreads, Lay<D, NT>::ctas) kv8_chunk_kernel(c
     uint32_t v_lane[VX];
 #pragma unroll
     for (int i = 0; i < VX; ++i) v_lane[i] = lr * D + (lc ^ ((lr + i * (512 / D)) & (D == 64 ? 2 : 6))) * 16;
+    // a cache that L2 cannot keep leaves it to the chunks' results
+    uint64_t policy;
+    if (p.streams) asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+    else asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
     int nth = 0, ld_nth = 0, ld_item = blockIdx.x, ld_t = 0, ld_k1 = 0, ld_stage = 0, free_slots = kStages;
     const uint8_t *ld_k = nullptr, *ld_v = nullptr;
     const float *ld_s = nullptr;
@@ -315,8 +319,8 @@ __global__ void __launch_bounds__(kThreads, Lay<D, NT>::ctas) kv8_chunk_kernel(c
             if (ld_t + TK <= ld_k1) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    cp16(dst + k_lane + i * 512, ld_k + i * 512);
-                    cp16(dst + kTileBytes + v_lane[i % VX] + i * 512, ld_v + i * 512);
+                    cp16(dst + k_lane + i * 512, ld_k + i * 512, policy);
+                    cp16(dst + kTileBytes + v_lane[i % VX] + i * 512, ld_v + i * 512, policy);
                 }
             } else {
                 // rows past the end are zeros, not what lies there
@@ -799,7 +803,7 @@ __global__ void __launch_bounds__(kMergeThreads) kv8_merge_kernel(const AttnP p,
 // Weight received by each position: the stored scores against the columns'
 // joined references and sums, in column order.  Bound by reading the scores
 // (from L2, mostly), four columns a load where a position's scores are aligned.
-constexpr int kAccThreads = 256;
+constexpr int kAccThreads = 256, kAccPer = 4, kAccSpan = kAccThreads * kAccPer;
 
 __global__ void __launch_bounds__(kAccThreads) kv8_weights_kernel(const AttnP p)
 {
@@ -808,53 +812,79 @@ __global__ void __launch_bounds__(kAccThreads) kv8_weights_kernel(const AttnP p)
     int p0;
     bool bad;
     const int rows = kv8_rows(p.pos, p.counts, b, p.M, p.T_cap, p0, bad);
-    const int n = rows > 0 ? p0 + rows : 0, t = blockIdx.x * kAccThreads + tid;
-    if (t - tid >= n) return;
+    const int n = rows > 0 ? p0 + rows : 0, t0 = blockIdx.x * kAccSpan + tid;
+    if (t0 - tid >= n) return;
     const size_t head = (size_t)b * p.Hkv + g;
     // what does not come from the merge is loaded ahead of it
-    float a = t < p0 && p.acc_in ? p.decay * p.acc_in[head * p.T_cap + t] : 0.f;
+    float a[kAccPer];
+#pragma unroll
+    for (int i = 0; i < kAccPer; ++i) {
+        const int t = t0 + i * kAccThreads;
+        a[i] = t < min(p0, n) && p.acc_in ? p.decay * p.acc_in[head * p.T_cap + t] : 0.f;
+    }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     for (int i = tid; i < 2 * p.C; i += kAccThreads) st[i] = __ldcg(p.fin + head * p.C * 2 + i);
     __syncthreads();
-    if (t >= n) return;
-    const float *sc = p.sc + (head * p.T_cap + t) * p.C;
-    auto add = [&](int c, float s) {
-        int h = c;
-        const int m = p.by_group.by(h);
-        if (m < rows && t <= p0 + m) a = fmaf(exp2f(s - st[2 * c]), st[2 * c + 1], a);
+    const float *sc = p.sc + (head * p.T_cap + t0) * p.C;
+    auto add = [&](int i, int c, int m, float s) {
+        if (m < rows && t0 + i * kAccThreads <= p0 + m) a[i] = fmaf(exp2f(s - st[2 * c]), st[2 * c + 1], a[i]);
     };
     if (p.C % 4 == 0) {
 #pragma unroll 2
         for (int c = 0; c < p.C; c += 4) {
-            const float4 v = __ldcg(reinterpret_cast<const float4 *>(sc + c));
-            add(c, v.x);
-            add(c + 1, v.y);
-            add(c + 2, v.z);
-            add(c + 3, v.w);
+            float4 v[kAccPer];
+#pragma unroll
+            for (int i = 0; i < kAccPer; ++i)
+                v[i] = t0 + i * kAccThreads < n ? __ldcg(reinterpret_cast<const float4 *>(sc + (size_t)i * kAccThreads * p.C + c))
+                                                : make_float4(0.f, 0.f, 0.f, 0.f);
+            int m[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                int h = c + k;
+                m[k] = p.by_group.by(h);
+            }
+#pragma unroll
+            for (int i = 0; i < kAccPer; ++i) {
+                add(i, c, m[0], v[i].x);
+                add(i, c + 1, m[1], v[i].y);
+                add(i, c + 2, m[2], v[i].z);
+                add(i, c + 3, m[3], v[i].w);
+            }
         }
     } else
-        for (int c = 0; c < p.C; ++c) add(c, __ldcg(sc + c));
-    p.acc[head * p.T_cap + t] = a;
+        for (int c = 0; c < p.C; ++c) {
+            int h = c;
+            const int m = p.by_group.by(h);
+#pragma unroll
+            for (int i = 0; i < kAccPer; ++i)
+                add(i, c, m, t0 + i * kAccThreads < n ? __ldcg(sc + (size_t)i * kAccThreads * p.C + c) : 0.f);
+        }
+#pragma unroll
+    for (int i = 0; i < kAccPer; ++i)
+        if (t0 + i * kAccThreads < n) p.acc[head * p.T_cap + t0 + i * kAccThreads] = a[i];
 }
 
-// Positions per chunk: r tiles a warp.  The chunks of a full cache run in waves
-// over the 456 CTA slots of 152 SMs; the r that makes waves (r + 2) least is
-// taken, a chunk's end costing about two tiles, the larger of equals.  A rule
-// of the cache's shape alone.
+// Positions per chunk: r tiles a warp.  The chunks of a full cache are taken
+// by the 456 CTA slots of 152 SMs; the end of one costs about D / 100 tiles
+// (joining D dimensions and expanding the next queries), and half a chunk is lost
+// where the last ones end.  Of the r that come within 3% of the least cost
+// the smallest is taken: caches are seldom full.  (8 x 128K of 256: r = 8,
+// 10, 16 take 182, 177, 167 us; 32 of up to 16K of 128: 92, 97, 106.)  A rule of
+// the cache's shape alone.
 int kv8_chunk(const moe_kv8 &c)
 {
-    const int round = kWarps * kTileBytes / c.head_dim;
-    int best = 1;
-    long long least = LLONG_MAX;
-    for (const int r : {1, 2, 3, 4, 5, 6, 8, 10, 16}) {
+    const int choice[] = {1, 2, 3, 4, 5, 6, 8, 10, 16}, round = kWarps * kTileBytes / c.head_dim;
+    long long cost[9], least = LLONG_MAX;                            // in tenths of a tile, per slot
+    for (int i = 0; i < 9; ++i) {
+        const int r = choice[i];
         const long long chunks = (long long)c.batch * c.kv_heads * ((c.T_cap + r * round - 1) / (r * round));
-        const long long cost = (chunks + 455) / 456 * (r + 2);
-        if (cost <= least) {
-            least = cost;
-            best = r;
-        }
+        const long long one = 10 * r + c.head_dim / 10;
+        cost[i] = chunks <= 3 * 456 ? (chunks + 455) / 456 * one : chunks * one / 456 + 5 * r;
+        least = std::min(least, cost[i]);
     }
-    return best * round;
+    for (int i = 0; i < 9; ++i)
+        if (cost[i] * 100 <= least * 103) return choice[i] * round;
+    return round;
 }
 
 // Once per kernel and device.
@@ -928,6 +958,7 @@ int launch_kv8_attn(const moe_kv8 &c, const moe_rows &q, int M, const int32_t *p
     p.by_group = div_of(p.G);
     p.f16 = q.type == MOE_F16;
     p.o_type = o_type;
+    p.streams = 2LL * c.batch * c.kv_heads * c.T_cap * c.head_dim > (96LL << 20);
     p.qvec = reinterpret_cast<uintptr_t>(q.data_dev) % 16 == 0 && q.seq % 8 == 0 && q.row % 8 == 0 && q.head % 8 == 0;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -1003,7 +1034,7 @@ int launch_kv8_attn(const moe_kv8 &c, const moe_rows &q, int M, const int32_t *p
     note_launch();
     if (acc) {
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((c.T_cap + kAccThreads - 1) / kAccThreads, p.Hkv, p.B);
+        cfg.gridDim = dim3((c.T_cap + kAccSpan - 1) / kAccSpan, p.Hkv, p.B);
         cfg.blockDim = dim3(kAccThreads);
         cfg.dynamicSmemBytes = p.C * 2 * sizeof(float);
         cfg.stream = stream;
