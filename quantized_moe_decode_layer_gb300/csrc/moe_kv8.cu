@@ -110,8 +110,8 @@ struct Raw {
     }
 };
 
-template <int FMT, int TYPE>
-__global__ void __launch_bounds__(512) kv8_append_kernel(const AppendParams p)
+template <int FMT, int TYPE, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS == 512 ? (TYPE == MOE_F32 ? 1 : 2) : TYPE == MOE_F32 ? 2 : 4) kv8_append_kernel(const AppendParams p)
 {
     __shared__ float red[16];
     const int b = blockIdx.z, g = blockIdx.y >> 1, which = blockIdx.y & 1;
@@ -284,6 +284,7 @@ __global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(const EvictPara
     int *copies = reinterpret_cast<int *>(sel);                     // [bins][copies]
     float *weights = reinterpret_cast<float *>(sel + kSelBins * kSelCopies);   // [kSelKeys]: this slice's
     __shared__ int hist[2][kSelBins], wsum[32], weq[32], total[2], sh_digit, sh_need;   // hist: the passes take turns
+    asm volatile("griddepcontrol.launch_dependents;");               // the move may start, and waits for the positions
     const int rank = blockIdx.x % ctas, g = blockIdx.x / ctas, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int len = p.lens[b];
     if (len > p.T_cap && blockIdx.x == 0 && tid == 0) atomicOr(p.err, kKv8ErrRange);
@@ -431,13 +432,14 @@ __global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(const EvictPara
 // Moving: a destination block's step is the smallest that holds its values; a
 // code whose own step was smaller is rounded to it, one whose step was larger
 // is exact.
-template <int FMT>
-__global__ void __launch_bounds__(512) kv8_move_kernel(const EvictParams p)
+template <int FMT, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS == 512 ? 1 : 3) kv8_move_kernel(const EvictParams p)
 {
     __shared__ float red[16];
     const int g = blockIdx.y >> 1, which = blockIdx.y & 1, b = blockIdx.z;
     const Place q = place_of(p.blk, p.D);
-    const int kept = p.lens_out[b], j = blockIdx.x * (blockDim.x / q.threads) + q.j, i0 = j * p.blk;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int kept = __ldcg(p.lens_out + b), j = blockIdx.x * (blockDim.x / q.threads) + q.j, i0 = j * p.blk;
     if ((int)(blockIdx.x * (blockDim.x / q.threads)) * p.blk >= kept) return;
     const size_t head = (size_t)b * p.Hkv + g;
     const uint8_t *src = p.codes[which] + head * p.T_cap * p.D + q.d;
@@ -449,7 +451,7 @@ __global__ void __launch_bounds__(512) kv8_move_kernel(const EvictParams p)
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int at = i0 + q.row + i * (p.blk >> 3);
-        t[i] = at < kept ? idx[at] : -1;
+        t[i] = at < kept ? __ldcg(idx + at) : -1;
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -523,16 +525,21 @@ int launch_kv8_append(const moe_kv8 &c, const moe_rows &k_new, const moe_rows &v
     p.nblk = c.T_cap / c.block;
     const int per = place_blocks(c.block, c.head_dim), threads = place_threads(c.block, c.head_dim);
     const dim3 grid((min((M - 1) / c.block + 2, p.nblk) + per - 1) / per, 2 * c.kv_heads, c.batch);
-    auto go = [&](auto kernel) { kernel<<<grid, threads, 0, stream>>>(p); };
+#define KV8_APPEND(F, T)                                                                    \
+    do {                                                                                    \
+        if (threads == 256) kv8_append_kernel<F, T, 256><<<grid, 256, 0, stream>>>(p);      \
+        else kv8_append_kernel<F, T, 512><<<grid, 512, 0, stream>>>(p);                     \
+    } while (0)
     if (c.format == MOE_KV8_INT8) {
-        if (type == MOE_BF16) go(kv8_append_kernel<MOE_KV8_INT8, MOE_BF16>);
-        else if (type == MOE_F16) go(kv8_append_kernel<MOE_KV8_INT8, MOE_F16>);
-        else go(kv8_append_kernel<MOE_KV8_INT8, MOE_F32>);
+        if (type == MOE_BF16) KV8_APPEND(MOE_KV8_INT8, MOE_BF16);
+        else if (type == MOE_F16) KV8_APPEND(MOE_KV8_INT8, MOE_F16);
+        else KV8_APPEND(MOE_KV8_INT8, MOE_F32);
     } else {
-        if (type == MOE_BF16) go(kv8_append_kernel<MOE_KV8_E4M3, MOE_BF16>);
-        else if (type == MOE_F16) go(kv8_append_kernel<MOE_KV8_E4M3, MOE_F16>);
-        else go(kv8_append_kernel<MOE_KV8_E4M3, MOE_F32>);
+        if (type == MOE_BF16) KV8_APPEND(MOE_KV8_E4M3, MOE_BF16);
+        else if (type == MOE_F16) KV8_APPEND(MOE_KV8_E4M3, MOE_F16);
+        else KV8_APPEND(MOE_KV8_E4M3, MOE_F32);
     }
+#undef KV8_APPEND
     note_launch();
     return launched();
 }
@@ -622,8 +629,21 @@ int launch_kv8_evict(const moe_kv8 &c, const moe_kv8 &d, const int32_t *lens, co
     note_launch();
     const int per = place_blocks(c.block, c.head_dim), threads = place_threads(c.block, c.head_dim);
     const dim3 grid(((budget + c.block - 1) / c.block + per - 1) / per, 2 * c.kv_heads, c.batch);
-    if (c.format == MOE_KV8_INT8) kv8_move_kernel<MOE_KV8_INT8><<<grid, threads, 0, stream>>>(p);
-    else kv8_move_kernel<MOE_KV8_E4M3><<<grid, threads, 0, stream>>>(p);
+    {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = grid;
+        cfg.blockDim = dim3(threads);
+        cfg.stream = stream;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        const bool i8 = c.format == MOE_KV8_INT8;
+        e = threads == 256 ? cudaLaunchKernelEx(&cfg, i8 ? kv8_move_kernel<MOE_KV8_INT8, 256> : kv8_move_kernel<MOE_KV8_E4M3, 256>, p)
+                           : cudaLaunchKernelEx(&cfg, i8 ? kv8_move_kernel<MOE_KV8_INT8, 512> : kv8_move_kernel<MOE_KV8_E4M3, 512>, p);
+        if (e != cudaSuccess) { note_cuda_error((int)e); return MOE_ERR_CUDA; }
+    }
     note_launch();
     return launched();
 }
