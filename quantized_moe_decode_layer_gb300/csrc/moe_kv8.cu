@@ -431,52 +431,59 @@ __global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(const EvictPara
 
 // Moving: a destination block's step is the smallest that holds its values; a
 // code whose own step was smaller is rounded to it, one whose step was larger
-// is exact.
+// is exact.  As many threads to a block as above, here with 16 codes of 4 rows
+// each.  Bound by gathering rows of D bytes.
 template <int FMT, int THREADS>
 __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 1 : 3) kv8_move_kernel(const EvictParams p)
 {
     __shared__ float red[16];
     const int g = blockIdx.y >> 1, which = blockIdx.y & 1, b = blockIdx.z;
-    const Place q = place_of(p.blk, p.D);
+    Place q = place_of(p.blk, p.D);
+    const int r = threadIdx.x & (q.threads - 1), step = p.blk >> 2;
+    q.row = r / (p.D >> 4);
+    q.d = r % (p.D >> 4) * 16;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int kept = __ldcg(p.lens_out + b), j = blockIdx.x * (blockDim.x / q.threads) + q.j, i0 = j * p.blk;
-    if ((int)(blockIdx.x * (blockDim.x / q.threads)) * p.blk >= kept) return;
+    const int kept = __ldcg(p.lens_out + b), j = blockIdx.x * (THREADS / q.threads) + q.j, i0 = j * p.blk;
+    if ((int)(blockIdx.x * (THREADS / q.threads)) * p.blk >= kept) return;
     const size_t head = (size_t)b * p.Hkv + g;
     const uint8_t *src = p.codes[which] + head * p.T_cap * p.D + q.d;
     const float *scale = p.scale[which] + head * p.nblk;
     const int32_t *idx = p.idx + head * p.budget;
-    uint2 w[8];
-    float s[8], amax = 0.f;
-    int t[8];
+    uint4 w[4];
+    float s[4], amax = 0.f;
+    int t[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int at = i0 + q.row + i * (p.blk >> 3);
+    for (int i = 0; i < 4; ++i) {
+        const int at = i0 + q.row + i * step;
         t[i] = at < kept ? __ldcg(idx + at) : -1;
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        w[i] = make_uint2(0u, 0u);
+    for (int i = 0; i < 4; ++i) {
+        w[i] = make_uint4(0u, 0u, 0u, 0u);
         s[i] = 0.f;
         if (t[i] >= 0) {
-            w[i] = __ldg(reinterpret_cast<const uint2 *>(src + (size_t)t[i] * p.D));
+            w[i] = __ldg(reinterpret_cast<const uint4 *>(src + (size_t)t[i] * p.D));
             s[i] = __ldg(scale + (t[i] >> p.blk_log));
         }
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, amax8<FMT>(w[i]) * s[i]);
+    for (int i = 0; i < 4; ++i)
+        amax = fmaxf(amax, fmaxf(amax8<FMT>(make_uint2(w[i].x, w[i].y)), amax8<FMT>(make_uint2(w[i].z, w[i].w))) * s[i]);
     amax = place_max(amax, q, red);
     if (i0 >= kept) return;
     const int e = step_exp<FMT>(amax);
     const float inv = pow2f(-e);
-    if (q.row == 0 && q.d == 0) p.dscale[which][head * p.dnblk + j] = pow2f(e);
+    if (r == 0) p.dscale[which][head * p.dnblk + j] = pow2f(e);
     uint8_t *dst = p.dcodes[which] + head * p.dT_cap * p.D + q.d;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 4; ++i) {
         if (t[i] < 0) continue;
         // no more than 2^17, see recode4; a row of zeros may have any step
         const float ratio = fminf(s[i] * inv, 131072.f);
-        *reinterpret_cast<uint2 *>(dst + (size_t)(i0 + q.row + i * (p.blk >> 3)) * p.D) =
-            ratio == 1.f ? w[i] : recode8<FMT>(w[i], ratio);
+        if (ratio != 1.f)
+            w[i] = make_uint4(recode4<FMT>(w[i].x, ratio), recode4<FMT>(w[i].y, ratio), recode4<FMT>(w[i].z, ratio),
+                              recode4<FMT>(w[i].w, ratio));
+        *reinterpret_cast<uint4 *>(dst + (size_t)(i0 + q.row + i * step) * p.D) = w[i];
     }
 }
 
