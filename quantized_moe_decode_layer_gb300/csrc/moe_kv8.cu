@@ -114,6 +114,7 @@ template <int FMT, int TYPE, int THREADS>
 __global__ void __launch_bounds__(THREADS, THREADS == 512 ? (TYPE == MOE_F32 ? 1 : 2) : TYPE == MOE_F32 ? 2 : 4) kv8_append_kernel(const AppendParams p)
 {
     __shared__ float red[16];
+    after_previous();
     const int b = blockIdx.z, g = blockIdx.y >> 1, which = blockIdx.y & 1;
     int p0;
     bool bad;
@@ -203,6 +204,7 @@ struct ReadParams {
 template <int FMT>
 __global__ void __launch_bounds__(256) kv8_read_kernel(const ReadParams p)
 {
+    after_previous();
     const int lanes = p.D / 8, b = blockIdx.y;
     const long long i = (long long)blockIdx.x * 256 + threadIdx.x;   // (row, head, 8 values)
     if (i >= (long long)p.n * p.Hkv * lanes) return;
@@ -284,7 +286,7 @@ __global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(const EvictPara
     int *copies = reinterpret_cast<int *>(sel);                     // [bins][copies]
     float *weights = reinterpret_cast<float *>(sel + kSelBins * kSelCopies);   // [kSelKeys]: this slice's
     __shared__ int hist[2][kSelBins], wsum[32], weq[32], total[2], sh_digit, sh_need;   // hist: the passes take turns
-    asm volatile("griddepcontrol.launch_dependents;");               // the move may start, and waits for the positions
+    after_previous();
     const int rank = blockIdx.x % ctas, g = blockIdx.x / ctas, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int len = p.lens[b];
     if (len > p.T_cap && blockIdx.x == 0 && tid == 0) atomicOr(p.err, kKv8ErrRange);
@@ -442,7 +444,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 1 : 3) kv8_move_kern
     const int r = threadIdx.x & (q.threads - 1), step = p.blk >> 2;
     q.row = r / (p.D >> 4);
     q.d = r % (p.D >> 4) * 16;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    after_previous();
     const int kept = __ldcg(p.lens_out + b), j = blockIdx.x * (THREADS / q.threads) + q.j, i0 = j * p.blk;
     if ((int)(blockIdx.x * (THREADS / q.threads)) * p.blk >= kept) return;
     const size_t head = (size_t)b * p.Hkv + g;
@@ -494,10 +496,10 @@ int ilog2(int v)
     return r;
 }
 
-int launched()
+int launched(cudaError_t e)
 {
-    const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) { note_cuda_error((int)e); return MOE_ERR_CUDA; }
+    note_launch();
     return MOE_OK;
 }
 
@@ -532,10 +534,11 @@ int launch_kv8_append(const moe_kv8 &c, const moe_rows &k_new, const moe_rows &v
     p.nblk = c.T_cap / c.block;
     const int per = place_blocks(c.block, c.head_dim), threads = place_threads(c.block, c.head_dim);
     const dim3 grid((min((M - 1) / c.block + 2, p.nblk) + per - 1) / per, 2 * c.kv_heads, c.batch);
+    cudaError_t e;
 #define KV8_APPEND(F, T)                                                                    \
     do {                                                                                    \
-        if (threads == 256) kv8_append_kernel<F, T, 256><<<grid, 256, 0, stream>>>(p);      \
-        else kv8_append_kernel<F, T, 512><<<grid, 512, 0, stream>>>(p);                     \
+        if (threads == 256) e = launch_after(kv8_append_kernel<F, T, 256>, grid, 256, 0, 0, stream, p); \
+        else e = launch_after(kv8_append_kernel<F, T, 512>, grid, 512, 0, 0, stream, p);    \
     } while (0)
     if (c.format == MOE_KV8_INT8) {
         if (type == MOE_BF16) KV8_APPEND(MOE_KV8_INT8, MOE_BF16);
@@ -547,8 +550,7 @@ int launch_kv8_append(const moe_kv8 &c, const moe_rows &k_new, const moe_rows &v
         else KV8_APPEND(MOE_KV8_E4M3, MOE_F32);
     }
 #undef KV8_APPEND
-    note_launch();
-    return launched();
+    return launched(e);
 }
 
 int launch_kv8_read(const moe_kv8 &c, const int32_t *start, int n, const int32_t *lens, uint16_t *k_out, uint16_t *v_out,
@@ -571,10 +573,8 @@ int launch_kv8_read(const moe_kv8 &c, const int32_t *start, int n, const int32_t
     p.nblk = c.T_cap / c.block;
     const long long items = (long long)n * c.kv_heads * (c.head_dim / 8);
     const dim3 grid((unsigned)((items + 255) / 256), c.batch);
-    if (c.format == MOE_KV8_INT8) kv8_read_kernel<MOE_KV8_INT8><<<grid, 256, 0, stream>>>(p);
-    else kv8_read_kernel<MOE_KV8_E4M3><<<grid, 256, 0, stream>>>(p);
-    note_launch();
-    return launched();
+    return launched(launch_after(c.format == MOE_KV8_INT8 ? kv8_read_kernel<MOE_KV8_INT8> : kv8_read_kernel<MOE_KV8_E4M3>, grid,
+                                 256, 0, 0, stream, p));
 }
 
 int launch_kv8_evict(const moe_kv8 &c, const moe_kv8 &d, const int32_t *lens, const float *acc, int budget, int sinks,
@@ -618,41 +618,16 @@ int launch_kv8_evict(const moe_kv8 &c, const moe_kv8 &d, const int32_t *lens, co
     std::call_once(once[dev], [&] {
         e = cudaFuncSetAttribute((const void *)kv8_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     });
-    if (e == cudaSuccess) {
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(ctas * c.kv_heads, c.batch);
-        cfg.blockDim = dim3(kSelThreads);
-        cfg.dynamicSmemBytes = smem;
-        cfg.stream = stream;
-        cudaLaunchAttribute at[1];
-        at[0].id = cudaLaunchAttributeClusterDimension;
-        at[0].val.clusterDim.x = ctas;
-        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-        cfg.attrs = at;
-        cfg.numAttrs = 1;
-        e = cudaLaunchKernelEx(&cfg, kv8_select_kernel, p, ctas);
-    }
-    if (e != cudaSuccess) { note_cuda_error((int)e); return MOE_ERR_CUDA; }
-    note_launch();
+    if (e == cudaSuccess)
+        e = launch_after(kv8_select_kernel, dim3(ctas * c.kv_heads, c.batch), kSelThreads, smem, ctas, stream, p, ctas);
+    if (const int rc = launched(e)) return rc;
     const int per = place_blocks(c.block, c.head_dim), threads = place_threads(c.block, c.head_dim);
     const dim3 grid(((budget + c.block - 1) / c.block + per - 1) / per, 2 * c.kv_heads, c.batch);
-    {
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = grid;
-        cfg.blockDim = dim3(threads);
-        cfg.stream = stream;
-        cudaLaunchAttribute at[1];
-        at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        at[0].val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = at;
-        cfg.numAttrs = 1;
-        const bool i8 = c.format == MOE_KV8_INT8;
-        e = threads == 256 ? cudaLaunchKernelEx(&cfg, i8 ? kv8_move_kernel<MOE_KV8_INT8, 256> : kv8_move_kernel<MOE_KV8_E4M3, 256>, p)
-                           : cudaLaunchKernelEx(&cfg, i8 ? kv8_move_kernel<MOE_KV8_INT8, 512> : kv8_move_kernel<MOE_KV8_E4M3, 512>, p);
-        if (e != cudaSuccess) { note_cuda_error((int)e); return MOE_ERR_CUDA; }
-    }
-    note_launch();
-    return launched();
+    const bool i8 = c.format == MOE_KV8_INT8;
+    return launched(
+        threads == 256
+            ? launch_after(i8 ? kv8_move_kernel<MOE_KV8_INT8, 256> : kv8_move_kernel<MOE_KV8_E4M3, 256>, grid, 256, 0, 0, stream, p)
+            : launch_after(i8 ? kv8_move_kernel<MOE_KV8_INT8, 512> : kv8_move_kernel<MOE_KV8_E4M3, 512>, grid, 512, 0, 0, stream, p));
 }
 
 }  // namespace moe

@@ -102,8 +102,8 @@ template <int D, int NT>
 struct Lay {
     static constexpr bool wide = NT * D > 256 || NT > 2;
     static constexpr int ctas = wide ? 2 : 3, NC = 8 * NT;
-    static constexpr int ring = 0, ml = kWarps * kStages * kStageBytes, unit = ml + kWarps * NC * 8, seq = unit + kWarps * 8,
-                         q = seq + 16, qf = q + (wide ? NT * D * 16 : 0), first = qf + (wide ? NC * 4 : 0);
+    static constexpr int ring = 0, ml = kWarps * kStages * kStageBytes, unit = ml + kWarps * NC * 8, items = unit + kWarps * 8,
+                         q = items + 4 * 32, qf = q + NT * D * 16, first = qf + NC * 4;
     static constexpr int total(int B) { return first + (3 * B + 1) * 4; }   // first[B + 1], then position and rows of each sequence
 };
 
@@ -158,14 +158,19 @@ __device__ __forceinline__ void cross(uint32_t r0, uint32_t r1, uint32_t (&d)[4]
     }
 }
 
-// One (sequence, chunk, head, column pass).
-struct Item {
-    int b, g, cp, k0, k1, p0, rows;    // positions k0 .. k1 - 1
+// One (sequence, chunk, head, column pass); b < 0: no more.
+struct __align__(16) Item {
+    int b, g, cp, k0, k1, p0, rows, nth;   // positions k0 .. k1 - 1, the nth chunk
 };
 
-__device__ __forceinline__ Item decode_item(const AttnP &p, const int *first, int item)
+__device__ __forceinline__ Item decode_item(const AttnP &p, const int *first, int item, int total)
 {
     Item it;
+    if (item >= total) {
+        it.b = -1;
+        it.g = it.cp = it.k0 = it.k1 = it.p0 = it.rows = it.nth = 0;
+        return it;
+    }
     it.cp = item;
     item = p.by_pass.by(it.cp);
     it.g = item;
@@ -179,57 +184,63 @@ __device__ __forceinline__ Item decode_item(const AttnP &p, const int *first, in
     it.b = lo;
     it.p0 = first[p.B + 1 + lo];
     it.rows = first[2 * p.B + 1 + lo];
-    it.k0 = (item - first[lo]) * p.chunk;
+    it.nth = item - first[lo];
+    it.k0 = it.nth * p.chunk;
     it.k1 = min(it.k0 + p.chunk, it.p0 + it.rows);
     return it;
 }
 
-// A lane's query fragments: column g, dimensions 64 i + 16 t .. + 15, as the
-// B operands of k-steps 4 i .. 4 i + 3, in the order of pairs(); scaled by a
-// power of two (exactly; the row's largest to 2^12 .. 2^13, so that only
-// elements 2^26 times smaller lose bits).  Returns its inverse.
-template <int FMT, int D>
-__device__ __forceinline__ float load_q(const AttnP &p, const Item &it, int c, int tq, uint32_t (&b)[D / 16][2])
+// An item's queries into shared memory, each warp 512 / D of its columns: as
+// the B operands of the k-steps, [column tile][two k-steps][lane], in the order
+// of pairs(); scaled by a power of two (exactly; the row's largest to 2^12 ..
+// 2^13, so that only elements 2^26 times smaller lose bits).
+template <int FMT, int D, int NT>
+__device__ __forceinline__ void stage_q(const AttnP &p, const Item &it, uint4 *qs, float *qf)
 {
-    int h = c;
-    const int m = p.by_group.by(h);
-    const bool in = c < p.C && m < it.rows;
-    const uint16_t *src = static_cast<const uint16_t *>(p.q) + it.b * p.qb + m * p.qm + (it.g * p.G + h) * p.qh + 16 * tq;
-    uint16_t raw[D / 64][16];
+    constexpr int kLanes = D / 16, kCols = 32 / kLanes;              // lanes (16 elements each) of a column, columns at once
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e0 = lane % kLanes;
 #pragma unroll
-    for (int i = 0; i < D / 64; ++i) {
+    for (int u = 0; u < (8 * NT / kCols + kWarps - 1) / kWarps; ++u) {
+        const int col = (u * kWarps + warp) * kCols + lane / kLanes, c = it.cp * 8 * NT + col;
+        if ((u * kWarps + warp) * kCols >= 8 * NT) break;
+        int h = c;
+        const int m = p.by_group.by(h);
+        const bool in = c < p.C && m < it.rows;
+        const uint16_t *src = static_cast<const uint16_t *>(p.q) + it.b * p.qb + m * p.qm + (it.g * p.G + h) * p.qh + 16 * e0;
+        uint16_t raw[16];
         if (p.qvec) {
             const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-            *reinterpret_cast<uint4 *>(raw[i]) = in ? __ldg(reinterpret_cast<const uint4 *>(src + 64 * i)) : zero;
-            *reinterpret_cast<uint4 *>(raw[i] + 8) = in ? __ldg(reinterpret_cast<const uint4 *>(src + 64 * i + 8)) : zero;
+            *reinterpret_cast<uint4 *>(raw) = in ? __ldg(reinterpret_cast<const uint4 *>(src)) : zero;
+            *reinterpret_cast<uint4 *>(raw + 8) = in ? __ldg(reinterpret_cast<const uint4 *>(src) + 1) : zero;
         } else {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) raw[i][j] = in ? __ldg(src + 64 * i + j) : (uint16_t)0;
+            for (int j = 0; j < 16; ++j) raw[j] = in ? __ldg(src + j) : (uint16_t)0;
         }
-    }
-    auto value = [&](int i, int j) {
-        return p.f16 ? __half2float(__ushort_as_half(raw[i][j])) : __uint_as_float((uint32_t)raw[i][j] << 16);
-    };
-    float a = 0.f;
+        float v[16], a = 0.f;
 #pragma unroll
-    for (int i = 0; i < D / 64; ++i)
+        for (int j = 0; j < 16; ++j) {
+            v[j] = p.f16 ? __half2float(__ushort_as_half(raw[j])) : __uint_as_float((uint32_t)raw[j] << 16);
+            a = fmaxf(a, fabsf(v[j]));
+        }
 #pragma unroll
-        for (int j = 0; j < 16; ++j) a = fmaxf(a, fabsf(value(i, j)));
-    a = fmaxf(a, __shfl_xor_sync(0xFFFFFFFFu, a, 1));
-    a = fmaxf(a, __shfl_xor_sync(0xFFFFFFFFu, a, 2));
-    const int e = (int)(__float_as_uint(a) >> 23) - 127;
-    const bool odd = a == 0.f || e == 128;                       // zero or infinite: as it is
-    const int up = odd ? 0 : max(-126, min(126, 12 - e));
-    const float f = pow2f(up);
-#pragma unroll
-    for (int i = 0; i < D / 64; ++i)
+        for (int o = kLanes / 2; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
+        const int e = (int)(__float_as_uint(a) >> 23) - 127;
+        const bool odd = a == 0.f || e == 128;                       // zero or infinite: as it is
+        const int up = odd ? 0 : max(-126, min(126, 12 - e));
+        const float f = pow2f(up);
+        uint32_t w[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const int x = FMT == MOE_KV8_INT8 ? 4 * (j >> 1) + (j & 1) : 2 * j, y = FMT == MOE_KV8_INT8 ? x + 2 : x + 1;
-            const __half2 t = __floats2half2_rn(value(i, x) * f, value(i, y) * f);
-            b[4 * i + (j >> 1)][j & 1] = *reinterpret_cast<const uint32_t *>(&t);
+            const __half2 t = __floats2half2_rn(v[x] * f, v[y] * f);
+            w[j] = *reinterpret_cast<const uint32_t *>(&t);
         }
-    return pow2f(-up);
+        // elements 64 i + 16 t ..: k-steps 4 i .. 4 i + 3 of lane (column, t)
+        uint4 *dst = qs + ((col / 8 * (D / 16) + 4 * (e0 / 4)) / 2) * 32 + col % 8 * 4 + e0 % 4;
+        dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        dst[32] = make_uint4(w[4], w[5], w[6], w[7]);
+        if (e0 == 0) qf[col] = __fmul_rn(p.scale_log2, pow2f(-up));
+    }
 }
 
 template <int FMT, int D, int NT>
@@ -239,15 +250,15 @@ __global__ void __launch_bounds__(kThreads, Lay<D, NT>::ctas) kv8_chunk_kernel(c
     constexpr int R = 256 / D, TK = 16 * R, KS = D / 16, NC = 8 * NT;   // KS: k-steps of S, m-tiles of O
     extern __shared__ __align__(128) uint8_t sm[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, tq = lane & 3;
-    int *first = reinterpret_cast<int *>(sm + L::first), *seq = reinterpret_cast<int *>(sm + L::seq);
+    int *first = reinterpret_cast<int *>(sm + L::first);
+    Item *items = reinterpret_cast<Item *>(sm + L::items);          // the nth in slot n mod 4
     float2 *red_ml = reinterpret_cast<float2 *>(sm + L::ml), *red_unit = reinterpret_cast<float2 *>(sm + L::unit);
     const int passes = (p.C + NC - 1) / NC;
 
+    after_previous();
+    int claim = 0;                     // thread 0: the item after next
+    if (tid == 0) claim = gridDim.x + (p.counter ? atomicAdd(p.counter, 1) : (int)blockIdx.x);
     // chunks before each sequence's
-    if (tid == 0) {
-        seq[0] = blockIdx.x;
-        seq[1] = gridDim.x + (p.counter ? atomicAdd(p.counter, 1) : (int)blockIdx.x);
-    }
     for (int b = tid; b < p.B; b += kThreads) {
         int p0;
         bool bad;
@@ -275,8 +286,14 @@ __global__ void __launch_bounds__(kThreads, Lay<D, NT>::ctas) kv8_chunk_kernel(c
     __syncthreads();
     const int total = first[p.B] * p.Hkv * passes;
     if ((int)blockIdx.x >= total) return;
+    if (warp == 0) {
+        const int second = __shfl_sync(0xFFFFFFFFu, claim, 0);
+        if (lane < 2) items[lane] = decode_item(p, first, lane ? second : (int)blockIdx.x, total);
+    }
+    uint4 *const qs = reinterpret_cast<uint4 *>(sm + L::q);
+    float *const qf = reinterpret_cast<float *>(sm + L::qf);
+    __syncthreads();
 
-    asm volatile("griddepcontrol.launch_dependents;");               // the merge may start, and waits for the results
     uint8_t *ring = sm + L::ring + warp * kStages * kStageBytes;
     const uint32_t ring_u = smem_u32(ring);
 
@@ -294,26 +311,23 @@ __global__ void __launch_bounds__(kThreads, Lay<D, NT>::ctas) kv8_chunk_kernel(c
     uint64_t policy;
     if (p.streams) asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
     else asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
-    int nth = 0, ld_nth = 0, ld_item = blockIdx.x, ld_t = 0, ld_k1 = 0, ld_stage = 0, free_slots = kStages;
+    int nth = 0, ld_nth = -1, ld_t = 0, ld_k1 = 0, ld_stage = 0, free_slots = kStages;
     const uint8_t *ld_k = nullptr, *ld_v = nullptr;
     const float *ld_s = nullptr;
-    auto open_item = [&]() {
-        const Item x = decode_item(p, first, ld_item);
-        const size_t head = (size_t)x.b * p.Hkv + x.g;
-        ld_t = x.k0 + warp * TK;
-        ld_k1 = x.k1;
-        ld_k = p.k + (head * p.T_cap + ld_t) * D + lane * 16;
-        ld_v = p.v + (head * p.T_cap + ld_t) * D + lane * 16;
-        ld_s = (lane & 1 ? p.vs : p.ks) + head * p.nblk;
-    };
-    open_item();
+    bool ld_more = true;
     auto fill = [&]() {
         while (free_slots > 0) {
             while (ld_t >= ld_k1) {
-                if (ld_nth > nth || ld_item >= total) return;
-                ld_item = seq[++ld_nth & 3];
-                if (ld_item >= total) return;
-                open_item();
+                if (ld_nth > nth || !ld_more) return;
+                const Item x = items[++ld_nth & 3];
+                ld_more = x.b >= 0;
+                if (!ld_more) return;
+                const size_t head = (size_t)x.b * p.Hkv + x.g;
+                ld_t = x.k0 + warp * TK;
+                ld_k1 = x.k1;
+                ld_k = p.k + (head * p.T_cap + ld_t) * D + lane * 16;
+                ld_v = p.v + (head * p.T_cap + ld_t) * D + lane * 16;
+                ld_s = (lane & 1 ? p.vs : p.ks) + head * p.nblk;
             }
             const uint32_t dst = ring_u + ld_stage * kStageBytes;
             if (ld_t + TK <= ld_k1) {
@@ -346,25 +360,8 @@ __global__ void __launch_bounds__(kThreads, Lay<D, NT>::ctas) kv8_chunk_kernel(c
     };
     static_assert(kStages == 2, "stages alternate");
     fill();
-
-    // Queries of an item into shared memory (wide form): warp n column tile n
-    uint4 *const qs = reinterpret_cast<uint4 *>(sm + L::q);
-    float *const qf = reinterpret_cast<float *>(sm + L::qf);
-    auto stage_q = [&](const Item &x) {
-        if (warp < NT) {
-            uint32_t b[KS][2];
-            const float back = __fmul_rn(p.scale_log2, load_q<FMT, D>(p, x, x.cp * NC + 8 * warp + gq, tq, b));
-#pragma unroll
-            for (int k = 0; k < KS; k += 2)
-                qs[(warp * KS + k) * 16 + lane] = make_uint4(b[k][0], b[k][1], b[k + 1][0], b[k + 1][1]);
-            if (tq == 0) qf[8 * warp + gq] = back;
-        }
-    };
-    Item it = decode_item(p, first, blockIdx.x);
-    if (L::wide) {
-        stage_q(it);
-        __syncthreads();
-    }
+    stage_q<FMT, D, NT>(p, items[0], qs, qf);
+    __syncthreads();
 
     // A lane's reads of a tile: chunk 4 i + t of key rows g and g + 8 (the
     // swap turns i even into i + 1 and back in odd rows), 16 (8) bytes of
@@ -374,31 +371,26 @@ __global__ void __launch_bounds__(kThreads, Lay<D, NT>::ctas) kv8_chunk_kernel(c
     int stage = 0;
 #pragma unroll 1
     for (;;) {
-        int after = 0;                 // the item after next
-        if (!L::wide && warp == kWarps - 1 && seq[(nth + 1) & 3] < total) {
-            // the next item's queries into L1: 128-byte lines of its columns
-            const Item x = decode_item(p, first, seq[(nth + 1) & 3]);
-            for (int i = lane; i < NC * D / 64; i += 32) {
-                int h = x.cp * NC + i / (D / 64);
-                const bool in = h < p.C;
-                const int m = p.by_group.by(h);
-                if (in)
-                    asm volatile("prefetch.global.L1 [%0];" ::"l"(static_cast<const uint16_t *>(p.q) + x.b * p.qb + m * p.qm +
-                                                                  (x.g * p.G + h) * p.qh + i % (D / 64) * 64));
-            }
-        }
-        if (tid == 0) after = p.counter ? gridDim.x + atomicAdd(p.counter, 1) : seq[(nth + 1) & 3] + gridDim.x;
+        const Item it = items[nth & 3];
+        if (tid == 0) claim = p.counter ? gridDim.x + atomicAdd(p.counter, 1) : claim + gridDim.x;
         float f[NT][2], m[NT][2], l[NT][2], o[NT][KS][4], vref = 0.f, inv_vref = 0.f;
         bool fresh = true;             // no tile yet: m = -inf, everything else 0
         uint32_t qr[L::wide ? 1 : NT][L::wide ? 1 : KS][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            float back = 0.f;
-            if constexpr (!L::wide) back = __fmul_rn(p.scale_log2, load_q<FMT, D>(p, it, it.cp * NC + 8 * n + gq, tq, qr[n]));
+            if constexpr (!L::wide) {
+#pragma unroll
+                for (int k = 0; k < KS; k += 2) {
+                    const uint4 x = qs[(n * KS + k) * 16 + lane];
+                    qr[n][k][0] = x.x;
+                    qr[n][k][1] = x.y;
+                    qr[n][k + 1][0] = x.z;
+                    qr[n][k + 1][1] = x.w;
+                }
+            }
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                // of the columns that the lane's scores belong to
-                f[n][c] = L::wide ? qf[8 * n + 2 * tq + c] : __shfl_sync(0xFFFFFFFFu, back, 4 * (2 * tq + c));
+                f[n][c] = qf[8 * n + 2 * tq + c];
                 m[n][c] = -INFINITY;
                 l[n][c] = 0.f;
             }
@@ -602,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, Lay<D, NT>::ctas) kv8_chunk_kernel(c
 
         // ---- the chunk's result from the warps' that had a tile
         const int having = min(kWarps, (it.k1 - it.k0 + TK - 1) / TK), cols = min(NC, p.C - it.cp * NC);
-        const size_t slot = (((size_t)it.b * p.nchunk + it.k0 / p.chunk) * p.Hkv + it.g) * passes + it.cp;
+        const size_t slot = (((size_t)it.b * p.nchunk + it.nth) * p.Hkv + it.g) * passes + it.cp;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -614,7 +606,6 @@ __global__ void __launch_bounds__(kThreads, Lay<D, NT>::ctas) kv8_chunk_kernel(c
                 if (gq == 0) red_ml[warp * NC + 8 * n + 2 * tq + c] = make_float2(m[n][c], x);
             }
         if (lane == 0) red_unit[warp] = make_float2(__fmul_rn(vref, 1.f / kWeightUnit), __int_as_float(stage ^ 1));
-        if (tid == 0) seq[(nth + 2) & 3] = after;
         constexpr int kAll = NT * KS, kRound = kAll < 16 ? kAll : 16;    // m-tiles, and of them a slot's worth
 #pragma unroll
         for (int h = 0; h < kAll / kRound; ++h) {
@@ -627,9 +618,10 @@ __global__ void __launch_bounds__(kThreads, Lay<D, NT>::ctas) kv8_chunk_kernel(c
                 }
             }
             __syncthreads();
-            if (L::wide && h == 0) {                               // every warp is done with the queries
-                const int ni = seq[(nth + 1) & 3];
-                if (ni < total) stage_q(decode_item(p, first, ni));
+            if (h == 0) {                                          // every warp is done with the item and its queries
+                if (tid == 0) items[(nth + 2) & 3] = decode_item(p, first, claim, total);
+                const Item x = items[(nth + 1) & 3];
+                if (x.b >= 0) stage_q<FMT, D, NT>(p, x, qs, qf);
             }
             constexpr int kShare = kRound / kWarps;                // m-tiles a warp adds up, of one column tile
             const int x0 = h * kRound + warp * kShare, n = x0 / KS;
@@ -676,9 +668,7 @@ __global__ void __launch_bounds__(kThreads, Lay<D, NT>::ctas) kv8_chunk_kernel(c
             }
             __syncthreads();
         }
-        const int ni = seq[++nth & 3];
-        if (ni >= total) break;
-        it = decode_item(p, first, ni);
+        if (items[++nth & 3].b < 0) break;
         fill();
     }
     cp_wait<0>();
@@ -732,8 +722,7 @@ __global__ void __launch_bounds__(kMergeThreads) kv8_merge_kernel(const AttnP p,
     bool bad;
     const int rows = kv8_rows(p.pos, p.counts, b, p.M, p.T_cap, p0, bad);
     const int n = rows > 0 ? p0 + rows : 0, nch = (n + p.chunk - 1) / p.chunk;
-    asm volatile("griddepcontrol.launch_dependents;");
-    asm volatile("griddepcontrol.wait;" ::: "memory");              // the chunks' results
+    after_previous();                                                // the chunks' results
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     const bool on = 8 * ct + 2 * tq < p.C;
@@ -813,7 +802,10 @@ __global__ void __launch_bounds__(kAccThreads) kv8_weights_kernel(const AttnP p)
     bool bad;
     const int rows = kv8_rows(p.pos, p.counts, b, p.M, p.T_cap, p0, bad);
     const int n = rows > 0 ? p0 + rows : 0, t0 = blockIdx.x * kAccSpan + tid;
-    if (t0 - tid >= n) return;
+    if (t0 - tid >= n) {
+        after_previous();
+        return;
+    }
     const size_t head = (size_t)b * p.Hkv + g;
     // what does not come from the merge is loaded ahead of it
     float a[kAccPer];
@@ -822,7 +814,7 @@ __global__ void __launch_bounds__(kAccThreads) kv8_weights_kernel(const AttnP p)
         const int t = t0 + i * kAccThreads;
         a[i] = t < min(p0, n) && p.acc_in ? p.decay * p.acc_in[head * p.T_cap + t] : 0.f;
     }
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    after_previous();
     for (int i = tid; i < 2 * p.C; i += kAccThreads) st[i] = __ldcg(p.fin + head * p.C * 2 + i);
     __syncthreads();
     const float *sc = p.sc + (head * p.T_cap + t0) * p.C;
@@ -984,7 +976,7 @@ int launch_kv8_attn(const moe_kv8 &c, const moe_rows &q, int M, const int32_t *p
             e = cudaMemsetAsync(p.counter, 0, sizeof(int), stream);
             if (e != cudaSuccess) return;
         }
-        kernel<<<grid, kThreads, smem, stream>>>(p);
+        e = launch_after(kernel, dim3(grid), kThreads, smem, 0, stream, p);
     };
 #define KV8_GO(F, D, N)                                                                      \
     do {                                                                                     \
@@ -1016,39 +1008,17 @@ int launch_kv8_attn(const moe_kv8 &c, const moe_rows &q, int M, const int32_t *p
     {
         int shares = 1;
         while (shares < kMergeShares && p.nchunk > 32 * shares) shares *= 2;
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(shares * (c.head_dim / 32) * ((p.C + 7) / 8), p.Hkv, p.B);
-        cfg.blockDim = dim3(kMergeThreads);
-        cfg.stream = stream;
-        cudaLaunchAttribute at[2];
-        at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        at[0].val.programmaticStreamSerializationAllowed = 1;
-        at[1].id = cudaLaunchAttributeClusterDimension;
-        at[1].val.clusterDim.x = shares;
-        at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
-        cfg.attrs = at;
-        cfg.numAttrs = 2;
-        e = cudaLaunchKernelEx(&cfg, kv8_merge_kernel, p, c.head_dim, shares);
+        e = launch_after(kv8_merge_kernel, dim3(shares * (c.head_dim / 32) * ((p.C + 7) / 8), p.Hkv, p.B), kMergeThreads, 0, shares,
+                         stream, p, c.head_dim, shares);
         if (e != cudaSuccess) { note_cuda_error((int)e); return MOE_ERR_CUDA; }
     }
     note_launch();
     if (acc) {
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((c.T_cap + kAccSpan - 1) / kAccSpan, p.Hkv, p.B);
-        cfg.blockDim = dim3(kAccThreads);
-        cfg.dynamicSmemBytes = p.C * 2 * sizeof(float);
-        cfg.stream = stream;
-        cudaLaunchAttribute at[1];
-        at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        at[0].val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = at;
-        cfg.numAttrs = 1;
-        e = cudaLaunchKernelEx(&cfg, kv8_weights_kernel, p);
+        e = launch_after(kv8_weights_kernel, dim3((c.T_cap + kAccSpan - 1) / kAccSpan, p.Hkv, p.B), kAccThreads,
+                         p.C * 2 * (int)sizeof(float), 0, stream, p);
         if (e != cudaSuccess) { note_cuda_error((int)e); return MOE_ERR_CUDA; }
         note_launch();
     }
-    e = cudaGetLastError();
-    if (e != cudaSuccess) { note_cuda_error((int)e); return MOE_ERR_CUDA; }
     return MOE_OK;
 }
 
