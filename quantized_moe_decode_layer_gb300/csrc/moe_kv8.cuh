@@ -173,8 +173,8 @@ __device__ __forceinline__ float cta_max(float v, float *red)
 // the wait, so that a kernel's end means the end of all before it.
 __device__ __forceinline__ void after_previous()
 {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 template <typename... P, typename... A>
