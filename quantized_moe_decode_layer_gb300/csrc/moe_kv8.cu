@@ -444,7 +444,8 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 1 : 3) kv8_move_kern
     const int r = threadIdx.x & (q.threads - 1), step = p.blk >> 2;
     q.row = r / (p.D >> 4);
     q.d = r % (p.D >> 4) * 16;
-    after_previous();
+    place_next();
+    wait_for_previous();
     const int kept = __ldcg(p.lens_out + b), j = blockIdx.x * (THREADS / q.threads) + q.j, i0 = j * p.blk;
     if ((int)(blockIdx.x * (THREADS / q.threads)) * p.blk >= kept) return;
     const size_t head = (size_t)b * p.Hkv + g;

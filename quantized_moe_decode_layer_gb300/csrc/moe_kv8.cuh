@@ -168,13 +168,18 @@ __device__ __forceinline__ float cta_max(float v, float *red)
 }
 
 // Every kernel of the cache is launched as a dependent of the one before it on
-// the stream: its CTAs may be placed while that one ends, wait here for all of
-// its results, and let their own dependents be placed.  No CTA leaves without
-// the wait, so that a kernel's end means the end of all before it.
+// the stream: its CTAs may be placed while that one ends.  A call's first
+// kernel waits before anything else, and only then lets the next be placed
+// (after_previous); so when a call's later kernel runs, whatever came before
+// the call is complete, and it may read the call's inputs ahead of its own
+// wait (wait_for_previous) for what the call's earlier kernels write.  No CTA
+// leaves without the wait: a kernel's end means the end of all before it.
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void place_next() { asm volatile("griddepcontrol.launch_dependents;"); }
 __device__ __forceinline__ void after_previous()
 {
-    asm volatile("griddepcontrol.launch_dependents;");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_for_previous();
+    place_next();
 }
 
 template <typename... P, typename... A>

@@ -713,6 +713,7 @@ __global__ void __launch_bounds__(kMergeThreads) kv8_merge_kernel(const AttnP p,
 {
     __shared__ float4 so[8][32], sml[8][32];
     __shared__ float4 co[kMergeShares][64], cml[kMergeShares][64];   // the shares' results, in the cluster's first CTA
+    place_next();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, tq = lane & 3;
     const int KS = D / 16, nt = kv8_nt(p.C, D), NC = 8 * nt, passes = (p.C + NC - 1) / NC;
     // blockIdx.x: share, then pair of m-tiles, then column tile
@@ -722,7 +723,7 @@ __global__ void __launch_bounds__(kMergeThreads) kv8_merge_kernel(const AttnP p,
     bool bad;
     const int rows = kv8_rows(p.pos, p.counts, b, p.M, p.T_cap, p0, bad);
     const int n = rows > 0 ? p0 + rows : 0, nch = (n + p.chunk - 1) / p.chunk;
-    after_previous();                                                // the chunks' results
+    wait_for_previous();                                             // the chunks' results
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     const bool on = 8 * ct + 2 * tq < p.C;
@@ -797,13 +798,14 @@ constexpr int kAccThreads = 256, kAccPer = 4, kAccSpan = kAccThreads * kAccPer;
 __global__ void __launch_bounds__(kAccThreads) kv8_weights_kernel(const AttnP p)
 {
     extern __shared__ float st[];   // [C][2]: reference, 1 / sum
+    place_next();
     const int g = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
     int p0;
     bool bad;
     const int rows = kv8_rows(p.pos, p.counts, b, p.M, p.T_cap, p0, bad);
     const int n = rows > 0 ? p0 + rows : 0, t0 = blockIdx.x * kAccSpan + tid;
     if (t0 - tid >= n) {
-        after_previous();
+        wait_for_previous();
         return;
     }
     const size_t head = (size_t)b * p.Hkv + g;
@@ -814,7 +816,7 @@ __global__ void __launch_bounds__(kAccThreads) kv8_weights_kernel(const AttnP p)
         const int t = t0 + i * kAccThreads;
         a[i] = t < min(p0, n) && p.acc_in ? p.decay * p.acc_in[head * p.T_cap + t] : 0.f;
     }
-    after_previous();
+    wait_for_previous();
     for (int i = tid; i < 2 * p.C; i += kAccThreads) st[i] = __ldcg(p.fin + head * p.C * 2 + i);
     __syncthreads();
     const float *sc = p.sc + (head * p.T_cap + t0) * p.C;

@@ -582,3 +582,40 @@ def test_evict_far_apart_steps_and_zeros(fmt):
     acc[0, 1, 33:64] += 2.0
     check_evict(cache, [256], acc, 40, 0, 0)
     check_evict(cache, [256], 3 - acc, 100, 2, 5)
+
+
+@pytest.mark.parametrize("T,lens", [(512, [300, 64, 1]), (40960, [30000, 12, 40900])])
+def test_calls_in_a_row_equal_calls_waited_for(T, lens):
+    """Steps enqueued without a wait, each reading what the ones before wrote (rows,
+    lengths, weights in place, kept positions), give the bits of the same steps
+    with the device waited for after every call."""
+    B, Hq, G, D = 3, 8, 2, 128
+    out = []
+    for wait in (True, False):
+        cache, r = filled(B, Hq, G, D, T, 32, "int8", lens, 29, weights=True)
+        dst = moe.KV8Cache(256, batch=B, q_heads=Hq, kv_heads=G, head_dim=D, block=32)
+        pos, acc, dacc = i32(lens), torch.zeros((B, G, T), device=DEV), torch.zeros((B, G, 256), device=DEV)
+        steps = [(rows(r, B, 1, G, D), rows(r, B, 1, G, D), rows(r, B, 1, Hq, D, size=2.0)) for _ in range(25)]
+        torch.cuda.synchronize()
+        got = []
+
+        def done():
+            if wait:
+                torch.cuda.synchronize()
+        for k, v, q in steps:
+            cache.append(k, v, pos)
+            done()
+            o, _ = cache.attend(q, pos, acc=acc, decay=0.97)
+            done()
+            pos.add_(1)
+            done()
+            idx, n = cache.evict_into(dst, pos, acc, 200, sinks=2, recent=5, dst_acc=dacc)
+            done()
+            kv = dst.read(None, 200, lens=n)
+            done()
+            got += [o, idx, *kv]
+        torch.cuda.synchronize()
+        assert err_of(cache) == 0
+        out.append(got + [acc, dacc])
+    for x, y in zip(*out):
+        assert torch.equal(x, y)
