@@ -138,6 +138,13 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// The first of a chain: nothing to add to.
+__device__ __forceinline__ void mma_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ uint32_t movtrans(uint32_t a)
 {
     uint32_t d;
@@ -411,12 +418,9 @@ __global__ void __launch_bounds__(kThreads, Lay<D, NT>::ctas) kv8_chunk_kernel(c
             float s[R][NT][4];
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                float acc[NT][2][4];
+                constexpr int kChains = D == 64 ? 1 : 2;           // of 4 to 8 MMAs that wait on one another
+                float acc[NT][kChains][4];
                 uint4 qw[NT];
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) acc[n][0][c] = acc[n][1][c] = 0.f;
 #pragma unroll
                 for (int i = 0; i < D / 64; ++i) {
                     const uint8_t *src = kt + (i & 1 ? k_odd : k_even) + 16 * r * D + 64 * i;
@@ -434,8 +438,18 @@ __global__ void __launch_bounds__(kThreads, Lay<D, NT>::ctas) kv8_chunk_kernel(c
                         pairs<FMT>(ww[j], a1, a3);
 #pragma unroll
                         for (int n = 0; n < NT; ++n)
-                            if constexpr (L::wide) mma(acc[n][j & 1], a0, a1, a2, a3, j & 1 ? qw[n].z : qw[n].x, j & 1 ? qw[n].w : qw[n].y);
-                            else mma(acc[n][j & 1], a0, a1, a2, a3, qr[n][4 * i + j][0], qr[n][4 * i + j][1]);
+                        {
+                            uint32_t b0, b1;
+                            if constexpr (L::wide) {
+                                b0 = j & 1 ? qw[n].z : qw[n].x;
+                                b1 = j & 1 ? qw[n].w : qw[n].y;
+                            } else {
+                                b0 = qr[n][4 * i + j][0];
+                                b1 = qr[n][4 * i + j][1];
+                            }
+                            if (4 * i + j < kChains) mma_first(acc[n][j % kChains], a0, a1, a2, a3, b0, b1);
+                            else mma(acc[n][j % kChains], a0, a1, a2, a3, b0, b1);
+                        }
                     }
                 }
                 const float ks = steps[2 * r];
@@ -443,23 +457,24 @@ __global__ void __launch_bounds__(kThreads, Lay<D, NT>::ctas) kv8_chunk_kernel(c
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
-                        s[r][n][c] = __fmul_rn(__fadd_rn(acc[n][0][c], acc[n][1][c]), __fmul_rn(ks, f[n][c & 1]));
+                        s[r][n][c] = __fmul_rn(kChains == 1 ? acc[n][0][c] : __fadd_rn(acc[n][0][c], acc[n][kChains - 1][c]),
+                                               __fmul_rn(ks, f[n][c & 1]));
             }
             if (p.sc) {
-                float *sc = p.sc + (((size_t)it.b * p.Hkv + it.g) * p.T_cap + t0) * p.C + it.cp * NC;
+                float *dst = p.sc + (((size_t)it.b * p.Hkv + it.g) * p.T_cap + t0 + gq) * p.C + it.cp * NC + 2 * tq;
+                const int end = it.k1 - t0 - gq, cols = p.C - it.cp * NC - 2 * tq, step = 8 * p.C;
+                const bool two = !(p.C & 1);                       // pairs are aligned, and whole
 #pragma unroll
                 for (int r = 0; r < R; ++r)
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
+                    for (int c = 0; c < 4; c += 2, dst += step)
 #pragma unroll
-                        for (int c = 0; c < 4; c += 2) {
-                            const int row = 16 * r + gq + 4 * c, col = 8 * n + 2 * tq;
-                            if (t0 + row >= it.k1 || it.cp * NC + col >= p.C) continue;
-                            float *dst = sc + (size_t)row * p.C + col;
-                            if (!(p.C & 1)) *reinterpret_cast<float2 *>(dst) = make_float2(s[r][n][c], s[r][n][c + 1]);
+                        for (int n = 0; n < NT; ++n) {
+                            if (16 * r + 4 * c >= end || 8 * n >= cols) continue;
+                            if (two) *reinterpret_cast<float2 *>(dst + 8 * n) = make_float2(s[r][n][c], s[r][n][c + 1]);
                             else {
-                                dst[0] = s[r][n][c];
-                                if (it.cp * NC + col + 1 < p.C) dst[1] = s[r][n][c + 1];
+                                dst[8 * n] = s[r][n][c];
+                                if (8 * n + 1 < cols) dst[8 * n + 1] = s[r][n][c + 1];
                             }
                         }
             }
