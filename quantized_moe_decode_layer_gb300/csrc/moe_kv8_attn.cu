@@ -873,27 +873,38 @@ __global__ void __launch_bounds__(kAccThreads) kv8_weights_kernel(const AttnP p)
         if (t0 + i * kAccThreads < n) p.acc[head * p.T_cap + t0 + i * kAccThreads] = a[i];
 }
 
-// Positions per chunk: r tiles a warp.  The chunks of a full cache are taken
-// by the 456 CTA slots of 152 SMs; the end of one costs about D / 100 tiles
-// (joining D dimensions and expanding the next queries), and half a chunk is lost
-// where the last ones end.  Of the r that come within 3% of the least cost
-// the smallest is taken: caches are seldom full.  (8 x 128K of 256: r = 8,
-// 10, 16 take 182, 177, 167 us; 32 of up to 16K of 128: 92, 97, 106.)  A rule of
-// the cache's shape alone.
+// Positions per chunk: r tiles a warp, from the cache's shape alone.  152 SMs
+// take three CTAs each, and the end of a chunk costs about two tiles (8 x 8K of
+// 256 to 8 x 24K of 64, r = 1 and 2: 1.1 to 4).  One sequence is taken as full: its
+// chunks run in waves of 456, of which the last takes 0.45 (0.7) of a wave's
+// time when it has at most one (two) for an SM.  Of a batch three quarters are taken as
+// full, and half a chunk's time for where the last ones end.  (One of 40K
+// of 256, r = 3, 5, 10: 19, 20, 20 us, four rows 38, 33, 29; of 132K, r = 5, 8,
+// 10: 38, 44, 34; 16 of up to 16K of 128, r = 4, 6, 10: 80, 71, 76; 8 of up to
+// 128K of 256, r = 8, 10, 16: 182, 177, 167.)
 int kv8_chunk(const moe_kv8 &c)
 {
-    const int choice[] = {1, 2, 3, 4, 5, 6, 8, 10, 16}, round = kWarps * kTileBytes / c.head_dim;
-    long long cost[9], least = LLONG_MAX;                            // in tenths of a tile, per slot
-    for (int i = 0; i < 9; ++i) {
-        const int r = choice[i];
-        const long long chunks = (long long)c.batch * c.kv_heads * ((c.T_cap + r * round - 1) / (r * round));
-        const long long one = 10 * r + c.head_dim / 10;
-        cost[i] = chunks <= 3 * 456 ? (chunks + 455) / 456 * one : chunks * one / 456 + 5 * r;
-        least = std::min(least, cost[i]);
+    const int round = kWarps * kTileBytes / c.head_dim;
+    const long long heads = (long long)c.batch * c.kv_heads, slots = 456;
+    long long least = LLONG_MAX;                                     // in twentieths of a tile
+    int best = 1;
+    for (const int r : {1, 2, 3, 4, 5, 6, 8, 10, 16}) {
+        const long long one = 20 * (r + 2);
+        long long cost;
+        if (c.batch == 1) {
+            const long long n = heads * ((c.T_cap + r * round - 1) / (r * round)), rest = n % slots;
+            cost = n / slots * one + (rest == 0 ? 0 : rest <= 152 ? one * 9 / 20 : rest <= 304 ? one * 14 / 20 : one);
+        } else {
+            // chunks in quarters of a head's: 3/4 of its capacity and half a chunk
+            const long long n4 = heads * (3LL * c.T_cap / (r * round) + 2);
+            cost = std::max(n4, 4 * slots) * one / (4 * slots) + one / 2;
+        }
+        if (cost <= least) {
+            least = cost;
+            best = r;
+        }
     }
-    for (int i = 0; i < 9; ++i)
-        if (cost[i] * 100 <= least * 103) return choice[i] * round;
-    return round;
+    return best * round;
 }
 
 // Once per kernel and device.
