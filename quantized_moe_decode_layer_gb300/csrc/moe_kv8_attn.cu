@@ -10,8 +10,10 @@
 // Split: the positions are cut into chunks whose size is a rule of the cache
 // alone (kv8_chunk), so a row's result depends neither on the other rows nor
 // on the other sequences.  A chunk yields, per query column (row and head of
-// a key/value head's group), the maximum, the sum of exp(s - max) and the
-// unnormalised output; the merge kernel joins a row's chunks in order.
+// a key/value head's group), a reference exponent near its maximum, the sum
+// of exp(s - reference) and the unnormalised output; the merge kernel joins a
+// row's chunks in an order that is fixed as well.  What only other rows see
+// (later positions of the same call) adds exact zeros.
 #include <algorithm>
 #include <climits>
 #include <mutex>
@@ -57,13 +59,19 @@ struct AttnP {
 
 // ------------------------------------------------------------------ chunks
 // Persistent CTAs of 4 warps, three on an SM, take (sequence, chunk,
-// key/value head, column pass) items; long runs take them from a counter, as
-// SMs that share a GPC's port with fewer others run a tenth faster.  Within a
-// chunk a warp works alone on tiles of 16 R positions (R = 256 / D: 4 KB of
-// keys and 4 KB of values), every fourth one, through a ring of two tiles of
-// its own that cp.async fills ahead, across items.  At the end of a chunk the
-// warps join their outputs through the ring slots that their last tiles
-// left, while the other slots and the other CTAs keep the loads going.
+// key/value head, column pass) items, in turn or, in long runs, from a counter
+// (8 x 128K of 256: 162 us against 168).  Within a chunk a warp works alone on
+// tiles of 16 R positions (R = 256 / D: 4 KB of keys and 4 KB of values), every
+// fourth one, through a ring of two tiles of its own that cp.async fills
+// ahead, across items.  At the end of a chunk the warps join their outputs
+// through the ring slots that their last tiles left, while the other slots and
+// the other CTAs keep the loads going.  (Warps with chunks of their own, 12 to
+// an SM, wrote four times the results and took 183 us where this took 163.)
+//
+// Bound, at 8 columns: the read of the cache (8 x 128K of 256: 1.07 GB of
+// capacity, 86% of the copy bandwidth over the whole call) and, for int8,
+// issuing the 650 instructions that 8 KB of codes take; below some 100 MB the
+// launches, the first loads and the last chunks (8 us) weigh as much.
 //
 // Per 16 positions and 8 query columns, on m16n8k16 fp16 MMAs:
 //     S^T [16 positions x 8] = K Q^T,   O^T [D x 8] += V^T P^T.
@@ -493,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, Lay<D, NT>::ctas) kv8_chunk_kernel(c
                         }
                     }
             }
-            // ---- reference exponents; the values' largest step so far is the unit of the output
+            // ---- reference exponents
             float mn[NT][2];
             bool grew = false;
 #pragma unroll
@@ -509,35 +517,23 @@ __global__ void __launch_bounds__(kThreads, Lay<D, NT>::ctas) kv8_chunk_kernel(c
                     mn[n][c] = x > m[n][c] + kSlack ? x : m[n][c];
                     grew |= mn[n][c] != m[n][c];
                 }
-            float vmax = steps[1];
-#pragma unroll
-            for (int r = 1; r < R; ++r) vmax = fmaxf(vmax, steps[2 * r + 1]);
             if (fresh) {
                 fresh = false;
-                vref = vmax;
-                inv_vref = vmax > 0.f ? 1.f / vmax : 0.f;
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int c = 0; c < 2; ++c) m[n][c] = mn[n][c];      // from -inf: the maximum itself
-            } else if (__any_sync(0xFFFFFFFFu, grew) || vmax > vref) {
-                float down = 1.f;
-                if (vmax > vref) {
-                    inv_vref = 1.f / vmax;
-                    down = __fmul_rn(vref, inv_vref);
-                    vref = vmax;
-                }
+            } else if (__any_sync(0xFFFFFFFFu, grew)) {
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
                         const float al = mn[n][c] == -INFINITY ? 1.f : ex2(__fsub_rn(m[n][c], mn[n][c]));
                         l[n][c] = __fmul_rn(l[n][c], al);
-                        const float ao = __fmul_rn(al, down);
 #pragma unroll
                         for (int k = 0; k < KS; ++k) {
-                            o[n][k][c] = __fmul_rn(o[n][k][c], ao);
-                            o[n][k][c + 2] = __fmul_rn(o[n][k][c + 2], ao);
+                            o[n][k][c] = __fmul_rn(o[n][k][c], al);
+                            o[n][k][c + 2] = __fmul_rn(o[n][k][c + 2], al);
                         }
                         m[n][c] = mn[n][c];
                     }
@@ -545,8 +541,24 @@ __global__ void __launch_bounds__(kThreads, Lay<D, NT>::ctas) kv8_chunk_kernel(c
             // ---- weights, their sums, and the output
 #pragma unroll
             for (int r = 0; r < R; ++r) {
+                // The output's unit is the largest step of values so far.  It
+                // grows by groups of 16 positions and not by tiles: a group
+                // that only later rows see comes after all that a row sees, and
+                // scales its output exactly.
+                const float vstep = steps[2 * r + 1];
+                if (vstep > vref) {
+                    inv_vref = 1.f / vstep;
+                    const float down = __fmul_rn(vref, inv_vref);
+                    vref = vstep;
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int k = 0; k < KS; ++k)
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) o[n][k][c] = __fmul_rn(o[n][k][c], down);
+                }
                 uint32_t ph[NT][2], pl[NT][2];
-                const float unit = __fmul_rn(__fmul_rn(steps[2 * r + 1], inv_vref), kWeightUnit);
+                const float unit = __fmul_rn(__fmul_rn(vstep, inv_vref), kWeightUnit);
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     float w[4];

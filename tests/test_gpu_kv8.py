@@ -619,3 +619,21 @@ def test_calls_in_a_row_equal_calls_waited_for(T, lens):
         out.append(got + [acc, dacc])
     for x, y in zip(*out):
         assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("D,Hq,G", [(64, 4, 2), (128, 8, 2), (256, 8, 1)])
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_rows_do_not_feel_later_rows_steps(fmt, D, Hq, G):
+    """A call whose last rows' values lie in a block of a far larger step gives its
+    first rows the bits of one-row calls, whose positions end before that block."""
+    T, n = 512, 328                                   # rows 328 .. 335 | 336 ..: blocks of 16, tiles of up to 64
+    cache, r = filled(1, Hq, G, D, T, 16, fmt, [n], 30)
+    k, v = rows(r, 1, 16, G, D), rows(r, 1, 16, G, D)
+    v[:, 8:] *= 3000.0
+    cache.append(k, v, i32([n]))
+    q = rows(r, 1, 8, Hq, D, size=3.0)
+    for first in (n, n + 4, n + 7):
+        all_rows, _ = cache.attend(q, i32([first]))
+        for m in range(8):
+            one, _ = cache.attend(q[:, m:m + 1], i32([first + m]))
+            assert torch.equal(one[:, 0], all_rows[:, m]), (first, m)
