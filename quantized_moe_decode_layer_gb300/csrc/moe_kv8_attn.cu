@@ -108,8 +108,8 @@ __host__ __device__ constexpr int kv8_nt(int C, int D)
 }
 template <int D, int NT>
 struct Lay {
-    static constexpr bool wide = NT * D > 256 || NT > 2;
-    static constexpr int ctas = wide ? 2 : 3, NC = 8 * NT;
+    static constexpr bool wide = NT * D >= 256 || NT > 2;            // queries in shared memory
+    static constexpr int ctas = NT * D > 256 || NT > 2 ? 2 : 3, NC = 8 * NT;
     static constexpr int ring = 0, ml = kWarps * kStages * kStageBytes, unit = ml + kWarps * NC * 8, items = unit + kWarps * 8,
                          q = items + 4 * 32, qf = q + NT * D * 16, first = qf + NC * 4;
     static constexpr int total(int B) { return first + (3 * B + 1) * 4; }   // first[B + 1], then position and rows of each sequence
