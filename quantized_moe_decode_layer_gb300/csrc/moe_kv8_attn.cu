@@ -84,11 +84,12 @@ struct AttnP {
 // keep fp32's precision, and an fp32 output means something.
 //
 // 12 warps on an SM leave 168 registers a thread: the output of 8 columns of
-// 256 dimensions (64) with its queries (32), or 16 of 128, or 16 of 64.  More
-// columns run twice as many at a time, two CTAs on an SM with 255 registers,
-// their queries in shared memory: expanding the codes is most of the work,
-// and it is done once per column pass.  A column's arithmetic is the same
-// either way, to the bit.
+// 256 dimensions (64), or 16 of 128 or 64, the queries in registers where they
+// take 16 or less and in shared memory otherwise.  More columns run twice as
+// many at a time, two CTAs on an SM with 255 registers: expanding the codes is
+// most of the work, and it is done once per column pass.  A column's
+// arithmetic is the same either way, to the bit.  (16 warps with 128 registers
+// and slots of half a tile took 178 us where this takes 163.)
 constexpr int kWarps = 4, kThreads = 32 * kWarps, kStages = 2;
 constexpr int kTileBytes = 4096;                       // keys (or values) of a warp's tile
 constexpr int kStageBytes = 2 * kTileBytes + 64;       // and the steps of its up to 4 groups of 16 positions

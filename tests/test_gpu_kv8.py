@@ -637,3 +637,84 @@ def test_rows_do_not_feel_later_rows_steps(fmt, D, Hq, G):
         for m in range(8):
             one, _ = cache.attend(q[:, m:m + 1], i32([first + m]))
             assert torch.equal(one[:, 0], all_rows[:, m]), (first, m)
+
+
+def test_many_sequences():
+    """More sequences than threads of a CTA and more chunks than CTAs: every
+    sequence's rows against a batched 64-bit softmax."""
+    B, Hq, G, D, T = 700, 8, 4, 64, 128
+    r = gen(31)
+    lens = torch.randint(0, T - 1, (B,), generator=r, device=DEV, dtype=torch.int32)
+    lens[::7] = -1
+    lens[5] = T - 2
+    cache = moe.KV8Cache(T, batch=B, q_heads=Hq, kv_heads=G, head_dim=D, block=16, fmt="int8", max_rows=2, weights=True)
+    cache.append(rows(r, B, T, G, D), rows(r, B, T, G, D), torch.zeros_like(lens))
+    q = rows(r, B, 2, Hq, D, size=1.5)
+    acc = torch.full((B, G, T), -3.0, device=DEV)
+    o, _ = cache.attend(q, lens, acc=acc, acc_in=torch.zeros_like(acc))
+    assert err_of(cache) == 0
+    k, v = (t.double().transpose(1, 2) for t in cache.read(None, T))                 # [B, G, T, D]
+    s = torch.einsum("bmghd,bgtd->bgmht", q.double().view(B, 2, G, Hq // G, D), k) * D ** -0.5
+    see = torch.where(lens[:, None] >= 0, lens[:, None] + 1 + torch.arange(2, device=DEV), 0)
+    s = s.masked_fill((torch.arange(T, device=DEV) >= see[:, :, None])[:, None, :, None], -float("inf"))
+    w = torch.softmax(s, -1).nan_to_num(0.0)
+    want = torch.einsum("bgmht,bgtd->bmghd", w, v).reshape(B, 2, Hq, D)
+    wabs = torch.einsum("bgmht,bgtd->bmghd", w, v.abs()).reshape(B, 2, Hq, D)
+    smax = 1.5 * 6 * D ** 0.5 * 4 * D ** -0.5 * D ** 0.5                             # above any scale * sum |q k| here
+    assert ((o.double() - want).abs() <= 2 * ((D + 12) * E23 * smax + 2.0 ** -12) * wabs + 1e-30).all()
+    total = w.sum((2, 3))
+    seen = torch.arange(T, device=DEV) < see[:, 1][:, None, None]
+    assert ((acc.double() - torch.where(seen, total, -3.0)).abs() <= 2 * ((D + 12) * E23 * smax + 2.0 ** -12) * total).all()
+
+
+def test_more_chunks_than_three_waves():
+    """2048 heads: CTAs take their chunks from the counter, call after call."""
+    B, Hq, G, D, T = 256, 8, 8, 64, 512
+    r = gen(32)
+    cache = moe.KV8Cache(T, batch=B, q_heads=Hq, kv_heads=G, head_dim=D, block=32, fmt="e4m3", max_rows=1)
+    cache.append(rows(r, B, T, G, D), rows(r, B, T, G, D), torch.zeros(B, dtype=torch.int32, device=DEV))
+    q = rows(r, B, 1, Hq, D)
+    pos = torch.randint(0, T, (B,), generator=r, device=DEV, dtype=torch.int32)
+    k, v = (t.double().transpose(1, 2) for t in cache.read(None, T))
+    s = torch.einsum("bhd,bhtd->bht", q[:, 0].double(), k) * D ** -0.5
+    w = torch.softmax(s.masked_fill((torch.arange(T, device=DEV) > pos[:, None])[:, None], -float("inf")), -1)
+    want, wabs = torch.einsum("bht,bhtd->bhd", w, v), torch.einsum("bht,bhtd->bhd", w, v.abs())
+    first = None
+    for _ in range(4):
+        cache.ws.fill_(0xFF)
+        o, _ = cache.attend(q, pos)
+        assert ((o[:, 0].double() - want).abs() <= 2 * (76 * E23 * 24 * 4 + 2.0 ** -12) * wabs).all()
+        first = o if first is None else first
+        assert torch.equal(o, first)
+
+
+@pytest.mark.parametrize("D,Hq,G,M,T,lens", [(64, 64, 1, 8, 64, [64, 30]), (128, 64, 1, 8, 64, [64, 9]), (256, 64, 1, 8, 64, [63, 64]),
+                                             (64, 5, 1, 3, 96, [96, 17]), (256, 3, 3, 5, 16, [16, 5]), (128, 7, 1, 1, 32, [32, 1])])
+def test_column_counts(D, Hq, G, M, T, lens):
+    """512 columns, odd numbers of them, the smallest cache; with weights."""
+    cache, r = filled(2, Hq, G, D, T, 16, "int8", lens, 33, weights=True)
+    acc = torch.rand((2, G, T), generator=r, device=DEV)
+    check(cache, rows(r, 2, M, Hq, D), [n - M for n in lens], acc=acc, decay=0.5)
+
+
+def test_evict_into_a_larger_cache():
+    cache, r = filled(2, 2, 2, 128, 256, 32, "int8", [256, 90], 34)
+    check_evict(cache, [256, 90], torch.rand((2, 2, 256), generator=r, device=DEV), 100, 3, 10, dT=1024)
+
+
+def test_a_stream_of_ones_own():
+    """Calls on an explicit stream, with the inputs made on another."""
+    cache, r = filled(1, 4, 2, 64, 64, 16, "int8", [40], 35)
+    q, k, pos = rows(r, 1, 1, 4, 64), rows(r, 1, 1, 2, 64), i32([40])
+    cache.append(k, k, pos)
+    want, _ = cache.attend(q, pos)
+    kv = cache.read(None, 41)
+    other = moe.KV8Cache(64, batch=1, q_heads=4, kv_heads=2, head_dim=64, block=16,
+                         buffers=tuple(t.clone() for t in (cache.k, cache.v, cache.k_scale, cache.v_scale)))
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    other.append(k, k, pos, stream=st)
+    o, _ = other.attend(q, pos, stream=st)
+    kv2 = other.read(None, 41, stream=st)
+    torch.cuda.current_stream().wait_stream(st)
+    assert torch.equal(o, want) and torch.equal(kv[0], kv2[0]) and torch.equal(kv[1], kv2[1])
