@@ -85,11 +85,11 @@ struct AttnP {
 //
 // 12 warps on an SM leave 168 registers a thread: the output of 8 columns of
 // 256 dimensions (64), or 16 of 128 or 64, the queries in registers where they
-// take 16 or less and in shared memory otherwise.  More columns run twice as
-// many at a time, two CTAs on an SM with 255 registers: expanding the codes is
-// most of the work, and it is done once per column pass.  A column's
-// arithmetic is the same either way, to the bit.  (16 warps with 128 registers
-// and slots of half a tile took 178 us where this takes 163.)
+// take 16 or less and in shared memory otherwise.  16 columns of 256 run with
+// two CTAs on an SM and 255 registers: expanding the codes is most of the
+// work, and it is done once per column pass.  A column's arithmetic is the
+// same either way, to the bit.  (16 warps with 128 registers and slots of half
+// a tile took 178 us where this takes 163.)
 constexpr int kWarps = 4, kThreads = 32 * kWarps, kStages = 2;
 constexpr int kTileBytes = 4096;                       // keys (or values) of a warp's tile
 constexpr int kStageBytes = 2 * kTileBytes + 64;       // and the steps of its up to 4 groups of 16 positions
@@ -101,16 +101,13 @@ constexpr int kStageBytes = 2 * kTileBytes + 64;       // and the steps of its u
 // positions at most) loses below is under 2^-20 of its largest weight.
 constexpr float kSlack = 8.f, kWeightUnit = 128.f;
 
-// Column tiles of 8 that a warp holds, and with how many CTAs on an SM.
-__host__ __device__ constexpr int kv8_nt(int C, int D)
-{
-    const int most = D == 256 ? 2 : 4;
-    return C <= 8 ? 1 : C <= 16 || most == 2 ? 2 : 4;
-}
+// Column tiles of 8 that a warp holds.  (Four for 32 columns and more, of 64 or
+// 128 dimensions with 255 registers, took 0.9 to 1.7 times as long.)
+__host__ __device__ constexpr int kv8_nt(int C) { return C <= 8 ? 1 : 2; }
 template <int D, int NT>
 struct Lay {
-    static constexpr bool wide = NT * D >= 256 || NT > 2;            // queries in shared memory
-    static constexpr int ctas = NT * D > 256 || NT > 2 ? 2 : 3, NC = 8 * NT;
+    static constexpr bool wide = NT * D >= 256;                      // queries in shared memory
+    static constexpr int ctas = NT * D > 256 ? 2 : 3, NC = 8 * NT;
     static constexpr int ring = 0, ml = kWarps * kStages * kStageBytes, unit = ml + kWarps * NC * 8, items = unit + kWarps * 8,
                          q = items + 4 * 32, qf = q + NT * D * 16, first = qf + NC * 4;
     static constexpr int total(int B) { return first + (3 * B + 1) * 4; }   // first[B + 1], then position and rows of each sequence
@@ -743,7 +740,7 @@ __global__ void __launch_bounds__(kMergeThreads) kv8_merge_kernel(const AttnP p,
     __shared__ float4 co[kMergeShares][64], cml[kMergeShares][64];   // the shares' results, in the cluster's first CTA
     place_next();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, tq = lane & 3;
-    const int KS = D / 16, nt = kv8_nt(p.C, D), NC = 8 * nt, passes = (p.C + NC - 1) / NC;
+    const int KS = D / 16, nt = kv8_nt(p.C), NC = 8 * nt, passes = (p.C + NC - 1) / NC;
     // blockIdx.x: share, then pair of m-tiles, then column tile
     const int share = blockIdx.x % shares, pair = blockIdx.x / shares % (KS / 2), ct = blockIdx.x / shares / (KS / 2);
     const int g = blockIdx.y, b = blockIdx.z, k = 2 * pair + (warp & 1);
@@ -932,7 +929,7 @@ struct Kv8Ws {
 Kv8Ws kv8_ws(const moe_kv8 &c, int M, bool weights)
 {
     const size_t slots = (size_t)c.batch * ((c.T_cap + kv8_chunk(c) - 1) / kv8_chunk(c)) * c.kv_heads;
-    const int C = c.q_heads / c.kv_heads * M, NC = 8 * kv8_nt(C, c.head_dim);
+    const int C = c.q_heads / c.kv_heads * M, NC = 8 * kv8_nt(C);
     const size_t cols = (size_t)(C + NC - 1) / NC * NC;
     Kv8Ws w;
     w.cnt = 0;
@@ -996,7 +993,7 @@ int launch_kv8_attn(const moe_kv8 &c, const moe_rows &q, int M, const int32_t *p
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess || dev < 0 || dev >= 64) { note_cuda_error((int)e); return MOE_ERR_CUDA; }
-    const int nt = kv8_nt(p.C, c.head_dim);
+    const int nt = kv8_nt(p.C);
     p.by_pass = div_of((p.C + 8 * nt - 1) / (8 * nt));
     const long long items = (long long)p.nchunk * p.B * p.Hkv * ((p.C + 8 * nt - 1) / (8 * nt));
     if (items > INT_MAX / 2) return MOE_ERR_UNSUPPORTED;
@@ -1025,24 +1022,21 @@ int launch_kv8_attn(const moe_kv8 &c, const moe_rows &q, int M, const int32_t *p
         static_assert(Lay<D, N>::total(MOE_KV8_MAX_BATCH) <= kSmemMax, "shared memory");     \
         go(kv8_chunk_kernel<F, D, N>, Lay<D, N>::total(p.B), Lay<D, N>::ctas, once);         \
     } while (0)
-#define KV8_GO_F(F)                              \
-    do {                                         \
-        if (c.head_dim == 256) {                 \
-            if (nt == 1) KV8_GO(F, 256, 1);      \
-            else KV8_GO(F, 256, 2);              \
-        } else if (c.head_dim == 128) {          \
-            if (nt == 1) KV8_GO(F, 128, 1);      \
-            else if (nt == 2) KV8_GO(F, 128, 2); \
-            else KV8_GO(F, 128, 4);              \
-        } else {                                 \
-            if (nt == 1) KV8_GO(F, 64, 1);       \
-            else if (nt == 2) KV8_GO(F, 64, 2);  \
-            else KV8_GO(F, 64, 4);               \
-        }                                        \
+#define KV8_GO_D(F, D)                \
+    do {                              \
+        if (nt == 1) KV8_GO(F, D, 1); \
+        else KV8_GO(F, D, 2);         \
+    } while (0)
+#define KV8_GO_F(F)                                \
+    do {                                           \
+        if (c.head_dim == 256) KV8_GO_D(F, 256);   \
+        else if (c.head_dim == 128) KV8_GO_D(F, 128); \
+        else KV8_GO_D(F, 64);                      \
     } while (0)
     if (c.format == MOE_KV8_INT8) KV8_GO_F(MOE_KV8_INT8);
     else KV8_GO_F(MOE_KV8_E4M3);
 #undef KV8_GO_F
+#undef KV8_GO_D
 #undef KV8_GO
     if (e != cudaSuccess) { note_cuda_error((int)e); return MOE_ERR_CUDA; }
     note_launch();
