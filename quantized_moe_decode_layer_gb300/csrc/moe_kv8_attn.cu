@@ -883,32 +883,37 @@ __global__ void __launch_bounds__(kAccThreads) kv8_weights_kernel(const AttnP p)
         if (t0 + i * kAccThreads < n) p.acc[head * p.T_cap + t0 + i * kAccThreads] = a[i];
 }
 
-// Positions per chunk: r tiles a warp, from the cache's shape alone.  152 SMs
-// take three CTAs each, and the end of a chunk costs about two tiles (8 x 8K of
-// 256 to 8 x 24K of 64, r = 1 and 2: 1.1 to 4).  One sequence is taken as full: its
-// chunks run in waves of 456, of which the last takes 0.45 (0.7) of a wave's
-// time when it has at most one (two) for an SM.  Of a batch three quarters are taken as
-// full, and half a chunk's time for where the last ones end.  (One of 40K
-// of 256, r = 3, 5, 10: 19, 20, 20 us, four rows 38, 33, 29; of 132K, r = 5, 8,
-// 10: 38, 44, 34; 16 of up to 16K of 128, r = 4, 6, 10: 80, 71, 76; 8 of up to
-// 128K of 256, r = 8, 10, 16: 182, 177, 167.)
+// Positions per chunk: r tiles a warp, from the cache's shape alone, so that a
+// row's result does not depend on the call.  152 SMs take three CTAs each (two
+// of two column tiles of 256), so chunks run in waves of 456.  A batch is taken
+// as three quarters full with half a chunk more per head: the smallest r that
+// runs in one wave, and at most 2048 positions, which leave uneven lengths
+// something to share out.  One sequence is taken as full; a chunk's end costs
+// about two tiles, and its last wave takes 0.45 (0.7) of a wave's time when it
+// has at most one chunk (two) for an SM.
+// (Microseconds at r = 3, 4, 5, 6, 8, 10, 16: 8 x 8K of 2 heads of 256: 25, 20, 20,
+// 21, 23, 25, 28, with four rows a sequence 55, 47, 45, 38, 43, 44, 39;
+// 4 x 64K of 2 heads of 256: 56, 53, 53, 51, 47, 52, 42; 16 x 16K of 8 heads of 128,
+// e4m3: 86, 80, 79, 79, 78, 78, 74; 8 x 24K of 8 heads of 64 with
+// uneven lengths and weights, at 6, 8, 10, 16: 45, 38, 40, 51; one of 132K of
+// 2 heads of 256: 45, 44, 38, 39, 44, 33, -.)
 int kv8_chunk(const moe_kv8 &c)
 {
     const int round = kWarps * kTileBytes / c.head_dim;
-    const long long heads = (long long)c.batch * c.kv_heads, slots = 456;
+    const long long heads = (long long)c.batch * c.kv_heads, slots = 456, quarters = c.head_dim == 256 ? 1216 : 1824;
     long long least = LLONG_MAX;                                     // in twentieths of a tile
     int best = 1;
     for (const int r : {1, 2, 3, 4, 5, 6, 8, 10, 16}) {
-        const long long one = 20 * (r + 2);
-        long long cost;
-        if (c.batch == 1) {
-            const long long n = heads * ((c.T_cap + r * round - 1) / (r * round)), rest = n % slots;
-            cost = n / slots * one + (rest == 0 ? 0 : rest <= 152 ? one * 9 / 20 : rest <= 304 ? one * 14 / 20 : one);
-        } else {
-            // chunks in quarters of a head's: 3/4 of its capacity and half a chunk
-            const long long n4 = heads * (3LL * c.T_cap / (r * round) + 2);
-            cost = std::max(n4, 4 * slots) * one / (4 * slots) + one / 2;
+        if (c.batch > 1) {
+            if (r * round > 2048)
+                break;
+            best = r;
+            if (heads * (3LL * c.T_cap / (r * round) + 2) <= quarters)
+                break;
+            continue;
         }
+        const long long one = 20 * (r + 2), n = heads * ((c.T_cap + r * round - 1) / (r * round)), rest = n % slots;
+        const long long cost = n / slots * one + (rest == 0 ? 0 : rest <= 152 ? one * 9 / 20 : rest <= 304 ? one * 14 / 20 : one);
         if (cost <= least) {
             least = cost;
             best = r;
