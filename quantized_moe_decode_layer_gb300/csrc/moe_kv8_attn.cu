@@ -739,6 +739,7 @@ __global__ void __launch_bounds__(kMergeThreads) kv8_merge_kernel(const AttnP p,
     __shared__ float4 so[8][32], sml[8][32];
     __shared__ float4 co[kMergeShares][64], cml[kMergeShares][64];   // the shares' results, in the cluster's first CTA
     place_next();
+    if (shares > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, tq = lane & 3;
     const int KS = D / 16, nt = kv8_nt(p.C), NC = 8 * nt, passes = (p.C + NC - 1) / NC;
     // blockIdx.x: share, then pair of m-tiles, then column tile
@@ -780,6 +781,7 @@ __global__ void __launch_bounds__(kMergeThreads) kv8_merge_kernel(const AttnP p,
         for (int w = 1; w < 4; ++w) join(m, l, o, sml[warp + 2 * w][lane], so[warp + 2 * w][lane]);
     }
     if (shares > 1) {
+        asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // the first CTA has started: its shared memory is there
         if (warp < 2) {
             // to the first CTA of the cluster
             uint32_t dst;
