@@ -558,7 +558,7 @@ int moe_kv8_attn(const moe_kv8 *cache, const moe_rows *q, int M, const int32_t *
  * NaN last).  A dst block's step is the smallest that holds its values; codes
  * that had a smaller one are rounded to it, the others move exactly.
  * idx_dev int32 [batch][kv_heads][budget]: the kept positions, -1 past the
- * last; lens_out_dev int32 [batch] = min(lens[b], budget); dst_acc_dev (or
+ * last; lens_out_dev int32 [batch] = min(lens[b], budget), 0 for lens[b] < 0; dst_acc_dev (or
  * NULL) fp32 [batch][kv_heads][dst T_cap]: the kept positions' weights.  What
  * lies past the kept positions in dst and dst_acc is left as it was.  Outputs
  * must not overlap inputs.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */

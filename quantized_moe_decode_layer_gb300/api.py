@@ -496,7 +496,8 @@ class KV8Cache:
 
     pos, counts, lens are int32 [batch] CUDA tensors, read on the device.
     buffers: (k, v, k_scale, v_scale) to use instead of new ones.  Calls run
-    on the current stream of the cache's device; calls that can overlap on the
+    on the current stream of the cache's device, or on `stream`, whose memory their
+    results then are; calls that can overlap on the
     GPU need caches of their own (or, to read one cache twice at a time,
     caches over the same buffers)."""
 
@@ -549,9 +550,9 @@ class KV8Cache:
     def _view(self, t, name: str, heads: int, types) -> Rows:
         """A [batch, M, heads, head_dim] tensor, strided but for its last dimension."""
         if isinstance(t, torch.Tensor) and t.dim() == 4 and t.dtype in types and t.get_device() == self._index:
-            b, _, h, d = t.shape
+            b, m, h, d = t.shape
             s0, s1, s2, s3 = t.stride()
-            if b == self.batch and h == heads and d == self.head_dim and s3 == 1:
+            if b == self.batch and h == heads and d == self.head_dim and s3 == 1 and m < 1 << 31:
                 return Rows(t.data_ptr(), _ROW_TYPES[t.dtype], s0, s1, s2)
         got = f"{tuple(t.shape)} {t.dtype} on {t.device}, strides {t.stride()}" if isinstance(t, torch.Tensor) else type(t).__name__
         raise ValueError(f"{name} must be [{self.batch}, M, {heads}, {self.head_dim}] with a contiguous last dimension, one of "
@@ -572,6 +573,14 @@ class KV8Cache:
         if stream.device != self.device:
             raise ValueError(f"the stream must be on {self.device}")
         return stream.cuda_stream
+
+    def _new(self, shape, dtype, stream):
+        """A result, in memory of the stream that writes it: what the current
+        stream freed may still be read there."""
+        if stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(stream):
+            return torch.empty(shape, dtype=dtype, device=self.device)
 
     def _run(self, name: str, f, *args) -> None:
         """A call of the library with the cache's device current."""
@@ -601,10 +610,10 @@ class KV8Cache:
         start[b] .. start[b] + n - 1 (start None: 0); zero outside the cache and
         from lens[b] on (moe_kv8_read)."""
         shape = (self.batch, n, self.kv_heads, self.head_dim)
-        k = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
-        v = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
+        h = self._on(stream)
+        k, v = self._new(shape, torch.bfloat16, stream), self._new(shape, torch.bfloat16, stream)
         self._run("moe_kv8_read", self._f_read, self._ref, None if start is None else self._vec(start, "start"), n,
-                  None if lens is None else self._vec(lens, "lens"), k.data_ptr(), v.data_ptr(), self._on(stream))
+                  None if lens is None else self._vec(lens, "lens"), k.data_ptr(), v.data_ptr(), h)
         return k, v
 
     def attend(self, q: torch.Tensor, pos: torch.Tensor, counts=None, scale=None, acc=None, acc_in=None, decay: float = 1.0,
@@ -616,13 +625,13 @@ class KV8Cache:
         cache built with weights=True) receives decay * acc_in + the weight each
         position got; acc_in defaults to acc."""
         r = self._view(q, "q", self.q_heads, _Q_TYPES)
-        M = q.size(1)
+        M, h = q.size(1), self._on(stream)
         if M > self.max_rows:
             raise ValueError(f"q has {M} rows; the cache was built for max_rows={self.max_rows}")
         if out is None:
             if out_dtype not in _ROW_TYPES:
                 raise ValueError("out_dtype must be fp32, bf16 or fp16")
-            out = torch.empty((self.batch, M, self.q_heads, self.head_dim), dtype=out_dtype, device=self.device)
+            out = self._new((self.batch, M, self.q_heads, self.head_dim), out_dtype, stream)
             o = out.data_ptr()
         else:
             out_dtype = getattr(out, "dtype", None)
@@ -640,7 +649,7 @@ class KV8Cache:
         e = self._err if err is None else self._like(err, "err", torch.int32, (1,))
         self._run("moe_kv8_attn", self._f_attn, self._ref, r, M, self._vec(pos, "pos"),
                   None if counts is None else self._vec(counts, "counts"), self.head_dim ** -0.5 if scale is None else scale, o,
-                  _ROW_TYPES[out_dtype], a_in, a, decay, self._ws, self._ws_bytes, e, self._on(stream))
+                  _ROW_TYPES[out_dtype], a_in, a, decay, self._ws, self._ws_bytes, e, h)
         return out, self.err if err is None else err
 
     def evict_into(self, dst: "KV8Cache", lens: torch.Tensor, acc: torch.Tensor, budget: int, sinks: int = 4,
@@ -651,15 +660,16 @@ class KV8Cache:
         dst int32 [batch])."""
         if not isinstance(dst, KV8Cache) or dst._index != self._index:
             raise ValueError(f"dst must be a KV8Cache on {self.device}")
-        if budget < 1:
-            raise ValueError("budget must be at least 1")
+        if not (1 <= budget < 1 << 31 and 0 <= sinks < 1 << 31 and 0 <= recent < 1 << 31):
+            raise ValueError("budget must be at least 1, sinks and recent at least 0, all below 2^31")
         a = self._like(acc, "acc", torch.float32, self._acc_shape)
         da = None if dst_acc is None else self._like(dst_acc, "dst_acc", torch.float32, (self.batch, self.kv_heads, dst.T_cap))
         e = self._err if err is None else self._like(err, "err", torch.int32, (1,))
-        idx = torch.empty((self.batch, self.kv_heads, budget), dtype=torch.int32, device=self.device)
-        n = torch.empty(self.batch, dtype=torch.int32, device=self.device)
+        h = self._on(stream)
+        idx = self._new((self.batch, self.kv_heads, budget), torch.int32, stream)
+        n = self._new((self.batch,), torch.int32, stream)
         self._run("moe_kv8_evict", self._f_evict, self._ref, dst._ref, self._vec(lens, "lens"), a, budget, sinks, recent, da,
-                  idx.data_ptr(), n.data_ptr(), e, self._on(stream))
+                  idx.data_ptr(), n.data_ptr(), e, h)
         return idx, n
 
 

@@ -718,3 +718,34 @@ def test_a_stream_of_ones_own():
     kv2 = other.read(None, 41, stream=st)
     torch.cuda.current_stream().wait_stream(st)
     assert torch.equal(o, want) and torch.equal(kv[0], kv2[0]) and torch.equal(kv[1], kv2[1])
+
+
+def test_results_lie_in_the_writing_streams_memory():
+    """A result for an explicit stream does not reuse memory that the current
+    stream has freed and may still be reading."""
+    cache, r = filled(1, 4, 2, 64, 64, 16, "int8", [40], 36)
+    q, pos, lens, acc = rows(r, 1, 1, 4, 64), i32([39]), i32([40]), torch.zeros((1, 2, 64), device=DEV)
+    dst = moe.KV8Cache(64, batch=1, q_heads=4, kv_heads=2, head_dim=64, block=16)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    for make, call in ((lambda: torch.empty((1, 33, 2, 64), dtype=torch.bfloat16, device=DEV), lambda: cache.read(None, 33, stream=st)),
+                       (lambda: torch.empty((1, 1, 4, 64), device=DEV), lambda: cache.attend(q, pos, stream=st)[:1]),
+                       (lambda: torch.empty((1, 2, 17), dtype=torch.int32, device=DEV),
+                        lambda: cache.evict_into(dst, lens, acc, 17, stream=st))):
+        old = [make() for _ in range(4)]
+        freed = {t.data_ptr() for t in old}
+        del old
+        got = call()
+        assert not freed & {t.data_ptr() for t in got}
+    torch.cuda.synchronize()
+
+
+def test_numbers_past_31_bits_are_refused():
+    cache = moe.KV8Cache(64, batch=1, q_heads=2, kv_heads=1, head_dim=64, block=16)
+    dst = moe.KV8Cache(64, batch=1, q_heads=2, kv_heads=1, head_dim=64, block=16)
+    lens, acc = i32([40]), torch.zeros((1, 1, 64), device=DEV)
+    k = torch.zeros((1, 1, 1, 64), device=DEV).expand(1, 2 ** 32 + 1, 1, 64)
+    for bad in (lambda: cache.evict_into(dst, lens, acc, 2 ** 32 + 8), lambda: cache.evict_into(dst, lens, acc, 8, sinks=2 ** 32),
+                lambda: cache.evict_into(dst, lens, acc, 8, sinks=0, recent=2 ** 32 + 1), lambda: cache.append(k, k, lens)):
+        with pytest.raises(ValueError):
+            bad()
