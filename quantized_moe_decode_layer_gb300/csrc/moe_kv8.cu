@@ -240,8 +240,10 @@ __global__ void __launch_bounds__(256) kv8_read_kernel(const ReadParams p)
 // it do.  Bound by latency: four passes over keys in shared memory (in L2 where
 // a slice has more than 16K), a cluster barrier each, the slices' 256 counts
 // added up through distributed shared memory (2048 counts, in three passes,
-// took 25 us where these take fewer).  Weights share few exponents, so a
-// CTA counts in 8 copies, a lane in its own.
+// took 25 us where these take fewer), and no more passes once all of a bin stays:
+// distinct weights take three.  (8 heads of 32K: 13.4 us, 8 of 128K: 25; with
+// the keys in registers and 32 copies of the counts 15.4 and 23.)  Weights share
+// few exponents, so a CTA counts in 8 copies, a lane in its own.
 constexpr int kSelThreads = 1024, kSelKeys = 16384, kSelBins = 256, kSelCopies = 8, kSelCtas = 8, kSelSlice = 4096;
 
 struct EvictParams {
@@ -285,7 +287,7 @@ __global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(const EvictPara
     extern __shared__ uint32_t sel[];
     int *copies = reinterpret_cast<int *>(sel);                     // [bins][copies]
     float *weights = reinterpret_cast<float *>(sel + kSelBins * kSelCopies);   // [kSelKeys]: this slice's
-    __shared__ int hist[2][kSelBins], wsum[32], weq[32], total[2], sh_digit, sh_need;   // hist: the passes take turns
+    __shared__ int hist[2][kSelBins], wsum[32], weq[32], total[2], sh_digit, sh_need, sh_all;   // hist: the passes take turns
     after_previous();
     const int rank = blockIdx.x % ctas, g = blockIdx.x / ctas, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int len = p.lens[b];
@@ -319,7 +321,8 @@ __global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(const EvictPara
     auto key = [&](int t) { return weight_key(weight(t)); };
     uint32_t prefix = 0u, mask = 0u;
     const int c0 = max(lo, s0), c1 = min(hi, s1);
-    for (int pass = 0; pass < 4 && any; ++pass) {
+    bool open = any;                                                // the bin holds more than stay
+    for (int pass = 0; pass < 4 && open; ++pass) {
         const int shift = 24 - 8 * pass;
         int *h = hist[pass & 1];
         for (int i = tid; i < kSelBins * kSelCopies; i += kSelThreads) copies[i] = 0;
@@ -362,21 +365,23 @@ __global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(const EvictPara
             if (before < need && need <= before + c) {
                 sh_digit = bin;
                 sh_need = need - before;
+                sh_all = need == before + c;
             }
         }
         __syncthreads();
         prefix |= (uint32_t)sh_digit << shift;
         mask |= 255u << shift;
         need = sh_need;
+        open = !sh_all;
     }
     if (!any) __syncthreads();
-    // kept: sinks, recent, keys above `prefix`, and the first `need` equal to it
+    // kept: sinks, recent, keys above `prefix` in the digits seen, and the first `need` equal to it
     auto kind = [&](int t, bool &above, bool &equal) {
         above = equal = false;
         if (t >= w1) return;
         if (t < lo || t >= hi) above = true;
         else if (any) {
-            const uint32_t k = key(t);
+            const uint32_t k = key(t) & mask;
             above = k > prefix;
             equal = k == prefix;
         }
@@ -434,9 +439,10 @@ __global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(const EvictPara
 // Moving: a destination block's step is the smallest that holds its values; a
 // code whose own step was smaller is rounded to it, one whose step was larger
 // is exact.  As many threads to a block as above, here with 16 codes of 4 rows
-// each.  Bound by gathering rows of D bytes.
+// each.  Bound by gathering rows of D bytes, hence four CTAs on an SM (three:
+// 8 heads of 16K rows of 256 take 3 us longer).
 template <int FMT, int THREADS>
-__global__ void __launch_bounds__(THREADS, THREADS == 512 ? 1 : 3) kv8_move_kernel(const EvictParams p)
+__global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 4) kv8_move_kernel(const EvictParams p)
 {
     __shared__ float red[16];
     const int g = blockIdx.y >> 1, which = blockIdx.y & 1, b = blockIdx.z;
@@ -480,7 +486,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 1 : 3) kv8_move_kern
     uint8_t *dst = p.dcodes[which] + head * p.dT_cap * p.D + q.d;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        if (t[i] < 0) continue;
+        if (i0 + q.row + i * step >= kept) continue;
         // no more than 2^17, see recode4; a row of zeros may have any step
         const float ratio = fminf(s[i] * inv, 131072.f);
         if (ratio != 1.f)
