@@ -891,19 +891,21 @@ __global__ void __launch_bounds__(kAccThreads) kv8_weights_kernel(const AttnP p)
 // as three quarters full with half a chunk more per head: the smallest r that
 // runs in one wave, and at most 2048 positions, which leave uneven lengths
 // something to share out.  One sequence is taken as full; a chunk's end costs
-// about two tiles, and its last wave takes 0.45 (0.7) of a wave's time when it
-// has at most one chunk (two) for an SM.
+// about two tiles, and its last wave takes 7 (12) of a wave's 17 parts of time
+// when it has at most one chunk (two) for an SM.
 // (Microseconds at r = 3, 4, 5, 6, 8, 10, 16: 8 x 8K of 2 heads of 256: 25, 20, 20,
 // 21, 23, 25, 28, with four rows a sequence 55, 47, 45, 38, 43, 44, 39;
 // 4 x 64K of 2 heads of 256: 56, 53, 53, 51, 47, 52, 42; 16 x 16K of 8 heads of 128,
 // e4m3: 86, 80, 79, 79, 78, 78, 74; 8 x 24K of 8 heads of 64 with
-// uneven lengths and weights, at 6, 8, 10, 16: 45, 38, 40, 51; one of 132K of
-// 2 heads of 256: 45, 44, 38, 39, 44, 33, -.)
+// uneven lengths and weights, at 6, 8, 10, 16: 45, 38, 40, 51; one of 40K of 2
+// heads of 256: 19, 19, 20, 21, 20, 19, 24, with four rows 39, 42, 34, 37, 40, 30, 38;
+// one of 132K: 45, 44, 38, 39, 44, 33, -; one of 32K of 8 heads of 128: 25, 26, 22, 22,
+// 24, 23, 28, of 128K: 61, 59, 57, 55, 60, 53, 67.)
 int kv8_chunk(const moe_kv8 &c)
 {
     const int round = kWarps * kTileBytes / c.head_dim;
     const long long heads = (long long)c.batch * c.kv_heads, slots = 456, quarters = c.head_dim == 256 ? 1216 : 1824;
-    long long least = LLONG_MAX;                                     // in twentieths of a tile
+    long long least = LLONG_MAX;                                     // in seventeenths of a tile
     int best = 1;
     for (const int r : {1, 2, 3, 4, 5, 6, 8, 10, 16}) {
         if (c.batch > 1) {
@@ -914,8 +916,8 @@ int kv8_chunk(const moe_kv8 &c)
                 break;
             continue;
         }
-        const long long one = 20 * (r + 2), n = heads * ((c.T_cap + r * round - 1) / (r * round)), rest = n % slots;
-        const long long cost = n / slots * one + (rest == 0 ? 0 : rest <= 152 ? one * 9 / 20 : rest <= 304 ? one * 14 / 20 : one);
+        const long long n = heads * ((c.T_cap + r * round - 1) / (r * round)), rest = n % slots;
+        const long long cost = (n / slots * 17 + (rest == 0 ? 0 : rest <= 152 ? 7 : rest <= 304 ? 12 : 17)) * (r + 2);
         if (cost <= least) {
             least = cost;
             best = r;
