@@ -712,7 +712,11 @@ __device__ __forceinline__ void store_out(void *o, int type, size_t i, float v)
 // of a cluster joined through its first CTA's shared memory.  Within a CTA
 // 4 warps per m-tile take every 4th chunk, so the order of additions depends
 // on the number of chunks and the cache's shape alone; chunks that a column does not see
-// (another row's) add exact zeros.
+// (another row's) add exact zeros.  Bound by latency: up to 304 CTAs load all
+// their chunks at once, U in flight (one of 128K of 2 heads of 256: 32.9 us a
+// call with U = 4, 31.8 with 8); more CTAs take little of the registers, so as to
+// run beside the chunks that end last (32 of up to 16K of 8 heads of 128: 106 us
+// with 4, 104 with 2).  U changes no addition's place.
 constexpr int kMergeThreads = 256, kMergeShares = 8;
 
 // (m, l, o) += another, with per-column references; -inf: nothing.
@@ -734,6 +738,7 @@ __device__ __forceinline__ void join(float (&m)[2], float (&l)[2], float4 &o, co
     o.w = o.w * fa[1] + fb[1] * x.w;
 }
 
+template <int U>
 __global__ void __launch_bounds__(kMergeThreads) kv8_merge_kernel(const AttnP p, int D, int shares)
 {
     __shared__ float4 so[8][32], sml[8][32];
@@ -756,10 +761,10 @@ __global__ void __launch_bounds__(kMergeThreads) kv8_merge_kernel(const AttnP p,
     const int stride = 4 * shares;
     auto slot = [&](int j) { return (((size_t)b * p.nchunk + j) * p.Hkv + g) * passes + ct / nt; };
     if (on) {
-        for (int j = share * 4 + (warp >> 1); j < nch; j += 4 * stride) {
-            float4 ml[4], x[4];
+        for (int j = share * 4 + (warp >> 1); j < nch; j += U * stride) {
+            float4 ml[U], x[U];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
+            for (int u = 0; u < U; ++u) {
                 const int ju = j + u * stride;
                 ml[u] = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
                 x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -770,7 +775,7 @@ __global__ void __launch_bounds__(kMergeThreads) kv8_merge_kernel(const AttnP p,
                 }
             }
 #pragma unroll
-            for (int u = 0; u < 4; ++u) join(m, l, o, ml[u], x[u]);
+            for (int u = 0; u < U; ++u) join(m, l, o, ml[u], x[u]);
         }
     }
     so[warp][lane] = o;
@@ -1023,6 +1028,10 @@ int launch_kv8_attn(const moe_kv8 &c, const moe_rows &q, int M, const int32_t *p
             e = cudaMemsetAsync(p.counter, 0, sizeof(int), stream);
             if (e != cudaSuccess) return;
         }
+        // One or two CTAs on every SM rather than more on some, which a call
+        // right behind another otherwise gets (one of 40K of 2 heads of 256: 21.6 us
+        // against 18.8 where it does not).
+        if (grid <= 2 * once.sms[dev]) smem = std::max(smem, grid <= once.sms[dev] ? 116 << 10 : 78 << 10);
         e = launch_after(kernel, dim3(grid), kThreads, smem, 0, stream, p);
     };
 #define KV8_GO(F, D, N)                                                                      \
@@ -1052,8 +1061,11 @@ int launch_kv8_attn(const moe_kv8 &c, const moe_rows &q, int M, const int32_t *p
     {
         int shares = 1;
         while (shares < kMergeShares && p.nchunk > 32 * shares) shares *= 2;
-        e = launch_after(kv8_merge_kernel, dim3(shares * (c.head_dim / 32) * ((p.C + 7) / 8), p.Hkv, p.B), kMergeThreads, 0, shares,
-                         stream, p, c.head_dim, shares);
+        const int each = (p.nchunk + 4 * shares - 1) / (4 * shares);             // chunks a warp
+        const dim3 grid(shares * (c.head_dim / 32) * ((p.C + 7) / 8), p.Hkv, p.B);
+        const bool few = (long long)grid.x * grid.y * grid.z <= 304;
+        e = launch_after(few && each > 4 ? kv8_merge_kernel<8> : few && each > 2 ? kv8_merge_kernel<4> : kv8_merge_kernel<2>, grid,
+                         kMergeThreads, 0, shares, stream, p, c.head_dim, shares);
         if (e != cudaSuccess) { note_cuda_error((int)e); return MOE_ERR_CUDA; }
     }
     note_launch();
