@@ -898,14 +898,14 @@ __global__ void __launch_bounds__(kAccThreads) kv8_weights_kernel(const AttnP p)
 // something to share out.  One sequence is taken as full; a chunk's end costs
 // about two tiles, and its last wave takes 7 (12) of a wave's 17 parts of time
 // when it has at most one chunk (two) for an SM.
-// (Microseconds at r = 3, 4, 5, 6, 8, 10, 16: 8 x 8K of 2 heads of 256: 25, 20, 20,
-// 21, 23, 25, 28, with four rows a sequence 55, 47, 45, 38, 43, 44, 39;
-// 4 x 64K of 2 heads of 256: 56, 53, 53, 51, 47, 52, 42; 16 x 16K of 8 heads of 128,
-// e4m3: 86, 80, 79, 79, 78, 78, 74; 8 x 24K of 8 heads of 64 with
+// (Microseconds a call among other kernels at r = 3, 4, 5, 6, 8, 10, 16: 8 x 8K of
+// 2 heads of 256: 23, 20, 21, 20, 21, 22, 25, with four rows a sequence 55, 47, 44,
+// 38, 42, 44, 39; 4 x 64K of 2 heads of 256: 56, 53, 53, 51, 44, 47, 42; 16 x 16K of
+// 8 heads of 128, e4m3: 86, 81, 79, 79, 78, 78, 73; 8 x 24K of 8 heads of 64 with
 // uneven lengths and weights, at 6, 8, 10, 16: 45, 38, 40, 51; one of 40K of 2
-// heads of 256: 19, 19, 20, 21, 20, 19, 24, with four rows 39, 42, 34, 37, 40, 30, 38;
-// one of 132K: 45, 44, 38, 39, 44, 33, -; one of 32K of 8 heads of 128: 25, 26, 22, 22,
-// 24, 23, 28, of 128K: 61, 59, 57, 55, 60, 53, 67.)
+// heads of 256: 19, 20, 19, 19, 21, 20, 25, with four rows 38, 39, 33, 36, 38, 30, 38;
+// one of 132K: 46, 39, 36, 38, 38, 33, 33; one of 32K of 8 heads of 128: 24, 24, 22,
+// 23, 22, 24, 25.)
 int kv8_chunk(const moe_kv8 &c)
 {
     const int round = kWarps * kTileBytes / c.head_dim;
