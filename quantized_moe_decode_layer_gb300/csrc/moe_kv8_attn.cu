@@ -775,7 +775,8 @@ __global__ void __launch_bounds__(kMergeThreads) kv8_merge_kernel(const AttnP p,
                 }
             }
 #pragma unroll
-            for (int u = 0; u < U; ++u) join(m, l, o, ml[u], x[u]);
+            for (int u = 0; u < U; ++u)
+                if (j + u * stride < nch) join(m, l, o, ml[u], x[u]);
         }
     }
     so[warp][lane] = o;

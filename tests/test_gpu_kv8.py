@@ -749,3 +749,13 @@ def test_numbers_past_31_bits_are_refused():
                 lambda: cache.evict_into(dst, lens, acc, 8, sinks=0, recent=2 ** 32 + 1), lambda: cache.append(k, k, lens)):
         with pytest.raises(ValueError):
             bad()
+
+
+def test_rows_of_a_long_cache_do_not_interact():
+    """As above where one row and eight are joined by different forms of the merge."""
+    cache, r = filled(1, 16, 2, 256, 65536, 64, "int8", [65000], 37)
+    q = rows(r, 1, 8, 16, 256)
+    all_rows, _ = cache.attend(q, i32([64992]))
+    for m in (0, 5, 7):
+        one, _ = cache.attend(q[:, m:m + 1], i32([64992 + m]))
+        assert torch.equal(one[:, 0].view(torch.int32), all_rows[:, m].view(torch.int32))
