@@ -284,7 +284,8 @@ __device__ __forceinline__ int peer(const int *p, int rank)
 
 __global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(const EvictParams p, int ctas)
 {
-    extern __shared__ uint32_t sel[];
+    extern __shared__ __align__(16) uint32_t sel[];
+    static_assert(__alignof__(sel) >= alignof(int4), "the counts are read four at a time");
     int *copies = reinterpret_cast<int *>(sel);                     // [bins][copies]
     float *weights = reinterpret_cast<float *>(sel + kSelBins * kSelCopies);   // [kSelKeys]: this slice's
     __shared__ int hist[2][kSelBins], wsum[32], weq[32], total[2], sh_digit, sh_need, sh_all;   // hist: the passes take turns
