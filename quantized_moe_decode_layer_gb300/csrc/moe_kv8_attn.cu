@@ -512,7 +512,8 @@ __global__ void __launch_bounds__(kThreads, Lay<D, NT>::ctas) kv8_chunk_kernel(c
                     x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 4));
                     x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
                     x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
-                    mn[n][c] = x > m[n][c] + kSlack ? x : m[n][c];
+                    // the difference: a sum would round past x where scores are 16 apart
+                    mn[n][c] = __fsub_rn(x, m[n][c]) > kSlack ? x : m[n][c];
                     grew |= mn[n][c] != m[n][c];
                 }
             if (fresh) {
