@@ -11,9 +11,9 @@
 // alone (kv8_chunk), so a row's result depends neither on the other rows nor
 // on the other sequences.  A chunk yields, per query column (row and head of
 // a key/value head's group), a reference exponent near its maximum, the sum
-// of exp(s - reference) and the unnormalised output; the merge kernel joins a
-// row's chunks in an order that is fixed as well.  What only other rows see
-// (later positions of the same call) adds exact zeros.
+// of exp(s - reference), and the unnormalised output with a unit of its own;
+// the merge kernel joins a row's chunks in an order that is fixed as well.
+// What only other rows see (later positions of the same call) adds exact zeros.
 #include <algorithm>
 #include <climits>
 #include <mutex>
@@ -47,7 +47,8 @@ struct AttnP {
     const uint8_t *k, *v;
     const float *ks, *vs;
     const int32_t *pos, *counts;
-    float *part_o, *part_ml, *fin, *sc;   // chunks' results; joined (reference, 1 / sum); scores [B][Hkv][T_cap][C] or NULL
+    float *part_o, *part_ml, *part_e;     // chunks' results: output, (reference, sum), log2 of the output's unit
+    float *fin, *sc;                      // joined (reference, 1 / sum); scores [B][Hkv][T_cap][C] or NULL
     void *o;                        // [B][M][Hq][D]
     const float *acc_in;
     float *acc;
@@ -93,13 +94,25 @@ struct AttnP {
 constexpr int kWarps = 4, kThreads = 32 * kWarps, kStages = 2;
 constexpr int kTileBytes = 4096;                       // keys (or values) of a warp's tile
 constexpr int kStageBytes = 2 * kTileBytes + 64;       // and the steps of its up to 4 groups of 16 positions
-// A column's exponents are taken from a reference that follows its maximum
-// only when that has grown by more than 2^8 (rescaling the output takes a tenth
-// of a tile's instructions, and with 8 columns every other tile had a new
-// maximum).  Weights are then at most 2^8, held in units of 2^-7; their low
-// halves reach down to 2^-31, and what a warp's share of a chunk (2048
-// positions at most) loses below is under 2^-20 of its largest weight.
-constexpr float kSlack = 8.f, kWeightUnit = 128.f;
+// A column's softmax is taken against m, a whole number that follows its
+// maximum when that has grown by more than 2^8 (with 8 columns every other tile
+// has a new maximum), and its output is held in a unit of its own: weights
+// go into the product as exp2(s - m) * step * 2^off, where step is the
+// values' of the position, and off a whole number.  Changes of either are
+// exact.  off leaves the largest such weight of a tile between 2^-7 and
+// 2^15: it is chosen anew, for 2^8, when a tile's falls outside.  A
+// weight's two halves reach down to 2^-24, so it is off by 2^-22 of itself or 2^-18
+// of the largest weight * step of its tile (2^-14 where the tile's steps differ, by up
+// to the factor of 16 that is not looked into), whatever the steps of other tiles.
+// (One unit for all columns, of the largest step so far, lost what came after a
+// block of values 2^24 times larger, however little weight that block had.)
+// Following it costs nothing to speak of where a tile's largest weight is within
+// a few octaves of the first one's; with scores of a standard deviation of 7 (nats) and
+// 16 columns a tile, most tiles move some column: 4 rows at 128K of 2 heads of 256 take
+// 87 us for 73.
+constexpr float kSlack = 8.f, kTop = 0x1p15f, kLow = 0x1p-7f;
+constexpr int kAim = 8, kOffMin = -126, kOffMax = 120;  // the latter: values below 2^-100 need no finer unit
+constexpr int kOutTop = 90;                             // a finer unit takes no output beyond 2^91
 
 // Column tiles of 8 that a warp holds.  (Four for 32 columns and more, of 64 or
 // 128 dimensions with 255 registers, took 0.9 to 1.7 times as long.)
@@ -108,8 +121,8 @@ template <int D, int NT>
 struct Lay {
     static constexpr bool wide = NT * D >= 256;                      // queries in shared memory
     static constexpr int ctas = NT * D > 256 ? 2 : 3, NC = 8 * NT;
-    static constexpr int ring = 0, ml = kWarps * kStages * kStageBytes, unit = ml + kWarps * NC * 8, items = unit + kWarps * 8,
-                         q = items + 4 * 32, qf = q + NT * D * 16, first = qf + NC * 4;
+    static constexpr int ring = 0, ml = kWarps * kStages * kStageBytes, off = ml + kWarps * NC * 8, slot = off + kWarps * NC * 4,
+                         items = slot + kWarps * 4, q = items + 4 * 32, qf = q + NT * D * 16, first = qf + NC * 4;
     static constexpr int total(int B) { return first + (3 * B + 1) * 4; }   // first[B + 1], then position and rows of each sequence
 };
 
@@ -137,6 +150,9 @@ __device__ __forceinline__ float ex2(float x)
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+
+// log2 of a positive number, rounded down; -127 of one below 2^-126.
+__device__ __forceinline__ int log2_of(float v) { return (int)(__float_as_uint(v) >> 23) - 127; }
 
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
 {
@@ -265,7 +281,9 @@ __global__ void __launch_bounds__(kThreads, Lay<D, NT>::ctas) kv8_chunk_kernel(c
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, tq = lane & 3;
     int *first = reinterpret_cast<int *>(sm + L::first);
     Item *items = reinterpret_cast<Item *>(sm + L::items);          // the nth in slot n mod 4
-    float2 *red_ml = reinterpret_cast<float2 *>(sm + L::ml), *red_unit = reinterpret_cast<float2 *>(sm + L::unit);
+    float2 *red_ml = reinterpret_cast<float2 *>(sm + L::ml);
+    float *red_off = reinterpret_cast<float *>(sm + L::off);
+    int *red_slot = reinterpret_cast<int *>(sm + L::slot);
     const int passes = (p.C + NC - 1) / NC;
 
     after_previous();
@@ -386,7 +404,8 @@ __global__ void __launch_bounds__(kThreads, Lay<D, NT>::ctas) kv8_chunk_kernel(c
     for (;;) {
         const Item it = items[nth & 3];
         if (tid == 0) claim = p.counter ? gridDim.x + atomicAdd(p.counter, 1) : claim + gridDim.x;
-        float f[NT][2], m[NT][2], l[NT][2], o[NT][KS][4], vref = 0.f, inv_vref = 0.f;
+        float f[NT][2], m[NT][2], l[NT][2], o[NT][KS][4];
+        int off[NT][2];                // off in an exponent's place
         bool fresh = true;             // no tile yet: m = -inf, everything else 0
         uint32_t qr[L::wide ? 1 : NT][L::wide ? 1 : KS][2];
 #pragma unroll
@@ -406,6 +425,7 @@ __global__ void __launch_bounds__(kThreads, Lay<D, NT>::ctas) kv8_chunk_kernel(c
                 f[n][c] = qf[8 * n + 2 * tq + c];
                 m[n][c] = -INFINITY;
                 l[n][c] = 0.f;
+                off[n][c] = 0;
             }
 #pragma unroll
             for (int k = 0; k < KS; ++k)
@@ -499,74 +519,134 @@ __global__ void __launch_bounds__(kThreads, Lay<D, NT>::ctas) kv8_chunk_kernel(c
                         }
                     }
             }
-            // ---- reference exponents
-            float mn[NT][2];
-            bool grew = false;
+            // ---- reference exponents and units
+            float most = steps[1], least = steps[1];
+#pragma unroll
+            for (int r = 1; r < R; ++r) {
+                most = fmaxf(most, steps[2 * r + 1]);
+                least = fminf(least, steps[2 * r + 1]);
+            }
+            const bool near = R == 1 || most <= 16.f * least, whole = R == 1 || (near && t0 + TK <= it.p0 + 1);
+            auto all = [](float v) {                               // over a column's lanes
+                v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 4));
+                v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 8));
+                return fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 16));
+            };
+            // Where a column sees the whole tile and the steps are within a factor of
+            // 16, its largest weight is taken to be that of its largest score and the largest step.
+            float x[NT][2];                                        // the largest score
+            bool move = false;
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    float x = fmaxf(s[0][n][c], s[0][n][c + 2]);
+                    float a = fmaxf(s[0][n][c], s[0][n][c + 2]);
 #pragma unroll
-                    for (int r = 1; r < R; ++r) x = fmaxf(x, fmaxf(s[r][n][c], s[r][n][c + 2]));
-                    x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 4));
-                    x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
-                    x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
+                    for (int r = 1; r < R; ++r) a = fmaxf(a, fmaxf(s[r][n][c], s[r][n][c + 2]));
+                    x[n][c] = all(a);
                     // the difference: a sum would round past x where scores are 16 apart
-                    mn[n][c] = __fsub_rn(x, m[n][c]) > kSlack ? x : m[n][c];
-                    grew |= mn[n][c] != m[n][c];
+                    const float d = __fsub_rn(x[n][c], m[n][c]), top = __fmul_rn(ex2(d), __fmul_rn(most, __int_as_float(off[n][c] + 0x3F800000)));
+                    move |= d > kSlack || top >= kTop || top < kLow;
                 }
-            if (fresh) {
-                fresh = false;
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) m[n][c] = mn[n][c];      // from -inf: the maximum itself
-            } else if (__any_sync(0xFFFFFFFFu, grew)) {
+            if (fresh && whole) {
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        const float al = mn[n][c] == -INFINITY ? 1.f : ex2(__fsub_rn(m[n][c], mn[n][c]));
-                        l[n][c] = __fmul_rn(l[n][c], al);
+                        m[n][c] = ceilf(x[n][c]);
+                        const int e = log2_of(__fmul_rn(ex2(__fsub_rn(x[n][c], m[n][c])), most));
+                        off[n][c] = max(kOffMin, min(kOffMax, kAim - e)) << 23;
+                    }
+                fresh = false;
+            } else if (!whole || __any_sync(0xFFFFFFFFu, move)) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    int by[2];                                     // the output's change, as a power of two
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        int want = off[n][c] >> 23;                // of the same unit under the new m
+                        const bool first = m[n][c] == -INFINITY;   // nothing there: any unit
+                        if (__fsub_rn(x[n][c], m[n][c]) > kSlack) {
+                            const float mn = ceilf(x[n][c]);
+                            const int up = (int)fminf(__fsub_rn(mn, m[n][c]), 1024.f);
+                            l[n][c] = up > 126 ? 0.f : __fmul_rn(l[n][c], pow2f(-up));
+                            want += up;
+                            m[n][c] = mn;
+                        }
+                        // the largest exp2(s - m) * step, and the largest step that the column sees
+                        float top = __fmul_rn(ex2(__fsub_rn(x[n][c], m[n][c])), most), big = most;
+                        if (R > 1 && !whole) {
+                            int col = it.cp * NC + 8 * n + 2 * tq + c;
+                            float a = 0.f, b = 0.f;
+#pragma unroll
+                            for (int r = 0; r < R; ++r) {
+                                const float y = fmaxf(s[r][n][c], s[r][n][c + 2]);
+                                a = fmaxf(a, __fmul_rn(ex2(__fsub_rn(y, m[n][c])), steps[2 * r + 1]));
+                                if (y > -INFINITY) b = fmaxf(b, steps[2 * r + 1]);
+                            }
+                            a = all(a);
+                            b = all(b);
+                            if (!near || t0 + TK > it.p0 + 1 + p.by_group.by(col)) {
+                                top = a;
+                                big = b;
+                            }
+                        }
+                        // as above, so that a column does not depend on who else moves
+                        const int e = log2_of(top);
+                        int next = want;
+                        if (e > -127) {                            // else a tile of no weight
+                            if (e + want > 14 || e + want < -7) next = kAim - e;
+                            next = min(next, 127 - log2_of(big));  // 2^off step is finite
+                        }
+                        next = max(kOffMin, min(kOffMax, next));
+                        by[c] = first ? 0 : next - want;
+                        off[n][c] = next << 23;
+                    }
+                    if (!__any_sync(0xFFFFFFFFu, (by[0] | by[1]) != 0)) continue;
+                    if (__any_sync(0xFFFFFFFFu, max(by[0], by[1]) > 0)) {
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            float a = 0.f;
+#pragma unroll
+                            for (int k = 0; k < KS; ++k) a = fmaxf(a, fmaxf(fabsf(o[n][k][c]), fabsf(o[n][k][c + 2])));
+                            a = all(a);
+                            if (by[c] > 0 && a > 0.f) {            // where there is nothing yet, any unit
+                                const int cut = min(by[c], max(0, min(127, kOutTop - log2_of(a))));
+                                off[n][c] -= (by[c] - cut) << 23;
+                                by[c] = cut;
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const float al = by[c] < -126 ? 0.f : pow2f(min(by[c], 127));
 #pragma unroll
                         for (int k = 0; k < KS; ++k) {
                             o[n][k][c] = __fmul_rn(o[n][k][c], al);
                             o[n][k][c + 2] = __fmul_rn(o[n][k][c + 2], al);
                         }
-                        m[n][c] = mn[n][c];
                     }
+                }
+                fresh = false;
             }
             // ---- weights, their sums, and the output
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                // The output's unit is the largest step of values so far.  It
-                // grows by groups of 16 positions and not by tiles: a group
-                // that only later rows see comes after all that a row sees, and
-                // scales its output exactly.
-                const float vstep = steps[2 * r + 1];
-                if (vstep > vref) {
-                    inv_vref = 1.f / vstep;
-                    const float down = __fmul_rn(vref, inv_vref);
-                    vref = vstep;
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int k = 0; k < KS; ++k)
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) o[n][k][c] = __fmul_rn(o[n][k][c], down);
-                }
+                const int vstep = __float_as_int(steps[2 * r + 1]);
                 uint32_t ph[NT][2], pl[NT][2];
-                const float unit = __fmul_rn(__fmul_rn(vstep, inv_vref), kWeightUnit);
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    float w[4];
+                    // step * 2^off by adding exponents; below 2^-126 and where it is too
+                    // large (of positions that are not seen) zero
+                    float unit[2], w[4];
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) unit[c] = __int_as_float(__viaddmin_s32_relu(vstep, off[n][c], 0x7F000000));
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         const float base = m[n][c & 1] == -INFINITY ? 0.f : m[n][c & 1];
                         const float x = ex2(__fsub_rn(s[r][n][c], base));
                         l[n][c & 1] = __fadd_rn(l[n][c & 1], x);
-                        w[c] = __fmul_rn(x, unit);
+                        w[c] = __fmul_rn(x, unit[c & 1]);
                     }
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
@@ -629,9 +709,12 @@ __global__ void __launch_bounds__(kThreads, Lay<D, NT>::ctas) kv8_chunk_kernel(c
                 x = __fadd_rn(x, __shfl_xor_sync(0xFFFFFFFFu, x, 4));
                 x = __fadd_rn(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
                 x = __fadd_rn(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
-                if (gq == 0) red_ml[warp * NC + 8 * n + 2 * tq + c] = make_float2(m[n][c], x);
+                if (gq == 0) {
+                    red_ml[warp * NC + 8 * n + 2 * tq + c] = make_float2(m[n][c], x);
+                    red_off[warp * NC + 8 * n + 2 * tq + c] = (float)(off[n][c] >> 23);
+                }
             }
-        if (lane == 0) red_unit[warp] = make_float2(__fmul_rn(vref, 1.f / kWeightUnit), __int_as_float(stage ^ 1));
+        if (lane == 0) red_slot[warp] = stage ^ 1;
         constexpr int kAll = NT * KS, kRound = kAll < 16 ? kAll : 16;    // m-tiles, and of them a slot's worth
 #pragma unroll
         for (int h = 0; h < kAll / kRound; ++h) {
@@ -651,7 +734,7 @@ __global__ void __launch_bounds__(kThreads, Lay<D, NT>::ctas) kv8_chunk_kernel(c
             }
             constexpr int kShare = kRound / kWarps;                // m-tiles a warp adds up, of one column tile
             const int x0 = h * kRound + warp * kShare, n = x0 / KS;
-            float cf[kWarps][2], mx[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
+            float cf[kWarps][2], mx[2] = {-INFINITY, -INFINITY}, top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
             const float4 *src[kWarps];
 #pragma unroll
             for (int v = 0; v < kWarps; ++v)
@@ -659,23 +742,33 @@ __global__ void __launch_bounds__(kThreads, Lay<D, NT>::ctas) kv8_chunk_kernel(c
 #pragma unroll
                     for (int c = 0; c < 2; ++c) mx[c] = fmaxf(mx[c], red_ml[v * NC + 8 * n + 2 * tq + c].x);
                 }
+            // in the coarsest unit of the warps'
 #pragma unroll
             for (int v = 0; v < kWarps; ++v)
                 if (v < having) {
-                    const float2 u = red_unit[v];
-                    src[v] = reinterpret_cast<const float4 *>(sm + L::ring + (v * kStages + __float_as_int(u.y)) * kStageBytes) +
+                    src[v] = reinterpret_cast<const float4 *>(sm + L::ring + (v * kStages + red_slot[v]) * kStageBytes) +
                              (x0 - h * kRound) * 32 + lane;
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
                         const float2 x = red_ml[v * NC + 8 * n + 2 * tq + c];
-                        const float w = mx[c] == -INFINITY ? 1.f : ex2(__fsub_rn(x.x, mx[c]));
-                        sum[c] = __fmaf_rn(w, x.y, sum[c]);
-                        cf[v][c] = __fmul_rn(w, u.x);
+                        const float d = x.x == -INFINITY ? x.x : __fsub_rn(x.x, mx[c]);
+                        sum[c] = __fmaf_rn(ex2(d), x.y, sum[c]);
+                        cf[v][c] = __fsub_rn(d, red_off[v * NC + 8 * n + 2 * tq + c]);
+                        top[c] = fmaxf(top[c], cf[v][c]);
                     }
                 }
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                if (top[c] == -INFINITY) top[c] = 0.f;             // no weight at all
+#pragma unroll
+                for (int v = 0; v < kWarps; ++v)
+                    if (v < having) cf[v][c] = ex2(__fsub_rn(cf[v][c], top[c]));
+            }
             if (8 * n + 2 * tq < cols) {
-                if (x0 % KS == 0 && gq == 0)
+                if (x0 % KS == 0 && gq == 0) {
                     *reinterpret_cast<float4 *>(p.part_ml + (slot * NC + 8 * n + 2 * tq) * 2) = make_float4(mx[0], sum[0], mx[1], sum[1]);
+                    *reinterpret_cast<float2 *>(p.part_e + slot * NC + 8 * n + 2 * tq) = make_float2(top[0], top[1]);
+                }
                 float4 *dst = reinterpret_cast<float4 *>(p.part_o) + (slot * kAll + x0) * 32 + lane;
 #pragma unroll
                 for (int x = 0; x < kShare; ++x) {
@@ -720,30 +813,43 @@ __device__ __forceinline__ void store_out(void *o, int type, size_t i, float v)
 // with 4, 104 with 2).  U changes no addition's place.
 constexpr int kMergeThreads = 256, kMergeShares = 8;
 
-// (m, l, o) += another, with per-column references; -inf: nothing.
-__device__ __forceinline__ void join(float (&m)[2], float (&l)[2], float4 &o, const float4 &ml, const float4 &x)
-{
-    const float bm[2] = {ml.x, ml.z}, bl[2] = {ml.y, ml.w};
-    float fa[2], fb[2];
+// A column pair's share: references, sums, log2 of the outputs' units, outputs.
+struct Share {
+    float m[2], l[2], e[2];
+    float4 o;
+
+    __device__ __forceinline__ float4 ml() const { return make_float4(m[0], l[0], m[1], l[1]); }
+    __device__ __forceinline__ float2 unit() const { return make_float2(e[0], e[1]); }
+    // += another; reference -inf: nothing.  Units keep what they hold: the
+    // output is a sum of its terms in the coarser of two.
+    __device__ __forceinline__ void join(const float4 &ml, const float2 &unit, const float4 &x)
+    {
+        const float bm[2] = {ml.x, ml.z}, bl[2] = {ml.y, ml.w}, be[2] = {unit.x, unit.y};
+        float fa[2], fb[2];
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-        const float r = fmaxf(m[c], bm[c]), base = r == -INFINITY ? 0.f : r;
-        fa[c] = exp2f(m[c] - base);
-        fb[c] = exp2f(bm[c] - base);
-        l[c] = l[c] * fa[c] + fb[c] * bl[c];
-        m[c] = r;
+        for (int c = 0; c < 2; ++c) {
+            const float r = fmaxf(m[c], bm[c]), base = r == -INFINITY ? 0.f : r, da = m[c] - base, db = bm[c] - base;
+            l[c] = l[c] * ex2(da) + ex2(db) * bl[c];
+            m[c] = r;
+            const float ea = da + e[c], eb = db + be[c], top = fmaxf(ea, eb);
+            e[c] = top == -INFINITY ? 0.f : top;
+            fa[c] = ex2(ea - e[c]);
+            fb[c] = ex2(eb - e[c]);
+        }
+        o.x = o.x * fa[0] + fb[0] * x.x;
+        o.y = o.y * fa[1] + fb[1] * x.y;
+        o.z = o.z * fa[0] + fb[0] * x.z;
+        o.w = o.w * fa[1] + fb[1] * x.w;
     }
-    o.x = o.x * fa[0] + fb[0] * x.x;
-    o.y = o.y * fa[1] + fb[1] * x.y;
-    o.z = o.z * fa[0] + fb[0] * x.z;
-    o.w = o.w * fa[1] + fb[1] * x.w;
-}
+};
 
 template <int U>
 __global__ void __launch_bounds__(kMergeThreads) kv8_merge_kernel(const AttnP p, int D, int shares)
 {
     __shared__ float4 so[8][32], sml[8][32];
+    __shared__ float2 se[8][32];
     __shared__ float4 co[kMergeShares][64], cml[kMergeShares][64];   // the shares' results, in the cluster's first CTA
+    __shared__ float2 ce[kMergeShares][64];
     place_next();
     if (shares > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, tq = lane & 3;
@@ -756,57 +862,63 @@ __global__ void __launch_bounds__(kMergeThreads) kv8_merge_kernel(const AttnP p,
     const int rows = kv8_rows(p.pos, p.counts, b, p.M, p.T_cap, p0, bad);
     const int n = rows > 0 ? p0 + rows : 0, nch = (n + p.chunk - 1) / p.chunk;
     wait_for_previous();                                             // the chunks' results
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    Share a = {{-INFINITY, -INFINITY}, {0.f, 0.f}, {0.f, 0.f}, make_float4(0.f, 0.f, 0.f, 0.f)};
     const bool on = 8 * ct + 2 * tq < p.C;
     const int stride = 4 * shares;
     auto slot = [&](int j) { return (((size_t)b * p.nchunk + j) * p.Hkv + g) * passes + ct / nt; };
     if (on) {
         for (int j = share * 4 + (warp >> 1); j < nch; j += U * stride) {
             float4 ml[U], x[U];
+            float2 e[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int ju = j + u * stride;
                 ml[u] = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
                 x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                e[u] = make_float2(0.f, 0.f);
                 if (ju < nch) {
                     const size_t s = slot(ju);
                     ml[u] = __ldcg(reinterpret_cast<const float4 *>(p.part_ml + (s * NC + 8 * (ct % nt) + 2 * tq) * 2));
+                    e[u] = __ldcg(reinterpret_cast<const float2 *>(p.part_e + s * NC + 8 * (ct % nt) + 2 * tq));
                     x[u] = __ldcg(reinterpret_cast<const float4 *>(p.part_o) + ((s * nt + ct % nt) * KS + k) * 32 + lane);
                 }
             }
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                if (j + u * stride < nch) join(m, l, o, ml[u], x[u]);
+                if (j + u * stride < nch) a.join(ml[u], e[u], x[u]);
         }
     }
-    so[warp][lane] = o;
-    sml[warp][lane] = make_float4(m[0], l[0], m[1], l[1]);
+    so[warp][lane] = a.o;
+    sml[warp][lane] = a.ml();
+    se[warp][lane] = a.unit();
     __syncthreads();
     if (warp < 2) {
 #pragma unroll
-        for (int w = 1; w < 4; ++w) join(m, l, o, sml[warp + 2 * w][lane], so[warp + 2 * w][lane]);
+        for (int w = 1; w < 4; ++w) a.join(sml[warp + 2 * w][lane], se[warp + 2 * w][lane], so[warp + 2 * w][lane]);
     }
     if (shares > 1) {
         asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // the first CTA has started: its shared memory is there
         if (warp < 2) {
             // to the first CTA of the cluster
             uint32_t dst;
-            const float4 ml = make_float4(m[0], l[0], m[1], l[1]);
+            const float4 ml = a.ml(), o = a.o;
+            const float2 e = a.unit();
             asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(dst) : "r"(smem_u32(&co[share][warp * 32 + lane])));
             asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "f"(o.x), "f"(o.y), "f"(o.z), "f"(o.w) : "memory");
             asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(dst) : "r"(smem_u32(&cml[share][warp * 32 + lane])));
             asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "f"(ml.x), "f"(ml.y), "f"(ml.z), "f"(ml.w) : "memory");
+            asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(dst) : "r"(smem_u32(&ce[share][warp * 32 + lane])));
+            asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(dst), "f"(e.x), "f"(e.y) : "memory");
         }
         asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
         if (share != 0) return;
         if (warp < 2)
-            for (int s = 1; s < shares; ++s) join(m, l, o, cml[s][warp * 32 + lane], co[s][warp * 32 + lane]);
+            for (int s = 1; s < shares; ++s) a.join(cml[s][warp * 32 + lane], ce[s][warp * 32 + lane], co[s][warp * 32 + lane]);
     }
     if (warp >= 2) return;
     // dimensions of m-tile k: d (rows g) and d + 1 (rows g + 8)
     const int VW = D >= 128 ? 4 : 2, d = 4 * VW * (gq + 8 * (k / (2 * VW))) + 4 * (k / 2 % VW) + 2 * (k & 1);
-    const float v[4] = {o.x, o.y, o.z, o.w};
+    const float v[4] = {a.o.x, a.o.y, a.o.z, a.o.w};
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
         const int col = 8 * ct + 2 * tq + c;
@@ -814,12 +926,13 @@ __global__ void __launch_bounds__(kMergeThreads) kv8_merge_kernel(const AttnP p,
         const int row = col / p.G, h = g * p.G + col % p.G;
         const size_t out = (((size_t)b * p.M + row) * p.Hq + h) * D + d;
         const bool seen = row < rows;
-        store_out(p.o, p.o_type, out, seen ? v[c] / l[c] : 0.f);
-        store_out(p.o, p.o_type, out + 1, seen ? v[2 + c] / l[c] : 0.f);
+        const int e = (int)a.e[c];
+        store_out(p.o, p.o_type, out, seen ? scalbnf(v[c] / a.l[c], e) : 0.f);
+        store_out(p.o, p.o_type, out + 1, seen ? scalbnf(v[2 + c] / a.l[c], e) : 0.f);
         if (p.sc && k == 0 && gq == 0) {
             float *fin = p.fin + (((size_t)b * p.Hkv + g) * p.C + col) * 2;
-            fin[0] = m[c];
-            fin[1] = 1.f / l[c];
+            fin[0] = a.m[c];
+            fin[1] = 1.f / a.l[c];
         }
     }
 }
@@ -940,7 +1053,7 @@ struct Once {
 };
 
 struct Kv8Ws {
-    size_t cnt, ml, o, fin, sc, total;
+    size_t cnt, ml, e, o, fin, sc, total;
 };
 Kv8Ws kv8_ws(const moe_kv8 &c, int M, bool weights)
 {
@@ -950,7 +1063,8 @@ Kv8Ws kv8_ws(const moe_kv8 &c, int M, bool weights)
     Kv8Ws w;
     w.cnt = 0;
     w.ml = 256;
-    w.o = align_up(w.ml + slots * cols * 2 * sizeof(float), 256);
+    w.e = align_up(w.ml + slots * cols * 2 * sizeof(float), 256);
+    w.o = align_up(w.e + slots * cols * sizeof(float), 256);
     w.fin = align_up(w.o + slots * cols * c.head_dim * sizeof(float), 256);
     w.sc = align_up(w.fin + (size_t)c.batch * c.kv_heads * C * 2 * sizeof(float), 256);
     w.total = weights ? align_up(w.sc + (size_t)c.batch * c.kv_heads * c.T_cap * C * sizeof(float), 256) : w.sc;
@@ -979,6 +1093,7 @@ int launch_kv8_attn(const moe_kv8 &c, const moe_rows &q, int M, const int32_t *p
     p.pos = pos;
     p.counts = counts;
     p.part_ml = reinterpret_cast<float *>(base + w.ml);
+    p.part_e = reinterpret_cast<float *>(base + w.e);
     p.part_o = reinterpret_cast<float *>(base + w.o);
     p.fin = reinterpret_cast<float *>(base + w.fin);
     p.sc = acc ? reinterpret_cast<float *>(base + w.sc) : nullptr;

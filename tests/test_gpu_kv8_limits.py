@@ -3,7 +3,7 @@ import pytest
 import torch
 
 import quantized_moe_decode_layer_gb300 as moe
-from test_gpu_kv8 import DEV, gen, i32, rows
+from test_gpu_kv8 import DEV, E23, gen, i32, rows
 
 pytestmark = pytest.mark.gpu
 
@@ -28,3 +28,97 @@ def test_scores_one_spacing_apart():
         scale = 2.0 ** 21 * 0.6931471805599453 * (1 + step * 2.0 ** -23)
         o, _ = cache.attend(q, i32([1023]), scale=scale)
         assert ((o[0, 0, 0].double() >= low - 1e-4) & (o[0, 0, 0].double() <= high + 1e-4)).all(), step
+
+
+def one_head(cache, q, n, scale):
+    """In 64 bits: the output of rows q [M, heads, D] over a cache of one
+    key/value head whose first n positions all rows see, and its tolerance.
+
+    A score is off by (D + 4) 2^-23 of scale * sum |q_d k_d| (test_gpu_kv8), its
+    exponential by that and a few 2^-23 more, and a weight by 2^-22 when it is
+    split; what this does to each term counts with the term's own weight, twice
+    for the normaliser.  Sums add up to 1024 + chunks terms in a row.  Beside that, a
+    weight is off by 2^-18 of the largest weight * step among the 64 positions around it
+    (of the largest weight times the largest step, where that is less than 16 times as much),
+    in units of its own step."""
+    blk = cache.block
+    step = [s[0, 0].repeat_interleave(blk)[:n, None].double() for s in (cache.k_scale, cache.v_scale)]
+    k, code = cache.k[0, 0, :n].float().double() * step[0], cache.v[0, 0, :n].float().double()
+    v = code * step[1]
+    z, a = torch.einsum("mhd,td->mht", q.double(), k) * scale, torch.einsum("mhd,td->mht", q.double().abs(), k.abs()) * scale
+    w = torch.softmax(z, -1)
+    e = (cache.head_dim + 12) * E23 * a + 8 * E23 + 2.0 ** -22
+    o, oabs = w @ v, w @ v.abs()
+    most, wide, both = (torch.nn.functional.pad(x, (0, -n % 64)).unflatten(-1, (-1, 64)).amax(-1).repeat_interleave(64, -1)[..., :n]
+                        for x in (w, step[1][:, 0], w * step[1][:, 0]))
+    top = torch.minimum(most * wide, 16 * both)
+    tol = (w * e) @ v.abs() + (w * e).sum(-1, keepdim=True) * o.abs() + 2 * (1024 + cache.T_cap // 128) * E23 * oabs
+    return o, tol + 2.0 ** -18 * (top @ code.abs()) + 1e-37
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("M", [1, 2])
+def test_weight_behind_a_block_of_far_larger_values(fmt, D, M):
+    """A block of 16 whose values are 2^ratio times the others' and whose weights are 2^-low
+    of theirs, at the start of a warp's share of a chunk or inside it: the others' output stays."""
+    n, T = 700, 40960
+    for i, (ratio, low, at) in enumerate([(16, 100, 0), (20, 100, 0), (24, 100, 0), (28, 100, 16), (32, 100, 0), (40, 60, 0),
+                                          (48, 100, 32), (64, 100, 0), (100, 100, 0), (100, 118, 0), (60, 40, 0), (100, 110, 320),
+                                          (32, 100, 672), (None, -30, 0), (None, -80, 0), (None, -60, 256)]):
+        r = gen(41 + i)
+        cache = moe.KV8Cache(T, q_heads=8, kv_heads=1, head_dim=D, block=16, fmt=fmt)
+        k, v = rows(r, 1, n, 1, D, dtype=torch.float32), rows(r, 1, n, 1, D, dtype=torch.float32)
+        q = rows(r, 1, M, 8, D)
+        q[..., 0] = 8.0
+        k[..., 0] = 0.0
+        k[:, at:at + 16] = 0.0
+        k[:, at:at + 16, :, 0] = -low * 0.6931471805599453 * D ** 0.5 / 8
+        v[:, at:at + 16] *= 0.0 if ratio is None else 2.0 ** ratio        # None: nothing but zeros where the weight is
+        cache.append(k, v, i32([0]))
+        for m in range(M):
+            o, tol = one_head(cache, q[0, m:m + 1], n - M + 1 + m, D ** -0.5)
+            got, _ = cache.attend(q, i32([n - M]))
+            d = (got[0, m:m + 1].double() - o).abs()
+            assert (d <= tol).all(), f"2^{ratio}, weight 2^-{low}, at {at}: worst {float((d / tol).max()):.3g} tolerances"
+
+
+@pytest.mark.parametrize("fmt,D,Hq,G,T,n", [("int8", 256, 16, 2, 2048, 1500), ("e4m3", 128, 8, 1, 40960, 700), ("int8", 64, 4, 4, 40960, 40000)])
+def test_values_of_any_size(fmt, D, Hq, G, T, n):
+    """Values times a power of two give exactly the output times it, up to where sums of
+    values would overflow."""
+    r = gen(60)
+    k, v, q = rows(r, 1, n, G, D), rows(r, 1, n, G, D, dtype=torch.float32), rows(r, 1, 2, Hq, D)
+    want = None
+    for e in (0, -90, -30, 60, 118, 124):
+        cache = moe.KV8Cache(T, q_heads=Hq, kv_heads=G, head_dim=D, block=16, fmt=fmt)
+        cache.append(k.float(), v * 2.0 ** e, i32([0]))
+        o, _ = cache.attend(q, i32([n - 2]))
+        want = o.double() if want is None else want
+        assert torch.equal(o.double(), want * 2.0 ** e), e
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_rows_do_not_interact_over_uneven_blocks(fmt, D):
+    """Steps of values 2^-60 to 2^60 apart, whole blocks of zeros, scores of a few and of
+    a hundred: every row of a call is bitwise the one-row call at its position, alone or beside
+    another sequence."""
+    for case, (T, n, spread, size) in enumerate([(40960, 1500, 60, 40.0), (40960, 1500, 3, 1.0), (512, 300, 60, 5.0), (40960, 1100, 0, 100.0)]):
+        r = gen(70 + case)
+        cache = moe.KV8Cache(T, batch=2, q_heads=3, kv_heads=1, head_dim=D, block=16, fmt=fmt)
+        k, v = rows(r, 2, n, 1, D, dtype=torch.float32), rows(r, 2, n, 1, D, dtype=torch.float32)
+        blocks = -(-n // 16)
+        e = torch.randint(-spread, spread + 1, (2, blocks), generator=r, device=DEV).float()
+        s = torch.exp2(e) * (torch.rand((2, blocks), generator=r, device=DEV) > 0.1)
+        v *= s.repeat_interleave(16, 1)[:, :n, None, None]
+        cache.append(k, v, i32([0, 0]))
+        q = rows(r, 2, 8, 3, D, size=size)
+        for first in (n - 8, n - 13, 321):
+            got, _ = cache.attend(q, i32([first, first - 5]))
+            assert torch.isfinite(got).all()
+            for m in range(8):
+                one, _ = cache.attend(q[:, m:m + 1], i32([first + m, -1]))
+                two, _ = cache.attend(q[:, m:m + 1], i32([-1, first - 5 + m]))
+                assert torch.equal(one[0, 0].view(torch.int32), got[0, m].view(torch.int32)), (case, first, m)
+                assert torch.equal(two[1, 0].view(torch.int32), got[1, m].view(torch.int32)), (case, first, m)
