@@ -521,7 +521,8 @@ int moe_kv8_append(const moe_kv8 *cache, const moe_rows *k_new, const moe_rows *
 /* Values of positions start[b] .. start[b] + n - 1 (start NULL: 0) as bf16,
  * k_out_dev and v_out_dev [batch][n][kv_heads][head_dim], for attention over a
  * prompt's earlier part, or moving a sequence.  Exact (a code has at most 7
- * bits; magnitudes below 2^-133 round).  Zero at positions outside the
+ * bits; magnitudes below 2^-133 round, and 2^128, to which the largest numbers
+ * may have rounded, becomes the largest finite one).  Zero at positions outside the
  * cache, or from lens[b] on (lens NULL: T_cap).  One launch. */
 int moe_kv8_read(const moe_kv8 *cache, const int32_t *start_dev, int n, const int32_t *lens_dev, uint16_t *k_out_dev,
                  uint16_t *v_out_dev, moe_stream_t stream);
@@ -534,7 +535,8 @@ int moe_kv8_attn_workspace_size(const moe_kv8 *cache, int M, int weights, size_t
  * fp16) over the cache, whose positions up to the rows' own are valid:
  *   s_t = scale q . k_t,  t <= pos[b] + m;  o = sum_t softmax(s)_t v_t,
  * query head h reading key/value head h / (q_heads / kv_heads).  o_dev
- * [batch][M][q_heads][head_dim] of o_type.  The keys are split into chunks whose
+ * [batch][M][q_heads][head_dim] of o_type (bf16 and fp32: at most the largest
+ * finite number where the queries are finite).  The keys are split into chunks whose
  * size depends on the cache's shape alone and joined in order, so a row's result
  * is bitwise the same for any M and whatever the other sequences are.
  * Scores, softmax sums and outputs are fp32.  A query row is taken to 2^-26 of its

@@ -222,9 +222,8 @@ __global__ void __launch_bounds__(256) kv8_read_kernel(const ReadParams p)
             float a[4], c[4];
             decode4<FMT>(w.x, a);
             decode4<FMT>(w.y, c);
-            __nv_bfloat162 h[4] = {__floats2bfloat162_rn(a[0] * s, a[1] * s), __floats2bfloat162_rn(a[2] * s, a[3] * s),
-                                   __floats2bfloat162_rn(c[0] * s, c[1] * s), __floats2bfloat162_rn(c[2] * s, c[3] * s)};
-            o = *reinterpret_cast<uint4 *>(h);
+            o = make_uint4(bf16_pair(a[0] * s, a[1] * s), bf16_pair(a[2] * s, a[3] * s), bf16_pair(c[0] * s, c[1] * s),
+                           bf16_pair(c[2] * s, c[3] * s));
         }
         *reinterpret_cast<uint4 *>(p.out[which] + ((size_t)b * p.n * p.Hkv * lanes + i) * 8) = o;
     }

@@ -92,6 +92,15 @@ __device__ __forceinline__ void pairs(uint32_t w, uint32_t &x, uint32_t &y)
     }
 }
 
+// Two fp32 numbers to bf16, low and high half, nearest; past the largest finite
+// number that number (a code of a block of the largest steps may stand for 2^128).
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
 __device__ __forceinline__ __half2 as_half2(uint32_t w) { return *reinterpret_cast<const __half2 *>(&w); }
 
 // Four codes to four values in units of the step.

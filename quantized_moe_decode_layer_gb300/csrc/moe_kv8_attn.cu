@@ -793,11 +793,12 @@ __global__ void __launch_bounds__(kThreads, Lay<D, NT>::ctas) kv8_chunk_kernel(c
     cp_wait<0>();
 }
 
+// A mean of values of up to 2^128: bf16 and fp32 keep to finite numbers.
 __device__ __forceinline__ void store_out(void *o, int type, size_t i, float v)
 {
-    if (type == MOE_BF16) static_cast<__nv_bfloat16 *>(o)[i] = __float2bfloat16_rn(v);
+    if (type == MOE_BF16) static_cast<uint16_t *>(o)[i] = (uint16_t)bf16_pair(v, 0.f);
     else if (type == MOE_F16) static_cast<__half *>(o)[i] = __float2half_rn(v);
-    else static_cast<float *>(o)[i] = v;
+    else static_cast<float *>(o)[i] = fabsf(v) == INFINITY ? copysignf(__uint_as_float(0x7F7FFFFFu), v) : v;
 }
 
 // ------------------------------------------------------------------- merge

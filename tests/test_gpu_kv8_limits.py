@@ -3,7 +3,7 @@ import pytest
 import torch
 
 import quantized_moe_decode_layer_gb300 as moe
-from test_gpu_kv8 import DEV, E23, gen, i32, rows
+from test_gpu_kv8 import DEV, E23, err_of, gen, i32, rows
 
 pytestmark = pytest.mark.gpu
 
@@ -122,3 +122,41 @@ def test_rows_do_not_interact_over_uneven_blocks(fmt, D):
                 two, _ = cache.attend(q[:, m:m + 1], i32([-1, first - 5 + m]))
                 assert torch.equal(one[0, 0].view(torch.int32), got[0, m].view(torch.int32)), (case, first, m)
                 assert torch.equal(two[1, 0].view(torch.int32), got[1, m].view(torch.int32)), (case, first, m)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_largest_numbers_stay_finite(fmt, dtype):
+    """The type's largest number, and infinities, which count as it, come back as
+    finite ones: at most the largest of the result's type."""
+    D, big = 64, torch.finfo(dtype).max
+    cache = moe.KV8Cache(32, q_heads=2, kv_heads=1, head_dim=D, block=16, fmt=fmt)
+    v = torch.zeros((1, 32, 1, D), dtype=dtype, device=DEV)
+    v[0, :16, 0, 0], v[0, :16, 0, 1], v[0, :16, 0, 2] = big, -big, big / 2
+    v[0, 16:, 0, 0], v[0, 16:, 0, 1] = float("inf"), -float("inf")
+    cache.append(torch.zeros_like(v), v, i32([0]))
+    assert err_of(cache) == moe.KV8Cache.ERR_NONFINITE
+    code = cache.v[0, 0, :, :3].float().double() * cache.v_scale[0, 0].repeat_interleave(16)[:, None].double()
+    assert ((code[:16] - torch.tensor([big, -big, big / 2], device=DEV, dtype=torch.float64)).abs() <= 2.0 ** 124).all()
+    top = torch.finfo(torch.bfloat16).max
+    assert torch.equal(cache.read(None, 32)[1][0, :, 0, :3].double(), code.clamp(-top, top))
+    q = torch.zeros((1, 1, 2, D), dtype=torch.bfloat16, device=DEV)
+    for out in (torch.float32, torch.bfloat16):
+        top = torch.finfo(out).max
+        for pos in (0, 9, 31):
+            o, _ = cache.attend(q, i32([pos]), out_dtype=out)
+            want = code[:pos + 1].mean(0).clamp(-top, top)
+            assert torch.isfinite(o).all()
+            assert ((o[0, 0, :, :3].double() - want).abs() <= want.abs() * (2.0 ** -8 if out == torch.bfloat16 else 2.0 ** -18)).all()
+
+
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16, torch.float16])
+def test_nan_is_an_output_of_every_type(out):
+    """A query with a NaN or an infinity gives NaN, and not the type's largest number."""
+    cache = moe.KV8Cache(32, q_heads=3, kv_heads=1, head_dim=64, block=16)
+    k = rows(gen(63), 1, 20, 1, 64)
+    cache.append(k, k, i32([0]))
+    q = rows(gen(64), 1, 1, 3, 64)
+    q[0, 0, 0, 5], q[0, 0, 2, 7] = float("nan"), float("inf")
+    o, _ = cache.attend(q, i32([19]), out_dtype=out)
+    assert o[0, 0, 0].isnan().all() and o[0, 0, 2].isnan().all() and torch.isfinite(o[0, 0, 1]).all()
