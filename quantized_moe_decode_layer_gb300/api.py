@@ -495,11 +495,16 @@ class KV8Cache:
     count or length outside the cache, 2 = an infinity or NaN was appended).
 
     pos, counts, lens are int32 [batch] CUDA tensors, read on the device.
-    buffers: (k, v, k_scale, v_scale) to use instead of new ones.  Calls run
-    on the current stream of the cache's device, or on `stream`, whose memory their
-    results then are; calls that can overlap on the
-    GPU need caches of their own (or, to read one cache twice at a time,
-    caches over the same buffers)."""
+    buffers: (k, v, k_scale, v_scale) to use instead of new ones.  Calls that
+    can overlap on the GPU need caches of their own (or, to read one cache twice
+    at a time, caches over the same buffers).
+
+    Calls run on the current stream of the cache's device, or on `stream`.
+    The first call on a stream waits for what made the cache (not while the stream is
+    captured into a graph: capture after the device has been waited for), and the
+    cache's memory is kept until the streams that used it are done.  Inputs and results
+    of a call on an explicit `stream` are ordered by the caller, with wait_stream, as tensors
+    between streams are; they may be dropped right after it."""
 
     ERR_RANGE, ERR_NONFINITE = 1, 2
 
@@ -529,6 +534,10 @@ class KV8Cache:
             raise ValueError("the cache's buffers must be on one device")
         self.ws = torch.empty(n.value, dtype=torch.uint8, device=self.device)
         self.err = torch.zeros(1, dtype=torch.int32, device=self.device)
+        made = torch.cuda.current_stream(self.device)
+        self._met, self._own = {made.cuda_stream}, (*buffers, self.ws, self.err)
+        with torch.cuda.stream(made):
+            self._ready = None if torch.cuda.is_current_stream_capturing() else made.record_event()
         c = self._c
         c.k_dev, c.v_dev, c.k_scale_dev, c.v_scale_dev = (t.data_ptr() for t in buffers)
         # What every call needs, once: a decode step is a few microseconds of
@@ -569,18 +578,44 @@ class KV8Cache:
     def _on(self, stream) -> int:
         """The stream's handle (default: the current one of the cache's device)."""
         if stream is None:
-            return torch._C._cuda_getCurrentRawStream(self._index)
-        if stream.device != self.device:
+            h = torch._C._cuda_getCurrentRawStream(self._index)
+        elif stream.device != self.device:
             raise ValueError(f"the stream must be on {self.device}")
-        return stream.cuda_stream
+        else:
+            h = stream.cuda_stream
+        if h not in self._met:
+            self._meet(torch.cuda.current_stream(self.device) if stream is None else stream)
+        return h
+
+    def _meet(self, stream) -> None:
+        """Before the first call on a stream other than the one that made the cache."""
+        for t in self._own:
+            t.record_stream(stream)
+        with torch.cuda.stream(stream):
+            if torch.cuda.is_current_stream_capturing():
+                return
+        if self._ready is not None:
+            stream.wait_event(self._ready)
+        self._met.add(stream.cuda_stream)
 
     def _new(self, shape, dtype, stream):
         """A result, in memory of the stream that writes it: what the current
-        stream freed may still be read there."""
+        stream freed may still be read there.  And kept for the current stream,
+        which may read it and drop it."""
         if stream is None:
             return torch.empty(shape, dtype=dtype, device=self.device)
         with torch.cuda.stream(stream):
-            return torch.empty(shape, dtype=dtype, device=self.device)
+            t = torch.empty(shape, dtype=dtype, device=self.device)
+        t.record_stream(torch.cuda.current_stream(self.device))
+        return t
+
+    @staticmethod
+    def _keep(stream, *tensors) -> None:
+        """The inputs of a call on an explicit stream outlive it there."""
+        if stream is not None:
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(stream)
 
     def _run(self, name: str, f, *args) -> None:
         """A call of the library with the cache's device current."""
@@ -604,6 +639,7 @@ class KV8Cache:
         self._run("moe_kv8_append", self._f_append, self._ref, k, v, M, self._vec(pos, "pos"),
                   None if counts is None else self._vec(counts, "counts"),
                   self._err if err is None else self._like(err, "err", torch.int32, (1,)), self._on(stream))
+        self._keep(stream, k_new, v_new, pos, counts, err)
 
     def read(self, start, n: int, lens=None, stream=None):
         """(k, v) bf16 [batch, n, kv_heads, head_dim]: the values of positions
@@ -614,6 +650,7 @@ class KV8Cache:
         k, v = self._new(shape, torch.bfloat16, stream), self._new(shape, torch.bfloat16, stream)
         self._run("moe_kv8_read", self._f_read, self._ref, None if start is None else self._vec(start, "start"), n,
                   None if lens is None else self._vec(lens, "lens"), k.data_ptr(), v.data_ptr(), h)
+        self._keep(stream, start, lens)
         return k, v
 
     def attend(self, q: torch.Tensor, pos: torch.Tensor, counts=None, scale=None, acc=None, acc_in=None, decay: float = 1.0,
@@ -650,6 +687,7 @@ class KV8Cache:
         self._run("moe_kv8_attn", self._f_attn, self._ref, r, M, self._vec(pos, "pos"),
                   None if counts is None else self._vec(counts, "counts"), self.head_dim ** -0.5 if scale is None else scale, o,
                   _ROW_TYPES[out_dtype], a_in, a, decay, self._ws, self._ws_bytes, e, h)
+        self._keep(stream, q, pos, counts, out, acc, acc_in, err)
         return out, self.err if err is None else err
 
     def evict_into(self, dst: "KV8Cache", lens: torch.Tensor, acc: torch.Tensor, budget: int, sinks: int = 4,
@@ -666,10 +704,12 @@ class KV8Cache:
         da = None if dst_acc is None else self._like(dst_acc, "dst_acc", torch.float32, (self.batch, self.kv_heads, dst.T_cap))
         e = self._err if err is None else self._like(err, "err", torch.int32, (1,))
         h = self._on(stream)
+        dst._on(stream)
         idx = self._new((self.batch, self.kv_heads, budget), torch.int32, stream)
         n = self._new((self.batch,), torch.int32, stream)
         self._run("moe_kv8_evict", self._f_evict, self._ref, dst._ref, self._vec(lens, "lens"), a, budget, sinks, recent, da,
                   idx.data_ptr(), n.data_ptr(), e, h)
+        self._keep(stream, lens, acc, dst_acc, err)
         return idx, n
 
 

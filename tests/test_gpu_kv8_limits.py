@@ -1,9 +1,10 @@
-"""GPU tests of the 8-bit key/value cache at the limits of its numbers."""
+"""GPU tests of the 8-bit key/value cache at the limits of its numbers, and on
+streams other than the one that made it."""
 import pytest
 import torch
 
 import quantized_moe_decode_layer_gb300 as moe
-from test_gpu_kv8 import DEV, E23, err_of, gen, i32, rows
+from test_gpu_kv8 import DEV, E23, err_of, filled, gen, i32, rows
 
 pytestmark = pytest.mark.gpu
 
@@ -160,3 +161,129 @@ def test_nan_is_an_output_of_every_type(out):
     q[0, 0, 0, 5], q[0, 0, 2, 7] = float("nan"), float("inf")
     o, _ = cache.attend(q, i32([19]), out_dtype=out)
     assert o[0, 0, 0].isnan().all() and o[0, 0, 2].isnan().all() and torch.isfinite(o[0, 0, 1]).all()
+
+
+# -------------------------------------------------------------------- streams
+
+def busy(stream):
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(100_000_000)
+
+
+def test_what_an_explicit_stream_reads_is_kept():
+    """A caller may drop a call's inputs right after it: their memory is not
+    handed out while the call's stream still has to read it."""
+    B, G, D = 1, 2, 64
+    cache, r = filled(B, 4, G, D, 64, 16, "int8", [40], 61, weights=True)
+    dst = moe.KV8Cache(64, batch=B, q_heads=4, kv_heads=G, head_dim=D, block=16)
+    st = torch.cuda.Stream()
+    f32 = torch.float32
+    make = {"k": lambda: rows(r, B, 3, G, D), "q": lambda: rows(r, B, 3, 4, D), "pos": lambda: i32([37]), "acc": lambda: torch.zeros((B, G, 64), device=DEV),
+            "out": lambda: torch.empty((B, 3, 4, D), device=DEV, dtype=f32), "err": lambda: torch.zeros(1, dtype=torch.int32, device=DEV)}
+    calls = [(("k", "k", "pos", "pos", "err"), lambda k, v, pos, counts, err: cache.append(k, v, pos, counts=counts, err=err, stream=st)),
+             (("pos", "pos"), lambda start, lens: cache.read(start, 3, lens=lens, stream=st)),
+             (("q", "pos", "pos", "acc", "acc", "out", "err"), lambda q, pos, counts, acc, acc_in, out, err:
+              cache.attend(q, pos, counts=counts, acc=acc, acc_in=acc_in, out=out, err=err, stream=st) and None),
+             (("pos", "acc", "acc", "err"), lambda lens, acc, dacc, err: cache.evict_into(dst, lens, acc, 8, dst_acc=dacc, err=err, stream=st))]
+    for names, call in calls:
+        spare = [make[x]() for x in 3 * names]                # below, neither an allocation nor a
+        call(*spare[:len(names)])                             # kernel's loading waits for the device
+        torch.cuda.synchronize()
+        del spare
+        args = [make[x]() for x in names]
+        torch.cuda.synchronize()
+        busy(st)
+        result = call(*args)
+        freed = {t.data_ptr() for t in args}
+        del args
+        new = [make[x]() for x in names]
+        assert not st.query() and not freed & {t.data_ptr() for t in new}, names
+        torch.cuda.synchronize()
+        del result, new
+
+
+@pytest.mark.parametrize("explicit", [True, False])
+def test_a_dropped_caches_memory_is_kept(explicit):
+    """The cache's own buffers, scratch and error word, used on another stream
+    than they were made on, outlive the cache until that stream is done."""
+    q, pos = torch.zeros((1, 1, 4, 64), dtype=torch.bfloat16, device=DEV), i32([0])
+    st = torch.cuda.Stream()
+    cache = moe.KV8Cache(4096, q_heads=4, kv_heads=2, head_dim=64, block=16)
+    cache.attend(q, pos)
+    parts = (cache.k, cache.v, cache.k_scale, cache.v_scale, cache.ws, cache.err)
+    shapes, freed = [(t.shape, t.dtype) for t in parts], {t.data_ptr() for t in parts}
+    spare = [torch.empty(s, dtype=d, device=DEV) for s, d in 2 * shapes]       # no allocation below waits for the device
+    del parts, spare
+    torch.cuda.synchronize()
+    busy(st)
+    if explicit:
+        o = cache.attend(q, pos, stream=st)[0]
+    else:
+        with torch.cuda.stream(st):
+            o = cache.attend(q, pos)[0]
+    del cache
+    new = [torch.empty(s, dtype=d, device=DEV) for s, d in shapes]
+    assert not st.query() and not freed & {t.data_ptr() for t in new}
+    torch.cuda.synchronize()
+    del o
+
+
+@pytest.mark.parametrize("explicit", [True, False])
+def test_a_new_cache_is_ready_on_any_stream(explicit):
+    """The first call on a stream comes after the cache's own initialisation."""
+    k, pos = rows(gen(62), 1, 16, 1, 64), i32([0])
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    busy(torch.cuda.current_stream())
+    cache = moe.KV8Cache(64, q_heads=1, kv_heads=1, head_dim=64, block=16)
+    if explicit:
+        cache.append(k, k, pos, stream=st)
+    else:
+        with torch.cuda.stream(st):
+            cache.append(k, k, pos)
+    torch.cuda.synchronize()
+    assert cache.k[0, 0, :16].any() and (cache.k_scale[0, 0, :1] > 0).all()
+
+
+def test_a_result_dropped_by_its_reader_is_kept():
+    """A result of an explicit stream that the current stream reads and drops is
+    not handed to that stream's next call before it has been read."""
+    cache, r = filled(1, 4, 2, 64, 64, 16, "int8", [40], 65)
+    q, pos = rows(r, 1, 1, 4, 64), i32([39])
+    st, cur = torch.cuda.Stream(), torch.cuda.current_stream()
+    zero, seen = torch.zeros_like(q), torch.empty((1, 1, 4, 64), device=DEV)
+    st.wait_stream(cur)
+    o = cache.attend(q, pos, stream=st)[0]
+    spare = cache.attend(q, pos, stream=st)[0]
+    cur.wait_stream(st)
+    seen.copy_(o)
+    del spare
+    torch.cuda.synchronize()
+    busy(cur)
+    seen.copy_(o)
+    at = o.data_ptr()
+    del o
+    again = cache.attend(zero, pos, stream=st)[0]
+    assert not cur.query() and again.data_ptr() != at
+    torch.cuda.synchronize()
+    assert torch.equal(seen, cache.attend(q, pos)[0])
+
+
+def test_first_call_of_a_stream_in_a_capture():
+    """A stream's first call may be one that is captured, on a fork of the
+    captured stream too; eager calls on it wait as ever."""
+    cache, r = filled(1, 4, 2, 64, 64, 16, "int8", [40], 66)
+    q, pos = rows(r, 1, 1, 4, 64), i32([39])
+    want = cache.attend(q, pos)[0]
+    st, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        a = cache.attend(q, pos)[0]
+        st.wait_stream(torch.cuda.current_stream())
+        b = cache.attend(q, pos, stream=st)[0]
+        torch.cuda.current_stream().wait_stream(st)
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(a, want) and torch.equal(b, want)
+    assert torch.equal(cache.attend(q, pos, stream=st)[0].cpu(), want.cpu())
