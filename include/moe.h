@@ -460,9 +460,10 @@ int moe_attn_append(const uint16_t *k_new_dev, const uint16_t *v_new_dev, int M,
  * [batch][kv_heads][T_cap][head_dim] (keys and values alike); each block of
  * `block` positions of a head has one step 2^e, stored as the fp32 number, in
  * [batch][kv_heads][T_cap / block].  Powers of two, because codes are rounded
- * again when a growing block or an eviction gives them a larger step: then a
- * value stays within one step of what was appended however often that
- * happens.  All four buffers are the caller's, 16-byte aligned; they need no
+ * again when a growing block or an eviction gives them a larger step: however
+ * often that happens, a value x stays within one step of what was appended
+ * (int8), or within 2^-4 |x| + 2^-9 of a step (e4m3, whose codes have 4 bits),
+ * the step being the largest that the value has had.  All four buffers are the caller's, 16-byte aligned; they need no
  * initialisation.
  *
  * Common to the calls: pos_dev, counts_dev, lens_dev are int32 [batch] on

@@ -2,11 +2,14 @@
 //
 // A cached value is code * 2^e: an 8-bit code (int8 or e4m3) and one step
 // 2^e per block of positions of a head, kept as fp32.  Steps are powers of
-// two so that rounding a code again to the same step is exact, and to a
-// larger one only drops bits: half steps that at least double add up to less
-// than one last step, so a value that was rounded again any number of times
-// (a growing block, eviction) is within one step of what was appended.  With
-// arbitrary scales each rounding would add its own half step.
+// two so that rounding a code again to a step it has had, or a smaller one, is
+// exact, and to a larger one only drops bits.  int8: half steps that at least double
+// add up to less than the last, so a value that was rounded again any number of
+// times (a growing block, eviction) is within one step, the largest it has had, of
+// what was appended.  e4m3: the first rounding is off by 2^-4 of the value at most, and a
+// larger step costs only what falls below 2^-6 steps, where codes are 2^-9 apart: halves
+// of that add up to less than 2^-9 steps.  With arbitrary scales each
+// rounding would add its own half step (or 2^-4).
 #pragma once
 
 #include <cuda_bf16.h>

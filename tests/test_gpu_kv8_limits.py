@@ -287,3 +287,51 @@ def test_first_call_of_a_stream_in_a_capture():
     torch.cuda.synchronize()
     assert torch.equal(a, want) and torch.equal(b, want)
     assert torch.equal(cache.attend(q, pos, stream=st)[0].cpu(), want.cpu())
+
+
+# ------------------------------------------------------------- what a code keeps
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_values_stay_near_what_was_appended(fmt):
+    """Through blocks that grow and evictions that gather values of other steps: within
+    one step (int8), or 2^-4 of the value and 2^-9 of a step (e4m3), of the largest step that a
+    value has had.  (A rounding is off by half a step, or 2^-4 |x| and by 2^-10 steps below 2^-6
+    steps; a value is rounded again only to a step at least twice any before, so these
+    halves add up to less than twice the last.)"""
+    B, G, D, T, block = 2, 2, 64, 256, 16
+    a, c = (moe.KV8Cache(T, batch=B, q_heads=2, kv_heads=G, head_dim=D, block=block, fmt=fmt) for _ in range(2))
+    r = gen(80)
+    x = torch.zeros((2, B, G, T, D), dtype=torch.float64, device=DEV)         # what was appended where
+    largest = torch.zeros((2, B, G, T), dtype=torch.float64, device=DEV)      # the steps it has had
+    n, worst = 0, 0.0
+
+    def look():
+        nonlocal worst
+        for i, (codes, steps) in enumerate(((a.k, a.k_scale), (a.v, a.v_scale))):
+            step = steps.double().repeat_interleave(block, 2)
+            largest[i, :, :, :n] = torch.maximum(largest[i], step)[:, :, :n]
+            got = codes.float().double() * step[..., None]
+            s, d = largest[i, :, :, :n, None], (got - x[i])[:, :, :n].abs()
+            bound = s if fmt == "int8" else x[i, :, :, :n].abs() * 2.0 ** -4 + s * 2.0 ** -9
+            assert (d <= bound).all(), float((d / bound).max())
+            worst = max(worst, float((d / s).max()))
+
+    for turn in range(150):
+        m = 1 + turn % 4
+        size = 2.0 ** float(torch.randint(-12, 12, (1,), generator=r, device=DEV))
+        rows_ = torch.randn((2, B, m, G, D), generator=r, device=DEV) * size
+        a.append(rows_[0], rows_[1], i32([n] * B))
+        x[:, :, :, n:n + m] = rows_.transpose(2, 3).double()
+        largest[:, :, :, n:n + m] = 0.0
+        n += m
+        look()
+        if n > T - 8:
+            acc = torch.rand((B, G, T), generator=r, device=DEV)
+            idx, lens = a.evict_into(c, i32([n] * B), acc, 100, sinks=2, recent=3)
+            at = idx.long()
+            x[:, :, :, :100] = torch.gather(x, 3, at.expand(2, B, G, 100)[..., None].expand(2, B, G, 100, D))
+            largest[..., :100] = torch.gather(largest, 3, at.expand(2, B, G, 100))
+            a, c, n = c, a, 100
+            look()
+    # int8: within a step; e4m3 is not (codes of 256 to 448 are 32 apart)
+    assert worst <= 1.0 if fmt == "int8" else worst > 1.0
