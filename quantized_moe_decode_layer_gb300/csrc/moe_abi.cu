@@ -8,6 +8,7 @@
 #include <cstring>
 
 #include "moe_internal.h"
+#include "moe_kv8.h"
 #include "moe_unpack.cuh"
 
 namespace moe {

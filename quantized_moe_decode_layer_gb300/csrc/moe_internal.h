@@ -230,17 +230,6 @@ int launch_attn(const uint16_t *q, const uint16_t *k, const uint16_t *vt, int T_
                 void *ws, int *err, long long timeout_ns, cudaStream_t stream);
 int launch_attn_append(const uint16_t *kn, const uint16_t *vn, int M, int pos0, uint16_t *kc, uint16_t *vtc, int T_cap,
                        cudaStream_t stream);
-// 8-bit key/value cache (moe_kv8.cu, moe_kv8_attn.cu)
-int launch_kv8_append(const moe_kv8 &c, const moe_rows &k_new, const moe_rows &v_new, int M, const int32_t *pos,
-                      const int32_t *counts, int *err, cudaStream_t stream);
-int launch_kv8_read(const moe_kv8 &c, const int32_t *start, int n, const int32_t *lens, uint16_t *k_out, uint16_t *v_out,
-                    cudaStream_t stream);
-int launch_kv8_evict(const moe_kv8 &c, const moe_kv8 &d, const int32_t *lens, const float *acc, int budget, int sinks,
-                     int recent, float *dacc, int32_t *idx, int32_t *lens_out, int *err, cudaStream_t stream);
-size_t kv8_attn_workspace_bytes(const moe_kv8 &c, int M, bool weights);
-int launch_kv8_attn(const moe_kv8 &c, const moe_rows &q, int M, const int32_t *pos, const int32_t *counts, float scale,
-                    void *o, int o_type, const float *acc_in, float *acc, float decay, void *ws, int *err,
-                    cudaStream_t stream);
 int launch_export(const moe_layer &L, int tensor_id, int expert, uint8_t *codes, uint16_t *scales,
                   uint16_t *biases, cudaStream_t stream);
 // One set of grouped tensor-core products (moe_tc.cu): slot u's expert

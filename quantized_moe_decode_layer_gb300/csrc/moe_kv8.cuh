@@ -16,7 +16,7 @@
 #include <cuda_fp16.h>
 #include <stdint.h>
 
-#include "moe_internal.h"
+#include "moe_kv8.h"
 
 namespace moe {
 
