@@ -156,29 +156,6 @@ __device__ __forceinline__ float amax8(uint2 w)
     return fmaxf(__low2float(m), __high2float(m));
 }
 
-__device__ __forceinline__ float warp_max(float v)
-{
-#pragma unroll
-    for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-    return v;
-}
-
-// Maximum over a CTA of up to 32 warps; `red` holds 33 floats.
-__device__ __forceinline__ float cta_max(float v, float *red)
-{
-    v = warp_max(v);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
-    __syncthreads();
-    if (lane == 0) red[warp] = v;
-    __syncthreads();
-    if (warp == 0) {
-        v = warp_max(lane < nw ? red[lane] : -INFINITY);
-        if (lane == 0) red[32] = v;
-    }
-    __syncthreads();
-    return red[32];
-}
-
 // Every kernel of the cache is launched as a dependent of the one before it on
 // the stream: its CTAs may be placed while that one ends.  A call's first
 // kernel waits before anything else, and only then lets the next be placed
