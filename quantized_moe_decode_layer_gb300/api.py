@@ -495,9 +495,13 @@ class KV8Cache:
     count or length outside the cache, 2 = an infinity or NaN was appended).
 
     pos, counts, lens are int32 [batch] CUDA tensors, read on the device.
-    buffers: (k, v, k_scale, v_scale) to use instead of new ones.  Calls that
-    can overlap on the GPU need caches of their own (or, to read one cache twice
-    at a time, caches over the same buffers).
+    buffers: (k, v, k_scale, v_scale) to use instead of new ones.  ws: scratch
+    (uint8, at least as large as the cache's own would be) to use instead
+    of new one.  The scratch grows with max_rows and the query heads, and with weights
+    by 4 bytes a position, query head and row: it can be as large as the codes, so
+    caches whose calls follow one another, as a model's layers do, share one
+    (ws=first.ws).  Calls that can overlap on the GPU need scratch of
+    their own and must not write one cache.
 
     Calls run on the current stream of the cache's device, or on `stream`.
     The first call on a stream waits for what made the cache (not while the stream is
@@ -510,7 +514,7 @@ class KV8Cache:
 
     def __init__(self, T_cap: int, batch: int = 1, q_heads: int = 16, kv_heads: int = 2, head_dim: int = 256,
                  block: int = 64, fmt: str = "int8", max_rows: int = 8, weights: bool = False, device="cuda",
-                 buffers=None):
+                 buffers=None, ws=None):
         if fmt not in _KV8_FMT:
             raise ValueError(f"fmt must be one of {sorted(_KV8_FMT)}")
         code, self.dtype = _KV8_FMT[fmt]
@@ -532,7 +536,12 @@ class KV8Cache:
         self.device = self.k.device
         if any(t.device != self.device for t in buffers):
             raise ValueError("the cache's buffers must be on one device")
-        self.ws = torch.empty(n.value, dtype=torch.uint8, device=self.device)
+        if ws is None:
+            ws = torch.empty(n.value, dtype=torch.uint8, device=self.device)
+        _need(ws, "ws", torch.uint8, (None,))
+        if ws.numel() < n.value or ws.device != self.device:
+            raise ValueError(f"ws must have at least {n.value} bytes, on {self.device}; got {ws.numel()} on {ws.device}")
+        self.ws = ws
         self.err = torch.zeros(1, dtype=torch.int32, device=self.device)
         made = torch.cuda.current_stream(self.device)
         self._met, self._own = {made.cuda_stream}, (*buffers, self.ws, self.err)
@@ -544,7 +553,7 @@ class KV8Cache:
         # device time, so the binding's own time is most of a small call's.
         self._index = self.device.index
         self._ref = C.byref(c)
-        self._ws, self._err, self._ws_bytes = self.ws.data_ptr(), self.err.data_ptr(), n.value
+        self._ws, self._err, self._ws_bytes = self.ws.data_ptr(), self.err.data_ptr(), ws.numel()
         self._vec_shape, self._acc_shape = (batch,), (batch, kv_heads, T_cap)
         L = lib()
         self._f_append, self._f_read, self._f_attn, self._f_evict = (L.moe_kv8_append, L.moe_kv8_read, L.moe_kv8_attn,

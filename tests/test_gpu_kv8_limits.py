@@ -335,3 +335,30 @@ def test_values_stay_near_what_was_appended(fmt):
             look()
     # int8: within a step; e4m3 is not (codes of 256 to 448 are 32 apart)
     assert worst <= 1.0 if fmt == "int8" else worst > 1.0
+
+
+# ------------------------------------------------------------------- scratch
+
+def test_caches_share_scratch():
+    """Caches whose calls follow one another, of unequal shapes, over the scratch of the
+    largest; scratch that is too small or no such tensor is refused."""
+    big, r = filled(2, 16, 2, 128, 4096, 64, "int8", [4000, 1234], 90, weights=True)
+    small, _ = filled(1, 8, 2, 64, 512, 32, "e4m3", [500], 91)
+    q, qs = rows(r, 2, 3, 16, 128), rows(r, 1, 8, 8, 64)
+    acc, acc2 = torch.zeros((2, 2, 4096), device=DEV), torch.zeros((2, 2, 4096), device=DEV)
+    want, _ = big.attend(q, i32([3997, 1231]), acc=acc)
+    wants, _ = small.attend(qs, i32([492]))
+    over = moe.KV8Cache(512, batch=1, q_heads=8, kv_heads=2, head_dim=64, block=32, fmt="e4m3",
+                        buffers=(small.k, small.v, small.k_scale, small.v_scale), ws=big.ws)
+    assert over.ws is big.ws and over.ws.numel() > small.ws.numel()
+    for _ in range(3):
+        a, _ = over.attend(qs, i32([492]))
+        b, _ = big.attend(q, i32([3997, 1231]), acc=acc2, acc_in=torch.zeros_like(acc2))
+        assert torch.equal(a, wants) and torch.equal(b, want) and torch.equal(acc2, acc)
+    for bad in (small.ws, big.ws.view(torch.int32), big.ws.cpu(), big.ws[:-1], big.ws.view(2, -1)):
+        with pytest.raises(ValueError):
+            moe.KV8Cache(4096, batch=2, q_heads=16, kv_heads=2, head_dim=128, weights=True, ws=bad)
+    with pytest.raises(moe.MoeError):                     # not on a 16-byte boundary: refused by the call
+        odd = moe.KV8Cache(512, batch=1, q_heads=8, kv_heads=2, head_dim=64, block=32, ws=big.ws[1:])
+        odd.attend(qs, i32([0]))
+    torch.cuda.synchronize()
