@@ -540,8 +540,9 @@ int moe_kv8_attn_workspace_size(const moe_kv8 *cache, int M, int weights, size_t
  * finite number where the queries are finite).  The keys are split into chunks whose
  * size depends on the cache's shape alone and joined in order, so a row's result
  * is bitwise the same for any M and whatever the other sequences are.
- * Scores, softmax sums and outputs are fp32.  A query row is taken to 2^-26 of its
- * largest element.  A weight is off by 2^-22 of itself or, where that is more,
+ * Scores, softmax sums and outputs are fp32.  Queries are exact, but for elements
+ * below 2^-26 of their row's largest, which are off by 2^-37 of that at most.
+ * A weight is off by 2^-22 of itself or, where that is more,
  * by 2^-14 of the largest weight * step among the 4096 / head_dim positions
  * that it is taken with (2^-18 where their steps are equal), in units of its own step.
  *

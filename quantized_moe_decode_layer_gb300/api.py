@@ -621,10 +621,9 @@ class KV8Cache:
     @staticmethod
     def _keep(stream, *tensors) -> None:
         """The inputs of a call on an explicit stream outlive it there."""
-        if stream is not None:
-            for t in tensors:
-                if t is not None:
-                    t.record_stream(stream)
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
 
     def _run(self, name: str, f, *args) -> None:
         """A call of the library with the cache's device current."""
@@ -648,7 +647,8 @@ class KV8Cache:
         self._run("moe_kv8_append", self._f_append, self._ref, k, v, M, self._vec(pos, "pos"),
                   None if counts is None else self._vec(counts, "counts"),
                   self._err if err is None else self._like(err, "err", torch.int32, (1,)), self._on(stream))
-        self._keep(stream, k_new, v_new, pos, counts, err)
+        if stream is not None:
+            self._keep(stream, k_new, v_new, pos, counts, err)
 
     def read(self, start, n: int, lens=None, stream=None):
         """(k, v) bf16 [batch, n, kv_heads, head_dim]: the values of positions
@@ -659,7 +659,8 @@ class KV8Cache:
         k, v = self._new(shape, torch.bfloat16, stream), self._new(shape, torch.bfloat16, stream)
         self._run("moe_kv8_read", self._f_read, self._ref, None if start is None else self._vec(start, "start"), n,
                   None if lens is None else self._vec(lens, "lens"), k.data_ptr(), v.data_ptr(), h)
-        self._keep(stream, start, lens)
+        if stream is not None:
+            self._keep(stream, start, lens)
         return k, v
 
     def attend(self, q: torch.Tensor, pos: torch.Tensor, counts=None, scale=None, acc=None, acc_in=None, decay: float = 1.0,
@@ -696,7 +697,8 @@ class KV8Cache:
         self._run("moe_kv8_attn", self._f_attn, self._ref, r, M, self._vec(pos, "pos"),
                   None if counts is None else self._vec(counts, "counts"), self.head_dim ** -0.5 if scale is None else scale, o,
                   _ROW_TYPES[out_dtype], a_in, a, decay, self._ws, self._ws_bytes, e, h)
-        self._keep(stream, q, pos, counts, out, acc, acc_in, err)
+        if stream is not None:
+            self._keep(stream, q, pos, counts, out, acc, acc_in, err)
         return out, self.err if err is None else err
 
     def evict_into(self, dst: "KV8Cache", lens: torch.Tensor, acc: torch.Tensor, budget: int, sinks: int = 4,
@@ -713,12 +715,14 @@ class KV8Cache:
         da = None if dst_acc is None else self._like(dst_acc, "dst_acc", torch.float32, (self.batch, self.kv_heads, dst.T_cap))
         e = self._err if err is None else self._like(err, "err", torch.int32, (1,))
         h = self._on(stream)
-        dst._on(stream)
+        if h not in dst._met:
+            dst._on(stream)
         idx = self._new((self.batch, self.kv_heads, budget), torch.int32, stream)
         n = self._new((self.batch,), torch.int32, stream)
         self._run("moe_kv8_evict", self._f_evict, self._ref, dst._ref, self._vec(lens, "lens"), a, budget, sinks, recent, da,
                   idx.data_ptr(), n.data_ptr(), e, h)
-        self._keep(stream, lens, acc, dst_acc, err)
+        if stream is not None:
+            self._keep(stream, lens, acc, dst_acc, err)
         return idx, n
 
 

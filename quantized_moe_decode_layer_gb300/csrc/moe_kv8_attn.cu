@@ -76,7 +76,8 @@ struct AttnP {
 //
 // Per 16 positions and 8 query columns, on m16n8k16 fp16 MMAs:
 //     S^T [16 positions x 8] = K Q^T,   O^T [D x 8] += V^T P^T.
-// Codes are exact in fp16; queries are, after a power of two per row.  The
+// Codes are exact in fp16; queries are, after a power of two per row, but for
+// elements below 2^-26 of the row's largest.  The
 // contraction index may be any order of the dimensions as long as both
 // operands share it, so a lane's 16 loaded bytes of a key row are its elements
 // of four MMAs as they come.  Values need pairs of positions in one register:
