@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(const EvictPara
 // code whose own step was smaller is rounded to it, one whose step was larger
 // is exact.  As many threads to a block as above, here with 16 codes of 4 rows
 // each.  Bound by gathering rows of D bytes, hence four CTAs on an SM (three:
-// 8 heads of 16K rows of 256 take 3 us longer).
+// 8 heads of 16K rows of 256 take 3 us longer), whose 64 registers a thread spill 16 bytes.
 template <int FMT, int THREADS>
 __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 4) kv8_move_kernel(const EvictParams p)
 {

@@ -70,8 +70,8 @@ struct AttnP {
 // an SM, wrote four times the results and took 183 us where this took 163.)
 //
 // Bound, at 8 columns: the read of the cache (8 x 128K of 256: 1.07 GB of
-// capacity, 86% of the copy bandwidth over the whole call) and, for int8,
-// issuing the 650 instructions that 8 KB of codes take; below some 100 MB the
+// capacity, 85% of the copy bandwidth over the whole call) and, for int8,
+// issuing the 665 instructions that 8 KB of codes take; below some 100 MB the
 // launches, the first loads and the last chunks (8 us) weigh as much.
 //
 // Per 16 positions and 8 query columns, on m16n8k16 fp16 MMAs:
@@ -82,12 +82,13 @@ struct AttnP {
 // operands share it, so a lane's 16 loaded bytes of a key row are its elements
 // of four MMAs as they come.  Values need pairs of positions in one register:
 // byte permutes of two rows' words.  P^T's transpose is movmatrix.  The
-// weights go in as two fp16 halves (22 bits): sums of many small weights
-// keep fp32's precision, and an fp32 output means something.
+// weights go in as two fp16 halves (22 bits; below for what is smaller): an
+// fp32 output means something.
 //
 // 12 warps on an SM leave 168 registers a thread: the output of 8 columns of
 // 256 dimensions (64), or 16 of 128 or 64, the queries in registers where they
-// take 16 or less and in shared memory otherwise.  16 columns of 256 run with
+// take 16 or less and in shared memory otherwise.  (16 columns of 128 or 64, and the
+// change of units, spill up to 122 bytes.)  16 columns of 256 run with
 // two CTAs on an SM and 255 registers: expanding the codes is most of the
 // work, and it is done once per column pass.  A column's arithmetic is the
 // same either way, to the bit.  (16 warps with 128 registers and slots of half
@@ -1016,13 +1017,16 @@ __global__ void __launch_bounds__(kAccThreads) kv8_weights_kernel(const AttnP p)
 // about two tiles, and its last wave takes 7 (12) of a wave's 17 parts of time
 // when it has at most one chunk (two) for an SM.
 // (Microseconds a call among other kernels at r = 3, 4, 5, 6, 8, 10, 16: 8 x 8K of
-// 2 heads of 256: 23, 20, 21, 20, 21, 22, 25, with four rows a sequence 55, 47, 44,
-// 38, 42, 44, 39; 4 x 64K of 2 heads of 256: 56, 53, 53, 51, 44, 47, 42; 16 x 16K of
+// 2 heads of 256: 25, 19, 20, 21, 21, 22, 23, with four rows a sequence 55, 47, 46,
+// 37, 43, 44, 37; 4 x 64K of 2 heads of 256: 57, 53, 53, 52, 46, 52, 42; 16 x 16K of
 // 8 heads of 128, e4m3: 86, 81, 79, 79, 78, 78, 73; 8 x 24K of 8 heads of 64 with
-// uneven lengths and weights, at 6, 8, 10, 16: 45, 38, 40, 51; one of 40K of 2
-// heads of 256: 19, 20, 19, 19, 21, 20, 25, with four rows 38, 39, 33, 36, 38, 30, 38;
-// one of 132K: 46, 39, 36, 38, 38, 33, 33; one of 32K of 8 heads of 128: 24, 24, 22,
-// 23, 22, 24, 25.)
+// uneven lengths and weights: 47, 44, 42, 45, 41, 41, 50; one of 40K of 2
+// heads of 256: 18, 19, 18, 19, 20, 19, 24, with four rows 38, 42, 33, 36, 40, 28, 37;
+// one of 132K: 46, 43, 36, 39, 44, 33, 32; one of 32K of 8 heads of 128: 25, 26, 21,
+// 22, 21, 22, 23.  The rule takes 6, 16, 16, 8, 10, 10 and 5 for these caches; its two tiles
+// and its 7 and 12 of 17 are fitted to such figures and stand for nothing else.)  A cache that is
+// mostly empty pays for it: at 2K positions one sequence of 2 heads of 256
+// takes 17 us in a capacity of 132K and 8 in one of 2K.
 int kv8_chunk(const moe_kv8 &c)
 {
     const int round = kWarps * kTileBytes / c.head_dim;
