@@ -575,15 +575,16 @@ __global__ void __launch_bounds__(kThreads, Lay<D, NT>::ctas) kv8_chunk_kernel(c
                             want += up;
                             m[n][c] = mn;
                         }
-                        // the largest exp2(s - m) * step, and the largest step that the column sees
-                        float top = __fmul_rn(ex2(__fsub_rn(x[n][c], m[n][c])), most), big = most;
+                        // the largest exp2(s - m) * step (of up to 2^130: in units of 2^8), and
+                        // the largest step that the column sees
+                        float top = __fmul_rn(ex2(__fsub_rn(x[n][c], m[n][c])), most * 0x1p-8f), big = most;
                         if (R > 1 && !whole) {
                             int col = it.cp * NC + 8 * n + 2 * tq + c;
                             float a = 0.f, b = 0.f;
 #pragma unroll
                             for (int r = 0; r < R; ++r) {
                                 const float y = fmaxf(s[r][n][c], s[r][n][c + 2]);
-                                a = fmaxf(a, __fmul_rn(ex2(__fsub_rn(y, m[n][c])), steps[2 * r + 1]));
+                                a = fmaxf(a, __fmul_rn(ex2(__fsub_rn(y, m[n][c])), steps[2 * r + 1] * 0x1p-8f));
                                 if (y > -INFINITY) b = fmaxf(b, steps[2 * r + 1]);
                             }
                             a = all(a);
@@ -594,9 +595,9 @@ __global__ void __launch_bounds__(kThreads, Lay<D, NT>::ctas) kv8_chunk_kernel(c
                             }
                         }
                         // as above, so that a column does not depend on who else moves
-                        const int e = log2_of(top);
+                        const int e = log2_of(top) + 8;
                         int next = want;
-                        if (e > -127) {                            // else a tile of no weight
+                        if (e > -119) {                            // else a tile of no weight
                             if (e + want > 14 || e + want < -7) next = kAim - e;
                             next = min(next, 127 - log2_of(big));  // 2^off step is finite
                         }

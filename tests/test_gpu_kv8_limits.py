@@ -102,17 +102,18 @@ def test_values_of_any_size(fmt, D, Hq, G, T, n):
 @pytest.mark.parametrize("fmt", ["int8", "e4m3"])
 @pytest.mark.parametrize("D", [64, 128, 256])
 def test_rows_do_not_interact_over_uneven_blocks(fmt, D):
-    """Steps of values 2^-60 to 2^60 apart, whole blocks of zeros, scores of a few and of
-    a hundred: every row of a call is bitwise the one-row call at its position, alone or beside
+    """Steps of values 2^-60 to 2^60 apart, near the largest and the smallest, whole blocks of zeros, scores
+    of a few and of a hundred: every row of a call is bitwise the one-row call at its position, alone or beside
     another sequence."""
-    for case, (T, n, spread, size) in enumerate([(40960, 1500, 60, 40.0), (40960, 1500, 3, 1.0), (512, 300, 60, 5.0), (40960, 1100, 0, 100.0)]):
+    for case, (T, n, spread, size, base) in enumerate([(40960, 1500, 60, 40.0, 0), (40960, 1500, 3, 1.0, 0), (512, 300, 60, 5.0, 0),
+                                                       (40960, 1100, 0, 100.0, 0), (40960, 1100, 2, 10.0, 122), (40960, 1100, 4, 30.0, -115)]):
         r = gen(70 + case)
         cache = moe.KV8Cache(T, batch=2, q_heads=3, kv_heads=1, head_dim=D, block=16, fmt=fmt)
         k, v = rows(r, 2, n, 1, D, dtype=torch.float32), rows(r, 2, n, 1, D, dtype=torch.float32)
         blocks = -(-n // 16)
         e = torch.randint(-spread, spread + 1, (2, blocks), generator=r, device=DEV).float()
         s = torch.exp2(e) * (torch.rand((2, blocks), generator=r, device=DEV) > 0.1)
-        v *= s.repeat_interleave(16, 1)[:, :n, None, None]
+        v *= s.repeat_interleave(16, 1)[:, :n, None, None] * 2.0 ** base
         cache.append(k, v, i32([0, 0]))
         q = rows(r, 2, 8, 3, D, size=size)
         for first in (n - 8, n - 13, 321):
