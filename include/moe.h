@@ -537,7 +537,7 @@ int moe_kv8_attn_workspace_size(const moe_kv8 *cache, int M, int weights, size_t
  *   s_t = scale q . k_t,  t <= pos[b] + m;  o = sum_t softmax(s)_t v_t,
  * query head h reading key/value head h / (q_heads / kv_heads).  o_dev
  * [batch][M][q_heads][head_dim] of o_type (bf16 and fp32: at most the largest
- * finite number where the queries are finite).  The keys are split into chunks whose
+ * finite number; NaN where a score is NaN or +infinity).  The keys are split into chunks whose
  * size depends on the cache's shape alone and joined in order, so a row's result
  * is bitwise the same for any M and whatever the other sequences are.
  * Scores, softmax sums and outputs are fp32.  Queries are exact, but for elements
