@@ -575,6 +575,105 @@ int moe_kv8_evict(const moe_kv8 *src, const moe_kv8 *dst, const int32_t *lens_de
                   moe_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * 16-bit key/value cache for a batch of sequences, with attention that may
+ * have a sliding window and a few first positions that stay visible, and that may
+ * share a long prefix over the batch; and the same attention for prompts.
+ *
+ * Query row at position p, head h, key/value head g = h / (q_heads / kv_heads):
+ *   s_t = scale q . k_t,   t <= p and (t > p - window or t < sinks)
+ *   o   = sum_t softmax(s)_t v_t      (window 0: every t <= p)
+ *
+ * The cache: keys and values, bf16 or fp16, as [batch][kv_heads][T_cap]
+ * [head_dim], 16-byte aligned, the caller's.  Position t < T_cap lies in slot t.
+ * With a window the slots from `sinks` on are a ring: position t >= T_cap lies in slot
+ * sinks + (t - sinks) mod (T_cap - sinks), so a sequence may grow to
+ * MOE_KV_MAX_POSITIONS while T_cap stays; T_cap has to hold sinks + window +
+ * M - 1 positions for calls of M rows (those that the first row sees and the rows
+ * themselves).  Without a window positions end at T_cap.
+ *
+ * Common to the calls: pos_dev, counts_dev are int32 [batch] on the device.
+ * Sequence b has positions 0 .. pos[b] - 1 before the call, and the call's row m
+ * is position pos[b] + m, for m < counts[b] (NULL: all M).  pos[b] < 0 marks an
+ * idle sequence: nothing of it is read or written and its outputs are zero.
+ * Rows past counts[b] are padding: never read, their outputs zero.  What lies
+ * past a sequence's positions is never used, whatever it holds; keys and values
+ * at its positions are finite.  (A value that is not makes rows NaN
+ * whose tile of positions has it, also where they do not see it; a key, rows that see it.)
+ * err_dev (int, the caller clears it) collects MOE_KV8_ERR_RANGE (positions or
+ * counts outside the cache; those rows are left out) and MOE_KV_ERR_TIMEOUT (a device
+ * wait gave up; the outputs are not valid).  The current device is the buffers'.  Calls
+ * that write the same cache, or share a workspace, must not overlap on the GPU; two captured
+ * graphs that can run at once need a workspace each.  Outputs must not overlap
+ * inputs.  Every call only enqueues.
+ *
+ * Scores, maxima, sums and outputs are fp32; a softmax weight is rounded to the
+ * 16-bit type for its product with the values, and the output once at the end.  Which
+ * partial sums there are depends on the lengths of the whole batch, so a row's last bits
+ * may differ between batches; the same call gives the same bits. */
+#define MOE_KV_ERR_TIMEOUT 4
+#define MOE_KV_MAX_ROWS 8                     /* rows of a cache attention call */
+#define MOE_KV_MAX_GROUP 64                   /* query heads per key/value head */
+#define MOE_KV_MAX_BATCH 1024
+#define MOE_KV_MAX_HEADS 1024                 /* key/value heads */
+#define MOE_KV_MAX_SLOTS (1 << 22)            /* T_cap; positions of a prompt or prefix */
+#define MOE_KV_MAX_POSITIONS (1 << 30)        /* of a sequence whose cache is a ring */
+
+typedef struct moe_kv {
+    int batch, q_heads, kv_heads;  /* q_heads a multiple of kv_heads */
+    int head_dim;                  /* 64, 128 or 256 */
+    int T_cap;                     /* slots per sequence */
+    int type;                      /* MOE_BF16 or MOE_F16 */
+    int window, sinks;             /* window 0: none (sinks 0 then) */
+    void *k_dev, *v_dev;
+} moe_kv;
+
+/* Writes M rows per sequence (bf16, fp16 or fp32, rounded to nearest; any
+ * strides, the last dimension contiguous) into the cache.  M from 1 (a token) to
+ * any length (a prompt): rows that a later row of the call would overwrite in the ring
+ * are left out.  One launch.  Errors: INVALID_ARG, UNSUPPORTED (head
+ * layout, type), CUDA. */
+int moe_kv_append(const moe_kv *cache, const moe_rows *k_new, const moe_rows *v_new, int M, const int32_t *pos_dev,
+                  const int32_t *counts_dev, int *err_dev, moe_stream_t stream);
+
+/* Scratch of moe_kv_attn for up to M rows and a prefix of up to max_prefix positions
+ * (0: none), no initialisation.  Errors: INVALID_ARG, UNSUPPORTED. */
+int moe_kv_attn_workspace_size(const moe_kv *cache, int M, int max_prefix, size_t *bytes);
+
+/* Attention of M rows (1 .. 8) of q [batch][M][q_heads][head_dim] over the cache, whose
+ * positions up to the rows' own are valid (see moe_kv_append).  o_dev
+ * [batch][M][q_heads][head_dim].  q has the cache's type; its base is 16-byte
+ * aligned and its strides are multiples of 8 elements.
+ *
+ * prefix_k, prefix_v (or NULL): keys and values of prefix_len positions that
+ * lie ahead of every sequence's own, [prefix_len][kv_heads][head_dim] with
+ * strides row and head (seq is not used), of the cache's type, 16-byte aligned, strides
+ * multiples of 8.  All rows see all of them, in one softmax with their
+ * own positions; they are read once for the batch.  For caches without a window.
+ * Two launches, three with a prefix and many rows.  Errors: INVALID_ARG, UNSUPPORTED,
+ * BUFFER_TOO_SMALL, CUDA. */
+int moe_kv_attn(const moe_kv *cache, const moe_rows *q, int M, const int32_t *pos_dev, const int32_t *counts_dev,
+                const moe_rows *prefix_k, const moe_rows *prefix_v, int prefix_len, float scale, void *o_dev, void *ws_dev,
+                size_t ws_bytes, int *err_dev, moe_stream_t stream);
+
+/* The same attention without a cache, for prompts: `rows` rows per sequence of q
+ * [batch][rows][q_heads][head_dim] against k, v [batch][positions][kv_heads]
+ * [head_dim], whose rows' own are among them: row m is position pos[b] + m (pos_dev
+ * NULL: the last `rows` positions), pos[b] + counts[b] <= positions.  q, k and v as they
+ * lie: one type (bf16 or fp16), bases 16-byte aligned, strides multiples of 8
+ * elements and, where the dimension has more than one entry, not 0.  o_dev
+ * [batch][rows][q_heads][head_dim].  A workspace of moe_window_attn_workspace_size bytes
+ * (0: none is needed, ws_dev may be NULL).  Errors: as moe_kv_attn. */
+typedef struct moe_window {
+    int batch, q_heads, kv_heads, head_dim;
+    int rows, positions;
+    int window, sinks;             /* window 0: none (sinks 0 then) */
+} moe_window;
+int moe_window_attn_workspace_size(const moe_window *shape, size_t *bytes);
+int moe_window_attn(const moe_window *shape, const moe_rows *q, const moe_rows *k, const moe_rows *v,
+                    const int32_t *pos_dev, const int32_t *counts_dev, float scale, void *o_dev, void *ws_dev,
+                    size_t ws_bytes, int *err_dev, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * Streamed layers: the routed experts of a layer live in host memory (the
  * Grace side of a GB300, over NVLink-C2C) and only the experts the router
  * selects are copied into an HBM cache of n_slots expert slots, least

@@ -7,7 +7,7 @@ import ctypes as C
 import torch
 
 from . import _lib
-from ._lib import Kv8, LayerDesc, QkvDesc, Rows, SrcLayer, SrcMatrix, check, lib
+from ._lib import Kv, Kv8, LayerDesc, QkvDesc, Rows, SrcLayer, SrcMatrix, Window, check, lib
 
 
 def _ptr(t) -> int | None:
@@ -486,78 +486,10 @@ _ROW_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _Q_TYPES = (torch.bfloat16, torch.float16)
 
 
-class KV8Cache:
-    """An 8-bit key/value cache of `batch` sequences (moe_kv8_*): codes k, v
-    [batch, kv_heads, T_cap, head_dim] (int8 or e4m3) and steps k_scale,
-    v_scale, fp32 powers of two, [batch, kv_heads, T_cap / block]; with the
-    scratch that attention of up to max_rows rows needs (weights: also for its
-    position weights) and the calls' error word err (int32 [1]: 1 = a position,
-    count or length outside the cache, 2 = an infinity or NaN was appended).
-
-    pos, counts, lens are int32 [batch] CUDA tensors, read on the device.
-    buffers: (k, v, k_scale, v_scale) to use instead of new ones.  ws: scratch
-    (uint8, at least as large as the cache's own would be) to use instead
-    of new one.  The scratch grows with max_rows and the query heads, and with weights
-    by 4 bytes a position, query head and row: it can be as large as the codes, so
-    caches whose calls follow one another, as a model's layers do, share one
-    (ws=first.ws).  Calls that can overlap on the GPU need scratch of
-    their own and must not write one cache.
-
-    Calls run on the current stream of the cache's device, or on `stream`.
-    The first call on a stream waits for what made the cache (not while the stream is
-    captured into a graph: capture after the device has been waited for), and the
-    cache's memory is kept until the streams that used it are done.  Inputs and results
-    of a call on an explicit `stream` are ordered by the caller, with wait_stream, as tensors
-    between streams are; they may be dropped right after it."""
-
-    ERR_RANGE, ERR_NONFINITE = 1, 2
-
-    def __init__(self, T_cap: int, batch: int = 1, q_heads: int = 16, kv_heads: int = 2, head_dim: int = 256,
-                 block: int = 64, fmt: str = "int8", max_rows: int = 8, weights: bool = False, device="cuda",
-                 buffers=None, ws=None):
-        if fmt not in _KV8_FMT:
-            raise ValueError(f"fmt must be one of {sorted(_KV8_FMT)}")
-        code, self.dtype = _KV8_FMT[fmt]
-        self.T_cap, self.batch, self.q_heads, self.kv_heads = T_cap, batch, q_heads, kv_heads
-        self.head_dim, self.block, self.fmt, self.max_rows, self.weights = head_dim, block, fmt, max_rows, weights
-        self._c = Kv8(batch, q_heads, kv_heads, head_dim, T_cap, block, code)
-        n = C.c_size_t()
-        check("moe_kv8_attn_workspace_size",
-              lib().moe_kv8_attn_workspace_size(C.byref(self._c), max_rows, 1 if weights else 0, C.byref(n)))
-        rows, steps = (batch, kv_heads, T_cap, head_dim), (batch, kv_heads, T_cap // block)
-        if buffers is None:
-            buffers = (torch.zeros(rows, dtype=self.dtype, device=device), torch.zeros(rows, dtype=self.dtype, device=device),
-                       torch.zeros(steps, device=device), torch.zeros(steps, device=device))
-        self.k, self.v, self.k_scale, self.v_scale = buffers
-        for name, t, dt, shape in (("k", self.k, self.dtype, rows), ("v", self.v, self.dtype, rows),
-                                   ("k_scale", self.k_scale, torch.float32, steps),
-                                   ("v_scale", self.v_scale, torch.float32, steps)):
-            _need(t, name, dt, shape)
-        self.device = self.k.device
-        if any(t.device != self.device for t in buffers):
-            raise ValueError("the cache's buffers must be on one device")
-        if ws is None:
-            ws = torch.empty(n.value, dtype=torch.uint8, device=self.device)
-        _need(ws, "ws", torch.uint8, (None,))
-        if ws.numel() < n.value or ws.device != self.device:
-            raise ValueError(f"ws must have at least {n.value} bytes, on {self.device}; got {ws.numel()} on {ws.device}")
-        self.ws = ws
-        self.err = torch.zeros(1, dtype=torch.int32, device=self.device)
-        made = torch.cuda.current_stream(self.device)
-        self._met, self._own = {made.cuda_stream}, (*buffers, self.ws, self.err)
-        with torch.cuda.stream(made):
-            self._ready = None if torch.cuda.is_current_stream_capturing() else made.record_event()
-        c = self._c
-        c.k_dev, c.v_dev, c.k_scale_dev, c.v_scale_dev = (t.data_ptr() for t in buffers)
-        # What every call needs, once: a decode step is a few microseconds of
-        # device time, so the binding's own time is most of a small call's.
-        self._index = self.device.index
-        self._ref = C.byref(c)
-        self._ws, self._err, self._ws_bytes = self.ws.data_ptr(), self.err.data_ptr(), ws.numel()
-        self._vec_shape, self._acc_shape = (batch,), (batch, kv_heads, T_cap)
-        L = lib()
-        self._f_append, self._f_read, self._f_attn, self._f_evict = (L.moe_kv8_append, L.moe_kv8_read, L.moe_kv8_attn,
-                                                                     L.moe_kv8_evict)
+class _CacheCalls:
+    """What the calls of a batched cache share: checks of their tensors, and
+    their device and streams.  A cache sets batch, head_dim, device, _index, _own,
+    _met, _ready, _vec_shape."""
 
     def _vec(self, t, name: str):
         if (isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.shape == self._vec_shape and t.is_contiguous()
@@ -634,6 +566,80 @@ class KV8Cache:
                 rc = f(*args)
         if rc:
             check(name, rc)
+
+
+class KV8Cache(_CacheCalls):
+    """An 8-bit key/value cache of `batch` sequences (moe_kv8_*): codes k, v
+    [batch, kv_heads, T_cap, head_dim] (int8 or e4m3) and steps k_scale,
+    v_scale, fp32 powers of two, [batch, kv_heads, T_cap / block]; with the
+    scratch that attention of up to max_rows rows needs (weights: also for its
+    position weights) and the calls' error word err (int32 [1]: 1 = a position,
+    count or length outside the cache, 2 = an infinity or NaN was appended).
+
+    pos, counts, lens are int32 [batch] CUDA tensors, read on the device.
+    buffers: (k, v, k_scale, v_scale) to use instead of new ones.  ws: scratch
+    (uint8, at least as large as the cache's own would be) to use instead
+    of new one.  The scratch grows with max_rows and the query heads, and with weights
+    by 4 bytes a position, query head and row: it can be as large as the codes, so
+    caches whose calls follow one another, as a model's layers do, share one
+    (ws=first.ws).  Calls that can overlap on the GPU need scratch of
+    their own and must not write one cache.
+
+    Calls run on the current stream of the cache's device, or on `stream`.
+    The first call on a stream waits for what made the cache (not while the stream is
+    captured into a graph: capture after the device has been waited for), and the
+    cache's memory is kept until the streams that used it are done.  Inputs and results
+    of a call on an explicit `stream` are ordered by the caller, with wait_stream, as tensors
+    between streams are; they may be dropped right after it."""
+
+    ERR_RANGE, ERR_NONFINITE = 1, 2
+
+    def __init__(self, T_cap: int, batch: int = 1, q_heads: int = 16, kv_heads: int = 2, head_dim: int = 256,
+                 block: int = 64, fmt: str = "int8", max_rows: int = 8, weights: bool = False, device="cuda",
+                 buffers=None, ws=None):
+        if fmt not in _KV8_FMT:
+            raise ValueError(f"fmt must be one of {sorted(_KV8_FMT)}")
+        code, self.dtype = _KV8_FMT[fmt]
+        self.T_cap, self.batch, self.q_heads, self.kv_heads = T_cap, batch, q_heads, kv_heads
+        self.head_dim, self.block, self.fmt, self.max_rows, self.weights = head_dim, block, fmt, max_rows, weights
+        self._c = Kv8(batch, q_heads, kv_heads, head_dim, T_cap, block, code)
+        n = C.c_size_t()
+        check("moe_kv8_attn_workspace_size",
+              lib().moe_kv8_attn_workspace_size(C.byref(self._c), max_rows, 1 if weights else 0, C.byref(n)))
+        rows, steps = (batch, kv_heads, T_cap, head_dim), (batch, kv_heads, T_cap // block)
+        if buffers is None:
+            buffers = (torch.zeros(rows, dtype=self.dtype, device=device), torch.zeros(rows, dtype=self.dtype, device=device),
+                       torch.zeros(steps, device=device), torch.zeros(steps, device=device))
+        self.k, self.v, self.k_scale, self.v_scale = buffers
+        for name, t, dt, shape in (("k", self.k, self.dtype, rows), ("v", self.v, self.dtype, rows),
+                                   ("k_scale", self.k_scale, torch.float32, steps),
+                                   ("v_scale", self.v_scale, torch.float32, steps)):
+            _need(t, name, dt, shape)
+        self.device = self.k.device
+        if any(t.device != self.device for t in buffers):
+            raise ValueError("the cache's buffers must be on one device")
+        if ws is None:
+            ws = torch.empty(n.value, dtype=torch.uint8, device=self.device)
+        _need(ws, "ws", torch.uint8, (None,))
+        if ws.numel() < n.value or ws.device != self.device:
+            raise ValueError(f"ws must have at least {n.value} bytes, on {self.device}; got {ws.numel()} on {ws.device}")
+        self.ws = ws
+        self.err = torch.zeros(1, dtype=torch.int32, device=self.device)
+        made = torch.cuda.current_stream(self.device)
+        self._met, self._own = {made.cuda_stream}, (*buffers, self.ws, self.err)
+        with torch.cuda.stream(made):
+            self._ready = None if torch.cuda.is_current_stream_capturing() else made.record_event()
+        c = self._c
+        c.k_dev, c.v_dev, c.k_scale_dev, c.v_scale_dev = (t.data_ptr() for t in buffers)
+        # What every call needs, once: a decode step is a few microseconds of
+        # device time, so the binding's own time is most of a small call's.
+        self._index = self.device.index
+        self._ref = C.byref(c)
+        self._ws, self._err, self._ws_bytes = self.ws.data_ptr(), self.err.data_ptr(), ws.numel()
+        self._vec_shape, self._acc_shape = (batch,), (batch, kv_heads, T_cap)
+        L = lib()
+        self._f_append, self._f_read, self._f_attn, self._f_evict = (L.moe_kv8_append, L.moe_kv8_read, L.moe_kv8_attn,
+                                                                     L.moe_kv8_evict)
 
     def append(self, k_new: torch.Tensor, v_new: torch.Tensor, pos: torch.Tensor, counts=None, err=None, stream=None):
         """Quantise rows [batch, M, kv_heads, head_dim] (bf16, fp16 or fp32; strided
@@ -724,6 +730,204 @@ class KV8Cache:
         if stream is not None:
             self._keep(stream, lens, acc, dst_acc, err)
         return idx, n
+
+
+class KVCache(_CacheCalls):
+    """A 16-bit key/value cache of `batch` sequences (moe_kv_*): k, v bf16 or fp16
+    [batch, kv_heads, T_cap, head_dim], with the scratch that attention of up to
+    max_rows rows, behind a shared prefix of up to max_prefix positions, needs, and the
+    calls' error word err (int32 [1]: 1 = a position or count outside the cache, 4 = a
+    device wait gave up).
+
+    window: a row at position p sees the positions t <= p with t > p - window or t <
+    sinks; None: all t <= p.  With a window the slots behind the first `sinks` are a
+    ring: sequences may grow past T_cap, which has to be at least sinks + window +
+    max_rows - 1.
+
+    pos, counts are int32 [batch] CUDA tensors, read on the device.  buffers: (k, v) to
+    use instead of new ones.  ws: scratch to use instead of new one, as KV8Cache's; caches whose
+    calls follow one another share one (ws=first.ws).  Streams: as KV8Cache's."""
+
+    ERR_RANGE, ERR_TIMEOUT = 1, 4
+
+    def __init__(self, T_cap: int, batch: int = 1, q_heads: int = 16, kv_heads: int = 2, head_dim: int = 256,
+                 dtype=torch.bfloat16, window=None, sinks: int = 0, max_rows: int = 8, max_prefix: int = 0, device="cuda",
+                 buffers=None, ws=None):
+        if dtype not in _Q_TYPES:
+            raise ValueError("dtype must be torch.bfloat16 or torch.float16")
+        if window is not None and window < 1:
+            raise ValueError("window must be at least 1, or None")
+        self.dtype = dtype
+        self.T_cap, self.batch, self.q_heads, self.kv_heads, self.head_dim = T_cap, batch, q_heads, kv_heads, head_dim
+        self.window, self.sinks, self.max_rows, self.max_prefix = window, sinks, max_rows, max_prefix
+        self._c = Kv(batch, q_heads, kv_heads, head_dim, T_cap, _ROW_TYPES[dtype], window or 0, sinks)
+        n = C.c_size_t()
+        check("moe_kv_attn_workspace_size",
+              lib().moe_kv_attn_workspace_size(C.byref(self._c), max_rows, max_prefix, C.byref(n)))
+        shape = (batch, kv_heads, T_cap, head_dim)
+        if buffers is None:
+            buffers = (torch.zeros(shape, dtype=dtype, device=device), torch.zeros(shape, dtype=dtype, device=device))
+        self.k, self.v = buffers
+        for name, t in (("k", self.k), ("v", self.v)):
+            _need(t, name, dtype, shape)
+        self.device = self.k.device
+        if self.v.device != self.device:
+            raise ValueError("the cache's buffers must be on one device")
+        if ws is None:
+            ws = torch.empty(n.value, dtype=torch.uint8, device=self.device)
+        _need(ws, "ws", torch.uint8, (None,))
+        if ws.numel() < n.value or ws.device != self.device:
+            raise ValueError(f"ws must have at least {n.value} bytes, on {self.device}; got {ws.numel()} on {ws.device}")
+        self.ws = ws
+        self.err = torch.zeros(1, dtype=torch.int32, device=self.device)
+        made = torch.cuda.current_stream(self.device)
+        self._met, self._own = {made.cuda_stream}, (self.k, self.v, self.ws, self.err)
+        with torch.cuda.stream(made):
+            self._ready = None if torch.cuda.is_current_stream_capturing() else made.record_event()
+        self._c.k_dev, self._c.v_dev = self.k.data_ptr(), self.v.data_ptr()
+        self._index = self.device.index
+        self._ref = C.byref(self._c)
+        self._ws, self._err, self._ws_bytes = self.ws.data_ptr(), self.err.data_ptr(), ws.numel()
+        self._vec_shape = (batch,)
+        L = lib()
+        self._f_append, self._f_attn = L.moe_kv_append, L.moe_kv_attn
+
+    def append(self, k_new: torch.Tensor, v_new: torch.Tensor, pos: torch.Tensor, counts=None, err=None, stream=None):
+        """Rows [batch, M, kv_heads, head_dim] (bf16, fp16 or fp32; strided views with a
+        contiguous last dimension) into positions pos[b] .. pos[b] + M - 1, or +
+        counts[b] - 1 (moe_kv_append)."""
+        k = self._view(k_new, "k_new", self.kv_heads, _ROW_TYPES)
+        v = self._view(v_new, "v_new", self.kv_heads, _ROW_TYPES)
+        M = k_new.size(1)
+        if k.type != v.type or M != v_new.size(1):
+            raise ValueError("k_new and v_new must have one shape and type")
+        self._run("moe_kv_append", self._f_append, self._ref, k, v, M, self._vec(pos, "pos"),
+                  None if counts is None else self._vec(counts, "counts"),
+                  self._err if err is None else self._like(err, "err", torch.int32, (1,)), self._on(stream))
+        if stream is not None:
+            self._keep(stream, k_new, v_new, pos, counts, err)
+
+    def _prefix(self, t, name: str) -> Rows:
+        """A [n, kv_heads, head_dim] tensor, strided but for its last dimension."""
+        if isinstance(t, torch.Tensor) and t.dim() == 3 and t.dtype is self.dtype and t.get_device() == self._index:
+            n, g, d = t.shape
+            if g == self.kv_heads and d == self.head_dim and 1 <= n <= self.max_prefix:
+                return _rows_of(t.unsqueeze(0), name)
+        got = f"{tuple(t.shape)} {t.dtype} on {t.device}" if isinstance(t, torch.Tensor) else type(t).__name__
+        raise ValueError(f"{name} must be {self.dtype} [n, {self.kv_heads}, {self.head_dim}] on {self.device}, 1 <= n <= "
+                         f"max_prefix={self.max_prefix}; got {got}")
+
+    def attend(self, q: torch.Tensor, pos: torch.Tensor, counts=None, scale=None, prefix=None, out=None, err=None, stream=None):
+        """Attention of q [batch, M, q_heads, head_dim] (the cache's dtype, M <= max_rows)
+        at positions pos[b] .. pos[b] + M - 1 (moe_kv_attn); returns (o, err) with o like q.
+        scale: 1 / sqrt(head_dim) by default.  prefix: (k, v), each [n, kv_heads,
+        head_dim], that every row sees besides its sequence's own positions (which count from
+        0 behind it); read once for the batch."""
+        self._view(q, "q", self.q_heads, (self.dtype,))
+        r, M, h = _rows_of(q, "q"), q.size(1), self._on(stream)
+        if M > self.max_rows:
+            raise ValueError(f"q has {M} rows; the cache was built for max_rows={self.max_rows}")
+        shape = (self.batch, M, self.q_heads, self.head_dim)
+        pk = pv = None
+        n = 0
+        if prefix is not None:
+            if self.window is not None:
+                raise ValueError("a prefix needs a cache without a window")
+            pk, pv = self._prefix(prefix[0], "prefix k"), self._prefix(prefix[1], "prefix v")
+            n = prefix[0].size(0)
+            if prefix[1].size(0) != n:
+                raise ValueError("the prefix's k and v must have one length")
+        if out is None:
+            out = self._new(shape, self.dtype, stream)
+        o = self._like(out, "out", self.dtype, shape)
+        e = self._err if err is None else self._like(err, "err", torch.int32, (1,))
+        self._run("moe_kv_attn", self._f_attn, self._ref, r, M, self._vec(pos, "pos"),
+                  None if counts is None else self._vec(counts, "counts"), pk, pv, n,
+                  self.head_dim ** -0.5 if scale is None else scale, o, self._ws, self._ws_bytes, e, h)
+        if stream is not None:
+            self._keep(stream, q, pos, counts, out, err, *(prefix or ()))
+        return out, self.err if err is None else err
+
+
+def _rows_of(t: torch.Tensor, name: str) -> Rows:
+    """moe_rows of [batch, M, heads, head_dim] that the attention kernels read
+    in 16-byte pieces; dimensions of one entry have no stride."""
+    s = [0 if n == 1 else x for n, x in zip(t.shape[:3], t.stride())]
+    if t.stride(3) != 1 or t.data_ptr() % 16 or any(x % 8 for x in s):
+        raise ValueError(f"{name} must have a contiguous last dimension, a base that is a multiple of 16 bytes and strides that are "
+                         f"multiples of 8 elements; got strides {t.stride()}, base {t.data_ptr():#x}")
+    return Rows(t.data_ptr(), _ROW_TYPES[t.dtype], *s)
+
+
+def window_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window=None, sinks: int = 0, pos=None, counts=None,
+                     scale=None, out=None, err=None, ws=None, stream=None):
+    """Causal attention of prompts (moe_window_attn): q [batch, M, q_heads, head_dim] against
+    k, v [batch, T, kv_heads, head_dim] (bf16 or fp16, one type; strided views with a
+    contiguous last dimension), row m of sequence b at position pos[b] + m (pos None: T - M),
+    m < counts[b] (None: M).  A row at position p sees the positions t <= p with t > p -
+    window or t < sinks (window None: all t <= p).  Returns (o like q, contiguous; err int32 [1]: 1 =
+    rows outside the positions, 4 = a device wait gave up).  pos, counts: int32 [batch] on q's device;
+    pos[b] < 0: an idle sequence.  Rows without work get zeros.
+
+    Runs on the current stream of q's device, or on `stream`: then inputs and results are
+    ordered by the caller, as tensors between streams are; inputs may be dropped right after the call.
+    ws: scratch (uint8, window_attention_workspace bytes) to use instead of new one."""
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == 4 and t.dtype in _Q_TYPES and t.dtype is q.dtype
+                and t.device == q.device):
+            got = f"{tuple(t.shape)} {t.dtype} on {t.device}" if isinstance(t, torch.Tensor) else type(t).__name__
+            raise ValueError(f"{name} must be a [batch, rows, heads, head_dim] CUDA tensor, bf16 or fp16 like q; got {got}")
+    B, M, Hq, D = q.shape
+    _, T, Hkv, _ = k.shape
+    if k.shape != v.shape or k.size(0) != B or k.size(3) != D:
+        raise ValueError(f"q {tuple(q.shape)}, k {tuple(k.shape)} and v {tuple(v.shape)} do not go together")
+    if window is not None and window < 1:
+        raise ValueError("window must be at least 1, or None")
+    dev = q.device
+    for name, t in (("pos", pos), ("counts", counts)):
+        if t is not None and not (isinstance(t, torch.Tensor) and t.dtype is torch.int32 and tuple(t.shape) == (B,)
+                                  and t.is_contiguous() and t.device == dev):
+            raise ValueError(f"{name} must be a contiguous int32 tensor of shape [{B}] on {dev}")
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"the stream must be on {dev}")
+    rq, rk, rv = _rows_of(q, "q"), _rows_of(k, "k"), _rows_of(v, "v")
+    d = Window(B, Hq, Hkv, D, M, T, window or 0, sinks)
+    n = C.c_size_t()
+    check("moe_window_attn_workspace_size", lib().moe_window_attn_workspace_size(C.byref(d), C.byref(n)))
+    with torch.cuda.device(dev), torch.cuda.stream(stream):
+        made = []
+        if out is None:
+            out = torch.empty((B, M, Hq, D), dtype=q.dtype, device=dev)
+            made.append(out)
+        if err is None:
+            err = torch.zeros(1, dtype=torch.int32, device=dev)
+            made.append(err)
+        if ws is None and n.value:
+            ws = torch.empty(n.value, dtype=torch.uint8, device=dev)
+        _need(out, "out", q.dtype, (B, M, Hq, D))
+        _need(err, "err", torch.int32, (1,))
+        if ws is not None:
+            _need(ws, "ws", torch.uint8, (None,))
+        if any(t is not None and t.device != dev for t in (out, err, ws)):
+            raise ValueError(f"out, err and ws must be on {dev}")
+        check("moe_window_attn",
+              lib().moe_window_attn(C.byref(d), rq, rk, rv, None if pos is None else pos.data_ptr(),
+                                    None if counts is None else counts.data_ptr(), D ** -0.5 if scale is None else scale,
+                                    out.data_ptr(), None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
+                                    err.data_ptr(), torch.cuda.current_stream(dev).cuda_stream))
+    if stream is not None:
+        _CacheCalls._keep(stream, q, k, v, pos, counts, out, err, ws)
+        for t in made:
+            t.record_stream(torch.cuda.current_stream(dev))
+    return out, err
+
+
+def window_attention_workspace(batch: int, q_heads: int, kv_heads: int, head_dim: int, rows: int, positions: int) -> int:
+    """Bytes of scratch that window_attention of these sizes needs (moe_window_attn_workspace_size)."""
+    n = C.c_size_t()
+    check("moe_window_attn_workspace_size",
+          lib().moe_window_attn_workspace_size(C.byref(Window(batch, q_heads, kv_heads, head_dim, rows, positions, 0, 0)), C.byref(n)))
+    return n.value
 
 
 def debug_set(skip_row: int = -1, timeout_ns: int = 0) -> None:

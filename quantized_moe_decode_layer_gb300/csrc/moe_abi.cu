@@ -8,6 +8,7 @@
 #include <cstring>
 
 #include "moe_internal.h"
+#include "moe_kv.h"
 #include "moe_kv8.h"
 #include "moe_unpack.cuh"
 
@@ -899,6 +900,182 @@ int moe_kv8_evict(const moe_kv8 *src, const moe_kv8 *dst, const int32_t *lens_de
     }
     return launch_kv8_evict(*src, *dst, lens_dev, acc_dev, budget, sinks, recent, dst_acc_dev, idx_dev, lens_out_dev,
                             err_dev, reinterpret_cast<cudaStream_t>(stream));
+}
+
+// Head layout, window and lengths of the 16-bit cache's calls.
+static int kv_shape_check(int batch, int q_heads, int kv_heads, int head_dim, int slots, int window, int sinks)
+{
+    if (batch < 1 || kv_heads < 1 || q_heads < 1 || slots < 1 || window < 0 || sinks < 0) return MOE_ERR_INVALID_ARG;
+    if (window == 0 && sinks != 0) return MOE_ERR_INVALID_ARG;
+    if (head_dim != 64 && head_dim != 128 && head_dim != 256) return MOE_ERR_UNSUPPORTED;
+    if (batch > MOE_KV_MAX_BATCH || kv_heads > MOE_KV_MAX_HEADS || slots > MOE_KV_MAX_SLOTS) return MOE_ERR_UNSUPPORTED;
+    if (window > MOE_KV_MAX_POSITIONS || sinks > MOE_KV_MAX_SLOTS) return MOE_ERR_UNSUPPORTED;
+    if (q_heads % kv_heads != 0 || q_heads / kv_heads > MOE_KV_MAX_GROUP) return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
+// Shape of a 16-bit cache for calls of M rows; the buffers too when `buffers`.
+static int kv_check(const moe_kv *c, int M, bool buffers)
+{
+    if (!c) return MOE_ERR_INVALID_ARG;
+    const int rc = kv_shape_check(c->batch, c->q_heads, c->kv_heads, c->head_dim, c->T_cap, c->window, c->sinks);
+    if (rc) return rc;
+    if (c->type != MOE_BF16 && c->type != MOE_F16) return MOE_ERR_UNSUPPORTED;
+    if (c->window && (long long)c->sinks + c->window + M - 1 > c->T_cap) return MOE_ERR_INVALID_ARG;
+    if (buffers && (!c->k_dev || !c->v_dev || !aligned16(c->k_dev) || !aligned16(c->v_dev))) return MOE_ERR_INVALID_ARG;
+    return MOE_OK;
+}
+
+// Rows that the attention kernels read in 16-byte pieces.
+static bool kv_rows_ok(const moe_rows *r, int type)
+{
+    return r && r->data_dev && r->type == type && aligned16(r->data_dev) && r->seq >= 0 && r->row >= 0 && r->head >= 0 &&
+           r->seq % 8 == 0 && r->row % 8 == 0 && r->head % 8 == 0;
+}
+
+static bool kv_scale_ok(float scale) { return scale > 0.f && scale <= 1e30f; }
+
+int moe_kv_append(const moe_kv *cache, const moe_rows *k_new, const moe_rows *v_new, int M, const int32_t *pos_dev,
+                  const int32_t *counts_dev, int *err_dev, moe_stream_t stream)
+{
+    const int rc = kv_check(cache, 1, true);
+    if (rc) return rc;
+    if (!kv8_rows_ok(k_new, MOE_F32) || !kv8_rows_ok(v_new, MOE_F32) || k_new->type != v_new->type)
+        return MOE_ERR_INVALID_ARG;
+    if (!pos_dev || !err_dev || M < 1 || M > MOE_KV_MAX_SLOTS || (!cache->window && M > cache->T_cap))
+        return MOE_ERR_INVALID_ARG;
+    return launch_kv_append(*cache, *k_new, *v_new, M, pos_dev, counts_dev, err_dev,
+                            reinterpret_cast<cudaStream_t>(stream));
+}
+
+int moe_kv_attn_workspace_size(const moe_kv *cache, int M, int max_prefix, size_t *bytes)
+{
+    if (M < 1 || M > MOE_KV_MAX_ROWS || max_prefix < 0 || max_prefix > MOE_KV_MAX_SLOTS || !bytes) return MOE_ERR_INVALID_ARG;
+    const int rc = kv_check(cache, M, false);
+    if (rc) return rc;
+    if (cache->window && max_prefix) return MOE_ERR_INVALID_ARG;
+    *bytes = kv_attn_workspace_bytes(cache->batch, cache->kv_heads, cache->q_heads / cache->kv_heads, cache->head_dim, M,
+                                     max_prefix);
+    return MOE_OK;
+}
+
+int moe_kv_attn(const moe_kv *cache, const moe_rows *q, int M, const int32_t *pos_dev, const int32_t *counts_dev,
+                const moe_rows *prefix_k, const moe_rows *prefix_v, int prefix_len, float scale, void *o_dev, void *ws_dev,
+                size_t ws_bytes, int *err_dev, moe_stream_t stream)
+{
+    if (M < 1 || M > MOE_KV_MAX_ROWS) return MOE_ERR_INVALID_ARG;
+    const int rc = kv_check(cache, M, true);
+    if (rc) return rc;
+    if (!kv_rows_ok(q, cache->type) || !pos_dev || !o_dev || !ws_dev || !err_dev || !aligned16(o_dev) || !aligned16(ws_dev) ||
+        M > cache->T_cap || !kv_scale_ok(scale))
+        return MOE_ERR_INVALID_ARG;
+    if ((prefix_k == nullptr) != (prefix_v == nullptr) || (prefix_k == nullptr) != (prefix_len == 0) || prefix_len < 0 ||
+        prefix_len > MOE_KV_MAX_SLOTS)
+        return MOE_ERR_INVALID_ARG;
+    if (prefix_len && (cache->window || !kv_rows_ok(prefix_k, cache->type) || !kv_rows_ok(prefix_v, cache->type)))
+        return MOE_ERR_INVALID_ARG;
+    const int G = cache->q_heads / cache->kv_heads;
+    if (ws_bytes < kv_attn_workspace_bytes(cache->batch, cache->kv_heads, G, cache->head_dim, M, prefix_len))
+        return MOE_ERR_BUFFER_TOO_SMALL;
+    KvCall p = {};
+    p.q = static_cast<const uint16_t *>(q->data_dev);
+    p.qb = q->seq;
+    p.qm = q->row;
+    p.qh = q->head;
+    p.k = static_cast<const uint16_t *>(cache->k_dev);
+    p.v = static_cast<const uint16_t *>(cache->v_dev);
+    p.km = p.vm = cache->head_dim;
+    p.kh = p.vh = (long long)cache->T_cap * cache->head_dim;
+    p.kb = p.vb = p.kh * cache->kv_heads;
+    if (prefix_len) {
+        p.pk = static_cast<const uint16_t *>(prefix_k->data_dev);
+        p.pkm = prefix_k->row;
+        p.pkh = prefix_k->head;
+        p.pv = static_cast<const uint16_t *>(prefix_v->data_dev);
+        p.pvm = prefix_v->row;
+        p.pvh = prefix_v->head;
+    }
+    p.P = prefix_len;
+    p.pos = pos_dev;
+    p.counts = counts_dev;
+    p.err = err_dev;
+    p.o = o_dev;
+    p.B = cache->batch;
+    p.M = M;
+    p.Hq = cache->q_heads;
+    p.Hkv = cache->kv_heads;
+    p.G = G;
+    p.D = cache->head_dim;
+    p.T = cache->T_cap;
+    p.limit = cache->window ? kKvMaxPos : cache->T_cap;
+    p.W = cache->window ? cache->window : kKvAll;
+    p.S = cache->sinks;
+    p.f16 = cache->type == MOE_F16;
+    p.c = scale * 1.4426950408889634f;
+    p.timeout_ns = g_timeout_ns;
+    return launch_kv_attn(p, ws_dev, reinterpret_cast<cudaStream_t>(stream));
+}
+
+static int window_check(const moe_window *s)
+{
+    if (!s || s->rows < 1 || s->rows > s->positions) return MOE_ERR_INVALID_ARG;
+    return kv_shape_check(s->batch, s->q_heads, s->kv_heads, s->head_dim, s->positions, s->window, s->sinks);
+}
+
+int moe_window_attn_workspace_size(const moe_window *shape, size_t *bytes)
+{
+    const int rc = window_check(shape);
+    if (rc) return rc;
+    if (!bytes) return MOE_ERR_INVALID_ARG;
+    *bytes = window_attn_workspace_bytes(*shape);
+    return MOE_OK;
+}
+
+int moe_window_attn(const moe_window *shape, const moe_rows *q, const moe_rows *k, const moe_rows *v,
+                    const int32_t *pos_dev, const int32_t *counts_dev, float scale, void *o_dev, void *ws_dev,
+                    size_t ws_bytes, int *err_dev, moe_stream_t stream)
+{
+    const int rc = window_check(shape);
+    if (rc) return rc;
+    if (!q || (q->type != MOE_BF16 && q->type != MOE_F16) || !kv_rows_ok(q, q->type) || !kv_rows_ok(k, q->type) ||
+        !kv_rows_ok(v, q->type) || !o_dev || !aligned16(o_dev) || !err_dev || !kv_scale_ok(scale))
+        return MOE_ERR_INVALID_ARG;
+    for (const moe_rows *r : {k, v})
+        if ((shape->batch > 1 && r->seq == 0) || (shape->positions > 1 && r->row == 0) || (shape->kv_heads > 1 && r->head == 0))
+            return MOE_ERR_INVALID_ARG;
+    const size_t need = window_attn_workspace_bytes(*shape);
+    if (need && (!ws_dev || !aligned16(ws_dev))) return MOE_ERR_INVALID_ARG;
+    if (ws_bytes < need) return MOE_ERR_BUFFER_TOO_SMALL;
+    KvCall p = {};
+    p.q = static_cast<const uint16_t *>(q->data_dev);
+    p.qb = q->seq;
+    p.qm = q->row;
+    p.qh = q->head;
+    p.k = static_cast<const uint16_t *>(k->data_dev);
+    p.kb = k->seq;
+    p.km = k->row;
+    p.kh = k->head;
+    p.v = static_cast<const uint16_t *>(v->data_dev);
+    p.vb = v->seq;
+    p.vm = v->row;
+    p.vh = v->head;
+    p.pos = pos_dev;
+    p.counts = counts_dev;
+    p.err = err_dev;
+    p.o = o_dev;
+    p.B = shape->batch;
+    p.M = shape->rows;
+    p.Hq = shape->q_heads;
+    p.Hkv = shape->kv_heads;
+    p.G = p.Hq / p.Hkv;
+    p.D = shape->head_dim;
+    p.T = p.limit = shape->positions;
+    p.W = shape->window ? shape->window : kKvAll;
+    p.S = shape->sinks;
+    p.f16 = q->type == MOE_F16;
+    p.c = scale * 1.4426950408889634f;
+    p.timeout_ns = g_timeout_ns;
+    return launch_window_attn(p, ws_dev, reinterpret_cast<cudaStream_t>(stream));
 }
 
 const char *moe_status_str(int status)

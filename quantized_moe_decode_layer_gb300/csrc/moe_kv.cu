@@ -1,0 +1,889 @@
+// 16-bit key/value cache of a batch of sequences: appending rows, and attention
+// of few rows (tokens, drafts, questions about one document) over it.
+//
+// What it computes: query row at position p, head h, g = h / (Hq / Hkv):
+//     s_t = scale q . k_t,  t <= p and (t > p - W or t < S)
+//     o   = sum_t softmax(s)_t v_t
+// and, behind a shared prefix, the prefix's positions in the same softmax.
+//
+// Split kernel.  A problem is the rows of one sequence that share a key/value
+// head (M rows times Hq / Hkv heads, in blocks of 16, 32 or 64) against the
+// positions that any of them sees, counted through: the first S, then the
+// window.  The prefix is one more problem per head with the whole batch's rows:
+// its keys are read once.  Every problem is cut into tiles of 64 positions, the
+// tiles of all problems lie in one line, and each CTA takes an equal stretch of
+// it: whatever the lengths are (they are read on the device), all CTAs move
+// the same number of bytes.  A stretch that holds a whole problem writes its outputs;
+// a part of one leaves its unnormalised sum, maximum and sum of weights (the
+// running maximum and sum of a softmax), which the merge kernel joins in
+// order.  Slot (CTA + problem) is a part's own: along the line either grows.
+//
+// It is bound by HBM: a tile's keys and values (64 to 16 KB) come through
+// cp.async into a ring of stages that runs ahead across problems; the products
+// (m16n8k16, 16 rows a warp) take less than half a tile's time at 16 rows.
+// Few rows leave the 128-row tcgen05 tiles seven eighths empty; those are taken where
+// rows are many (moe_kv_tile.cu).
+//
+// Scores, maxima, sums and outputs are fp32; the weights are rounded to the
+// cache's 16-bit type for the second product, an error of the size
+// of the output's own rounding.
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <cstring>
+#include <mutex>
+
+#include "moe_kv.h"
+#include "moe_kv8.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kWarps = kThreads / 32;
+
+struct Once {
+    std::once_flag flag[64];
+    int sms[64];
+};
+
+__device__ __forceinline__ uint32_t su32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool valid)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void ldsm(uint32_t (&r)[4], uint32_t a)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void ldsm_t(uint32_t (&r)[4], uint32_t a)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+template <bool F16>
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    if (F16)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <bool F16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi)
+{
+    uint32_t r;
+    if (F16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Rows of sequence b that the call works on, and the first one's position.
+__device__ __forceinline__ int rows_of(const KvCall &p, int b, int &p0, bool &bad)
+{
+    const int32_t last = p.T - p.M;
+    return kv8_rows(p.pos ? p.pos + b : &last, p.counts ? p.counts + b : nullptr, 0, p.M, p.limit, p0, bad);
+}
+
+// Positions that any of a sequence's n rows from p0 on sees: 0 .. ns - 1, then lo .. p0 + n - 1.
+__device__ __forceinline__ int visible(const KvCall &p, int p0, int n, int &lo, int &ns)
+{
+    lo = ns = 0;
+    if (n == 0) return 0;
+    lo = max(0, p0 - p.W + 1);
+    ns = min(p.S, lo);
+    return ns + p0 + n - lo;
+}
+
+// The line of tiles: the prefix's (all of head 0's, then head 1's ...), then for
+// each sequence its heads' and row blocks'.
+struct Line {
+    int HN;             // problems of a sequence
+    int NP;             // problems of the prefix
+    int ptiles;         // tiles of one of them
+    int total, share;   // tiles; tiles a CTA
+};
+__device__ __forceinline__ Line line_of(const KvCall &p, int seq_tiles, int ctas)
+{
+    Line l;
+    l.HN = p.Hkv * p.NRB;
+    l.NP = p.Hkv * p.NRBP;
+    l.ptiles = p.NRBP ? (p.P + kKvTile - 1) / kKvTile : 0;
+    l.total = l.NP * l.ptiles + seq_tiles * l.HN;
+    l.share = max(p.min_tiles, (l.total + ctas - 1) / ctas);
+    return l;
+}
+
+// What the threads need to know of a problem while its tiles are computed.
+struct Problem {
+    int id;         // slot = CTA + id
+    int n, ns, lo;  // positions seen; the first ns are 0 .. ns - 1, then from lo on
+    int p0, cnt;    // first row's position, rows; the prefix: every row of the batch, all of it visible
+    int tiles;
+    int whole;      // the CTA has all its tiles: outputs are written at once
+    int b, row0;    // sequence (-1: the prefix), first of the block's rows
+    int g;
+};
+
+template <int D, int WR>
+struct Lay {
+    static constexpr int RB = 16 * WR;
+    static constexpr int kRow = D * 2;
+    static constexpr int kStage = 2 * kKvTile * kRow;      // keys, values
+    static constexpr int kQ = RB * kRow;
+    static constexpr int NST = D == 64 ? (WR == 4 ? 3 : 4) : WR == 1 ? 3 : 2;
+    static constexpr int probs = NST * (kStage + kQ);
+    static constexpr int misc = probs + (NST + 1) * (int)sizeof(Problem);   // maxima and sums of the key groups
+    static constexpr int cum = misc + (2 * kWarps * 64 + 8) * 4;
+    static constexpr int total(int B) { return cum + (B + 1) * 4; }
+    static constexpr int ctas = D == 256 ? 1 : D == 128 ? 2 : 3;
+};
+
+// 16-byte chunk c of row r of a tile, swizzled so that eight rows' equal chunks lie in eight banks' groups.
+template <int D>
+__device__ __forceinline__ uint32_t at(int r, int c) { return (uint32_t)(r * (D * 2) + ((c ^ (r & 7)) << 4)); }
+
+template <bool F16, int D, int WR>
+__global__ void __launch_bounds__(kThreads, (Lay<D, WR>::ctas)) kv_split_kernel(const KvCall p)
+{
+    using L = Lay<D, WR>;
+    constexpr int RB = L::RB, WK = kWarps / WR, KW = kKvTile / WK, NST = L::NST;
+    extern __shared__ __align__(128) uint8_t sm[];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    Problem *probs = reinterpret_cast<Problem *>(sm + L::probs);
+    float *gm = reinterpret_cast<float *>(sm + L::misc), *gl = gm + kWarps * 64;
+    int *wsum = reinterpret_cast<int *>(gl + kWarps * 64);
+    int *cum = reinterpret_cast<int *>(sm + L::cum);
+    after_previous();
+
+    // tiles of every sequence, summed up
+    {
+        const int per = (p.B + kThreads - 1) / kThreads, b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+        int sum = 0;
+        for (int b = b0; b < b1; ++b) {
+            int p0, lo, ns;
+            bool bad;
+            const int n = rows_of(p, b, p0, bad);
+            if (bad && blockIdx.x == 0) atomicOr(p.err, kKv8ErrRange);
+            sum += (visible(p, p0, n, lo, ns) + kKvTile - 1) / kKvTile;
+            cum[b + 1] = sum;
+        }
+        int incl = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        if (lane == 31) wsum[warp] = incl;
+        __syncthreads();
+        int before = incl - sum;
+        for (int w = 0; w < warp; ++w) before += wsum[w];
+        for (int b = b0; b < b1; ++b) cum[b + 1] += before;
+        if (tid == 0) cum[0] = 0;
+        __syncthreads();
+    }
+    if (blockIdx.x == 0)
+        for (int b = tid; b <= p.B; b += kThreads) p.cum[b] = cum[b];
+    const Line ln = line_of(p, cum[p.B], gridDim.x);
+    const int t0 = min(ln.total, (int)blockIdx.x * ln.share), t1 = min(ln.total, t0 + ln.share);
+    if (t0 >= t1) return;
+
+    // ------------------------------------------------------------- loading
+    // cursor of the loads: tile li of problem lp (registers), NST - 1 tiles ahead
+    Problem lp;
+    int li, lcount = -1;            // problems opened by this CTA, less one
+    const uint16_t *lk, *lv;
+    long long lkm, lvm;
+    int lbase;                      // slot of position lo
+
+    auto open = [&](int id, int i) {
+        lp.id = id;
+        if (id < ln.NP) {
+            lp.b = -1;
+            lp.g = id / p.NRBP;
+            lp.row0 = (id - lp.g * p.NRBP) * RB;
+            lp.n = p.P;
+            lp.ns = lp.lo = 0;
+            lp.p0 = INT_MAX;
+            lp.cnt = p.M;
+            lk = p.pk + lp.g * p.pkh;
+            lv = p.pv + lp.g * p.pvh;
+            lkm = p.pkm;
+            lvm = p.pvm;
+            lbase = 0;
+        } else {
+            const int x = id - ln.NP, b = x / ln.HN, j = x - b * ln.HN;
+            bool bad;
+            lp.b = b;
+            lp.g = j / p.NRB;
+            lp.row0 = (j - lp.g * p.NRB) * RB;
+            lp.cnt = rows_of(p, b, lp.p0, bad);
+            lp.n = visible(p, lp.p0, lp.cnt, lp.lo, lp.ns);
+            lk = p.k + b * p.kb + lp.g * p.kh;
+            lv = p.v + b * p.vb + lp.g * p.vh;
+            lkm = p.km;
+            lvm = p.vm;
+            lbase = lp.lo < p.T ? lp.lo : p.S + (lp.lo - p.S) % (p.T - p.S);
+        }
+        lp.tiles = (lp.n + kKvTile - 1) / kKvTile;
+        li = i;
+        const int mine = t1 - t0;   // tiles of the CTA; from here on at most so many
+        lp.whole = i == 0 && lp.tiles <= mine;
+        ++lcount;
+        // its rows of q beside the stage of its first tile
+        constexpr int CH = D / 8;
+        uint8_t *qs = sm + NST * L::kStage + (lcount % NST) * L::kQ;
+        for (int x = tid; x < RB * CH; x += kThreads) {
+            const int r = x / CH, c = x % CH;
+            int row = lp.row0 + r, b = lp.b;
+            bool ok;
+            if (b < 0) {
+                b = row / (p.M * p.G);
+                row -= b * p.M * p.G;
+                ok = b < p.B;
+            } else {
+                ok = row < p.M * p.G;
+            }
+            const int m = row / p.G, h = row - m * p.G;
+            if (lp.b < 0 && ok) {
+                int q0;
+                bool bad;
+                ok = m < rows_of(p, b, q0, bad);
+            } else {
+                ok = ok && m < lp.cnt;
+            }
+            const uint16_t *src = ok ? p.q + b * p.qb + m * p.qm + (long long)(lp.g * p.G + h) * p.qh + 8 * c : p.q;
+            cp16(su32(qs) + at<D>(r, c), src, ok);
+        }
+    };
+    auto load = [&](int stage) {
+        constexpr int CH = D / 8, RPI = kThreads / CH;
+        const uint32_t ks = su32(sm + stage * L::kStage), vs = ks + kKvTile * L::kRow;
+        const int c = tid % CH;
+#pragma unroll
+        for (int r0 = 0; r0 < kKvTile; r0 += RPI) {
+            const int r = r0 + tid / CH, v = li * kKvTile + r;
+            int slot = v;
+            if (v >= lp.ns) {
+                slot = lbase + (v - lp.ns);
+                if (lp.b >= 0 && slot >= p.T) slot -= p.T - p.S;
+            }
+            const bool ok = v < lp.n;
+            if (!ok) slot = 0;
+            cp16(ks + at<D>(r, c), lk + slot * lkm + 8 * c, ok);
+            cp16(vs + at<D>(r, c), lv + slot * lvm + 8 * c, ok);
+        }
+    };
+
+    // the problem and tile that t0 falls on
+    int left = t1 - t0;   // tiles not yet loaded
+    {
+        int id, i;
+        const int pt = ln.NP * ln.ptiles;
+        if (t0 < pt) {
+            id = t0 / ln.ptiles;
+            i = t0 - id * ln.ptiles;
+        } else {
+            const int x = t0 - pt;
+            int lo = 0, hi = p.B - 1;   // the last b with cum[b] HN <= x and tiles of its own
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (cum[mid] * ln.HN <= x) lo = mid;
+                else hi = mid - 1;
+            }
+            const int each = cum[lo + 1] - cum[lo], y = x - cum[lo] * ln.HN, j = y / each;
+            id = ln.NP + lo * ln.HN + j;
+            i = y - j * each;
+        }
+        open(id, i);
+        if (tid == 0) probs[0] = lp;
+    }
+    // the next tile of the line; false at the CTA's end
+    auto advance = [&]() -> bool {
+        if (--left == 0) return false;
+        if (++li < lp.tiles) return true;
+        const int rest = left;
+        int id = lp.id + 1;
+        if (id >= ln.NP)
+            while (cum[(id - ln.NP) / ln.HN + 1] == cum[(id - ln.NP) / ln.HN]) ++id;   // a sequence without tiles (there is one with tiles behind it)
+        open(id, 0);
+        lp.whole = lp.tiles <= rest;
+        if (tid == 0) probs[lcount % (NST + 1)] = lp;
+        return true;
+    };
+
+    bool more = true;
+    load(0);
+    cp_commit();
+#pragma unroll 1
+    for (int s = 1; s < NST - 1; ++s) {
+        if (more) more = advance();
+        if (more) load(s);
+        cp_commit();
+    }
+
+    // ----------------------------------------------------------- computing
+    const int wr = warp % WR, wk = warp / WR;
+    const int rA = wr * 16 + (lane >> 2);          // this thread's rows: rA, rA + 8
+    float acc[D / 8][4];
+    float mrun[2], lrun[2];
+    int lowA = 0, highA = 0, lowB = 0, highB = 0;  // positions rows see: low < t <= high, or t < S
+    Problem cp;
+    int ci = -1, ccount = -1;
+    const int ntiles = t1 - t0;
+
+#pragma unroll 1
+    for (int it = 0; it < ntiles; ++it) {
+        const int stage = it % NST;
+        cp_wait<NST - 2>();
+        __syncthreads();
+        {
+            const int s = (it + NST - 1) % NST;
+            if (more) more = advance();
+            if (more) load(s);
+            cp_commit();
+        }
+        if (ci < 0 || ++ci == cp.tiles) {
+            ++ccount;
+            cp = probs[ccount % (NST + 1)];
+            if (ci < 0) {
+                // the CTA's first: where in the problem it starts
+                const int pt = ln.NP * ln.ptiles;
+                if (cp.b < 0) ci = t0 - cp.id * ln.ptiles;
+                else ci = (t0 - pt - cum[cp.b] * ln.HN) % cp.tiles;
+            } else {
+                ci = 0;
+            }
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+            mrun[0] = mrun[1] = -INFINITY;
+            lrun[0] = lrun[1] = 0.f;
+            auto limits = [&](int r, int &low, int &high) {
+                const int m = (cp.row0 + r) / p.G;
+                high = cp.b < 0 ? INT_MAX : m < cp.cnt ? cp.p0 + m : -1;
+                low = cp.b < 0 || m >= cp.cnt ? -1 : cp.p0 + m - p.W;
+            };
+            limits(rA, lowA, highA);
+            limits(rA + 8, lowB, highB);
+        }
+        const uint32_t ks = su32(sm + stage * L::kStage), vs = ks + kKvTile * L::kRow;
+        const uint32_t qs = su32(sm + NST * L::kStage + (ccount % NST) * L::kQ);
+        const int key0 = wk * KW;
+
+        // scores
+        float s[KW / 8][4];
+#pragma unroll
+        for (int j = 0; j < KW / 8; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+            uint32_t a[4], b[4];
+            ldsm(a, qs + at<D>(wr * 16 + (lane & 15), 2 * kk + (lane >> 4)));
+#pragma unroll
+            for (int j = 0; j < KW / 16; ++j) {
+                ldsm(b, ks + at<D>(key0 + 16 * j + (lane & 7) + ((lane >> 4) << 3), 2 * kk + ((lane >> 3) & 1)));
+                mma<F16>(s[2 * j], a, b[0], b[1]);
+                mma<F16>(s[2 * j + 1], a, b[2], b[3]);
+            }
+        }
+        // in units of log2; positions that a row does not see
+        const int v0 = ci * kKvTile + key0 + 2 * (lane & 3);
+        const int first = ci * kKvTile, last = min(first + kKvTile, cp.n) - 1;
+        const bool edge = first + kKvTile > cp.n ||
+                          (cp.b >= 0 && cp.cnt > 1 && last >= cp.ns &&
+                           (cp.lo + last - cp.ns > cp.p0 || cp.lo + max(first - cp.ns, 0) <= cp.p0 + cp.cnt - 1 - p.W));
+#pragma unroll
+        for (int j = 0; j < KW / 8; ++j)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) s[j][x] *= p.c;
+        if (edge) {
+#pragma unroll
+            for (int j = 0; j < KW / 8; ++j)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const int v = v0 + 8 * j + (x & 1), t = v < cp.ns ? v : cp.lo + v - cp.ns;
+                    const int low = x < 2 ? lowA : lowB, high = x < 2 ? highA : highB;
+                    if (!(v < cp.n && t <= high && (t > low || t < p.S))) s[j][x] = -INFINITY;
+                }
+        }
+        // running maximum and sum
+        float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int j = 0; j < KW / 8; ++j) {
+            mx[0] = fmaxf(mx[0], fmaxf(s[j][0], s[j][1]));
+            mx[1] = fmaxf(mx[1], fmaxf(s[j][2], s[j][3]));
+        }
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {
+            mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xFFFFFFFFu, mx[0], o));
+            mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xFFFFFFFFu, mx[1], o));
+        }
+        // The reference follows the maximum only when that is above it by more
+        // than 8 (a factor of 256, far from fp16's and fp32's ends): the
+        // output is hardly ever rescaled.
+        if (__any_sync(0xFFFFFFFFu, mx[0] > mrun[0] + 8.f || mx[1] > mrun[1] + 8.f)) {
+            float al[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const float mn = fmaxf(mrun[x], mx[x]);
+                al[x] = mrun[x] == mn ? 1.f : exp2f(mrun[x] - mn);
+                mrun[x] = mn;
+                lrun[x] *= al[x];
+            }
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+                acc[i][0] *= al[0];
+                acc[i][1] *= al[0];
+                acc[i][2] *= al[1];
+                acc[i][3] *= al[1];
+            }
+        }
+        const float ref[2] = {mrun[0] == -INFINITY ? 0.f : mrun[0], mrun[1] == -INFINITY ? 0.f : mrun[1]};
+#pragma unroll
+        for (int j = 0; j < KW / 8; ++j)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                s[j][x] = exp2f(s[j][x] - ref[x >> 1]);
+                lrun[x >> 1] += s[j][x];
+            }
+        // weighted values
+#pragma unroll
+        for (int j = 0; j < KW / 16; ++j) {
+            const uint32_t a[4] = {pack2<F16>(s[2 * j][0], s[2 * j][1]), pack2<F16>(s[2 * j][2], s[2 * j][3]),
+                                   pack2<F16>(s[2 * j + 1][0], s[2 * j + 1][1]), pack2<F16>(s[2 * j + 1][2], s[2 * j + 1][3])};
+#pragma unroll
+            for (int dd = 0; dd < D / 16; ++dd) {
+                uint32_t b[4];
+                ldsm_t(b, vs + at<D>(key0 + 16 * j + (lane & 15), 2 * dd + (lane >> 4)));
+                mma<F16>(acc[2 * dd], a, b[0], b[1]);
+                mma<F16>(acc[2 * dd + 1], a, b[2], b[3]);
+            }
+        }
+        if (ci + 1 < cp.tiles && it + 1 < ntiles) continue;
+
+        // ---------------------------------------- the problem's or CTA's end
+        // The key groups' outputs are joined in the stage that was just read
+        // (its next load comes after the next barrier).
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {
+            lrun[0] += __shfl_xor_sync(0xFFFFFFFFu, lrun[0], o);
+            lrun[1] += __shfl_xor_sync(0xFFFFFFFFu, lrun[1], o);
+        }
+        if ((lane & 3) == 0) {
+            gm[wk * RB + rA] = mrun[0];
+            gm[wk * RB + rA + 8] = mrun[1];
+            gl[wk * RB + rA] = lrun[0];
+            gl[wk * RB + rA + 8] = lrun[1];
+        }
+        __syncthreads();
+        float *out = reinterpret_cast<float *>(sm + stage * L::kStage);   // [RB][D]
+        float w[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            float m = gm[rA + 8 * x];
+            for (int k = 1; k < WK; ++k) m = fmaxf(m, gm[k * RB + rA + 8 * x]);
+            w[x] = mrun[x] == -INFINITY ? 0.f : exp2f(mrun[x] - m);
+        }
+#pragma unroll 1
+        for (int k = 0; k < WK; ++k) {
+            if (wk == k) {
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        // columns in an order that spreads a warp's rows over the banks
+                        float2 *to = reinterpret_cast<float2 *>(out + (rA + 8 * x) * D + ((8 * i + 2 * (lane & 3)) ^ (8 * ((rA + 8 * x) & 3))));
+                        float2 v = make_float2(acc[i][2 * x] * w[x], acc[i][2 * x + 1] * w[x]);
+                        if (k > 0) {
+                            const float2 was = *to;
+                            v.x += was.x;
+                            v.y += was.y;
+                        }
+                        *to = v;
+                    }
+            }
+            __syncthreads();
+        }
+        const bool direct = cp.whole && p.P == 0;
+        const int R = cp.b < 0 ? p.B * p.M * p.G : p.M * p.G;
+        const size_t slot = (size_t)blockIdx.x + cp.id;
+        constexpr int C4 = D / 4;
+        for (int x = tid; x < RB * C4; x += kThreads) {
+            const int r = x / C4, c = 4 * (x % C4), row = cp.row0 + r;
+            if (row >= R) break;
+            float m = gm[r], l = gl[r];
+            if (WK > 1) {
+                for (int k = 1; k < WK; ++k) m = fmaxf(m, gm[k * RB + r]);
+                l = 0.f;
+                for (int k = 0; k < WK; ++k) {
+                    const float mk = gm[k * RB + r];
+                    l += mk == -INFINITY ? 0.f : gl[k * RB + r] * exp2f(mk - m);
+                }
+            }
+            const float4 v = *reinterpret_cast<const float4 *>(out + r * D + (c ^ (8 * (r & 3))));
+            if (direct) {
+                const int mm = row / p.G, h = row - mm * p.G;
+                const float f = mm < cp.cnt && l != 0.f ? 1.f / l : 0.f;
+                uint2 u = make_uint2(0u, 0u);
+                if (mm < cp.cnt) u = make_uint2(pack2<F16>(v.x * f, v.y * f), pack2<F16>(v.z * f, v.w * f));
+                *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.o) +
+                                           (((size_t)cp.b * p.M + mm) * p.Hq + cp.g * p.G + h) * D + c) = u;
+            } else {
+                *reinterpret_cast<float4 *>(p.part_o + (slot * RB + r) * D + c) = v;
+                if (c == 0) *reinterpret_cast<float2 *>(p.part_ml + (slot * RB + r) * 2) = make_float2(m, l);
+            }
+        }
+    }
+}
+
+// Joins a row's parts in order: o = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m)
+// l_i with m the largest m_i.  One CTA per row and head; each warp takes every
+// kMergeWarps-th part, its lanes the columns.  Rows without positions get zeros.
+constexpr int kMergeWarps = 4;
+template <int D>
+__global__ void __launch_bounds__(32 * kMergeWarps) kv_merge_kernel(const KvCall p, int ctas)
+{
+    constexpr int VEC = D / 32;
+    __shared__ float red[kMergeWarps][D + 1], redm[kMergeWarps];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int hq = blockIdx.x % p.Hq, bm = blockIdx.x / p.Hq, m = bm % p.M, b = bm / p.M;
+    const int g = hq / p.G, h = hq - g * p.G;
+    uint16_t *o = static_cast<uint16_t *>(p.o) + ((size_t)bm * p.Hq + hq) * D;
+    int p0;
+    bool bad;
+    const int cnt = rows_of(p, b, p0, bad);
+    wait_for_previous();
+    if (m >= cnt) {
+        for (int d = tid; d < D; d += 32 * kMergeWarps) o[d] = 0;
+        return;
+    }
+    const Line ln = line_of(p, p.cum[p.B], ctas);
+    // the sequence's own parts: slots first .. first + n1 - 1
+    const int row = m * p.G + h, rb = row / p.RB, each = p.cum[b + 1] - p.cum[b];
+    const int j = g * p.NRB + rb, T0 = ln.NP * ln.ptiles + p.cum[b] * ln.HN + j * each;
+    const int c0 = T0 / ln.share, n1 = (T0 + each - 1) / ln.share - c0 + 1;
+    if (n1 == 1 && p.P == 0) return;   // written by the split kernel
+    const size_t first = (size_t)c0 + ln.NP + b * ln.HN + j;
+    const int r1 = row - rb * p.RB;
+    // the prefix's, of the split kernel or the tile kernel
+    const int prow = (b * p.M + m) * p.G + h;
+    size_t pfirst = 0;
+    int n2 = 0, r2 = 0;
+    if (p.P && p.NRBP) {
+        const int rbp = prow / p.RB, id = g * p.NRBP + rbp, q0 = id * ln.ptiles, a = q0 / ln.share;
+        n2 = (q0 + ln.ptiles - 1) / ln.share - a + 1;
+        pfirst = (size_t)a + id;
+        r2 = prow - rbp * p.RB;
+    } else if (p.P) {
+        n2 = p.nsplit;
+    }
+    const size_t rows = (size_t)p.B * p.M * p.G;
+    auto part = [&](int i, const float *&po) -> const float * {
+        if (i >= n1 && p.NRBP == 0) {
+            const size_t x = ((size_t)(i - n1) * p.Hkv + g) * rows + prow;
+            po = p.tile_o + x * D;
+            return p.tile_ml + x * 2;
+        }
+        const size_t x = i < n1 ? (first + i) * p.RB + r1 : (pfirst + i - n1) * p.RB + r2;
+        po = p.part_o + x * D;
+        return p.part_ml + x * 2;
+    };
+    const int n = n1 + n2;
+    float mx = -INFINITY;
+    for (int i = tid; i < n; i += 32 * kMergeWarps) {
+        const float *po;
+        mx = fmaxf(mx, __ldcg(part(i, po)));
+    }
+#pragma unroll
+    for (int s = 16; s >= 1; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, s));
+    if (lane == 0) redm[warp] = mx;
+    __syncthreads();
+    mx = redm[0];
+#pragma unroll
+    for (int w = 1; w < kMergeWarps; ++w) mx = fmaxf(mx, redm[w]);
+    float acc[VEC] = {}, l = 0.f;
+#pragma unroll 4
+    for (int i = warp; i < n; i += kMergeWarps) {
+        const float *po, *ml = part(i, po);
+        const float2 x = __ldcg(reinterpret_cast<const float2 *>(ml));
+        const float w = x.x == -INFINITY ? 0.f : exp2f(x.x - mx);
+        l = fmaf(x.y, w, l);
+#pragma unroll
+        for (int v = 0; v < VEC / 2; ++v) {
+            const float2 y = __ldcg(reinterpret_cast<const float2 *>(po) + v * 32 + lane);
+            acc[2 * v] = fmaf(y.x, w, acc[2 * v]);
+            acc[2 * v + 1] = fmaf(y.y, w, acc[2 * v + 1]);
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < VEC / 2; ++v) {
+        red[warp][64 * v + 2 * lane] = acc[2 * v];
+        red[warp][64 * v + 2 * lane + 1] = acc[2 * v + 1];
+    }
+    if (lane == 0) red[warp][D] = l;
+    __syncthreads();
+    float ls = 0.f;
+#pragma unroll
+    for (int w = 0; w < kMergeWarps; ++w) ls += red[w][D];
+    for (int d = 2 * tid; d < D; d += 64 * kMergeWarps) {
+        float x = 0.f, y = 0.f;
+#pragma unroll
+        for (int w = 0; w < kMergeWarps; ++w) {
+            x += red[w][d];
+            y += red[w][d + 1];
+        }
+        const float f = ls != 0.f ? 1.f / ls : 0.f;
+        *reinterpret_cast<uint32_t *>(o + d) = p.f16 ? pack2<true>(x * f, y * f) : pack2<false>(x * f, y * f);
+    }
+}
+
+// ------------------------------------------------------------------ append
+
+// Rows of a call that stay: of each sequence the last T - S (T where it has no
+// window), and those at the first S positions.  Thread: 8 elements of a row's head.
+struct AppendCall {
+    const void *k, *v;
+    long long kb, km, kh, vb, vm, vh;
+    uint16_t *to_k, *to_v;
+    const int32_t *pos, *counts;
+    int *err;
+    int B, M, Hkv, D, T, S, limit, f16, type, vec;
+    int nring, nfirst;   // candidates a sequence: in the ring, at the first positions
+};
+
+template <int TYPE>
+__device__ __forceinline__ void get8(const void *base, long long at, bool vec, float (&x)[8])
+{
+    if (TYPE == MOE_F32) {
+        const float *f = static_cast<const float *>(base) + at;
+        if (vec) {
+            const float4 a = __ldg(reinterpret_cast<const float4 *>(f)), b = __ldg(reinterpret_cast<const float4 *>(f) + 1);
+            x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+            x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = __ldg(f + i);
+        }
+    } else {
+        const uint16_t *h = static_cast<const uint16_t *>(base) + at;
+        uint32_t w[4];
+        if (vec) {
+            const uint4 a = __ldg(reinterpret_cast<const uint4 *>(h));
+            w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = __ldg(h + 2 * i) | (uint32_t)__ldg(h + 2 * i + 1) << 16;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (TYPE == MOE_F16) {
+                const float2 f = __half22float2(as_half2(w[i]));
+                x[2 * i] = f.x;
+                x[2 * i + 1] = f.y;
+            } else {
+                x[2 * i] = __uint_as_float(w[i] << 16);
+                x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+            }
+        }
+    }
+}
+
+template <int TYPE>
+__global__ void __launch_bounds__(256) kv_append_kernel(const AppendCall p)
+{
+    after_previous();
+    const int CH = p.D / 8, b = blockIdx.y;
+    int p0;
+    bool bad;
+    const int n = kv8_rows(p.pos, p.counts, b, p.M, p.limit, p0, bad);
+    if (bad && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.err, kKv8ErrRange);
+    if (n == 0) return;
+    const long long per = (long long)p.Hkv * CH, all = per * (p.nring + p.nfirst) * 2;
+    for (long long x = (long long)blockIdx.x * blockDim.x + threadIdx.x; x < all; x += (long long)gridDim.x * blockDim.x) {
+        const int is_v = x >= all / 2;
+        const long long y = is_v ? x - all / 2 : x;
+        const int u = (int)(y / per), e = (int)(y - u * per), g = e / CH, c = e - g * CH;
+        int t;
+        if (u < p.nring) {
+            t = p0 + n - 1 - u;
+            if (t < p0 || t < p.S) continue;
+        } else {
+            t = p0 + (u - p.nring);
+            if (t >= p0 + n || t >= p.S) continue;
+        }
+        const int slot = t < p.T ? t : p.S + (t - p.S) % (p.T - p.S);
+        float f[8];
+        if (is_v) get8<TYPE>(p.v, b * p.vb + (long long)(t - p0) * p.vm + g * p.vh + 8 * c, p.vec, f);
+        else get8<TYPE>(p.k, b * p.kb + (long long)(t - p0) * p.km + g * p.kh + 8 * c, p.vec, f);
+        uint4 w;
+        if (p.f16) w = make_uint4(pack2<true>(f[0], f[1]), pack2<true>(f[2], f[3]), pack2<true>(f[4], f[5]), pack2<true>(f[6], f[7]));
+        else w = make_uint4(pack2<false>(f[0], f[1]), pack2<false>(f[2], f[3]), pack2<false>(f[4], f[5]), pack2<false>(f[6], f[7]));
+        *reinterpret_cast<uint4 *>((is_v ? p.to_v : p.to_k) + (((long long)b * p.Hkv + g) * p.T + slot) * p.D + 8 * c) = w;
+    }
+}
+
+int row_block(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+
+struct KvWs {
+    size_t cum, ml, o, tml, to, total;
+};
+
+// Rows of the batch from which on the prefix goes through the tile kernel.
+constexpr int kTileRows = 1 << 30;
+
+KvWs kv_ws(int B, int Hkv, int G, int D, int M, int P)
+{
+    KvWs w;
+    const int rows = M * G, prows = B * rows;
+    const bool tiles = P > 0 && prows > kTileRows;
+    const int RB = row_block(P > 0 && !tiles ? prows : rows);
+    const size_t nprob = (size_t)B * Hkv * ((rows + RB - 1) / RB) + (P > 0 && !tiles ? (size_t)Hkv * ((prows + RB - 1) / RB) : 0);
+    const size_t slots = nprob + kKvMaxCtas, ns = tiles ? kv_prefix_splits(prows, Hkv, D, P) : 0;
+    w.cum = 0;
+    w.ml = align_up(((size_t)B + 1) * 4, 256);
+    w.o = align_up(w.ml + slots * RB * 8, 256);
+    w.tml = align_up(w.o + slots * RB * D * 4, 256);
+    w.to = align_up(w.tml + ns * Hkv * prows * 8, 256);
+    w.total = align_up(w.to + ns * Hkv * prows * D * 4, 256);
+    return w;
+}
+
+}  // namespace
+
+int kv_prefix_splits(int, int, int, int) { return 1; }
+
+size_t kv_attn_workspace_bytes(int batch, int kv_heads, int group, int head_dim, int M, int max_prefix)
+{
+    return kv_ws(batch, kv_heads, group, head_dim, M, max_prefix).total;
+}
+
+int launch_kv_append(const moe_kv &c, const moe_rows &k_new, const moe_rows &v_new, int M, const int32_t *pos,
+                     const int32_t *counts, int *err, cudaStream_t stream)
+{
+    AppendCall p;
+    memset(&p, 0, sizeof p);
+    p.k = k_new.data_dev;
+    p.kb = k_new.seq;
+    p.km = k_new.row;
+    p.kh = k_new.head;
+    p.v = v_new.data_dev;
+    p.vb = v_new.seq;
+    p.vm = v_new.row;
+    p.vh = v_new.head;
+    p.to_k = static_cast<uint16_t *>(c.k_dev);
+    p.to_v = static_cast<uint16_t *>(c.v_dev);
+    p.pos = pos;
+    p.counts = counts;
+    p.err = err;
+    p.B = c.batch;
+    p.M = M;
+    p.Hkv = c.kv_heads;
+    p.D = c.head_dim;
+    p.T = c.T_cap;
+    p.S = c.window ? c.sinks : 0;
+    p.limit = c.window ? kKvMaxPos : c.T_cap;
+    p.f16 = c.type == MOE_F16;
+    p.nring = std::min(M, c.T_cap - p.S);
+    p.nfirst = std::min(M, p.S);
+    const int unit = k_new.type == MOE_F32 ? 4 : 8;
+    auto wide = [&](const moe_rows &r) {
+        return reinterpret_cast<uintptr_t>(r.data_dev) % 16 == 0 && r.seq % unit == 0 && r.row % unit == 0 && r.head % unit == 0;
+    };
+    p.vec = wide(k_new) && wide(v_new);
+    const long long all = 2LL * p.Hkv * (p.D / 8) * (p.nring + p.nfirst);
+    const dim3 grid((unsigned)std::min<long long>((all + 255) / 256, std::max(1, 8192 / p.B)), p.B);
+    auto *kernel = k_new.type == MOE_F32 ? kv_append_kernel<MOE_F32> : k_new.type == MOE_F16 ? kv_append_kernel<MOE_F16> : kv_append_kernel<MOE_BF16>;
+    const cudaError_t e = launch_after(kernel, grid, 256, 0, 0, stream, p);
+    if (e != cudaSuccess) { note_cuda_error((int)e); return MOE_ERR_CUDA; }
+    note_launch();
+    return MOE_OK;
+}
+
+// p: q, k, v, the prefix, lengths, shapes, scale and output; the rest is set here.
+int launch_kv_attn(KvCall &p, void *ws, cudaStream_t stream)
+{
+    const int rows = p.M * p.G, prows = p.B * rows;
+    const bool tiles = p.P > 0 && prows > kTileRows;
+    const KvWs w = kv_ws(p.B, p.Hkv, p.G, p.D, p.M, p.P);
+    uint8_t *base = static_cast<uint8_t *>(ws);
+    p.RB = row_block(p.P > 0 && !tiles ? prows : rows);
+    p.NRB = (rows + p.RB - 1) / p.RB;
+    p.NRBP = p.P > 0 && !tiles ? (prows + p.RB - 1) / p.RB : 0;
+    p.min_tiles = 1;
+    p.cum = reinterpret_cast<int *>(base + w.cum);
+    p.part_ml = reinterpret_cast<float *>(base + w.ml);
+    p.part_o = reinterpret_cast<float *>(base + w.o);
+    p.tile_ml = reinterpret_cast<float *>(base + w.tml);
+    p.tile_o = reinterpret_cast<float *>(base + w.to);
+    p.nsplit = tiles ? kv_prefix_splits(prows, p.Hkv, p.D, p.P) : 0;
+    // the line's length has to fit an int
+    const long long seen = std::min<long long>((long long)p.S + p.W + p.M, (long long)p.T);
+    const long long most = (seen / kKvTile + 2) * p.B * p.Hkv * p.NRB + ((long long)p.P / kKvTile + 1) * p.Hkv * p.NRBP;
+    if (most > INT_MAX / 2) return MOE_ERR_UNSUPPORTED;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || dev < 0 || dev >= 64) { note_cuda_error((int)e); return MOE_ERR_CUDA; }
+    int grid = 0;
+    auto go = [&](auto kernel, int smem, int ctas, Once &once) {
+        std::call_once(once.flag[dev], [&] {
+            e = cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+            if (e == cudaSuccess)
+                e = cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                         (int)cudaSharedmemCarveoutMaxShared);
+            if (e == cudaSuccess) e = cudaDeviceGetAttribute(&once.sms[dev], cudaDevAttrMultiProcessorCount, dev);
+        });
+        if (e == cudaSuccess && once.sms[dev] < 1) e = cudaErrorInvalidDevice;
+        if (e != cudaSuccess) return;
+        grid = (int)std::min<long long>(most, (long long)std::min(once.sms[dev], kMaxCtas) * ctas);
+        e = launch_after(kernel, dim3(grid), kThreads, smem, 0, stream, p);
+    };
+#define KV_GO(F, D, W)                                                                            \
+    do {                                                                                          \
+        static Once once;                                                                         \
+        static_assert(Lay<D, W>::total(MOE_KV8_MAX_BATCH) <= kSmemMax, "shared memory");          \
+        go(kv_split_kernel<F, D, W>, Lay<D, W>::total(p.B), Lay<D, W>::ctas, once);               \
+    } while (0)
+#define KV_GO_D(F, D)                  \
+    do {                               \
+        if (p.RB == 16) KV_GO(F, D, 1); \
+        else if (p.RB == 32) KV_GO(F, D, 2); \
+        else KV_GO(F, D, 4);           \
+    } while (0)
+#define KV_GO_F(F)                                 \
+    do {                                           \
+        if (p.D == 256) KV_GO_D(F, 256);           \
+        else if (p.D == 128) KV_GO_D(F, 128);      \
+        else KV_GO_D(F, 64);                       \
+    } while (0)
+    if (p.f16) KV_GO_F(true);
+    else KV_GO_F(false);
+#undef KV_GO_F
+#undef KV_GO_D
+#undef KV_GO
+    if (e != cudaSuccess) { note_cuda_error((int)e); return MOE_ERR_CUDA; }
+    note_launch();
+    auto *merge = p.D == 256 ? kv_merge_kernel<256> : p.D == 128 ? kv_merge_kernel<128> : kv_merge_kernel<64>;
+    e = launch_after(merge, dim3(p.B * p.M * p.Hq), 32 * kMergeWarps, 0, 0, stream, p, grid);
+    if (e != cudaSuccess) { note_cuda_error((int)e); return MOE_ERR_CUDA; }
+    note_launch();
+    return MOE_OK;
+}
+
+size_t window_attn_workspace_bytes(const moe_window &s)
+{
+    return kv_ws(s.batch, s.kv_heads, s.q_heads / s.kv_heads, s.head_dim, s.rows, 0).total;
+}
+
+int launch_window_attn(KvCall &p, void *ws, cudaStream_t stream) { return launch_kv_attn(p, ws, stream); }
+
+}  // namespace moe

@@ -1,0 +1,53 @@
+// Launches of the 16-bit key/value cache (moe_kv.cu, moe_kv_tile.cu) and the
+// parameters that its kernels share.
+#pragma once
+
+#include "moe_internal.h"
+
+namespace moe {
+
+constexpr int kKvTile = 64;           // positions a tile of the split kernel
+constexpr int kKvMaxCtas = 4 * kMaxCtas;
+constexpr int kKvMaxPos = 1 << 30;    // positions of a sequence whose cache is a ring
+constexpr int kKvAll = 1 << 30;       // window of a sequence that sees everything
+
+// One attention call: q, k, v as they lie (strides in elements), the visible
+// positions, and where partial results go.
+struct KvCall {
+    const uint16_t *q, *k, *v, *pk, *pv;
+    long long qb, qm, qh;             // q: sequence, row, head
+    long long kb, km, kh, vb, vm, vh; // keys, values: sequence, position (slot), head
+    long long pkm, pkh, pvm, pvh;     // the prefix's: position, head
+    const int32_t *pos, *counts;      // pos NULL: T - M
+    int *err;
+    void *o;                          // [B][M][Hq][D], q's type
+    int B, M, Hq, Hkv, G, D;
+    int T;                            // slots of a sequence
+    int limit;                        // positions that a sequence may have
+    int W, S;                         // window (kKvAll: none), first positions that stay visible
+    int P;                            // prefix positions (0: none)
+    int f16;
+    float c;                          // scale * log2(e)
+    // split kernel: problems of RB rows, NRB of them a sequence and head, NRBP of the prefix and head
+    int RB, NRB, NRBP;
+    int min_tiles;
+    float *part_o, *part_ml;          // [slot][RB][D], [slot][RB][2]: unnormalised output; maximum (log2), sum
+    int *cum;                         // [B + 1]: tiles of the sequences before b, for one head and row block
+    // tile kernel: the prefix's partial results, nsplit of them a row
+    int nsplit;
+    float *tile_o, *tile_ml;          // [split][Hkv][B M G][D], [...][2]
+    int *tile_flag;
+    long long timeout_ns;
+};
+
+size_t kv_attn_workspace_bytes(int batch, int kv_heads, int group, int head_dim, int M, int max_prefix);
+int launch_kv_append(const moe_kv &c, const moe_rows &k_new, const moe_rows &v_new, int M, const int32_t *pos,
+                     const int32_t *counts, int *err, cudaStream_t stream);
+int launch_kv_attn(KvCall &p, void *ws, cudaStream_t stream);
+size_t window_attn_workspace_bytes(const moe_window &s);
+int launch_window_attn(KvCall &p, void *ws, cudaStream_t stream);
+// Tiles of 128 rows: prompts (outputs written), or the prefix (partial results).
+int launch_kv_tiles(const KvCall &p, bool prefix, cudaStream_t stream);
+int kv_prefix_splits(int rows, int kv_heads, int head_dim, int P);
+
+}  // namespace moe
