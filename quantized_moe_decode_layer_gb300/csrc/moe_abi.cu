@@ -955,7 +955,7 @@ int moe_kv_attn_workspace_size(const moe_kv *cache, int M, int max_prefix, size_
     if (rc) return rc;
     if (cache->window && max_prefix) return MOE_ERR_INVALID_ARG;
     *bytes = kv_attn_workspace_bytes(cache->batch, cache->kv_heads, cache->q_heads / cache->kv_heads, cache->head_dim, M,
-                                     max_prefix);
+                                     max_prefix, false);
     return MOE_OK;
 }
 
@@ -975,7 +975,7 @@ int moe_kv_attn(const moe_kv *cache, const moe_rows *q, int M, const int32_t *po
     if (prefix_len && (cache->window || !kv_rows_ok(prefix_k, cache->type) || !kv_rows_ok(prefix_v, cache->type)))
         return MOE_ERR_INVALID_ARG;
     const int G = cache->q_heads / cache->kv_heads;
-    if (ws_bytes < kv_attn_workspace_bytes(cache->batch, cache->kv_heads, G, cache->head_dim, M, prefix_len))
+    if (ws_bytes < kv_attn_workspace_bytes(cache->batch, cache->kv_heads, G, cache->head_dim, M, prefix_len, true))
         return MOE_ERR_BUFFER_TOO_SMALL;
     KvCall p = {};
     p.q = static_cast<const uint16_t *>(q->data_dev);

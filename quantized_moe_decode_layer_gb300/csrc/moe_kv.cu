@@ -567,25 +567,26 @@ __global__ void __launch_bounds__(32 * kMergeWarps) kv_merge_kernel(const KvCall
         for (int d = tid; d < D; d += 32 * kMergeWarps) o[d] = 0;
         return;
     }
-    const Line ln = line_of(p, p.cum[p.B], ctas);
-    // the sequence's own parts: slots first .. first + n1 - 1
-    const int row = m * p.G + h, rb = row / p.RB, each = p.cum[b + 1] - p.cum[b];
-    const int j = g * p.NRB + rb, T0 = ln.NP * ln.ptiles + p.cum[b] * ln.HN + j * each;
-    const int c0 = T0 / ln.share, n1 = (T0 + each - 1) / ln.share - c0 + 1;
-    if (n1 == 1 && p.P == 0) return;   // written by the split kernel
-    const size_t first = (size_t)c0 + ln.NP + b * ln.HN + j;
-    const int r1 = row - rb * p.RB;
-    // the prefix's, of the split kernel or the tile kernel
+    // the sequence's own parts, of the split kernel: slots first .. first + n1 - 1
     const int prow = (b * p.M + m) * p.G + h;
-    size_t pfirst = 0;
-    int n2 = 0, r2 = 0;
-    if (p.P && p.NRBP) {
-        const int rbp = prow / p.RB, id = g * p.NRBP + rbp, q0 = id * ln.ptiles, a = q0 / ln.share;
-        n2 = (q0 + ln.ptiles - 1) / ln.share - a + 1;
-        pfirst = (size_t)a + id;
-        r2 = prow - rbp * p.RB;
-    } else if (p.P) {
-        n2 = p.nsplit;
+    size_t first = 0, pfirst = 0;
+    int n1 = 0, n2 = p.nsplit, r1 = 0, r2 = 0;
+    if (p.NRB) {
+        const Line ln = line_of(p, p.cum[p.B], ctas);
+        const int row = m * p.G + h, rb = row / p.RB, each = p.cum[b + 1] - p.cum[b];
+        const int j = g * p.NRB + rb, T0 = ln.NP * ln.ptiles + p.cum[b] * ln.HN + j * each;
+        const int c0 = T0 / ln.share;
+        n1 = (T0 + each - 1) / ln.share - c0 + 1;
+        if (n1 == 1 && p.P == 0) return;   // written by the split kernel
+        first = (size_t)c0 + ln.NP + b * ln.HN + j;
+        r1 = row - rb * p.RB;
+        // the prefix's, of the same kernel (or, nsplit of them, of the tile kernel)
+        if (p.NRBP) {
+            const int rbp = prow / p.RB, id = g * p.NRBP + rbp, q0 = id * ln.ptiles, a = q0 / ln.share;
+            n2 = (q0 + ln.ptiles - 1) / ln.share - a + 1;
+            pfirst = (size_t)a + id;
+            r2 = prow - rbp * p.RB;
+        }
     }
     const size_t rows = (size_t)p.B * p.M * p.G;
     auto part = [&](int i, const float *&po) -> const float * {
@@ -616,7 +617,8 @@ __global__ void __launch_bounds__(32 * kMergeWarps) kv_merge_kernel(const KvCall
     for (int i = warp; i < n; i += kMergeWarps) {
         const float *po, *ml = part(i, po);
         const float2 x = __ldcg(reinterpret_cast<const float2 *>(ml));
-        const float w = x.x == -INFINITY ? 0.f : exp2f(x.x - mx);
+        if (x.x == -INFINITY) continue;   // an empty part: its output was not written
+        const float w = exp2f(x.x - mx);
         l = fmaf(x.y, w, l);
 #pragma unroll
         for (int v = 0; v < VEC / 2; ++v) {
@@ -739,7 +741,7 @@ struct KvWs {
 };
 
 // Rows of the batch from which on the prefix goes through the tile kernel.
-constexpr int kTileRows = 1 << 30;
+constexpr int kTileRows = 64;
 
 KvWs kv_ws(int B, int Hkv, int G, int D, int M, int P)
 {
@@ -748,7 +750,7 @@ KvWs kv_ws(int B, int Hkv, int G, int D, int M, int P)
     const bool tiles = P > 0 && prows > kTileRows;
     const int RB = row_block(P > 0 && !tiles ? prows : rows);
     const size_t nprob = (size_t)B * Hkv * ((rows + RB - 1) / RB) + (P > 0 && !tiles ? (size_t)Hkv * ((prows + RB - 1) / RB) : 0);
-    const size_t slots = nprob + kKvMaxCtas, ns = tiles ? kv_prefix_splits(prows, Hkv, D, P) : 0;
+    const size_t slots = nprob + kKvMaxCtas, ns = tiles ? kv_tile_most(kv_row_tiles(prows, D) * Hkv) : 0;
     w.cum = 0;
     w.ml = align_up(((size_t)B + 1) * 4, 256);
     w.o = align_up(w.ml + slots * RB * 8, 256);
@@ -760,11 +762,15 @@ KvWs kv_ws(int B, int Hkv, int G, int D, int M, int P)
 
 }  // namespace
 
-int kv_prefix_splits(int, int, int, int) { return 1; }
-
-size_t kv_attn_workspace_bytes(int batch, int kv_heads, int group, int head_dim, int M, int max_prefix)
+// For every call of up to M rows, with a prefix or without.
+size_t kv_attn_workspace_bytes(int batch, int kv_heads, int group, int head_dim, int M, int max_prefix, bool exact)
 {
-    return kv_ws(batch, kv_heads, group, head_dim, M, max_prefix).total;
+    size_t most = 0;
+    for (int m = exact ? M : 1; m <= M; ++m) {
+        most = std::max(most, kv_ws(batch, kv_heads, group, head_dim, m, max_prefix).total);
+        if (!exact) most = std::max(most, kv_ws(batch, kv_heads, group, head_dim, m, 0).total);
+    }
+    return most;
 }
 
 int launch_kv_append(const moe_kv &c, const moe_rows &k_new, const moe_rows &v_new, int M, const int32_t *pos,
@@ -809,6 +815,17 @@ int launch_kv_append(const moe_kv &c, const moe_rows &k_new, const moe_rows &v_n
     return MOE_OK;
 }
 
+static int launch_merge(const KvCall &p, int ctas, cudaStream_t stream)
+{
+    auto *merge = p.D == 256 ? kv_merge_kernel<256> : p.D == 128 ? kv_merge_kernel<128> : kv_merge_kernel<64>;
+    const long long grid = (long long)p.B * p.M * p.Hq;
+    if (grid > INT_MAX) return MOE_ERR_UNSUPPORTED;
+    const cudaError_t e = launch_after(merge, dim3((unsigned)grid), 32 * kMergeWarps, 0, 0, stream, p, ctas);
+    if (e != cudaSuccess) { note_cuda_error((int)e); return MOE_ERR_CUDA; }
+    note_launch();
+    return MOE_OK;
+}
+
 // p: q, k, v, the prefix, lengths, shapes, scale and output; the rest is set here.
 int launch_kv_attn(KvCall &p, void *ws, cudaStream_t stream)
 {
@@ -825,7 +842,12 @@ int launch_kv_attn(KvCall &p, void *ws, cudaStream_t stream)
     p.part_o = reinterpret_cast<float *>(base + w.o);
     p.tile_ml = reinterpret_cast<float *>(base + w.tml);
     p.tile_o = reinterpret_cast<float *>(base + w.to);
-    p.nsplit = tiles ? kv_prefix_splits(prows, p.Hkv, p.D, p.P) : 0;
+    p.nsplit = 0;
+    if (tiles) {
+        p.nsplit = kv_tile_splits(kv_row_tiles(prows, p.D) * p.Hkv, (p.P + 127) / 128);
+        const int rc = launch_kv_tiles(p, true, stream);
+        if (rc) return rc;
+    }
     // the line's length has to fit an int
     const long long seen = std::min<long long>((long long)p.S + p.W + p.M, (long long)p.T);
     const long long most = (seen / kKvTile + 2) * p.B * p.Hkv * p.NRB + ((long long)p.P / kKvTile + 1) * p.Hkv * p.NRBP;
@@ -872,18 +894,38 @@ int launch_kv_attn(KvCall &p, void *ws, cudaStream_t stream)
 #undef KV_GO
     if (e != cudaSuccess) { note_cuda_error((int)e); return MOE_ERR_CUDA; }
     note_launch();
-    auto *merge = p.D == 256 ? kv_merge_kernel<256> : p.D == 128 ? kv_merge_kernel<128> : kv_merge_kernel<64>;
-    e = launch_after(merge, dim3(p.B * p.M * p.Hq), 32 * kMergeWarps, 0, 0, stream, p, grid);
-    if (e != cudaSuccess) { note_cuda_error((int)e); return MOE_ERR_CUDA; }
-    note_launch();
-    return MOE_OK;
+    return launch_merge(p, grid, stream);
 }
+
+// Prompts of few rows, whose tiles of 128 would be mostly empty, go through the split kernel.
+static bool few_rows(const moe_window &s) { return (long long)s.rows * (s.q_heads / s.kv_heads) <= kTileRows; }
+
+static long long window_ctas(int B, int Hkv, long long rows, int D) { return kv_row_tiles(rows, D) * Hkv * B; }
 
 size_t window_attn_workspace_bytes(const moe_window &s)
 {
-    return kv_ws(s.batch, s.kv_heads, s.q_heads / s.kv_heads, s.head_dim, s.rows, 0).total;
+    const int G = s.q_heads / s.kv_heads;
+    if (few_rows(s)) return kv_ws(s.batch, s.kv_heads, G, s.head_dim, s.rows, 0).total;
+    const long long rows = (long long)s.rows * G;
+    const size_t ns = kv_tile_most(window_ctas(s.batch, s.kv_heads, rows, s.head_dim));
+    return ns == 1 ? 0 : ns * s.batch * s.kv_heads * rows * (s.head_dim + 2) * 4;
 }
 
-int launch_window_attn(KvCall &p, void *ws, cudaStream_t stream) { return launch_kv_attn(p, ws, stream); }
+int launch_window_attn(KvCall &p, void *ws, cudaStream_t stream)
+{
+    const long long rows = (long long)p.M * p.G;
+    if (rows <= kTileRows) return launch_kv_attn(p, ws, stream);
+    const long long ctas = window_ctas(p.B, p.Hkv, rows, p.D);
+    const int most = kv_tile_most(ctas);
+    // tiles of a CTA's rows at most: as long as its window and first positions, or the prompt
+    const long long seen = std::min<long long>((long long)p.W + p.S + 256 / p.G, p.T);
+    p.nsplit = most == 1 ? 1 : kv_tile_splits(ctas, (seen + 127) / 128);
+    p.tile_o = static_cast<float *>(ws);
+    p.tile_ml = p.tile_o + (size_t)most * p.B * p.Hkv * rows * p.D;
+    const int rc = launch_kv_tiles(p, false, stream);
+    if (rc || p.nsplit == 1) return rc;
+    p.NRB = 0;
+    return launch_merge(p, 1, stream);
+}
 
 }  // namespace moe

@@ -36,11 +36,10 @@ struct KvCall {
     // tile kernel: the prefix's partial results, nsplit of them a row
     int nsplit;
     float *tile_o, *tile_ml;          // [split][Hkv][B M G][D], [...][2]
-    int *tile_flag;
     long long timeout_ns;
 };
 
-size_t kv_attn_workspace_bytes(int batch, int kv_heads, int group, int head_dim, int M, int max_prefix);
+size_t kv_attn_workspace_bytes(int batch, int kv_heads, int group, int head_dim, int M, int max_prefix, bool exact);
 int launch_kv_append(const moe_kv &c, const moe_rows &k_new, const moe_rows &v_new, int M, const int32_t *pos,
                      const int32_t *counts, int *err, cudaStream_t stream);
 int launch_kv_attn(KvCall &p, void *ws, cudaStream_t stream);
@@ -48,6 +47,8 @@ size_t window_attn_workspace_bytes(const moe_window &s);
 int launch_window_attn(KvCall &p, void *ws, cudaStream_t stream);
 // Tiles of 128 rows: prompts (outputs written), or the prefix (partial results).
 int launch_kv_tiles(const KvCall &p, bool prefix, cudaStream_t stream);
-int kv_prefix_splits(int rows, int kv_heads, int head_dim, int P);
+long long kv_row_tiles(long long rows, int D);
+int kv_tile_most(long long ctas);                     // parts of a row tile's positions at most
+int kv_tile_splits(long long ctas, long long tiles);  // parts taken
 
 }  // namespace moe
