@@ -42,12 +42,15 @@ namespace {
 constexpr int kRows = 128;            // rows of a tile (MMA M)
 constexpr int kKeys = 128;            // positions of a tile (MMA N of the scores)
 constexpr int kBox = 128 * 128;       // one TMA box: 128 positions of 64 elements
-constexpr int kTThreads = 320;
+constexpr int kTThreads = 384;        // softmax: warps 0-3, 4-7; loads 8; products 9; q 10, 11
+constexpr int kQThreads = 64;
 constexpr int kErrTimeout = 4;
 
 template <int D>
 struct TLay {
     static constexpr bool kPair = D <= 128;                   // two row tiles a CTA
+    static constexpr bool kOwnP = D == 64;                    // P beside S in tensor memory, not over it
+    static constexpr bool kAhead = !kPair || kOwnP;           // the next tile's scores come before this one's values
     static constexpr int NQ = kPair ? 2 : 1;
     static constexpr int RT = NQ * kRows;
     static constexpr int kUnit = D == 64 ? kBox : 2 * kBox;   // 128 positions x min(D, 128)
@@ -56,21 +59,30 @@ struct TLay {
     static constexpr int q = 0;
     static constexpr int ring = NQ * (D / 64) * kBox;
     static constexpr int bars = ring + NU * kUnit;
-    static constexpr int kBars = 2 * NU + 2 + 2 + 2 + 8 + 1;
+    static constexpr int kBars = 2 * NU + 2 * 5 + 8 + 3;
     static constexpr int misc = bars + kBars * 8;             // tensor-memory address, abort flag
-    static constexpr int refs = misc + 8;                     // [128] references
-    static constexpr int total = refs + 128 * 4;
+    static constexpr int refs = misc + 8;                     // [128] references, [2][128] sums (one row tile)
+    static constexpr int total = refs + 3 * 128 * 4;
 };
 static_assert(TLay<64>::total + 1024 <= kSmemMax && TLay<128>::total + 1024 <= kSmemMax && TLay<256>::total + 1024 <= kSmemMax,
               "shared memory");
-// tensor memory: S of the streams at columns 0 and 128, O from 256 on
+// tensor memory: S of the streams at columns 0 and 128, O from 256 on, P over S or from 384 on
 constexpr uint32_t kTmemCols = 512;
+// registers a thread: launched with 168; the softmax warps take what the others leave
+constexpr int kRegsSoft = 208, kRegsRest = 88;
+static_assert(256 * kRegsSoft + 128 * kRegsRest <= kTThreads * 168, "registers");
+
+struct Once {
+    std::once_flag flag[64];
+    int sms[64];
+};
 
 struct TileParams {
     CUtensorMap tk, tv;
     KvCall c;
     int ntile;     // row tiles (CTAs' worth) of a head
     int nsplit;
+    int items;     // row tiles times parts times heads (times sequences)
 };
 
 __device__ __forceinline__ uint32_t su32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -105,7 +117,7 @@ __device__ __forceinline__ bool bar_test(uint32_t b, unsigned parity)
 }
 // Bounded wait on an mbarrier phase; gives up when the CTA's abort flag is
 // set, or sets it (and the error word) when the time runs out.
-__device__ __noinline__ bool bar_wait_slow(uint32_t b, unsigned parity, volatile int *abort, long long timeout_ns, int *err)
+__device__ __forceinline__ bool bar_wait_slow(uint32_t b, unsigned parity, volatile int *abort, long long timeout_ns, int *err)
 {
     const unsigned long long t0 = gtime();
 #pragma unroll 1
@@ -124,19 +136,14 @@ __device__ __forceinline__ bool bar_wait(uint32_t b, unsigned parity, volatile i
     return bar_test(b, parity) || bar_wait_slow(b, parity, abort, c.timeout_ns, c.err);
 }
 
-// Shared-memory descriptors (tcgen05, version 1), 128-byte swizzle.  K-major:
-// rows of 64 elements, 8-row groups 1024 bytes apart; 16 elements on are 32 bytes.
-__device__ __forceinline__ uint64_t desc_k(uint32_t addr)
-{
-    return (uint64_t)((addr & 0x3FFFFu) >> 4) | (1ull << 16) | ((uint64_t)(1024u >> 4) << 32) | (1ull << 46) | (2ull << 61);
-}
+// Shared-memory descriptors (tcgen05, version 1), 128-byte swizzle: the low word has the address
+// (in 16 bytes), the high word is the same for all.  K-major: rows of 64 elements, 8-row
+// groups 1024 bytes apart; 16 elements on are 32 bytes.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_k(uint32_t addr) { return ((addr & 0x3FFFFu) >> 4) | (1u << 16); }
 // MN-major: 64 elements of N in a row of 128 bytes, the next 64 a box further; rows are
 // K, 8-row groups 1024 bytes apart; 16 of K on are 2048 bytes.
-__device__ __forceinline__ uint64_t desc_mn(uint32_t addr)
-{
-    return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(kBox >> 4) << 16) | ((uint64_t)(1024u >> 4) << 32) | (1ull << 46) |
-           (2ull << 61);
-}
+__device__ __forceinline__ uint32_t desc_mn(uint32_t addr) { return ((addr & 0x3FFFFu) >> 4) | ((uint32_t)(kBox >> 4) << 16); }
 // kind::f16, fp32 accumulator, M = 128; b_mn: B is MN-major.
 template <bool F16>
 __device__ __forceinline__ constexpr uint32_t idesc(int n, bool b_mn)
@@ -144,16 +151,25 @@ __device__ __forceinline__ constexpr uint32_t idesc(int n, bool b_mn)
     return (1u << 4) | (F16 ? 0u : (1u << 7) | (1u << 10)) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) |
            ((uint32_t)(128 >> 4) << 24);
 }
-__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc)
+// One thread of the warp, the same each time.
+__device__ __forceinline__ bool elect_one()
 {
-    asm volatile("{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
-                 "l"(a), "l"(b), "r"(id), "r"(acc)
+    uint32_t r;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xFFFFFFFF; selp.u32 %0, 1, 0, p; }" : "=r"(r)::"memory");
+    return r != 0;
+}
+__device__ __forceinline__ void umma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc)
+{
+    asm volatile("{ .reg .pred p; .reg .b64 x, y; setp.ne.b32 p, %4, 0; mov.b64 x, {%1, %5}; mov.b64 y, {%2, %5}; "
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p; }" ::"r"(d),
+                 "r"(a), "r"(b), "r"(id), "r"(acc), "n"(kDescHi)
                  : "memory");
 }
-__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc)
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc)
 {
-    asm volatile("{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d),
-                 "r"(a), "l"(b), "r"(id), "r"(acc)
+    asm volatile("{ .reg .pred p; .reg .b64 y; setp.ne.b32 p, %4, 0; mov.b64 y, {%2, %5}; "
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p; }" ::"r"(d),
+                 "r"(a), "r"(b), "r"(id), "r"(acc), "n"(kDescHi)
                  : "memory");
 }
 __device__ __forceinline__ void umma_commit(uint32_t bar)
@@ -210,6 +226,31 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi)
     else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
+__device__ __forceinline__ uint64_t two(float a, float b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void split2(uint64_t v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 __device__ __forceinline__ float ex2(float x)
 {
     float y;
@@ -225,77 +266,73 @@ __device__ __forceinline__ int rows_of(const KvCall &p, int b, int &p0, bool &ba
 }
 
 // The order in which a tile's keys (or values) are loaded: as the steps first use them.
-template <bool PAIR>
-__device__ __forceinline__ int k_order(int t) { return PAIR ? 2 * t : t == 0 ? 0 : 2 * t - 1; }
-template <bool PAIR>
-__device__ __forceinline__ int v_order(int t, int nt) { return PAIR ? 2 * t + 1 : t == nt - 1 ? 2 * nt - 1 : 2 * t + 2; }
+template <bool AHEAD>
+__device__ __forceinline__ int k_order(int t) { return !AHEAD ? 2 * t : t == 0 ? 0 : 2 * t - 1; }
+template <bool AHEAD>
+__device__ __forceinline__ int v_order(int t, int nt) { return !AHEAD ? 2 * t + 1 : t == nt - 1 ? 2 * nt - 1 : 2 * t + 2; }
+
+// A CTA's worth of work: row tile(s) r0 .. of one head against nt tiles of positions:
+// tiles i0 .. i0 + nt - 1 of the list that has the first nsink tiles and then those from kt_lo on.
+struct Item {
+    int z, g, b, r0;
+    int p0, cnt, nvalid;
+    int kt_lo, nsink, i0, nt;
+    __device__ __forceinline__ int first_key(int t) const { return kKeys * (i0 + t < nsink ? i0 + t : kt_lo + i0 + t - nsink); }
+};
+template <int RT, bool PREFIX>
+__device__ __forceinline__ Item item_of(const TileParams &tp, int x)
+{
+    const KvCall &p = tp.c;
+    Item it;
+    it.z = x % tp.nsplit;
+    x /= tp.nsplit;
+    it.g = x % p.Hkv;
+    x /= p.Hkv;
+    const int seqs = PREFIX ? 1 : p.B;
+    it.b = x % seqs;
+    const int tile = tp.ntile - 1 - x / seqs;   // later row tiles, which see more, first
+    it.r0 = tile * RT;
+    it.p0 = it.kt_lo = it.nsink = it.nt = 0;
+    it.cnt = p.M;
+    it.nvalid = INT_MAX;
+    if (PREFIX) {
+        it.nt = (p.P + kKeys - 1) / kKeys;
+    } else {
+        bool bad;
+        it.cnt = rows_of(p, it.b, it.p0, bad);
+        if (bad && threadIdx.x == 0) atomicOr(p.err, kKv8ErrRange);
+        const int first = it.r0 / p.G, last = min((it.r0 + RT - 1) / p.G, it.cnt - 1);
+        it.nvalid = it.p0 + it.cnt;
+        if (first < it.cnt) {
+            it.kt_lo = max(0, it.p0 + first - p.W + 1) / kKeys;
+            it.nsink = min((p.S + kKeys - 1) / kKeys, it.kt_lo);
+            it.nt = it.nsink + (it.p0 + last) / kKeys - it.kt_lo + 1;
+        }
+    }
+    const int each = (it.nt + tp.nsplit - 1) / tp.nsplit;
+    it.i0 = min(it.nt, it.z * each);
+    it.nt = min(it.nt - it.i0, each);
+    return it;
+}
 
 template <bool F16, int D, bool PREFIX>
 __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_constant__ TileParams tp)
 {
     using L = TLay<D>;
-    constexpr bool PAIR = L::kPair;
-    constexpr int NU = L::NU, UPT = L::UPT;
+    constexpr bool PAIR = L::kPair, OWNP = L::kOwnP, AHEAD = L::kAhead;
+    constexpr int NU = L::NU, UPT = L::UPT, RT = L::RT;
     const KvCall &p = tp.c;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;   // warp: uniform, as the products' operands have to be
+    // barriers, each two one for a stream: S is there; it has been read; P is
+    // there; P V is done; O has been read
     uint64_t *full = reinterpret_cast<uint64_t *>(sm + L::bars), *empty = full + NU;
-    uint64_t *s_full = empty + NU, *p_full = s_full + 2, *o_done = p_full + 2, *ref_rdy = o_done + 2, *all_done = ref_rdy + 8;
+    uint64_t *s_full = empty + NU, *s_read = s_full + 2, *p_full = s_read + 2, *o_done = p_full + 2,
+             *o_free = o_done + 2, *ref_rdy = o_free + 2, *q_full = ref_rdy + 8, *q_free = q_full + 1, *all_done = q_free + 1;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + L::misc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    float *refs = reinterpret_cast<float *>(sm + L::refs);
-
-    // which rows and positions: later row tiles, which see more, first
-    int x = blockIdx.x;
-    const int tile = tp.ntile - 1 - x % tp.ntile;
-    x /= tp.ntile;
-    const int z = x % tp.nsplit;
-    x /= tp.nsplit;
-    const int g = x % p.Hkv, b = x / p.Hkv;
-    const int r0 = tile * L::RT;
-    after_previous();
-    // tiles of positions i0 .. i0 + nt - 1 of the list: the first nsink, then from kt_lo on
-    int p0 = 0, cnt = p.M, kt_lo = 0, nsink = 0, nt = 0, i0 = 0, nvalid = INT_MAX;
-    if (PREFIX) {
-        nt = (p.P + kKeys - 1) / kKeys;
-    } else {
-        bool bad;
-        cnt = rows_of(p, b, p0, bad);
-        if (bad && tile == 0 && g == 0 && z == 0 && tid == 0) atomicOr(p.err, kKv8ErrRange);
-        const int first = r0 / p.G, last = min((r0 + L::RT - 1) / p.G, cnt - 1);
-        nvalid = p0 + cnt;
-        if (first < cnt) {
-            kt_lo = max(0, p0 + first - p.W + 1) / kKeys;
-            nsink = min((p.S + kKeys - 1) / kKeys, kt_lo);
-            nt = nsink + (p0 + last) / kKeys - kt_lo + 1;
-        }
-    }
-    {
-        const int each = (nt + tp.nsplit - 1) / tp.nsplit;
-        i0 = min(nt, z * each);
-        nt = min(nt - i0, each);
-    }
-    auto first_key = [&](int t) { return kKeys * (i0 + t < nsink ? i0 + t : kt_lo + i0 + t - nsink); };
-    const long long rows = PREFIX ? (long long)p.B * p.M * p.G : (long long)p.M * p.G;   // of a head (and sequence)
-    const bool parts = PREFIX || tp.nsplit > 1;
-    const size_t part0 = ((size_t)z * p.Hkv + g) * ((size_t)p.B * p.M * p.G) + (PREFIX ? 0 : (size_t)b * p.M * p.G);
-    uint16_t *const out = static_cast<uint16_t *>(p.o);
-    if (nt == 0) {
-        // nothing to see: zeros, or an empty part
-        for (int i = tid; i < L::RT; i += kTThreads)
-            if (parts && r0 + i < rows) *reinterpret_cast<float2 *>(p.tile_ml + (part0 + r0 + i) * 2) = make_float2(-INFINITY, 0.f);
-        if (!parts)
-            for (int i = tid; i < L::RT * (D / 8); i += kTThreads) {
-                const int r = r0 + i / (D / 8), c = i % (D / 8);
-                if (r < rows) {
-                    const int m = r / p.G, h = r - m * p.G;
-                    *reinterpret_cast<uint4 *>(out + (((size_t)b * p.M + m) * p.Hq + g * p.G + h) * D + 8 * c) = make_uint4(0u, 0u, 0u, 0u);
-                }
-            }
-        return;
-    }
-    const int nsteps = PAIR ? 2 * nt : nt;
+    float *refs = reinterpret_cast<float *>(sm + L::refs), *sums = refs + 128;
 
     if (tid == 0) {
         for (int s = 0; s < NU; ++s) {
@@ -304,10 +341,14 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
         }
         for (int s = 0; s < 2; ++s) {
             bar_init(su32(&s_full[s]), 1);
+            bar_init(su32(&s_read[s]), 4);
             bar_init(su32(&p_full[s]), 4);
             bar_init(su32(&o_done[s]), 1);
+            bar_init(su32(&o_free[s]), PAIR ? 4 : 8);
         }
         for (int s = 0; s < 8; ++s) bar_init(su32(&ref_rdy[s]), 1);
+        bar_init(su32(q_full), kQThreads);
+        bar_init(su32(q_free), 1);
         bar_init(su32(all_done), 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -317,204 +358,284 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
+    after_previous();
     fence_before();
     __syncthreads();
     fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
+    const long long rows = (long long)p.M * p.G * (PREFIX ? p.B : 1);   // of a head (and sequence)
+    const bool parts = PREFIX || tp.nsplit > 1;
 
-    float l = 0.f, ref = -INFINITY;    // of the thread's row, as its stream knows them
-    if (warp == 8) {
-        // ---------------------------------------------------------------- loads
-        if (lane == 0) {
-            bool go = true;
-            int n = 0;   // units issued
-            auto load = [&](const CUtensorMap *map, int t) {
-                const int key = first_key(t);
-                for (int u = 0; u < UPT && go; ++u) {
-                    const int s = n % NU, turn = n / NU;
-                    if (turn > 0 && !bar_wait(su32(&empty[s]), (unsigned)(turn - 1) & 1u, abort_flag, p)) {
-                        go = false;
-                        return;
-                    }
-                    const uint32_t dst = su32(sm + L::ring + s * L::kUnit), fb = su32(&full[s]);
-                    bar_expect(fb, L::kUnit);
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+        if (warp == 8) {
+            // ------------------------------------------------------------- loads
+            if (lane == 0) {
+                bool go = true;
+                int slot = 0, turn = 0, n = 0;   // of the next unit; units issued
+                for (int x = blockIdx.x; x < tp.items && go; x += gridDim.x) {
+                    const Item it = item_of<RT, PREFIX>(tp, x);
+                    auto load = [&](const CUtensorMap *map, int t) {
+                        const int key = it.first_key(t);
+                        for (int u = 0; u < UPT && go; ++u) {
+                            if (turn > 0 && !bar_wait(su32(&empty[slot]), (unsigned)(turn - 1) & 1u, abort_flag, p)) {
+                                go = false;
+                                return;
+                            }
+                            const uint32_t dst = su32(sm + L::ring + slot * L::kUnit), fb = su32(&full[slot]);
+                            bar_expect(fb, L::kUnit);
 #pragma unroll
-                    for (int h = 0; h < L::kUnit / kBox; ++h) tma_load4(dst + h * kBox, map, 128 * u + 64 * h, key, g, PREFIX ? 0 : b, fb);
-                    ++n;
+                            for (int h = 0; h < L::kUnit / kBox; ++h)
+                                tma_load4(dst + h * kBox, map, 128 * u + 64 * h, key, it.g, PREFIX ? 0 : it.b, fb);
+                            ++n;
+                            if (++slot == NU) {
+                                slot = 0;
+                                ++turn;
+                            }
+                        }
+                    };
+                    if (AHEAD && it.nt > 0) load(&tp.tk, 0);
+                    for (int t = 0; t < it.nt && go; ++t) {
+                        const int kt = AHEAD ? t + 1 : t;
+                        if (kt < it.nt) load(&tp.tk, kt);
+                        if (go) load(&tp.tv, t);
+                    }
                 }
-            };
-            if (PAIR) {
-                for (int t = 0; t < nt && go; ++t) {
-                    load(&tp.tk, t);
-                    if (go) load(&tp.tv, t);
-                }
-            } else {
-                load(&tp.tk, 0);
-                if (go && nt > 1) load(&tp.tk, 1);
-                for (int t = 0; t < nt && go; ++t) {
-                    load(&tp.tv, t);
-                    if (go && t + 2 < nt) load(&tp.tk, t + 2);
+                // every copy issued has landed before the CTA ends
+                const unsigned long long t0 = gtime();
+                for (int s = 0; s < NU && s < n; ++s) {
+                    const unsigned last = (unsigned)((n - 1 - s) / NU) & 1u;
+                    while (!bar_test(su32(&full[s]), last) && (long long)(gtime() - t0) <= p.timeout_ns) {}
                 }
             }
-            // every copy issued has landed before the CTA ends
-            const unsigned long long t0 = gtime();
-            for (int s = 0; s < NU && s < n; ++s) {
-                const unsigned last = (unsigned)((n - 1 - s) / NU) & 1u;
-                while (!bar_test(su32(&full[s]), last) && (long long)(gtime() - t0) <= p.timeout_ns) {}
-            }
-        }
-        __syncwarp();
-    } else {
-        // q, packed: rows that are not there are zeros
-        if (warp != 9) {
+        } else if (warp >= 10) {
+            // ---------------------------------------------------- q, packed into rows
             constexpr int CH = D / 8;
-            for (int i = tid; i < L::RT * CH; i += 256) {
-                const int rr = i / CH, c = i % CH, r = r0 + rr;
-                bool ok = r < rows;
-                int bb = b, m = r / p.G;
-                const int h = r - m * p.G;
+            const int t = tid - 320;
+            int qn = 0;
+            bool go = true;
+            for (int x = blockIdx.x; x < tp.items; x += gridDim.x) {
+                const Item it = item_of<RT, PREFIX>(tp, x);
+                if (it.nt == 0) continue;
+                if (qn > 0) go = __all_sync(0xFFFFFFFFu, bar_wait(su32(q_free), (unsigned)(qn - 1) & 1u, abort_flag, p));
+                if (!go) break;
+                // (rows of idle sequences and padding are read like the others; nothing of them is used)
+                constexpr int STEP = kQThreads / CH;   // rows a pass
+                const int c = t % CH, rr0 = t / CH;
+                int r = it.r0 + rr0, m = r / p.G, h = r - m * p.G, bb = it.b;
                 if (PREFIX) {
                     bb = m / p.M;
                     m -= bb * p.M;
-                    int q0;
-                    bool bad;
-                    ok = ok && m < rows_of(p, bb, q0, bad);
-                } else {
-                    ok = ok && m < cnt;
                 }
-                uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                if (ok) v = __ldg(reinterpret_cast<const uint4 *>(p.q + bb * p.qb + m * p.qm + (long long)(g * p.G + h) * p.qh) + c);
-                *reinterpret_cast<uint4 *>(sm + L::q + ((rr >> 7) * (D / 64) + (c >> 3)) * kBox + (rr & 127) * 128 +
-                                           (((c & 7) ^ (rr & 7)) << 4)) = v;
-            }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        }
-        asm volatile("bar.sync 1, 288;" ::: "memory");   // q is there: softmax warps and the products' warp
-
-        if (warp == 9) {
-            // ---------------------------------------------------------- products
-            bool go = true;
-            const uint32_t id_s = idesc<F16>(kKeys, false), id_o = idesc<F16>(D < 128 ? D : 128, true);
-            auto wait = [&](uint64_t *bar, int parity) {
-                go = __all_sync(0xFFFFFFFFu, go && bar_wait(su32(bar), (unsigned)parity & 1u, abort_flag, p));
-                fence_after();
-            };
-            auto scores = [&](int i) {
-                const int xs = i & 1, t = PAIR ? i >> 1 : i, n0 = UPT * k_order<PAIR>(t);
-#pragma unroll
-                for (int u = 0; u < UPT; ++u) {
-                    const int s = (n0 + u) % NU;
-                    if (go) wait(&full[s], (n0 + u) / NU);
-                    if (!go) return;
-                    if (lane == 0) {
-                        const uint32_t a0 = su32(sm + L::q + ((PAIR ? xs : 0) * (D / 64) + 2 * u) * kBox);
-                        const uint32_t b0 = su32(sm + L::ring + s * L::kUnit);
-#pragma unroll
-                        for (int k = 0; k < (D < 128 ? D : 128) / 16; ++k) {
-                            const uint32_t off = (uint32_t)((k >> 2) * kBox + (k & 3) * 32);
-                            umma_ss(tmem + 128u * xs, desc_k(a0 + off), desc_k(b0 + off), id_s, (u | k) != 0 ? 1u : 0u);
+                const uint16_t *src = p.q + (long long)bb * p.qb + (long long)m * p.qm + (long long)(it.g * p.G + h) * p.qh + 8 * c;
+#pragma unroll 4
+                for (int rr = rr0; rr < RT; rr += STEP) {
+                    const bool ok = r < rows;   // rows that are not there are zeros
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                                     su32(sm + L::q) + ((rr >> 7) * (D / 64) + (c >> 3)) * kBox + (rr & 127) * 128 + (((c & 7) ^ (rr & 7)) << 4)),
+                                 "l"(ok ? src : p.q), "r"(ok ? 16 : 0)
+                                 : "memory");
+                    r += STEP;
+                    h += STEP;
+                    src += STEP * p.qh;
+                    while (h >= p.G) {   // the next query row
+                        h -= p.G;
+                        src += p.qm - p.G * p.qh;
+                        if (PREFIX && ++m == p.M) {
+                            m = 0;
+                            src += p.qb - p.M * p.qm;
                         }
-                        if (!PAIR || xs == 1) umma_commit(su32(&empty[s]));
                     }
                 }
-                if (lane == 0) umma_commit(su32(&s_full[xs]));
-                __syncwarp();
-            };
-            auto values = [&](int i) {
-                const int xs = i & 1, t = PAIR ? i >> 1 : i, n0 = UPT * v_order<PAIR>(t, nt);
-                const int gone = nvalid - first_key(t);   // positions from here on hold anything
-                if (go) wait(&p_full[xs], i >> 1);
-#pragma unroll
-                for (int u = 0; u < UPT; ++u) {
-                    const int s = (n0 + u) % NU;
-                    if (go) wait(&full[s], (n0 + u) / NU);
-                    if (!go) return;
-                    uint8_t *unit = sm + L::ring + s * L::kUnit;
-                    if (!PREFIX && gone < kKeys && (!PAIR || xs == 0)) {
-                        for (int j = lane; j < (kKeys - gone) * 8; j += 32)
-#pragma unroll
-                            for (int h = 0; h < L::kUnit / kBox; ++h)
-                                *reinterpret_cast<uint4 *>(unit + h * kBox + gone * 128 + j * 16) = make_uint4(0u, 0u, 0u, 0u);
-                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                        __syncwarp();
-                    }
-                    if (lane == 0) {
-                        const uint32_t o = tmem + 256u + (PAIR ? (uint32_t)(D * xs) : 128u * u);
-#pragma unroll
-                        for (int k = 0; k < kKeys / 16; ++k)
-                            umma_ts(o, tmem + 128u * xs + 8u * k, desc_mn(su32(unit) + 2048u * k), id_o, (t | k) != 0 ? 1u : 0u);
-                        if (!PAIR || xs == 1) umma_commit(su32(&empty[s]));
-                    }
-                }
-                if (lane == 0) umma_commit(su32(&o_done[xs]));
-                __syncwarp();
-            };
-            scores(0);
-            if (nsteps > 1) scores(1);
-#pragma unroll 1
-            for (int i = 0; i < nsteps && go; ++i) {
-                values(i);
-                if (go && i + 2 < nsteps) scores(i + 2);
+                asm volatile("cp.async.wait_all;" ::: "memory");
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                bar_arrive(su32(q_full));
+                ++qn;
             }
-            // every product issued has finished before O is read or tensor memory freed
-            if (lane == 0) {
+        } else {
+            // ---------------------------------------------------------- products
+            // One thread, and as few instructions between the products as can be: they are issued in order,
+            // and a step's 16 of 128 x 128 x 16 take the tensor core about 1000 cycles.
+            if (elect_one()) {
+                bool go = true;
+                constexpr uint32_t id_s = idesc<F16>(kKeys, false), id_o = idesc<F16>(D < 128 ? D : 128, true);
+                const uint32_t ring = su32(sm + L::ring), qd = desc_k(su32(sm + L::q));
+                auto wait = [&](uint64_t *bar, int parity) { go = go && bar_wait(su32(bar), (unsigned)parity & 1u, abort_flag, p); };
+                struct Place {   // of a unit in the ring, with its phase
+                    int slot, phase;
+                    __device__ __forceinline__ void move(int by)
+                    {
+                        slot += by;
+                        if (slot >= NU) {
+                            slot -= NU;
+                            phase ^= 1;
+                        }
+                    }
+                };
+                Place base = {0, 0};
+                int qn = 0, done[2] = {0, 0};   // items and steps of the streams before this item
+                for (int x = blockIdx.x; x < tp.items && go; x += gridDim.x) {
+                    const int nt = item_of<RT, PREFIX>(tp, x).nt;
+                    if (nt == 0) continue;
+                    const int nsteps = PAIR ? 2 * nt : nt;
+                    Place kp = base, vp = base;         // of the next tile of keys, of values
+                    vp.move(AHEAD && nt > 1 ? 2 * UPT : UPT);
+                    auto scores = [&](int i, int xs) {
+                        const int t = PAIR ? i >> 1 : i;
+                        if (OWNP && done[xs] + (i >> 1) > 0) wait(&s_read[xs], done[xs] + (i >> 1) - 1);
+                        Place at = kp;
+#pragma unroll
+                        for (int u = 0; u < UPT; ++u) {
+                            if (!PAIR || xs == 0) wait(&full[at.slot], at.phase);
+                            if (!go) return;
+                            fence_after();
+                            const uint32_t a0 = qd + (uint32_t)((((PAIR ? xs : 0) * (D / 64) + 2 * u) * kBox) >> 4);
+                            const uint32_t b0 = desc_k(ring + at.slot * L::kUnit);
+#pragma unroll
+                            for (int k = 0; k < (D < 128 ? D : 128) / 16; ++k) {
+                                const uint32_t off = (uint32_t)((k >> 2) * kBox + (k & 3) * 32) >> 4;
+                                umma_ss(tmem + 128u * xs, a0 + off, b0 + off, id_s, (u | k) != 0 ? 1u : 0u);
+                            }
+                            if (!PAIR || xs == 1) umma_commit(su32(&empty[at.slot]));
+                            at.move(1);
+                        }
+                        umma_commit(su32(&s_full[xs]));
+                        if (i == nsteps - 1) umma_commit(su32(q_free));
+                        if (!PAIR || xs == 1) kp.move(AHEAD && t == 0 ? UPT : 2 * UPT);
+                    };
+                    auto values = [&](int i, int xs) {
+                        const int t = PAIR ? i >> 1 : i, step = done[xs] + (i >> 1);
+                        if (t == 0 && qn > 0) wait(&o_free[PAIR ? xs : 0], qn - 1);
+                        if (!PAIR || xs == 0) {
+                            Place at = vp;
+#pragma unroll
+                            for (int u = 0; u < UPT; ++u) {
+                                wait(&full[at.slot], at.phase);
+                                at.move(1);
+                            }
+                        }
+                        wait(&p_full[xs], step);
+                        if (!go) return;
+                        fence_after();
+                        Place at = vp;
+#pragma unroll
+                        for (int u = 0; u < UPT; ++u) {
+                            const uint32_t o = tmem + 256u + (PAIR ? (uint32_t)(D * xs) : 128u * u);
+                            const uint32_t a0 = tmem + (OWNP ? 384u + 64u * xs : 128u * xs), b0 = desc_mn(ring + at.slot * L::kUnit);
+#pragma unroll
+                            for (int k = 0; k < kKeys / 16; ++k)
+                                umma_ts(o, a0 + 8u * k, b0 + 128u * k, id_o, (t | k) != 0 ? 1u : 0u);
+                            if (!PAIR || xs == 1) umma_commit(su32(&empty[at.slot]));
+                            at.move(1);
+                        }
+                        umma_commit(su32(&o_done[xs]));
+                        if (!PAIR || xs == 1) vp.move(AHEAD && t + 2 >= nt ? UPT : 2 * UPT);
+                    };
+                    auto step = [&](int i, int xs) {
+                        if (OWNP && i + 2 < nsteps) scores(i + 2, xs);
+                        if (go) values(i, xs);
+                        if (!OWNP && go && i + 2 < nsteps) scores(i + 2, xs);
+                    };
+                    wait(q_full, qn);
+                    if (go) scores(0, 0);
+                    if (go && nsteps > 1) scores(1, 1);
+#pragma unroll 1
+                    for (int i = 0; i < nsteps && go; i += 2) {
+                        step(i, 0);
+                        if (go && i + 1 < nsteps) step(i + 1, 1);
+                    }
+                    for (int n = 0; n < (2 * nt) % NU; ++n) base.move(UPT);
+                    base.phase ^= (2 * nt / NU * UPT) & 1;
+                    done[0] += PAIR ? nt : (nt + 1) / 2;
+                    done[1] += PAIR ? nt : nt / 2;
+                    ++qn;
+                }
+                // every product issued has finished before tensor memory is freed
                 umma_commit(su32(all_done));
                 const unsigned long long t0 = gtime();
                 while (!bar_test(su32(all_done), 0u) && (long long)(gtime() - t0) <= p.timeout_ns) {}
             }
-            __syncwarp();
-        } else {
-            // ----------------------------------------------------------- softmax
-            const int xs = warp >> 2, w = warp & 3, r = r0 + (PAIR ? 128 * xs : 0) + (tid & 127);
-            const uint32_t lanes = tmem + ((uint32_t)(32 * w) << 16), sc = lanes + 128u * xs;
-            const uint32_t oc = lanes + 256u + (PAIR ? (uint32_t)(D * xs) : 0u);
-            // positions t the row sees: t <= high and (t > low or t < S)
-            int high, low, all_high, all_low;   // of the row; that all the warp group's rows have at least (at most)
+        }
+        __syncwarp();
+    } else {
+        // --------------------------------------------------------------- softmax
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
+        const int xs = warp >> 2, w = warp & 3, row = tid & 127;
+        const uint32_t lanes = tmem + ((uint32_t)(32 * w) << 16), sc = lanes + 128u * xs, pc = OWNP ? lanes + 384u + 64u * xs : sc;
+        const uint32_t oc = lanes + 256u + (PAIR ? (uint32_t)(D * xs) : 0u);
+        const float c = p.c;
+        const uint64_t c2 = two(c, c);
+        int done[2] = {0, 0}, units = 0;   // steps of the streams, units of the ring before this item
+        bool go = true;
+        auto wait = [&](uint64_t *bar, int parity) {
+            go = __all_sync(0xFFFFFFFFu, go && bar_wait(su32(bar), (unsigned)parity & 1u, abort_flag, p));
+        };
+        // (after a wait has given up the streams of one row tile still meet at each item's barriers)
+#pragma unroll 1
+        for (int x = blockIdx.x; x < tp.items; x += gridDim.x) {
+            const Item it = item_of<RT, PREFIX>(tp, x);
+            const int nt = it.nt, nsteps = PAIR ? 2 * nt : nt, r = it.r0 + (PAIR ? 128 * xs : 0) + row;
+            const size_t part0 = ((size_t)it.z * p.Hkv + it.g) * ((size_t)p.B * p.M * p.G) + (PREFIX ? 0 : (size_t)it.b * p.M * p.G);
+            // positions t the row sees: t <= high and (t > low or t < S); all_*: the strictest of the tile's rows
+            int high, low, all_high, all_low;
             if (PREFIX) {
                 high = all_high = p.P - 1;
                 low = all_low = -1;
             } else {
-                const int ra = r0 + (PAIR ? 128 * xs : 0);
-                high = p0 + r / p.G;
+                const int ra = it.r0 + (PAIR ? 128 * xs : 0);
+                high = it.p0 + r / p.G;
                 low = high - p.W;
-                all_high = p0 + ra / p.G;
-                all_low = p0 + (ra + kRows - 1) / p.G - p.W;
+                all_high = it.p0 + ra / p.G;
+                all_low = it.p0 + (ra + kRows - 1) / p.G - p.W;
             }
-            const float c = p.c;
-            bool ok = true;
+            float l = 0.f, ref = -INFINITY;    // of the row, as the stream knows them
 #pragma unroll 1
-            for (int i = xs; i < nsteps; i += 2) {
-                const int t = PAIR ? i >> 1 : i, key = first_key(t);
-                ok = bar_wait(su32(&s_full[xs]), (unsigned)(i >> 1) & 1u, abort_flag, p);
-                if (!__all_sync(0xFFFFFFFFu, ok)) break;
+            for (int i = xs; i < nsteps && go; i += 2) {
+                const int t = PAIR ? i >> 1 : i, key = it.first_key(t), step = done[xs] + (i >> 1);
+                wait(&s_full[xs], step);
+                if (!go) break;
                 fence_after();
                 uint32_t s[kKeys];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) tmem_ld32(sc + 32u * k, s + 32 * k);
                 tmem_wait_ld();
+                if (OWNP) {
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(su32(&s_read[xs]));
+                }
                 // a tile that some row does not see all of
                 if (key + kKeys - 1 > all_high || (key <= all_low && key + kKeys > p.S)) {
-                    const int a = high - key, lo = low - key, f = p.S - key;
+                    auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; };
 #pragma unroll
-                    for (int k = 0; k < kKeys; ++k)
-                        if (!(k <= a && (k > lo || k < f))) s[k] = 0xFF800000u;
+                    for (int k = 0; k < 4; ++k) {
+                        const int at = key + 32 * k;
+                        const uint32_t sees = below(high + 1 - at) & (~below(low + 1 - at) | below(p.S - at));
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (!(sees >> j & 1u)) s[32 * k + j] = 0xFF800000u;
+                    }
                 }
-                float mx[4] = {__uint_as_float(s[0]), __uint_as_float(s[1]), __uint_as_float(s[2]), __uint_as_float(s[3])};
+                float mx[4];
 #pragma unroll
-                for (int k = 4; k < kKeys; k += 4)
+                for (int j = 0; j < 4; ++j) mx[j] = __uint_as_float(s[j]);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) mx[j] = fmaxf(mx[j], __uint_as_float(s[k + j]));
+                for (int k = 4; k + 8 <= kKeys; k += 8)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) mx[j] = max3(mx[j], __uint_as_float(s[k + j]), __uint_as_float(s[k + 4 + j]));
+#pragma unroll
+                for (int j = 0; j < 4; ++j) mx[j] = fmaxf(mx[j], __uint_as_float(s[kKeys - 4 + j]));
                 const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
                 float was = ref;
                 if (!PAIR && i > 0) {   // the reference, from the stream that has the tile before
-                    ok = bar_wait(su32(&ref_rdy[4 * (xs ^ 1) + w]), (unsigned)((i - 1) >> 1) & 1u, abort_flag, p);
-                    if (!__all_sync(0xFFFFFFFFu, ok)) break;
-                    was = refs[tid & 127];
+                    wait(&ref_rdy[4 * (xs ^ 1) + w], done[xs ^ 1] + ((i - 1) >> 1));
+                    if (!go) break;
+                    was = refs[row];
                 }
                 const bool raise = top > was + 8.f;
                 const float now = raise ? top : was;
                 if (!PAIR) {
-                    refs[tid & 127] = now;
+                    refs[row] = now;
                     __syncwarp();
                     if (lane == 0) bar_arrive(su32(&ref_rdy[4 * xs + w]));
                 }
@@ -522,9 +643,9 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                 ref = now;
                 if (__any_sync(0xFFFFFFFFu, raise) && t > 0) {
                     // O, which has the tiles up to the one before, in the new reference's units
-                    const int before = PAIR ? i - 2 : i - 1;
-                    ok = bar_wait(su32(&o_done[PAIR ? xs : xs ^ 1]), (unsigned)(before >> 1) & 1u, abort_flag, p);
-                    if (!__all_sync(0xFFFFFFFFu, ok)) break;
+                    const int y = PAIR ? xs : xs ^ 1;
+                    wait(&o_done[y], done[y] + ((PAIR ? i - 2 : i - 1) >> 1));
+                    if (!go) break;
                     fence_after();
                     const float f = raise ? ex2(was - now) : 1.f;
 #pragma unroll 1
@@ -537,86 +658,118 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                         tmem_st32(oc + k, o);
                     }
                 }
-                const float sub = ref == -INFINITY ? 0.f : ref;
-                float add[4] = {0.f, 0.f, 0.f, 0.f};
+                if (!PREFIX && it.nvalid - key < kKeys && (!PAIR || xs == 0)) {
+                    // values behind the sequence's last position may be anything: zeros
+                    const int gone = it.nvalid - key;
+                    const int n0 = units + UPT * v_order<AHEAD>(t, nt);
+#pragma unroll 1
+                    for (int u = n0; u < n0 + UPT; ++u) {
+                        wait(&full[u % NU], u / NU);
+                        if (!go) break;
+                        uint8_t *unit = sm + L::ring + (u % NU) * L::kUnit;
+                        for (int j = row; j < (kKeys - gone) * 8; j += 128)
+#pragma unroll
+                            for (int h = 0; h < L::kUnit / kBox; ++h)
+                                *reinterpret_cast<uint4 *>(unit + h * kBox + gone * 128 + j * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    if (!go) break;
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                }
+                if (OWNP && t > 0) {   // P of the step before has been read
+                    wait(&o_done[xs], step - 1);
+                    if (!go) break;
+                }
+                const float sub = ref == -INFINITY ? 0.f : -ref;
+                const uint64_t sub2 = two(sub, sub);
+                uint64_t add[2] = {0ull, 0ull};
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     uint32_t pk[16];
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
-                        const float e0 = ex2(fmaf(__uint_as_float(s[32 * k + 2 * j]), c, -sub));
-                        const float e1 = ex2(fmaf(__uint_as_float(s[32 * k + 2 * j + 1]), c, -sub));
-                        add[(2 * j) & 3] += e0;
-                        add[(2 * j + 1) & 3] += e1;
+                        float e0, e1;
+                        split2(fma2(two(__uint_as_float(s[32 * k + 2 * j]), __uint_as_float(s[32 * k + 2 * j + 1])), c2, sub2), e0, e1);
+                        e0 = ex2(e0);
+                        e1 = ex2(e1);
+                        add[j & 1] = add2(add[j & 1], two(e0, e1));
                         pk[j] = pack2<F16>(e0, e1);
                     }
-                    tmem_st16(sc + 16u * k, pk);
+                    tmem_st16(pc + 16u * k, pk);
                 }
-                l += (add[0] + add[1]) + (add[2] + add[3]);
+                float a0, a1;
+                split2(add2(add[0], add[1]), a0, a1);
+                l += a0 + a1;
                 tmem_wait_st();
                 fence_before();
                 __syncwarp();
                 if (lane == 0) bar_arrive(su32(&p_full[xs]));
             }
+
+            // -------------------------------------------------------------- outputs
+            // thread = row; with one row tile a CTA the warp groups take half of the columns each
+            constexpr int NC = PAIR ? D : 128;
+            const int col0 = PAIR ? 0 : 128 * xs;
+            if (!PAIR) {
+                asm volatile("bar.sync 1, 256;" ::: "memory");    // the references are final
+                const float end = refs[row];
+                sums[128 * xs + row] = ref == -INFINITY ? 0.f : l * ex2(ref - end);
+                ref = end;
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+                l = sums[row] + sums[128 + row];
+                if (nt == 0) l = 0.f, ref = -INFINITY;
+            }
+            if (nt > 0) {
+                if (PAIR) {
+                    wait(&o_done[xs], done[xs] + nt - 1);
+                } else {
+                    if (nsteps > 1) wait(&o_done[nsteps & 1], done[nsteps & 1] + ((nsteps - 2) >> 1));
+                    wait(&o_done[(nsteps - 1) & 1], done[(nsteps - 1) & 1] + ((nsteps - 1) >> 1));
+                }
+                if (!go) continue;
+                fence_after();
+            }
+            done[0] += PAIR ? nt : (nt + 1) / 2;
+            done[1] += PAIR ? nt : nt / 2;
+            units += 2 * nt * UPT;
+            const int m = r / p.G, h = r - m * p.G;
+            const bool live = m < it.cnt && nt > 0;
+            const float inv = live && l != 0.f ? 1.f / l : 0.f;
+            float4 *part = reinterpret_cast<float4 *>(p.tile_o + (part0 + r) * D + col0);
+            uint4 *out = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.o) +
+                                                   (((size_t)it.b * p.M + m) * p.Hq + it.g * p.G + h) * D + col0);
+            if (parts && r < rows && col0 == 0) *reinterpret_cast<float2 *>(p.tile_ml + (part0 + r) * 2) = make_float2(ref, l);
+#pragma unroll 1
+            for (int k = 0; k < NC / 32; ++k) {
+                uint32_t o[32];
+                if (nt > 0) {
+                    tmem_ld32(oc + col0 + 32 * k, o);
+                    tmem_wait_ld();
+                }
+                if (r < rows && parts && nt > 0) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        part[8 * k + j] = make_float4(__uint_as_float(o[4 * j]), __uint_as_float(o[4 * j + 1]),
+                                                      __uint_as_float(o[4 * j + 2]), __uint_as_float(o[4 * j + 3]));
+                } else if (r < rows && !parts) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t v[4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            v[q] = live ? pack2<F16>(__uint_as_float(o[8 * j + 2 * q]) * inv, __uint_as_float(o[8 * j + 2 * q + 1]) * inv) : 0u;
+                        out[4 * k + j] = make_uint4(v[0], v[1], v[2], v[3]);
+                    }
+                }
+                __syncwarp();
+            }
+            if (nt > 0) {
+                fence_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive(su32(&o_free[PAIR ? xs : 0]));
+            }
         }
     }
     fence_before();
-    __syncthreads();
-    fence_after();
-    float *lsum = reinterpret_cast<float *>(sm + L::ring), *lref = lsum + 256;   // the ring is done with
-    if (!PAIR) {
-        if (warp < 8) {
-            lsum[tid] = l;
-            lref[tid] = ref;
-        }
-        __syncthreads();
-    }
-    if (warp < 8 && *abort_flag == 0) {
-        // --------------------------------------------------------------- outputs
-        // thread = row; with one row tile a CTA the warp groups take half of the columns each
-        const int xs = warp >> 2, w = warp & 3, r = r0 + (PAIR ? 128 * xs : 0) + (tid & 127);
-        constexpr int NC = PAIR ? D : 128;
-        const int col0 = PAIR ? 0 : 128 * xs;
-        const uint32_t oc = tmem + ((uint32_t)(32 * w) << 16) + 256u + (PAIR ? (uint32_t)(D * xs) : (uint32_t)col0);
-        if (!PAIR) {
-            ref = refs[tid & 127];
-            l = 0.f;
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const float rk = lref[128 * k + (tid & 127)];
-                if (rk != -INFINITY) l += lsum[128 * k + (tid & 127)] * ex2(rk - ref);
-            }
-        }
-        const int m = r / p.G, h = r - m * p.G;   // windows only
-        const float inv = parts ? 1.f : l != 0.f ? 1.f / l : 0.f;
-        const bool live = PREFIX || m < cnt;
-#pragma unroll 1
-        for (int k = 0; k < NC; k += 32) {
-            uint32_t o[32];
-            tmem_ld32(oc + k, o);
-            tmem_wait_ld();
-            if (r >= rows) continue;
-            if (parts) {
-                float4 *to = reinterpret_cast<float4 *>(p.tile_o + (part0 + r) * D + col0 + k);
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    to[j] = make_float4(__uint_as_float(o[4 * j]), __uint_as_float(o[4 * j + 1]), __uint_as_float(o[4 * j + 2]),
-                                        __uint_as_float(o[4 * j + 3]));
-            } else {
-                uint4 *to = reinterpret_cast<uint4 *>(out + (((size_t)b * p.M + m) * p.Hq + g * p.G + h) * D + col0 + k);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    uint32_t v[4];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        v[q] = live ? pack2<F16>(__uint_as_float(o[8 * j + 2 * q]) * inv, __uint_as_float(o[8 * j + 2 * q + 1]) * inv) : 0u;
-                    to[j] = make_uint4(v[0], v[1], v[2], v[3]);
-                }
-            }
-        }
-        if (parts && r < rows && col0 == 0) *reinterpret_cast<float2 *>(p.tile_ml + (part0 + r) * 2) = make_float2(ref, l);
-        fence_before();
-    }
     __syncthreads();
     if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
 }
@@ -691,18 +844,22 @@ int launch_kv_tiles(const KvCall &c, bool prefix, cudaStream_t stream)
     const long long ntile = kv_row_tiles(rows, c.D), ctas = ntile * c.nsplit * c.Hkv * (prefix ? 1 : c.B);
     if (rows > INT_MAX - 1024 || ctas > INT_MAX) return MOE_ERR_UNSUPPORTED;
     tp.ntile = (int)ntile;
+    tp.items = (int)ctas;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess || dev < 0 || dev >= 64) { note_cuda_error((int)e); return MOE_ERR_CUDA; }
-    auto go = [&](auto kernel, int smem, std::once_flag *once) {
-        std::call_once(once[dev], [&] {
+    auto go = [&](auto kernel, int smem, Once &once) {
+        std::call_once(once.flag[dev], [&] {
             e = cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+            if (e == cudaSuccess) e = cudaDeviceGetAttribute(&once.sms[dev], cudaDevAttrMultiProcessorCount, dev);
         });
-        if (e == cudaSuccess) e = launch_after(kernel, dim3((unsigned)ctas), kTThreads, smem, 0, stream, tp);
+        if (e == cudaSuccess && once.sms[dev] < 1) e = cudaErrorInvalidDevice;
+        if (e == cudaSuccess)
+            e = launch_after(kernel, dim3((unsigned)std::min<long long>(ctas, once.sms[dev])), kTThreads, smem, 0, stream, tp);
     };
 #define KV_TILE(F, D, P)                                                 \
     do {                                                                 \
-        static std::once_flag once[64];                                  \
+        static Once once;                                                \
         go(kv_tile_kernel<F, D, P>, TLay<D>::total + 1024, once);        \
     } while (0)
 #define KV_TILE_P(F, D)                  \
