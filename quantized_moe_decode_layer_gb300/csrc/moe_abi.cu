@@ -1005,6 +1005,7 @@ int moe_kv_attn(const moe_kv *cache, const moe_rows *q, int M, const int32_t *po
     p.Hq = cache->q_heads;
     p.Hkv = cache->kv_heads;
     p.G = G;
+    p.by_g = div_by(G);
     p.D = cache->head_dim;
     p.T = cache->T_cap;
     p.limit = cache->window ? kKvMaxPos : cache->T_cap;
@@ -1068,6 +1069,7 @@ int moe_window_attn(const moe_window *shape, const moe_rows *q, const moe_rows *
     p.Hq = shape->q_heads;
     p.Hkv = shape->kv_heads;
     p.G = p.Hq / p.Hkv;
+    p.by_g = div_by(p.G);
     p.D = shape->head_dim;
     p.T = p.limit = shape->positions;
     p.W = shape->window ? shape->window : kKvAll;

@@ -11,6 +11,19 @@ constexpr int kKvMaxCtas = 4 * kMaxCtas;
 constexpr int kKvMaxPos = 1 << 30;    // positions of a sequence whose cache is a ring
 constexpr int kKvAll = 1 << 30;       // window of a sequence that sees everything
 
+// Division of 0 <= x < 2^31 by a number known to the host.
+struct Div {
+    uint32_t m;
+    int s;
+    __host__ __device__ int operator()(int x) const { return (int)(((unsigned long long)(uint32_t)x * m) >> s); }
+};
+inline Div div_by(uint32_t d)
+{
+    int l = 0;
+    while ((1ull << l) < d) ++l;
+    return {(uint32_t)((1ull << (31 + l)) / d + 1), 31 + l};
+}
+
 // One attention call: q, k, v as they lie (strides in elements), the visible
 // positions, and where partial results go.
 struct KvCall {
@@ -22,6 +35,7 @@ struct KvCall {
     int *err;
     void *o;                          // [B][M][Hq][D], q's type
     int B, M, Hq, Hkv, G, D;
+    Div by_g;                         // G
     int T;                            // slots of a sequence
     int limit;                        // positions that a sequence may have
     int W, S;                         // window (kKvAll: none), first positions that stay visible

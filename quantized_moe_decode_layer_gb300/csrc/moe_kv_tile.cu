@@ -45,28 +45,29 @@ constexpr int kBox = 128 * 128;       // one TMA box: 128 positions of 64 elemen
 constexpr int kTThreads = 384;        // softmax: warps 0-3, 4-7; loads 8; products 9; q 10, 11
 constexpr int kQThreads = 64;
 constexpr int kErrTimeout = 4;
+constexpr int kItems = 4, kItemBytes = 48;   // items known ahead
 
 template <int D>
 struct TLay {
     static constexpr bool kPair = D <= 128;                   // two row tiles a CTA
-    static constexpr bool kOwnP = D == 64;                    // P beside S in tensor memory, not over it
-    static constexpr bool kAhead = !kPair || kOwnP;           // the next tile's scores come before this one's values
     static constexpr int NQ = kPair ? 2 : 1;
     static constexpr int RT = NQ * kRows;
     static constexpr int kUnit = D == 64 ? kBox : 2 * kBox;   // 128 positions x min(D, 128)
     static constexpr int UPT = D == 256 ? 2 : 1;              // units of a tile of keys or values
-    static constexpr int NU = D == 64 ? 8 : 5;
+        static constexpr int NU = 4;                              // (5 or 8 measured no faster)
     static constexpr int q = 0;
     static constexpr int ring = NQ * (D / 64) * kBox;
-    static constexpr int bars = ring + NU * kUnit;
-    static constexpr int kBars = 2 * NU + 2 * 5 + 8 + 3;
+    static constexpr int stage = ring + NU * kUnit;           // outputs on their way, a box a stream
+    static constexpr int bars = stage + 2 * kBox;
+    static constexpr int kBars = 2 * NU + 2 * 4 + 8 + 3 + 2 * kItems;
     static constexpr int misc = bars + kBars * 8;             // tensor-memory address, abort flag
     static constexpr int refs = misc + 8;                     // [128] references, [2][128] sums (one row tile)
-    static constexpr int total = refs + 3 * 128 * 4;
+    static constexpr int items = refs + 3 * 128 * 4;          // [kItems] items
+    static constexpr int total = items + kItems * kItemBytes;
 };
 static_assert(TLay<64>::total + 1024 <= kSmemMax && TLay<128>::total + 1024 <= kSmemMax && TLay<256>::total + 1024 <= kSmemMax,
               "shared memory");
-// tensor memory: S of the streams at columns 0 and 128, O from 256 on, P over S or from 384 on
+// tensor memory: S of the streams at columns 0 and 128, O from 256 on, P over S
 constexpr uint32_t kTmemCols = 512;
 // registers a thread: launched with 168; the softmax warps take what the others leave
 constexpr int kRegsSoft = 208, kRegsRest = 88;
@@ -78,8 +79,9 @@ struct Once {
 };
 
 struct TileParams {
-    CUtensorMap tk, tv;
+    CUtensorMap tk, tv, tq, to;
     KvCall c;
+    int qmap, omap;   // q and outputs by TMA: 128 packed rows are a rectangle of theirs
     int ntile;     // row tiles (CTAs' worth) of a head
     int nsplit;
     int items;     // row tiles times parts times heads (times sequences)
@@ -218,6 +220,23 @@ __device__ __forceinline__ void tma_load4(uint32_t dst, const CUtensorMap *map, 
         : "memory");
 }
 
+__device__ __forceinline__ void tma_load5(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, int c3, int c4, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(
+            dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_store5(const CUtensorMap *map, uint32_t src, int c0, int c1, int c2, int c3, int c4)
+{
+    asm volatile("cp.async.bulk.tensor.5d.global.shared::cta.bulk_group [%0, {%2, %3, %4, %5, %6}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(src), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
+                 : "memory");
+}
+
 template <bool F16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi)
 {
@@ -265,11 +284,10 @@ __device__ __forceinline__ int rows_of(const KvCall &p, int b, int &p0, bool &ba
     return kv8_rows(p.pos ? p.pos + b : &last, p.counts ? p.counts + b : nullptr, 0, p.M, p.limit, p0, bad);
 }
 
-// The order in which a tile's keys (or values) are loaded: as the steps first use them.
-template <bool AHEAD>
-__device__ __forceinline__ int k_order(int t) { return !AHEAD ? 2 * t : t == 0 ? 0 : 2 * t - 1; }
-template <bool AHEAD>
-__device__ __forceinline__ int v_order(int t, int nt) { return !AHEAD ? 2 * t + 1 : t == nt - 1 ? 2 * nt - 1 : 2 * t + 2; }
+// The order in which tiles of keys and values are loaded: as the steps first use them.
+// Two row tiles: K0 V0 K1 V1 ...; one: K0 K1 V0 K2 V1 ... (both streams' scores come first).
+template <bool PAIR>
+__device__ __forceinline__ int v_order(int t, int nt) { return PAIR ? 2 * t + 1 : t == nt - 1 ? 2 * nt - 1 : 2 * t + 2; }
 
 // A CTA's worth of work: row tile(s) r0 .. of one head against nt tiles of positions:
 // tiles i0 .. i0 + nt - 1 of the list that has the first nsink tiles and then those from kt_lo on.
@@ -284,11 +302,11 @@ __device__ __forceinline__ Item item_of(const TileParams &tp, int x)
 {
     const KvCall &p = tp.c;
     Item it;
+    const int seqs = PREFIX ? 1 : p.B;
     it.z = x % tp.nsplit;
     x /= tp.nsplit;
     it.g = x % p.Hkv;
     x /= p.Hkv;
-    const int seqs = PREFIX ? 1 : p.B;
     it.b = x % seqs;
     const int tile = tp.ntile - 1 - x / seqs;   // later row tiles, which see more, first
     it.r0 = tile * RT;
@@ -300,8 +318,8 @@ __device__ __forceinline__ Item item_of(const TileParams &tp, int x)
     } else {
         bool bad;
         it.cnt = rows_of(p, it.b, it.p0, bad);
-        if (bad && threadIdx.x == 0) atomicOr(p.err, kKv8ErrRange);
-        const int first = it.r0 / p.G, last = min((it.r0 + RT - 1) / p.G, it.cnt - 1);
+        if (bad) atomicOr(p.err, kKv8ErrRange);
+        const int first = p.by_g(it.r0), last = min(p.by_g(it.r0 + RT - 1), it.cnt - 1);
         it.nvalid = it.p0 + it.cnt;
         if (first < it.cnt) {
             it.kt_lo = max(0, it.p0 + first - p.W + 1) / kKeys;
@@ -315,21 +333,70 @@ __device__ __forceinline__ Item item_of(const TileParams &tp, int x)
     return it;
 }
 
+static_assert(sizeof(Item) <= kItemBytes, "an item's words");
+
+// The items of a CTA, in turn.
+struct Items {
+    uint8_t *ring;
+    uint64_t *ready, *read;
+    // The n-th, once it is there.  After the last of a role's threads has it: done(n).
+    __device__ __forceinline__ bool get(int n, Item &it, volatile int *abort, const KvCall &c) const
+    {
+        const int s = n % kItems;
+        const bool ok = bar_wait(su32(&ready[s]), (unsigned)(n / kItems) & 1u, abort, c);
+        const int4 *w = reinterpret_cast<const int4 *>(ring + s * kItemBytes);
+        const int4 a = w[0], b = w[1], d = w[2];
+        it.z = a.x, it.g = a.y, it.b = a.z, it.r0 = a.w;
+        it.p0 = b.x, it.cnt = b.y, it.nvalid = b.z, it.kt_lo = b.w;
+        it.nsink = d.x, it.i0 = d.y, it.nt = d.z;
+        return ok;
+    }
+    __device__ __forceinline__ void done(int n) const { bar_arrive(su32(&read[n % kItems])); }
+    __device__ __forceinline__ void put(int n, const Item &it) const
+    {
+        int4 *w = reinterpret_cast<int4 *>(ring + n % kItems * kItemBytes);
+        w[0] = make_int4(it.z, it.g, it.b, it.r0);
+        w[1] = make_int4(it.p0, it.cnt, it.nvalid, it.kt_lo);
+        w[2] = make_int4(it.nsink, it.i0, it.nt, 0);
+        bar_arrive(su32(&ready[n % kItems]));
+    }
+};
+
+// Four lanes with 64 bytes each (16 words): lane j gets the j-th 16 bytes of each of the four, so that a store
+// of the warp has 64 bytes in a row instead of 16 (128 x 128 outputs: 3 us -> below 1).
+__device__ __forceinline__ void quad_transpose(uint32_t (&v)[16], int lane)
+{
+#pragma unroll
+    for (int d = 1; d <= 2; d <<= 1)
+#pragma unroll
+        for (int a = 0; a < 4; ++a) {
+            if (a & d) continue;
+            const bool up = lane & d;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t &lo = v[4 * a + j], &hi = v[4 * (a + d) + j];
+                const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, up ? lo : hi, d);
+                if (up) lo = got;
+                else hi = got;
+            }
+        }
+}
+
 template <bool F16, int D, bool PREFIX>
 __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_constant__ TileParams tp)
 {
     using L = TLay<D>;
-    constexpr bool PAIR = L::kPair, OWNP = L::kOwnP, AHEAD = L::kAhead;
+    constexpr bool PAIR = L::kPair;
+    constexpr int KS = kKeys / 2;
     constexpr int NU = L::NU, UPT = L::UPT, RT = L::RT;
     const KvCall &p = tp.c;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;   // warp: uniform, as the products' operands have to be
-    // barriers, each two one for a stream: S is there; it has been read; P is
-    // there; P V is done; O has been read
+    // barriers, each two one for a stream: S is there; P is there; P V is done; O has been read
     uint64_t *full = reinterpret_cast<uint64_t *>(sm + L::bars), *empty = full + NU;
-    uint64_t *s_full = empty + NU, *s_read = s_full + 2, *p_full = s_read + 2, *o_done = p_full + 2,
-             *o_free = o_done + 2, *ref_rdy = o_free + 2, *q_full = ref_rdy + 8, *q_free = q_full + 1, *all_done = q_free + 1;
+    uint64_t *s_full = empty + NU, *p_full = s_full + 2, *o_done = p_full + 2,
+             *o_free = o_done + 2, *ref_rdy = o_free + 2, *q_full = ref_rdy + 8, *q_free = q_full + 1, *all_done = q_free + 1, *i_ready = all_done + 1, *i_read = i_ready + kItems;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + L::misc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     float *refs = reinterpret_cast<float *>(sm + L::refs), *sums = refs + 128;
@@ -341,13 +408,16 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
         }
         for (int s = 0; s < 2; ++s) {
             bar_init(su32(&s_full[s]), 1);
-            bar_init(su32(&s_read[s]), 4);
             bar_init(su32(&p_full[s]), 4);
             bar_init(su32(&o_done[s]), 1);
             bar_init(su32(&o_free[s]), PAIR ? 4 : 8);
         }
         for (int s = 0; s < 8; ++s) bar_init(su32(&ref_rdy[s]), 1);
-        bar_init(su32(q_full), kQThreads);
+        for (int s = 0; s < kItems; ++s) {
+            bar_init(su32(&i_ready[s]), 1);
+            bar_init(su32(&i_read[s]), 12);   // the softmax warps, loads, products, q
+        }
+        bar_init(su32(q_full), tp.qmap ? 1 : kQThreads);
         bar_init(su32(q_free), 1);
         bar_init(su32(all_done), 1);
         *abort_flag = 0;
@@ -365,6 +435,8 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
     const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
     const long long rows = (long long)p.M * p.G * (PREFIX ? p.B : 1);   // of a head (and sequence)
     const bool parts = PREFIX || tp.nsplit > 1;
+    const Items items = {sm + L::items, i_ready, i_read};
+    const int mine = blockIdx.x < tp.items ? (tp.items - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;   // items of the CTA
 
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
@@ -373,8 +445,11 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
             if (lane == 0) {
                 bool go = true;
                 int slot = 0, turn = 0, n = 0;   // of the next unit; units issued
-                for (int x = blockIdx.x; x < tp.items && go; x += gridDim.x) {
-                    const Item it = item_of<RT, PREFIX>(tp, x);
+                for (int k = 0; k < mine && go; ++k) {
+                    Item it;
+                    go = items.get(k, it, abort_flag, p);
+                    items.done(k);
+                    if (!go) break;
                     auto load = [&](const CUtensorMap *map, int t) {
                         const int key = it.first_key(t);
                         for (int u = 0; u < UPT && go; ++u) {
@@ -394,9 +469,9 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                             }
                         }
                     };
-                    if (AHEAD && it.nt > 0) load(&tp.tk, 0);
+                    if (!PAIR && it.nt > 0) load(&tp.tk, 0);
                     for (int t = 0; t < it.nt && go; ++t) {
-                        const int kt = AHEAD ? t + 1 : t;
+                        const int kt = !PAIR ? t + 1 : t;
                         if (kt < it.nt) load(&tp.tk, kt);
                         if (go) load(&tp.tv, t);
                     }
@@ -410,19 +485,49 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
             }
         } else if (warp >= 10) {
             // ---------------------------------------------------- q, packed into rows
+            // and, ahead of all others, which items there are: warp 11 writes two more than are worked on
             constexpr int CH = D / 8;
             const int t = tid - 320;
             int qn = 0;
             bool go = true;
-            for (int x = blockIdx.x; x < tp.items; x += gridDim.x) {
-                const Item it = item_of<RT, PREFIX>(tp, x);
-                if (it.nt == 0) continue;
-                if (qn > 0) go = __all_sync(0xFFFFFFFFu, bar_wait(su32(q_free), (unsigned)(qn - 1) & 1u, abort_flag, p));
+            auto tell = [&](int k) {
+                if (warp != 11 || lane != 0 || k >= mine) return;
+                const Item it = item_of<RT, PREFIX>(tp, blockIdx.x + k * gridDim.x);
+                if (k >= kItems && !bar_wait(su32(&i_read[k % kItems]), (unsigned)(k / kItems - 1) & 1u, abort_flag, p)) return;
+                items.put(k, it);
+            };
+            tell(0);
+            tell(1);
+            for (int k = 0; k < mine; ++k) {
+                tell(k + 2);
+                __syncwarp();
+                Item it;
+                go = items.get(k, it, abort_flag, p);
+                __syncwarp();
+                if (lane == 0) items.done(k);
+                if (go && it.nt > 0 && qn > 0) go = bar_wait(su32(q_free), (unsigned)(qn - 1) & 1u, abort_flag, p);
+                go = __all_sync(0xFFFFFFFFu, go);
                 if (!go) break;
+                if (it.nt == 0) continue;
+                ++qn;
+                if (tp.qmap) {
+                    if (t == 0) {
+                        bar_expect(su32(q_full), L::ring);
+                        // packed rows r0 .. : the token of r0 (of all sequences' in turn, for a prefix)
+                        const int m = p.by_g(it.r0);
+#pragma unroll
+                        for (int j = 0; j < L::NQ; ++j)
+#pragma unroll
+                            for (int h = 0; h < D / 64; ++h)
+                                tma_load5(su32(sm + L::q) + (j * (D / 64) + h) * kBox, &tp.tq, 64 * h, 0, it.g, m + j * (kRows / p.G),
+                                          PREFIX ? 0 : it.b, su32(q_full));
+                    }
+                    continue;
+                }
                 // (rows of idle sequences and padding are read like the others; nothing of them is used)
                 constexpr int STEP = kQThreads / CH;   // rows a pass
                 const int c = t % CH, rr0 = t / CH;
-                int r = it.r0 + rr0, m = r / p.G, h = r - m * p.G, bb = it.b;
+                int r = it.r0 + rr0, m = p.by_g(r), h = r - m * p.G, bb = it.b;
                 if (PREFIX) {
                     bb = m / p.M;
                     m -= bb * p.M;
@@ -450,7 +555,11 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                 asm volatile("cp.async.wait_all;" ::: "memory");
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 bar_arrive(su32(q_full));
-                ++qn;
+            }
+            // the last copies have landed before the CTA ends
+            if (tp.qmap && t == 0 && qn > 0) {
+                const unsigned long long t0 = gtime();
+                while (!bar_test(su32(q_full), (unsigned)(qn - 1) & 1u) && (long long)(gtime() - t0) <= p.timeout_ns) {}
             }
         } else {
             // ---------------------------------------------------------- products
@@ -474,15 +583,18 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                 };
                 Place base = {0, 0};
                 int qn = 0, done[2] = {0, 0};   // items and steps of the streams before this item
-                for (int x = blockIdx.x; x < tp.items && go; x += gridDim.x) {
-                    const int nt = item_of<RT, PREFIX>(tp, x).nt;
+                for (int n = 0; n < mine && go; ++n) {
+                    Item it;
+                    go = items.get(n, it, abort_flag, p);
+                    items.done(n);
+                    if (!go) break;
+                    const int nt = it.nt;
                     if (nt == 0) continue;
                     const int nsteps = PAIR ? 2 * nt : nt;
                     Place kp = base, vp = base;         // of the next tile of keys, of values
-                    vp.move(AHEAD && nt > 1 ? 2 * UPT : UPT);
+                    vp.move(!PAIR && nt > 1 ? 2 * UPT : UPT);
                     auto scores = [&](int i, int xs) {
                         const int t = PAIR ? i >> 1 : i;
-                        if (OWNP && done[xs] + (i >> 1) > 0) wait(&s_read[xs], done[xs] + (i >> 1) - 1);
                         Place at = kp;
 #pragma unroll
                         for (int u = 0; u < UPT; ++u) {
@@ -501,7 +613,7 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                         }
                         umma_commit(su32(&s_full[xs]));
                         if (i == nsteps - 1) umma_commit(su32(q_free));
-                        if (!PAIR || xs == 1) kp.move(AHEAD && t == 0 ? UPT : 2 * UPT);
+                        if (!PAIR || xs == 1) kp.move(!PAIR && t == 0 ? UPT : 2 * UPT);
                     };
                     auto values = [&](int i, int xs) {
                         const int t = PAIR ? i >> 1 : i, step = done[xs] + (i >> 1);
@@ -521,20 +633,19 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
 #pragma unroll
                         for (int u = 0; u < UPT; ++u) {
                             const uint32_t o = tmem + 256u + (PAIR ? (uint32_t)(D * xs) : 128u * u);
-                            const uint32_t a0 = tmem + (OWNP ? 384u + 64u * xs : 128u * xs), b0 = desc_mn(ring + at.slot * L::kUnit);
+                            const uint32_t b0 = desc_mn(ring + at.slot * L::kUnit);
 #pragma unroll
                             for (int k = 0; k < kKeys / 16; ++k)
-                                umma_ts(o, a0 + 8u * k, b0 + 128u * k, id_o, (t | k) != 0 ? 1u : 0u);
+                                umma_ts(o, tmem + 128u * xs + 8u * k, b0 + 128u * k, id_o, (t | k) != 0 ? 1u : 0u);
                             if (!PAIR || xs == 1) umma_commit(su32(&empty[at.slot]));
                             at.move(1);
                         }
                         umma_commit(su32(&o_done[xs]));
-                        if (!PAIR || xs == 1) vp.move(AHEAD && t + 2 >= nt ? UPT : 2 * UPT);
+                        if (!PAIR || xs == 1) vp.move(!PAIR && t + 2 >= nt ? UPT : 2 * UPT);
                     };
                     auto step = [&](int i, int xs) {
-                        if (OWNP && i + 2 < nsteps) scores(i + 2, xs);
-                        if (go) values(i, xs);
-                        if (!OWNP && go && i + 2 < nsteps) scores(i + 2, xs);
+                        values(i, xs);
+                        if (go && i + 2 < nsteps) scores(i + 2, xs);
                     };
                     wait(q_full, qn);
                     if (go) scores(0, 0);
@@ -544,7 +655,7 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                         step(i, 0);
                         if (go && i + 1 < nsteps) step(i + 1, 1);
                     }
-                    for (int n = 0; n < (2 * nt) % NU; ++n) base.move(UPT);
+                    for (int j = 0; j < (2 * nt) % NU; ++j) base.move(UPT);
                     base.phase ^= (2 * nt / NU * UPT) & 1;
                     done[0] += PAIR ? nt : (nt + 1) / 2;
                     done[1] += PAIR ? nt : nt / 2;
@@ -561,7 +672,7 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
         // --------------------------------------------------------------- softmax
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
         const int xs = warp >> 2, w = warp & 3, row = tid & 127;
-        const uint32_t lanes = tmem + ((uint32_t)(32 * w) << 16), sc = lanes + 128u * xs, pc = OWNP ? lanes + 384u + 64u * xs : sc;
+        const uint32_t lanes = tmem + ((uint32_t)(32 * w) << 16), sc = lanes + 128u * xs;
         const uint32_t oc = lanes + 256u + (PAIR ? (uint32_t)(D * xs) : 0u);
         const float c = p.c;
         const uint64_t c2 = two(c, c);
@@ -572,8 +683,13 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
         };
         // (after a wait has given up the streams of one row tile still meet at each item's barriers)
 #pragma unroll 1
-        for (int x = blockIdx.x; x < tp.items; x += gridDim.x) {
-            const Item it = item_of<RT, PREFIX>(tp, x);
+        for (int n = 0; n < mine; ++n) {
+            Item it;
+            {
+                const bool ok = items.get(n, it, abort_flag, p);
+                go = __all_sync(0xFFFFFFFFu, go && ok);
+                if (lane == 0) items.done(n);
+            }
             const int nt = it.nt, nsteps = PAIR ? 2 * nt : nt, r = it.r0 + (PAIR ? 128 * xs : 0) + row;
             const size_t part0 = ((size_t)it.z * p.Hkv + it.g) * ((size_t)p.B * p.M * p.G) + (PREFIX ? 0 : (size_t)it.b * p.M * p.G);
             // positions t the row sees: t <= high and (t > low or t < S); all_*: the strictest of the tile's rows
@@ -583,85 +699,23 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                 low = all_low = -1;
             } else {
                 const int ra = it.r0 + (PAIR ? 128 * xs : 0);
-                high = it.p0 + r / p.G;
+                high = it.p0 + p.by_g(r);
                 low = high - p.W;
-                all_high = it.p0 + ra / p.G;
-                all_low = it.p0 + (ra + kRows - 1) / p.G - p.W;
+                all_high = it.p0 + p.by_g(ra);
+                all_low = it.p0 + p.by_g(ra + kRows - 1) - p.W;
             }
             float l = 0.f, ref = -INFINITY;    // of the row, as the stream knows them
+            bool primed = false;               // every row of the warp has a reference
 #pragma unroll 1
             for (int i = xs; i < nsteps && go; i += 2) {
                 const int t = PAIR ? i >> 1 : i, key = it.first_key(t), step = done[xs] + (i >> 1);
                 wait(&s_full[xs], step);
                 if (!go) break;
                 fence_after();
-                uint32_t s[kKeys];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) tmem_ld32(sc + 32u * k, s + 32 * k);
-                tmem_wait_ld();
-                if (OWNP) {
-                    fence_before();
-                    __syncwarp();
-                    if (lane == 0) bar_arrive(su32(&s_read[xs]));
-                }
-                // a tile that some row does not see all of
-                if (key + kKeys - 1 > all_high || (key <= all_low && key + kKeys > p.S)) {
-                    auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; };
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int at = key + 32 * k;
-                        const uint32_t sees = below(high + 1 - at) & (~below(low + 1 - at) | below(p.S - at));
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (!(sees >> j & 1u)) s[32 * k + j] = 0xFF800000u;
-                    }
-                }
-                float mx[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) mx[j] = __uint_as_float(s[j]);
-#pragma unroll
-                for (int k = 4; k + 8 <= kKeys; k += 8)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) mx[j] = max3(mx[j], __uint_as_float(s[k + j]), __uint_as_float(s[k + 4 + j]));
-#pragma unroll
-                for (int j = 0; j < 4; ++j) mx[j] = fmaxf(mx[j], __uint_as_float(s[kKeys - 4 + j]));
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-                float was = ref;
-                if (!PAIR && i > 0) {   // the reference, from the stream that has the tile before
-                    wait(&ref_rdy[4 * (xs ^ 1) + w], done[xs ^ 1] + ((i - 1) >> 1));
-                    if (!go) break;
-                    was = refs[row];
-                }
-                const bool raise = top > was + 8.f;
-                const float now = raise ? top : was;
-                if (!PAIR) {
-                    refs[row] = now;
-                    __syncwarp();
-                    if (lane == 0) bar_arrive(su32(&ref_rdy[4 * xs + w]));
-                }
-                if (now != ref) l *= ref == -INFINITY ? 0.f : ex2(ref - now);
-                ref = now;
-                if (__any_sync(0xFFFFFFFFu, raise) && t > 0) {
-                    // O, which has the tiles up to the one before, in the new reference's units
-                    const int y = PAIR ? xs : xs ^ 1;
-                    wait(&o_done[y], done[y] + ((PAIR ? i - 2 : i - 1) >> 1));
-                    if (!go) break;
-                    fence_after();
-                    const float f = raise ? ex2(was - now) : 1.f;
-#pragma unroll 1
-                    for (int k = 0; k < D; k += 32) {
-                        uint32_t o[32];
-                        tmem_ld32(oc + k, o);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                        tmem_st32(oc + k, o);
-                    }
-                }
                 if (!PREFIX && it.nvalid - key < kKeys && (!PAIR || xs == 0)) {
                     // values behind the sequence's last position may be anything: zeros
                     const int gone = it.nvalid - key;
-                    const int n0 = units + UPT * v_order<AHEAD>(t, nt);
+                    const int n0 = units + UPT * v_order<PAIR>(t, nt);
 #pragma unroll 1
                     for (int u = n0; u < n0 + UPT; ++u) {
                         wait(&full[u % NU], u / NU);
@@ -675,30 +729,116 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                     if (!go) break;
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 }
-                if (OWNP && t > 0) {   // P of the step before has been read
-                    wait(&o_done[xs], step - 1);
-                    if (!go) break;
-                }
-                const float sub = ref == -INFINITY ? 0.f : -ref;
-                const uint64_t sub2 = two(sub, sub);
+                // Two row tiles: the weights are taken with the reference as it was, along with the maximum, and once more
+                // in the rare case that it was too low.  (One row tile: the reference is handed on at once.)
+                const bool partly = key + kKeys - 1 > all_high || (key <= all_low && key + kKeys > p.S);   // hidden from some row
+                bool again = !PAIR || !primed;
+                uint32_t s0[KS], s1[KS];    // the positions' halves
+                uint32_t pk[kKeys / 2];
                 uint64_t add[2] = {0ull, 0ull};
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                auto load = [&](int half, uint32_t *s) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    uint32_t pk[16];
+                    for (int k = 0; k < KS / 32; ++k) tmem_ld32(sc + (uint32_t)(KS * half + 32 * k), s + 32 * k);
+                };
+                auto hide = [&](int half, uint32_t *s) {
+                    if (!partly) return;
+                    auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; };
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
+                    for (int k = 0; k < KS / 32; ++k) {
+                        const int at = key + KS * half + 32 * k;
+                        const uint32_t sees = below(high + 1 - at) & (~below(low + 1 - at) | below(p.S - at));
+                        if (__all_sync(0xFFFFFFFFu, sees == ~0u)) continue;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (!(sees >> j & 1u)) s[32 * k + j] = 0xFF800000u;
+                    }
+                };
+                auto largest = [&](const uint32_t *s) {
+#pragma unroll
+                    for (int k = 0; k < KS; k += 8)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) mx[j] = max3(mx[j], __uint_as_float(s[k + j]), __uint_as_float(s[k + 4 + j]));
+                };
+                auto weights = [&](int half, const uint32_t *s, uint64_t sub2) {
+#pragma unroll
+                    for (int j = 0; j < KS / 2; ++j) {
                         float e0, e1;
-                        split2(fma2(two(__uint_as_float(s[32 * k + 2 * j]), __uint_as_float(s[32 * k + 2 * j + 1])), c2, sub2), e0, e1);
+                        split2(fma2(two(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), c2, sub2), e0, e1);
                         e0 = ex2(e0);
                         e1 = ex2(e1);
                         add[j & 1] = add2(add[j & 1], two(e0, e1));
-                        pk[j] = pack2<F16>(e0, e1);
+                        pk[KS / 2 * half + j] = pack2<F16>(e0, e1);
                     }
-                    tmem_st16(pc + 16u * k, pk);
+                };
+                load(0, s0);
+                tmem_wait_ld();
+                load(1, s1);
+                if (!again) {
+                    const uint64_t sub2 = two(-ref, -ref);
+                    hide(0, s0);
+                    largest(s0);
+                    weights(0, s0, sub2);
+                    tmem_wait_ld();
+                    hide(1, s1);
+                    largest(s1);
+                    weights(1, s1, sub2);
+                    again = __any_sync(0xFFFFFFFFu, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c > ref + 8.f);
+                    if (again) {
+                        load(0, s0);
+                        load(1, s1);
+                    }
+                }
+                if (again) {
+                    tmem_wait_ld();
+                    hide(0, s0);
+                    hide(1, s1);
+                    largest(s0);
+                    largest(s1);
+                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+                    float was = ref;
+                    if (!PAIR && i > 0) {   // the reference, from the stream that has the tile before
+                        wait(&ref_rdy[4 * (xs ^ 1) + w], done[xs ^ 1] + ((i - 1) >> 1));
+                        if (!go) break;
+                        was = refs[row];
+                    }
+                    const bool raise = top > was + 8.f;
+                    const float now = raise ? top : was;
+                    if (!PAIR) {
+                        refs[row] = now;
+                        __syncwarp();
+                        if (lane == 0) bar_arrive(su32(&ref_rdy[4 * xs + w]));
+                    }
+                    if (now != ref) l *= ref == -INFINITY ? 0.f : ex2(ref - now);
+                    ref = now;
+                    primed = !__any_sync(0xFFFFFFFFu, ref == -INFINITY);
+                    if (__any_sync(0xFFFFFFFFu, raise) && t > 0) {
+                        // O, which has the tiles up to the one before, in the new reference's units
+                        if (PAIR) wait(&o_done[xs], step - 1);
+                        else wait(&o_done[xs ^ 1], done[xs ^ 1] + ((i - 1) >> 1));
+                        if (!go) break;
+                        fence_after();
+                        const float f = raise ? ex2(was - now) : 1.f;
+#pragma unroll 1
+                        for (int k = 0; k < D; k += 32) {
+                            uint32_t o[32];
+                            tmem_ld32(oc + k, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                            tmem_st32(oc + k, o);
+                        }
+                    }
+                    const float sub = ref == -INFINITY ? 0.f : -ref;
+                    add[0] = add[1] = 0ull;
+                    weights(0, s0, two(sub, sub));
+                    weights(1, s1, two(sub, sub));
                 }
                 float a0, a1;
                 split2(add2(add[0], add[1]), a0, a1);
                 l += a0 + a1;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) tmem_st16(sc + 16u * k, pk + 16 * k);
                 tmem_wait_st();
                 fence_before();
                 __syncwarp();
@@ -725,49 +865,93 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                     if (nsteps > 1) wait(&o_done[nsteps & 1], done[nsteps & 1] + ((nsteps - 2) >> 1));
                     wait(&o_done[(nsteps - 1) & 1], done[(nsteps - 1) & 1] + ((nsteps - 1) >> 1));
                 }
-                if (!go) continue;
-                fence_after();
+                if (go) fence_after();
             }
             done[0] += PAIR ? nt : (nt + 1) / 2;
             done[1] += PAIR ? nt : nt / 2;
             units += 2 * nt * UPT;
-            const int m = r / p.G, h = r - m * p.G;
-            const bool live = m < it.cnt && nt > 0;
-            const float inv = live && l != 0.f ? 1.f / l : 0.f;
-            float4 *part = reinterpret_cast<float4 *>(p.tile_o + (part0 + r) * D + col0);
-            uint4 *out = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.o) +
-                                                   (((size_t)it.b * p.M + m) * p.Hq + it.g * p.G + h) * D + col0);
-            if (parts && r < rows && col0 == 0) *reinterpret_cast<float2 *>(p.tile_ml + (part0 + r) * 2) = make_float2(ref, l);
+            const bool live = PREFIX || p.by_g(r) < it.cnt;
+            const float inv = live && nt > 0 && l != 0.f ? 1.f / l : 0.f;
+            if (!PREFIX && tp.omap) {
+                // 64 columns at a time into the stream's box, and from there by TMA while the next item starts
+                uint8_t *box = sm + L::stage + xs * kBox;
 #pragma unroll 1
-            for (int k = 0; k < NC / 32; ++k) {
-                uint32_t o[32];
-                if (nt > 0) {
-                    tmem_ld32(oc + col0 + 32 * k, o);
-                    tmem_wait_ld();
-                }
-                if (r < rows && parts && nt > 0) {
+                for (int k = 0; k < NC / 64; ++k) {
+                    if ((tid & 127) == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                    asm volatile("bar.sync %0, 128;" ::"r"(2 + xs) : "memory");   // the box is free
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        part[8 * k + j] = make_float4(__uint_as_float(o[4 * j]), __uint_as_float(o[4 * j + 1]),
-                                                      __uint_as_float(o[4 * j + 2]), __uint_as_float(o[4 * j + 3]));
-                } else if (r < rows && !parts) {
+                    for (int half = 0; half < 2; ++half) {
+                        uint32_t o[32];
+                        tmem_ld32(oc + col0 + 64 * k + 32 * half, o);   // (not used where there is nothing to see)
+                        tmem_wait_ld();
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        uint32_t v[4];
+                        for (int j = 0; j < 4; ++j) {
+                            uint32_t v[4];
 #pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            v[q] = live ? pack2<F16>(__uint_as_float(o[8 * j + 2 * q]) * inv, __uint_as_float(o[8 * j + 2 * q + 1]) * inv) : 0u;
-                        out[4 * k + j] = make_uint4(v[0], v[1], v[2], v[3]);
+                            for (int q = 0; q < 4; ++q)
+                                v[q] = live && nt > 0 ? pack2<F16>(__uint_as_float(o[8 * j + 2 * q]) * inv, __uint_as_float(o[8 * j + 2 * q + 1]) * inv) : 0u;
+                            *reinterpret_cast<uint4 *>(box + row * 128 + (((4 * half + j) ^ (row & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+                        }
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    asm volatile("bar.sync %0, 128;" ::"r"(2 + xs) : "memory");   // and full
+                    const int m = p.by_g(r);
+                    if ((tid & 127) == 0 && go && m < p.M) {
+                        tma_store5(&tp.to, su32(box), col0 + 64 * k, 0, it.g, m, it.b);
+                        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                     }
                 }
-                __syncwarp();
+            } else if (go) {
+                // Four lanes exchange 64-byte pieces: lane 4 a + j then has piece j of rows 4 a .. 4 a + 3.
+                if (parts && r < rows && col0 == 0) *reinterpret_cast<float2 *>(p.tile_ml + (part0 + r) * 2) = make_float2(ref, l);
+                const int rq = r - (lane & 3);
+                uint8_t *to[4];     // the four rows' places
+                int m = p.by_g(rq), h = rq - m * p.G - 1;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (++h == p.G) {
+                        h = 0;
+                        ++m;
+                    }
+                    to[j] = parts ? reinterpret_cast<uint8_t *>(p.tile_o + (part0 + rq + j) * D + col0)
+                                  : reinterpret_cast<uint8_t *>(static_cast<uint16_t *>(p.o) +
+                                                                (((size_t)it.b * p.M + m) * p.Hq + it.g * p.G + h) * D + col0);
+                    to[j] += 16 * (lane & 3);
+                }
+#pragma unroll 1
+                for (int k = 0; k < NC / 32; ++k) {
+                    uint32_t o[32];
+                    if (nt > 0) {
+                        tmem_ld32(oc + col0 + 32 * k, o);
+                        tmem_wait_ld();
+                    } else if (parts) {
+                        break;      // an empty part
+                    }
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        if (!parts && half) break;
+                        uint32_t v[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            if (parts) v[j] = o[16 * half + j];
+                            else v[j] = live && nt > 0 ? pack2<F16>(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv) : 0u;
+                        }
+                        quad_transpose(v, lane);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (rq + j < rows)
+                                *reinterpret_cast<uint4 *>(to[j] + (parts ? 128 * k + 64 * half : 64 * k)) =
+                                    make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                    }
+                }
             }
-            if (nt > 0) {
+            if (nt > 0 && go) {
                 fence_before();
                 __syncwarp();
                 if (lane == 0) bar_arrive(su32(&o_free[PAIR ? xs : 0]));
             }
         }
+        if (!PREFIX && tp.omap && (tid & 127) == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
     fence_before();
     __syncthreads();
@@ -799,6 +983,23 @@ bool map_of(CUtensorMap *map, const uint16_t *base, bool f16, int D, int T, int 
     const cuuint64_t strides[3] = {bytes(row, T), bytes(head, heads), bytes(seq, seqs)};
     const cuuint32_t box[4] = {64, (cuuint32_t)kKeys, 1, 1}, es[4] = {1, 1, 1, 1};
     return enc(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint16_t *>(base), dims,
+               strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Packed rows as rectangles of a tensor: [sequence][token][key/value head][head of the group][d].  Needs a group
+// that divides a row tile, and strides that are not 0 (an expanded q is left to plain loads).
+bool packed_map(CUtensorMap *map, const KvCall &c, const void *base, long long tokens, int seqs, long long head, long long token,
+                long long seq)
+{
+    PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
+    if (!enc || kRows % c.G != 0 || tokens > INT_MAX) return false;
+    if ((c.Hq > 1 && head == 0) || (tokens > 1 && token == 0) || (seqs > 1 && seq == 0)) return false;
+    const cuuint64_t dims[5] = {(cuuint64_t)c.D, (cuuint64_t)c.G, (cuuint64_t)c.Hkv, (cuuint64_t)tokens, (cuuint64_t)seqs};
+    auto bytes = [&](long long s, long long n) { return (cuuint64_t)(n > 1 ? s * 2 : c.D * 2); };   // (one entry: any stride)
+    const cuuint64_t strides[4] = {bytes(head, c.G), bytes(c.G * head, c.Hkv), bytes(token, tokens), bytes(seq, seqs)};
+    const cuuint32_t box[5] = {64, (cuuint32_t)c.G, 1, (cuuint32_t)(kRows / c.G), 1}, es[5] = {1, 1, 1, 1, 1};
+    return enc(map, c.f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void *>(base), dims,
                strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -839,6 +1040,13 @@ int launch_kv_tiles(const KvCall &c, bool prefix, cudaStream_t stream)
         ok = map_of(&tp.tk, c.k, c.f16, c.D, c.T, c.Hkv, c.B, c.km, c.kh, c.kb) &&
              map_of(&tp.tv, c.v, c.f16, c.D, c.T, c.Hkv, c.B, c.vm, c.vh, c.vb);
     if (!ok) return MOE_ERR_UNSUPPORTED;
+    if (!prefix) {
+        tp.qmap = packed_map(&tp.tq, c, c.q, c.M, c.B, c.qh, c.qm, c.qb);
+        const long long row = (long long)c.Hq * c.D;
+        tp.omap = c.nsplit == 1 && packed_map(&tp.to, c, c.o, c.M, c.B, c.D, row, row * c.M);
+    } else if (c.B == 1 || c.M == 1 || c.qb == c.M * c.qm) {   // the batch's tokens have one stride
+        tp.qmap = packed_map(&tp.tq, c, c.q, (long long)c.B * c.M, 1, c.qh, c.M == 1 ? c.qb : c.qm, 0);
+    }
     const long long rows = (long long)c.M * c.G * (prefix ? c.B : 1);
     tp.nsplit = c.nsplit;
     const long long ntile = kv_row_tiles(rows, c.D), ctas = ntile * c.nsplit * c.Hkv * (prefix ? 1 : c.B);
