@@ -954,8 +954,14 @@ int moe_kv_attn_workspace_size(const moe_kv *cache, int M, int max_prefix, size_
     const int rc = kv_check(cache, M, false);
     if (rc) return rc;
     if (cache->window && max_prefix) return MOE_ERR_INVALID_ARG;
-    *bytes = kv_attn_workspace_bytes(cache->batch, cache->kv_heads, cache->q_heads / cache->kv_heads, cache->head_dim, M,
-                                     max_prefix, false);
+    // the most that a call of up to M rows, with a prefix or without, takes
+    size_t most = 0;
+    for (int m = 1; m <= M; ++m)
+        for (int P : {0, max_prefix}) {
+            const size_t n = kv_attn_workspace_bytes(cache->batch, cache->kv_heads, cache->q_heads / cache->kv_heads, cache->head_dim, m, P);
+            if (n > most) most = n;
+        }
+    *bytes = most;
     return MOE_OK;
 }
 
@@ -975,7 +981,7 @@ int moe_kv_attn(const moe_kv *cache, const moe_rows *q, int M, const int32_t *po
     if (prefix_len && (cache->window || !kv_rows_ok(prefix_k, cache->type) || !kv_rows_ok(prefix_v, cache->type)))
         return MOE_ERR_INVALID_ARG;
     const int G = cache->q_heads / cache->kv_heads;
-    if (ws_bytes < kv_attn_workspace_bytes(cache->batch, cache->kv_heads, G, cache->head_dim, M, prefix_len, true))
+    if (ws_bytes < kv_attn_workspace_bytes(cache->batch, cache->kv_heads, G, cache->head_dim, M, prefix_len))
         return MOE_ERR_BUFFER_TOO_SMALL;
     KvCall p = {};
     p.q = static_cast<const uint16_t *>(q->data_dev);
@@ -1009,6 +1015,7 @@ int moe_kv_attn(const moe_kv *cache, const moe_rows *q, int M, const int32_t *po
     p.D = cache->head_dim;
     p.T = cache->T_cap;
     p.limit = cache->window ? kKvMaxPos : cache->T_cap;
+    p.ring = cache->window != 0;
     p.W = cache->window ? cache->window : kKvAll;
     p.S = cache->sinks;
     p.f16 = cache->type == MOE_F16;
@@ -1028,7 +1035,7 @@ int moe_window_attn_workspace_size(const moe_window *shape, size_t *bytes)
     const int rc = window_check(shape);
     if (rc) return rc;
     if (!bytes) return MOE_ERR_INVALID_ARG;
-    *bytes = window_attn_workspace_bytes(*shape);
+    *bytes = kv_attn_workspace_bytes(shape->batch, shape->kv_heads, shape->q_heads / shape->kv_heads, shape->head_dim, shape->rows, 0);
     return MOE_OK;
 }
 
@@ -1044,7 +1051,7 @@ int moe_window_attn(const moe_window *shape, const moe_rows *q, const moe_rows *
     for (const moe_rows *r : {k, v})
         if ((shape->batch > 1 && r->seq == 0) || (shape->positions > 1 && r->row == 0) || (shape->kv_heads > 1 && r->head == 0))
             return MOE_ERR_INVALID_ARG;
-    const size_t need = window_attn_workspace_bytes(*shape);
+    const size_t need = kv_attn_workspace_bytes(shape->batch, shape->kv_heads, shape->q_heads / shape->kv_heads, shape->head_dim, shape->rows, 0);
     if (need && (!ws_dev || !aligned16(ws_dev))) return MOE_ERR_INVALID_ARG;
     if (ws_bytes < need) return MOE_ERR_BUFFER_TOO_SMALL;
     KvCall p = {};
@@ -1077,7 +1084,7 @@ int moe_window_attn(const moe_window *shape, const moe_rows *q, const moe_rows *
     p.f16 = q->type == MOE_F16;
     p.c = scale * 1.4426950408889634f;
     p.timeout_ns = g_timeout_ns;
-    return launch_window_attn(p, ws_dev, reinterpret_cast<cudaStream_t>(stream));
+    return launch_kv_attn(p, ws_dev, reinterpret_cast<cudaStream_t>(stream));
 }
 
 const char *moe_status_str(int status)

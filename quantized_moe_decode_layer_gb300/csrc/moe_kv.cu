@@ -39,8 +39,6 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kWarps = kThreads / 32;
 
 struct Once {
     std::once_flag flag[64];
@@ -80,6 +78,12 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
         asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 template <bool F16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi)
 {
@@ -107,20 +111,18 @@ __device__ __forceinline__ int visible(const KvCall &p, int p0, int n, int &lo, 
 }
 
 // The line of tiles: the prefix's (all of head 0's, then head 1's ...), then for
-// each sequence its heads' and row blocks'.
+// each sequence its heads'.
 struct Line {
-    int HN;             // problems of a sequence
-    int NP;             // problems of the prefix
+    int NP;             // problems of the prefix: its heads, or none
     int ptiles;         // tiles of one of them
     int total, share;   // tiles; tiles a CTA
 };
 __device__ __forceinline__ Line line_of(const KvCall &p, int seq_tiles, int ctas)
 {
     Line l;
-    l.HN = p.Hkv * p.NRB;
-    l.NP = p.Hkv * p.NRBP;
-    l.ptiles = p.NRBP ? (p.P + kKvTile - 1) / kKvTile : 0;
-    l.total = l.NP * l.ptiles + seq_tiles * l.HN;
+    l.NP = p.split_prefix ? p.Hkv : 0;
+    l.ptiles = p.split_prefix ? (p.P + kKvTile - 1) / kKvTile : 0;
+    l.total = l.NP * l.ptiles + seq_tiles * p.Hkv;
     l.share = max(p.min_tiles, (l.total + ctas - 1) / ctas);
     return l;
 }
@@ -132,38 +134,47 @@ struct Problem {
     int p0, cnt;    // first row's position, rows; the prefix: every row of the batch, all of it visible
     int tiles;
     int whole;      // the CTA has all its tiles: outputs are written at once
-    int b, row0;    // sequence (-1: the prefix), first of the block's rows
-    int g;
+    int b, g;       // sequence (-1: the prefix), head
 };
 
-template <int D, int WR>
+// A CTA: four groups of 16 of a tile's positions, times WD parts of the output's columns (the warps of every
+// column part take the scores of their positions themselves).  With 256 columns a warp's output takes 128
+// registers, so two warps share it.
+template <int D>
 struct Lay {
-    static constexpr int RB = 16 * WR;
+    static constexpr int WD = D == 256 ? 2 : 1;
+    static constexpr int WK = 4, KW = kKvTile / WK;        // position groups, positions of one
+    static constexpr int kThreads = 32 * WK * WD;
+    static constexpr int RB = kKvFewRows;
     static constexpr int kRow = D * 2;
-    static constexpr int kStage = 2 * kKvTile * kRow;      // keys, values
+    static constexpr int kUnit = kKvTile * kRow;           // keys or values of a tile
     static constexpr int kQ = RB * kRow;
-    static constexpr int NST = D == 64 ? (WR == 4 ? 3 : 4) : WR == 1 ? 3 : 2;
-    static constexpr int probs = NST * (kStage + kQ);
-    static constexpr int misc = probs + (NST + 1) * (int)sizeof(Problem);   // maxima and sums of the key groups
-    static constexpr int cum = misc + (2 * kWarps * 64 + 8) * 4;
-    static constexpr int total(int B) { return cum + (B + 1) * 4; }
     static constexpr int ctas = D == 256 ? 1 : D == 128 ? 2 : 3;
+    // units in the ring, and problems whose q is there: the one whose keys are waited for, and those that the NU - 1
+    // units ahead may have begun (q goes to registers with a problem's first keys)
+    static constexpr int NU = D == 64 ? 8 : 6, NQ = NU / 2;
+    static constexpr int q = NU * kUnit;
+    static constexpr int probs = q + NQ * kQ;
+    static constexpr int misc = probs + (NQ + 1) * (int)sizeof(Problem);   // maxima and sums of the position groups
+    static constexpr int cum = misc + (2 * WK * RB + 8) * 4;
+    static constexpr int total(int B) { return cum + (B + 1) * 4; }
 };
 
 // 16-byte chunk c of row r of a tile, swizzled so that eight rows' equal chunks lie in eight banks' groups.
 template <int D>
 __device__ __forceinline__ uint32_t at(int r, int c) { return (uint32_t)(r * (D * 2) + ((c ^ (r & 7)) << 4)); }
 
-template <bool F16, int D, int WR>
-__global__ void __launch_bounds__(kThreads, (Lay<D, WR>::ctas)) kv_split_kernel(const KvCall p)
+template <bool F16, int D>
+__global__ void __launch_bounds__(Lay<D>::kThreads, Lay<D>::ctas) kv_split_kernel(const KvCall p)
 {
-    using L = Lay<D, WR>;
-    constexpr int RB = L::RB, WK = kWarps / WR, KW = kKvTile / WK, NST = L::NST;
+    using L = Lay<D>;
+    constexpr int RB = L::RB, WK = L::WK, WD = L::WD, KW = L::KW, NU = L::NU, kThreads = L::kThreads;
+    constexpr int DW = D / WD;      // a warp's columns
     extern __shared__ __align__(128) uint8_t sm[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     Problem *probs = reinterpret_cast<Problem *>(sm + L::probs);
-    float *gm = reinterpret_cast<float *>(sm + L::misc), *gl = gm + kWarps * 64;
-    int *wsum = reinterpret_cast<int *>(gl + kWarps * 64);
+    float *gm = reinterpret_cast<float *>(sm + L::misc), *gl = gm + WK * RB;
+    int *wsum = reinterpret_cast<int *>(gl + WK * RB);
     int *cum = reinterpret_cast<int *>(sm + L::cum);
     after_previous();
 
@@ -200,19 +211,18 @@ __global__ void __launch_bounds__(kThreads, (Lay<D, WR>::ctas)) kv_split_kernel(
     if (t0 >= t1) return;
 
     // ------------------------------------------------------------- loading
-    // cursor of the loads: tile li of problem lp (registers), NST - 1 tiles ahead
+    // cursor of the loads: unit (keys, then values) of tile li of problem lp, NU - 1 units ahead
     Problem lp;
-    int li, lcount = -1;            // problems opened by this CTA, less one
+    int li, lcount = -1, lvalues = 0;   // lcount: problems opened by this CTA, less one
     const uint16_t *lk, *lv;
     long long lkm, lvm;
-    int lbase;                      // slot of position lo
+    int lbase;                          // slot of position lo
 
     auto open = [&](int id, int i) {
         lp.id = id;
         if (id < ln.NP) {
             lp.b = -1;
-            lp.g = id / p.NRBP;
-            lp.row0 = (id - lp.g * p.NRBP) * RB;
+            lp.g = id;
             lp.n = p.P;
             lp.ns = lp.lo = 0;
             lp.p0 = INT_MAX;
@@ -223,11 +233,10 @@ __global__ void __launch_bounds__(kThreads, (Lay<D, WR>::ctas)) kv_split_kernel(
             lvm = p.pvm;
             lbase = 0;
         } else {
-            const int x = id - ln.NP, b = x / ln.HN, j = x - b * ln.HN;
+            const int x = id - ln.NP, b = x / p.Hkv;
             bool bad;
             lp.b = b;
-            lp.g = j / p.NRB;
-            lp.row0 = (j - lp.g * p.NRB) * RB;
+            lp.g = x - b * p.Hkv;
             lp.cnt = rows_of(p, b, lp.p0, bad);
             lp.n = visible(p, lp.p0, lp.cnt, lp.lo, lp.ns);
             lk = p.k + b * p.kb + lp.g * p.kh;
@@ -238,56 +247,60 @@ __global__ void __launch_bounds__(kThreads, (Lay<D, WR>::ctas)) kv_split_kernel(
         }
         lp.tiles = (lp.n + kKvTile - 1) / kKvTile;
         li = i;
-        const int mine = t1 - t0;   // tiles of the CTA; from here on at most so many
-        lp.whole = i == 0 && lp.tiles <= mine;
+        lp.whole = i == 0 && lp.tiles <= t1 - t0;
         ++lcount;
-        // its rows of q beside the stage of its first tile
+        // its rows of q (those of idle sequences and padding are loaded like the others; nothing of them is used)
         constexpr int CH = D / 8;
-        uint8_t *qs = sm + NST * L::kStage + (lcount % NST) * L::kQ;
+        uint8_t *qs = sm + L::q + (lcount % L::NQ) * L::kQ;
+        const int R = lp.b < 0 ? p.B * p.M * p.G : p.M * p.G;
         for (int x = tid; x < RB * CH; x += kThreads) {
             const int r = x / CH, c = x % CH;
-            int row = lp.row0 + r, b = lp.b;
-            bool ok;
+            int m = p.by_g(r), b = lp.b;
+            const int h = r - m * p.G;
             if (b < 0) {
-                b = row / (p.M * p.G);
-                row -= b * p.M * p.G;
-                ok = b < p.B;
-            } else {
-                ok = row < p.M * p.G;
+                b = m / p.M;
+                m -= b * p.M;
             }
-            const int m = row / p.G, h = row - m * p.G;
-            if (lp.b < 0 && ok) {
-                int q0;
-                bool bad;
-                ok = m < rows_of(p, b, q0, bad);
-            } else {
-                ok = ok && m < lp.cnt;
-            }
+            const bool ok = r < R;
             const uint16_t *src = ok ? p.q + b * p.qb + m * p.qm + (long long)(lp.g * p.G + h) * p.qh + 8 * c : p.q;
             cp16(su32(qs) + at<D>(r, c), src, ok);
         }
     };
-    auto load = [&](int stage) {
+    auto load = [&](int slot_of_ring) {
         constexpr int CH = D / 8, RPI = kThreads / CH;
-        const uint32_t ks = su32(sm + stage * L::kStage), vs = ks + kKvTile * L::kRow;
-        const int c = tid % CH;
+        const uint32_t to = su32(sm + slot_of_ring * L::kUnit);
+        const uint16_t *src = lvalues ? lv : lk;
+        const long long step = lvalues ? lvm : lkm;
+        static_assert(RPI % 8 == 0, "a thread's rows have one swizzle");
+        const int c = tid % CH, r0 = tid / CH, v0 = li * kKvTile;
+        const uint32_t dst = to + at<D>(r0, c);
+        int first = lbase + v0 - lp.ns;     // slot of the tile's first position, where it is not among the first S
+        if (lp.b >= 0 && first >= p.T) first -= p.T - p.S;
+        if (v0 >= lp.ns && v0 + kKvTile <= lp.n && (lp.b < 0 || first + kKvTile <= p.T)) {   // 64 slots in a row
+            const uint16_t *from = src + (first + r0) * step + 8 * c;
 #pragma unroll
-        for (int r0 = 0; r0 < kKvTile; r0 += RPI) {
-            const int r = r0 + tid / CH, v = li * kKvTile + r;
+            for (int i = 0; i < kKvTile / RPI; ++i) {
+                cp16(dst + (uint32_t)(i * RPI * L::kRow), from, true);
+                from += RPI * step;
+            }
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < kKvTile / RPI; ++i) {
+            const int v = v0 + r0 + i * RPI;
             int slot = v;
             if (v >= lp.ns) {
                 slot = lbase + (v - lp.ns);
                 if (lp.b >= 0 && slot >= p.T) slot -= p.T - p.S;
             }
-            const bool ok = v < lp.n;
+            const bool ok = v < lp.n;   // behind the last: zeros
             if (!ok) slot = 0;
-            cp16(ks + at<D>(r, c), lk + slot * lkm + 8 * c, ok);
-            cp16(vs + at<D>(r, c), lv + slot * lvm + 8 * c, ok);
+            cp16(dst + (uint32_t)(i * RPI * L::kRow), src + slot * step + 8 * c, ok);
         }
     };
 
     // the problem and tile that t0 falls on
-    int left = t1 - t0;   // tiles not yet loaded
+    int left = t1 - t0;   // tiles whose values are not yet loaded
     {
         int id, i;
         const int pt = ln.NP * ln.ptiles;
@@ -296,106 +309,103 @@ __global__ void __launch_bounds__(kThreads, (Lay<D, WR>::ctas)) kv_split_kernel(
             i = t0 - id * ln.ptiles;
         } else {
             const int x = t0 - pt;
-            int lo = 0, hi = p.B - 1;   // the last b with cum[b] HN <= x and tiles of its own
+            int lo = 0, hi = p.B - 1;   // the last b with cum[b] heads <= x: it has tiles
             while (lo < hi) {
                 const int mid = (lo + hi + 1) >> 1;
-                if (cum[mid] * ln.HN <= x) lo = mid;
+                if (cum[mid] * p.Hkv <= x) lo = mid;
                 else hi = mid - 1;
             }
-            const int each = cum[lo + 1] - cum[lo], y = x - cum[lo] * ln.HN, j = y / each;
-            id = ln.NP + lo * ln.HN + j;
+            const int each = cum[lo + 1] - cum[lo], y = x - cum[lo] * p.Hkv, j = y / each;
+            id = ln.NP + lo * p.Hkv + j;
             i = y - j * each;
         }
         open(id, i);
         if (tid == 0) probs[0] = lp;
     }
-    // the next tile of the line; false at the CTA's end
-    auto advance = [&]() -> bool {
-        if (--left == 0) return false;
-        if (++li < lp.tiles) return true;
-        const int rest = left;
-        int id = lp.id + 1;
-        if (id >= ln.NP)
-            while (cum[(id - ln.NP) / ln.HN + 1] == cum[(id - ln.NP) / ln.HN]) ++id;   // a sequence without tiles (there is one with tiles behind it)
-        open(id, 0);
-        lp.whole = lp.tiles <= rest;
-        if (tid == 0) probs[lcount % (NST + 1)] = lp;
-        return true;
-    };
-
-    bool more = true;
-    load(0);
-    cp_commit();
-#pragma unroll 1
-    for (int s = 1; s < NST - 1; ++s) {
-        if (more) more = advance();
-        if (more) load(s);
+    // the next unit of the line into the ring
+    auto next = [&](int slot_of_ring) {
+        if (left > 0) {
+            if (li == lp.tiles) {
+                int id = lp.id + 1;
+                if (id >= ln.NP)
+                    while (cum[(id - ln.NP) / p.Hkv + 1] == cum[(id - ln.NP) / p.Hkv]) ++id;   // sequences without tiles (some with are behind)
+                open(id, 0);
+                lp.whole = lp.tiles <= left;
+                if (tid == 0) probs[lcount % (L::NQ + 1)] = lp;
+            }
+            load(slot_of_ring);
+            lvalues ^= 1;
+            if (lvalues == 0) {
+                --left;
+                ++li;
+            }
+        }
         cp_commit();
-    }
+    };
+#pragma unroll 1
+    for (int u = 0; u < NU - 1; ++u) next(u);
 
     // ----------------------------------------------------------- computing
-    const int wr = warp % WR, wk = warp / WR;
-    const int rA = wr * 16 + (lane >> 2);          // this thread's rows: rA, rA + 8
-    float acc[D / 8][4];
+    const int wd = warp % WD, wk = warp / WD;
+    const int rA = lane >> 2;                      // this thread's rows: rA, rA + 8
+    const int key0 = wk * KW;
+    uint32_t qf[D / 16][4];                        // the rows of q, as operands
+    float acc[DW / 8][4];
     float mrun[2], lrun[2];
     int lowA = 0, highA = 0, lowB = 0, highB = 0;  // positions rows see: low < t <= high, or t < S
     Problem cp;
-    int ci = -1, ccount = -1;
+    int ci = -1, ccount = -1, slot = 0;
     const int ntiles = t1 - t0;
 
 #pragma unroll 1
     for (int it = 0; it < ntiles; ++it) {
-        const int stage = it % NST;
-        cp_wait<NST - 2>();
+        cp_wait<NU - 2>();
         __syncthreads();
-        {
-            const int s = (it + NST - 1) % NST;
-            if (more) more = advance();
-            if (more) load(s);
-            cp_commit();
-        }
+        next(slot == 0 ? NU - 1 : slot - 1);
         if (ci < 0 || ++ci == cp.tiles) {
             ++ccount;
-            cp = probs[ccount % (NST + 1)];
+            cp = probs[ccount % (L::NQ + 1)];
             if (ci < 0) {
                 // the CTA's first: where in the problem it starts
                 const int pt = ln.NP * ln.ptiles;
                 if (cp.b < 0) ci = t0 - cp.id * ln.ptiles;
-                else ci = (t0 - pt - cum[cp.b] * ln.HN) % cp.tiles;
+                else ci = (t0 - pt - cum[cp.b] * p.Hkv) % cp.tiles;
             } else {
                 ci = 0;
             }
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+            for (int i = 0; i < DW / 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
             mrun[0] = mrun[1] = -INFINITY;
             lrun[0] = lrun[1] = 0.f;
             auto limits = [&](int r, int &low, int &high) {
-                const int m = (cp.row0 + r) / p.G;
+                const int m = p.by_g(r);
                 high = cp.b < 0 ? INT_MAX : m < cp.cnt ? cp.p0 + m : -1;
                 low = cp.b < 0 || m >= cp.cnt ? -1 : cp.p0 + m - p.W;
             };
             limits(rA, lowA, highA);
             limits(rA + 8, lowB, highB);
+            const uint32_t qs = su32(sm + L::q + (ccount % L::NQ) * L::kQ);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) ldsm(qf[kk], qs + at<D>(lane & 15, 2 * kk + (lane >> 4)));
         }
-        const uint32_t ks = su32(sm + stage * L::kStage), vs = ks + kKvTile * L::kRow;
-        const uint32_t qs = su32(sm + NST * L::kStage + (ccount % NST) * L::kQ);
-        const int key0 = wk * KW;
 
         // scores
         float s[KW / 8][4];
+        {
+            const uint32_t ks = su32(sm + slot * L::kUnit);
 #pragma unroll
-        for (int j = 0; j < KW / 8; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
+            for (int j = 0; j < KW / 8; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-            uint32_t a[4], b[4];
-            ldsm(a, qs + at<D>(wr * 16 + (lane & 15), 2 * kk + (lane >> 4)));
+            for (int kk = 0; kk < D / 16; ++kk)
 #pragma unroll
-            for (int j = 0; j < KW / 16; ++j) {
-                ldsm(b, ks + at<D>(key0 + 16 * j + (lane & 7) + ((lane >> 4) << 3), 2 * kk + ((lane >> 3) & 1)));
-                mma<F16>(s[2 * j], a, b[0], b[1]);
-                mma<F16>(s[2 * j + 1], a, b[2], b[3]);
-            }
+                for (int j = 0; j < KW / 16; ++j) {
+                    uint32_t b[4];
+                    ldsm(b, ks + at<D>(key0 + 16 * j + (lane & 7) + ((lane >> 4) << 3), 2 * kk + ((lane >> 3) & 1)));
+                    mma<F16>(s[2 * j], qf[kk], b[0], b[1]);
+                    mma<F16>(s[2 * j + 1], qf[kk], b[2], b[3]);
+                }
         }
+        if (++slot == NU) slot = 0;
         // in units of log2; positions that a row does not see
         const int v0 = ci * kKvTile + key0 + 2 * (lane & 3);
         const int first = ci * kKvTile, last = min(first + kKvTile, cp.n) - 1;
@@ -436,12 +446,12 @@ __global__ void __launch_bounds__(kThreads, (Lay<D, WR>::ctas)) kv_split_kernel(
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 const float mn = fmaxf(mrun[x], mx[x]);
-                al[x] = mrun[x] == mn ? 1.f : exp2f(mrun[x] - mn);
+                al[x] = mrun[x] == mn ? 1.f : ex2(mrun[x] - mn);
                 mrun[x] = mn;
                 lrun[x] *= al[x];
             }
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i) {
+            for (int i = 0; i < DW / 8; ++i) {
                 acc[i][0] *= al[0];
                 acc[i][1] *= al[0];
                 acc[i][2] *= al[1];
@@ -449,60 +459,89 @@ __global__ void __launch_bounds__(kThreads, (Lay<D, WR>::ctas)) kv_split_kernel(
             }
         }
         const float ref[2] = {mrun[0] == -INFINITY ? 0.f : mrun[0], mrun[1] == -INFINITY ? 0.f : mrun[1]};
+        uint32_t w16[KW / 8][2];
 #pragma unroll
-        for (int j = 0; j < KW / 8; ++j)
+        for (int j = 0; j < KW / 8; ++j) {
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-                s[j][x] = exp2f(s[j][x] - ref[x >> 1]);
+                s[j][x] = ex2(s[j][x] - ref[x >> 1]);
                 lrun[x >> 1] += s[j][x];
             }
+            w16[j][0] = pack2<F16>(s[j][0], s[j][1]);
+            w16[j][1] = pack2<F16>(s[j][2], s[j][3]);
+        }
         // weighted values
+        cp_wait<NU - 2>();
+        __syncthreads();
+        next(slot == 0 ? NU - 1 : slot - 1);
+        const uint32_t vs = su32(sm + slot * L::kUnit);
 #pragma unroll
         for (int j = 0; j < KW / 16; ++j) {
-            const uint32_t a[4] = {pack2<F16>(s[2 * j][0], s[2 * j][1]), pack2<F16>(s[2 * j][2], s[2 * j][3]),
-                                   pack2<F16>(s[2 * j + 1][0], s[2 * j + 1][1]), pack2<F16>(s[2 * j + 1][2], s[2 * j + 1][3])};
+            const uint32_t a[4] = {w16[2 * j][0], w16[2 * j][1], w16[2 * j + 1][0], w16[2 * j + 1][1]};
 #pragma unroll
-            for (int dd = 0; dd < D / 16; ++dd) {
+            for (int dd = 0; dd < DW / 16; ++dd) {
                 uint32_t b[4];
-                ldsm_t(b, vs + at<D>(key0 + 16 * j + (lane & 15), 2 * dd + (lane >> 4)));
+                ldsm_t(b, vs + at<D>(key0 + 16 * j + (lane & 15), wd * (DW / 8) + 2 * dd + (lane >> 4)));
                 mma<F16>(acc[2 * dd], a, b[0], b[1]);
                 mma<F16>(acc[2 * dd + 1], a, b[2], b[3]);
             }
         }
+        const int used = slot;
+        if (++slot == NU) slot = 0;
         if (ci + 1 < cp.tiles && it + 1 < ntiles) continue;
 
         // ---------------------------------------- the problem's or CTA's end
-        // The key groups' outputs are joined in the stage that was just read
-        // (its next load comes after the next barrier).
 #pragma unroll
         for (int o = 1; o < 4; o <<= 1) {
             lrun[0] += __shfl_xor_sync(0xFFFFFFFFu, lrun[0], o);
             lrun[1] += __shfl_xor_sync(0xFFFFFFFFu, lrun[1], o);
         }
-        if ((lane & 3) == 0) {
+        const bool direct = cp.whole && p.P == 0;
+        const int R = cp.b < 0 ? p.B * p.M * p.G : p.M * p.G;
+        const size_t part = ((size_t)blockIdx.x + cp.id) * RB;
+        // n columns from c on of the block's row r
+        auto put = [&](int r, int c, const float *v, int n, float m, float l) {
+            if (r >= R) return;
+            if (direct) {
+                const int mm = p.by_g(r), h = r - mm * p.G;
+                const float f = mm < cp.cnt && l != 0.f ? 1.f / l : 0.f;
+                uint32_t *to = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.o) +
+                                                            (((size_t)cp.b * p.M + mm) * p.Hq + cp.g * p.G + h) * D + c);
+                for (int i = 0; i < n; i += 2) to[i / 2] = mm < cp.cnt ? pack2<F16>(v[i] * f, v[i + 1] * f) : 0u;
+            } else {
+                float *to = p.part_o + (part + r) * D + c;
+                for (int i = 0; i < n; i += 2) *reinterpret_cast<float2 *>(to + i) = make_float2(v[i], v[i + 1]);
+                if (c == 0) *reinterpret_cast<float2 *>(p.part_ml + (part + r) * 2) = make_float2(m, l);
+            }
+        };
+        // The position groups' outputs are joined in the unit that was just read (its next load comes after the
+        // next barrier).
+        if ((lane & 3) == 0 && wd == 0) {
             gm[wk * RB + rA] = mrun[0];
             gm[wk * RB + rA + 8] = mrun[1];
             gl[wk * RB + rA] = lrun[0];
             gl[wk * RB + rA + 8] = lrun[1];
         }
         __syncthreads();
-        float *out = reinterpret_cast<float *>(sm + stage * L::kStage);   // [RB][D]
+        float *out = reinterpret_cast<float *>(sm + used * L::kUnit);   // [RB][D]
+        static_assert(RB * D * 4 <= L::kUnit, "outputs in a unit");
         float w[2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             float m = gm[rA + 8 * x];
             for (int k = 1; k < WK; ++k) m = fmaxf(m, gm[k * RB + rA + 8 * x]);
-            w[x] = mrun[x] == -INFINITY ? 0.f : exp2f(mrun[x] - m);
+            w[x] = mrun[x] == -INFINITY ? 0.f : ex2(mrun[x] - m);
         }
 #pragma unroll 1
         for (int k = 0; k < WK; ++k) {
             if (wk == k) {
 #pragma unroll
-                for (int i = 0; i < D / 8; ++i)
+                for (int i = 0; i < DW / 8; ++i)
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         // columns in an order that spreads a warp's rows over the banks
-                        float2 *to = reinterpret_cast<float2 *>(out + (rA + 8 * x) * D + ((8 * i + 2 * (lane & 3)) ^ (8 * ((rA + 8 * x) & 3))));
+                        const int r = rA + 8 * x, c = wd * DW + 8 * i + 2 * (lane & 3);
+                        float2 *to = reinterpret_cast<float2 *>(out + r * D + (c ^ (8 * (r & 3))));
                         float2 v = make_float2(acc[i][2 * x] * w[x], acc[i][2 * x + 1] * w[x]);
                         if (k > 0) {
                             const float2 was = *to;
@@ -514,34 +553,18 @@ __global__ void __launch_bounds__(kThreads, (Lay<D, WR>::ctas)) kv_split_kernel(
             }
             __syncthreads();
         }
-        const bool direct = cp.whole && p.P == 0;
-        const int R = cp.b < 0 ? p.B * p.M * p.G : p.M * p.G;
-        const size_t slot = (size_t)blockIdx.x + cp.id;
         constexpr int C4 = D / 4;
         for (int x = tid; x < RB * C4; x += kThreads) {
-            const int r = x / C4, c = 4 * (x % C4), row = cp.row0 + r;
-            if (row >= R) break;
-            float m = gm[r], l = gl[r];
-            if (WK > 1) {
-                for (int k = 1; k < WK; ++k) m = fmaxf(m, gm[k * RB + r]);
-                l = 0.f;
-                for (int k = 0; k < WK; ++k) {
-                    const float mk = gm[k * RB + r];
-                    l += mk == -INFINITY ? 0.f : gl[k * RB + r] * exp2f(mk - m);
-                }
+            const int r = x / C4, c = 4 * (x % C4);
+            float m = gm[r], l = 0.f;
+            for (int k = 1; k < WK; ++k) m = fmaxf(m, gm[k * RB + r]);
+            for (int k = 0; k < WK; ++k) {
+                const float mk = gm[k * RB + r];
+                l += mk == -INFINITY ? 0.f : gl[k * RB + r] * ex2(mk - m);
             }
             const float4 v = *reinterpret_cast<const float4 *>(out + r * D + (c ^ (8 * (r & 3))));
-            if (direct) {
-                const int mm = row / p.G, h = row - mm * p.G;
-                const float f = mm < cp.cnt && l != 0.f ? 1.f / l : 0.f;
-                uint2 u = make_uint2(0u, 0u);
-                if (mm < cp.cnt) u = make_uint2(pack2<F16>(v.x * f, v.y * f), pack2<F16>(v.z * f, v.w * f));
-                *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.o) +
-                                           (((size_t)cp.b * p.M + mm) * p.Hq + cp.g * p.G + h) * D + c) = u;
-            } else {
-                *reinterpret_cast<float4 *>(p.part_o + (slot * RB + r) * D + c) = v;
-                if (c == 0) *reinterpret_cast<float2 *>(p.part_ml + (slot * RB + r) * 2) = make_float2(m, l);
-            }
+            const float u[4] = {v.x, v.y, v.z, v.w};
+            put(r, c, u, 4, m, l);
         }
     }
 }
@@ -567,37 +590,36 @@ __global__ void __launch_bounds__(32 * kMergeWarps) kv_merge_kernel(const KvCall
         for (int d = tid; d < D; d += 32 * kMergeWarps) o[d] = 0;
         return;
     }
-    // the sequence's own parts, of the split kernel: slots first .. first + n1 - 1
-    const int prow = (b * p.M + m) * p.G + h;
+    // parts of the own positions, then of the prefix's: of the tile kernel, or slots of the split kernel
+    const int row = (b * p.M + m) * p.G + h;
+    const size_t rows = (size_t)p.B * p.M * p.G;
     size_t first = 0, pfirst = 0;
-    int n1 = 0, n2 = p.nsplit, r1 = 0, r2 = 0;
-    if (p.NRB) {
+    int n1 = p.own.n, n2 = p.prefix.n;
+    if (p.split_own) {
         const Line ln = line_of(p, p.cum[p.B], ctas);
-        const int row = m * p.G + h, rb = row / p.RB, each = p.cum[b + 1] - p.cum[b];
-        const int j = g * p.NRB + rb, T0 = ln.NP * ln.ptiles + p.cum[b] * ln.HN + j * each;
-        const int c0 = T0 / ln.share;
+        const int each = p.cum[b + 1] - p.cum[b], j = b * p.Hkv + g;
+        const int T0 = ln.NP * ln.ptiles + p.cum[b] * p.Hkv + g * each, c0 = T0 / ln.share;
         n1 = (T0 + each - 1) / ln.share - c0 + 1;
         if (n1 == 1 && p.P == 0) return;   // written by the split kernel
-        first = (size_t)c0 + ln.NP + b * ln.HN + j;
-        r1 = row - rb * p.RB;
-        // the prefix's, of the same kernel (or, nsplit of them, of the tile kernel)
-        if (p.NRBP) {
-            const int rbp = prow / p.RB, id = g * p.NRBP + rbp, q0 = id * ln.ptiles, a = q0 / ln.share;
+        first = ((size_t)c0 + ln.NP + j) * kKvFewRows + m * p.G + h;
+        if (p.split_prefix) {
+            const int q0 = g * ln.ptiles, a = q0 / ln.share;
             n2 = (q0 + ln.ptiles - 1) / ln.share - a + 1;
-            pfirst = (size_t)a + id;
-            r2 = prow - rbp * p.RB;
+            pfirst = ((size_t)a + g) * kKvFewRows + row;
         }
     }
-    const size_t rows = (size_t)p.B * p.M * p.G;
     auto part = [&](int i, const float *&po) -> const float * {
-        if (i >= n1 && p.NRBP == 0) {
-            const size_t x = ((size_t)(i - n1) * p.Hkv + g) * rows + prow;
-            po = p.tile_o + x * D;
-            return p.tile_ml + x * 2;
+        const bool own = i < n1;
+        if (!own) i -= n1;
+        if (own ? p.split_own : p.split_prefix) {
+            const size_t x = (own ? first : pfirst) + (size_t)i * kKvFewRows;
+            po = p.part_o + x * D;
+            return p.part_ml + x * 2;
         }
-        const size_t x = i < n1 ? (first + i) * p.RB + r1 : (pfirst + i - n1) * p.RB + r2;
-        po = p.part_o + x * D;
-        return p.part_ml + x * 2;
+        const KvCall::Parts &t = own ? p.own : p.prefix;
+        const size_t x = ((size_t)i * p.Hkv + g) * rows + row;
+        po = t.o + x * D;
+        return t.ml + x * 2;
     };
     const int n = n1 + n2;
     float mx = -INFINITY;
@@ -618,7 +640,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) kv_merge_kernel(const KvCall
         const float *po, *ml = part(i, po);
         const float2 x = __ldcg(reinterpret_cast<const float2 *>(ml));
         if (x.x == -INFINITY) continue;   // an empty part: its output was not written
-        const float w = exp2f(x.x - mx);
+        const float w = ex2(x.x - mx);
         l = fmaf(x.y, w, l);
 #pragma unroll
         for (int v = 0; v < VEC / 2; ++v) {
@@ -734,43 +756,43 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const AppendCall p)
     }
 }
 
-int row_block(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
-
 struct KvWs {
-    size_t cum, ml, o, tml, to, total;
+    size_t cum, ml, o, own_ml, own_o, pre_ml, pre_o, total;
+    long long own_ctas, pre_ctas;   // row tiles of the tile kernel (0: the split kernel's)
+    int own_most, pre_most;         // their positions' parts at most
 };
 
-// Rows of the batch from which on the prefix goes through the tile kernel.
-constexpr int kTileRows = 64;
-
-KvWs kv_ws(int B, int Hkv, int G, int D, int M, int P)
+KvWs kv_ws(int B, int Hkv, int G, int D, long long M, int P)
 {
-    KvWs w;
-    const int rows = M * G, prows = B * rows;
-    const bool tiles = P > 0 && prows > kTileRows;
-    const int RB = row_block(P > 0 && !tiles ? prows : rows);
-    const size_t nprob = (size_t)B * Hkv * ((rows + RB - 1) / RB) + (P > 0 && !tiles ? (size_t)Hkv * ((prows + RB - 1) / RB) : 0);
-    const size_t slots = nprob + kKvMaxCtas, ns = tiles ? kv_tile_most(kv_row_tiles(prows, D) * Hkv) : 0;
+    KvWs w = {};
+    const long long rows = M * G, prows = B * rows;
+    const bool split_own = rows <= kKvFewRows, split_pre = P > 0 && prows <= kKvFewRows;
+    const size_t slots = split_own ? (size_t)B * Hkv + (split_pre ? Hkv : 0) + kKvMaxCtas : 0;
+    if (!split_own) {
+        w.own_ctas = kv_row_tiles(rows, D) * Hkv * B;
+        w.own_most = kv_tile_most(w.own_ctas);
+    }
+    if (P > 0 && !split_pre) {
+        w.pre_ctas = kv_row_tiles(prows, D) * Hkv;
+        w.pre_most = kv_tile_most(w.pre_ctas);
+    }
+    const size_t own = w.own_most > 1 || P > 0 ? (size_t)w.own_most * Hkv * prows : 0, pre = (size_t)w.pre_most * Hkv * prows;
     w.cum = 0;
-    w.ml = align_up(((size_t)B + 1) * 4, 256);
-    w.o = align_up(w.ml + slots * RB * 8, 256);
-    w.tml = align_up(w.o + slots * RB * D * 4, 256);
-    w.to = align_up(w.tml + ns * Hkv * prows * 8, 256);
-    w.total = align_up(w.to + ns * Hkv * prows * D * 4, 256);
+    w.ml = split_own ? align_up(((size_t)B + 1) * 4, 256) : 0;
+    w.o = align_up(w.ml + slots * kKvFewRows * 8, 256);
+    w.own_ml = align_up(w.o + slots * kKvFewRows * D * 4, 256);
+    w.own_o = align_up(w.own_ml + own * 8, 256);
+    w.pre_ml = align_up(w.own_o + own * D * 4, 256);
+    w.pre_o = align_up(w.pre_ml + pre * 8, 256);
+    w.total = align_up(w.pre_o + pre * D * 4, 256);
     return w;
 }
 
 }  // namespace
 
-// For every call of up to M rows, with a prefix or without.
-size_t kv_attn_workspace_bytes(int batch, int kv_heads, int group, int head_dim, int M, int max_prefix, bool exact)
+size_t kv_attn_workspace_bytes(int batch, int kv_heads, int group, int head_dim, long long M, int P)
 {
-    size_t most = 0;
-    for (int m = exact ? M : 1; m <= M; ++m) {
-        most = std::max(most, kv_ws(batch, kv_heads, group, head_dim, m, max_prefix).total);
-        if (!exact) most = std::max(most, kv_ws(batch, kv_heads, group, head_dim, m, 0).total);
-    }
-    return most;
+    return kv_ws(batch, kv_heads, group, head_dim, M, P).total;
 }
 
 int launch_kv_append(const moe_kv &c, const moe_rows &k_new, const moe_rows &v_new, int M, const int32_t *pos,
@@ -815,117 +837,77 @@ int launch_kv_append(const moe_kv &c, const moe_rows &k_new, const moe_rows &v_n
     return MOE_OK;
 }
 
-static int launch_merge(const KvCall &p, int ctas, cudaStream_t stream)
-{
-    auto *merge = p.D == 256 ? kv_merge_kernel<256> : p.D == 128 ? kv_merge_kernel<128> : kv_merge_kernel<64>;
-    const long long grid = (long long)p.B * p.M * p.Hq;
-    if (grid > INT_MAX) return MOE_ERR_UNSUPPORTED;
-    const cudaError_t e = launch_after(merge, dim3((unsigned)grid), 32 * kMergeWarps, 0, 0, stream, p, ctas);
-    if (e != cudaSuccess) { note_cuda_error((int)e); return MOE_ERR_CUDA; }
-    note_launch();
-    return MOE_OK;
-}
-
-// p: q, k, v, the prefix, lengths, shapes, scale and output; the rest is set here.
 int launch_kv_attn(KvCall &p, void *ws, cudaStream_t stream)
 {
-    const int rows = p.M * p.G, prows = p.B * rows;
-    const bool tiles = p.P > 0 && prows > kTileRows;
     const KvWs w = kv_ws(p.B, p.Hkv, p.G, p.D, p.M, p.P);
     uint8_t *base = static_cast<uint8_t *>(ws);
-    p.RB = row_block(p.P > 0 && !tiles ? prows : rows);
-    p.NRB = (rows + p.RB - 1) / p.RB;
-    p.NRBP = p.P > 0 && !tiles ? (prows + p.RB - 1) / p.RB : 0;
+    auto f = [&](size_t at) { return reinterpret_cast<float *>(base + at); };
+    p.split_own = w.own_ctas == 0;
+    p.split_prefix = p.P > 0 && w.pre_ctas == 0;
     p.min_tiles = 1;
     p.cum = reinterpret_cast<int *>(base + w.cum);
-    p.part_ml = reinterpret_cast<float *>(base + w.ml);
-    p.part_o = reinterpret_cast<float *>(base + w.o);
-    p.tile_ml = reinterpret_cast<float *>(base + w.tml);
-    p.tile_o = reinterpret_cast<float *>(base + w.to);
-    p.nsplit = 0;
-    if (tiles) {
-        p.nsplit = kv_tile_splits(kv_row_tiles(prows, p.D) * p.Hkv, (p.P + 127) / 128);
+    p.part_ml = f(w.ml);
+    p.part_o = f(w.o);
+    p.own = {0, f(w.own_o), f(w.own_ml)};
+    p.prefix = {0, f(w.pre_o), f(w.pre_ml)};
+    const long long merged = (long long)p.B * p.M * p.Hq;
+    // positions that a row tile sees at most
+    const long long seen = std::min<long long>((long long)p.W + p.S + 256 / p.G + 1, p.T);
+    if (w.pre_ctas) {
+        p.prefix.n = kv_tile_splits(w.pre_ctas, (p.P + 127) / 128);
         const int rc = launch_kv_tiles(p, true, stream);
         if (rc) return rc;
     }
-    // the line's length has to fit an int
-    const long long seen = std::min<long long>((long long)p.S + p.W + p.M, (long long)p.T);
-    const long long most = (seen / kKvTile + 2) * p.B * p.Hkv * p.NRB + ((long long)p.P / kKvTile + 1) * p.Hkv * p.NRBP;
-    if (most > INT_MAX / 2) return MOE_ERR_UNSUPPORTED;
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess || dev < 0 || dev >= 64) { note_cuda_error((int)e); return MOE_ERR_CUDA; }
-    int grid = 0;
-    auto go = [&](auto kernel, int smem, int ctas, Once &once) {
-        std::call_once(once.flag[dev], [&] {
-            e = cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
-            if (e == cudaSuccess)
-                e = cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                         (int)cudaSharedmemCarveoutMaxShared);
-            if (e == cudaSuccess) e = cudaDeviceGetAttribute(&once.sms[dev], cudaDevAttrMultiProcessorCount, dev);
-        });
-        if (e == cudaSuccess && once.sms[dev] < 1) e = cudaErrorInvalidDevice;
-        if (e != cudaSuccess) return;
-        grid = (int)std::min<long long>(most, (long long)std::min(once.sms[dev], kMaxCtas) * ctas);
-        e = launch_after(kernel, dim3(grid), kThreads, smem, 0, stream, p);
-    };
-#define KV_GO(F, D, W)                                                                            \
-    do {                                                                                          \
-        static Once once;                                                                         \
-        static_assert(Lay<D, W>::total(MOE_KV8_MAX_BATCH) <= kSmemMax, "shared memory");          \
-        go(kv_split_kernel<F, D, W>, Lay<D, W>::total(p.B), Lay<D, W>::ctas, once);               \
+    int grid = 1;
+    if (w.own_ctas) {
+        p.own.n = w.own_most == 1 ? 1 : kv_tile_splits(w.own_ctas, (seen + 127) / 128);
+        const int rc = launch_kv_tiles(p, false, stream);
+        if (rc || (p.own.n == 1 && p.P == 0)) return rc;
+    } else {
+        // the line's length has to fit an int
+        const long long most = (seen / kKvTile + 2) * p.B * p.Hkv + (p.split_prefix ? ((long long)p.P / kKvTile + 1) * p.Hkv : 0);
+        if (most > INT_MAX / 2) return MOE_ERR_UNSUPPORTED;
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess || dev < 0 || dev >= 64) { note_cuda_error((int)e); return MOE_ERR_CUDA; }
+        auto go = [&](auto kernel, int smem, int threads, int ctas, Once &once) {
+            std::call_once(once.flag[dev], [&] {
+                e = cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+                if (e == cudaSuccess)
+                    e = cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                             (int)cudaSharedmemCarveoutMaxShared);
+                if (e == cudaSuccess) e = cudaDeviceGetAttribute(&once.sms[dev], cudaDevAttrMultiProcessorCount, dev);
+            });
+            if (e == cudaSuccess && once.sms[dev] < 1) e = cudaErrorInvalidDevice;
+            if (e != cudaSuccess) return;
+            grid = (int)std::min<long long>(most, (long long)std::min(once.sms[dev], kMaxCtas) * ctas);
+            e = launch_after(kernel, dim3(grid), threads, smem, 0, stream, p);
+        };
+#define KV_GO(F, D)                                                                         \
+    do {                                                                                    \
+        static Once once;                                                                   \
+        static_assert(Lay<D>::total(MOE_KV_MAX_BATCH) <= kSmemMax, "shared memory");        \
+        go(kv_split_kernel<F, D>, Lay<D>::total(p.B), Lay<D>::kThreads, Lay<D>::ctas, once); \
     } while (0)
-#define KV_GO_D(F, D)                  \
-    do {                               \
-        if (p.RB == 16) KV_GO(F, D, 1); \
-        else if (p.RB == 32) KV_GO(F, D, 2); \
-        else KV_GO(F, D, 4);           \
+#define KV_GO_F(F)                        \
+    do {                                  \
+        if (p.D == 256) KV_GO(F, 256);    \
+        else if (p.D == 128) KV_GO(F, 128); \
+        else KV_GO(F, 64);                \
     } while (0)
-#define KV_GO_F(F)                                 \
-    do {                                           \
-        if (p.D == 256) KV_GO_D(F, 256);           \
-        else if (p.D == 128) KV_GO_D(F, 128);      \
-        else KV_GO_D(F, 64);                       \
-    } while (0)
-    if (p.f16) KV_GO_F(true);
-    else KV_GO_F(false);
+        if (p.f16) KV_GO_F(true);
+        else KV_GO_F(false);
 #undef KV_GO_F
-#undef KV_GO_D
 #undef KV_GO
+        if (e != cudaSuccess) { note_cuda_error((int)e); return MOE_ERR_CUDA; }
+        note_launch();
+    }
+    if (merged > INT_MAX) return MOE_ERR_UNSUPPORTED;
+    auto *merge = p.D == 256 ? kv_merge_kernel<256> : p.D == 128 ? kv_merge_kernel<128> : kv_merge_kernel<64>;
+    const cudaError_t e = launch_after(merge, dim3((unsigned)merged), 32 * kMergeWarps, 0, 0, stream, p, grid);
     if (e != cudaSuccess) { note_cuda_error((int)e); return MOE_ERR_CUDA; }
     note_launch();
-    return launch_merge(p, grid, stream);
-}
-
-// Prompts of few rows, whose tiles of 128 would be mostly empty, go through the split kernel.
-static bool few_rows(const moe_window &s) { return (long long)s.rows * (s.q_heads / s.kv_heads) <= kTileRows; }
-
-static long long window_ctas(int B, int Hkv, long long rows, int D) { return kv_row_tiles(rows, D) * Hkv * B; }
-
-size_t window_attn_workspace_bytes(const moe_window &s)
-{
-    const int G = s.q_heads / s.kv_heads;
-    if (few_rows(s)) return kv_ws(s.batch, s.kv_heads, G, s.head_dim, s.rows, 0).total;
-    const long long rows = (long long)s.rows * G;
-    const size_t ns = kv_tile_most(window_ctas(s.batch, s.kv_heads, rows, s.head_dim));
-    return ns == 1 ? 0 : ns * s.batch * s.kv_heads * rows * (s.head_dim + 2) * 4;
-}
-
-int launch_window_attn(KvCall &p, void *ws, cudaStream_t stream)
-{
-    const long long rows = (long long)p.M * p.G;
-    if (rows <= kTileRows) return launch_kv_attn(p, ws, stream);
-    const long long ctas = window_ctas(p.B, p.Hkv, rows, p.D);
-    const int most = kv_tile_most(ctas);
-    // tiles of a CTA's rows at most: as long as its window and first positions, or the prompt
-    const long long seen = std::min<long long>((long long)p.W + p.S + 256 / p.G, p.T);
-    p.nsplit = most == 1 ? 1 : kv_tile_splits(ctas, (seen + 127) / 128);
-    p.tile_o = static_cast<float *>(ws);
-    p.tile_ml = p.tile_o + (size_t)most * p.B * p.Hkv * rows * p.D;
-    const int rc = launch_kv_tiles(p, false, stream);
-    if (rc || p.nsplit == 1) return rc;
-    p.NRB = 0;
-    return launch_merge(p, 1, stream);
+    return MOE_OK;
 }
 
 }  // namespace moe

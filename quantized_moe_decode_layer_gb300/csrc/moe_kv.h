@@ -7,6 +7,7 @@
 namespace moe {
 
 constexpr int kKvTile = 64;           // positions a tile of the split kernel
+constexpr int kKvFewRows = 16;        // rows that it takes; more go through the tile kernel
 constexpr int kKvMaxCtas = 4 * kMaxCtas;
 constexpr int kKvMaxPos = 1 << 30;    // positions of a sequence whose cache is a ring
 constexpr int kKvAll = 1 << 30;       // window of a sequence that sees everything
@@ -42,24 +43,26 @@ struct KvCall {
     int P;                            // prefix positions (0: none)
     int f16;
     float c;                          // scale * log2(e)
-    // split kernel: problems of RB rows, NRB of them a sequence and head, NRBP of the prefix and head
-    int RB, NRB, NRBP;
+    int ring;                         // positions from T on lie in the slots from S on, again and again
+    // split kernel: of the sequences' own positions, of the prefix's
+    int split_own, split_prefix;
     int min_tiles;
-    float *part_o, *part_ml;          // [slot][RB][D], [slot][RB][2]: unnormalised output; maximum (log2), sum
-    int *cum;                         // [B + 1]: tiles of the sequences before b, for one head and row block
-    // tile kernel: the prefix's partial results, nsplit of them a row
-    int nsplit;
-    float *tile_o, *tile_ml;          // [split][Hkv][B M G][D], [...][2]
+    float *part_o, *part_ml;          // [slot][16][D], [slot][16][2]: unnormalised output; maximum (log2), sum
+    int *cum;                         // [B + 1]: tiles of the sequences before b, for one head
+    // tile kernel: parts of the own positions, of the prefix's
+    struct Parts {
+        int n;                        // 0: not taken; own positions, 1 without a prefix: outputs are written
+        float *o, *ml;                // [part][Hkv][B M G][D], [...][2]
+    } own, prefix;
     long long timeout_ns;
 };
 
-size_t kv_attn_workspace_bytes(int batch, int kv_heads, int group, int head_dim, int M, int max_prefix, bool exact);
+size_t kv_attn_workspace_bytes(int batch, int kv_heads, int group, int head_dim, long long M, int P);
 int launch_kv_append(const moe_kv &c, const moe_rows &k_new, const moe_rows &v_new, int M, const int32_t *pos,
                      const int32_t *counts, int *err, cudaStream_t stream);
+// Attention over a cache, or of a prompt.  p: q, k, v, the prefix, lengths, shapes, scale and output; the rest is set there.
 int launch_kv_attn(KvCall &p, void *ws, cudaStream_t stream);
-size_t window_attn_workspace_bytes(const moe_window &s);
-int launch_window_attn(KvCall &p, void *ws, cudaStream_t stream);
-// Tiles of 128 rows: prompts (outputs written), or the prefix (partial results).
+// Tiles of 128 rows against the own positions, or the prefix.
 int launch_kv_tiles(const KvCall &p, bool prefix, cudaStream_t stream);
 long long kv_row_tiles(long long rows, int D);
 int kv_tile_most(long long ctas);                     // parts of a row tile's positions at most

@@ -45,7 +45,7 @@ constexpr int kBox = 128 * 128;       // one TMA box: 128 positions of 64 elemen
 constexpr int kTThreads = 384;        // softmax: warps 0-3, 4-7; loads 8; products 9; q 10, 11
 constexpr int kQThreads = 64;
 constexpr int kErrTimeout = 4;
-constexpr int kItems = 4, kItemBytes = 48;   // items known ahead
+constexpr int kItems = 3, kItemBytes = 64;   // items known ahead
 
 template <int D>
 struct TLay {
@@ -295,6 +295,7 @@ struct Item {
     int z, g, b, r0;
     int p0, cnt, nvalid;
     int kt_lo, nsink, i0, nt;
+    int sl, off;    // slot of the first position in the window; that position less its slot
     __device__ __forceinline__ int first_key(int t) const { return kKeys * (i0 + t < nsink ? i0 + t : kt_lo + i0 + t - nsink); }
 };
 template <int RT, bool PREFIX>
@@ -310,7 +311,7 @@ __device__ __forceinline__ Item item_of(const TileParams &tp, int x)
     it.b = x % seqs;
     const int tile = tp.ntile - 1 - x / seqs;   // later row tiles, which see more, first
     it.r0 = tile * RT;
-    it.p0 = it.kt_lo = it.nsink = it.nt = 0;
+    it.p0 = it.kt_lo = it.nsink = it.nt = it.sl = it.off = 0;
     it.cnt = p.M;
     it.nvalid = INT_MAX;
     if (PREFIX) {
@@ -322,10 +323,17 @@ __device__ __forceinline__ Item item_of(const TileParams &tp, int x)
         const int first = p.by_g(it.r0), last = min(p.by_g(it.r0 + RT - 1), it.cnt - 1);
         it.nvalid = it.p0 + it.cnt;
         if (first < it.cnt) {
-            it.kt_lo = max(0, it.p0 + first - p.W + 1) / kKeys;
-            it.nsink = min((p.S + kKeys - 1) / kKeys, it.kt_lo);
-            it.nt = it.nsink + (it.p0 + last) / kKeys - it.kt_lo + 1;
+            // positions lo .. hi, slots sl .. T - 1 and (a ring that they wrap around in) on from S
+            const int lo = max(0, it.p0 + first - p.W + 1), hi = it.p0 + last;
+            it.sl = lo < p.T ? lo : p.S + (lo - p.S) % (p.T - p.S);
+            it.off = lo - it.sl;
+            const int end = it.sl + (hi - lo);
+            it.kt_lo = it.sl / kKeys;
+            const int low = max(min(p.S, lo), end >= p.T ? p.S + end - p.T + 1 : 0);   // slots from 0 on
+            it.nsink = min((low + kKeys - 1) / kKeys, it.kt_lo);
+            it.nt = it.nsink + min(end, p.T - 1) / kKeys - it.kt_lo + 1;
         }
+        if (it.nvalid > p.T) it.nvalid = INT_MAX;   // the ring is full
     }
     const int each = (it.nt + tp.nsplit - 1) / tp.nsplit;
     it.i0 = min(it.nt, it.z * each);
@@ -348,7 +356,9 @@ struct Items {
         const int4 a = w[0], b = w[1], d = w[2];
         it.z = a.x, it.g = a.y, it.b = a.z, it.r0 = a.w;
         it.p0 = b.x, it.cnt = b.y, it.nvalid = b.z, it.kt_lo = b.w;
-        it.nsink = d.x, it.i0 = d.y, it.nt = d.z;
+        const int2 e = *reinterpret_cast<const int2 *>(w + 3);
+        it.nsink = d.x, it.i0 = d.y, it.nt = d.z, it.sl = d.w;
+        it.off = e.x;
         return ok;
     }
     __device__ __forceinline__ void done(int n) const { bar_arrive(su32(&read[n % kItems])); }
@@ -357,7 +367,8 @@ struct Items {
         int4 *w = reinterpret_cast<int4 *>(ring + n % kItems * kItemBytes);
         w[0] = make_int4(it.z, it.g, it.b, it.r0);
         w[1] = make_int4(it.p0, it.cnt, it.nvalid, it.kt_lo);
-        w[2] = make_int4(it.nsink, it.i0, it.nt, 0);
+        w[2] = make_int4(it.nsink, it.i0, it.nt, it.sl);
+        w[3] = make_int4(it.off, 0, 0, 0);
         bar_arrive(su32(&ready[n % kItems]));
     }
 };
@@ -434,7 +445,10 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
     fence_after();
     const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
     const long long rows = (long long)p.M * p.G * (PREFIX ? p.B : 1);   // of a head (and sequence)
-    const bool parts = PREFIX || tp.nsplit > 1;
+    const bool parts = p.P > 0 || tp.nsplit > 1;
+    const KvCall::Parts &to_parts = PREFIX ? p.prefix : p.own;
+    // whether a pair's second row tile has rows that see anything
+    auto two_tiles = [&](const Item &it) { return PAIR && it.r0 + kRows < (PREFIX ? rows : (long long)it.cnt * p.G); };
     const Items items = {sm + L::items, i_ready, i_read};
     const int mine = blockIdx.x < tp.items ? (tp.items - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;   // items of the CTA
 
@@ -582,7 +596,7 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                     }
                 };
                 Place base = {0, 0};
-                int qn = 0, done[2] = {0, 0};   // items and steps of the streams before this item
+                int qn = 0, turns[2] = {0, 0}, done[2] = {0, 0};   // items; items and steps of the streams before this item
                 for (int n = 0; n < mine && go; ++n) {
                     Item it;
                     go = items.get(n, it, abort_flag, p);
@@ -591,6 +605,8 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                     const int nt = it.nt;
                     if (nt == 0) continue;
                     const int nsteps = PAIR ? 2 * nt : nt;
+                    const bool duo = two_tiles(it);     // else a pair's second stream has nothing to do
+                    const int last = PAIR && !duo ? nsteps - 2 : nsteps - 1;
                     Place kp = base, vp = base;         // of the next tile of keys, of values
                     vp.move(!PAIR && nt > 1 ? 2 * UPT : UPT);
                     auto scores = [&](int i, int xs) {
@@ -608,16 +624,16 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                                 const uint32_t off = (uint32_t)((k >> 2) * kBox + (k & 3) * 32) >> 4;
                                 umma_ss(tmem + 128u * xs, a0 + off, b0 + off, id_s, (u | k) != 0 ? 1u : 0u);
                             }
-                            if (!PAIR || xs == 1) umma_commit(su32(&empty[at.slot]));
+                            if (!duo || xs == 1) umma_commit(su32(&empty[at.slot]));
                             at.move(1);
                         }
                         umma_commit(su32(&s_full[xs]));
-                        if (i == nsteps - 1) umma_commit(su32(q_free));
-                        if (!PAIR || xs == 1) kp.move(!PAIR && t == 0 ? UPT : 2 * UPT);
+                        if (i == last) umma_commit(su32(q_free));
+                        if (!duo || xs == 1) kp.move(!PAIR && t == 0 ? UPT : 2 * UPT);
                     };
                     auto values = [&](int i, int xs) {
                         const int t = PAIR ? i >> 1 : i, step = done[xs] + (i >> 1);
-                        if (t == 0 && qn > 0) wait(&o_free[PAIR ? xs : 0], qn - 1);
+                        if (t == 0 && turns[xs] > 0) wait(&o_free[PAIR ? xs : 0], turns[xs] - 1);
                         if (!PAIR || xs == 0) {
                             Place at = vp;
 #pragma unroll
@@ -637,28 +653,31 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
 #pragma unroll
                             for (int k = 0; k < kKeys / 16; ++k)
                                 umma_ts(o, tmem + 128u * xs + 8u * k, b0 + 128u * k, id_o, (t | k) != 0 ? 1u : 0u);
-                            if (!PAIR || xs == 1) umma_commit(su32(&empty[at.slot]));
+                            if (!duo || xs == 1) umma_commit(su32(&empty[at.slot]));
                             at.move(1);
                         }
                         umma_commit(su32(&o_done[xs]));
-                        if (!PAIR || xs == 1) vp.move(!PAIR && t + 2 >= nt ? UPT : 2 * UPT);
+                        if (!duo || xs == 1) vp.move(!PAIR && t + 2 >= nt ? UPT : 2 * UPT);
                     };
                     auto step = [&](int i, int xs) {
                         values(i, xs);
-                        if (go && i + 2 < nsteps) scores(i + 2, xs);
+                        if (go && i + 2 <= last) scores(i + 2, xs);
                     };
                     wait(q_full, qn);
                     if (go) scores(0, 0);
-                    if (go && nsteps > 1) scores(1, 1);
+                    const bool both = !PAIR || duo;
+                    if (go && both && last > 0) scores(1, 1);
 #pragma unroll 1
-                    for (int i = 0; i < nsteps && go; i += 2) {
+                    for (int i = 0; i <= last && go; i += 2) {
                         step(i, 0);
-                        if (go && i + 1 < nsteps) step(i + 1, 1);
+                        if (go && both && i < last) step(i + 1, 1);
                     }
                     for (int j = 0; j < (2 * nt) % NU; ++j) base.move(UPT);
                     base.phase ^= (2 * nt / NU * UPT) & 1;
                     done[0] += PAIR ? nt : (nt + 1) / 2;
-                    done[1] += PAIR ? nt : nt / 2;
+                    done[1] += PAIR ? (duo ? nt : 0) : nt / 2;
+                    ++turns[0];
+                    turns[1] += duo;
                     ++qn;
                 }
                 // every product issued has finished before tensor memory is freed
@@ -690,19 +709,17 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                 go = __all_sync(0xFFFFFFFFu, go && ok);
                 if (lane == 0) items.done(n);
             }
-            const int nt = it.nt, nsteps = PAIR ? 2 * nt : nt, r = it.r0 + (PAIR ? 128 * xs : 0) + row;
+            const int nt = PAIR && xs == 1 && !two_tiles(it) ? 0 : it.nt, nsteps = PAIR ? 2 * nt : nt, r = it.r0 + (PAIR ? 128 * xs : 0) + row;
             const size_t part0 = ((size_t)it.z * p.Hkv + it.g) * ((size_t)p.B * p.M * p.G) + (PREFIX ? 0 : (size_t)it.b * p.M * p.G);
-            // positions t the row sees: t <= high and (t > low or t < S); all_*: the strictest of the tile's rows
-            int high, low, all_high, all_low;
-            if (PREFIX) {
-                high = all_high = p.P - 1;
-                low = all_low = -1;
-            } else {
+            // The row is at position pos, the tile's at pos_lo .. pos_hi.  Slot s has position s (s < S), else s + off (s >= sl),
+            // else s + off + R; it is seen if pos - W < position <= pos, or s < S.
+            int pos = 0, pos_lo = 0, pos_hi = 0;
+            const int R = p.ring ? p.T - p.S : kKvAll;
+            if (!PREFIX) {
                 const int ra = it.r0 + (PAIR ? 128 * xs : 0);
-                high = it.p0 + p.by_g(r);
-                low = high - p.W;
-                all_high = it.p0 + p.by_g(ra);
-                all_low = it.p0 + p.by_g(ra + kRows - 1) - p.W;
+                pos = it.p0 + p.by_g(r);
+                pos_lo = it.p0 + p.by_g(ra);
+                pos_hi = it.p0 + p.by_g(ra + kRows - 1);
             }
             float l = 0.f, ref = -INFINITY;    // of the row, as the stream knows them
             bool primed = false;               // every row of the warp has a reference
@@ -731,7 +748,13 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                 }
                 // Two row tiles: the weights are taken with the reference as it was, along with the maximum, and once more
                 // in the rare case that it was too low.  (One row tile: the reference is handed on at once.)
-                const bool partly = key + kKeys - 1 > all_high || (key <= all_low && key + kKeys > p.S);   // hidden from some row
+                // a tile that some row does not see all of
+                bool partly = key + kKeys > p.P;
+                if (!PREFIX) {
+                    const int off = key >= it.sl ? it.off : it.off + R;     // of a tile that is all on one side of sl, and past S
+                    partly = !((key + kKeys <= p.S && key + kKeys - 1 <= pos_lo) ||
+                               (key >= p.S && (key >= it.sl ? key + kKeys <= p.T : key + kKeys <= it.sl) && key + kKeys - 1 <= pos_lo - off && key > pos_hi - p.W - off));
+                }
                 bool again = !PAIR || !primed;
                 uint32_t s0[KS], s1[KS];    // the positions' halves
                 uint32_t pk[kKeys / 2];
@@ -747,7 +770,12 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
 #pragma unroll
                     for (int k = 0; k < KS / 32; ++k) {
                         const int at = key + KS * half + 32 * k;
-                        const uint32_t sees = below(high + 1 - at) & (~below(low + 1 - at) | below(p.S - at));
+                        uint32_t sees = below(p.P - at);
+                        if (!PREFIX) {
+                            const int a = pos - it.off + 1;      // past the last slot
+                            sees = below(min(p.S, pos + 1) - at) | (below(min(a, p.T) - at) & ~below(max(a - p.W, max(it.sl, p.S)) - at));
+                            if (p.ring) sees |= below(min(a - R, it.sl) - at) & ~below(max(a - R - p.W, p.S) - at);   // on the other side of sl
+                        }
                         if (__all_sync(0xFFFFFFFFu, sees == ~0u)) continue;
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
@@ -869,7 +897,7 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
             }
             done[0] += PAIR ? nt : (nt + 1) / 2;
             done[1] += PAIR ? nt : nt / 2;
-            units += 2 * nt * UPT;
+            units += 2 * it.nt * UPT;
             const bool live = PREFIX || p.by_g(r) < it.cnt;
             const float inv = live && nt > 0 && l != 0.f ? 1.f / l : 0.f;
             if (!PREFIX && tp.omap) {
@@ -903,7 +931,7 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                 }
             } else if (go) {
                 // Four lanes exchange 64-byte pieces: lane 4 a + j then has piece j of rows 4 a .. 4 a + 3.
-                if (parts && r < rows && col0 == 0) *reinterpret_cast<float2 *>(p.tile_ml + (part0 + r) * 2) = make_float2(ref, l);
+                if (parts && r < rows && col0 == 0) *reinterpret_cast<float2 *>(to_parts.ml + (part0 + r) * 2) = make_float2(ref, l);
                 const int rq = r - (lane & 3);
                 uint8_t *to[4];     // the four rows' places
                 int m = p.by_g(rq), h = rq - m * p.G - 1;
@@ -913,7 +941,7 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                         h = 0;
                         ++m;
                     }
-                    to[j] = parts ? reinterpret_cast<uint8_t *>(p.tile_o + (part0 + rq + j) * D + col0)
+                    to[j] = parts ? reinterpret_cast<uint8_t *>(to_parts.o + (part0 + rq + j) * D + col0)
                                   : reinterpret_cast<uint8_t *>(static_cast<uint16_t *>(p.o) +
                                                                 (((size_t)it.b * p.M + m) * p.Hq + it.g * p.G + h) * D + col0);
                     to[j] += 16 * (lane & 3);
@@ -1043,13 +1071,13 @@ int launch_kv_tiles(const KvCall &c, bool prefix, cudaStream_t stream)
     if (!prefix) {
         tp.qmap = packed_map(&tp.tq, c, c.q, c.M, c.B, c.qh, c.qm, c.qb);
         const long long row = (long long)c.Hq * c.D;
-        tp.omap = c.nsplit == 1 && packed_map(&tp.to, c, c.o, c.M, c.B, c.D, row, row * c.M);
+        tp.omap = c.own.n == 1 && c.P == 0 && packed_map(&tp.to, c, c.o, c.M, c.B, c.D, row, row * c.M);
     } else if (c.B == 1 || c.M == 1 || c.qb == c.M * c.qm) {   // the batch's tokens have one stride
         tp.qmap = packed_map(&tp.tq, c, c.q, (long long)c.B * c.M, 1, c.qh, c.M == 1 ? c.qb : c.qm, 0);
     }
     const long long rows = (long long)c.M * c.G * (prefix ? c.B : 1);
-    tp.nsplit = c.nsplit;
-    const long long ntile = kv_row_tiles(rows, c.D), ctas = ntile * c.nsplit * c.Hkv * (prefix ? 1 : c.B);
+    tp.nsplit = prefix ? c.prefix.n : c.own.n;
+    const long long ntile = kv_row_tiles(rows, c.D), ctas = ntile * tp.nsplit * c.Hkv * (prefix ? 1 : c.B);
     if (rows > INT_MAX - 1024 || ctas > INT_MAX) return MOE_ERR_UNSUPPORTED;
     tp.ntile = (int)ntile;
     tp.items = (int)ctas;
