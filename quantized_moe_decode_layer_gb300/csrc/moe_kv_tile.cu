@@ -32,6 +32,7 @@
 #include <climits>
 #include <cstring>
 #include <mutex>
+#include <type_traits>
 
 #include "moe_kv.h"
 #include "moe_kv8.cuh"
@@ -45,7 +46,7 @@ constexpr int kBox = 128 * 128;       // one TMA box: 128 positions of 64 elemen
 constexpr int kTThreads = 384;        // softmax: warps 0-3, 4-7; loads 8; products 9; q 10, 11
 constexpr int kQThreads = 64;
 constexpr int kErrTimeout = 4;
-constexpr int kItems = 3, kItemBytes = 64;   // items known ahead
+constexpr int kItems = 4, kItemBytes = 48;   // items known ahead
 
 template <int D>
 struct TLay {
@@ -119,23 +120,20 @@ __device__ __forceinline__ bool bar_test(uint32_t b, unsigned parity)
 }
 // Bounded wait on an mbarrier phase; gives up when the CTA's abort flag is
 // set, or sets it (and the error word) when the time runs out.
-__device__ __forceinline__ bool bar_wait_slow(uint32_t b, unsigned parity, volatile int *abort, long long timeout_ns, int *err)
+__device__ __forceinline__ bool bar_wait(uint32_t b, unsigned parity, volatile int *abort, const KvCall &c)
 {
+    if (bar_test(b, parity)) return true;
     const unsigned long long t0 = gtime();
 #pragma unroll 1
     for (;;) {
         if (bar_test(b, parity)) return true;
         if (*abort) return false;
-        if ((long long)(gtime() - t0) > timeout_ns) {
+        if ((long long)(gtime() - t0) > c.timeout_ns) {
             *abort = 1;
-            atomicOr(err, kErrTimeout);
+            atomicOr(c.err, kErrTimeout);
             return false;
         }
     }
-}
-__device__ __forceinline__ bool bar_wait(uint32_t b, unsigned parity, volatile int *abort, const KvCall &c)
-{
-    return bar_test(b, parity) || bar_wait_slow(b, parity, abort, c.timeout_ns, c.err);
 }
 
 // Shared-memory descriptors (tcgen05, version 1), 128-byte swizzle: the low word has the address
@@ -293,7 +291,7 @@ __device__ __forceinline__ int v_order(int t, int nt) { return PAIR ? 2 * t + 1 
 // tiles i0 .. i0 + nt - 1 of the list that has the first nsink tiles and then those from kt_lo on.
 struct Item {
     int z, g, b, r0;
-    int p0, cnt, nvalid;
+    int p0, cnt;
     int kt_lo, nsink, i0, nt;
     int sl, off;    // slot of the first position in the window; that position less its slot
     __device__ __forceinline__ int first_key(int t) const { return kKeys * (i0 + t < nsink ? i0 + t : kt_lo + i0 + t - nsink); }
@@ -313,7 +311,6 @@ __device__ __forceinline__ Item item_of(const TileParams &tp, int x)
     it.r0 = tile * RT;
     it.p0 = it.kt_lo = it.nsink = it.nt = it.sl = it.off = 0;
     it.cnt = p.M;
-    it.nvalid = INT_MAX;
     if (PREFIX) {
         it.nt = (p.P + kKeys - 1) / kKeys;
     } else {
@@ -321,7 +318,6 @@ __device__ __forceinline__ Item item_of(const TileParams &tp, int x)
         it.cnt = rows_of(p, it.b, it.p0, bad);
         if (bad) atomicOr(p.err, kKv8ErrRange);
         const int first = p.by_g(it.r0), last = min(p.by_g(it.r0 + RT - 1), it.cnt - 1);
-        it.nvalid = it.p0 + it.cnt;
         if (first < it.cnt) {
             // positions lo .. hi, slots sl .. T - 1 and (a ring that they wrap around in) on from S
             const int lo = max(0, it.p0 + first - p.W + 1), hi = it.p0 + last;
@@ -333,7 +329,6 @@ __device__ __forceinline__ Item item_of(const TileParams &tp, int x)
             it.nsink = min((low + kKeys - 1) / kKeys, it.kt_lo);
             it.nt = it.nsink + min(end, p.T - 1) / kKeys - it.kt_lo + 1;
         }
-        if (it.nvalid > p.T) it.nvalid = INT_MAX;   // the ring is full
     }
     const int each = (it.nt + tp.nsplit - 1) / tp.nsplit;
     it.i0 = min(it.nt, it.z * each);
@@ -355,10 +350,8 @@ struct Items {
         const int4 *w = reinterpret_cast<const int4 *>(ring + s * kItemBytes);
         const int4 a = w[0], b = w[1], d = w[2];
         it.z = a.x, it.g = a.y, it.b = a.z, it.r0 = a.w;
-        it.p0 = b.x, it.cnt = b.y, it.nvalid = b.z, it.kt_lo = b.w;
-        const int2 e = *reinterpret_cast<const int2 *>(w + 3);
+        it.p0 = b.x, it.cnt = b.y, it.off = b.z, it.kt_lo = b.w;
         it.nsink = d.x, it.i0 = d.y, it.nt = d.z, it.sl = d.w;
-        it.off = e.x;
         return ok;
     }
     __device__ __forceinline__ void done(int n) const { bar_arrive(su32(&read[n % kItems])); }
@@ -366,9 +359,8 @@ struct Items {
     {
         int4 *w = reinterpret_cast<int4 *>(ring + n % kItems * kItemBytes);
         w[0] = make_int4(it.z, it.g, it.b, it.r0);
-        w[1] = make_int4(it.p0, it.cnt, it.nvalid, it.kt_lo);
+        w[1] = make_int4(it.p0, it.cnt, it.off, it.kt_lo);
         w[2] = make_int4(it.nsink, it.i0, it.nt, it.sl);
-        w[3] = make_int4(it.off, 0, 0, 0);
         bar_arrive(su32(&ready[n % kItems]));
     }
 };
@@ -513,8 +505,6 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
             tell(0);
             tell(1);
             for (int k = 0; k < mine; ++k) {
-                tell(k + 2);
-                __syncwarp();
                 Item it;
                 go = items.get(k, it, abort_flag, p);
                 __syncwarp();
@@ -522,7 +512,11 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                 if (go && it.nt > 0 && qn > 0) go = bar_wait(su32(q_free), (unsigned)(qn - 1) & 1u, abort_flag, p);
                 go = __all_sync(0xFFFFFFFFu, go);
                 if (!go) break;
-                if (it.nt == 0) continue;
+                if (it.nt == 0) {
+                    tell(k + 2);
+                    __syncwarp();
+                    continue;
+                }
                 ++qn;
                 if (tp.qmap) {
                     if (t == 0) {
@@ -536,6 +530,8 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                                 tma_load5(su32(sm + L::q) + (j * (D / 64) + h) * kBox, &tp.tq, 64 * h, 0, it.g, m + j * (kRows / p.G),
                                           PREFIX ? 0 : it.b, su32(q_full));
                     }
+                    tell(k + 2);    // (behind the loads, which others wait for)
+                    __syncwarp();
                     continue;
                 }
                 // (rows of idle sequences and padding are read like the others; nothing of them is used)
@@ -569,6 +565,8 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                 asm volatile("cp.async.wait_all;" ::: "memory");
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 bar_arrive(su32(q_full));
+                tell(k + 2);
+                __syncwarp();
             }
             // the last copies have landed before the CTA ends
             if (tp.qmap && t == 0 && qn > 0) {
@@ -605,7 +603,8 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                     const int nt = it.nt;
                     if (nt == 0) continue;
                     const int nsteps = PAIR ? 2 * nt : nt;
-                    const bool duo = two_tiles(it);     // else a pair's second stream has nothing to do
+                    auto work = [&](auto duo_v) {
+                    constexpr bool duo = decltype(duo_v)::value;   // a pair's second stream has something to do
                     const int last = PAIR && !duo ? nsteps - 2 : nsteps - 1;
                     Place kp = base, vp = base;         // of the next tile of keys, of values
                     vp.move(!PAIR && nt > 1 ? 2 * UPT : UPT);
@@ -665,7 +664,7 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                     };
                     wait(q_full, qn);
                     if (go) scores(0, 0);
-                    const bool both = !PAIR || duo;
+                    constexpr bool both = !PAIR || duo;
                     if (go && both && last > 0) scores(1, 1);
 #pragma unroll 1
                     for (int i = 0; i <= last && go; i += 2) {
@@ -679,6 +678,9 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                     ++turns[0];
                     turns[1] += duo;
                     ++qn;
+                    };
+                    if (PAIR && two_tiles(it)) work(std::true_type());
+                    else work(std::false_type());
                 }
                 // every product issued has finished before tensor memory is freed
                 umma_commit(su32(all_done));
@@ -711,27 +713,33 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
             }
             const int nt = PAIR && xs == 1 && !two_tiles(it) ? 0 : it.nt, nsteps = PAIR ? 2 * nt : nt, r = it.r0 + (PAIR ? 128 * xs : 0) + row;
             const size_t part0 = ((size_t)it.z * p.Hkv + it.g) * ((size_t)p.B * p.M * p.G) + (PREFIX ? 0 : (size_t)it.b * p.M * p.G);
-            // The row is at position pos, the tile's at pos_lo .. pos_hi.  Slot s has position s (s < S), else s + off (s >= sl),
+            // The row is at position pos.  Slot s has position s (s < S), else s + off (s >= sl),
             // else s + off + R; it is seen if pos - W < position <= pos, or s < S.
-            int pos = 0, pos_lo = 0, pos_hi = 0;
+            int pos = 0, valid = INT_MAX;      // valid: slots from there on hold anything (a ring that is full has none)
             const int R = p.ring ? p.T - p.S : kKvAll;
+            // slots that all rows see: a_lo .. a_hi - 1 from sl on, b_lo .. b_hi - 1 before it, those below s_hi
+            int a_lo = 0, a_hi = p.P, b_lo = 0, b_hi = 0, s_hi = 0;
             if (!PREFIX) {
                 const int ra = it.r0 + (PAIR ? 128 * xs : 0);
+                const int pos_lo = it.p0 + p.by_g(ra), pos_hi = it.p0 + p.by_g(ra + kRows - 1);
                 pos = it.p0 + p.by_g(r);
-                pos_lo = it.p0 + p.by_g(ra);
-                pos_hi = it.p0 + p.by_g(ra + kRows - 1);
+                if (it.p0 + it.cnt <= p.T) valid = it.p0 + it.cnt;
+                a_lo = max(max(it.sl, p.S), pos_hi - it.off - p.W + 1);
+                a_hi = min(p.T, pos_lo - it.off + 1);
+                b_lo = max(p.S, pos_hi - it.off - R - p.W + 1);
+                b_hi = min(it.sl, pos_lo - it.off - R + 1);
+                s_hi = min(p.S, pos_lo + 1);
             }
             float l = 0.f, ref = -INFINITY;    // of the row, as the stream knows them
-            bool primed = false;               // every row of the warp has a reference
 #pragma unroll 1
             for (int i = xs; i < nsteps && go; i += 2) {
                 const int t = PAIR ? i >> 1 : i, key = it.first_key(t), step = done[xs] + (i >> 1);
                 wait(&s_full[xs], step);
                 if (!go) break;
                 fence_after();
-                if (!PREFIX && it.nvalid - key < kKeys && (!PAIR || xs == 0)) {
+                if (!PREFIX && valid - key < kKeys && (!PAIR || xs == 0)) {
                     // values behind the sequence's last position may be anything: zeros
-                    const int gone = it.nvalid - key;
+                    const int gone = valid - key;
                     const int n0 = units + UPT * v_order<PAIR>(t, nt);
 #pragma unroll 1
                     for (int u = n0; u < n0 + UPT; ++u) {
@@ -746,16 +754,9 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                     if (!go) break;
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 }
-                // Two row tiles: the weights are taken with the reference as it was, along with the maximum, and once more
-                // in the rare case that it was too low.  (One row tile: the reference is handed on at once.)
                 // a tile that some row does not see all of
-                bool partly = key + kKeys > p.P;
-                if (!PREFIX) {
-                    const int off = key >= it.sl ? it.off : it.off + R;     // of a tile that is all on one side of sl, and past S
-                    partly = !((key + kKeys <= p.S && key + kKeys - 1 <= pos_lo) ||
-                               (key >= p.S && (key >= it.sl ? key + kKeys <= p.T : key + kKeys <= it.sl) && key + kKeys - 1 <= pos_lo - off && key > pos_hi - p.W - off));
-                }
-                bool again = !PAIR || !primed;
+                const bool partly = !((key >= a_lo && key + kKeys <= a_hi) || key + kKeys <= s_hi || (key >= b_lo && key + kKeys <= b_hi));
+
                 uint32_t s0[KS], s1[KS];    // the positions' halves
                 uint32_t pk[kKeys / 2];
                 uint64_t add[2] = {0ull, 0ull};
@@ -802,66 +803,47 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                 load(0, s0);
                 tmem_wait_ld();
                 load(1, s1);
-                if (!again) {
-                    const uint64_t sub2 = two(-ref, -ref);
-                    hide(0, s0);
-                    largest(s0);
-                    weights(0, s0, sub2);
-                    tmem_wait_ld();
-                    hide(1, s1);
-                    largest(s1);
-                    weights(1, s1, sub2);
-                    again = __any_sync(0xFFFFFFFFu, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c > ref + 8.f);
-                    if (again) {
-                        load(0, s0);
-                        load(1, s1);
-                    }
+                hide(0, s0);
+                largest(s0);
+                tmem_wait_ld();
+                hide(1, s1);
+                largest(s1);
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+                float was = ref;
+                if (!PAIR && i > 0) {   // the reference, from the stream that has the tile before
+                    wait(&ref_rdy[4 * (xs ^ 1) + w], done[xs ^ 1] + ((i - 1) >> 1));
+                    if (!go) break;
+                    was = refs[row];
                 }
-                if (again) {
-                    tmem_wait_ld();
-                    hide(0, s0);
-                    hide(1, s1);
-                    largest(s0);
-                    largest(s1);
-                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-                    float was = ref;
-                    if (!PAIR && i > 0) {   // the reference, from the stream that has the tile before
-                        wait(&ref_rdy[4 * (xs ^ 1) + w], done[xs ^ 1] + ((i - 1) >> 1));
-                        if (!go) break;
-                        was = refs[row];
-                    }
-                    const bool raise = top > was + 8.f;
-                    const float now = raise ? top : was;
-                    if (!PAIR) {
-                        refs[row] = now;
-                        __syncwarp();
-                        if (lane == 0) bar_arrive(su32(&ref_rdy[4 * xs + w]));
-                    }
-                    if (now != ref) l *= ref == -INFINITY ? 0.f : ex2(ref - now);
-                    ref = now;
-                    primed = !__any_sync(0xFFFFFFFFu, ref == -INFINITY);
-                    if (__any_sync(0xFFFFFFFFu, raise) && t > 0) {
-                        // O, which has the tiles up to the one before, in the new reference's units
-                        if (PAIR) wait(&o_done[xs], step - 1);
-                        else wait(&o_done[xs ^ 1], done[xs ^ 1] + ((i - 1) >> 1));
-                        if (!go) break;
-                        fence_after();
-                        const float f = raise ? ex2(was - now) : 1.f;
+                const bool raise = top > was + 8.f;
+                const float now = raise ? top : was;
+                if (!PAIR) {
+                    refs[row] = now;
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(su32(&ref_rdy[4 * xs + w]));
+                }
+                if (now != ref) l *= ref == -INFINITY ? 0.f : ex2(ref - now);
+                ref = now;
+                if (__any_sync(0xFFFFFFFFu, raise) && t > 0) {
+                    // O, which has the tiles up to the one before, in the new reference's units
+                    if (PAIR) wait(&o_done[xs], step - 1);
+                    else wait(&o_done[xs ^ 1], done[xs ^ 1] + ((i - 1) >> 1));
+                    if (!go) break;
+                    fence_after();
+                    const float f = raise ? ex2(was - now) : 1.f;
 #pragma unroll 1
-                        for (int k = 0; k < D; k += 32) {
-                            uint32_t o[32];
-                            tmem_ld32(oc + k, o);
-                            tmem_wait_ld();
+                    for (int k = 0; k < D; k += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(oc + k, o);
+                        tmem_wait_ld();
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                            tmem_st32(oc + k, o);
-                        }
+                        for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                        tmem_st32(oc + k, o);
                     }
-                    const float sub = ref == -INFINITY ? 0.f : -ref;
-                    add[0] = add[1] = 0ull;
-                    weights(0, s0, two(sub, sub));
-                    weights(1, s1, two(sub, sub));
                 }
+                const float sub = ref == -INFINITY ? 0.f : -ref;
+                weights(0, s0, two(sub, sub));
+                weights(1, s1, two(sub, sub));
                 float a0, a1;
                 split2(add2(add[0], add[1]), a0, a1);
                 l += a0 + a1;
