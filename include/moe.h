@@ -594,8 +594,8 @@ int moe_kv8_evict(const moe_kv8 *src, const moe_kv8 *dst, const int32_t *lens_de
  * Common to the calls: pos_dev, counts_dev are int32 [batch] on the device.
  * Sequence b has positions 0 .. pos[b] - 1 before the call, and the call's row m
  * is position pos[b] + m, for m < counts[b] (NULL: all M).  pos[b] < 0 marks an
- * idle sequence: nothing of it is read or written and its outputs are zero.
- * Rows past counts[b] are padding: never read, their outputs zero.  What lies
+ * idle sequence: nothing of it is used or written and its outputs are zero.
+ * Rows past counts[b] are padding: never used, their outputs zero.  What lies
  * past a sequence's positions is never used, whatever it holds; keys and values
  * at its positions are finite.  (A value that is not makes rows NaN
  * whose tile of positions has it, also where they do not see it; a key, rows that see it.)
@@ -607,7 +607,8 @@ int moe_kv8_evict(const moe_kv8 *src, const moe_kv8 *dst, const int32_t *lens_de
  * inputs.  Every call only enqueues.
  *
  * Scores, maxima, sums and outputs are fp32; a softmax weight is rounded to the
- * 16-bit type for its product with the values, and the output once at the end.  Which
+ * 16-bit type for its product with the values, and the output once at the end; a row
+ * that sees a score of NaN or +infinity is NaN.  Which
  * partial sums there are depends on the lengths of the whole batch, so a row's last bits
  * may differ between batches; the same call gives the same bits. */
 #define MOE_KV_ERR_TIMEOUT 4
@@ -636,7 +637,8 @@ int moe_kv_append(const moe_kv *cache, const moe_rows *k_new, const moe_rows *v_
                   const int32_t *counts_dev, int *err_dev, moe_stream_t stream);
 
 /* Scratch of moe_kv_attn for up to M rows and a prefix of up to max_prefix positions
- * (0: none), no initialisation.  Errors: INVALID_ARG, UNSUPPORTED. */
+ * (0: none), no initialisation (0 bytes: none is needed, ws_dev may be NULL).  Errors:
+ * INVALID_ARG, UNSUPPORTED. */
 int moe_kv_attn_workspace_size(const moe_kv *cache, int M, int max_prefix, size_t *bytes);
 
 /* Attention of M rows (1 .. 8) of q [batch][M][q_heads][head_dim] over the cache, whose

@@ -788,7 +788,7 @@ class KVCache(_CacheCalls):
         self._index = self.device.index
         self._ref = C.byref(self._c)
         self._ws, self._err, self._ws_bytes = self.ws.data_ptr(), self.err.data_ptr(), ws.numel()
-        self._vec_shape = (batch,)
+        self._vec_shape, self._q_shape = (batch,), torch.Size((q_heads, head_dim))
         L = lib()
         self._f_append, self._f_attn = L.moe_kv_append, L.moe_kv_attn
 
@@ -823,7 +823,10 @@ class KVCache(_CacheCalls):
         scale: 1 / sqrt(head_dim) by default.  prefix: (k, v), each [n, kv_heads,
         head_dim], that every row sees besides its sequence's own positions (which count from
         0 behind it); read once for the batch."""
-        self._view(q, "q", self.q_heads, (self.dtype,))
+        if not (isinstance(q, torch.Tensor) and q.dim() == 4 and q.dtype is self.dtype and q.get_device() == self._index
+                and q.shape[0] == self.batch and q.shape[2:] == self._q_shape and q.size(1) > 0):
+            self._view(q, "q", self.q_heads, (self.dtype,))
+            raise ValueError("q must have at least one row")
         r, M, h = _rows_of(q, "q"), q.size(1), self._on(stream)
         if M > self.max_rows:
             raise ValueError(f"q has {M} rows; the cache was built for max_rows={self.max_rows}")
@@ -839,7 +842,9 @@ class KVCache(_CacheCalls):
                 raise ValueError("the prefix's k and v must have one length")
         if out is None:
             out = self._new(shape, self.dtype, stream)
-        o = self._like(out, "out", self.dtype, shape)
+            o = out.data_ptr()
+        else:
+            o = self._like(out, "out", self.dtype, shape)
         e = self._err if err is None else self._like(err, "err", torch.int32, (1,))
         self._run("moe_kv_attn", self._f_attn, self._ref, r, M, self._vec(pos, "pos"),
                   None if counts is None else self._vec(counts, "counts"), pk, pv, n,
@@ -852,11 +857,35 @@ class KVCache(_CacheCalls):
 def _rows_of(t: torch.Tensor, name: str) -> Rows:
     """moe_rows of [batch, M, heads, head_dim] that the attention kernels read
     in 16-byte pieces; dimensions of one entry have no stride."""
-    s = [0 if n == 1 else x for n, x in zip(t.shape[:3], t.stride())]
-    if t.stride(3) != 1 or t.data_ptr() % 16 or any(x % 8 for x in s):
+    n0, n1, n2, _ = t.shape
+    s0, s1, s2, s3 = t.stride()
+    if n0 == 1:
+        s0 = 0
+    if n1 == 1:
+        s1 = 0
+    if n2 == 1:
+        s2 = 0
+    at = t.data_ptr()
+    if s3 != 1 or at % 16 or (s0 | s1 | s2) % 8:
         raise ValueError(f"{name} must have a contiguous last dimension, a base that is a multiple of 16 bytes and strides that are "
-                         f"multiples of 8 elements; got strides {t.stride()}, base {t.data_ptr():#x}")
-    return Rows(t.data_ptr(), _ROW_TYPES[t.dtype], *s)
+                         f"multiples of 8 elements; got strides {t.stride()}, base {at:#x}")
+    return Rows(at, _ROW_TYPES[t.dtype], s0, s1, s2)
+
+
+_window_err: dict = {}   # device index -> the error word of window_attention's calls
+
+
+def _err_of(index: int) -> torch.Tensor:
+    """The device's word; during a capture that comes before any other call, one of the graph's own."""
+    err = _window_err.get(index)
+    if err is None:
+        err = torch.zeros(1, dtype=torch.int32, device=index)
+        with torch.cuda.device(index):
+            if torch.cuda.is_current_stream_capturing():
+                return err
+            torch.cuda.current_stream().synchronize()
+        _window_err[index] = err
+    return err
 
 
 def window_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window=None, sinks: int = 0, pos=None, counts=None,
@@ -865,16 +894,18 @@ def window_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window=N
     k, v [batch, T, kv_heads, head_dim] (bf16 or fp16, one type; strided views with a
     contiguous last dimension), row m of sequence b at position pos[b] + m (pos None: T - M),
     m < counts[b] (None: M).  A row at position p sees the positions t <= p with t > p -
-    window or t < sinks (window None: all t <= p).  Returns (o like q, contiguous; err int32 [1]: 1 =
-    rows outside the positions, 4 = a device wait gave up).  pos, counts: int32 [batch] on q's device;
-    pos[b] < 0: an idle sequence.  Rows without work get zeros.
+    window or t < sinks (window None: all t <= p).  Returns (o like q, contiguous; err).  pos, counts: int32
+    [batch] on q's device; pos[b] < 0: an idle sequence.  Rows without work get zeros.
+
+    err (int32 [1]) collects 1 = rows outside the positions, 4 = a device wait gave up; where none is given, a word
+    of the device that all such calls share.
 
     Runs on the current stream of q's device, or on `stream`: then inputs and results are
     ordered by the caller, as tensors between streams are; inputs may be dropped right after the call.
     ws: scratch (uint8, window_attention_workspace bytes) to use instead of new one."""
     for name, t in (("q", q), ("k", k), ("v", v)):
         if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == 4 and t.dtype in _Q_TYPES and t.dtype is q.dtype
-                and t.device == q.device):
+                and t.get_device() == q.get_device()):
             got = f"{tuple(t.shape)} {t.dtype} on {t.device}" if isinstance(t, torch.Tensor) else type(t).__name__
             raise ValueError(f"{name} must be a [batch, rows, heads, head_dim] CUDA tensor, bf16 or fp16 like q; got {got}")
     B, M, Hq, D = q.shape
@@ -883,50 +914,65 @@ def window_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window=N
         raise ValueError(f"q {tuple(q.shape)}, k {tuple(k.shape)} and v {tuple(v.shape)} do not go together")
     if window is not None and window < 1:
         raise ValueError("window must be at least 1, or None")
-    dev = q.device
-    for name, t in (("pos", pos), ("counts", counts)):
-        if t is not None and not (isinstance(t, torch.Tensor) and t.dtype is torch.int32 and tuple(t.shape) == (B,)
-                                  and t.is_contiguous() and t.device == dev):
-            raise ValueError(f"{name} must be a contiguous int32 tensor of shape [{B}] on {dev}")
-    if stream is not None and stream.device != dev:
-        raise ValueError(f"the stream must be on {dev}")
+    index = q.get_device()
+    if stream is not None and stream.device.index != index:
+        raise ValueError(f"the stream must be on {q.device}")
+    if stream is not None or torch._C._cuda_getDevice() != index:
+        with torch.cuda.device(index), torch.cuda.stream(stream):
+            got = _window_call(q, k, v, (B, Hq, Hkv, D, M, T, window or 0, sinks), pos, counts, scale, out, err, ws, index)
+        if stream is not None:
+            _CacheCalls._keep(stream, q, k, v, pos, counts, out, err, ws)
+            for given, t in zip((out, err), got):
+                if given is None:
+                    t.record_stream(torch.cuda.current_stream(index))
+        return got
+    return _window_call(q, k, v, (B, Hq, Hkv, D, M, T, window or 0, sinks), pos, counts, scale, out, err, ws, index)
+
+
+def _window_call(q, k, v, shape, pos, counts, scale, out, err, ws, index):
+    """window_attention's call, on the current stream of the current device."""
+    def ptr(t, name, dtype, size):
+        if (isinstance(t, torch.Tensor) and t.dtype is dtype and (size is None or t.shape == size) and t.is_contiguous()
+                and t.get_device() == index):
+            return t.data_ptr()
+        got = (f"{tuple(t.shape)} {t.dtype} on {t.device}, contiguous={t.is_contiguous()}" if isinstance(t, torch.Tensor)
+               else type(t).__name__)
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor{'' if size is None else f' of shape {list(size)}'} on {q.device}; got {got}")
+
+    B, Hq, _, D, M = shape[:5]
+    d, n, L = Window(*shape), C.c_size_t(), lib()
+    rc = L.moe_window_attn_workspace_size(d, n)
+    if rc:
+        check("moe_window_attn_workspace_size", rc)
     rq, rk, rv = _rows_of(q, "q"), _rows_of(k, "k"), _rows_of(v, "v")
-    d = Window(B, Hq, Hkv, D, M, T, window or 0, sinks)
-    n = C.c_size_t()
-    check("moe_window_attn_workspace_size", lib().moe_window_attn_workspace_size(C.byref(d), C.byref(n)))
-    with torch.cuda.device(dev), torch.cuda.stream(stream):
-        made = []
-        if out is None:
-            out = torch.empty((B, M, Hq, D), dtype=q.dtype, device=dev)
-            made.append(out)
-        if err is None:
-            err = torch.zeros(1, dtype=torch.int32, device=dev)
-            made.append(err)
-        if ws is None and n.value:
-            ws = torch.empty(n.value, dtype=torch.uint8, device=dev)
-        _need(out, "out", q.dtype, (B, M, Hq, D))
-        _need(err, "err", torch.int32, (1,))
-        if ws is not None:
-            _need(ws, "ws", torch.uint8, (None,))
-        if any(t is not None and t.device != dev for t in (out, err, ws)):
-            raise ValueError(f"out, err and ws must be on {dev}")
-        check("moe_window_attn",
-              lib().moe_window_attn(C.byref(d), rq, rk, rv, None if pos is None else pos.data_ptr(),
-                                    None if counts is None else counts.data_ptr(), D ** -0.5 if scale is None else scale,
-                                    out.data_ptr(), None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
-                                    err.data_ptr(), torch.cuda.current_stream(dev).cuda_stream))
-    if stream is not None:
-        _CacheCalls._keep(stream, q, k, v, pos, counts, out, err, ws)
-        for t in made:
-            t.record_stream(torch.cuda.current_stream(dev))
+    pp = None if pos is None else ptr(pos, "pos", torch.int32, (B,))
+    pc = None if counts is None else ptr(counts, "counts", torch.int32, (B,))
+    if out is None:
+        out = torch.empty((B, M, Hq, D), dtype=q.dtype, device=q.device)
+        po = out.data_ptr()
+    else:
+        po = ptr(out, "out", q.dtype, (B, M, Hq, D))
+    if err is None:
+        err = _err_of(index)
+        pe = err.data_ptr()
+    else:
+        pe = ptr(err, "err", torch.int32, (1,))
+    if ws is None and n.value:
+        ws = torch.empty(n.value, dtype=torch.uint8, device=q.device)
+    pw = None if ws is None else ptr(ws, "ws", torch.uint8, None)
+    rc = L.moe_window_attn(d, rq, rk, rv, pp, pc, D ** -0.5 if scale is None else scale, po, pw, 0 if ws is None else ws.numel(), pe,
+                           torch._C._cuda_getCurrentRawStream(index))
+    if rc:
+        check("moe_window_attn", rc)
     return out, err
 
 
-def window_attention_workspace(batch: int, q_heads: int, kv_heads: int, head_dim: int, rows: int, positions: int) -> int:
+def window_attention_workspace(batch: int, q_heads: int, kv_heads: int, head_dim: int, rows: int, positions: int, window=None,
+                               sinks: int = 0) -> int:
     """Bytes of scratch that window_attention of these sizes needs (moe_window_attn_workspace_size)."""
     n = C.c_size_t()
     check("moe_window_attn_workspace_size",
-          lib().moe_window_attn_workspace_size(C.byref(Window(batch, q_heads, kv_heads, head_dim, rows, positions, 0, 0)), C.byref(n)))
+          lib().moe_window_attn_workspace_size(Window(batch, q_heads, kv_heads, head_dim, rows, positions, window or 0, sinks), n))
     return n.value
 
 

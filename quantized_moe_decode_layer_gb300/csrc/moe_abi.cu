@@ -958,7 +958,8 @@ int moe_kv_attn_workspace_size(const moe_kv *cache, int M, int max_prefix, size_
     size_t most = 0;
     for (int m = 1; m <= M; ++m)
         for (int P : {0, max_prefix}) {
-            const size_t n = kv_attn_workspace_bytes(cache->batch, cache->kv_heads, cache->q_heads / cache->kv_heads, cache->head_dim, m, P);
+            const size_t n = kv_attn_workspace_bytes(cache->batch, cache->kv_heads, cache->q_heads / cache->kv_heads, cache->head_dim, m,
+                                                     cache->T_cap, cache->window, cache->sinks, P);
             if (n > most) most = n;
         }
     *bytes = most;
@@ -972,8 +973,7 @@ int moe_kv_attn(const moe_kv *cache, const moe_rows *q, int M, const int32_t *po
     if (M < 1 || M > MOE_KV_MAX_ROWS) return MOE_ERR_INVALID_ARG;
     const int rc = kv_check(cache, M, true);
     if (rc) return rc;
-    if (!kv_rows_ok(q, cache->type) || !pos_dev || !o_dev || !ws_dev || !err_dev || !aligned16(o_dev) || !aligned16(ws_dev) ||
-        M > cache->T_cap || !kv_scale_ok(scale))
+    if (!kv_rows_ok(q, cache->type) || !pos_dev || !o_dev || !err_dev || !aligned16(o_dev) || M > cache->T_cap || !kv_scale_ok(scale))
         return MOE_ERR_INVALID_ARG;
     if ((prefix_k == nullptr) != (prefix_v == nullptr) || (prefix_k == nullptr) != (prefix_len == 0) || prefix_len < 0 ||
         prefix_len > MOE_KV_MAX_SLOTS)
@@ -981,8 +981,10 @@ int moe_kv_attn(const moe_kv *cache, const moe_rows *q, int M, const int32_t *po
     if (prefix_len && (cache->window || !kv_rows_ok(prefix_k, cache->type) || !kv_rows_ok(prefix_v, cache->type)))
         return MOE_ERR_INVALID_ARG;
     const int G = cache->q_heads / cache->kv_heads;
-    if (ws_bytes < kv_attn_workspace_bytes(cache->batch, cache->kv_heads, G, cache->head_dim, M, prefix_len))
-        return MOE_ERR_BUFFER_TOO_SMALL;
+    const size_t need = kv_attn_workspace_bytes(cache->batch, cache->kv_heads, G, cache->head_dim, M, cache->T_cap, cache->window,
+                                                cache->sinks, prefix_len);
+    if (need && (!ws_dev || !aligned16(ws_dev))) return MOE_ERR_INVALID_ARG;
+    if (ws_bytes < need) return MOE_ERR_BUFFER_TOO_SMALL;
     KvCall p = {};
     p.q = static_cast<const uint16_t *>(q->data_dev);
     p.qb = q->seq;
@@ -1024,6 +1026,11 @@ int moe_kv_attn(const moe_kv *cache, const moe_rows *q, int M, const int32_t *po
     return launch_kv_attn(p, ws_dev, reinterpret_cast<cudaStream_t>(stream));
 }
 
+static size_t window_bytes(const moe_window &s)
+{
+    return kv_attn_workspace_bytes(s.batch, s.kv_heads, s.q_heads / s.kv_heads, s.head_dim, s.rows, s.positions, s.window, s.sinks, 0);
+}
+
 static int window_check(const moe_window *s)
 {
     if (!s || s->rows < 1 || s->rows > s->positions) return MOE_ERR_INVALID_ARG;
@@ -1035,7 +1042,7 @@ int moe_window_attn_workspace_size(const moe_window *shape, size_t *bytes)
     const int rc = window_check(shape);
     if (rc) return rc;
     if (!bytes) return MOE_ERR_INVALID_ARG;
-    *bytes = kv_attn_workspace_bytes(shape->batch, shape->kv_heads, shape->q_heads / shape->kv_heads, shape->head_dim, shape->rows, 0);
+    *bytes = window_bytes(*shape);
     return MOE_OK;
 }
 
@@ -1051,7 +1058,7 @@ int moe_window_attn(const moe_window *shape, const moe_rows *q, const moe_rows *
     for (const moe_rows *r : {k, v})
         if ((shape->batch > 1 && r->seq == 0) || (shape->positions > 1 && r->row == 0) || (shape->kv_heads > 1 && r->head == 0))
             return MOE_ERR_INVALID_ARG;
-    const size_t need = kv_attn_workspace_bytes(shape->batch, shape->kv_heads, shape->q_heads / shape->kv_heads, shape->head_dim, shape->rows, 0);
+    const size_t need = window_bytes(*shape);
     if (need && (!ws_dev || !aligned16(ws_dev))) return MOE_ERR_INVALID_ARG;
     if (ws_bytes < need) return MOE_ERR_BUFFER_TOO_SMALL;
     KvCall p = {};

@@ -156,8 +156,8 @@ struct Lay {
     static constexpr int q = NU * kUnit;
     static constexpr int probs = q + NQ * kQ;
     static constexpr int misc = probs + (NQ + 1) * (int)sizeof(Problem);   // maxima and sums of the position groups
-    static constexpr int cum = misc + (2 * WK * RB + 8) * 4;
-    static constexpr int total(int B) { return cum + (B + 1) * 4; }
+    static constexpr int cum = misc + (2 * WK * RB + 8) * 4;               // tiles before a sequence; its first row's position; its rows
+    static constexpr int total(int B) { return cum + (B + 1) * 4 + B * 5; }
 };
 
 // 16-byte chunk c of row r of a tile, swizzled so that eight rows' equal chunks lie in eight banks' groups.
@@ -175,8 +175,10 @@ __global__ void __launch_bounds__(Lay<D>::kThreads, Lay<D>::ctas) kv_split_kerne
     Problem *probs = reinterpret_cast<Problem *>(sm + L::probs);
     float *gm = reinterpret_cast<float *>(sm + L::misc), *gl = gm + WK * RB;
     int *wsum = reinterpret_cast<int *>(gl + WK * RB);
-    int *cum = reinterpret_cast<int *>(sm + L::cum);
-    after_previous();
+    int *cum = reinterpret_cast<int *>(sm + L::cum), *first_pos = cum + p.B + 1;
+    uint8_t *n_rows = reinterpret_cast<uint8_t *>(first_pos + p.B);
+    if (p.late) place_next();
+    else after_previous();
 
     // tiles of every sequence, summed up
     {
@@ -187,6 +189,8 @@ __global__ void __launch_bounds__(Lay<D>::kThreads, Lay<D>::ctas) kv_split_kerne
             bool bad;
             const int n = rows_of(p, b, p0, bad);
             if (bad && blockIdx.x == 0) atomicOr(p.err, kKv8ErrRange);
+            first_pos[b] = p0;
+            n_rows[b] = (uint8_t)n;
             sum += (visible(p, p0, n, lo, ns) + kKvTile - 1) / kKvTile;
             cum[b + 1] = sum;
         }
@@ -204,11 +208,12 @@ __global__ void __launch_bounds__(Lay<D>::kThreads, Lay<D>::ctas) kv_split_kerne
         if (tid == 0) cum[0] = 0;
         __syncthreads();
     }
-    if (blockIdx.x == 0)
-        for (int b = tid; b <= p.B; b += kThreads) p.cum[b] = cum[b];
     const Line ln = line_of(p, cum[p.B], gridDim.x);
     const int t0 = min(ln.total, (int)blockIdx.x * ln.share), t1 = min(ln.total, t0 + ln.share);
-    if (t0 >= t1) return;
+    if (t0 >= t1) {
+        if (p.late) wait_for_previous();
+        return;
+    }
 
     // ------------------------------------------------------------- loading
     // cursor of the loads: unit (keys, then values) of tile li of problem lp, NU - 1 units ahead
@@ -234,10 +239,10 @@ __global__ void __launch_bounds__(Lay<D>::kThreads, Lay<D>::ctas) kv_split_kerne
             lbase = 0;
         } else {
             const int x = id - ln.NP, b = x / p.Hkv;
-            bool bad;
             lp.b = b;
             lp.g = x - b * p.Hkv;
-            lp.cnt = rows_of(p, b, lp.p0, bad);
+            lp.cnt = n_rows[b];
+            lp.p0 = first_pos[b];
             lp.n = visible(p, lp.p0, lp.cnt, lp.lo, lp.ns);
             lk = p.k + b * p.kb + lp.g * p.kh;
             lv = p.v + b * p.vb + lp.g * p.vh;
@@ -496,111 +501,118 @@ __global__ void __launch_bounds__(Lay<D>::kThreads, Lay<D>::ctas) kv_split_kerne
             lrun[0] += __shfl_xor_sync(0xFFFFFFFFu, lrun[0], o);
             lrun[1] += __shfl_xor_sync(0xFFFFFFFFu, lrun[1], o);
         }
+        // a row of NaN alone has no maximum, but is not empty
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+            if (lrun[x] != lrun[x] && mrun[x] == -INFINITY) mrun[x] = 0.f;
         const bool direct = cp.whole && p.P == 0;
         const int R = cp.b < 0 ? p.B * p.M * p.G : p.M * p.G;
         const size_t part = ((size_t)blockIdx.x + cp.id) * RB;
-        // n columns from c on of the block's row r
-        auto put = [&](int r, int c, const float *v, int n, float m, float l) {
-            if (r >= R) return;
-            if (direct) {
-                const int mm = p.by_g(r), h = r - mm * p.G;
-                const float f = mm < cp.cnt && l != 0.f ? 1.f / l : 0.f;
-                uint32_t *to = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.o) +
-                                                            (((size_t)cp.b * p.M + mm) * p.Hq + cp.g * p.G + h) * D + c);
-                for (int i = 0; i < n; i += 2) to[i / 2] = mm < cp.cnt ? pack2<F16>(v[i] * f, v[i + 1] * f) : 0u;
-            } else {
-                float *to = p.part_o + (part + r) * D + c;
-                for (int i = 0; i < n; i += 2) *reinterpret_cast<float2 *>(to + i) = make_float2(v[i], v[i + 1]);
-                if (c == 0) *reinterpret_cast<float2 *>(p.part_ml + (part + r) * 2) = make_float2(m, l);
-            }
-        };
         // The position groups' outputs are joined in the unit that was just read (its next load comes after the
-        // next barrier).
+        // next barrier), eight rows at a time: every group's as they are, then their weighted sum.
         if ((lane & 3) == 0 && wd == 0) {
             gm[wk * RB + rA] = mrun[0];
             gm[wk * RB + rA + 8] = mrun[1];
             gl[wk * RB + rA] = lrun[0];
             gl[wk * RB + rA + 8] = lrun[1];
         }
-        __syncthreads();
-        float *out = reinterpret_cast<float *>(sm + used * L::kUnit);   // [RB][D]
-        static_assert(RB * D * 4 <= L::kUnit, "outputs in a unit");
-        float w[2];
+        float *out = reinterpret_cast<float *>(sm + used * L::kUnit);   // [WK][8][D]
+        static_assert(WK * 8 * D * 4 <= L::kUnit, "outputs in a unit");
+        __syncthreads();                                                // the unit has been read by all
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            float m = gm[rA + 8 * x];
-            for (int k = 1; k < WK; ++k) m = fmaxf(m, gm[k * RB + rA + 8 * x]);
-            w[x] = mrun[x] == -INFINITY ? 0.f : ex2(mrun[x] - m);
-        }
-#pragma unroll 1
-        for (int k = 0; k < WK; ++k) {
-            if (wk == k) {
+        for (int half = 0; half < 2; ++half) {
+            if (8 * half >= R) break;
+            if (half) __syncthreads();
 #pragma unroll
-                for (int i = 0; i < DW / 8; ++i)
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        // columns in an order that spreads a warp's rows over the banks
-                        const int r = rA + 8 * x, c = wd * DW + 8 * i + 2 * (lane & 3);
-                        float2 *to = reinterpret_cast<float2 *>(out + r * D + (c ^ (8 * (r & 3))));
-                        float2 v = make_float2(acc[i][2 * x] * w[x], acc[i][2 * x + 1] * w[x]);
-                        if (k > 0) {
-                            const float2 was = *to;
-                            v.x += was.x;
-                            v.y += was.y;
-                        }
-                        *to = v;
-                    }
+            for (int i = 0; i < DW / 8; ++i) {
+                // columns in an order that spreads a warp's rows over the banks
+                const int c = wd * DW + 8 * i + 2 * (lane & 3);
+                *reinterpret_cast<float2 *>(out + (wk * 8 + rA) * D + (c ^ (8 * (rA & 3)))) = make_float2(acc[i][2 * half], acc[i][2 * half + 1]);
             }
             __syncthreads();
-        }
-        constexpr int C4 = D / 4;
-        for (int x = tid; x < RB * C4; x += kThreads) {
-            const int r = x / C4, c = 4 * (x % C4);
-            float m = gm[r], l = 0.f;
-            for (int k = 1; k < WK; ++k) m = fmaxf(m, gm[k * RB + r]);
-            for (int k = 0; k < WK; ++k) {
-                const float mk = gm[k * RB + r];
-                l += mk == -INFINITY ? 0.f : gl[k * RB + r] * ex2(mk - m);
+            constexpr int C4 = D / 4;
+            for (int x = tid; x < 8 * C4; x += kThreads) {
+                const int rr = x / C4, r = 8 * half + rr, c = 4 * (x % C4);
+                if (r >= R) break;
+                float m = gm[r], l = 0.f;
+#pragma unroll
+                for (int k = 1; k < WK; ++k) m = fmaxf(m, gm[k * RB + r]);
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int k = 0; k < WK; ++k) {
+                    const float mk = gm[k * RB + r], w = mk == -INFINITY ? 0.f : ex2(mk - m);
+                    const float4 u = *reinterpret_cast<const float4 *>(out + (k * 8 + rr) * D + (c ^ (8 * (rr & 3))));
+                    l = fmaf(gl[k * RB + r], w, l);
+                    v.x = fmaf(u.x, w, v.x);
+                    v.y = fmaf(u.y, w, v.y);
+                    v.z = fmaf(u.z, w, v.z);
+                    v.w = fmaf(u.w, w, v.w);
+                }
+                if (direct) {
+                    const int mm = p.by_g(r), h = r - mm * p.G;
+                    const float f = l != 0.f ? 1.f / l : 0.f;
+                    uint2 u = make_uint2(0u, 0u);
+                    if (mm < cp.cnt) u = make_uint2(pack2<F16>(v.x * f, v.y * f), pack2<F16>(v.z * f, v.w * f));
+                    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.o) + (((size_t)cp.b * p.M + mm) * p.Hq + cp.g * p.G + h) * D + c) = u;
+                } else {
+                    *reinterpret_cast<float4 *>(p.part_o + (part + r) * D + c) = v;
+                    if (c == 0) *reinterpret_cast<float2 *>(p.part_ml + (part + r) * 2) = make_float2(m, l);
+                }
             }
-            const float4 v = *reinterpret_cast<const float4 *>(out + r * D + (c ^ (8 * (r & 3))));
-            const float u[4] = {v.x, v.y, v.z, v.w};
-            put(r, c, u, 4, m, l);
         }
     }
+    if (p.late) wait_for_previous();   // the end of this kernel means the end of the one before
 }
 
 // Joins a row's parts in order: o = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m)
 // l_i with m the largest m_i.  One CTA per row and head; each warp takes every
-// kMergeWarps-th part, its lanes the columns.  Rows without positions get zeros.
+// kMergeWarps-th part with a running maximum, its lanes the columns, and the warps' sums are joined.  Which parts there are
+// follows from the lengths, which are there before the kernel in front has ended.  Rows without positions get zeros.
 constexpr int kMergeWarps = 4;
 template <int D>
 __global__ void __launch_bounds__(32 * kMergeWarps) kv_merge_kernel(const KvCall p, int ctas)
 {
-    constexpr int VEC = D / 32;
-    __shared__ float red[kMergeWarps][D + 1], redm[kMergeWarps];
+    constexpr int VEC = D / 32, kThreads = 32 * kMergeWarps;
+    __shared__ float red[kMergeWarps][D + 2];
+    __shared__ int tsum[2][kMergeWarps];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int hq = blockIdx.x % p.Hq, bm = blockIdx.x / p.Hq, m = bm % p.M, b = bm / p.M;
     const int g = hq / p.G, h = hq - g * p.G;
     uint16_t *o = static_cast<uint16_t *>(p.o) + ((size_t)bm * p.Hq + hq) * D;
-    int p0;
+    int p0, lo, ns;
     bool bad;
     const int cnt = rows_of(p, b, p0, bad);
-    wait_for_previous();
-    if (m >= cnt) {
-        for (int d = tid; d < D; d += 32 * kMergeWarps) o[d] = 0;
-        return;
-    }
     // parts of the own positions, then of the prefix's: of the tile kernel, or slots of the split kernel
     const int row = (b * p.M + m) * p.G + h;
     const size_t rows = (size_t)p.B * p.M * p.G;
     size_t first = 0, pfirst = 0;
     int n1 = p.own.n, n2 = p.prefix.n;
-    if (p.split_own) {
-        const Line ln = line_of(p, p.cum[p.B], ctas);
-        const int each = p.cum[b + 1] - p.cum[b], j = b * p.Hkv + g;
-        const int T0 = ln.NP * ln.ptiles + p.cum[b] * p.Hkv + g * each, c0 = T0 / ln.share;
+    if (p.split_own && m < cnt) {
+        // tiles of all sequences, and of those before
+        int all = 0, before = 0;
+        for (int x = tid; x < p.B; x += kThreads) {
+            int q0, xlo, xns;
+            const int n = rows_of(p, x, q0, bad), t = (visible(p, q0, n, xlo, xns) + kKvTile - 1) / kKvTile;
+            all += t;
+            before += x < b ? t : 0;
+        }
+        all = __reduce_add_sync(0xFFFFFFFFu, all);
+        before = __reduce_add_sync(0xFFFFFFFFu, before);
+        if (lane == 0) {
+            tsum[0][warp] = all;
+            tsum[1][warp] = before;
+        }
+        __syncthreads();
+        all = before = 0;
+#pragma unroll
+        for (int w = 0; w < kMergeWarps; ++w) {
+            all += tsum[0][w];
+            before += tsum[1][w];
+        }
+        const Line ln = line_of(p, all, ctas);
+        const int each = (visible(p, p0, cnt, lo, ns) + kKvTile - 1) / kKvTile, j = b * p.Hkv + g;
+        const int T0 = ln.NP * ln.ptiles + before * p.Hkv + g * each, c0 = T0 / ln.share;
         n1 = (T0 + each - 1) / ln.share - c0 + 1;
-        if (n1 == 1 && p.P == 0) return;   // written by the split kernel
         first = ((size_t)c0 + ln.NP + j) * kKvFewRows + m * p.G + h;
         if (p.split_prefix) {
             const int q0 = g * ln.ptiles, a = q0 / ln.share;
@@ -608,6 +620,12 @@ __global__ void __launch_bounds__(32 * kMergeWarps) kv_merge_kernel(const KvCall
             pfirst = ((size_t)a + g) * kKvFewRows + row;
         }
     }
+    wait_for_previous();
+    if (m >= cnt) {
+        for (int d = tid; d < D; d += kThreads) o[d] = 0;
+        return;
+    }
+    if (p.split_own && n1 == 1 && p.P == 0) return;   // written by the split kernel
     auto part = [&](int i, const float *&po) -> const float * {
         const bool own = i < n1;
         if (!own) i -= n1;
@@ -622,31 +640,32 @@ __global__ void __launch_bounds__(32 * kMergeWarps) kv_merge_kernel(const KvCall
         return t.ml + x * 2;
     };
     const int n = n1 + n2;
-    float mx = -INFINITY;
-    for (int i = tid; i < n; i += 32 * kMergeWarps) {
-        const float *po;
-        mx = fmaxf(mx, __ldcg(part(i, po)));
-    }
+    float acc[VEC] = {}, l = 0.f, mx = -INFINITY;
+    constexpr int AHEAD = 4;    // parts whose loads are in flight
+    for (int i0 = warp; i0 < n; i0 += AHEAD * kMergeWarps) {
+        float2 ml[AHEAD], y[AHEAD][VEC / 2];
 #pragma unroll
-    for (int s = 16; s >= 1; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, s));
-    if (lane == 0) redm[warp] = mx;
-    __syncthreads();
-    mx = redm[0];
+        for (int k = 0; k < AHEAD; ++k) {
+            const int i = i0 + k * kMergeWarps;
+            ml[k] = make_float2(-INFINITY, 0.f);
+            if (i < n) {
+                const float *po, *at = part(i, po);
+                ml[k] = __ldcg(reinterpret_cast<const float2 *>(at));
 #pragma unroll
-    for (int w = 1; w < kMergeWarps; ++w) mx = fmaxf(mx, redm[w]);
-    float acc[VEC] = {}, l = 0.f;
-#pragma unroll 4
-    for (int i = warp; i < n; i += kMergeWarps) {
-        const float *po, *ml = part(i, po);
-        const float2 x = __ldcg(reinterpret_cast<const float2 *>(ml));
-        if (x.x == -INFINITY) continue;   // an empty part: its output was not written
-        const float w = ex2(x.x - mx);
-        l = fmaf(x.y, w, l);
+                for (int v = 0; v < VEC / 2; ++v) y[k][v] = __ldcg(reinterpret_cast<const float2 *>(po) + v * 32 + lane);
+            }
+        }
 #pragma unroll
-        for (int v = 0; v < VEC / 2; ++v) {
-            const float2 y = __ldcg(reinterpret_cast<const float2 *>(po) + v * 32 + lane);
-            acc[2 * v] = fmaf(y.x, w, acc[2 * v]);
-            acc[2 * v + 1] = fmaf(y.y, w, acc[2 * v + 1]);
+        for (int k = 0; k < AHEAD; ++k) {
+            if (ml[k].x == -INFINITY) continue;   // none, or empty: its output was not written
+            const float top = fmaxf(mx, ml[k].x), f = mx == -INFINITY ? 0.f : ex2(mx - top), w = ex2(ml[k].x - top);
+            mx = top;
+            l = fmaf(l, f, ml[k].y * w);
+#pragma unroll
+            for (int v = 0; v < VEC / 2; ++v) {
+                acc[2 * v] = fmaf(acc[2 * v], f, y[k][v].x * w);
+                acc[2 * v + 1] = fmaf(acc[2 * v + 1], f, y[k][v].y * w);
+            }
         }
     }
 #pragma unroll
@@ -654,19 +673,27 @@ __global__ void __launch_bounds__(32 * kMergeWarps) kv_merge_kernel(const KvCall
         red[warp][64 * v + 2 * lane] = acc[2 * v];
         red[warp][64 * v + 2 * lane + 1] = acc[2 * v + 1];
     }
-    if (lane == 0) red[warp][D] = l;
+    if (lane == 0) {
+        red[warp][D] = l;
+        red[warp][D + 1] = mx;
+    }
     __syncthreads();
-    float ls = 0.f;
+    float top = -INFINITY, w[kMergeWarps], ls = 0.f;
 #pragma unroll
-    for (int w = 0; w < kMergeWarps; ++w) ls += red[w][D];
-    for (int d = 2 * tid; d < D; d += 64 * kMergeWarps) {
+    for (int k = 0; k < kMergeWarps; ++k) top = fmaxf(top, red[k][D + 1]);
+#pragma unroll
+    for (int k = 0; k < kMergeWarps; ++k) {
+        w[k] = red[k][D + 1] == -INFINITY ? 0.f : ex2(red[k][D + 1] - top);
+        ls = fmaf(red[k][D], w[k], ls);
+    }
+    const float f = ls != 0.f ? 1.f / ls : 0.f;
+    for (int d = 2 * tid; d < D; d += 2 * kThreads) {
         float x = 0.f, y = 0.f;
 #pragma unroll
-        for (int w = 0; w < kMergeWarps; ++w) {
-            x += red[w][d];
-            y += red[w][d + 1];
+        for (int k = 0; k < kMergeWarps; ++k) {
+            x = fmaf(red[k][d], w[k], x);
+            y = fmaf(red[k][d + 1], w[k], y);
         }
-        const float f = ls != 0.f ? 1.f / ls : 0.f;
         *reinterpret_cast<uint32_t *>(o + d) = p.f16 ? pack2<true>(x * f, y * f) : pack2<false>(x * f, y * f);
     }
 }
@@ -757,12 +784,13 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const AppendCall p)
 }
 
 struct KvWs {
-    size_t cum, ml, o, own_ml, own_o, pre_ml, pre_o, total;
+    size_t ml, o, own_ml, own_o, pre_ml, pre_o, total;
     long long own_ctas, pre_ctas;   // row tiles of the tile kernel (0: the split kernel's)
-    int own_most, pre_most;         // their positions' parts at most
+    int own_n, pre_most;            // parts of the own positions; of a prefix at most
 };
 
-KvWs kv_ws(int B, int Hkv, int G, int D, long long M, int P)
+// T, window, sinks: what a row tile sees at most sets the parts that it is cut into.
+KvWs kv_ws(int B, int Hkv, int G, int D, long long M, int T, int W, int S, int P)
 {
     KvWs w = {};
     const long long rows = M * G, prows = B * rows;
@@ -770,15 +798,15 @@ KvWs kv_ws(int B, int Hkv, int G, int D, long long M, int P)
     const size_t slots = split_own ? (size_t)B * Hkv + (split_pre ? Hkv : 0) + kKvMaxCtas : 0;
     if (!split_own) {
         w.own_ctas = kv_row_tiles(rows, D) * Hkv * B;
-        w.own_most = kv_tile_most(w.own_ctas);
+        const long long seen = std::min<long long>((long long)W + S + 256 / G + 1, T);
+        w.own_n = kv_tile_splits(w.own_ctas, (seen + 127) / 128, rows <= 128);
     }
     if (P > 0 && !split_pre) {
         w.pre_ctas = kv_row_tiles(prows, D) * Hkv;
-        w.pre_most = kv_tile_most(w.pre_ctas);
+        w.pre_most = kv_tile_most(w.pre_ctas, false);
     }
-    const size_t own = w.own_most > 1 || P > 0 ? (size_t)w.own_most * Hkv * prows : 0, pre = (size_t)w.pre_most * Hkv * prows;
-    w.cum = 0;
-    w.ml = split_own ? align_up(((size_t)B + 1) * 4, 256) : 0;
+    const size_t own = w.own_n > 1 || P > 0 ? (size_t)w.own_n * Hkv * prows : 0, pre = (size_t)w.pre_most * Hkv * prows;
+    w.ml = 0;
     w.o = align_up(w.ml + slots * kKvFewRows * 8, 256);
     w.own_ml = align_up(w.o + slots * kKvFewRows * D * 4, 256);
     w.own_o = align_up(w.own_ml + own * 8, 256);
@@ -790,9 +818,9 @@ KvWs kv_ws(int B, int Hkv, int G, int D, long long M, int P)
 
 }  // namespace
 
-size_t kv_attn_workspace_bytes(int batch, int kv_heads, int group, int head_dim, long long M, int P)
+size_t kv_attn_workspace_bytes(int batch, int kv_heads, int group, int head_dim, long long M, int T, int window, int sinks, int P)
 {
-    return kv_ws(batch, kv_heads, group, head_dim, M, P).total;
+    return kv_ws(batch, kv_heads, group, head_dim, M, T, window ? window : kKvAll, sinks, P).total;
 }
 
 int launch_kv_append(const moe_kv &c, const moe_rows &k_new, const moe_rows &v_new, int M, const int32_t *pos,
@@ -839,33 +867,32 @@ int launch_kv_append(const moe_kv &c, const moe_rows &k_new, const moe_rows &v_n
 
 int launch_kv_attn(KvCall &p, void *ws, cudaStream_t stream)
 {
-    const KvWs w = kv_ws(p.B, p.Hkv, p.G, p.D, p.M, p.P);
+    const KvWs w = kv_ws(p.B, p.Hkv, p.G, p.D, p.M, p.T, p.W, p.S, p.P);
     uint8_t *base = static_cast<uint8_t *>(ws);
     auto f = [&](size_t at) { return reinterpret_cast<float *>(base + at); };
     p.split_own = w.own_ctas == 0;
     p.split_prefix = p.P > 0 && w.pre_ctas == 0;
     p.min_tiles = 1;
-    p.cum = reinterpret_cast<int *>(base + w.cum);
+    p.late = 0;
     p.part_ml = f(w.ml);
     p.part_o = f(w.o);
     p.own = {0, f(w.own_o), f(w.own_ml)};
     p.prefix = {0, f(w.pre_o), f(w.pre_ml)};
     const long long merged = (long long)p.B * p.M * p.Hq;
-    // positions that a row tile sees at most
-    const long long seen = std::min<long long>((long long)p.W + p.S + 256 / p.G + 1, p.T);
     if (w.pre_ctas) {
-        p.prefix.n = kv_tile_splits(w.pre_ctas, (p.P + 127) / 128);
+        p.prefix.n = kv_tile_splits(w.pre_ctas, (p.P + 127) / 128, false);
         const int rc = launch_kv_tiles(p, true, stream);
         if (rc) return rc;
+        p.late = 1;   // the own positions' kernel runs beside
     }
     int grid = 1;
     if (w.own_ctas) {
-        p.own.n = w.own_most == 1 ? 1 : kv_tile_splits(w.own_ctas, (seen + 127) / 128);
+        p.own.n = w.own_n;
         const int rc = launch_kv_tiles(p, false, stream);
         if (rc || (p.own.n == 1 && p.P == 0)) return rc;
     } else {
         // the line's length has to fit an int
-        const long long most = (seen / kKvTile + 2) * p.B * p.Hkv + (p.split_prefix ? ((long long)p.P / kKvTile + 1) * p.Hkv : 0);
+        const long long seen = std::min<long long>((long long)p.W + p.S + p.M, p.T), most = (seen / kKvTile + 2) * p.B * p.Hkv + (p.split_prefix ? ((long long)p.P / kKvTile + 1) * p.Hkv : 0);
         if (most > INT_MAX / 2) return MOE_ERR_UNSUPPORTED;
         int dev = 0;
         cudaError_t e = cudaGetDevice(&dev);

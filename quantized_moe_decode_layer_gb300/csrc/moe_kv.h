@@ -46,9 +46,9 @@ struct KvCall {
     int ring;                         // positions from T on lie in the slots from S on, again and again
     // split kernel: of the sequences' own positions, of the prefix's
     int split_own, split_prefix;
+    int late;                         // the call's second kernel: beside the first, whose end it waits for at its own
     int min_tiles;
     float *part_o, *part_ml;          // [slot][16][D], [slot][16][2]: unnormalised output; maximum (log2), sum
-    int *cum;                         // [B + 1]: tiles of the sequences before b, for one head
     // tile kernel: parts of the own positions, of the prefix's
     struct Parts {
         int n;                        // 0: not taken; own positions, 1 without a prefix: outputs are written
@@ -57,7 +57,7 @@ struct KvCall {
     long long timeout_ns;
 };
 
-size_t kv_attn_workspace_bytes(int batch, int kv_heads, int group, int head_dim, long long M, int P);
+size_t kv_attn_workspace_bytes(int batch, int kv_heads, int group, int head_dim, long long M, int T, int window, int sinks, int P);
 int launch_kv_append(const moe_kv &c, const moe_rows &k_new, const moe_rows &v_new, int M, const int32_t *pos,
                      const int32_t *counts, int *err, cudaStream_t stream);
 // Attention over a cache, or of a prompt.  p: q, k, v, the prefix, lengths, shapes, scale and output; the rest is set there.
@@ -65,7 +65,8 @@ int launch_kv_attn(KvCall &p, void *ws, cudaStream_t stream);
 // Tiles of 128 rows against the own positions, or the prefix.
 int launch_kv_tiles(const KvCall &p, bool prefix, cudaStream_t stream);
 long long kv_row_tiles(long long rows, int D);
-int kv_tile_most(long long ctas);                     // parts of a row tile's positions at most
-int kv_tile_splits(long long ctas, long long tiles);  // parts taken
+// Parts of a row tile's positions: at most, and taken.  `ragged`: lengths that the host does not know, few rows.
+int kv_tile_most(long long ctas, bool ragged);
+int kv_tile_splits(long long ctas, long long tiles, bool ragged);
 
 }  // namespace moe

@@ -431,7 +431,8 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    after_previous();
+    if (p.late) place_next();
+    else after_previous();
     fence_before();
     __syncthreads();
     fence_after();
@@ -862,7 +863,7 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
             if (!PAIR) {
                 asm volatile("bar.sync 1, 256;" ::: "memory");    // the references are final
                 const float end = refs[row];
-                sums[128 * xs + row] = ref == -INFINITY ? 0.f : l * ex2(ref - end);
+                sums[128 * xs + row] = ref == -INFINITY ? l : l * ex2(ref - end);   // (without a reference l is 0 or NaN)
                 ref = end;
                 asm volatile("bar.sync 1, 256;" ::: "memory");
                 l = sums[row] + sums[128 + row];
@@ -882,6 +883,7 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
             units += 2 * it.nt * UPT;
             const bool live = PREFIX || p.by_g(r) < it.cnt;
             const float inv = live && nt > 0 && l != 0.f ? 1.f / l : 0.f;
+            if (l != l && ref == -INFINITY) ref = 0.f;   // a row of NaN alone has no maximum, but is not empty
             if (!PREFIX && tp.omap) {
                 // 64 columns at a time into the stream's box, and from there by TMA while the next item starts
                 uint8_t *box = sm + L::stage + xs * kBox;
@@ -963,6 +965,7 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
         }
         if (!PREFIX && tp.omap && (tid & 127) == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
+    if (p.late) wait_for_previous();   // the end of this kernel means the end of the one before
     fence_before();
     __syncthreads();
     if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
@@ -1021,13 +1024,18 @@ int row_tile(int D) { return D == 256 ? kRows : 2 * kRows; }
 long long kv_row_tiles(long long rows, int D) { return (rows + row_tile(D) - 1) / row_tile(D); }
 
 // Parts that the positions of each row tile are cut into: as many as fill the SMs in as few
-// turns as possible.  `ctas` row tiles of all heads, `tiles` tiles of positions each.
-int kv_tile_most(long long ctas) { return (int)std::max<long long>(1, 3 * 152 / ctas); }
-int kv_tile_splits(long long ctas, long long tiles)
+// turns as possible.  `ctas` row tiles of all heads, `tiles` tiles of positions each; an item costs about four
+// tiles besides.  Where rows are few (a cache's attention: bound by HBM, loads run ahead into the next item) and more
+// than the SMs, shorter items, none below four tiles, even out what the lengths, which the host does not know, differ by
+// (256 of 100 to 2000 positions: 80 -> 56 us).
+int kv_tile_most(long long ctas, bool ragged) { return (int)std::max<long long>(1, (ragged ? 4 : 3) * 152 / ctas); }
+int kv_tile_splits(long long ctas, long long tiles, bool ragged)
 {
+    const int most = kv_tile_most(ctas, ragged);
+    if (ragged && ctas >= 152) return (int)std::max<long long>(1, std::min<long long>(most, tiles / 4));
     int best = 1;
     double cost = 1e30;
-    for (int s = 1; s <= kv_tile_most(ctas) && s <= tiles; ++s) {
+    for (int s = 1; s <= most && s <= tiles; ++s) {
         const double turns = (double)((ctas * s + 151) / 152), c = turns * ((double)((tiles + s - 1) / s) + 4.0) + 0.05 * s;
         if (c < cost) {
             cost = c;
