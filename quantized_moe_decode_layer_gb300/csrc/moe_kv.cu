@@ -158,6 +158,7 @@ struct Lay {
     static constexpr int misc = probs + (NQ + 1) * (int)sizeof(Problem);   // maxima and sums of the position groups
     static constexpr int cum = misc + (2 * WK * RB + 8) * 4;               // tiles before a sequence; its first row's position; its rows
     static constexpr int total(int B) { return cum + (B + 1) * 4 + B * 5; }
+    static_assert(q % 128 == 0 && probs % 4 == 0 && misc % 4 == 0 && cum % 4 == 0, "alignment");
 };
 
 // 16-byte chunk c of row r of a tile, swizzled so that eight rows' equal chunks lie in eight banks' groups.

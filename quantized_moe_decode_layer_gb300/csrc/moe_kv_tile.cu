@@ -51,25 +51,32 @@ constexpr int kItems = 4, kItemBytes = 48;   // items known ahead
 template <int D>
 struct TLay {
     static constexpr bool kPair = D <= 128;                   // two row tiles a CTA
+    // S in tensor memory: one for each stream, or three that all steps take in turn, so that a stream's next scores come
+    // before its P has been read
+    static constexpr bool kTurns = D == 64;
+    static constexpr int NB = kTurns ? 3 : 2;
+    static constexpr bool kAhead = !kPair || kTurns;          // the next tile's scores come before this one's values
     static constexpr int NQ = kPair ? 2 : 1;
     static constexpr int RT = NQ * kRows;
     static constexpr int kUnit = D == 64 ? kBox : 2 * kBox;   // 128 positions x min(D, 128)
     static constexpr int UPT = D == 256 ? 2 : 1;              // units of a tile of keys or values
-        static constexpr int NU = 4;                              // (5 or 8 measured no faster)
+        static constexpr int NU = D == 64 ? 8 : 4;                // (5 at 128, 256 measured no faster)
     static constexpr int q = 0;
     static constexpr int ring = NQ * (D / 64) * kBox;
     static constexpr int stage = ring + NU * kUnit;           // outputs on their way, a box a stream
     static constexpr int bars = stage + 2 * kBox;
-    static constexpr int kBars = 2 * NU + 2 * 4 + 8 + 3 + 2 * kItems;
+    static constexpr int kBars = 2 * NU + 3 * NB + 2 + 8 + 3 + 2 * kItems;
     static constexpr int misc = bars + kBars * 8;             // tensor-memory address, abort flag
     static constexpr int refs = misc + 8;                     // [128] references, [2][128] sums (one row tile)
-    static constexpr int items = refs + 3 * 128 * 4;          // [kItems] items
+    static constexpr int items = (refs + 3 * 128 * 4 + 15) / 16 * 16;   // [kItems] items, read 16 bytes at a time
     static constexpr int total = items + kItems * kItemBytes;
+    static_assert(bars % 1024 == 0 && misc % 8 == 0 && refs % 4 == 0 && items % 16 == 0 && kItemBytes % 16 == 0, "alignment");
 };
 static_assert(TLay<64>::total + 1024 <= kSmemMax && TLay<128>::total + 1024 <= kSmemMax && TLay<256>::total + 1024 <= kSmemMax,
               "shared memory");
-// tensor memory: S of the streams at columns 0 and 128, O from 256 on, P over S
+// tensor memory: S at columns 0 and 128 (and 384), O from 256 on, P over S
 constexpr uint32_t kTmemCols = 512;
+__device__ __forceinline__ uint32_t s_col(int b) { return b == 2 ? 384u : 128u * (uint32_t)b; }
 // registers a thread: launched with 168; the softmax warps take what the others leave
 constexpr int kRegsSoft = 208, kRegsRest = 88;
 static_assert(256 * kRegsSoft + 128 * kRegsRest <= kTThreads * 168, "registers");
@@ -283,9 +290,9 @@ __device__ __forceinline__ int rows_of(const KvCall &p, int b, int &p0, bool &ba
 }
 
 // The order in which tiles of keys and values are loaded: as the steps first use them.
-// Two row tiles: K0 V0 K1 V1 ...; one: K0 K1 V0 K2 V1 ... (both streams' scores come first).
-template <bool PAIR>
-__device__ __forceinline__ int v_order(int t, int nt) { return PAIR ? 2 * t + 1 : t == nt - 1 ? 2 * nt - 1 : 2 * t + 2; }
+// K0 V0 K1 V1 ..., or, ahead, K0 K1 V0 K2 V1 ...
+template <bool AHEAD>
+__device__ __forceinline__ int v_order(int t, int nt) { return !AHEAD ? 2 * t + 1 : t == nt - 1 ? 2 * nt - 1 : 2 * t + 2; }
 
 // A CTA's worth of work: row tile(s) r0 .. of one head against nt tiles of positions:
 // tiles i0 .. i0 + nt - 1 of the list that has the first nsink tiles and then those from kt_lo on.
@@ -389,17 +396,18 @@ template <bool F16, int D, bool PREFIX>
 __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_constant__ TileParams tp)
 {
     using L = TLay<D>;
-    constexpr bool PAIR = L::kPair;
-    constexpr int KS = kKeys / 2;
+    constexpr bool PAIR = L::kPair, AHEAD = L::kAhead, TURNS = L::kTurns;
+    constexpr int KS = kKeys / 2, NB = L::NB;
     constexpr int NU = L::NU, UPT = L::UPT, RT = L::RT;
     const KvCall &p = tp.c;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;   // warp: uniform, as the products' operands have to be
-    // barriers, each two one for a stream: S is there; P is there; P V is done; O has been read
+    // barriers: S is there, P is there, P V is done (one for each S: none gets two phases ahead of who waits); O has been
+    // read (one for each stream)
     uint64_t *full = reinterpret_cast<uint64_t *>(sm + L::bars), *empty = full + NU;
-    uint64_t *s_full = empty + NU, *p_full = s_full + 2, *o_done = p_full + 2,
-             *o_free = o_done + 2, *ref_rdy = o_free + 2, *q_full = ref_rdy + 8, *q_free = q_full + 1, *all_done = q_free + 1, *i_ready = all_done + 1, *i_read = i_ready + kItems;
+    uint64_t *s_full = empty + NU, *p_full = s_full + NB, *o_done = p_full + NB,
+             *o_free = o_done + NB, *ref_rdy = o_free + 2, *q_full = ref_rdy + 8, *q_free = q_full + 1, *all_done = q_free + 1, *i_ready = all_done + 1, *i_read = i_ready + kItems;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + L::misc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     float *refs = reinterpret_cast<float *>(sm + L::refs), *sums = refs + 128;
@@ -410,10 +418,12 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
             bar_init(su32(&empty[s]), 1);
         }
         for (int s = 0; s < 2; ++s) {
+            bar_init(su32(&o_free[s]), PAIR ? 4 : 8);
+        }
+        for (int s = 0; s < NB; ++s) {
             bar_init(su32(&s_full[s]), 1);
             bar_init(su32(&p_full[s]), 4);
             bar_init(su32(&o_done[s]), 1);
-            bar_init(su32(&o_free[s]), PAIR ? 4 : 8);
         }
         for (int s = 0; s < 8; ++s) bar_init(su32(&ref_rdy[s]), 1);
         for (int s = 0; s < kItems; ++s) {
@@ -476,9 +486,9 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                             }
                         }
                     };
-                    if (!PAIR && it.nt > 0) load(&tp.tk, 0);
+                    if (AHEAD && it.nt > 0) load(&tp.tk, 0);
                     for (int t = 0; t < it.nt && go; ++t) {
-                        const int kt = !PAIR ? t + 1 : t;
+                        const int kt = AHEAD ? t + 1 : t;
                         if (kt < it.nt) load(&tp.tk, kt);
                         if (go) load(&tp.tv, t);
                     }
@@ -595,7 +605,9 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                     }
                 };
                 Place base = {0, 0};
-                int qn = 0, turns[2] = {0, 0}, done[2] = {0, 0};   // items; items and steps of the streams before this item
+                int qn = 0, turns[2] = {0, 0};    // items, those of each stream
+                int sb = 0, pb = 0, pphase = 0;   // taken in turn: S of the next scores; P of the next values, with its phase
+                int phase0 = 0, phase1 = 0;       // else the phases of the streams' P
                 for (int n = 0; n < mine && go; ++n) {
                     Item it;
                     go = items.get(n, it, abort_flag, p);
@@ -603,18 +615,19 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                     if (!go) break;
                     const int nt = it.nt;
                     if (nt == 0) continue;
-                    const int nsteps = PAIR ? 2 * nt : nt;
                     auto work = [&](auto duo_v) {
                     constexpr bool duo = decltype(duo_v)::value;   // a pair's second stream has something to do
-                    const int last = PAIR && !duo ? nsteps - 2 : nsteps - 1;
-                    Place kp = base, vp = base;         // of the next tile of keys, of values
-                    vp.move(!PAIR && nt > 1 ? 2 * UPT : UPT);
-                    auto scores = [&](int i, int xs) {
-                        const int t = PAIR ? i >> 1 : i;
+                    constexpr bool both = !PAIR || duo;            // the streams take turns
+                    const int n = duo ? 2 * nt : nt;               // steps
+                    Place kp = base, vp = base;                    // of the next tile of keys, of values
+                    vp.move(AHEAD && nt > 1 ? 2 * UPT : UPT);
+                    auto scores = [&](int j, int xs) {
                         Place at = kp;
+                        const int sn = TURNS ? sb : xs;
+                        const uint32_t to = tmem + s_col(sn);
 #pragma unroll
                         for (int u = 0; u < UPT; ++u) {
-                            if (!PAIR || xs == 0) wait(&full[at.slot], at.phase);
+                            if (!duo || xs == 0) wait(&full[at.slot], at.phase);
                             if (!go) return;
                             fence_after();
                             const uint32_t a0 = qd + (uint32_t)((((PAIR ? xs : 0) * (D / 64) + 2 * u) * kBox) >> 4);
@@ -622,19 +635,20 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
 #pragma unroll
                             for (int k = 0; k < (D < 128 ? D : 128) / 16; ++k) {
                                 const uint32_t off = (uint32_t)((k >> 2) * kBox + (k & 3) * 32) >> 4;
-                                umma_ss(tmem + 128u * xs, a0 + off, b0 + off, id_s, (u | k) != 0 ? 1u : 0u);
+                                umma_ss(to, a0 + off, b0 + off, id_s, (u | k) != 0 ? 1u : 0u);
                             }
                             if (!duo || xs == 1) umma_commit(su32(&empty[at.slot]));
                             at.move(1);
                         }
-                        umma_commit(su32(&s_full[xs]));
-                        if (i == last) umma_commit(su32(q_free));
-                        if (!duo || xs == 1) kp.move(!PAIR && t == 0 ? UPT : 2 * UPT);
+                        umma_commit(su32(&s_full[sn]));
+                        if (j == n - 1) umma_commit(su32(q_free));
+                        if (TURNS && ++sb == NB) sb = 0;
+                        if (!duo || xs == 1) kp.move(AHEAD && (duo ? j < 2 : j < 1) ? UPT : 2 * UPT);
                     };
-                    auto values = [&](int i, int xs) {
-                        const int t = PAIR ? i >> 1 : i, step = done[xs] + (i >> 1);
+                    auto values = [&](int j, int xs) {
+                        const int t = duo ? j >> 1 : j;
                         if (t == 0 && turns[xs] > 0) wait(&o_free[PAIR ? xs : 0], turns[xs] - 1);
-                        if (!PAIR || xs == 0) {
+                        if (!duo || xs == 0) {
                             Place at = vp;
 #pragma unroll
                             for (int u = 0; u < UPT; ++u) {
@@ -642,40 +656,48 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                                 at.move(1);
                             }
                         }
-                        wait(&p_full[xs], step);
+                        const int pn = TURNS ? pb : xs;
+                        wait(&p_full[pn], TURNS ? pphase : xs ? phase1 : phase0);
                         if (!go) return;
                         fence_after();
                         Place at = vp;
+                        const uint32_t from = tmem + s_col(pn);
 #pragma unroll
                         for (int u = 0; u < UPT; ++u) {
                             const uint32_t o = tmem + 256u + (PAIR ? (uint32_t)(D * xs) : 128u * u);
                             const uint32_t b0 = desc_mn(ring + at.slot * L::kUnit);
 #pragma unroll
                             for (int k = 0; k < kKeys / 16; ++k)
-                                umma_ts(o, tmem + 128u * xs + 8u * k, b0 + 128u * k, id_o, (t | k) != 0 ? 1u : 0u);
+                                umma_ts(o, from + 8u * k, b0 + 128u * k, id_o, (t | k) != 0 ? 1u : 0u);
                             if (!duo || xs == 1) umma_commit(su32(&empty[at.slot]));
                             at.move(1);
                         }
-                        umma_commit(su32(&o_done[xs]));
-                        if (!duo || xs == 1) vp.move(!PAIR && t + 2 >= nt ? UPT : 2 * UPT);
+                        umma_commit(su32(&o_done[pn]));
+                        if (!TURNS) {
+                            if (xs) phase1 ^= 1;
+                            else phase0 ^= 1;
+                        } else if (++pb == NB) {
+                            pb = 0;
+                            pphase ^= 1;
+                        }
+                        if (!duo || xs == 1) vp.move(AHEAD && t + 2 >= nt ? UPT : 2 * UPT);
                     };
-                    auto step = [&](int i, int xs) {
-                        values(i, xs);
-                        if (go && i + 2 <= last) scores(i + 2, xs);
+                    constexpr int second = both ? 1 : 0, ahead = TURNS || both ? NB : 1;   // (a stream alone with its S waits for its P)
+                    auto step = [&](int j, int xs) {
+                        values(j, xs);
+                        if (go && j + ahead < n) scores(j + ahead, both && TURNS ? xs ^ 1 : xs);
                     };
                     wait(q_full, qn);
                     if (go) scores(0, 0);
-                    constexpr bool both = !PAIR || duo;
-                    if (go && both && last > 0) scores(1, 1);
+                    if (go && ahead > 1 && n > 1) scores(1, second);
+                    if (go && ahead > 2 && n > 2) scores(2, 0);
 #pragma unroll 1
-                    for (int i = 0; i <= last && go; i += 2) {
-                        step(i, 0);
-                        if (go && both && i < last) step(i + 1, 1);
+                    for (int j = 0; j < n && go; j += 2) {
+                        step(j, 0);
+                        if (go && j + 1 < n) step(j + 1, second);
                     }
                     for (int j = 0; j < (2 * nt) % NU; ++j) base.move(UPT);
                     base.phase ^= (2 * nt / NU * UPT) & 1;
-                    done[0] += PAIR ? nt : (nt + 1) / 2;
-                    done[1] += PAIR ? (duo ? nt : 0) : nt / 2;
                     ++turns[0];
                     turns[1] += duo;
                     ++qn;
@@ -694,16 +716,16 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
         // --------------------------------------------------------------- softmax
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
         const int xs = warp >> 2, w = warp & 3, row = tid & 127;
-        const uint32_t lanes = tmem + ((uint32_t)(32 * w) << 16), sc = lanes + 128u * xs;
+        const uint32_t lanes = tmem + ((uint32_t)(32 * w) << 16);
         const uint32_t oc = lanes + 256u + (PAIR ? (uint32_t)(D * xs) : 0u);
         const float c = p.c;
         const uint64_t c2 = two(c, c);
-        int done[2] = {0, 0}, units = 0;   // steps of the streams, units of the ring before this item
+        int done[2] = {0, 0}, all = 0, units = 0;   // steps of the streams and of both, units of the ring before this item
         bool go = true;
         auto wait = [&](uint64_t *bar, int parity) {
             go = __all_sync(0xFFFFFFFFu, go && bar_wait(su32(bar), (unsigned)parity & 1u, abort_flag, p));
         };
-        // (after a wait has given up the streams of one row tile still meet at each item's barriers)
+        // (after a wait has given up the streams still meet at each item's barriers)
 #pragma unroll 1
         for (int n = 0; n < mine; ++n) {
             Item it;
@@ -712,7 +734,8 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                 go = __all_sync(0xFFFFFFFFu, go && ok);
                 if (lane == 0) items.done(n);
             }
-            const int nt = PAIR && xs == 1 && !two_tiles(it) ? 0 : it.nt, nsteps = PAIR ? 2 * nt : nt, r = it.r0 + (PAIR ? 128 * xs : 0) + row;
+            const bool duo = two_tiles(it);
+            const int nt = PAIR && xs == 1 && !duo ? 0 : it.nt, nsteps = PAIR ? 2 * nt : nt, r = it.r0 + (PAIR ? 128 * xs : 0) + row;
             const size_t part0 = ((size_t)it.z * p.Hkv + it.g) * ((size_t)p.B * p.M * p.G) + (PREFIX ? 0 : (size_t)it.b * p.M * p.G);
             // The row is at position pos.  Slot s has position s (s < S), else s + off (s >= sl),
             // else s + off + R; it is seen if pos - W < position <= pos, or s < S.
@@ -734,14 +757,16 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
             float l = 0.f, ref = -INFINITY;    // of the row, as the stream knows them
 #pragma unroll 1
             for (int i = xs; i < nsteps && go; i += 2) {
-                const int t = PAIR ? i >> 1 : i, key = it.first_key(t), step = done[xs] + (i >> 1);
-                wait(&s_full[xs], step);
+                const int t = PAIR ? i >> 1 : i, key = it.first_key(t);
+                const int turn = TURNS ? all + (duo ? i : t) : done[xs] + (i >> 1), sb = TURNS ? turn % NB : xs;   // the step's turn at its S
+                const uint32_t sc = lanes + s_col(sb);
+                wait(&s_full[sb], TURNS ? turn / NB : turn);
                 if (!go) break;
                 fence_after();
                 if (!PREFIX && valid - key < kKeys && (!PAIR || xs == 0)) {
                     // values behind the sequence's last position may be anything: zeros
                     const int gone = valid - key;
-                    const int n0 = units + UPT * v_order<PAIR>(t, nt);
+                    const int n0 = units + UPT * v_order<AHEAD>(t, nt);
 #pragma unroll 1
                     for (int u = n0; u < n0 + UPT; ++u) {
                         wait(&full[u % NU], u / NU);
@@ -827,8 +852,12 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                 ref = now;
                 if (__any_sync(0xFFFFFFFFu, raise) && t > 0) {
                     // O, which has the tiles up to the one before, in the new reference's units
-                    if (PAIR) wait(&o_done[xs], step - 1);
-                    else wait(&o_done[xs ^ 1], done[xs ^ 1] + ((i - 1) >> 1));
+                    if (TURNS) {
+                        const int before = turn - (duo ? 2 : 1);
+                        wait(&o_done[before % NB], before / NB);
+                    } else {
+                        wait(&o_done[PAIR ? xs : xs ^ 1], PAIR ? turn - 1 : done[xs ^ 1] + ((i - 1) >> 1));
+                    }
                     if (!go) break;
                     fence_after();
                     const float f = raise ? ex2(was - now) : 1.f;
@@ -853,7 +882,7 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                 tmem_wait_st();
                 fence_before();
                 __syncwarp();
-                if (lane == 0) bar_arrive(su32(&p_full[xs]));
+                if (lane == 0) bar_arrive(su32(&p_full[sb]));
             }
 
             // -------------------------------------------------------------- outputs
@@ -870,16 +899,23 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                 if (nt == 0) l = 0.f, ref = -INFINITY;
             }
             if (nt > 0) {
-                if (PAIR) {
+                if (TURNS) {
+                    const int last = all + (duo ? 2 * nt - 2 + xs : nt - 1);
+                    wait(&o_done[last % NB], last / NB);
+                } else if (PAIR) {
                     wait(&o_done[xs], done[xs] + nt - 1);
                 } else {
-                    if (nsteps > 1) wait(&o_done[nsteps & 1], done[nsteps & 1] + ((nsteps - 2) >> 1));
-                    wait(&o_done[(nsteps - 1) & 1], done[(nsteps - 1) & 1] + ((nsteps - 1) >> 1));
+                    // the last step's, and the one's before (one of them is the other stream's, whose phases are not followed else)
+                    if (nt > 1) wait(&o_done[nt & 1], done[nt & 1] + ((nt - 2) >> 1));
+                    wait(&o_done[(nt - 1) & 1], done[(nt - 1) & 1] + ((nt - 1) >> 1));
                 }
                 if (go) fence_after();
             }
+            // A second stream without work stays behind the first: its next wait is for the phase after this item's.
+            if (TURNS && !duo && it.nt > 0) asm volatile("bar.sync 1, 256;" ::: "memory");
             done[0] += PAIR ? nt : (nt + 1) / 2;
             done[1] += PAIR ? nt : nt / 2;
+            all += duo ? 2 * it.nt : it.nt;
             units += 2 * it.nt * UPT;
             const bool live = PREFIX || p.by_g(r) < it.cnt;
             const float inv = live && nt > 0 && l != 0.f ? 1.f / l : 0.f;
