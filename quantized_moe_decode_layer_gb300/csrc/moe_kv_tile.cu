@@ -125,6 +125,14 @@ __device__ __forceinline__ bool bar_test(uint32_t b, unsigned parity)
                  : "memory");
     return done != 0;
 }
+// At a CTA's end: a phase that copies or products in flight complete.  A second at least, whatever the time limit of the
+// waits: what is in flight lands in microseconds, and must not land after the CTA.
+__device__ __forceinline__ void bar_drain(uint32_t b, unsigned parity, const KvCall &c)
+{
+    const unsigned long long t0 = gtime();
+    while (!bar_test(b, parity) && (long long)(gtime() - t0) <= max(c.timeout_ns, 1000000000LL)) {}
+}
+
 // Bounded wait on an mbarrier phase; gives up when the CTA's abort flag is
 // set, or sets it (and the error word) when the time runs out.
 __device__ __forceinline__ bool bar_wait(uint32_t b, unsigned parity, volatile int *abort, const KvCall &c)
@@ -494,11 +502,7 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                     }
                 }
                 // every copy issued has landed before the CTA ends
-                const unsigned long long t0 = gtime();
-                for (int s = 0; s < NU && s < n; ++s) {
-                    const unsigned last = (unsigned)((n - 1 - s) / NU) & 1u;
-                    while (!bar_test(su32(&full[s]), last) && (long long)(gtime() - t0) <= p.timeout_ns) {}
-                }
+                for (int s = 0; s < NU && s < n; ++s) bar_drain(su32(&full[s]), (unsigned)((n - 1 - s) / NU) & 1u, p);
             }
         } else if (warp >= 10) {
             // ---------------------------------------------------- q, packed into rows
@@ -580,10 +584,7 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                 __syncwarp();
             }
             // the last copies have landed before the CTA ends
-            if (tp.qmap && t == 0 && qn > 0) {
-                const unsigned long long t0 = gtime();
-                while (!bar_test(su32(q_full), (unsigned)(qn - 1) & 1u) && (long long)(gtime() - t0) <= p.timeout_ns) {}
-            }
+            if (tp.qmap && t == 0 && qn > 0) bar_drain(su32(q_full), (unsigned)(qn - 1) & 1u, p);
         } else {
             // ---------------------------------------------------------- products
             // One thread, and as few instructions between the products as can be: they are issued in order,
@@ -707,8 +708,7 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                 }
                 // every product issued has finished before tensor memory is freed
                 umma_commit(su32(all_done));
-                const unsigned long long t0 = gtime();
-                while (!bar_test(su32(all_done), 0u) && (long long)(gtime() - t0) <= p.timeout_ns) {}
+                bar_drain(su32(all_done), 0u, p);
             }
         }
         __syncwarp();
