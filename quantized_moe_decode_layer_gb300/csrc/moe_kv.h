@@ -12,7 +12,7 @@ constexpr int kKvMaxCtas = 4 * kMaxCtas;
 constexpr int kKvMaxPos = 1 << 30;    // positions of a sequence whose cache is a ring
 constexpr int kKvAll = 1 << 30;       // window of a sequence that sees everything
 
-// Division of 0 <= x < 2^31 by a number known to the host.
+// Division of 0 <= x < 2^31 by a number of heads (at most 2^20), exactly: x m / 2^s.
 struct Div {
     uint32_t m;
     int s;
@@ -47,7 +47,6 @@ struct KvCall {
     // split kernel: of the sequences' own positions, of the prefix's
     int split_own, split_prefix;
     int late;                         // the call's second kernel: beside the first, whose end it waits for at its own
-    int min_tiles;
     float *part_o, *part_ml;          // [slot][16][D], [slot][16][2]: unnormalised output; maximum (log2), sum
     // tile kernel: parts of the own positions, of the prefix's
     struct Parts {

@@ -1,26 +1,32 @@
 // Attention of many rows against one key/value head, on the 5th-generation tensor
 // cores (tcgen05, accumulators in tensor memory): prompts with a sliding window
-// and first positions, and a batch's rows against the prefix that they share.
+// and first positions, more than 16 rows of a cache's sequence, and a batch's rows against the prefix that they share.
 //
 // The rows that share a key/value head (query rows times heads per key/value
 // head) are packed into tiles of 128, the positions that any of a CTA's rows
-// sees into tiles of 128 positions: the first ones, then the window.  Per tile
-// of positions
+// sees into tiles of 128 slots: the first ones, then the window (in a ring, the slots that it
+// lies in; each slot's position follows from where the window starts).  Per tile of positions
 //     S = Q K^T            128 x 128, fp32 in tensor memory
 //     P = 2^(c S - ref)    16 bits, in tensor memory over S;  l += row sums
 //     O += P V             128 x D, fp32 in tensor memory
 // with ref a running maximum that follows only when the true one is above it by
 // more than 8: the weights stay below 2^8, far from any type's end, and O is
-// hardly ever rescaled.
+// hardly ever rescaled.  A weight is rounded to 16 bits for its product, an error of the size of the output's own
+// rounding; l has it as it was.
 //
 // Two streams of steps alternate on the tensor core, so that it has one's
 // products while the other's softmax runs: with D <= 128 two row tiles
-// (tensor memory holds two S and two O), with D = 256 the even and the odd position
+// (tensor memory holds their S and two O), with D = 256 the even and the odd position
 // tiles of one row tile (two S, one O); those hand the reference on from
-// one to the other.  Warps 0-3 and 4-7 are the streams' softmax (thread = row),
-// warp 8 loads by TMA (boxes of 128 positions x 64 elements, 128-byte swizzle),
-// warp 9 issues the products.  V is taken as it lies, [position][d] with d
-// contiguous (an MN-major operand), P from tensor memory.
+// one to the other.  A CTA is persistent and goes through items (row tiles of a head) that warp 11 finds
+// ahead of the others.  Warps 0-3 and 4-7 are the streams' softmax (thread = row),
+// warp 8 loads K and V by TMA (boxes of 128 positions x 64 elements, 128-byte swizzle), one thread of
+// warp 9 issues the products, warps 10 and 11 load q.  V is taken as it lies, [position][d] with d
+// contiguous (an MN-major operand), P from tensor memory; outputs leave through a box in shared memory.
+//
+// Bound by the tensor core with D = 256 (a prompt of 16K, window 4096, 16/2/256: 0.59 to 0.61 ms, 1.59 PFLOP/s of the
+// pairs that are seen, 84 % of the measured rate), by a stream's chain of S, softmax and P V with D = 128 (32/8/128:
+// 0.68 to 0.72 ms), by the softmax warps with D = 64 (32/8/64: 0.52 ms).
 //
 // Every wait is bounded; one that runs out sets *err, the roles stop, the CTA waits
 // (bounded) for its copies and products and frees its tensor memory.
@@ -410,12 +416,14 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
     const KvCall &p = tp.c;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;   // warp: uniform, as the products' operands have to be
+    // (warp: uniform, as the products' operands have to be)
+    const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
     // barriers: S is there, P is there, P V is done (one for each S: none gets two phases ahead of who waits); O has been
     // read (one for each stream)
     uint64_t *full = reinterpret_cast<uint64_t *>(sm + L::bars), *empty = full + NU;
     uint64_t *s_full = empty + NU, *p_full = s_full + NB, *o_done = p_full + NB,
-             *o_free = o_done + NB, *ref_rdy = o_free + 2, *q_full = ref_rdy + 8, *q_free = q_full + 1, *all_done = q_free + 1, *i_ready = all_done + 1, *i_read = i_ready + kItems;
+             *o_free = o_done + NB, *ref_rdy = o_free + 2, *q_full = ref_rdy + 8, *q_free = q_full + 1, *all_done = q_free + 1,
+             *i_ready = all_done + 1, *i_read = i_ready + kItems;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + L::misc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     float *refs = reinterpret_cast<float *>(sm + L::refs), *sums = refs + 128;
@@ -617,91 +625,91 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                     const int nt = it.nt;
                     if (nt == 0) continue;
                     auto work = [&](auto duo_v) {
-                    constexpr bool duo = decltype(duo_v)::value;   // a pair's second stream has something to do
-                    constexpr bool both = !PAIR || duo;            // the streams take turns
-                    const int n = duo ? 2 * nt : nt;               // steps
-                    Place kp = base, vp = base;                    // of the next tile of keys, of values
-                    vp.move(AHEAD && nt > 1 ? 2 * UPT : UPT);
-                    auto scores = [&](int j, int xs) {
-                        Place at = kp;
-                        const int sn = TURNS ? sb : xs;
-                        const uint32_t to = tmem + s_col(sn);
-#pragma unroll
-                        for (int u = 0; u < UPT; ++u) {
-                            if (!duo || xs == 0) wait(&full[at.slot], at.phase);
-                            if (!go) return;
-                            fence_after();
-                            const uint32_t a0 = qd + (uint32_t)((((PAIR ? xs : 0) * (D / 64) + 2 * u) * kBox) >> 4);
-                            const uint32_t b0 = desc_k(ring + at.slot * L::kUnit);
-#pragma unroll
-                            for (int k = 0; k < (D < 128 ? D : 128) / 16; ++k) {
-                                const uint32_t off = (uint32_t)((k >> 2) * kBox + (k & 3) * 32) >> 4;
-                                umma_ss(to, a0 + off, b0 + off, id_s, (u | k) != 0 ? 1u : 0u);
-                            }
-                            if (!duo || xs == 1) umma_commit(su32(&empty[at.slot]));
-                            at.move(1);
-                        }
-                        umma_commit(su32(&s_full[sn]));
-                        if (j == n - 1) umma_commit(su32(q_free));
-                        if (TURNS && ++sb == NB) sb = 0;
-                        if (!duo || xs == 1) kp.move(AHEAD && (duo ? j < 2 : j < 1) ? UPT : 2 * UPT);
-                    };
-                    auto values = [&](int j, int xs) {
-                        const int t = duo ? j >> 1 : j;
-                        if (t == 0 && turns[xs] > 0) wait(&o_free[PAIR ? xs : 0], turns[xs] - 1);
-                        if (!duo || xs == 0) {
-                            Place at = vp;
-#pragma unroll
+                        constexpr bool duo = decltype(duo_v)::value;   // a pair's second stream has something to do
+                        constexpr bool both = !PAIR || duo;            // the streams take turns
+                        const int n = duo ? 2 * nt : nt;               // steps
+                        Place kp = base, vp = base;                    // of the next tile of keys, of values
+                        vp.move(AHEAD && nt > 1 ? 2 * UPT : UPT);
+                        auto scores = [&](int j, int xs) {
+                            Place at = kp;
+                            const int sn = TURNS ? sb : xs;
+                            const uint32_t to = tmem + s_col(sn);
+    #pragma unroll
                             for (int u = 0; u < UPT; ++u) {
-                                wait(&full[at.slot], at.phase);
+                                if (!duo || xs == 0) wait(&full[at.slot], at.phase);
+                                if (!go) return;
+                                fence_after();
+                                const uint32_t a0 = qd + (uint32_t)((((PAIR ? xs : 0) * (D / 64) + 2 * u) * kBox) >> 4);
+                                const uint32_t b0 = desc_k(ring + at.slot * L::kUnit);
+    #pragma unroll
+                                for (int k = 0; k < (D < 128 ? D : 128) / 16; ++k) {
+                                    const uint32_t off = (uint32_t)((k >> 2) * kBox + (k & 3) * 32) >> 4;
+                                    umma_ss(to, a0 + off, b0 + off, id_s, (u | k) != 0 ? 1u : 0u);
+                                }
+                                if (!duo || xs == 1) umma_commit(su32(&empty[at.slot]));
                                 at.move(1);
                             }
+                            umma_commit(su32(&s_full[sn]));
+                            if (j == n - 1) umma_commit(su32(q_free));
+                            if (TURNS && ++sb == NB) sb = 0;
+                            if (!duo || xs == 1) kp.move(AHEAD && (duo ? j < 2 : j < 1) ? UPT : 2 * UPT);
+                        };
+                        auto values = [&](int j, int xs) {
+                            const int t = duo ? j >> 1 : j;
+                            if (t == 0 && turns[xs] > 0) wait(&o_free[PAIR ? xs : 0], turns[xs] - 1);
+                            if (!duo || xs == 0) {
+                                Place at = vp;
+    #pragma unroll
+                                for (int u = 0; u < UPT; ++u) {
+                                    wait(&full[at.slot], at.phase);
+                                    at.move(1);
+                                }
+                            }
+                            const int pn = TURNS ? pb : xs;
+                            wait(&p_full[pn], TURNS ? pphase : xs ? phase1 : phase0);
+                            if (!go) return;
+                            fence_after();
+                            Place at = vp;
+                            const uint32_t from = tmem + s_col(pn);
+    #pragma unroll
+                            for (int u = 0; u < UPT; ++u) {
+                                const uint32_t o = tmem + 256u + (PAIR ? (uint32_t)(D * xs) : 128u * u);
+                                const uint32_t b0 = desc_mn(ring + at.slot * L::kUnit);
+    #pragma unroll
+                                for (int k = 0; k < kKeys / 16; ++k)
+                                    umma_ts(o, from + 8u * k, b0 + 128u * k, id_o, (t | k) != 0 ? 1u : 0u);
+                                if (!duo || xs == 1) umma_commit(su32(&empty[at.slot]));
+                                at.move(1);
+                            }
+                            umma_commit(su32(&o_done[pn]));
+                            if (!TURNS) {
+                                if (xs) phase1 ^= 1;
+                                else phase0 ^= 1;
+                            } else if (++pb == NB) {
+                                pb = 0;
+                                pphase ^= 1;
+                            }
+                            if (!duo || xs == 1) vp.move(AHEAD && t + 2 >= nt ? UPT : 2 * UPT);
+                        };
+                        constexpr int second = both ? 1 : 0, ahead = TURNS || both ? NB : 1;   // (a stream alone with its S waits for its P)
+                        auto step = [&](int j, int xs) {
+                            values(j, xs);
+                            if (go && j + ahead < n) scores(j + ahead, both && TURNS ? xs ^ 1 : xs);
+                        };
+                        wait(q_full, qn);
+                        if (go) scores(0, 0);
+                        if (go && ahead > 1 && n > 1) scores(1, second);
+                        if (go && ahead > 2 && n > 2) scores(2, 0);
+    #pragma unroll 1
+                        for (int j = 0; j < n && go; j += 2) {
+                            step(j, 0);
+                            if (go && j + 1 < n) step(j + 1, second);
                         }
-                        const int pn = TURNS ? pb : xs;
-                        wait(&p_full[pn], TURNS ? pphase : xs ? phase1 : phase0);
-                        if (!go) return;
-                        fence_after();
-                        Place at = vp;
-                        const uint32_t from = tmem + s_col(pn);
-#pragma unroll
-                        for (int u = 0; u < UPT; ++u) {
-                            const uint32_t o = tmem + 256u + (PAIR ? (uint32_t)(D * xs) : 128u * u);
-                            const uint32_t b0 = desc_mn(ring + at.slot * L::kUnit);
-#pragma unroll
-                            for (int k = 0; k < kKeys / 16; ++k)
-                                umma_ts(o, from + 8u * k, b0 + 128u * k, id_o, (t | k) != 0 ? 1u : 0u);
-                            if (!duo || xs == 1) umma_commit(su32(&empty[at.slot]));
-                            at.move(1);
-                        }
-                        umma_commit(su32(&o_done[pn]));
-                        if (!TURNS) {
-                            if (xs) phase1 ^= 1;
-                            else phase0 ^= 1;
-                        } else if (++pb == NB) {
-                            pb = 0;
-                            pphase ^= 1;
-                        }
-                        if (!duo || xs == 1) vp.move(AHEAD && t + 2 >= nt ? UPT : 2 * UPT);
-                    };
-                    constexpr int second = both ? 1 : 0, ahead = TURNS || both ? NB : 1;   // (a stream alone with its S waits for its P)
-                    auto step = [&](int j, int xs) {
-                        values(j, xs);
-                        if (go && j + ahead < n) scores(j + ahead, both && TURNS ? xs ^ 1 : xs);
-                    };
-                    wait(q_full, qn);
-                    if (go) scores(0, 0);
-                    if (go && ahead > 1 && n > 1) scores(1, second);
-                    if (go && ahead > 2 && n > 2) scores(2, 0);
-#pragma unroll 1
-                    for (int j = 0; j < n && go; j += 2) {
-                        step(j, 0);
-                        if (go && j + 1 < n) step(j + 1, second);
-                    }
-                    for (int j = 0; j < (2 * nt) % NU; ++j) base.move(UPT);
-                    base.phase ^= (2 * nt / NU * UPT) & 1;
-                    ++turns[0];
-                    turns[1] += duo;
-                    ++qn;
+                        for (int j = 0; j < (2 * nt) % NU; ++j) base.move(UPT);
+                        base.phase ^= (2 * nt / NU * UPT) & 1;
+                        ++turns[0];
+                        turns[1] += duo;
+                        ++qn;
                     };
                     if (PAIR && two_tiles(it)) work(std::true_type());
                     else work(std::false_type());
