@@ -71,7 +71,7 @@ struct TLay {
     static constexpr int ring = NQ * (D / 64) * kBox;
     static constexpr int stage = ring + NU * kUnit;           // outputs on their way, a box a stream
     static constexpr int bars = stage + 2 * kBox;
-    static constexpr int kBars = 2 * NU + 3 * NB + 2 + 8 + 3 + 2 * kItems;
+    static constexpr int kBars = 2 * NU + 3 * NB + 2 + 8 + 4 + 2 * kItems;
     static constexpr int misc = bars + kBars * 8;             // tensor-memory address, abort flag
     static constexpr int refs = misc + 8;                     // [128] references, [2][128] sums (one row tile)
     static constexpr int items = (refs + 3 * 128 * 4 + 15) / 16 * 16;   // [kItems] items, read 16 bytes at a time
@@ -423,7 +423,7 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
     uint64_t *full = reinterpret_cast<uint64_t *>(sm + L::bars), *empty = full + NU;
     uint64_t *s_full = empty + NU, *p_full = s_full + NB, *o_done = p_full + NB,
              *o_free = o_done + NB, *ref_rdy = o_free + 2, *q_full = ref_rdy + 8, *q_free = q_full + 1, *all_done = q_free + 1,
-             *i_ready = all_done + 1, *i_read = i_ready + kItems;
+             *alone = all_done + 1, *i_ready = alone + 1, *i_read = i_ready + kItems;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + L::misc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     float *refs = reinterpret_cast<float *>(sm + L::refs), *sums = refs + 128;
@@ -449,6 +449,7 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
         bar_init(su32(q_full), tp.qmap ? 1 : kQThreads);
         bar_init(su32(q_free), 1);
         bar_init(su32(all_done), 1);
+        bar_init(su32(alone), 8);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -728,6 +729,7 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
         const uint32_t oc = lanes + 256u + (PAIR ? (uint32_t)(D * xs) : 0u);
         const float c = p.c;
         const uint64_t c2 = two(c, c);
+        int alones = 0;   // items of the first stream alone
         int done[2] = {0, 0}, all = 0, units = 0;   // steps of the streams and of both, units of the ring before this item
         bool go = true;
         auto wait = [&](uint64_t *bar, int parity) {
@@ -920,7 +922,11 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                 if (go) fence_after();
             }
             // A second stream without work stays behind the first: its next wait is for the phase after this item's.
-            if (TURNS && !duo && it.nt > 0) asm volatile("bar.sync 1, 256;" ::: "memory");
+            if (TURNS && !duo && it.nt > 0) {
+                __syncwarp();
+                if (lane == 0) bar_arrive(su32(alone));
+                wait(alone, alones++);
+            }
             done[0] += PAIR ? nt : (nt + 1) / 2;
             done[1] += PAIR ? nt : nt / 2;
             all += duo ? 2 * it.nt : it.nt;

@@ -545,3 +545,106 @@ def test_document_then_questions():
         cache.append(k[:, pos:pos + M], v[:, pos:pos + M], i32([pos] * B))
         check_cache(cache, k, v, q[:, pos:pos + M], [pos] * B, prefix=(dk[0], dv[0]))
         pos += M
+
+
+# ------------------------------------------------------------ ends of ranges
+
+@pytest.mark.parametrize("D,M", [(64, 1), (256, 1), (128, 9)])
+def test_many_heads(D, M):
+    """More key/value heads than a block's threads, one query head each."""
+    r, G = gen(40), 300
+    q, k, v = rows(r, 1, M, G, D), rows(r, 1, 200, G, D), rows(r, 1, 200, G, D)
+    check_prompt(q, k, v, 100, 2)
+    if M == 1:
+        cache = moe.KVCache(210, q_heads=G, kv_heads=G, head_dim=D)
+        cache.append(k, v, i32([0]))
+        check_cache(cache, k, v, q, [199])
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_largest_batch(D):
+    """1024 sequences, of 0 to 70 positions; with a prefix too."""
+    B, T = 1024, 70
+    lens = [(31 * b) % 71 for b in range(B)]
+    cache, k, v = filled(gen(41), T, lens, 1, D, FP, Hq=2, max_rows=1, max_prefix=100)
+    q = rows(gen(42), B, 1, 2, D, dtype=FP)
+    pos = [n - 1 for n in lens]
+    pk = rows(gen(43), 100, 1, D, dtype=FP)
+    for prefix in (None, (pk, pk)):
+        o, err = cache.attend(q, i32(pos), prefix=prefix)
+        assert err_of(err) == 0
+        for b in list(range(0, B, 61)) + [1022, 1023]:
+            if pos[b] < 0:
+                assert not o[b].any()
+                continue
+            own = [k[b, :pos[b] + 1], v[b, :pos[b] + 1]]
+            if prefix:
+                own = [torch.cat([pk, x]) for x in own]
+            want, tol = kv_ref.row(q[b, 0], *own, D ** -0.5)
+            kv_ref.close(o[b, 0], want, tol, f"sequence {b}")
+    with pytest.raises(moe.MoeError):
+        moe.KVCache(T, batch=1025, kv_heads=1, q_heads=2, head_dim=64)
+
+
+def test_far_positions_in_a_ring():
+    """Positions up to the last that a ring may have; the one behind it is refused."""
+    W, S, T = 30, 3, 48
+    for Hq, M in ((4, 1), (32, 4)):
+        for p in ((1 << 30) - M, 123456789):
+            r = gen(44)
+            cache = moe.KVCache(T, q_heads=Hq, kv_heads=2, head_dim=64, window=W, sinks=S, max_rows=M)
+            k, v = rows(r, 1, S + W + M, 2, 64), rows(r, 1, S + W + M, 2, 64)
+            cache.append(k[:, :S], v[:, :S], i32([0]))
+            cache.append(k[:, S:], v[:, S:], i32([p - W]))
+            q = rows(r, 1, M, Hq, 64)
+            o, err = cache.attend(q, i32([p]))
+            assert err_of(err) == 0
+            for m in range(M):
+                sees = list(range(S)) + list(range(S + 1 + m, S + W + 1 + m))
+                want, tol = kv_ref.row(q[0, m], k[0, sees], v[0, sees], 0.125)
+                kv_ref.close(o[0, m], want, tol, f"row {m} at {p}")
+        o, err = cache.attend(q, i32([(1 << 30) - M + 1]))
+        assert err_of(err) == 1 and not o[0, -1].any()
+
+
+def test_first_call_in_a_capture():
+    """A prompt's call whose device has had none before is captured: its error word is the graph's."""
+    from quantized_moe_decode_layer_gb300 import api
+    x = rows(gen(45), 1, 90, 2, 64)
+    want = moe.window_attention(x, x, x, 20)[0]
+    torch.cuda.synchronize()
+    kept = dict(api._window_err)
+    api._window_err.clear()
+    try:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            o, err = moe.window_attention(x, x, x, 20)
+        assert not api._window_err
+        graph.replay()
+        assert torch.equal(o, want) and int(err.item()) == 0
+    finally:
+        api._window_err.update(kept)
+
+
+@pytest.mark.parametrize("D,Hq,G", [(64, 8, 4), (128, 8, 4), (256, 8, 4)])
+def test_waits_that_run_out(D, Hq, G):
+    """With a time limit that no wait keeps the calls return, report it and leave the device usable."""
+    q, k = rows(gen(46), 2, 700, Hq, D), rows(gen(47), 2, 700, G, D)
+    want = moe.window_attention(q, k, k, 300, sinks=2)[0]
+    cache = moe.KVCache(64, batch=2, q_heads=8 * G, kv_heads=G, head_dim=D, max_prefix=700)
+    cache.append(k[:, :60], k[:, :60], i32([0, 0]))
+    few = rows(gen(48), 2, 4, 8 * G, D)
+    also = cache.attend(few, i32([56, 56]), prefix=(k[0], k[0]))[0]
+    torch.cuda.synchronize()
+    try:
+        moe.debug_set(-1, timeout_ns=1)
+        _, err = moe.window_attention(q, k, k, 300, sinks=2)
+        assert err_of(err) == 4
+        _, err = cache.attend(few, i32([56, 56]), prefix=(k[0], k[0]))
+        assert err_of(err) == moe.KVCache.ERR_TIMEOUT
+    finally:
+        moe.debug_set(-1, 0)
+    o, err = moe.window_attention(q, k, k, 300, sinks=2)
+    assert err_of(err) == 0 and torch.equal(o, want)
+    o, err = cache.attend(few, i32([56, 56]), prefix=(k[0], k[0]))
+    assert err_of(err) == 0 and torch.equal(o, also)
