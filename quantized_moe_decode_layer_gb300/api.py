@@ -812,7 +812,7 @@ class KVCache(_CacheCalls):
         if isinstance(t, torch.Tensor) and t.dim() == 3 and t.dtype is self.dtype and t.get_device() == self._index:
             n, g, d = t.shape
             if g == self.kv_heads and d == self.head_dim and 1 <= n <= self.max_prefix:
-                return _rows_of(t.unsqueeze(0), name)
+                return _rows_at(t, name, 0, t.stride(0) if n > 1 else 0, t.stride(1) if g > 1 else 0)
         got = f"{tuple(t.shape)} {t.dtype} on {t.device}" if isinstance(t, torch.Tensor) else type(t).__name__
         raise ValueError(f"{name} must be {self.dtype} [n, {self.kv_heads}, {self.head_dim}] on {self.device}, 1 <= n <= "
                          f"max_prefix={self.max_prefix}; got {got}")
@@ -854,22 +854,20 @@ class KVCache(_CacheCalls):
         return out, self.err if err is None else err
 
 
-def _rows_of(t: torch.Tensor, name: str) -> Rows:
-    """moe_rows of [batch, M, heads, head_dim] that the attention kernels read
-    in 16-byte pieces; dimensions of one entry have no stride."""
-    n0, n1, n2, _ = t.shape
-    s0, s1, s2, s3 = t.stride()
-    if n0 == 1:
-        s0 = 0
-    if n1 == 1:
-        s1 = 0
-    if n2 == 1:
-        s2 = 0
+def _rows_at(t: torch.Tensor, name: str, seq: int, row: int, head: int) -> Rows:
+    """moe_rows that the attention kernels read in 16-byte pieces."""
     at = t.data_ptr()
-    if s3 != 1 or at % 16 or (s0 | s1 | s2) % 8:
+    if t.stride(-1) != 1 or at % 16 or (seq | row | head) % 8:
         raise ValueError(f"{name} must have a contiguous last dimension, a base that is a multiple of 16 bytes and strides that are "
                          f"multiples of 8 elements; got strides {t.stride()}, base {at:#x}")
-    return Rows(at, _ROW_TYPES[t.dtype], s0, s1, s2)
+    return Rows(at, _ROW_TYPES[t.dtype], seq, row, head)
+
+
+def _rows_of(t: torch.Tensor, name: str) -> Rows:
+    """Those of [batch, M, heads, head_dim]; dimensions of one entry have no stride."""
+    n0, n1, n2, _ = t.shape
+    s0, s1, s2, _ = t.stride()
+    return _rows_at(t, name, s0 if n0 > 1 else 0, s1 if n1 > 1 else 0, s2 if n2 > 1 else 0)
 
 
 _window_err: dict = {}   # device index -> the error word of window_attention's calls
@@ -903,18 +901,18 @@ def window_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window=N
     Runs on the current stream of q's device, or on `stream`: then inputs and results are
     ordered by the caller, as tensors between streams are; inputs may be dropped right after the call.
     ws: scratch (uint8, window_attention_workspace bytes) to use instead of new one."""
+    dtype, index = getattr(q, "dtype", None), q.get_device() if isinstance(q, torch.Tensor) else -1
     for name, t in (("q", q), ("k", k), ("v", v)):
-        if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == 4 and t.dtype in _Q_TYPES and t.dtype is q.dtype
-                and t.get_device() == q.get_device()):
+        if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == 4 and dtype in _Q_TYPES and t.dtype is dtype
+                and t.get_device() == index):
             got = f"{tuple(t.shape)} {t.dtype} on {t.device}" if isinstance(t, torch.Tensor) else type(t).__name__
             raise ValueError(f"{name} must be a [batch, rows, heads, head_dim] CUDA tensor, bf16 or fp16 like q; got {got}")
     B, M, Hq, D = q.shape
-    _, T, Hkv, _ = k.shape
-    if k.shape != v.shape or k.size(0) != B or k.size(3) != D:
+    Bk, T, Hkv, Dk = k.shape
+    if k.shape != v.shape or Bk != B or Dk != D:
         raise ValueError(f"q {tuple(q.shape)}, k {tuple(k.shape)} and v {tuple(v.shape)} do not go together")
     if window is not None and window < 1:
         raise ValueError("window must be at least 1, or None")
-    index = q.get_device()
     if stream is not None and stream.device.index != index:
         raise ValueError(f"the stream must be on {q.device}")
     if stream is not None or torch._C._cuda_getDevice() != index:
