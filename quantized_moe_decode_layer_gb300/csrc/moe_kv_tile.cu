@@ -48,7 +48,8 @@ namespace {
 
 constexpr int kRows = 128;            // rows of a tile (MMA M)
 constexpr int kKeys = 128;            // positions of a tile (MMA N of the scores)
-constexpr int kBox = 128 * 128;       // one TMA box: 128 positions of 64 elements
+constexpr int kHalf = kKeys / 2;      // they come in halves
+constexpr int kBox = 128 * 128;       // 128 rows or positions of 64 elements
 constexpr int kTThreads = 384;        // softmax: warps 0-3, 4-7; loads 8; products 9; q 10, 11
 constexpr int kQThreads = 64;
 constexpr int kErrTimeout = 4;
@@ -308,18 +309,21 @@ __device__ __forceinline__ int rows_of(const KvCall &p, int b, int &p0, bool &ba
 template <bool AHEAD>
 __device__ __forceinline__ int v_order(int t, int nt) { return !AHEAD ? 2 * t + 1 : t == nt - 1 ? 2 * nt - 1 : 2 * t + 2; }
 
-// A CTA's worth of work: row tile(s) r0 .. of one head against nt tiles of positions:
-// tiles i0 .. i0 + nt - 1 of the list that has nfront tiles from slot 0 on and then those from slot `from` on.
-// A window's tiles begin at its first position, not at a multiple of their size: a window of 128 k positions and
+// A CTA's worth of work: row tile(s) r0 .. of one head against nt tiles of positions: halves 2 i0 .. of the list that
+// has nfront halves of a tile from slot 0 on and then those from slot `from` on.
+// A window's halves begin at its first position, not at a multiple of their size: a window of 128 k positions and
 // its rows' 64 or so take k + 1 tiles wherever they begin, and not k + 2 (8192 positions, 16/2/256, window 100:
-// 58 -> 43 us, 600: 109 -> 90; 32/8/128, 1700: 195 -> 182).
+// 58 -> 43 us, 600: 109 -> 90; 32/8/128, 1700: 195 -> 182).  The first tokens take a half and not a tile (MEASURED).
 struct Item {
     int z, g, b, r0;
     int p0, cnt;
     int from, nfront, i0, nt;
     int sl, off;    // slot of the first position in the window; that position less its slot
-    __device__ __forceinline__ bool front(int t) const { return i0 + t < nfront; }
-    __device__ __forceinline__ int first_key(int t) const { return front(t) ? kKeys * (i0 + t) : from + kKeys * (i0 + t - nfront); }
+    __device__ __forceinline__ int first_key(int t, int half) const
+    {
+        const int j = 2 * (i0 + t) + half;
+        return j < nfront ? kHalf * j : from + kHalf * (j - nfront);
+    }
 };
 template <int RT, bool PREFIX>
 __device__ __forceinline__ Item item_of(const TileParams &tp, int x)
@@ -351,9 +355,9 @@ __device__ __forceinline__ Item item_of(const TileParams &tp, int x)
             const int end = it.sl + (hi - lo);
             const int low = max(min(p.S, lo), end >= p.T ? p.S + end - p.T + 1 : 0);   // slots from 0 on
             it.from = it.sl;
-            it.nfront = (low + kKeys - 1) / kKeys;
-            if (kKeys * it.nfront >= it.sl) it.from = it.nfront = 0;   // one row of tiles
-            it.nt = it.nfront + (min(end, p.T - 1) - it.from) / kKeys + 1;
+            it.nfront = (low + kHalf - 1) / kHalf;
+            if (kHalf * it.nfront >= it.sl) it.from = it.nfront = 0;   // one row of them
+            it.nt = (it.nfront + (min(end, p.T - 1) - it.from) / kHalf + 2) / 2;
         }
     }
     const int each = (it.nt + tp.nsplit - 1) / tp.nsplit;
@@ -416,7 +420,7 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
 {
     using L = TLay<D>;
     constexpr bool PAIR = L::kPair, AHEAD = L::kAhead, TURNS = L::kTurns;
-    constexpr int KS = kKeys / 2, NB = L::NB;
+    constexpr int KS = kHalf, NB = L::NB;
     constexpr int NU = L::NU, UPT = L::UPT, RT = L::RT;
     const KvCall &p = tp.c;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -490,7 +494,7 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                     items.done(k);
                     if (!go) break;
                     auto load = [&](const CUtensorMap *map, int t) {
-                        const int key = it.first_key(t);
+                        const int key0 = it.first_key(t, 0), key1 = it.first_key(t, 1);
                         for (int u = 0; u < UPT && go; ++u) {
                             if (turn > 0 && !bar_wait(su32(&empty[slot]), (unsigned)(turn - 1) & 1u, abort_flag, p)) {
                                 go = false;
@@ -499,8 +503,10 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                             const uint32_t dst = su32(sm + L::ring + slot * L::kUnit), fb = su32(&full[slot]);
                             bar_expect(fb, L::kUnit);
 #pragma unroll
-                            for (int h = 0; h < L::kUnit / kBox; ++h)
-                                tma_load4(dst + h * kBox, map, 128 * u + 64 * h, key, it.g, PREFIX ? 0 : it.b, fb);
+                            for (int h = 0; h < L::kUnit / kBox; ++h) {
+                                tma_load4(dst + h * kBox, map, 128 * u + 64 * h, key0, it.g, PREFIX ? 0 : it.b, fb);
+                                tma_load4(dst + h * kBox + kBox / 2, map, 128 * u + 64 * h, key1, it.g, PREFIX ? 0 : it.b, fb);
+                            }
                             ++n;
                             if (++slot == NU) {
                                 slot = 0;
@@ -772,32 +778,33 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
             float l = 0.f, ref = -INFINITY;    // of the row, as the stream knows them
 #pragma unroll 1
             for (int i = xs; i < nsteps && go; i += 2) {
-                const int t = PAIR ? i >> 1 : i, key = it.first_key(t);
+                const int t = PAIR ? i >> 1 : i, keys[2] = {it.first_key(t, 0), it.first_key(t, 1)};
                 const int turn = TURNS ? all + (duo ? i : t) : done[xs] + (i >> 1), sb = TURNS ? turn % NB : xs;   // the step's turn at its S
                 const uint32_t sc = lanes + s_col(sb);
                 wait(&s_full[sb], TURNS ? turn / NB : turn);
                 if (!go) break;
                 fence_after();
-                if (!PREFIX && valid - key < kKeys && (!PAIR || xs == 0)) {
+                if (!PREFIX && valid - max(keys[0], keys[1]) < kHalf && (!PAIR || xs == 0)) {
                     // values behind the sequence's last position may be anything: zeros
-                    const int gone = valid - key;
                     const int n0 = units + UPT * v_order<AHEAD>(t, nt);
 #pragma unroll 1
                     for (int u = n0; u < n0 + UPT; ++u) {
                         wait(&full[u % NU], u / NU);
                         if (!go) break;
                         uint8_t *unit = sm + L::ring + (u % NU) * L::kUnit;
-                        for (int j = row; j < (kKeys - gone) * 8; j += 128)
 #pragma unroll
-                            for (int h = 0; h < L::kUnit / kBox; ++h)
-                                *reinterpret_cast<uint4 *>(unit + h * kBox + gone * 128 + j * 16) = make_uint4(0u, 0u, 0u, 0u);
+                        for (int half = 0; half < 2; ++half) {
+                            const int left = max(valid - keys[half], 0);
+                            for (int j = row; j < (kHalf - left) * 8; j += 128)
+#pragma unroll
+                                for (int h = 0; h < L::kUnit / kBox; ++h)
+                                    *reinterpret_cast<uint4 *>(unit + h * kBox + half * (kBox / 2) + left * 128 + j * 16) =
+                                        make_uint4(0u, 0u, 0u, 0u);
+                        }
                     }
                     if (!go) break;
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 }
-                // a tile that some row does not see all of
-                const bool partly = !((key >= a_lo && key + kKeys <= a_hi) || key + kKeys <= s_hi || (key >= b_lo && key + kKeys <= b_hi));
-
                 uint32_t s0[KS], s1[KS];    // the positions' halves
                 uint32_t pk[kKeys / 2];
                 uint64_t add[2] = {0ull, 0ull};
@@ -807,11 +814,13 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                     for (int k = 0; k < KS / 32; ++k) tmem_ld32(sc + (uint32_t)(KS * half + 32 * k), s + 32 * k);
                 };
                 auto hide = [&](int half, uint32_t *s) {
-                    if (!partly) return;
+                    const int key = keys[half];
+                    // a half that all rows see all of
+                    if ((key >= a_lo && key + kHalf <= a_hi) || key + kHalf <= s_hi || (key >= b_lo && key + kHalf <= b_hi)) return;
                     auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; };
 #pragma unroll
                     for (int k = 0; k < KS / 32; ++k) {
-                        const int at = key + KS * half + 32 * k;
+                        const int at = key + 32 * k;
                         uint32_t sees = below(p.P - at);
                         if (!PREFIX) {
                             const int a = pos - it.off + 1;      // past the last slot
@@ -1049,7 +1058,7 @@ bool map_of(CUtensorMap *map, const uint16_t *base, bool f16, int D, int T, int 
     const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)T, (cuuint64_t)heads, (cuuint64_t)seqs};
     auto bytes = [&](long long s, int n) { return (cuuint64_t)(n > 1 ? s * 2 : D * 2); };
     const cuuint64_t strides[3] = {bytes(row, T), bytes(head, heads), bytes(seq, seqs)};
-    const cuuint32_t box[4] = {64, (cuuint32_t)kKeys, 1, 1}, es[4] = {1, 1, 1, 1};
+    const cuuint32_t box[4] = {64, (cuuint32_t)kHalf, 1, 1}, es[4] = {1, 1, 1, 1};
     return enc(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint16_t *>(base), dims,
                strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
