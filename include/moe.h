@@ -651,7 +651,7 @@ int moe_kv_attn_workspace_size(const moe_kv *cache, int M, int max_prefix, size_
  * strides row and head (seq is not used), of the cache's type, 16-byte aligned, strides
  * multiples of 8.  All rows see all of them, in one softmax with their
  * own positions; they are read once for the batch.  For caches without a window.
- * Two launches, three with a prefix and many rows.  Errors: INVALID_ARG, UNSUPPORTED,
+ * One to three launches.  Errors: INVALID_ARG, UNSUPPORTED,
  * BUFFER_TOO_SMALL, CUDA. */
 int moe_kv_attn(const moe_kv *cache, const moe_rows *q, int M, const int32_t *pos_dev, const int32_t *counts_dev,
                 const moe_rows *prefix_k, const moe_rows *prefix_v, int prefix_len, float scale, void *o_dev, void *ws_dev,

@@ -313,7 +313,8 @@ __device__ __forceinline__ int v_order(int t, int nt) { return !AHEAD ? 2 * t + 
 // has nfront halves of a tile from slot 0 on and then those from slot `from` on.
 // A window's halves begin at its first position, not at a multiple of their size: a window of 128 k positions and
 // its rows' 64 or so take k + 1 tiles wherever they begin, and not k + 2 (8192 positions, 16/2/256, window 100:
-// 58 -> 43 us, 600: 109 -> 90; 32/8/128, 1700: 195 -> 182).  The first tokens take a half and not a tile (MEASURED).
+// 58 -> 43 us, 600: 109 -> 90; 32/8/128, 1700: 195 -> 182).  The first tokens take a half and not a tile (32/8/128,
+// window 1024 and 4 first tokens: 147 -> 133 us, window 100: 76 -> 61).
 struct Item {
     int z, g, b, r0;
     int p0, cnt;
@@ -762,29 +763,31 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
             // else s + off + R; it is seen if pos - W < position <= pos, or s < S.
             int pos = 0, valid = INT_MAX;      // valid: slots from there on hold anything (a ring that is full has none)
             const int R = p.ring ? p.T - p.S : kKvAll;
-            // slots that all rows see: a_lo .. a_hi - 1 from sl on, b_lo .. b_hi - 1 before it, those below s_hi
-            int a_lo = 0, a_hi = p.P, b_lo = 0, b_hi = 0, s_hi = 0;
+            // halves that all rows see all of: `inner` of the window's from inner0 on (others that are take the slower way)
+            int inner0 = 0, inner = p.P / kHalf - 2 * it.i0;
             if (!PREFIX) {
                 const int ra = it.r0 + (PAIR ? 128 * xs : 0);
                 const int pos_lo = it.p0 + p.by_g(ra), pos_hi = it.p0 + p.by_g(ra + kRows - 1);
                 pos = it.p0 + p.by_g(r);
                 if (it.p0 + it.cnt <= p.T) valid = it.p0 + it.cnt;
-                a_lo = max(max(it.sl, p.S), pos_hi - it.off - p.W + 1);
-                a_hi = min(p.T, pos_lo - it.off + 1);
-                b_lo = max(p.S, pos_hi - it.off - R - p.W + 1);
-                b_hi = min(it.sl, pos_lo - it.off - R + 1);
-                s_hi = min(p.S, pos_lo + 1);
+                int lo = pos_hi - it.off - p.W + 1;
+                if (lo <= max(it.sl, p.S)) lo = it.sl;
+                inner0 = it.nfront + (lo - it.from + kHalf - 1) / kHalf;
+                inner = it.nfront + (min(p.T, pos_lo - it.off + 1) - it.from) / kHalf - inner0;
+                inner0 -= 2 * it.i0;
             }
+            inner = max(inner, 0);
             float l = 0.f, ref = -INFINITY;    // of the row, as the stream knows them
 #pragma unroll 1
             for (int i = xs; i < nsteps && go; i += 2) {
-                const int t = PAIR ? i >> 1 : i, keys[2] = {it.first_key(t, 0), it.first_key(t, 1)};
+                const int t = PAIR ? i >> 1 : i;
                 const int turn = TURNS ? all + (duo ? i : t) : done[xs] + (i >> 1), sb = TURNS ? turn % NB : xs;   // the step's turn at its S
                 const uint32_t sc = lanes + s_col(sb);
                 wait(&s_full[sb], TURNS ? turn / NB : turn);
                 if (!go) break;
                 fence_after();
-                if (!PREFIX && valid - max(keys[0], keys[1]) < kHalf && (!PAIR || xs == 0)) {
+                auto all_seen = [&](int half) { return (unsigned)(2 * t + half - inner0) < (unsigned)inner; };
+                if (!PREFIX && !(all_seen(0) && all_seen(1)) && valid - max(it.first_key(t, 0), it.first_key(t, 1)) < kHalf && (!PAIR || xs == 0)) {
                     // values behind the sequence's last position may be anything: zeros
                     const int n0 = units + UPT * v_order<AHEAD>(t, nt);
 #pragma unroll 1
@@ -794,7 +797,7 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                         uint8_t *unit = sm + L::ring + (u % NU) * L::kUnit;
 #pragma unroll
                         for (int half = 0; half < 2; ++half) {
-                            const int left = max(valid - keys[half], 0);
+                            const int left = max(valid - it.first_key(t, half), 0);
                             for (int j = row; j < (kHalf - left) * 8; j += 128)
 #pragma unroll
                                 for (int h = 0; h < L::kUnit / kBox; ++h)
@@ -814,9 +817,8 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                     for (int k = 0; k < KS / 32; ++k) tmem_ld32(sc + (uint32_t)(KS * half + 32 * k), s + 32 * k);
                 };
                 auto hide = [&](int half, uint32_t *s) {
-                    const int key = keys[half];
-                    // a half that all rows see all of
-                    if ((key >= a_lo && key + kHalf <= a_hi) || key + kHalf <= s_hi || (key >= b_lo && key + kHalf <= b_hi)) return;
+                    if (all_seen(half)) return;
+                    const int key = it.first_key(t, half);
                     auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; };
 #pragma unroll
                     for (int k = 0; k < KS / 32; ++k) {
@@ -897,12 +899,16 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                 }
                 const float sub = ref == -INFINITY ? 0.f : -ref;
                 weights(0, s0, two(sub, sub));
+                // (one half's P on its way while the other's is computed: 16384 positions, all seen, 1157 -> 1132 us with 64
+                // columns, 1547 -> 1528 with 128, 1294 -> 1312 with 256)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) tmem_st16(sc + 16u * k, pk + 16 * k);
                 weights(1, s1, two(sub, sub));
                 float a0, a1;
                 split2(add2(add[0], add[1]), a0, a1);
                 l += a0 + a1;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) tmem_st16(sc + 16u * k, pk + 16 * k);
+                for (int k = 2; k < 4; ++k) tmem_st16(sc + 16u * k, pk + 16 * k);
                 tmem_wait_st();
                 fence_before();
                 __syncwarp();
