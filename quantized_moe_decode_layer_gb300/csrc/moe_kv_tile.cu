@@ -100,6 +100,7 @@ struct TileParams {
     int ntile;     // row tiles (CTAs' worth) of a head
     int nsplit;
     int items;     // row tiles times parts times heads (times sequences)
+    int full;      // items from there on are cut into two of one row tile
 };
 
 __device__ __forceinline__ uint32_t su32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -317,6 +318,7 @@ __device__ __forceinline__ int v_order(int t, int nt) { return !AHEAD ? 2 * t + 
 // window 1024 and 4 first tokens: 147 -> 133 us, window 100: 76 -> 61).
 struct Item {
     int z, g, b, r0;
+    int one;        // one row tile of a pair, by itself
     int p0, cnt;
     int from, nfront, i0, nt;
     int sl, off;    // slot of the first position in the window; that position less its slot
@@ -332,22 +334,25 @@ __device__ __forceinline__ Item item_of(const TileParams &tp, int x)
     const KvCall &p = tp.c;
     Item it;
     const int seqs = PREFIX ? 1 : p.B;
+    it.one = x >= tp.full;
+    const int second = it.one ? x - tp.full & 1 : 0, rt = it.one ? kRows : RT;
+    if (it.one) x = tp.full + (x - tp.full >> 1);
     it.z = x % tp.nsplit;
     x /= tp.nsplit;
     it.g = x % p.Hkv;
     x /= p.Hkv;
     it.b = x % seqs;
     const int tile = tp.ntile - 1 - x / seqs;   // later row tiles, which see more, first
-    it.r0 = tile * RT;
+    it.r0 = tile * RT + kRows * second;
     it.p0 = it.from = it.nfront = it.nt = it.sl = it.off = 0;
     it.cnt = p.M;
     if (PREFIX) {
-        it.nt = (p.P + kKeys - 1) / kKeys;
+        if (it.r0 < p.B * p.M * p.G) it.nt = (p.P + kKeys - 1) / kKeys;
     } else {
         bool bad;
         it.cnt = rows_of(p, it.b, it.p0, bad);
         if (bad) atomicOr(p.err, kKv8ErrRange);
-        const int first = p.by_g(it.r0), last = min(p.by_g(it.r0 + RT - 1), it.cnt - 1);
+        const int first = p.by_g(it.r0), last = min(p.by_g(it.r0 + rt - 1), it.cnt - 1);
         if (first < it.cnt) {
             // positions lo .. hi, slots sl .. T - 1 and (a ring that they wrap around in) on from S
             const int lo = max(0, it.p0 + first - p.W + 1), hi = it.p0 + last;
@@ -367,7 +372,7 @@ __device__ __forceinline__ Item item_of(const TileParams &tp, int x)
     return it;
 }
 
-static_assert(sizeof(Item) <= kItemBytes, "an item's words");
+static_assert(sizeof(Item) <= kItemBytes + 4, "an item's words (the last bit of r0 is `one`)");
 
 // The items of a CTA, in turn.
 struct Items {
@@ -380,7 +385,7 @@ struct Items {
         const bool ok = bar_wait(su32(&ready[s]), (unsigned)(n / kItems) & 1u, abort, c);
         const int4 *w = reinterpret_cast<const int4 *>(ring + s * kItemBytes);
         const int4 a = w[0], b = w[1], d = w[2];
-        it.z = a.x, it.g = a.y, it.b = a.z, it.r0 = a.w;
+        it.z = a.x, it.g = a.y, it.b = a.z, it.r0 = a.w & ~1, it.one = a.w & 1;
         it.p0 = b.x, it.cnt = b.y, it.off = b.z, it.from = b.w;
         it.nfront = d.x, it.i0 = d.y, it.nt = d.z, it.sl = d.w;
         return ok;
@@ -389,7 +394,7 @@ struct Items {
     __device__ __forceinline__ void put(int n, const Item &it) const
     {
         int4 *w = reinterpret_cast<int4 *>(ring + n % kItems * kItemBytes);
-        w[0] = make_int4(it.z, it.g, it.b, it.r0);
+        w[0] = make_int4(it.z, it.g, it.b, it.r0 | it.one);
         w[1] = make_int4(it.p0, it.cnt, it.off, it.from);
         w[2] = make_int4(it.nfront, it.i0, it.nt, it.sl);
         bar_arrive(su32(&ready[n % kItems]));
@@ -478,7 +483,7 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
     const bool parts = p.P > 0 || tp.nsplit > 1;
     const KvCall::Parts &to_parts = PREFIX ? p.prefix : p.own;
     // whether a pair's second row tile has rows that see anything
-    auto two_tiles = [&](const Item &it) { return PAIR && it.r0 + kRows < (PREFIX ? rows : (long long)it.cnt * p.G); };
+    auto two_tiles = [&](const Item &it) { return PAIR && !it.one && it.r0 + kRows < (PREFIX ? rows : (long long)it.cnt * p.G); };
     const Items items = {sm + L::items, i_ready, i_read};
     const int mine = blockIdx.x < tp.items ? (tp.items - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;   // items of the CTA
 
@@ -556,15 +561,18 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                 ++qn;
                 if (tp.qmap) {
                     if (t == 0) {
-                        bar_expect(su32(q_full), L::ring);
+                        const int nq = it.one ? 1 : L::NQ;
+                        bar_expect(su32(q_full), nq * (D / 64) * kBox);
                         // packed rows r0 .. : the token of r0 (of all sequences' in turn, for a prefix)
                         const int m = p.by_g(it.r0);
 #pragma unroll
-                        for (int j = 0; j < L::NQ; ++j)
+                        for (int j = 0; j < L::NQ; ++j) {
+                            if (j == nq) break;
 #pragma unroll
                             for (int h = 0; h < D / 64; ++h)
                                 tma_load5(su32(sm + L::q) + (j * (D / 64) + h) * kBox, &tp.tq, 64 * h, 0, it.g, m + j * (kRows / p.G),
                                           PREFIX ? 0 : it.b, su32(q_full));
+                        }
                     }
                     tell(k + 2);    // (behind the loads, which others wait for)
                     __syncwarp();
@@ -572,6 +580,7 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                 }
                 // (rows of idle sequences and padding are read like the others; nothing of them is used)
                 constexpr int STEP = kQThreads / CH;   // rows a pass
+                const int rt = it.one ? kRows : RT;
                 const int c = t % CH, rr0 = t / CH;
                 int r = it.r0 + rr0, m = p.by_g(r), h = r - m * p.G, bb = it.b;
                 if (PREFIX) {
@@ -580,7 +589,7 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                 }
                 const uint16_t *src = p.q + (long long)bb * p.qb + (long long)m * p.qm + (long long)(it.g * p.G + h) * p.qh + 8 * c;
 #pragma unroll 4
-                for (int rr = rr0; rr < RT; rr += STEP) {
+                for (int rr = rr0; rr < rt; rr += STEP) {
                     const bool ok = r < rows;   // rows that are not there are zeros
                     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
                                      su32(sm + L::q) + ((rr >> 7) * (D / 64) + (c >> 3)) * kBox + (rr & 127) * 128 + (((c & 7) ^ (rr & 7)) << 4)),
@@ -954,6 +963,7 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
             const bool live = PREFIX || p.by_g(r) < it.cnt;
             const float inv = live && nt > 0 && l != 0.f ? 1.f / l : 0.f;
             if (l != l && ref == -INFINITY) ref = 0.f;   // a row of NaN alone has no maximum, but is not empty
+            if (PAIR && xs == 1 && it.one) continue;   // (another item's)
             if (!PREFIX && tp.omap) {
                 // 64 columns at a time into the stream's box, and from there by TMA while the next item starts
                 uint8_t *box = sm + L::stage + xs * kBox;
@@ -1138,7 +1148,7 @@ int launch_kv_tiles(const KvCall &c, bool prefix, cudaStream_t stream)
     const long long rows = (long long)c.M * c.G * (prefix ? c.B : 1);
     tp.nsplit = prefix ? c.prefix.n : c.own.n;
     const long long ntile = kv_row_tiles(rows, c.D), ctas = ntile * tp.nsplit * c.Hkv * (prefix ? 1 : c.B);
-    if (rows > INT_MAX - 1024 || ctas > INT_MAX) return MOE_ERR_UNSUPPORTED;
+    if (rows > INT_MAX - 1024 || ctas > INT_MAX - 1024) return MOE_ERR_UNSUPPORTED;
     tp.ntile = (int)ntile;
     tp.items = (int)ctas;
     int dev = 0;
@@ -1150,8 +1160,16 @@ int launch_kv_tiles(const KvCall &c, bool prefix, cudaStream_t stream)
             if (e == cudaSuccess) e = cudaDeviceGetAttribute(&once.sms[dev], cudaDevAttrMultiProcessorCount, dev);
         });
         if (e == cudaSuccess && once.sms[dev] < 1) e = cudaErrorInvalidDevice;
+        // The last turn's pairs, where they leave half of the SMs without any, are cut: with 128 columns 2 x 2048 rows
+        // behind 6001, window 2048: 129 -> 121 us, 3 x 1700: 82 -> 79.  (With 64 a stream alone is no faster: 97 -> 94, 61 -> 64.)
+        const int left = e == cudaSuccess ? tp.items % once.sms[dev] : 0;
+        tp.full = tp.items;
+        if (c.D == 128 && rows > kRows && 2 * left <= once.sms[dev]) {
+            tp.full -= left;
+            tp.items += left;
+        }
         if (e == cudaSuccess)
-            e = launch_after(kernel, dim3((unsigned)std::min<long long>(ctas, once.sms[dev])), kTThreads, smem, 0, stream, tp);
+            e = launch_after(kernel, dim3((unsigned)std::min(tp.items, once.sms[dev])), kTThreads, smem, 0, stream, tp);
     };
 #define KV_TILE(F, D, P)                                                 \
     do {                                                                 \
