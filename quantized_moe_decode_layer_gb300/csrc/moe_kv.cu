@@ -569,15 +569,19 @@ __global__ void __launch_bounds__(Lay<D>::kThreads, Lay<D>::ctas) kv_split_kerne
 // l_i with m the largest m_i.  One CTA per row and head; each warp takes every
 // kMergeWarps-th part with a running maximum, its lanes the columns, and the warps' sums are joined.  Which parts there are
 // follows from the lengths, which are there before the kernel in front has ended.  Rows without positions get zeros.
-constexpr int kMergeWarps = 4;
-template <int D>
+// ONE: a warp per row, its CTA's other warps have other heads of the same row: where there are many rows, most CTAs would
+// wait for a place on an SM (512 prompt rows of 32 heads in two parts: 18 -> 10 us; 2048 rows behind a prefix: 9 -> 11).
+constexpr int kMergeWarps = 4, kMergeMany = 4096;
+template <int D, bool ONE>
 __global__ void __launch_bounds__(32 * kMergeWarps) kv_merge_kernel(const KvCall p, int ctas)
 {
     constexpr int VEC = D / 32, kThreads = 32 * kMergeWarps;
     __shared__ float red[kMergeWarps][D + 2];
     __shared__ int tsum[2][kMergeWarps];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int hq = blockIdx.x % p.Hq, bm = blockIdx.x / p.Hq, m = bm % p.M, b = bm / p.M;
+    constexpr int STEP = ONE ? 1 : kMergeWarps;   // warps of a row
+    const int x0 = ONE ? blockIdx.x * kMergeWarps + warp : blockIdx.x;
+    const int hq = x0 % p.Hq, bm = x0 / p.Hq, m = bm % p.M, b = bm / p.M;
     const int g = hq / p.G, h = hq - g * p.G;
     uint16_t *o = static_cast<uint16_t *>(p.o) + ((size_t)bm * p.Hq + hq) * D;
     int p0, lo, ns;
@@ -623,7 +627,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) kv_merge_kernel(const KvCall
     }
     wait_for_previous();
     if (m >= cnt) {
-        for (int d = tid; d < D; d += kThreads) o[d] = 0;
+        for (int d = ONE ? lane : tid; d < D; d += 32 * STEP) o[d] = 0;
         return;
     }
     if (p.split_own && n1 == 1 && p.P == 0) return;   // written by the split kernel
@@ -643,11 +647,11 @@ __global__ void __launch_bounds__(32 * kMergeWarps) kv_merge_kernel(const KvCall
     const int n = n1 + n2;
     float acc[VEC] = {}, l = 0.f, mx = -INFINITY;
     constexpr int AHEAD = 4;    // parts whose loads are in flight
-    for (int i0 = warp; i0 < n; i0 += AHEAD * kMergeWarps) {
+    for (int i0 = ONE ? 0 : warp; i0 < n; i0 += AHEAD * STEP) {
         float2 ml[AHEAD], y[AHEAD][VEC / 2];
 #pragma unroll
         for (int k = 0; k < AHEAD; ++k) {
-            const int i = i0 + k * kMergeWarps;
+            const int i = i0 + k * STEP;
             ml[k] = make_float2(-INFINITY, 0.f);
             if (i < n) {
                 const float *po, *at = part(i, po);
@@ -669,33 +673,41 @@ __global__ void __launch_bounds__(32 * kMergeWarps) kv_merge_kernel(const KvCall
             }
         }
     }
+    if constexpr (ONE) {
+        const float f = l != 0.f ? 1.f / l : 0.f;
 #pragma unroll
-    for (int v = 0; v < VEC / 2; ++v) {
-        red[warp][64 * v + 2 * lane] = acc[2 * v];
-        red[warp][64 * v + 2 * lane + 1] = acc[2 * v + 1];
-    }
-    if (lane == 0) {
-        red[warp][D] = l;
-        red[warp][D + 1] = mx;
-    }
-    __syncthreads();
-    float top = -INFINITY, w[kMergeWarps], ls = 0.f;
+        for (int v = 0; v < VEC / 2; ++v)
+            *reinterpret_cast<uint32_t *>(o + 64 * v + 2 * lane) =
+                p.f16 ? pack2<true>(acc[2 * v] * f, acc[2 * v + 1] * f) : pack2<false>(acc[2 * v] * f, acc[2 * v + 1] * f);
+    } else {
 #pragma unroll
-    for (int k = 0; k < kMergeWarps; ++k) top = fmaxf(top, red[k][D + 1]);
+        for (int v = 0; v < VEC / 2; ++v) {
+            red[warp][64 * v + 2 * lane] = acc[2 * v];
+            red[warp][64 * v + 2 * lane + 1] = acc[2 * v + 1];
+        }
+        if (lane == 0) {
+            red[warp][D] = l;
+            red[warp][D + 1] = mx;
+        }
+        __syncthreads();
+        float top = -INFINITY, w[kMergeWarps], ls = 0.f;
 #pragma unroll
-    for (int k = 0; k < kMergeWarps; ++k) {
-        w[k] = red[k][D + 1] == -INFINITY ? 0.f : ex2(red[k][D + 1] - top);
-        ls = fmaf(red[k][D], w[k], ls);
-    }
-    const float f = ls != 0.f ? 1.f / ls : 0.f;
-    for (int d = 2 * tid; d < D; d += 2 * kThreads) {
-        float x = 0.f, y = 0.f;
+        for (int k = 0; k < kMergeWarps; ++k) top = fmaxf(top, red[k][D + 1]);
 #pragma unroll
         for (int k = 0; k < kMergeWarps; ++k) {
-            x = fmaf(red[k][d], w[k], x);
-            y = fmaf(red[k][d + 1], w[k], y);
+            w[k] = red[k][D + 1] == -INFINITY ? 0.f : ex2(red[k][D + 1] - top);
+            ls = fmaf(red[k][D], w[k], ls);
         }
-        *reinterpret_cast<uint32_t *>(o + d) = p.f16 ? pack2<true>(x * f, y * f) : pack2<false>(x * f, y * f);
+        const float f = ls != 0.f ? 1.f / ls : 0.f;
+        for (int d = 2 * tid; d < D; d += 2 * kThreads) {
+            float x = 0.f, y = 0.f;
+#pragma unroll
+            for (int k = 0; k < kMergeWarps; ++k) {
+                x = fmaf(red[k][d], w[k], x);
+                y = fmaf(red[k][d + 1], w[k], y);
+            }
+            *reinterpret_cast<uint32_t *>(o + d) = p.f16 ? pack2<true>(x * f, y * f) : pack2<false>(x * f, y * f);
+        }
     }
 }
 
@@ -800,7 +812,7 @@ KvWs kv_ws(int B, int Hkv, int G, int D, long long M, int T, int W, int S, int P
     if (!split_own) {
         w.own_ctas = kv_row_tiles(rows, D) * Hkv * B;
         const long long seen = std::min<long long>((long long)W + S + 256 / G + 1, T);
-        w.own_n = kv_tile_splits(w.own_ctas, (seen + 127) / 128, rows <= 128);
+        w.own_n = kv_tile_splits(w.own_ctas, (seen + 127) / 128, rows <= 128, P > 0 ? 0 : prows * Hkv);
     }
     if (P > 0 && !split_pre) {
         w.pre_ctas = kv_row_tiles(prows, D) * Hkv;
@@ -880,7 +892,7 @@ int launch_kv_attn(KvCall &p, void *ws, cudaStream_t stream)
     p.prefix = {0, f(w.pre_o), f(w.pre_ml)};
     const long long merged = (long long)p.B * p.M * p.Hq;
     if (w.pre_ctas) {
-        p.prefix.n = kv_tile_splits(w.pre_ctas, (p.P + 127) / 128, false);
+        p.prefix.n = kv_tile_splits(w.pre_ctas, (p.P + 127) / 128, false, 0);
         const int rc = launch_kv_tiles(p, true, stream);
         if (rc) return rc;
         p.late = 1;   // the own positions' kernel runs beside
@@ -931,8 +943,11 @@ int launch_kv_attn(KvCall &p, void *ws, cudaStream_t stream)
         note_launch();
     }
     if (merged > INT_MAX) return MOE_ERR_UNSUPPORTED;
-    auto *merge = p.D == 256 ? kv_merge_kernel<256> : p.D == 128 ? kv_merge_kernel<128> : kv_merge_kernel<64>;
-    const cudaError_t e = launch_after(merge, dim3((unsigned)merged), 32 * kMergeWarps, 0, 0, stream, p, grid);
+    const bool one = merged >= kMergeMany && p.Hq % kMergeWarps == 0;
+    auto *merge = p.D == 256   ? (one ? kv_merge_kernel<256, true> : kv_merge_kernel<256, false>)
+                  : p.D == 128 ? (one ? kv_merge_kernel<128, true> : kv_merge_kernel<128, false>)
+                               : (one ? kv_merge_kernel<64, true> : kv_merge_kernel<64, false>);
+    const cudaError_t e = launch_after(merge, dim3((unsigned)(one ? merged / kMergeWarps : merged)), 32 * kMergeWarps, 0, 0, stream, p, grid);
     if (e != cudaSuccess) { note_cuda_error((int)e); return MOE_ERR_CUDA; }
     note_launch();
     return MOE_OK;

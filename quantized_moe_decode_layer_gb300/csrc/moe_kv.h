@@ -64,8 +64,9 @@ int launch_kv_attn(KvCall &p, void *ws, cudaStream_t stream);
 // Tiles of 128 rows against the own positions, or the prefix.
 int launch_kv_tiles(const KvCall &p, bool prefix, cudaStream_t stream);
 long long kv_row_tiles(long long rows, int D);
-// Parts of a row tile's positions: at most, and taken.  `ragged`: lengths that the host does not know, few rows.
+// Parts of a row tile's positions: at most, and taken.  `ragged`: lengths that the host does not know, few rows.  `rows`: to
+// be joined if there is more than one.
 int kv_tile_most(long long ctas, bool ragged);
-int kv_tile_splits(long long ctas, long long tiles, bool ragged);
+int kv_tile_splits(long long ctas, long long tiles, bool ragged, long long rows);
 
 }  // namespace moe

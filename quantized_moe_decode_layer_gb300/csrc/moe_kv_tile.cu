@@ -1105,18 +1105,22 @@ long long kv_row_tiles(long long rows, int D) { return (rows + row_tile(D) - 1) 
 
 // Parts that the positions of each row tile are cut into: as many as fill the SMs in as few
 // turns as possible.  `ctas` row tiles of all heads, `tiles` tiles of positions each; an item costs about four
-// tiles besides.  Where rows are few (a cache's attention: bound by HBM, loads run ahead into the next item) and more
+// tiles besides, one that leaves a part four more, and the merge that `rows` rows of all heads then need (0: they have it
+// anyway) two and a third of one for each thousand rows.  (32/8/64: 512 rows at 512 positions are 28 us in two parts, 10 in one; 64 at
+// 4096 are 15 in 16 parts, 34 in one.)  Where rows are few (a cache's attention: bound by HBM, loads run ahead into the next item) and more
 // than the SMs, shorter items, none below four tiles, even out what the lengths, which the host does not know, differ by
 // (256 of 100 to 2000 positions: 80 -> 56 us).
 int kv_tile_most(long long ctas, bool ragged) { return (int)std::max<long long>(1, (ragged ? 4 : 3) * 152 / ctas); }
-int kv_tile_splits(long long ctas, long long tiles, bool ragged)
+int kv_tile_splits(long long ctas, long long tiles, bool ragged, long long rows)
 {
     const int most = kv_tile_most(ctas, ragged);
     if (ragged && ctas >= 152) return (int)std::max<long long>(1, std::min<long long>(most, tiles / 4));
     int best = 1;
     double cost = 1e30;
     for (int s = 1; s <= most && s <= tiles; ++s) {
-        const double turns = (double)((ctas * s + 151) / 152), c = turns * ((double)((tiles + s - 1) / s) + 4.0) + 0.05 * s;
+        const bool cut = s > 1 && rows > 0;
+        const double turns = (double)((ctas * s + 151) / 152), item = (double)((tiles + s - 1) / s) + (cut ? 8.0 : 4.0);
+        const double c = turns * item + 0.05 * s + (cut ? 2.5 + rows / 3000.0 : 0.0);
         if (c < cost) {
             cost = c;
             best = s;
