@@ -264,6 +264,41 @@ def test_prompt_windows(window, sinks, D, Hq):
     check_prompt(q, k, v, window, sinks, some=23)
 
 
+@pytest.mark.parametrize("window,sinks", [(100, 1), (100, 63), (100, 64), (129, 65), (65, 128), (64, 129), (300, 200), (1, 500)])
+@pytest.mark.parametrize("D,Hq,M", [(64, 4, 200), (128, 4, 200), (128, 3, 90), (256, 8, 150), (64, 2, 70)])
+def test_window_far_from_the_first_positions(window, sinks, D, Hq, M):
+    """Tiles of which one half has first positions and the other the window's."""
+    r, T = gen(60), 1150
+    q, k, v = rows(r, 2, M, Hq, D, size=2.0), rows(r, 2, T, 1, D), rows(r, 2, T, 1, D)
+    pos = [T - M, 733]
+    k[1, 733 + M:], v[1, 733 + M:] = float("nan"), float("nan")
+    check_prompt(q, k, v, window, sinks, pos=pos, some=19)
+
+
+@pytest.mark.parametrize("Hq,G", [(8, 8), (24, 8)])
+@pytest.mark.parametrize("B", [1, 6, 10])
+def test_prompt_turns(B, Hq, G):
+    """As many pairs of row tiles as leave the last turn full, nearly empty, or with nothing else."""
+    r, M, D = gen(61), 300, 128
+    counts = [300, 0, 1, 128, 129, 256, 257, 299, 300, 127][:B]
+    q, k, v = rows(r, B, M, Hq, D), rows(r, B, M, G, D), rows(r, B, M, G, D)
+    for b, c in enumerate(counts):
+        k[b, c:], v[b, c:] = float("nan"), float("nan")
+    check_prompt(q, k, v, 70, 3, pos=[0] * B, counts=counts, some=29)
+    check_prompt(q, k, v, None, 0, pos=[0] * B, counts=counts, some=37)
+
+
+@pytest.mark.parametrize("D,Hq,G,M", [(64, 32, 8, 250), (128, 32, 8, 250), (256, 16, 2, 300), (64, 30, 6, 200), (128, 6, 2, 900)])
+def test_prompt_rows_in_parts(D, Hq, G, M):
+    """Many rows whose positions are cut into parts, some of them empty."""
+    r, T, B = gen(62), 5000, 2
+    q, k, v = rows(r, B, M, Hq, D, size=1.5), rows(r, B, T, G, D), rows(r, B, T, G, D)
+    assert moe.window_attention_workspace(B, Hq, G, D, M, T) > 0
+    pos, counts = [T - M, 90], [M, M - 5]
+    k[1, 90 + M - 5:], v[1, 90 + M - 5:] = float("nan"), float("nan")
+    check_prompt(q, k, v, None, 0, pos=pos, counts=counts, some=41)
+
+
 def test_prompt_views_and_pieces():
     """q, k and v as views of one projection; the prompt in pieces gives what
     it gives at once, up to rounding; sequences at places of their own."""
