@@ -111,18 +111,23 @@ __device__ __forceinline__ int visible(const KvCall &p, int p0, int n, int &lo, 
 }
 
 // The line of tiles: the prefix's (all of head 0's, then head 1's ...), then for
-// each sequence its heads'.
+// each sequence its heads'.  A sequence's problem has w more places ahead of its tiles, for what its start and end
+// cost, so that a CTA of many short problems has fewer tiles (32 sequences of up to 2000, 32/8/128: 25 -> 22 us; 64 behind a
+// prefix: 65 -> 59); none where a CTA has few tiles.
 struct Line {
     int NP;             // problems of the prefix: its heads, or none
     int ptiles;         // tiles of one of them
-    int total, share;   // tiles; tiles a CTA
+    int w;
+    int total, share;   // places; places a CTA
 };
+constexpr int kPlaces = 2;
 __device__ __forceinline__ Line line_of(const KvCall &p, int seq_tiles, int ctas)
 {
     Line l;
     l.NP = p.split_prefix ? p.Hkv : 0;
     l.ptiles = p.split_prefix ? (p.P + kKvTile - 1) / kKvTile : 0;
-    l.total = l.NP * l.ptiles + seq_tiles * p.Hkv;
+    l.w = l.NP * l.ptiles + seq_tiles * p.Hkv >= 4 * ctas ? kPlaces : 0;
+    l.total = l.NP * l.ptiles + (seq_tiles + l.w * p.B) * p.Hkv;
     l.share = max(1, (l.total + ctas - 1) / ctas);
     return l;
 }
@@ -211,7 +216,44 @@ __global__ void __launch_bounds__(Lay<D>::kThreads, Lay<D>::ctas) kv_split_kerne
     }
     const Line ln = line_of(p, cum[p.B], gridDim.x);
     const int t0 = min(ln.total, (int)blockIdx.x * ln.share), t1 = min(ln.total, t0 + ln.share);
-    if (t0 >= t1) {
+    // the problem and tile that t0 falls on, or the first behind it; tiles up to t1
+    int id0 = -1, i0 = 0, ntiles = 0;
+    {
+        const int pt = ln.NP * ln.ptiles;
+        int left = t1 - t0;
+        if (t0 < pt && left > 0) {
+            id0 = t0 / ln.ptiles;
+            i0 = t0 - id0 * ln.ptiles;
+            ntiles = min(left, pt - t0);
+            left -= ntiles;
+        }
+        if (left > 0) {
+            const int x = max(t0 - pt, 0);
+            int lo = 0, hi = p.B - 1;   // the last b with the places before it <= x
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if ((cum[mid] + ln.w * mid) * p.Hkv <= x) lo = mid;
+                else hi = mid - 1;
+            }
+            int each = cum[lo + 1] - cum[lo], y = x - (cum[lo] + ln.w * lo) * p.Hkv, j = y / (each + ln.w), at = y - j * (each + ln.w);
+            while (left > 0) {
+                const int take = min(left, each + ln.w - at), from = max(at - ln.w, 0), n = max(at + take - ln.w, 0) - from;
+                if (n > 0 && id0 < 0) {
+                    id0 = ln.NP + lo * p.Hkv + j;
+                    i0 = from;
+                }
+                ntiles += n;
+                left -= take;
+                at = 0;
+                if (++j == p.Hkv || each + ln.w == 0) {
+                    j = 0;
+                    if (++lo == p.B) break;
+                    each = cum[lo + 1] - cum[lo];
+                }
+            }
+        }
+    }
+    if (ntiles == 0) {
         if (p.late) wait_for_previous();
         return;
     }
@@ -253,7 +295,7 @@ __global__ void __launch_bounds__(Lay<D>::kThreads, Lay<D>::ctas) kv_split_kerne
         }
         lp.tiles = (lp.n + kKvTile - 1) / kKvTile;
         li = i;
-        lp.whole = i == 0 && lp.tiles <= t1 - t0;
+        lp.whole = i == 0 && lp.tiles <= ntiles;
         ++lcount;
         // its rows of q (those of idle sequences and padding are loaded like the others; nothing of them is used)
         constexpr int CH = D / 8;
@@ -305,36 +347,22 @@ __global__ void __launch_bounds__(Lay<D>::kThreads, Lay<D>::ctas) kv_split_kerne
         }
     };
 
-    // the problem and tile that t0 falls on
-    int left = t1 - t0;   // tiles whose values are not yet loaded
-    {
-        int id, i;
-        const int pt = ln.NP * ln.ptiles;
-        if (t0 < pt) {
-            id = t0 / ln.ptiles;
-            i = t0 - id * ln.ptiles;
-        } else {
-            const int x = t0 - pt;
-            int lo = 0, hi = p.B - 1;   // the last b with cum[b] heads <= x: it has tiles
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if (cum[mid] * p.Hkv <= x) lo = mid;
-                else hi = mid - 1;
-            }
-            const int each = cum[lo + 1] - cum[lo], y = x - cum[lo] * p.Hkv, j = y / each;
-            id = ln.NP + lo * p.Hkv + j;
-            i = y - j * each;
-        }
-        open(id, i);
-        if (tid == 0) probs[0] = lp;
-    }
+    int left = ntiles;   // tiles whose values are not yet loaded
+    open(id0, i0);
+    if (tid == 0) probs[0] = lp;
     // the next unit of the line into the ring
     auto next = [&](int slot_of_ring) {
         if (left > 0) {
             if (li == lp.tiles) {
                 int id = lp.id + 1;
-                if (id >= ln.NP)
-                    while (cum[(id - ln.NP) / p.Hkv + 1] == cum[(id - ln.NP) / p.Hkv]) ++id;   // sequences without tiles (some with are behind)
+                if (id >= ln.NP) {
+                    int b = (id - ln.NP) / p.Hkv;
+                    if (cum[b + 1] == cum[b]) {     // sequences without tiles (some with are behind)
+                        do ++b;
+                        while (cum[b + 1] == cum[b]);
+                        id = ln.NP + b * p.Hkv;
+                    }
+                }
                 open(id, 0);
                 lp.whole = lp.tiles <= left;
                 if (tid == 0) probs[lcount % (L::NQ + 1)] = lp;
@@ -361,7 +389,6 @@ __global__ void __launch_bounds__(Lay<D>::kThreads, Lay<D>::ctas) kv_split_kerne
     int lowA = 0, highA = 0, lowB = 0, highB = 0;  // positions rows see: low < t <= high, or t < S
     Problem cp;
     int ci = -1, ccount = -1, slot = 0;
-    const int ntiles = t1 - t0;
 
 #pragma unroll 1
     for (int it = 0; it < ntiles; ++it) {
@@ -371,14 +398,7 @@ __global__ void __launch_bounds__(Lay<D>::kThreads, Lay<D>::ctas) kv_split_kerne
         if (ci < 0 || ++ci == cp.tiles) {
             ++ccount;
             cp = probs[ccount % (L::NQ + 1)];
-            if (ci < 0) {
-                // the CTA's first: where in the problem it starts
-                const int pt = ln.NP * ln.ptiles;
-                if (cp.b < 0) ci = t0 - cp.id * ln.ptiles;
-                else ci = (t0 - pt - cum[cp.b] * p.Hkv) % cp.tiles;
-            } else {
-                ci = 0;
-            }
+            ci = ci < 0 ? i0 : 0;   // (the CTA's first starts where the CTA does)
 #pragma unroll
             for (int i = 0; i < DW / 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
             mrun[0] = mrun[1] = -INFINITY;
@@ -616,7 +636,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) kv_merge_kernel(const KvCall
         }
         const Line ln = line_of(p, all, ctas);
         const int each = (visible(p, p0, cnt, lo, ns) + kKvTile - 1) / kKvTile, j = b * p.Hkv + g;
-        const int T0 = ln.NP * ln.ptiles + before * p.Hkv + g * each, c0 = T0 / ln.share;
+        const int T0 = ln.NP * ln.ptiles + (before + ln.w * b) * p.Hkv + g * (each + ln.w) + ln.w, c0 = T0 / ln.share;
         n1 = (T0 + each - 1) / ln.share - c0 + 1;
         first = ((size_t)c0 + ln.NP + j) * kKvFewRows + m * p.G + h;
         if (p.split_prefix) {
