@@ -732,6 +732,13 @@ class KV8Cache(_CacheCalls):
         return idx, n
 
 
+def _window_of(window, sinks) -> tuple:
+    """The library's window (0: none) and first positions, which are 32-bit there."""
+    if window is not None and not 1 <= window < 1 << 31 or not 0 <= sinks < 1 << 31:
+        raise ValueError(f"window must be at least 1, or None, and sinks at least 0, both below 2^31; got {window}, {sinks}")
+    return window or 0, sinks
+
+
 class KVCache(_CacheCalls):
     """A 16-bit key/value cache of `batch` sequences (moe_kv_*): k, v bf16 or fp16
     [batch, kv_heads, T_cap, head_dim], with the scratch that attention of up to
@@ -755,12 +762,11 @@ class KVCache(_CacheCalls):
                  buffers=None, ws=None):
         if dtype not in _Q_TYPES:
             raise ValueError("dtype must be torch.bfloat16 or torch.float16")
-        if window is not None and window < 1:
-            raise ValueError("window must be at least 1, or None")
+        W, S = _window_of(window, sinks)
         self.dtype = dtype
         self.T_cap, self.batch, self.q_heads, self.kv_heads, self.head_dim = T_cap, batch, q_heads, kv_heads, head_dim
         self.window, self.sinks, self.max_rows, self.max_prefix = window, sinks, max_rows, max_prefix
-        self._c = Kv(batch, q_heads, kv_heads, head_dim, T_cap, _ROW_TYPES[dtype], window or 0, sinks)
+        self._c = Kv(batch, q_heads, kv_heads, head_dim, T_cap, _ROW_TYPES[dtype], W, S)
         n = C.c_size_t()
         check("moe_kv_attn_workspace_size",
               lib().moe_kv_attn_workspace_size(C.byref(self._c), max_rows, max_prefix, C.byref(n)))
@@ -911,20 +917,19 @@ def window_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window=N
     Bk, T, Hkv, Dk = k.shape
     if k.shape != v.shape or Bk != B or Dk != D:
         raise ValueError(f"q {tuple(q.shape)}, k {tuple(k.shape)} and v {tuple(v.shape)} do not go together")
-    if window is not None and window < 1:
-        raise ValueError("window must be at least 1, or None")
+    shape = (B, Hq, Hkv, D, M, T, *_window_of(window, sinks))
     if stream is not None and stream.device.index != index:
         raise ValueError(f"the stream must be on {q.device}")
     if stream is not None or torch._C._cuda_getDevice() != index:
         with torch.cuda.device(index), torch.cuda.stream(stream):
-            got = _window_call(q, k, v, (B, Hq, Hkv, D, M, T, window or 0, sinks), pos, counts, scale, out, err, ws, index)
+            got = _window_call(q, k, v, shape, pos, counts, scale, out, err, ws, index)
         if stream is not None:
             _CacheCalls._keep(stream, q, k, v, pos, counts, out, err, ws)
             for given, t in zip((out, err), got):
                 if given is None:
                     t.record_stream(torch.cuda.current_stream(index))
         return got
-    return _window_call(q, k, v, (B, Hq, Hkv, D, M, T, window or 0, sinks), pos, counts, scale, out, err, ws, index)
+    return _window_call(q, k, v, shape, pos, counts, scale, out, err, ws, index)
 
 
 def _window_call(q, k, v, shape, pos, counts, scale, out, err, ws, index):
@@ -970,7 +975,7 @@ def window_attention_workspace(batch: int, q_heads: int, kv_heads: int, head_dim
     """Bytes of scratch that window_attention of these sizes needs (moe_window_attn_workspace_size)."""
     n = C.c_size_t()
     check("moe_window_attn_workspace_size",
-          lib().moe_window_attn_workspace_size(Window(batch, q_heads, kv_heads, head_dim, rows, positions, window or 0, sinks), n))
+          lib().moe_window_attn_workspace_size(Window(batch, q_heads, kv_heads, head_dim, rows, positions, *_window_of(window, sinks)), n))
     return n.value
 
 

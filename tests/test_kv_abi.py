@@ -129,3 +129,12 @@ def test_binding_refuses_before_the_library():
         moe.window_attention(x, x, x)
     assert C.sizeof(Kv) == 48 and C.sizeof(Window) == 32
     assert {"moe_kv_append", "moe_kv_attn", "moe_window_attn"} <= set(_lib.SYMBOLS)
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (-1, 0), (2 ** 31, 0), (2 ** 32 + 5, 0), (7, -1), (7, 2 ** 31), (7, 2 ** 32 + 1)])
+def test_windows_outside_32_bits(window, sinks):
+    """None of them reaches the library, which would see their low 32 bits."""
+    with pytest.raises(ValueError, match="window must be"):
+        moe.window_attention_workspace(1, 8, 2, 64, 1000, 1000, window, sinks)
+    with pytest.raises(ValueError, match="window must be"):
+        moe.KVCache(2000, q_heads=8, kv_heads=2, head_dim=64, window=window, sinks=sinks, device="cpu")
