@@ -13,7 +13,7 @@
 // problem per head with the whole batch's rows: its keys are read once.  Every problem is
 // cut into tiles of 64 positions, the tiles of all problems lie in one line, and each
 // CTA takes an equal stretch of it: whatever the lengths are (they are read on the device),
-// all CTAs move the same number of bytes.  A stretch that holds a whole problem writes its
+// all CTAs move about the same number of bytes.  A stretch that holds a whole problem writes its
 // outputs; a part of one leaves its unnormalised sum, maximum and sum of weights (the
 // running maximum and sum of a softmax), which the merge kernel joins in
 // order.  Slot (CTA + problem) is a part's own: along the line either grows.

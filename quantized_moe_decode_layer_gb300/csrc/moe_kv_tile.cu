@@ -4,7 +4,7 @@
 //
 // The rows that share a key/value head (query rows times heads per key/value
 // head) are packed into tiles of 128, the positions that any of a CTA's rows
-// sees into tiles of 128 slots: the first ones, then the window (in a ring, the slots that it
+// sees into tiles of two halves of 64 slots: the first ones, then the window from where it begins (in a ring, the slots that it
 // lies in; each slot's position follows from where the window starts).  Per tile of positions
 //     S = Q K^T            128 x 128, fp32 in tensor memory
 //     P = 2^(c S - ref)    16 bits, in tensor memory over S;  l += row sums
@@ -20,13 +20,13 @@
 // tiles of one row tile (two S, one O); those hand the reference on from
 // one to the other.  A CTA is persistent and goes through items (row tiles of a head) that warp 11 finds
 // ahead of the others.  Warps 0-3 and 4-7 are the streams' softmax (thread = row),
-// warp 8 loads K and V by TMA (boxes of 128 positions x 64 elements, 128-byte swizzle), one thread of
+// warp 8 loads K and V by TMA (boxes of 64 positions x 64 elements, 128-byte swizzle), one thread of
 // warp 9 issues the products, warps 10 and 11 load q.  V is taken as it lies, [position][d] with d
 // contiguous (an MN-major operand), P from tensor memory; outputs leave through a box in shared memory.
 //
-// Bound by the tensor core with D = 256 (a prompt of 16K, window 4096, 16/2/256: 0.59 to 0.61 ms, 1.59 PFLOP/s of the
-// pairs that are seen, 84 % of the measured rate), by a stream's chain of S, softmax and P V with D = 128 (32/8/128:
-// 0.68 to 0.72 ms), by the softmax warps with D = 64 (32/8/64: 0.52 ms).
+// Bound by the tensor core with D = 256 (a prompt of 16K, window 4096, 16/2/256: 0.59 to 0.61 ms, 1.6 PFLOP/s of the
+// pairs that are seen, 85 % of the measured rate), by a stream's chain of S, softmax and P V with D = 128 (32/8/128:
+// 0.70 ms), by the softmax warps with D = 64 (32/8/64: 0.52 ms).
 //
 // Every wait is bounded; one that runs out sets *err, the roles stop, the CTA waits
 // (bounded) for its copies and products and frees its tensor memory.
@@ -67,7 +67,7 @@ struct TLay {
     static constexpr int RT = NQ * kRows;
     static constexpr int kUnit = D == 64 ? kBox : 2 * kBox;   // 128 positions x min(D, 128)
     static constexpr int UPT = D == 256 ? 2 : 1;              // units of a tile of keys or values
-        static constexpr int NU = D == 64 ? 8 : 4;                // (5 at 128, 256 measured no faster)
+    static constexpr int NU = D == 64 ? 8 : 4;                // (5 at 128, 256 measured no faster)
     static constexpr int q = 0;
     static constexpr int ring = NQ * (D / 64) * kBox;
     static constexpr int stage = ring + NU * kUnit;           // outputs on their way, a box a stream
