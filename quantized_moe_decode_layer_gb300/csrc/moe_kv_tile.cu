@@ -556,7 +556,9 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                 go = items.get(k, it, abort_flag, p);
                 __syncwarp();
                 if (lane == 0) items.done(k);
-                if (go && it.nt > 0 && qn > 0) go = bar_wait(su32(q_free), (unsigned)(qn - 1) & 1u, abort_flag, p);
+                // (warp 11 only where it loads, too: else q could be freed twice before it looks, and it would wait for a phase
+                // that is gone)
+                if (go && it.nt > 0 && qn > 0 && (warp == 10 || !tp.qmap)) go = bar_wait(su32(q_free), (unsigned)(qn - 1) & 1u, abort_flag, p);
                 go = __all_sync(0xFFFFFFFFu, go);
                 if (!go) break;
                 if (it.nt == 0) {

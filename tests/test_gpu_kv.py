@@ -288,6 +288,22 @@ def test_prompt_turns(B, Hq, G):
     check_prompt(q, k, v, None, 0, pos=[0] * B, counts=counts, some=37)
 
 
+@pytest.mark.parametrize("D,Hq,G", [(64, 16, 8), (128, 16, 8), (256, 16, 8)])
+def test_many_short_items(D, Hq, G):
+    """A window of 1: every row is its own value, and what a CTA does for 128 rows is as short as it gets, so that its
+    warps run as far ahead of each other as they can."""
+    r, B, M = gen(63), 6, 1500
+    q, k, v = rows(r, B, M, Hq, D), rows(r, B, M, G, D), rows(r, B, M, G, D)
+    pos = i32([0, 500, 0, -1, 3, 0])
+    for n in range(40):
+        counts = [(257 * n + 311 * b) % (M - 500) for b in range(B)]
+        o, err = moe.window_attention(q, k, v, 1, pos=pos, counts=i32(counts))
+        assert err_of(err) == 0
+        for b, (p, c) in enumerate(zip((0, 500, 0, -1, 3, 0), counts)):
+            c = c if p >= 0 else 0
+            assert torch.equal(o[b, :c], v[b, max(p, 0):max(p, 0) + c].repeat_interleave(Hq // G, 1)) and not o[b, c:].any()
+
+
 @pytest.mark.parametrize("D,Hq,G,M", [(64, 32, 8, 250), (128, 32, 8, 250), (256, 16, 2, 300), (64, 30, 6, 200), (128, 6, 2, 900)])
 def test_prompt_rows_in_parts(D, Hq, G, M):
     """Many rows whose positions are cut into parts, some of them empty."""
