@@ -441,7 +441,7 @@ __global__ void __launch_bounds__(Lay<D>::kThreads, Lay<D>::ctas) kv_split_kerne
 #pragma unroll
         for (int j = 0; j < KW / 8; ++j)
 #pragma unroll
-            for (int x = 0; x < 4; ++x) s[j][x] *= p.c;
+            for (int x = 0; x < 4; ++x) s[j][x] = __fmul_rn(s[j][x], p.c);
         if (edge) {
 #pragma unroll
             for (int j = 0; j < KW / 8; ++j)
@@ -466,8 +466,8 @@ __global__ void __launch_bounds__(Lay<D>::kThreads, Lay<D>::ctas) kv_split_kerne
         }
         // The reference follows the maximum only when that is above it by more
         // than 8 (a factor of 256, far from fp16's and fp32's ends): the
-        // output is hardly ever rescaled.
-        if (__any_sync(0xFFFFFFFFu, mx[0] > mrun[0] + 8.f || mx[1] > mrun[1] + 8.f)) {
+        // output is hardly ever rescaled.  (The difference: a sum would round past the maximum where scores are 16 apart.)
+        if (__any_sync(0xFFFFFFFFu, __fsub_rn(mx[0], mrun[0]) > 8.f || __fsub_rn(mx[1], mrun[1]) > 8.f)) {
             float al[2];
 #pragma unroll
             for (int x = 0; x < 2; ++x) {

@@ -877,14 +877,14 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                 tmem_wait_ld();
                 hide(1, s1);
                 largest(s1);
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+                const float top = __fmul_rn(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), c);
                 float was = ref;
                 if (!PAIR && i > 0) {   // the reference, from the stream that has the tile before
                     wait(&ref_rdy[4 * (xs ^ 1) + w], done[xs ^ 1] + ((i - 1) >> 1));
                     if (!go) break;
                     was = refs[row];
                 }
-                const bool raise = top > was + 8.f;
+                const bool raise = __fsub_rn(top, was) > 8.f;   // (was + 8 would round past top where scores are 16 apart)
                 const float now = raise ? top : was;
                 if (!PAIR) {
                     refs[row] = now;
