@@ -7,10 +7,10 @@
 // sees into tiles of two halves of 64 slots: the first ones, then the window from where it begins (in a ring, the slots that it
 // lies in; each slot's position follows from where the window starts).  Per tile of positions
 //     S = Q K^T            128 x 128, fp32 in tensor memory
-//     P = 2^(c S - ref)    16 bits, in tensor memory over S;  l += row sums
+//     P = 2^(c (S - ref))  16 bits, in tensor memory over S;  l += row sums
 //     O += P V             128 x D, fp32 in tensor memory
-// with ref a running maximum that follows only when the true one is above it by
-// more than 8: the weights stay below 2^8, far from any type's end, and O is
+// with c = scale log2(e) and ref a running maximum that follows only when the true one is above it by
+// more than 8 / c: the weights stay below 2^8, far from any type's end, and O is
 // hardly ever rescaled.  A weight is rounded to 16 bits for its product, an error of the size of the output's own
 // rounding; l has it as it was.
 //
@@ -84,6 +84,11 @@ static_assert(TLay<64>::total + 1024 <= kSmemMax && TLay<128>::total + 1024 <= k
 // tensor memory: S at columns 0 and 128 (and 384), O from 256 on, P over S
 constexpr uint32_t kTmemCols = 512;
 __device__ __forceinline__ uint32_t s_col(int b) { return b == 2 ? 384u : 128u * (uint32_t)b; }
+// A weight's exponent is c s - c ref, one fused product and sum with the rounded product c ref, so a row's largest one is off by
+// that rounding: up to half a spacing of c ref, 2^-14 at 2^10 and 64 at 2^30, which no 16-bit weight holds.  Rows whose c ref
+// is beyond 2^10 take c (s - ref) instead, where the largest is exact.  (The vote and its branch, taken by hardly any warp: 8195 rows,
+// window 1024, 32/8/128: 125 -> 128 us; 32/8/64 and 16/2/256 within 1 %.)
+constexpr float kFar = 1024.f;
 // registers a thread: launched with 168; the softmax warps take what the others leave
 constexpr int kRegsSoft = 208, kRegsRest = 88;
 static_assert(256 * kRegsSoft + 128 * kRegsRest <= kTThreads * 168, "registers");
@@ -877,21 +882,21 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                 tmem_wait_ld();
                 hide(1, s1);
                 largest(s1);
-                const float top = __fmul_rn(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), c);
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                 float was = ref;
                 if (!PAIR && i > 0) {   // the reference, from the stream that has the tile before
                     wait(&ref_rdy[4 * (xs ^ 1) + w], done[xs ^ 1] + ((i - 1) >> 1));
                     if (!go) break;
                     was = refs[row];
                 }
-                const bool raise = __fsub_rn(top, was) > 8.f;   // (was + 8 would round past top where scores are 16 apart)
+                const bool raise = __fsub_rn(top, was) * c > 8.f;   // (a sum of was and the slack would round past top where scores are far apart)
                 const float now = raise ? top : was;
                 if (!PAIR) {
                     refs[row] = now;
                     __syncwarp();
                     if (lane == 0) bar_arrive(su32(&ref_rdy[4 * xs + w]));
                 }
-                if (now != ref) l *= ref == -INFINITY ? 0.f : ex2(ref - now);
+                if (now != ref) l *= ref == -INFINITY ? 0.f : ex2((ref - now) * c);
                 ref = now;
                 if (__any_sync(0xFFFFFFFFu, raise) && t > 0) {
                     // O, which has the tiles up to the one before, in the new reference's units
@@ -903,7 +908,7 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                     }
                     if (!go) break;
                     fence_after();
-                    const float f = raise ? ex2(was - now) : 1.f;
+                    const float f = raise ? ex2((was - now) * c) : 1.f;
 #pragma unroll 1
                     for (int k = 0; k < D; k += 32) {
                         uint32_t o[32];
@@ -914,7 +919,24 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                         tmem_st32(oc + k, o);
                     }
                 }
-                const float sub = ref == -INFINITY ? 0.f : -ref;
+                float sub = ref == -INFINITY ? 0.f : __fmul_rn(-ref, c);
+                const bool far = fabsf(sub) > kFar;
+                if (__any_sync(0xFFFFFFFFu, far)) {
+                    const float shift = far ? -ref : 0.f;   // (0 changes nothing)
+                    const uint64_t shift2 = two(shift, shift);
+                    auto move = [&](uint32_t *s) {
+#pragma unroll
+                        for (int j = 0; j < KS; j += 2) {
+                            float a, b;
+                            split2(add2(two(__uint_as_float(s[j]), __uint_as_float(s[j + 1])), shift2), a, b);
+                            s[j] = __float_as_uint(a);
+                            s[j + 1] = __float_as_uint(b);
+                        }
+                    };
+                    move(s0);
+                    move(s1);
+                    if (far) sub = 0.f;
+                }
                 weights(0, s0, two(sub, sub));
                 // (one half's P on its way while the other's is computed: 16384 positions, all seen, 1157 -> 1132 us with 64
                 // columns, 1547 -> 1528 with 128, 1294 -> 1312 with 256)
@@ -939,7 +961,7 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
             if (!PAIR) {
                 asm volatile("bar.sync 1, 256;" ::: "memory");    // the references are final
                 const float end = refs[row];
-                sums[128 * xs + row] = ref == -INFINITY ? l : l * ex2(ref - end);   // (without a reference l is 0 or NaN)
+                sums[128 * xs + row] = ref == -INFINITY ? l : l * ex2((ref - end) * c);   // (without a reference l is 0 or NaN)
                 ref = end;
                 asm volatile("bar.sync 1, 256;" ::: "memory");
                 l = sums[row] + sums[128 + row];
@@ -1003,7 +1025,7 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                 }
             } else if (go) {
                 // Four lanes exchange 64-byte pieces: lane 4 a + j then has piece j of rows 4 a .. 4 a + 3.
-                if (parts && r < rows && col0 == 0) *reinterpret_cast<float2 *>(to_parts.ml + (part0 + r) * 2) = make_float2(ref, l);
+                if (parts && r < rows && col0 == 0) *reinterpret_cast<float2 *>(to_parts.ml + (part0 + r) * 2) = make_float2(ref * c, l);
                 const int rq = r - (lane & 3);
                 uint8_t *to[4];     // the four rows' places
                 int m = p.by_g(rq), h = rq - m * p.G - 1;

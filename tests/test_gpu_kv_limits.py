@@ -33,3 +33,58 @@ def test_scores_one_spacing_apart(dtype, D, tokens):
         o, err = moe.window_attention(q, k, v, scale=scale)
         assert err_of(err) == 0
         kv_ref.close(o, want[None, :, None], tol[None, :, None], f"scale {step}")
+
+
+def _sizes(D):
+    """Scales that make scores of 2^0 to 2^40, with full mantissas."""
+    return [1.2345 * 2.0 ** e * D ** -0.5 for e in (0, 5, 9, 10, 11, 13, 16, 19, 20, 21, 23, 24, 25, 26, 27, 28, 29, 30, 31, 32, 33, 36, 40)]
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_one_visible_position_at_any_score(dtype, D):
+    """A window of 1: the output is the value, however large the score: as prompts, tokens, drafts."""
+    r, n, G = gen(71), 300, 2
+    q, k, v = rows(r, 1, n, 8, D, dtype=dtype), rows(r, 1, n, G, D, dtype=dtype), rows(r, 1, n, G, D, dtype=dtype)
+    want = v.repeat_interleave(4, 2)
+    caches = []
+    for M, Hq in ((1, 2), (4, 8), (8, 8)):
+        c = moe.KVCache(M + 20, q_heads=Hq, kv_heads=G, head_dim=D, dtype=dtype, window=1, max_rows=M)
+        c.append(k, v, i32([0]))
+        caches.append((c, M, Hq))
+    for scale in _sizes(D):
+        o, err = moe.window_attention(q, k, v, 1, scale=scale)
+        assert err_of(err) == 0 and torch.equal(o, want), scale
+        for c, M, Hq in caches:
+            o, _ = c.attend(q[:, n - M:, ::8 // Hq].contiguous(), i32([n - M]), scale=scale)
+            assert torch.equal(o, want[:, n - M:, ::8 // Hq]), (scale, M)
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("window", [2, 5, 150])
+def test_few_visible_positions_at_any_score(dtype, D, window):
+    """A mean of the visible values; and where one score is above all others by more than all errors, its value.  (A weight
+    and the output are rounded: half a step each.)"""
+    r, n, half = gen(72), 300, kv_ref.HALF[dtype]
+    q, k, v = rows(r, 1, n, 4, D, dtype=dtype), rows(r, 1, n, 1, D, dtype=dtype), rows(r, 1, n, 1, D, dtype=dtype)
+    at = torch.arange(n, device=DEV)
+    sees = (at[None] <= at[:, None]) & (at[None] > at[:, None] - window)
+    vd = v[0, :, 0].double()
+    low = torch.stack([vd[max(0, p - window + 1):p + 1].amin(0) for p in range(n)])[:, None]
+    high = torch.stack([vd[max(0, p - window + 1):p + 1].amax(0) for p in range(n)])[:, None]
+    edge = 2.01 * half * torch.maximum(low.abs(), high.abs()) + 2.0 ** -24
+    z1 = torch.einsum("mhd,td->mht", q[0].double(), k[0, :, 0].double())
+    a1 = torch.einsum("mhd,td->mht", q[0].double().abs(), k[0, :, 0].double().abs())
+    for scale in _sizes(D):
+        z = (z1 * scale).masked_fill(~sees[:, None], -1e300)
+        top = z.topk(2, -1)
+        err = 2 * (D + 6) * kv_ref.E23 * (a1 * scale).masked_fill(~sees[:, None], 0).amax(-1)
+        clear = top.values[..., 0] - top.values[..., 1] > err + 40
+        o, e = moe.window_attention(q, k, v, window, scale=scale)
+        assert err_of(e) == 0
+        o = o[0].double()
+        assert bool(((o >= low - edge) & (o <= high + edge)).all()), scale
+        best = vd[top.indices[..., 0]]
+        assert scale < 2 ** 9 or bool(clear.any())
+        assert bool(((o - best).abs() <= 2.01 * half * best.abs() + 2.0 ** -24)[clear].all()), scale
