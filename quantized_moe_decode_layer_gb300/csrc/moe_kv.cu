@@ -25,8 +25,8 @@
 // sequences of up to 4096 positions, 8 heads of 128: 115 us, 6.6 TB/s, 97 to 99 % of a copy's rate.
 //
 // Scores, maxima, sums and outputs are fp32; the weights are rounded to the
-// cache's 16-bit type for the second product, an error of the size
-// of the output's own rounding.
+// cache's 16-bit type for the second product, an error of half a step, as the
+// output's own rounding is (fp16's smallest weights: kv_up in moe_kv.h).
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -176,6 +176,7 @@ __global__ void __launch_bounds__(Lay<D>::kThreads, Lay<D>::ctas) kv_split_kerne
     using L = Lay<D>;
     constexpr int RB = L::RB, WK = L::WK, WD = L::WD, KW = L::KW, NU = L::NU, kThreads = L::kThreads;
     constexpr int DW = D / WD;      // a warp's columns
+    constexpr float kUp = kv_up(F16);
     extern __shared__ __align__(128) uint8_t sm[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     Problem *probs = reinterpret_cast<Problem *>(sm + L::probs);
@@ -464,14 +465,15 @@ __global__ void __launch_bounds__(Lay<D>::kThreads, Lay<D>::ctas) kv_split_kerne
             mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xFFFFFFFFu, mx[0], o));
             mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xFFFFFFFFu, mx[1], o));
         }
-        // The reference follows the maximum only when that is above it by more
+        // The reference, kUp below a maximum, follows it only when that has grown by more
         // than 8 (a factor of 256, far from fp16's and fp32's ends): the
         // output is hardly ever rescaled.  (The difference: a sum would round past the maximum where scores are 16 apart.)
-        if (__any_sync(0xFFFFFFFFu, __fsub_rn(mx[0], mrun[0]) > 8.f || __fsub_rn(mx[1], mrun[1]) > 8.f)) {
+        const bool raise[2] = {__fsub_rn(mx[0], mrun[0]) > 8.f + kUp, __fsub_rn(mx[1], mrun[1]) > 8.f + kUp};
+        if (__any_sync(0xFFFFFFFFu, raise[0] || raise[1])) {
             float al[2];
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                const float mn = fmaxf(mrun[x], mx[x]);
+                const float mn = raise[x] ? __fsub_rn(mx[x], kUp) : mrun[x];
                 al[x] = mrun[x] == mn ? 1.f : ex2(mrun[x] - mn);
                 mrun[x] = mn;
                 lrun[x] *= al[x];

@@ -12,6 +12,11 @@ constexpr int kKvMaxCtas = 4 * kMaxCtas;
 constexpr int kKvMaxPos = 1 << 30;    // positions of a sequence whose cache is a ring
 constexpr int kKvAll = 1 << 30;       // window of a sequence that sees everything
 
+// Weights are held 2^kv_up times as large as the reference says.  fp16's smallest step is 2^-24: with 2^7, weights from 2^-21 of the
+// reference on have all bits, and what smaller ones lose is at most 2^-32 of the reference for each (131071 of 2^-25 behind one of
+// 1 were zeros, and are off by less than 1 %).  With the 2^8 that the maximum may be above it they stay below 2^15.  bf16 has fp32's exponents.
+constexpr __host__ __device__ float kv_up(bool f16) { return f16 ? 7.f : 0.f; }
+
 // Division of 0 <= x < 2^31 by a number of heads (at most 2^20), exactly: x m / 2^s.
 struct Div {
     uint32_t m;
@@ -47,7 +52,7 @@ struct KvCall {
     // split kernel: of the sequences' own positions, of the prefix's
     int split_own, split_prefix;
     int late;                         // the call's second kernel: beside the first, whose end it waits for at its own
-    float *part_o, *part_ml;          // [slot][16][D], [slot][16][2]: unnormalised output; maximum (log2), sum
+    float *part_o, *part_ml;          // [slot][16][D], [slot][16][2]: unnormalised output; reference (log2), sum
     // tile kernel: parts of the own positions, of the prefix's
     struct Parts {
         int n;                        // 0: not taken; own positions, 1 without a prefix: outputs are written

@@ -11,8 +11,9 @@
 //     O += P V             128 x D, fp32 in tensor memory
 // with c = scale log2(e) and ref a running maximum that follows only when the true one is above it by
 // more than 8 / c: the weights stay below 2^8, far from any type's end, and O is
-// hardly ever rescaled.  A weight is rounded to 16 bits for its product, an error of the size of the output's own
-// rounding; l has it as it was.
+// hardly ever rescaled.  A weight is rounded to 16 bits for its product, an error of half a step of the type, as the output's own
+// rounding is; l has it as it was.  fp16 holds weights 2^kUp times as large, below 2^15: its steps end at 2^-24, so those below 2^-21
+// of the reference are off by 2^-32 of it (kv_up in moe_kv.h).
 //
 // Two streams of steps alternate on the tensor core, so that it has one's
 // products while the other's softmax runs: with D <= 128 two row tiles
@@ -433,6 +434,7 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
     constexpr bool PAIR = L::kPair, AHEAD = L::kAhead, TURNS = L::kTurns;
     constexpr int KS = kHalf, NB = L::NB;
     constexpr int NU = L::NU, UPT = L::UPT, RT = L::RT;
+    constexpr float kUp = kv_up(F16), kDown = 1.f / (float)(1 << (int)kUp);
     const KvCall &p = tp.c;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -919,7 +921,7 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                         tmem_st32(oc + k, o);
                     }
                 }
-                float sub = ref == -INFINITY ? 0.f : __fmul_rn(-ref, c);
+                float sub = ref == -INFINITY ? 0.f : __fmaf_rn(-ref, c, kUp);
                 const bool far = fabsf(sub) > kFar;
                 if (__any_sync(0xFFFFFFFFu, far)) {
                     const float shift = far ? -ref : 0.f;   // (0 changes nothing)
@@ -935,7 +937,7 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                     };
                     move(s0);
                     move(s1);
-                    if (far) sub = 0.f;
+                    if (far) sub = kUp;
                 }
                 weights(0, s0, two(sub, sub));
                 // (one half's P on its way while the other's is computed: 16384 positions, all seen, 1157 -> 1132 us with 64
@@ -1025,7 +1027,7 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                 }
             } else if (go) {
                 // Four lanes exchange 64-byte pieces: lane 4 a + j then has piece j of rows 4 a .. 4 a + 3.
-                if (parts && r < rows && col0 == 0) *reinterpret_cast<float2 *>(to_parts.ml + (part0 + r) * 2) = make_float2(ref * c, l);
+                if (parts && r < rows && col0 == 0) *reinterpret_cast<float2 *>(to_parts.ml + (part0 + r) * 2) = make_float2(ref * c, l * kDown);
                 const int rq = r - (lane & 3);
                 uint8_t *to[4];     // the four rows' places
                 int m = p.by_g(rq), h = rq - m * p.G - 1;
@@ -1055,7 +1057,7 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                         uint32_t v[16];
 #pragma unroll
                         for (int j = 0; j < 16; ++j) {
-                            if (parts) v[j] = o[16 * half + j];
+                            if (parts) v[j] = __float_as_uint(__uint_as_float(o[16 * half + j]) * kDown);
                             else v[j] = live && nt > 0 ? pack2<F16>(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv) : 0u;
                         }
                         quad_transpose(v, lane);

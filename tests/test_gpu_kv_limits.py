@@ -88,3 +88,29 @@ def test_few_visible_positions_at_any_score(dtype, D, window):
         best = vd[top.indices[..., 0]]
         assert scale < 2 ** 9 or bool(clear.any())
         assert bool(((o - best).abs() <= 2.01 * half * best.abs() + 2.0 ** -24)[clear].all()), scale
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("low", [17.375, 20.25, 24.0, 25.125, 28.0])
+def test_many_small_weights_in_fp16(D, low):
+    """A strong first position whose values are 0 before 131071 whose weights are 2^-low of its own: rows enough that they are
+    not cut into many parts, and single tokens.  A weight below 2^-21 of the reference is off by 2^-32 of it (a weight of 1 is 2^7
+    in fp16, whose smallest step is 2^-24); the largest weight is at least the reference."""
+    n, half, r = 1 << 17, kv_ref.HALF[FP], gen(73)
+    k, v = torch.zeros((1, n, 1, D), dtype=FP, device=DEV), rows(r, 1, n, 1, D, dtype=FP).abs() + 0.5
+    k[0, 0, 0, 0], v[0, 0] = low, 0.0
+    scale, w = 0.6931471805599453, 2.0 ** -low                            # scores in units of log2
+
+    def check(got, seen, what):
+        x = v[0, :seen, 0].double()
+        want = w * x.sum(0) / (1 + w * (seen - 1))
+        tol = ((2 * half + 2 * (D + 6) * kv_ref.E23 * low + 2.0 ** -21 + (2 * n + 64) * kv_ref.E23) * want + n * 2.0 ** -32 * x.max() +
+               2.0 ** -25)
+        kv_ref.close(got, want, tol, what)
+    for M, Hq in ((1300, 32), (1, 1), (1, 32)):
+        q = torch.zeros((1, M, Hq, D), dtype=FP, device=DEV)
+        q[..., 0] = 1.0
+        o, err = moe.window_attention(q, k, v, scale=scale)
+        assert err_of(err) == 0
+        for m in sorted({0, M // 2, M - 1}):
+            check(o[0, m], n - M + m + 1, f"weights of 2^-{low}, row {m} of {M}")
