@@ -785,7 +785,9 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
             const size_t part0 = ((size_t)it.z * p.Hkv + it.g) * ((size_t)p.B * p.M * p.G) + (PREFIX ? 0 : (size_t)it.b * p.M * p.G);
             // The row is at position pos.  Slot s has position s (s < S), else s + off (s >= sl),
             // else s + off + R; it is seen if pos - W < position <= pos, or s < S.
-            int pos = 0, valid = INT_MAX;      // valid: slots from there on hold anything (a ring that is full has none)
+            // Slots hole0 .. hole1 - 1 and from valid on may hold anything.  In a ring: all that none of the item's rows sees, as rows that
+            // were appended and rejected lie behind the last position some way around.
+            int pos = 0, valid = INT_MAX, hole0 = 0, hole1 = 0;
             const int R = p.ring ? p.T - p.S : kKvAll;
             // halves that all rows see all of: `inner` of the window's from inner0 on (others that are take the slower way)
             int inner0 = 0, inner = p.P / kHalf - 2 * it.i0;
@@ -794,6 +796,12 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                 const int pos_lo = it.p0 + p.by_g(ra), pos_hi = it.p0 + p.by_g(ra + kRows - 1);
                 pos = it.p0 + p.by_g(r);
                 if (it.p0 + it.cnt <= p.T) valid = it.p0 + it.cnt;
+                if (p.ring) {
+                    const int last = min(p.by_g(it.r0 + (it.one ? kRows : RT) - 1), it.cnt - 1), end = it.p0 + last - it.off;
+                    hole0 = max(min(p.S, it.sl + it.off), end >= p.T ? p.S + end - p.T + 1 : 0);
+                    hole1 = it.sl;
+                    valid = min(end, p.T - 1) + 1;
+                }
                 int lo = pos_hi - it.off - p.W + 1;
                 if (lo <= max(it.sl, p.S)) lo = it.sl;
                 inner0 = it.nfront + (lo - it.from + kHalf - 1) / kHalf;
@@ -811,8 +819,9 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                 if (!go) break;
                 fence_after();
                 auto all_seen = [&](int half) { return (unsigned)(2 * t + half - inner0) < (unsigned)inner; };
-                if (!PREFIX && !(all_seen(0) && all_seen(1)) && valid - max(it.first_key(t, 0), it.first_key(t, 1)) < kHalf && (!PAIR || xs == 0)) {
-                    // values behind the sequence's last position may be anything: zeros
+                auto any_left = [&](int key) { return valid < key + kHalf || max(key, hole0) < min(key + kHalf, hole1); };
+                if (!PREFIX && !(all_seen(0) && all_seen(1)) && (any_left(it.first_key(t, 0)) || any_left(it.first_key(t, 1))) && (!PAIR || xs == 0)) {
+                    // values that may be anything: zeros
                     const int n0 = units + UPT * v_order<AHEAD>(t, nt);
 #pragma unroll 1
                     for (int u = n0; u < n0 + UPT; ++u) {
@@ -821,12 +830,14 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                         uint8_t *unit = sm + L::ring + (u % NU) * L::kUnit;
 #pragma unroll
                         for (int half = 0; half < 2; ++half) {
-                            const int left = max(valid - it.first_key(t, half), 0);
-                            for (int j = row; j < (kHalf - left) * 8; j += 128)
+                            const int key = it.first_key(t, half);
+                            for (int j = row; j < kHalf * 8; j += 128) {
+                                const int slot = key + (j >> 3);
+                                if (slot < valid && (slot < hole0 || slot >= hole1)) continue;
 #pragma unroll
                                 for (int h = 0; h < L::kUnit / kBox; ++h)
-                                    *reinterpret_cast<uint4 *>(unit + h * kBox + half * (kBox / 2) + left * 128 + j * 16) =
-                                        make_uint4(0u, 0u, 0u, 0u);
+                                    *reinterpret_cast<uint4 *>(unit + h * kBox + half * (kBox / 2) + j * 16) = make_uint4(0u, 0u, 0u, 0u);
+                            }
                         }
                     }
                     if (!go) break;

@@ -114,3 +114,36 @@ def test_many_small_weights_in_fp16(D, low):
         assert err_of(err) == 0
         for m in sorted({0, M // 2, M - 1}):
             check(o[0, m], n - M + m + 1, f"weights of 2^-{low}, row {m} of {M}")
+
+
+# -------------------------------------------------------------- what is past
+
+@pytest.mark.parametrize("D,Hq,M", [(64, 4, 8), (128, 4, 8), (128, 3, 6), (256, 16, 2), (256, 8, 8), (64, 64, 8), (128, 64, 8), (64, 2, 4)])
+@pytest.mark.parametrize("W,S,extra", [(100, 4, 3), (64, 0, 4), (57, 70, 3), (7, 3, 50), (200, 1, 120), (1, 0, 3)])
+def test_rejected_rows_in_a_full_ring(D, Hq, M, W, S, extra):
+    """Drafts behind a sequence's end, some way around the ring: their keys and values are NaN and infinity,
+    after padding, after all rows were rejected, and after a step back of three more."""
+    T = S + W + M - 1 + extra
+    ends = sorted({T - M, T - 1, T, T + 1, T + 9, 2 * T - S - M, 2 * T - S - 1, 2 * T - S, 2 * T - S + 3, T + 61, T + 64, T + 67, 3 * T + 17})
+    B, n = len(ends), max(ends) + M + 1
+    r = gen(74)
+    k, v, q = rows(r, B, n, 1, D), rows(r, B, n, 1, D), rows(r, B, M, Hq, D, size=1.5)
+    cache = moe.KVCache(T, batch=B, q_heads=Hq, kv_heads=1, head_dim=D, window=W, sinks=S, max_rows=M)
+    cache.k.fill_(float("nan"))
+    cache.v.fill_(float("nan"))
+    cache.append(k, v, i32([0] * B), counts=i32(ends))
+    bad = torch.full((B, M, 1, D), float("nan"), dtype=BF, device=DEV)
+    bad[:, ::2] = float("inf")
+    cache.append(bad, bad, i32(ends))
+    for back, counts in ((0, [1 + b % M for b in range(B)]), (0, [1] * B), (3, [1 + b % 2 for b in range(B)])):
+        pos = [max(e - back, 0) for e in ends]
+        at = torch.tensor(pos, device=DEV)[:, None] + torch.arange(M, device=DEV)
+        b = torch.arange(B, device=DEV)[:, None]
+        cache.append(bad, bad, i32(pos))
+        cache.append(k[b, at], v[b, at], i32(pos), counts=i32(counts))
+        o, err = cache.attend(q, i32(pos), counts=i32(counts))
+        assert err_of(err) == 0
+
+        def of(x):
+            return lambda b, m: x[b, kv_ref.seen(pos[b] + m, W, S).to(DEV)]
+        kv_ref.check_rows(o, q, of(k), of(v), lambda b, m: m < counts[b], D ** -0.5)
