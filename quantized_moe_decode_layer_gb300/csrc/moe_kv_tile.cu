@@ -384,7 +384,8 @@ static_assert(sizeof(Item) <= kItemBytes + 4, "an item's words (the last bit of 
 struct Items {
     uint8_t *ring;
     uint64_t *ready, *read;
-    // The n-th, once it is there.  After the last of a role's threads has it: done(n).
+    // The n-th, once it is there.  After the last of a role's threads has it: done(n).  Where the wait gave up it holds anything, and
+    // done is not called any more: an item's place is not written again while some thread may still read it.
     __device__ __forceinline__ bool get(int n, Item &it, volatile int *abort, const KvCall &c) const
     {
         const int s = n % kItems;
@@ -510,8 +511,8 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                 for (int k = 0; k < mine && go; ++k) {
                     Item it;
                     go = items.get(k, it, abort_flag, p);
-                    items.done(k);
                     if (!go) break;
+                    items.done(k);
                     auto load = [&](const CUtensorMap *map, int t) {
                         const int key0 = it.first_key(t, 0), key1 = it.first_key(t, 1);
                         for (int u = 0; u < UPT && go; ++u) {
@@ -560,12 +561,12 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
             tell(1);
             for (int k = 0; k < mine; ++k) {
                 Item it;
-                go = items.get(k, it, abort_flag, p);
-                __syncwarp();
+                go = __all_sync(0xFFFFFFFFu, items.get(k, it, abort_flag, p));
+                if (!go) break;
                 if (lane == 0) items.done(k);
                 // (warp 11 only where it loads, too: else q could be freed twice before it looks, and it would wait for a phase
                 // that is gone)
-                if (go && it.nt > 0 && qn > 0 && (warp == 10 || !tp.qmap)) go = bar_wait(su32(q_free), (unsigned)(qn - 1) & 1u, abort_flag, p);
+                if (it.nt > 0 && qn > 0 && (warp == 10 || !tp.qmap)) go = bar_wait(su32(q_free), (unsigned)(qn - 1) & 1u, abort_flag, p);
                 go = __all_sync(0xFFFFFFFFu, go);
                 if (!go) break;
                 if (it.nt == 0) {
@@ -657,8 +658,8 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                 for (int n = 0; n < mine && go; ++n) {
                     Item it;
                     go = items.get(n, it, abort_flag, p);
-                    items.done(n);
                     if (!go) break;
+                    items.done(n);
                     const int nt = it.nt;
                     if (nt == 0) continue;
                     auto work = [&](auto duo_v) {
@@ -771,17 +772,18 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
         auto wait = [&](uint64_t *bar, int parity) {
             go = __all_sync(0xFFFFFFFFu, go && bar_wait(su32(bar), (unsigned)parity & 1u, abort_flag, p));
         };
-        // (after a wait has given up the streams still meet at each item's barriers)
+        // After a wait has given up a warp goes through the rest without work, as all warps of a stream still meet at each
+        // item's barriers: whether they do must not depend on an item, which may be half written then.
 #pragma unroll 1
         for (int n = 0; n < mine; ++n) {
             Item it;
             {
                 const bool ok = items.get(n, it, abort_flag, p);
                 go = __all_sync(0xFFFFFFFFu, go && ok);
-                if (lane == 0) items.done(n);
+                if (go && lane == 0) items.done(n);
             }
             const bool duo = two_tiles(it);
-            const int nt = PAIR && xs == 1 && !duo ? 0 : it.nt, nsteps = PAIR ? 2 * nt : nt, r = it.r0 + (PAIR ? 128 * xs : 0) + row;
+            const int nt = !go || (PAIR && xs == 1 && !duo) ? 0 : it.nt, nsteps = PAIR ? 2 * nt : nt, r = it.r0 + (PAIR ? 128 * xs : 0) + row;
             const size_t part0 = ((size_t)it.z * p.Hkv + it.g) * ((size_t)p.B * p.M * p.G) + (PREFIX ? 0 : (size_t)it.b * p.M * p.G);
             // The row is at position pos.  Slot s has position s (s < S), else s + off (s >= sl),
             // else s + off + R; it is seen if pos - W < position <= pos, or s < S.
@@ -994,7 +996,7 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                 if (go) fence_after();
             }
             // A second stream without work stays behind the first: its next wait is for the phase after this item's.
-            if (TURNS && !duo && it.nt > 0) {
+            if (TURNS && go && !duo && it.nt > 0) {
                 __syncwarp();
                 if (lane == 0) bar_arrive(su32(alone));
                 wait(alone, alones++);
@@ -1006,7 +1008,7 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
             const bool live = PREFIX || p.by_g(r) < it.cnt;
             const float inv = live && nt > 0 && l != 0.f ? 1.f / l : 0.f;
             if (l != l && ref == -INFINITY) ref = 0.f;   // a row of NaN alone has no maximum, but is not empty
-            if (PAIR && xs == 1 && it.one) continue;   // (another item's)
+            const bool mine_too = go && !(PAIR && xs == 1 && it.one);   // (else another item's)
             if (!PREFIX && tp.omap) {
                 // 64 columns at a time into the stream's box, and from there by TMA while the next item starts
                 uint8_t *box = sm + L::stage + xs * kBox;
@@ -1016,6 +1018,7 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                     asm volatile("bar.sync %0, 128;" ::"r"(2 + xs) : "memory");   // the box is free
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
+                        if (!mine_too) break;
                         uint32_t o[32];
                         tmem_ld32(oc + col0 + 64 * k + 32 * half, o);   // (not used where there is nothing to see)
                         tmem_wait_ld();
@@ -1031,12 +1034,12 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     asm volatile("bar.sync %0, 128;" ::"r"(2 + xs) : "memory");   // and full
                     const int m = p.by_g(r);
-                    if ((tid & 127) == 0 && go && m < p.M) {
+                    if ((tid & 127) == 0 && mine_too && m < p.M) {
                         tma_store5(&tp.to, su32(box), col0 + 64 * k, 0, it.g, m, it.b);
                         asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                     }
                 }
-            } else if (go) {
+            } else if (mine_too) {
                 // Four lanes exchange 64-byte pieces: lane 4 a + j then has piece j of rows 4 a .. 4 a + 3.
                 if (parts && r < rows && col0 == 0) *reinterpret_cast<float2 *>(to_parts.ml + (part0 + r) * 2) = make_float2(ref * c, l * kDown);
                 const int rq = r - (lane & 3);

@@ -147,3 +147,34 @@ def test_rejected_rows_in_a_full_ring(D, Hq, M, W, S, extra):
         def of(x):
             return lambda b, m: x[b, kv_ref.seen(pos[b] + m, W, S).to(DEV)]
         kv_ref.check_rows(o, q, of(k), of(v), lambda b, m: m < counts[b], D ** -0.5)
+
+
+# --------------------------------------------------------------------- waits
+
+@pytest.mark.parametrize("D,Hq,G", [(64, 32, 8), (128, 32, 8), (256, 16, 2), (128, 24, 8), (64, 24, 8)])
+def test_waits_that_run_out_among_many_items(D, Hq, G):
+    """Limits at which waits give up in a CTA's first items, in later ones or not at all; with 128 columns the last turn's items
+    are cut in two, with groups of three outputs go without boxes, few rows leave parts.  A call returns and reports it, or is right;
+    the device stays usable."""
+    q, k = rows(gen(75), 2, 2048, Hq, D), rows(gen(76), 2, 2048, G, D)
+    few = rows(gen(77), 2, 40, Hq, D)
+    counts = i32([2048, 700])
+    calls = [lambda: moe.window_attention(q, k, k, 40, sinks=2), lambda: moe.window_attention(q, k, k, pos=i32([0, 0]), counts=counts),
+             lambda: moe.window_attention(few, k, k)]
+    want = [f()[0] for f in calls]
+    torch.cuda.synchronize()
+    errs = set()
+    try:
+        for ns in (1, 200, 1000, 3000, 10000, 100000):
+            moe.debug_set(-1, timeout_ns=ns)
+            for f, w in zip(calls, want):
+                o, err = f()
+                e = err_of(err)
+                errs.add(e)
+                assert e in (0, 4) and (e or torch.equal(o, w))
+    finally:
+        moe.debug_set(-1, 0)
+    assert 4 in errs
+    for f, w in zip(calls, want):
+        o, err = f()
+        assert err_of(err) == 0 and torch.equal(o, w)
