@@ -651,7 +651,7 @@ int moe_kv_attn_workspace_size(const moe_kv *cache, int M, int max_prefix, size_
  * prefix_k, prefix_v (or NULL): keys and values of prefix_len positions that
  * lie ahead of every sequence's own, [prefix_len][kv_heads][head_dim] with
  * strides row and head (seq is not used), of the cache's type, 16-byte aligned, strides
- * multiples of 8.  All rows see all of them, in one softmax with their
+ * multiples of 8 and, where the dimension has more than one entry, not 0.  All rows see all of them, in one softmax with their
  * own positions; they are read once for the batch.  For caches without a window.
  * One to three launches.  Errors: INVALID_ARG, UNSUPPORTED,
  * BUFFER_TOO_SMALL, CUDA. */

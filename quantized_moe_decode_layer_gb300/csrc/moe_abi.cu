@@ -985,6 +985,8 @@ int moe_kv_attn(const moe_kv *cache, const moe_rows *q, int M, const int32_t *po
                                                 cache->sinks, prefix_len);
     if (need && (!ws_dev || !aligned16(ws_dev))) return MOE_ERR_INVALID_ARG;
     if (ws_bytes < need) return MOE_ERR_BUFFER_TOO_SMALL;
+    for (const moe_rows *r : {prefix_k, prefix_v})
+        if (prefix_len && ((prefix_len > 1 && r->row == 0) || (cache->kv_heads > 1 && r->head == 0))) return MOE_ERR_INVALID_ARG;
     KvCall p = {};
     p.q = static_cast<const uint16_t *>(q->data_dev);
     p.qb = q->seq;

@@ -178,3 +178,23 @@ def test_waits_that_run_out_among_many_items(D, Hq, G):
     for f, w in zip(calls, want):
         o, err = f()
         assert err_of(err) == 0 and torch.equal(o, w)
+
+
+# ------------------------------------------------------------------ prefixes
+
+@pytest.mark.parametrize("B", [2, 40])
+def test_expanded_prefix(B):
+    """One head's prefix for two, one position's for many: refused for any batch; a dimension of one entry may have any stride."""
+    r = gen(78)
+    cache = moe.KVCache(20, batch=B, q_heads=4, kv_heads=2, head_dim=64, max_prefix=50)
+    q, x = rows(r, B, 1, 4, 64), rows(r, 50, 2, 64)
+    k = rows(r, B, 1, 2, 64)
+    cache.append(k, k, i32([0] * B))
+    for bad in (x[:1].expand(50, 2, 64), x[:, :1].expand(50, 2, 64)):
+        for prefix in ((bad, x), (x, bad)):
+            with pytest.raises(moe.MoeError):
+                cache.attend(q, i32([0] * B), prefix=prefix)
+    one = x[:1].as_strided((1, 2, 64), (0, 64, 1))
+    a, _ = cache.attend(q, i32([0] * B), prefix=(one, one))
+    b, err = cache.attend(q, i32([0] * B), prefix=(x[:1], x[:1]))
+    assert err_of(err) == 0 and torch.equal(a, b)

@@ -138,3 +138,14 @@ def test_windows_outside_32_bits(window, sinks):
         moe.window_attention_workspace(1, 8, 2, 64, 1000, 1000, window, sinks)
     with pytest.raises(ValueError, match="window must be"):
         moe.KVCache(2000, q_heads=8, kv_heads=2, head_dim=64, window=window, sinks=sinks, device="cpu")
+
+
+@pytest.mark.parametrize("q_heads,batch", [(2, 2), (16, 2), (16, 64)])
+def test_expanded_prefixes_refused(q_heads, batch):
+    """Positions or heads of a prefix that lie at one place, whatever the number of rows: few and many take different kernels."""
+    L = moe.lib()
+    c, far, q = cache(batch=batch, q_heads=q_heads), dict(row=512, head=256), row(seq=8192, row=4096, head=256)
+    for zero in ("row", "head"):
+        bad = row(**{**far, zero: 0})
+        for k, v in ((bad, row(**far)), (row(**far), bad)):
+            assert L.moe_kv_attn(c, q, 1, FAKE, None, k, v, 5, 1.0, FAKE, FAKE, 1 << 40, FAKE, None) == 1
