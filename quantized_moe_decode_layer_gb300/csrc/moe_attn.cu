@@ -711,10 +711,14 @@ int launch_attn(const uint16_t *q, const uint16_t *k, const uint16_t *vt, int T_
         const cuuint64_t dims[3] = {(cuuint64_t)kAD, (cuuint64_t)n_valid, (cuuint64_t)kAHkv};
         const cuuint64_t strides[2] = {(cuuint64_t)kAD * 2, (cuuint64_t)T_cap * kAD * 2};
         const cuuint32_t box[3] = {64, (cuuint32_t)kAKeys, 1}, es[3] = {1, 1, 1};
-        if (enc(&P.tk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t *>(k), dims, strides, box, es,
-                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-            return MOE_ERR_INVALID_ARG;
+        auto done = [&] {
+            return enc(&P.tk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t *>(k), dims, strides, box, es,
+                       CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+        };
+        // The encoder needs a current context, which a thread without a CUDA call so far has none of.
+        int cur = 0;
+        if (!done() && (cudaGetDevice(&cur) != cudaSuccess || cudaSetDevice(cur) != cudaSuccess || !done())) return MOE_ERR_INVALID_ARG;
     }
     {
         const cuuint64_t dims[3] = {(cuuint64_t)n_valid, (cuuint64_t)kAD, (cuuint64_t)kAHkv};

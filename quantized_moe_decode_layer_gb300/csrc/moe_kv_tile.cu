@@ -1111,7 +1111,14 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
     return fn;
 }
 
-// [sequence][head][position][d], strides in elements; a dimension of one entry may have any.
+// The encoder needs a current context, which a thread without a CUDA call so far has none of.
+bool bind_context()
+{
+    int dev = 0;
+    return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess;
+}
+
+// [sequence][head][position][d], strides in elements; a dimension of one entry may have any.  (A call's first map is one of these.)
 bool map_of(CUtensorMap *map, const uint16_t *base, bool f16, int D, int T, int heads, int seqs, long long row, long long head,
             long long seq)
 {
@@ -1121,9 +1128,12 @@ bool map_of(CUtensorMap *map, const uint16_t *base, bool f16, int D, int T, int 
     auto bytes = [&](long long s, int n) { return (cuuint64_t)(n > 1 ? s * 2 : D * 2); };
     const cuuint64_t strides[3] = {bytes(row, T), bytes(head, heads), bytes(seq, seqs)};
     const cuuint32_t box[4] = {64, (cuuint32_t)kHalf, 1, 1}, es[4] = {1, 1, 1, 1};
-    return enc(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint16_t *>(base), dims,
-               strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    auto done = [&] {
+        return enc(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint16_t *>(base), dims,
+                   strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    return done() || (bind_context() && done());
 }
 
 // Packed rows as rectangles of a tensor: [sequence][token][key/value head][head of the group][d].  Needs a group

@@ -198,3 +198,38 @@ def test_expanded_prefix(B):
     a, _ = cache.attend(q, i32([0] * B), prefix=(one, one))
     b, err = cache.attend(q, i32([0] * B), prefix=(x[:1], x[:1]))
     assert err_of(err) == 0 and torch.equal(a, b)
+
+
+# ------------------------------------------------------------------- threads
+
+def test_first_call_of_a_thread():
+    """A thread that has made no CUDA call: prompts, rows over a cache, behind a prefix, and the one-sequence decode attention."""
+    import threading
+    x, k = rows(gen(80), 1, 90, 4, 64), rows(gen(81), 1, 90, 2, 64)
+    cache = moe.KVCache(100, batch=1, q_heads=4, kv_heads=2, head_dim=64, max_prefix=90)
+    cache.append(k, k, i32([0]))
+    q, pos, err = rows(gen(82), 1, 8, 32, 64), i32([82]), i32([0])
+    many = moe.KVCache(100, batch=1, q_heads=32, kv_heads=2, head_dim=64, max_prefix=90, buffers=(cache.k, cache.v))
+    old = moe.AttnCache(64)
+    oq, oout = rows(gen(83), 2, 16, 256), torch.empty((2, 16, 256), device=DEV)
+    out, few = torch.empty_like(x), torch.empty_like(q)
+    calls = [lambda: moe.window_attention(x, k, k, 20, out=out, err=err)[0], lambda: many.attend(q, pos, out=few, err=err)[0],
+             lambda: many.attend(q, pos, prefix=(k[0], k[0]), out=few, err=err)[0], lambda: old.attend(oq, 3, out=oout, err=err)[0]]
+    for f in calls:
+        o = f()
+        want, failed = o.clone(), []
+        o.zero_()
+
+        def work():
+            try:
+                f()
+            except Exception as e:   # noqa: BLE001
+                failed.append(e)
+        t = threading.Thread(target=work)
+        torch.cuda.synchronize()
+        t.start()
+        t.join()
+        torch.cuda.synchronize()
+        assert not failed, failed
+        assert torch.equal(o, want)
+    assert err_of(err) == 0
