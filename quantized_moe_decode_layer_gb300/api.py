@@ -2,7 +2,9 @@
 streams, every step of the layer runs in libmoe.so's kernels."""
 from __future__ import annotations
 
+import collections
 import ctypes as C
+import threading
 
 import torch
 
@@ -876,19 +878,23 @@ def _rows_of(t: torch.Tensor, name: str) -> Rows:
     return _rows_at(t, name, s0 if n0 > 1 else 0, s1 if n1 > 1 else 0, s2 if n2 > 1 else 0)
 
 
-_window_err: dict = {}   # device index -> the error word of window_attention's calls
+class _PerThread(threading.local, collections.UserDict):
+    """A dict of each thread's own."""
+
+
+_window_err = _PerThread()   # (device index, stream) -> the error word of the thread's calls of window_attention there
 
 
 def _err_of(index: int) -> torch.Tensor:
-    """The device's word; during a capture that comes before any other call, one of the graph's own."""
-    err = _window_err.get(index)
+    """The word of the calling thread and the current stream of the current device, made on that stream; during a capture one of
+    the graph's own, in its memory, which each replay clears."""
+    if torch.cuda.is_current_stream_capturing():
+        return torch.zeros(1, dtype=torch.int32, device=index)
+    key = index, torch._C._cuda_getCurrentRawStream(index)
+    err = _window_err.data.get(key)
     if err is None:
-        err = torch.zeros(1, dtype=torch.int32, device=index)
-        with torch.cuda.device(index):
-            if torch.cuda.is_current_stream_capturing():
-                return err
-            torch.cuda.current_stream().synchronize()
-        _window_err[index] = err
+        with torch.inference_mode(False):   # calls outside of it get it, too
+            err = _window_err.data[key] = torch.zeros(1, dtype=torch.int32, device=index)
     return err
 
 
@@ -902,7 +908,8 @@ def window_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window=N
     [batch] on q's device; pos[b] < 0: an idle sequence.  Rows without work get zeros.
 
     err (int32 [1]) collects 1 = rows outside the positions, 4 = a device wait gave up; where none is given, a word
-    of the device that all such calls share.
+    that the calling thread's calls on that stream share, until it is cleared (in a captured graph one of the call's own, 0 again at
+    each replay).
 
     Runs on the current stream of q's device, or on `stream`: then inputs and results are
     ordered by the caller, as tensors between streams are; inputs may be dropped right after the call.

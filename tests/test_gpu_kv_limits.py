@@ -233,3 +233,58 @@ def test_first_call_of_a_thread():
         assert not failed, failed
         assert torch.equal(o, want)
     assert err_of(err) == 0
+
+
+# -------------------------------------------------------------- error words
+
+def test_error_words_are_not_shared():
+    """A call's error shows in no result of another thread, stream or graph; it stays until the caller clears it."""
+    import threading
+    x = rows(gen(79), 1, 90, 2, 64)
+    good, bad = i32([0]), i32([1])                        # 90 rows from position 1 on: one too many
+
+    def call(pos, **kw):
+        return moe.window_attention(x, x, x, 20, pos=pos, **kw)[1]
+    call(good)
+    side, found = torch.cuda.Stream(), {}
+    side.wait_stream(torch.cuda.current_stream())
+
+    def work(name, pos, **kw):
+        for _ in range(50):
+            err = call(pos, **kw)
+        torch.cuda.synchronize()
+        found[name] = int(err)
+    threads = [threading.Thread(target=work, args=("bad", bad)), threading.Thread(target=work, args=("good", good)),
+               threading.Thread(target=work, args=("bad there", bad), kwargs=dict(stream=side)),
+               threading.Thread(target=work, args=("good there", good), kwargs=dict(stream=side))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert found == {"bad": 1, "good": 0, "bad there": 1, "good there": 0}
+    there = call(bad, stream=side)
+    torch.cuda.synchronize()
+    assert int(there) == 1 and int(call(good)) == 0
+    with torch.cuda.stream(side):
+        assert int(call(good)) == 1                       # this thread's word of that stream
+        there.zero_()
+        assert int(call(good)) == 0
+    pos, graph = i32([1]), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        err = call(pos)
+    graph.replay()
+    assert int(err) == 1 and int(call(good)) == 0
+    pos.zero_()
+    graph.replay()
+    assert int(err) == 0
+
+
+def test_error_word_made_in_inference_mode():
+    x, stream = rows(gen(79), 1, 90, 2, 64), torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        with torch.inference_mode():
+            moe.window_attention(x, x, x, 20, pos=i32([1]))
+        _, err = moe.window_attention(x, x, x, 20)
+        assert int(err) == 1
+        err.zero_()
