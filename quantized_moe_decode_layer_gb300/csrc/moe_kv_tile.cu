@@ -825,6 +825,10 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                 if (!PREFIX && !(all_seen(0) && all_seen(1)) && (any_left(it.first_key(t, 0)) || any_left(it.first_key(t, 1))) && (!PAIR || xs == 0)) {
                     // values that may be anything: zeros
                     const int n0 = units + UPT * v_order<AHEAD>(t, nt);
+                    // Their place's phase before has to be over, or the wait below would take the one before that for it.  It is that of values
+                    // whose product came before these scores, or of keys; with one row tile, of the values of the tile before, which nothing
+                    // has waited for yet.  (The last tile's place had its own keys.)
+                    if (!PAIR && t > 0 && t + 1 < nt) wait(&o_done[xs ^ 1], done[xs ^ 1] + ((i - 1) >> 1));
 #pragma unroll 1
                     for (int u = n0; u < n0 + UPT; ++u) {
                         wait(&full[u % NU], u / NU);

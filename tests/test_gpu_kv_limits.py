@@ -149,6 +149,32 @@ def test_rejected_rows_in_a_full_ring(D, Hq, M, W, S, extra):
         kv_ref.check_rows(o, q, of(k), of(v), lambda b, m: m < counts[b], D ** -0.5)
 
 
+@pytest.mark.parametrize("D,Hq", [(64, 64), (128, 64), (256, 64), (256, 8)])
+@pytest.mark.parametrize("W,S,extra", [(128, 130, 1), (300, 300, 1), (600, 4, 60), (1000, 130, 9)])
+def test_rejected_rows_in_any_tile(D, Hq, W, S, extra):
+    """Rejected rows in tiles that others follow, many times over: values of the tiles before and behind stay as they are."""
+    M, B = 4, 40
+    T = S + W + M - 1 + extra
+    r = gen(85)
+    ends = [T + 3 + (37 * b) % (2 * T) for b in range(B)]
+    n = max(ends)
+    k, v, q = rows(r, B, n, 1, D), rows(r, B, n, 1, D), rows(r, B, M, Hq, D)
+    cache = moe.KVCache(T, batch=B, q_heads=Hq, kv_heads=1, head_dim=D, window=W, sinks=S, max_rows=M)
+    cache.append(k, v, i32([0] * B), counts=i32(ends))
+    bad = torch.full((B, M, 1, D), float("nan"), dtype=BF, device=DEV)
+    cache.append(bad, bad, i32(ends), counts=i32([min(M, extra)] * B))
+    pos = [e - M for e in ends]
+    want = None
+    for _ in range(30):
+        o, err = cache.attend(q, i32(pos))
+        assert err_of(err) == 0
+        want = o if want is None else want
+        assert torch.equal(o, want)
+    for b in range(0, B, 5):
+        sees = _sees(pos[b], M, ends[b], W, S)
+        kv_ref.close(o[b], *_definition(q[b], k[b, :ends[b]], v[b, :ends[b]], sees, D ** -0.5), f"sequence {b}")
+
+
 # --------------------------------------------------------------------- waits
 
 @pytest.mark.parametrize("D,Hq,G", [(64, 32, 8), (128, 32, 8), (256, 16, 2), (128, 24, 8), (64, 24, 8)])
@@ -288,3 +314,99 @@ def test_error_word_made_in_inference_mode():
         _, err = moe.window_attention(x, x, x, 20)
         assert int(err) == 1
         err.zero_()
+
+
+# ------------------------------------------------------------ random shapes
+
+def _definition(q, k, v, sees, scale):
+    """(o, tolerance) of rows q [m, Hq, D] over k, v [n, Hkv, D], in 64 bits; sees [m, n].  As kv_ref.row, with what fp16's small
+    weights lose as test_many_small_weights_in_fp16 has it."""
+    G, n, half = q.shape[1] // k.shape[1], k.shape[0], kv_ref.HALF[q.dtype]
+    qd, kd, vd = q.double(), k.double().repeat_interleave(G, 1), v.double().repeat_interleave(G, 1)
+    s = torch.einsum("mhd,nhd->hmn", qd, kd) * scale
+    size = (torch.einsum("mhd,nhd->hmn", qd.abs(), kd.abs()) * scale).masked_fill(~sees, 0).amax(-1).t()[..., None]
+    w = s.masked_fill(~sees, -torch.inf).softmax(-1)
+    o, oabs = torch.einsum("hmn,nhd->mhd", w, vd), torch.einsum("hmn,nhd->mhd", w, vd.abs())
+    tol = half * o.abs() + (half + 2 * ((q.shape[2] + 6) * kv_ref.E23 * size + 2.0 ** -22) + (2 * n + 64) * kv_ref.E23) * oabs
+    if q.dtype is FP:
+        tol = tol + n * 2.0 ** -32 * vd.abs().max() + 2.0 ** -25
+    return o, tol
+
+
+def _sees(pos, count, n, window, sinks):
+    p, t = torch.arange(pos, pos + count, device=DEV)[:, None], torch.arange(n, device=DEV)
+    return (t <= p) & ((t > p - (window or 1 << 40)) | (t < sinks))
+
+
+@pytest.mark.parametrize("seed", range(60))
+def test_random_prompts(seed):
+    """Shapes, windows, lengths and padding at random, NaN in all that is past a sequence."""
+    import random
+    r, g = random.Random(seed), gen(1000 + seed)
+    D, G, dt = r.choice((64, 128, 256)), r.choice((1, 2, 3, 4, 5, 7, 8, 16, 32, 64)), r.choice((BF, FP))
+    Hkv, B, M = r.choice((1, 2, 3)) if G < 16 else 1, r.choice((1, 2, 3, 6)), int(2 ** r.uniform(0, 10))
+    T = M + int(2 ** r.uniform(0, 11)) - 1
+    while B * M * G * Hkv * T > 1 << 25:
+        M = max(1, M // 2)
+        T = max(M, T // 2)
+    W = r.choice((None, 1, 2, 63, 64, 65, 100, 128, 129, 500, int(2 ** r.uniform(0, 11))))
+    S = 0 if W is None else r.choice((0, 0, 1, 4, 63, 64, 65, 130, 300))
+    q, k, v = rows(g, B, M, G * Hkv, D, dtype=dt), rows(g, B, T, Hkv, D, dtype=dt), rows(g, B, T, Hkv, D, dtype=dt)
+    ragged = r.random() < 0.6
+    counts = [r.choice((0, 1, M, r.randint(0, M))) if ragged else M for _ in range(B)]
+    pos = [r.randint(0, T - c) if r.random() > 0.1 else -1 for c in counts] if r.random() < 0.7 else [T - M] * B
+    for b in range(B):
+        end = pos[b] + counts[b] if pos[b] >= 0 else 0
+        k[b, end:], v[b, end:] = float("nan"), float("nan")
+    o, err = moe.window_attention(q, k, v, W, sinks=S, pos=i32(pos), counts=i32(counts) if ragged else None)
+    assert err_of(err) == 0
+    for b in range(B):
+        c = counts[b] if pos[b] >= 0 else 0
+        assert not o[b, c:].any()
+        if c:
+            n = pos[b] + c
+            kv_ref.close(o[b, :c], *_definition(q[b, :c], k[b, :n], v[b, :n], _sees(pos[b], c, n, W, S), D ** -0.5), f"sequence {b}")
+
+
+@pytest.mark.parametrize("seed", range(60))
+def test_random_caches(seed):
+    """The same over rings, with rejected rows behind the last position, and over linear caches behind prefixes."""
+    import random
+    r, g = random.Random(seed), gen(2000 + seed)
+    D, G, dt = r.choice((64, 128, 256)), r.choice((1, 2, 4, 5, 8, 16, 32, 64)), r.choice((BF, FP))
+    Hkv, M, B = r.choice((1, 2, 3)) if G < 16 else 1, r.randint(1, 8), r.choice((1, 2, 4, 9, 33))
+    W, S, P = None, 0, 0
+    if r.random() < 0.6:
+        W, S = r.choice((1, 7, 64, 100, 128, 300, 1000)), r.choice((0, 1, 4, 64, 70, 130))
+        T = S + W + M - 1 + r.choice((0, 1, 8, 50, 200))
+        top = 3 * T + 5
+    else:
+        T = top = max(M, r.choice((M, 70, 300, 1500)))
+        P = r.choice((0, 1, 100, 129, 1000, 4000))
+    ends = [r.choice((0, M, top, r.randint(0, top))) for _ in range(B)]        # positions with the call's rows
+    counts = [min(r.choice((M, M, 0, r.randint(0, M))), e) for e in ends]
+    pos = [e - c if c or r.random() < 0.5 else -1 for e, c in zip(ends, counts)]
+    n = max(max(ends), 1)
+    k, v = rows(g, B, n, Hkv, D, dtype=dt), rows(g, B, n, Hkv, D, dtype=dt)
+    cache = moe.KVCache(T, batch=B, q_heads=G * Hkv, kv_heads=Hkv, head_dim=D, dtype=dt, window=W, sinks=S, max_rows=M, max_prefix=P)
+    cache.k.fill_(float("nan"))
+    cache.v.fill_(float("nan"))
+    cache.append(k, v, i32([0 if e else -1 for e in ends]), counts=i32(ends))
+    # rows behind the last one, as many as leave what the first row sees
+    room = [min(M, T - e if W is None else T - S - W - c + 1) for e, c in zip(ends, counts)]
+    bad = torch.full((B, M, Hkv, D), float("nan"), dtype=dt, device=DEV)
+    cache.append(bad, bad, i32([e if x > 0 else -1 for e, x in zip(ends, room)]), counts=i32([max(x, 0) for x in room]))
+    assert err_of(cache.err) == 0
+    q = rows(g, B, M, G * Hkv, D, dtype=dt)
+    prefix = (rows(g, P, Hkv, D, dtype=dt), rows(g, P, Hkv, D, dtype=dt)) if P else None
+    o, err = cache.attend(q, i32(pos), counts=i32(counts), prefix=prefix)
+    assert err_of(err) == 0
+    for b in range(B):
+        c = counts[b] if pos[b] >= 0 else 0
+        assert not o[b, c:].any()
+        if c:
+            e, sees, own = ends[b], _sees(pos[b], c, ends[b], W, S), (k[b, :ends[b]], v[b, :ends[b]])
+            if P:
+                own = [torch.cat([x, y]) for x, y in zip(prefix, own)]
+                sees = torch.cat([torch.ones((c, P), dtype=torch.bool, device=DEV), sees], 1)
+            kv_ref.close(o[b, :c], *_definition(q[b, :c], *own, sees, D ** -0.5), f"sequence {b} of {e}")
