@@ -316,6 +316,25 @@ def test_error_word_made_in_inference_mode():
         err.zero_()
 
 
+# ----------------------------------------------------------- the last rows
+
+@pytest.mark.parametrize("M", [1, 8])
+def test_all_rows_far_in_a_large_cache(M):
+    """Every row of a call on the last sequence of a cache of more than 2^31 elements, in its first and last head."""
+    r, B, G, D, T = gen(84), 3, 8, 256, 400000
+    buf = [torch.zeros((B, G, T, D), dtype=BF, device=DEV) for _ in range(2)]
+    cache = moe.KVCache(T, batch=B, q_heads=32, kv_heads=G, head_dim=D, buffers=tuple(buf))
+    k, v, q = rows(r, B, 300, G, D), rows(r, B, 300, G, D), rows(r, B, M, 32, D)
+    cache.append(k, v, i32([-1, -1, T - 300]))
+    o, err = cache.attend(q, i32([-1, -1, T - M]))
+    assert err_of(err) == 0 and not o[:2].any()
+    for m in range(M):
+        for g in (0, G - 1):
+            h, n = slice(4 * g, 4 * g + 4), T - M + m + 1
+            want, tol = kv_ref.row(q[2, m, h], buf[0][2, g, :n, None], buf[1][2, g, :n, None], D ** -0.5)
+            kv_ref.close(o[2, m, h], want, tol, f"row {m}, head {g}")
+
+
 # ------------------------------------------------------------ random shapes
 
 def _definition(q, k, v, sees, scale):
