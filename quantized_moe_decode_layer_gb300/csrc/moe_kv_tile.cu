@@ -87,8 +87,8 @@ constexpr uint32_t kTmemCols = 512;
 __device__ __forceinline__ uint32_t s_col(int b) { return b == 2 ? 384u : 128u * (uint32_t)b; }
 // A weight's exponent is c s - c ref, one fused product and sum with the rounded product c ref, so a row's largest one is off by
 // that rounding: up to half a spacing of c ref, 2^-14 at 2^10 and 64 at 2^30, which no 16-bit weight holds.  Rows whose c ref
-// is beyond 2^10 take c (s - ref) instead, where the largest is exact.  (The vote and its branch, taken by hardly any warp: 8195 rows,
-// window 1024, 32/8/128: 125 -> 128 us; 32/8/64 and 16/2/256 within 1 %.)
+// is beyond 2^10 take c (s - ref) instead, where the largest is exact.  (Found by the vote that a rising reference needs anyway: 8195
+// rows, window 1024, 32/8/128: 125 -> 127 us, by a vote of its own 129.)
 constexpr float kFar = 1024.f;
 // registers a thread: launched with 168; the softmax warps take what the others leave
 constexpr int kRegsSoft = 208, kRegsRest = 88;
@@ -917,44 +917,46 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                 }
                 if (now != ref) l *= ref == -INFINITY ? 0.f : ex2((ref - now) * c);
                 ref = now;
-                if (__any_sync(0xFFFFFFFFu, raise) && t > 0) {
-                    // O, which has the tiles up to the one before, in the new reference's units
-                    if (TURNS) {
-                        const int before = turn - (duo ? 2 : 1);
-                        wait(&o_done[before % NB], before / NB);
-                    } else {
-                        wait(&o_done[PAIR ? xs : xs ^ 1], PAIR ? turn - 1 : done[xs ^ 1] + ((i - 1) >> 1));
-                    }
-                    if (!go) break;
-                    fence_after();
-                    const float f = raise ? ex2((was - now) * c) : 1.f;
-#pragma unroll 1
-                    for (int k = 0; k < D; k += 32) {
-                        uint32_t o[32];
-                        tmem_ld32(oc + k, o);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                        tmem_st32(oc + k, o);
-                    }
-                }
                 float sub = ref == -INFINITY ? 0.f : __fmaf_rn(-ref, c, kUp);
                 const bool far = fabsf(sub) > kFar;
-                if (__any_sync(0xFFFFFFFFu, far)) {
-                    const float shift = far ? -ref : 0.f;   // (0 changes nothing)
-                    const uint64_t shift2 = two(shift, shift);
-                    auto move = [&](uint32_t *s) {
-#pragma unroll
-                        for (int j = 0; j < KS; j += 2) {
-                            float a, b;
-                            split2(add2(two(__uint_as_float(s[j]), __uint_as_float(s[j + 1])), shift2), a, b);
-                            s[j] = __float_as_uint(a);
-                            s[j + 1] = __float_as_uint(b);
+                if (__any_sync(0xFFFFFFFFu, raise || far)) {     // (hardly ever)
+                    if (__any_sync(0xFFFFFFFFu, raise) && t > 0) {
+                        // O, which has the tiles up to the one before, in the new reference's units
+                        if (TURNS) {
+                            const int before = turn - (duo ? 2 : 1);
+                            wait(&o_done[before % NB], before / NB);
+                        } else {
+                            wait(&o_done[PAIR ? xs : xs ^ 1], PAIR ? turn - 1 : done[xs ^ 1] + ((i - 1) >> 1));
                         }
-                    };
-                    move(s0);
-                    move(s1);
-                    if (far) sub = kUp;
+                        if (!go) break;
+                        fence_after();
+                        const float f = raise ? ex2((was - now) * c) : 1.f;
+#pragma unroll 1
+                        for (int k = 0; k < D; k += 32) {
+                            uint32_t o[32];
+                            tmem_ld32(oc + k, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                            tmem_st32(oc + k, o);
+                        }
+                    }
+                    if (__any_sync(0xFFFFFFFFu, far)) {
+                        const float shift = far ? -ref : 0.f;   // (0 changes nothing)
+                        const uint64_t shift2 = two(shift, shift);
+                        auto move = [&](uint32_t *s) {
+#pragma unroll
+                            for (int j = 0; j < KS; j += 2) {
+                                float a, b;
+                                split2(add2(two(__uint_as_float(s[j]), __uint_as_float(s[j + 1])), shift2), a, b);
+                                s[j] = __float_as_uint(a);
+                                s[j + 1] = __float_as_uint(b);
+                            }
+                        };
+                        move(s0);
+                        move(s1);
+                        if (far) sub = kUp;
+                    }
                 }
                 weights(0, s0, two(sub, sub));
                 // (one half's P on its way while the other's is computed: 16384 positions, all seen, 1157 -> 1132 us with 64
