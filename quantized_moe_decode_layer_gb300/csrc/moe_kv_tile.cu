@@ -802,7 +802,7 @@ __global__ void __launch_bounds__(kTThreads, 1) kv_tile_kernel(const __grid_cons
                     const int last = min(p.by_g(it.r0 + (it.one ? kRows : RT) - 1), it.cnt - 1), end = it.p0 + last - it.off;
                     hole0 = max(min(p.S, it.sl + it.off), end >= p.T ? p.S + end - p.T + 1 : 0);
                     hole1 = it.sl;
-                    valid = min(end, p.T - 1) + 1;
+                    valid = end < p.T - 1 ? end + 1 : INT_MAX;
                 }
                 int lo = pos_hi - it.off - p.W + 1;
                 if (lo <= max(it.sl, p.S)) lo = it.sl;
