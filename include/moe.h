@@ -609,8 +609,8 @@ int moe_kv8_evict(const moe_kv8 *src, const moe_kv8 *dst, const int32_t *lens_de
  * Scores, maxima, sums and outputs are fp32; a softmax weight is rounded to the
  * 16-bit type for its product with the values (by half a step; fp16: weights below 2^-21
  * of the row's largest by up to 2^-32 of that one), and the output once at the end; a row
- * that sees a score of NaN or +infinity (in units of log2: a score is scale * log2(e) q . k in
- * fp32) is NaN.  Which
+ * that sees a q . k of NaN or +infinity is NaN (one whose score, times log2(e), is beyond fp32 may be).  Sums of
+ * values times weights of up to 2^8 have to be within fp32.  Which
  * partial sums there are depends on the lengths of the whole batch, so a row's last bits
  * may differ between batches; the same call gives the same bits. */
 #define MOE_KV_ERR_TIMEOUT 4

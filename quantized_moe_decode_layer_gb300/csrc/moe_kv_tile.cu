@@ -25,9 +25,9 @@
 // warp 9 issues the products, warps 10 and 11 load q.  V is taken as it lies, [position][d] with d
 // contiguous (an MN-major operand), P from tensor memory; outputs leave through a box in shared memory.
 //
-// Bound by the tensor core with D = 256 (a prompt of 16K, window 4096, 16/2/256: 0.59 to 0.61 ms, 1.6 PFLOP/s of the
+// Bound by the tensor core with D = 256 (a prompt of 16K, window 4096, 16/2/256: 0.57 to 0.61 ms, 1.6 PFLOP/s of the
 // pairs that are seen, 85 % of the measured rate), by a stream's chain of S, softmax and P V with D = 128 (32/8/128:
-// 0.70 ms), by the softmax warps with D = 64 (32/8/64: 0.52 ms).
+// 0.66 ms), by the latency of the softmax warps, two a scheduler, with D = 64 (32/8/64: 0.50 ms).
 //
 // Every wait is bounded; one that runs out sets *err, the roles stop, the CTA waits
 // (bounded) for its copies and products and frees its tensor memory.
